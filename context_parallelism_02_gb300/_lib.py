@@ -20,6 +20,7 @@ CP_ECUDA = -4
 CP_ETIMEOUT = -5
 CP_ESMEM = -6
 CP_EBOUNDS = -7
+CP_ECACHE = -8
 
 CP_LAYOUT_CONTIGUOUS = 0
 CP_LAYOUT_ZIGZAG = 1
@@ -57,6 +58,12 @@ SIGNATURES = {
     "lse_merge_n": (_I, [_P, _P, _I, _L, _I, _P, _P, _P]),
     "ulysses_seq_to_head": (_I, [_P, _P, _I, _L, _I, _I, _I, _I, _I, _P]),
     "ulysses_head_to_seq": (_I, [_P, _P, _I, _L, _I, _I, _I, _I, _I, _P]),
+    "kv4_append": (_I, [_P] * 13 + [_I] * 12 + [_P]),
+    "kv4_gather": (_I, [_P] * 6 + [_I] * 8 + [_P]),
+    "kv4_attn": (_I, [_P] * 8 + [_I] * 11 + [_F, _P, ctypes.c_size_t, _P]),
+    "kv4_attn_workspace": (ctypes.c_size_t, [_I]),
+    "kv4_select": (_I, [_P] * 6 + [_I] * 12 + [_P, ctypes.c_size_t, _P]),
+    "kv4_select_workspace": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "cp_get_error": (_I, [_P]),
     "cp_strerror": (ctypes.c_char_p, [_I]),
     "cp_debug_wait_timeout": (_I, [ctypes.c_uint64, _P]),

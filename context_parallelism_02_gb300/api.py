@@ -7,6 +7,7 @@ current torch stream (or ``stream``), like the C call.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import numpy as np
@@ -335,6 +336,227 @@ def ulysses_head_to_seq(y: torch.Tensor, N: int, layout: int, x=None, stream=Non
                                          y.element_size(), ctypes.c_void_p(_stream(stream)))
     check(rc, "ulysses_head_to_seq")
     return x
+
+
+def _kv4_check(**tensors):
+    """Tensors of one call: on the current CUDA device, contiguous, of the given dtype."""
+    for name, (t, dtype) in tensors.items():
+        if t is None:
+            continue
+        _need_cuda_contig(name, t)
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} must be on the current CUDA device")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}")
+
+
+def _kv4_shape(name, t, *shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+
+
+def _kv4_pool(cache, pages, lens, B):
+    """(n_pages, Hkv, page, D, max_pages) of a pool and a page table."""
+    if cache.dim() != 4 or cache.shape[3] % 5:
+        raise ValueError("cache must have shape [n_pages, Hkv, page, 5 D / 4]")
+    P, Hkv, page, w = cache.shape
+    if pages.dim() != 2:
+        raise ValueError("pages must have shape [B, max_pages]")
+    _kv4_shape("pages", pages, B, pages.shape[1])
+    _kv4_shape("lens", lens, B)
+    return P, Hkv, page, w // 5 * 4, pages.shape[1]
+
+
+@contextlib.contextmanager
+def _on(stream):
+    """Tensors made inside belong to ``stream``, so that their memory is not handed
+    on while its kernels may still use it."""
+    if stream is None:
+        yield
+    else:
+        with torch.cuda.stream(stream):
+            yield
+
+
+def kv4_cache(n_pages: int, Hkv: int, page: int, D: int, summary: bool = False):
+    """An empty pool for :func:`kv4_append`: uint8 ``[n_pages, Hkv, page, 5 D / 4]`` on
+    the current device, or with ``summary`` (pool, bf16 ``[n_pages, Hkv, 2, D]``)."""
+    if D not in (64, 128) or page not in (16, 32, 64, 128, 256):
+        raise CpError(_lib.CP_EUNSUPPORTED, "kv4_cache")
+    cache = torch.empty(n_pages, Hkv, page, D // 4 * 5, dtype=torch.uint8, device="cuda")
+    if not summary:
+        return cache
+    return cache, torch.empty(n_pages, Hkv, 2, D, dtype=torch.bfloat16, device="cuda")
+
+
+def kv4_append(k, v, cache, pages, lens, cos=None, sin=None, q=None, q_out=None, positions=None,
+               n_new=None, summary=None, interleaved: bool = False, stream=None):
+    """Rotate and quantise new tokens into the paged 4-bit cache, token (b, j) into
+    slot ``lens[b] + j``; returns the rotated q (None without q).
+
+    k, v ``[B, n, Hkv, D]`` and q ``[B, n, Hq, D]`` (fp32 or bf16) may be strided views
+    whose rows are contiguous (slices of one projection's output).  cache as
+    :func:`kv4_cache`, pages int32 ``[B, max_pages]``, lens int32 ``[B]``: tokens
+    cached before the call, which does not change it.  cos, sin fp32
+    ``[max_pos, rot / 2]`` (None: no rotation); positions int32 ``[B, n]`` (None: the
+    slots); n_new int32 ``[B]``: real tokens of a padded batch; summary: the pool's
+    key ranges, kept for :func:`kv4_select`.
+    """
+    if k.dim() != 4 or v.shape != k.shape:
+        raise ValueError("k and v must have shape [B, n, Hkv, D]")
+    if k.dtype not in _DT or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise ValueError("q, k, v must share dtype float32 or bfloat16")
+    B, n, Hkv, D = k.shape
+    i32 = torch.int32
+    _kv4_check(cache=(cache, torch.uint8), pages=(pages, i32), lens=(lens, i32),
+               cos=(cos, torch.float32), sin=(sin, torch.float32), positions=(positions, i32),
+               n_new=(n_new, i32), summary=(summary, torch.bfloat16), q_out=(q_out, k.dtype))
+    P, H, page, Dc, M = _kv4_pool(cache, pages, lens, B)
+    if (H, Dc) != (Hkv, D):
+        raise ValueError("cache and k must share Hkv and D")
+    if (cos is None) != (sin is None) or (cos is not None and (cos.dim() != 2 or cos.shape != sin.shape)):
+        raise ValueError("cos and sin must share shape [max_pos, rot / 2]")
+    _kv4_shape("positions", positions, B, n)
+    _kv4_shape("n_new", n_new, B)
+    _kv4_shape("summary", summary, P, Hkv, 2, D)
+    if q is not None:
+        if q.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != D:
+            raise ValueError("q must have shape [B, n, Hq, D]")
+        if q_out is None:
+            with _on(stream):
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _kv4_shape("q_out", q_out, *q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    strides = []
+    for name, t in (("k", k), ("v", v), ("q", q)):
+        if t is None:
+            strides += [0, 0, 0]
+            continue
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} must be on the current CUDA device")
+        if t.numel() and t.stride(3) != 1:
+            raise ValueError(f"{name}'s rows must be contiguous")
+        # an axis of one entry is not stepped along: its stride says nothing
+        strides += [0 if t.shape[i] <= 1 else t.stride(i) for i in range(3)]
+    rc = _lib.load().kv4_append(
+        _ptr(k), _ptr(v), _ptr(q), _ptr(q_out), _ptr(cache), _ptr(summary), _ptr(pages), _ptr(lens),
+        _ptr(n_new), _ptr(positions), _ptr(cos), _ptr(sin), (ctypes.c_int64 * 9)(*strides), B, n,
+        0 if q is None else q.shape[2], Hkv, D, P, page, M, 0 if cos is None else 2 * cos.shape[1],
+        int(interleaved), 0 if cos is None else cos.shape[0], _DT[k.dtype],
+        ctypes.c_void_p(_stream(stream)))
+    check(rc, "kv4_append")
+    return q_out
+
+
+def kv4_gather(cache, pages, lens, count: int, start=None, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """Cached tokens back as rows: (k, v) ``[B, count, Hkv, D]`` with row (b, j) the slot
+    ``start[b] + j`` (start int32 ``[B]``, None: 0); rows at or past ``lens[b]`` are 0."""
+    if k is not None:
+        dtype = k.dtype
+    if dtype not in _DT:
+        raise ValueError("dtype must be float32 or bfloat16")
+    B = lens.shape[0]
+    _kv4_check(cache=(cache, torch.uint8), pages=(pages, torch.int32), lens=(lens, torch.int32),
+               start=(start, torch.int32), k=(k, dtype), v=(v, dtype))
+    P, Hkv, page, D, M = _kv4_pool(cache, pages, lens, B)
+    _kv4_shape("start", start, B)
+    with _on(stream):
+        if k is None:
+            k = torch.empty(B, count, Hkv, D, dtype=dtype, device=cache.device)
+        if v is None:
+            v = torch.empty(B, count, Hkv, D, dtype=dtype, device=cache.device)
+    _kv4_shape("k", k, B, count, Hkv, D)
+    _kv4_shape("v", v, B, count, Hkv, D)
+    rc = _lib.load().kv4_gather(_ptr(cache), _ptr(pages), _ptr(lens), _ptr(start), _ptr(k), _ptr(v), B, count,
+                                Hkv, D, P, page, M, _DT[dtype], ctypes.c_void_p(_stream(stream)))
+    check(rc, "kv4_gather")
+    return k, v
+
+
+def kv4_attn_workspace(D: int) -> int:
+    return int(_lib.load().kv4_attn_workspace(D))
+
+
+def kv4_attn(q, cache, pages, lens, vis=None, causal: bool = True, scale: float | None = None, sel=None,
+             out=None, lse=None, workspace=None, stream=None):
+    """Attention of query tokens over the paged 4-bit cache; returns (out, lse).
+
+    q ``[B, n, Hq, D]`` bf16 (rotated); out like q (or fp32, if given so, as
+    :func:`lse_merge` takes it), lse ``[B, Hq, n]`` fp32.  Row (b, j) sees the slots
+    below ``vis[b, j]`` (int32 ``[B, n]``), else below ``lens[b] - (n - 1) + j`` if
+    causal, else below ``lens[b]``.  ``sel`` int32 ``[B, n, Hkv, n_sel]``
+    (:func:`kv4_select`): only the slots of these pages.
+    """
+    if q.dim() != 4:
+        raise ValueError("q must have shape [B, n, Hq, D]")
+    B, n, Hq, D = q.shape
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(B, Hq, n, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(max(kv4_attn_workspace(D), 16), dtype=torch.uint8, device=q.device)
+    if out.dtype not in _DT:
+        raise ValueError("out must be float32 or bfloat16")
+    _kv4_check(q=(q, torch.bfloat16), cache=(cache, torch.uint8), pages=(pages, torch.int32),
+               lens=(lens, torch.int32), vis=(vis, torch.int32), sel=(sel, torch.int32), out=(out, out.dtype),
+               lse=(lse, torch.float32), workspace=(workspace, workspace.dtype))
+    P, Hkv, page, Dc, M = _kv4_pool(cache, pages, lens, B)
+    if Dc != D:
+        raise ValueError("cache and q must share D")
+    _kv4_shape("vis", vis, B, n)
+    _kv4_shape("out", out, *q.shape)
+    _kv4_shape("lse", lse, B, Hq, n)
+    if sel is not None:
+        if sel.dim() != 4:
+            raise ValueError("sel must have shape [B, n, Hkv, n_sel]")
+        _kv4_shape("sel", sel, B, n, Hkv, sel.shape[3])
+    sc = -1.0 if scale is None else float(scale)
+    rc = _lib.load().kv4_attn(_ptr(q), _ptr(cache), _ptr(pages), _ptr(lens), _ptr(vis), _ptr(sel), _ptr(out),
+                              _ptr(lse), B, n, Hq, Hkv, D, P, page, M, 0 if sel is None else sel.shape[3],
+                              int(causal), _DT[out.dtype], sc, _ptr(workspace),
+                              workspace.numel() * workspace.element_size(), ctypes.c_void_p(_stream(stream)))
+    check(rc, "kv4_attn")
+    return out, lse
+
+
+def kv4_select_workspace(B: int, n: int, Hkv: int, max_pages: int) -> int:
+    return int(_lib.load().kv4_select_workspace(B, n, Hkv, max_pages))
+
+
+def kv4_select(q, summary, pages, lens, page: int, n_sel: int, vis=None, causal: bool = True,
+               keep_first: int = 1, keep_last: int = 1, sel=None, workspace=None, stream=None):
+    """The pages that each query token attends to, per kv head: int32
+    ``[B, n, Hkv, n_sel]``, ascending, then -1.  q as :func:`kv4_attn`; summary as
+    :func:`kv4_cache`; ``page``: tokens of a page.  The first ``keep_first`` and last
+    ``keep_last`` pages that the row sees are always among them."""
+    if q.dim() != 4 or summary.dim() != 4:
+        raise ValueError("q must have shape [B, n, Hq, D] and summary [n_pages, Hkv, 2, D]")
+    B, n, Hq, D = q.shape
+    P, Hkv = summary.shape[:2]
+    _kv4_shape("summary", summary, P, Hkv, 2, D)
+    if pages.dim() != 2:
+        raise ValueError("pages must have shape [B, max_pages]")
+    M = pages.shape[1]
+    _kv4_shape("pages", pages, B, M)
+    _kv4_shape("lens", lens, B)
+    _kv4_shape("vis", vis, B, n)
+    with _on(stream):
+        if sel is None:
+            sel = torch.empty(B, n, Hkv, max(n_sel, 0), dtype=torch.int32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(max(kv4_select_workspace(B, n, Hkv, M), 16), dtype=torch.uint8, device=q.device)
+    _kv4_shape("sel", sel, B, n, Hkv, n_sel)
+    _kv4_check(q=(q, torch.bfloat16), summary=(summary, torch.bfloat16), pages=(pages, torch.int32),
+               lens=(lens, torch.int32), vis=(vis, torch.int32), sel=(sel, torch.int32),
+               workspace=(workspace, workspace.dtype))
+    rc = _lib.load().kv4_select(_ptr(q), _ptr(summary), _ptr(pages), _ptr(lens), _ptr(vis), _ptr(sel), B, n, Hq,
+                                Hkv, D, P, page, M, n_sel, int(causal), keep_first, keep_last, _ptr(workspace),
+                                workspace.numel() * workspace.element_size(), ctypes.c_void_p(_stream(stream)))
+    check(rc, "kv4_select")
+    return sel
 
 
 def cp_get_error(stream=None) -> int:

@@ -511,6 +511,7 @@ int cp_get_error(void *stream)
     if (w == ERRW_TIMEOUT) return CP_ETIMEOUT;
     if (w == ERRW_SMEM_ALIGN) return CP_ESMEM;
     if (w == ERRW_BOUNDS) return CP_EBOUNDS;
+    if (w == ERRW_CACHE) return CP_ECACHE;
     return w ? CP_ECUDA : CP_OK;
 }
 
@@ -526,6 +527,8 @@ const char *cp_strerror(int code)
     case CP_ESMEM: return "a kernel's dynamic shared memory was not 1 KB aligned; it returned without work";
     case CP_EBOUNDS:
         return "debug-bounds build: a kernel met an out-of-range tile coordinate and skipped it";
+    case CP_ECACHE:
+        return "a page number, slot, length or position outside the cache's tables was met and skipped";
     default: return "unknown status code";
     }
 }

@@ -49,6 +49,7 @@ namespace cp {
 constexpr unsigned ERRW_TIMEOUT = 1u;       // a bounded wait ran out
 constexpr unsigned ERRW_SMEM_ALIGN = 2u;    // dynamic shared memory not 1 KB aligned
 constexpr unsigned ERRW_BOUNDS = 3u;        // debug-bounds build: tile coordinate out of range
+constexpr unsigned ERRW_CACHE = 4u;         // paged cache: page, slot, length or position out of range
 
 // All positions are int32: the library rejects S > INT32_MAX, and 32-bit
 // index arithmetic keeps the kernels free of 64-bit division routines.

@@ -61,6 +61,8 @@ extern "C" {
                                  (cp_get_error); the kernel returned without work */
 #define CP_EBOUNDS (-7)       /* debug-bounds build only: an out-of-range tile coordinate was
                                  met and skipped (cp_get_error) */
+#define CP_ECACHE (-8)        /* a page number, slot, length or position outside the paged cache's
+                                 tables was met and skipped (cp_get_error) */
 
 /* sequence layouts */
 #define CP_LAYOUT_CONTIGUOUS 0
@@ -351,6 +353,126 @@ int ring_attn_bwd_noalloc(const void *q, const void *k, const void *v, const voi
                           const float *lse, const void *dout, void *dq, void *dk, void *dv,
                           int B, int Hq, int Hkv, int64_t S, int D, int N, int causal, int layout,
                           int dtype, float scale, void *stream);
+
+/*
+ * The paged 4-bit key/value cache: what a long prompt leaves behind for
+ * decoding.  Four calls: kv4_append (rotate, quantise, write), kv4_gather (read
+ * slots back as BSHD, for ring_attn_fwd or flash_block_step on the next chunk),
+ * kv4_attn (attention of a few query tokens over the cache; its (out, lse) are
+ * partials that lse_merge joins when the ranks of a context-parallel group each
+ * hold a part of the sequence) and kv4_select (the pages that a query attends
+ * to, for kv4_attn).
+ *
+ * Pool: cache [n_pages][Hkv][page][5 D / 4] bytes, 16-byte aligned; page in
+ * {16, 32, 64, 128, 256}, D in {64, 128}.  A page holds `page` tokens of one
+ * sequence; a token and kv head takes 5 D / 4 bytes, K and V together: 4-bit
+ * codes, and for every 32 neighbouring elements an fp16 scale s and an fp16
+ * minimum m; a value is s code + m, code in 0..15.  The bytes of 16 tokens are
+ * interleaved (csrc/kv4.cuh has the order); the pool may start uninitialised.
+ * Page table: pages [B][max_pages] int32, entry i of sequence b the physical
+ * page of its slots [i page, (i + 1) page); entries behind a sequence's last
+ * page are not read.  lens [B] int32: tokens of the sequence in the cache.
+ * Sequences may share pages that are only read.
+ * pages, lens and the other int32 arrays are device memory: a call does not wait
+ * for them and can be captured in a graph.  An entry outside its range is
+ * therefore not an error of the call: the kernels skip what it names and record
+ * CP_ECACHE (cp_get_error).
+ */
+
+/*
+ * kv4_append -- writes new tokens behind the cached ones: token (b, j) goes to
+ * slot lens[b] + j.
+ *   k, v [B][n][Hkv][D], q [B][n][Hq][D] (or NULL): device, dtype CP_BF16 or
+ *   CP_F32, rows contiguous and 16-byte aligned; strides: HOST array of nine
+ *   element strides (batch, token, head of k, then v, then q), NULL for
+ *   contiguous tensors.
+ *   q_out [B][n][Hq][D], contiguous, q's dtype: the rotated q (NULL iff q is).
+ *   cosine, sine [max_pos][rot / 2] fp32: the rotation of k and q.  The first rot
+ *   elements of a row are rotated (rot % 16 == 0, 0 <= rot <= D; 0: none, and
+ *   cosine and sine may be NULL), in pairs (d, d + rot/2), or (2d, 2d + 1) if
+ *   interleaved: y1 = x1 cos - x2 sin, y2 = x2 cos + x1 sin, in fp32.
+ *   positions [B][n] int32 or NULL: the row of the tables for each token; NULL
+ *   takes its slot.  (A context-parallel rank appends its own tokens to its own
+ *   cache and passes their global positions.)
+ *   n_new [B] int32 or NULL: tokens of each sequence that are real (a padded
+ *   batch; clamped to [0, n]).  The others are not written; their q_out is 0.
+ *   summary [n_pages][Hkv][2][D] bf16 or NULL: per page, the smallest and largest
+ *   value of every element of its rotated keys; updated for kv4_select (a page
+ *   whose first slot is written starts afresh).
+ * Quantisation of a group of 32: s = fp16((max - min) / 15), m = fp16(min),
+ * code = rint((y - m) / s) held to 0..15; values beyond +-65504 count as that,
+ * and a group with a value that is not finite is held as NaN.
+ * Within one call no two sequences may write the same page.
+ * Errors: CP_EINVAL (null pointer, misalignment, sizes, Hq % Hkv), CP_EUNSUPPORTED
+ * (D, dtype, page), CP_ECUDA.
+ */
+int kv4_append(const void *k, const void *v, const void *q, void *q_out, void *cache, void *summary,
+               const int32_t *pages, const int32_t *lens, const int32_t *n_new,
+               const int32_t *positions, const float *cosine, const float *sine,
+               const int64_t *strides, int B, int n, int Hq, int Hkv, int D, int n_pages, int page,
+               int max_pages, int rot, int interleaved, int max_pos, int dtype, void *stream);
+
+/*
+ * kv4_gather -- cached tokens back as rows: row (b, j) of k and v
+ * [B][count][Hkv][D] (dtype CP_BF16, rounded to nearest even, or CP_F32) is slot
+ * start[b] + j; rows at or past lens[b] are 0.
+ *   start [B] int32 or NULL (0).
+ * Errors: as kv4_append.
+ */
+int kv4_gather(const void *cache, const int32_t *pages, const int32_t *lens, const int32_t *start,
+               void *k, void *v, int B, int count, int Hkv, int D, int n_pages, int page,
+               int max_pages, int dtype, void *stream);
+
+/*
+ * kv4_attn -- attention of query tokens over the cache.
+ *   q [B][n][Hq][D] bf16, contiguous (rotated, as kv4_append's q_out); query head
+ *   h reads kv head h / (Hq / Hkv).
+ *   Row (b, j) sees the slots below vis[b][j] if vis [B][n] (int32) is given, else
+ *   below lens[b] - (n - 1) + j if causal (the n tokens are the last of the
+ *   cache), else below lens[b]; in any case below lens[b].
+ *   sel [B][n][Hkv][n_sel] int32 or NULL: row (b, j) and kv head h attend only to
+ *   the slots that they see in these pages (numbers within the sequence; -1: no
+ *   page; a page named twice counts twice).
+ *   out [B][n][Hq][D]: bf16 (rounded to nearest even) or fp32 by out_dtype;
+ *   lse [B][Hq][n] fp32, natural log.  A row that sees nothing: (0, -inf).  What a
+ *   row does not see has no influence on it, whatever those slots hold.
+ *   fp32 sums; K enters exactly, V's values and the softmax weights rounded to
+ *   fp16.  scale <= 0 selects 1/sqrt(D).
+ *   workspace: device, kv4_attn_workspace(D) bytes, 16-byte aligned, contents
+ *   irrelevant; calls that may overlap on the GPU need their own.
+ * Errors: as kv4_append, plus a null or too small workspace.
+ */
+int kv4_attn(const void *q, const void *cache, const int32_t *pages, const int32_t *lens,
+             const int32_t *vis, const int32_t *sel, void *out, float *lse, int B, int n, int Hq,
+             int Hkv, int D, int n_pages, int page, int max_pages, int n_sel, int causal,
+             int out_dtype, float scale, void *workspace, size_t ws_bytes, void *stream);
+
+/* kv4_attn_workspace -- bytes of scratch kv4_attn needs; 0 for a D that is not
+ * built.  Host only. */
+size_t kv4_attn_workspace(int D);
+
+/*
+ * kv4_select -- per (b, j, kv head) the n_sel pages that kv4_attn should read.
+ * A page's score is max over the kv head's query heads of
+ *   sum_d max(q_d lo_d, q_d hi_d)
+ * with (lo, hi) its summary: no key of the page has a larger q.k.  Among the pages
+ * that hold a slot the row sees, the first keep_first and the last keep_last are
+ * always taken, then the best scores, ties to the lower page (a score that is not
+ * a number comes first).
+ *   sel [B][n][Hkv][n_sel] int32: page numbers within the sequence, ascending,
+ *   then -1.  vis, causal: as kv4_attn.  keep_first + keep_last <= n_sel.
+ *   workspace: device, kv4_select_workspace(B, n, Hkv, max_pages) bytes, 16-byte
+ *   aligned.
+ * Errors: as kv4_attn.
+ */
+int kv4_select(const void *q, const void *summary, const int32_t *pages, const int32_t *lens,
+               const int32_t *vis, int32_t *sel, int B, int n, int Hq, int Hkv, int D, int n_pages,
+               int page, int max_pages, int n_sel, int causal, int keep_first, int keep_last,
+               void *workspace, size_t ws_bytes, void *stream);
+
+/* kv4_select_workspace -- bytes of scratch kv4_select needs; 0 for bad sizes.
+ * Host only. */
+size_t kv4_select_workspace(int B, int n, int Hkv, int max_pages);
 
 /*
  * cp_get_error -- synchronise `stream`, then read and clear the calling
