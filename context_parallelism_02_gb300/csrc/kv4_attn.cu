@@ -22,6 +22,17 @@
 #include "kv4.cuh"
 #include "tc_helpers.cuh"
 
+// Schedule.  All items' blocks of 16 tokens form one line, batch by batch and
+// item by item, and every CTA of a launch that just fills the GPU takes an equal
+// stretch of it, whatever the lengths: lengths are read on the device, so a
+// captured step stays balanced as the sequences grow.  A stretch is cut into
+// pieces at the items' ends; a piece that is a whole item is written out, the
+// others leave partial sums that a second kernel joins by log-sum-exp, in the
+// order of the line (no atomics: results repeat bit for bit).  The four warps of
+// a CTA take the blocks of a piece in turn, each with its own ring of shared
+// memory stages filled by bulk copies, so no warp waits for another but at the
+// end of a piece.
+
 namespace cp {
 
 namespace {
@@ -410,118 +421,408 @@ __device__ __forceinline__ void block_step(const uint8_t *blk, int slot, const R
     block_values<D, NT>(blk, live, p, s);
 }
 
-// The warps' states of one item joined: rows' references and sums go through
-// shared memory, then the accumulators are added up in the warps' order.
 template <int D, int NT>
-struct Joined {
-    float m[WARPS][NT * 8], l[WARPS][NT * 8];
-    float o[WARPS][NT * 8][D];
+struct Part {              // a piece's result in the workspace
+    static constexpr int FLOATS = NT * 8 * (D + 2);   // m, l of each row, then the rows
 };
 
+// Blocks in a warp's ring.  12 warps per SM with 4 blocks of 2.5 KB on the way are
+// 120 KB, several times latency x bandwidth (about 46 KB per SM).
+template <int D>
+__host__ __device__ constexpr int stages() { return D == 128 ? 5 : 8; }
+
 template <int D, int NT>
-__device__ __forceinline__ void put_state(Joined<D, NT> &sm, const State<D, NT> &s)
+struct Smem {
+    uint8_t ring[WARPS][stages<D>()][Kv4<D>::BYTES];
+    float o[WARPS][NT * 8][D];
+    float m[WARPS][NT * 8], l[WARPS][NT * 8];
+    uint64_t full[WARPS][stages<D>()];
+    int slot[WARPS][stages<D>()];    // first slot of the block; -1: no block
+    int64_t scan[WARPS];
+    int64_t found[3];                // sequence, blocks before it, all blocks
+    int abort, never;
+};
+
+// Blocks of one item of sequence b (at least 1, so that every item is written).
+__device__ __forceinline__ int item_blocks(const Kv4AttnArgs &a, int b)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float l = s.l[t][e];
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (g == 0) {
-                sm.m[warp][t * 8 + 2 * c + e] = s.m[t][e];
-                sm.l[warp][t * 8 + 2 * c + e] = l;
-            }
-#pragma unroll
-            for (int gr = 0; gr < Kv4<D>::NG; ++gr)
-                *reinterpret_cast<float4 *>(&sm.o[warp][t * 8 + 2 * c + e][32 * gr + 4 * g]) =
-                    make_float4(s.o[t][2 * gr][e], s.o[t][2 * gr][e + 2], s.o[t][2 * gr + 1][e], s.o[t][2 * gr + 1][e + 2]);
-        }
+    if (a.sel) return a.n_sel << (a.pool.page_shift - 4);
+    const int len = kv4_len(a.pool, b);
+    return len > 0 ? (len - 1) / KV4_BLOCK + 1 : 1;
+}
+
+// Over the batch, with every thread of the block (blockDim.x = T): all blocks of
+// one item each, and the number before the sequences [upto, B).
+template <int T>
+__device__ __forceinline__ void count_blocks(const Kv4AttnArgs &a, int upto, int64_t &all, int64_t &before, int64_t *red)
+{
+    int64_t s = 0, p = 0;
+    for (int b = threadIdx.x; b < a.rows.B; b += T) {
+        const int n = item_blocks(a, b);
+        s += n;
+        if (b < upto) p += n;
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        p += __shfl_xor_sync(0xffffffffu, p, o);
+    }
+    if ((threadIdx.x & 31) == 0) red[2 * (threadIdx.x >> 5)] = s, red[2 * (threadIdx.x >> 5) + 1] = p;
+    __syncthreads();
+    all = before = 0;
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w) all += red[2 * w], before += red[2 * w + 1];
+    __syncthreads();
+}
+
+// Blocks of a CTA's stretch.
+__device__ __forceinline__ int64_t stretch(int64_t all, int ctas, int least)
+{
+    const int64_t per = (all + ctas - 1) / ctas;
+    return per > least ? per : least;
+}
+
+// A walk over the pieces of a CTA's stretch.
+struct Walk {
+    int b, i;        // sequence, item of it
+    int nb;          // the item's blocks
+    int t0, t1;      // the piece: blocks [t0, t1) of the item
+    int64_t left;    // blocks from t0 to the end of the stretch
+    __device__ __forceinline__ bool valid() const { return left > 0; }
+    __device__ __forceinline__ void cut() { t1 = left < nb - t0 ? t0 + (int)left : nb; }
+    __device__ __forceinline__ void next(const Kv4AttnArgs &a, int per_batch)
+    {
+        left -= t1 - t0;
+        if (left <= 0) return;
+        t0 = 0;
+        if (++i == per_batch) {
+            i = 0;
+            ++b;
+            nb = item_blocks(a, b);
+        }
+        cut();
+    }
+};
+
+// One output row's four elements.
+__device__ __forceinline__ void put_out(const Kv4AttnArgs &a, int64_t at, float4 o)
+{
+    if (a.out_f32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = o;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) =
+            make_uint2(tc::pack_bf16(o.x, o.y), tc::pack_bf16(o.z, o.w));
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Shape sh)
+__global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Shape sh, int ctas, int least)
 {
-    extern __shared__ __align__(16) uint8_t dyn[];
-    Joined<D, NT> &sm = *reinterpret_cast<Joined<D, NT> *>(dyn);
-    const int warp = threadIdx.x >> 5;
-    const int b = blockIdx.x / sh.per_batch;
-    const Item it = decode_item(sh, a.pool.Hkv, b, blockIdx.x % sh.per_batch);
-    const int len = kv4_len(a.pool, b);
-    Rows<D, NT> r;
-    load_rows<D, NT>(a, sh, it, len, r);
-    State<D, NT> s;
-    s.clear();
-    const int ps = a.pool.page_shift, bpp = 1 << (ps - 4);   // blocks per page
-    const int32_t *sel = a.sel ? a.sel + (((int64_t)b * a.rows.n + it.j0) * a.pool.Hkv + it.h) * a.n_sel : nullptr;
-    const int64_t blocks = sel ? (int64_t)a.n_sel * bpp : ((int64_t)r.max_limit + 15) >> 4;
-    const int pages = (int)(((int64_t)len + (1 << ps) - 1) >> ps);
-    for (int64_t i = warp; i < blocks; i += WARPS) {
-        int lp = (int)(i >> (ps - 4));
-        if (sel) {
-            lp = __ldg(sel + lp);
-            if (lp < 0) continue;
-            if (lp >= pages) {
-                kv4_report(a.pool.err);
-                continue;
+    extern __shared__ __align__(128) uint8_t dyn[];
+    Smem<D, NT> &sm = *reinterpret_cast<Smem<D, NT> *>(dyn);
+    constexpr int NS = stages<D>();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < WARPS; ++w)
+            for (int s = 0; s < NS; ++s) mbar_init(smem_u32(&sm.full[w][s]), 1);
+        sm.abort = sm.never = 0;
+        fence_mbar_init();
+    }
+    // where the stretch begins: lane-strided sums, then the one sequence that holds it
+    const int B = a.rows.B, chunk = (B + WARPS * 32 - 1) / (WARPS * 32);
+    int64_t mine = 0;
+    for (int x = 0; x < chunk; ++x) {
+        const int b = threadIdx.x * chunk + x;
+        if (b < B) mine += item_blocks(a, b);
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sm.scan[warp] = upto;
+    __syncthreads();
+    int64_t all = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) upto += sm.scan[w];
+        all += sm.scan[w];
+    }
+    all *= sh.per_batch;
+    const int64_t per = stretch(all, ctas, least), f0 = per * blockIdx.x;
+    if (f0 >= all) return;
+    if (f0 < upto * sh.per_batch && f0 >= (upto - mine) * sh.per_batch) {
+        int b = threadIdx.x * chunk;
+        int64_t before = upto - mine;
+        for (int n; f0 >= (before + (n = item_blocks(a, b))) * sh.per_batch; ++b) before += n;
+        sm.found[0] = b;
+        sm.found[1] = before;
+    }
+    __syncthreads();
+    Walk at;
+    at.b = (int)sm.found[0];
+    at.nb = item_blocks(a, at.b);
+    const int64_t rest = f0 - sm.found[1] * sh.per_batch;
+    at.i = (int)(rest / at.nb);
+    at.t0 = (int)(rest % at.nb);
+    at.left = min(per, all - f0);
+    at.cut();
+    Walk ahead = at;                        // the piece that copies are issued for
+    const WaitCtl wc{a.pool.err, &sm.abort, a.limit_ns};
+    const int ps = a.pool.page_shift, bpp = 1 << (ps - 4);
+    // The issuing side: each lane works out one of the warp's next 32 blocks.
+    int batch = 0, batch_n = 0;             // blocks of the batch issued, blocks in it
+    int done_t = ahead.t0 + warp;           // next block of the piece to be worked out
+    const uint8_t *src = nullptr;
+    int src_slot = -1;
+    unsigned issued = 0, taken = 0;
+    bool dead = false;
+    auto refill = [&]() {                   // false: the stretch has no more blocks for this warp
+        while (ahead.valid() && done_t >= ahead.t1) {
+            ahead.next(a, sh.per_batch);
+            done_t = ahead.t0 + warp;
+        }
+        if (!ahead.valid()) return false;
+        const int t = done_t + lane * WARPS;
+        src = nullptr;
+        src_slot = -1;
+        if (t < ahead.t1) {
+            const Item it = decode_item(sh, a.pool.Hkv, ahead.b, ahead.i);
+            const int len = kv4_len(a.pool, ahead.b);
+            int lp = t >> (ps - 4);
+            bool on = true;
+            if (a.sel) {
+                lp = __ldg(a.sel + (((int64_t)it.b * a.rows.n + it.j0) * a.pool.Hkv + it.h) * a.n_sel + lp);
+                on = lp >= 0;
+                if (on && lp > (len - 1) >> ps) {   // len 0: -1 >> ps is -1
+                    kv4_report(a.pool.err);
+                    on = false;
+                }
+            }
+            const int64_t slot = ((int64_t)lp << ps) + (t & (bpp - 1)) * KV4_BLOCK;
+            if (on && slot < len) {
+                const int id = kv4_page(a.pool, it.b, lp);
+                if (id >= 0) {
+                    src = kv4_block<D>(a.pool, id, it.h, t & (bpp - 1));
+                    src_slot = (int)slot;
+                }
             }
         }
-        const int slot = (lp << ps) + (int)(i & (bpp - 1)) * KV4_BLOCK;
-        if (slot >= r.max_limit) continue;
-        const int id = kv4_page(a.pool, b, lp);
-        if (id < 0) continue;
-        block_step<D, NT>(kv4_block<D>(a.pool, id, it.h, (int)(i & (bpp - 1))), slot, r, s);
-    }
-    put_state<D, NT>(sm, s);
-    __syncthreads();
-    for (int x = threadIdx.x; x < NT * 8 * (D / 4); x += WARPS * 32) {
-        const int row = x / (D / 4), d4 = x % (D / 4);
-        const int rr = it.tile * NT * 8 + row;
-        if (rr >= sh.rows) continue;
-        float m = -INFINITY;
-        for (int w = 0; w < WARPS; ++w) m = fmaxf(m, sm.m[w][row]);
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < WARPS; ++w) {
-            if (sm.m[w][row] == -INFINITY) continue;
-            const float f = ex2(sm.m[w][row] - m);
-            l = fmaf(f, sm.l[w][row], l);
-            const float4 v = *reinterpret_cast<const float4 *>(&sm.o[w][row][d4 * 4]);
-            o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+        const int n = (ahead.t1 - done_t + WARPS - 1) / WARPS;
+        batch_n = n < 32 ? n : 32;
+        batch = 0;
+        done_t += 32 * WARPS;
+        return true;
+    };
+    auto issue = [&]() {
+        if (dead || (batch == batch_n && !refill())) return;
+        if (lane == batch) {
+            const int s = issued % NS;
+            const uint32_t bar = smem_u32(&sm.full[warp][s]);
+            sm.slot[warp][s] = src_slot;
+            if (src) {
+                mbar_arrive_expect_tx(bar, Kv4<D>::BYTES);
+                bulk_load(smem_u32(sm.ring[warp][s]), src, Kv4<D>::BYTES, bar);
+            } else {
+                mbar_arrive(bar);
+            }
         }
-        const int j = it.j0 + rr / sh.group, head = it.h * sh.group + rr % sh.group;
-        const bool empty = l == 0.f;
-        const float inv = empty ? 0.f : 1.f / l;
-        o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-        const int64_t at = (((int64_t)b * a.rows.n + j) * a.rows.Hq + head) * D + d4 * 4;
-        if (a.out_f32) {
-            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = o;
-        } else {
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) =
-                make_uint2(tc::pack_bf16(o.x, o.y), tc::pack_bf16(o.z, o.w));
+        ++batch;
+        ++issued;
+    };
+    for (int s = 0; s < NS; ++s) issue();
+    __syncwarp();
+    for (; at.valid(); at.next(a, sh.per_batch)) {
+        const Item it = decode_item(sh, a.pool.Hkv, at.b, at.i);
+        Rows<D, NT> r;
+        load_rows<D, NT>(a, sh, it, kv4_len(a.pool, at.b), r);
+        State<D, NT> s;
+        s.clear();
+        for (int t = at.t0 + warp; t < at.t1; t += WARPS) {
+            const int st = taken % NS;
+            if (!dead && !waitw(smem_u32(&sm.full[warp][st]), (taken / NS) & 1, wc)) dead = true;
+            if (dead) break;
+            const int slot = sm.slot[warp][st];
+            if (slot >= 0 && slot < r.max_limit) block_step<D, NT>(sm.ring[warp][st], slot, r, s);
+            ++taken;
+            __syncwarp();                    // every lane has read the stage
+            issue();
+            __syncwarp();                    // ... and the slot is written before the next round reads it
         }
-        if (d4 == 0) a.lse[((int64_t)b * a.rows.Hq + head) * a.rows.n + j] = empty ? -INFINITY : fmaf(m, LN2, logf(l));
+        // the warps' sums joined
+        const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = s.l[u][e];
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                const int row = u * 8 + 2 * c + e;
+                if (g == 0) sm.m[warp][row] = s.m[u][e], sm.l[warp][row] = l;
+#pragma unroll
+                for (int gr = 0; gr < Kv4<D>::NG; ++gr)
+                    *reinterpret_cast<float4 *>(&sm.o[warp][row][32 * gr + 4 * g]) = make_float4(
+                        s.o[u][2 * gr][e], s.o[u][2 * gr][e + 2], s.o[u][2 * gr + 1][e], s.o[u][2 * gr + 1][e + 2]);
+            }
+        __syncthreads();
+        const bool whole = at.t0 == 0 && at.t1 == at.nb;
+        float *part = static_cast<float *>(a.ws) + (2 * (int64_t)blockIdx.x + (at.t0 == 0 ? 1 : 0)) * Part<D, NT>::FLOATS;
+        for (int x = threadIdx.x; x < NT * 8 * (D / 4); x += WARPS * 32) {
+            const int row = x / (D / 4), d4 = x % (D / 4);
+            const int rr = it.tile * NT * 8 + row;
+            if (rr >= sh.rows) continue;
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) m = fmaxf(m, sm.m[w][row]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                const float mw = sm.m[w][row];
+                const float f = mw == m ? 1.f : ex2(mw - m);
+                l = fmaf(f, sm.l[w][row], l);
+                const float4 v = *reinterpret_cast<const float4 *>(&sm.o[w][row][d4 * 4]);
+                o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+            }
+            if (!whole) {
+                *reinterpret_cast<float4 *>(part + 16 * NT + row * D + d4 * 4) = o;
+                if (d4 == 0) part[row] = m, part[8 * NT + row] = l;
+                continue;
+            }
+            const int j = it.j0 + rr / sh.group, head = it.h * sh.group + rr % sh.group;
+            const bool empty = l == 0.f;
+            const float inv = empty ? 0.f : 1.f / l;
+            put_out(a, (((int64_t)it.b * a.rows.n + j) * a.rows.Hq + head) * D + d4 * 4,
+                    make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+            if (d4 == 0) a.lse[((int64_t)it.b * a.rows.Hq + head) * a.rows.n + j] = empty ? -INFINITY : fmaf(m, LN2, logf(l));
+        }
+        __syncthreads();                     // before the next piece writes sm.o
     }
+    // after a wait that ran out: copies that were issued land before the block ends
+    const WaitCtl drain{a.pool.err, &sm.never, a.drain_ns};
+    for (; taken < issued; ++taken) waitw(smem_u32(&sm.full[warp][taken % NS]), (taken / NS) & 1, drain);
 }
+
+// Joins the pieces of the items that were cut: one block per output row.
+constexpr int JOIN_WARPS = 8;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) kv4_join_kernel(Kv4AttnArgs a, Shape sh, int ctas, int least)
+{
+    __shared__ int64_t red[2 * JOIN_WARPS];
+    __shared__ float sm_m[JOIN_WARPS], sm_l[JOIN_WARPS];
+    __shared__ __align__(16) float sm_o[JOIN_WARPS][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t item = blockIdx.x / sh.rows;
+    const int rr_all = blockIdx.x % sh.rows;
+    const int b = (int)(item / (sh.per_batch / sh.tiles));
+    const int x = (int)(item % (sh.per_batch / sh.tiles));      // (token, kv head)
+    int64_t all, before;
+    count_blocks<JOIN_WARPS * 32>(a, b, all, before, red);
+    all *= sh.per_batch;
+    const int64_t per = stretch(all, ctas, least);
+    const int nb = item_blocks(a, b);
+    // the item of this row: token, row tile, kv head
+    const int tile = rr_all / (NT * 8), row = rr_all % (NT * 8);
+    const int h = x % a.pool.Hkv, j0 = x / a.pool.Hkv;
+    const int i = (j0 * sh.tiles + tile) * a.pool.Hkv + h;
+    const int64_t f = before * sh.per_batch + (int64_t)i * nb;
+    const int c0 = (int)(f / per), c1 = (int)((f + nb - 1) / per);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (c0 == c1) return;
+    float m = -INFINITY, l = 0.f;
+    float o[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+    for (int c = c0 + warp; c <= c1; c += JOIN_WARPS) {
+        const float *part = static_cast<const float *>(a.ws) + (2 * (int64_t)c + (f >= c * per ? 1 : 0)) * Part<D, NT>::FLOATS;
+        const float pm = part[row], pl = part[8 * NT + row];
+        float v[D / 32];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) v[e] = part[16 * NT + row * D + e * 32 + lane];
+        const float mn = fmaxf(m, pm);
+        const float fa = m == mn ? 1.f : ex2(m - mn), fb = pm == mn ? 1.f : ex2(pm - mn);
+        l = fmaf(l, fa, pl * fb);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) o[e] = fmaf(o[e], fa, v[e] * fb);
+        m = mn;
+    }
+    if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) sm_o[warp][e * 32 + lane] = o[e];
+    __syncthreads();
+    if (threadIdx.x >= D / 4) return;
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < JOIN_WARPS; ++w) m = fmaxf(m, sm_m[w]);
+    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < JOIN_WARPS; ++w) {
+        const float fw = sm_m[w] == m ? 1.f : ex2(sm_m[w] - m);
+        l = fmaf(fw, sm_l[w], l);
+        const float4 v = *reinterpret_cast<const float4 *>(&sm_o[w][threadIdx.x * 4]);
+        r.x = fmaf(fw, v.x, r.x), r.y = fmaf(fw, v.y, r.y), r.z = fmaf(fw, v.z, r.z), r.w = fmaf(fw, v.w, r.w);
+    }
+    const int j = j0 + rr_all / sh.group, head = h * sh.group + rr_all % sh.group;
+    const bool empty = l == 0.f;
+    const float inv = empty ? 0.f : 1.f / l;
+    put_out(a, (((int64_t)b * a.rows.n + j) * a.rows.Hq + head) * D + threadIdx.x * 4,
+            make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv));
+    if (threadIdx.x == 0) a.lse[((int64_t)b * a.rows.Hq + head) * a.rows.n + j] = empty ? -INFINITY : fmaf(m, LN2, logf(l));
+}
+
+constexpr int MAX_CTAS = 640;     // what the workspace has room for
+constexpr int LEAST = 8;          // blocks that a CTA takes at least: two per warp
 
 template <int D, int NT>
 int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
 {
-    const int64_t items = (int64_t)a.rows.B * sh.per_batch;
-    if (items > 0x7fffffffLL) return CP_EUNSUPPORTED;
-    constexpr int smem = sizeof(Joined<D, NT>);
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    constexpr int smem = sizeof(Smem<D, NT>);
+    int resident = 0;
+    if (cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kv4_attn_kernel<D, NT>, WARPS * 32, smem) != cudaSuccess ||
+        resident < 1)
         return CP_ECUDA;
-    kv4_attn_kernel<D, NT><<<(unsigned)items, WARPS * 32, smem, st>>>(a, sh);
-    return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ECUDA;
+    int ctas = resident * sm_count();
+    if (ctas > MAX_CTAS) ctas = MAX_CTAS;
+    // an upper bound of the line from the sizes alone
+    const int64_t most = a.sel ? (int64_t)a.n_sel << (a.pool.page_shift - 4)
+                               : ((int64_t)a.pool.max_pages << (a.pool.page_shift - 4));
+    const int64_t line = (most > 0 ? most : 1) * a.rows.B * sh.per_batch;
+    const int grid = (int)min((int64_t)ctas, (line + LEAST - 1) / LEAST);
+    const int64_t joins = (int64_t)a.rows.B * (sh.per_batch / sh.tiles) * sh.rows;
+    if (joins > 0x7fffffffLL) return CP_EUNSUPPORTED;
+    kv4_attn_kernel<D, NT><<<grid, WARPS * 32, smem, st>>>(a, sh, grid, LEAST);
+    if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
+    if (grid == 1) return CP_OK;             // nothing was cut
+    // its blocks start while the first kernel's end, and wait for its results
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)joins);
+    cfg.blockDim = dim3(JOIN_WARPS * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, a, sh, grid, LEAST) == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 
 }  // namespace
 
-size_t kv4_attn_workspace_bytes(int D) { return D == 64 || D == 128 ? 256 : 0; }
+size_t kv4_attn_workspace_bytes(int D)
+{
+    if (D != 64 && D != 128) return 0;
+    return (size_t)2 * MAX_CTAS * 2 * 8 * (D + 2) * sizeof(float);
+}
 
 int launch_kv4_attn(const Kv4AttnArgs &a, int D, cudaStream_t st)
 {

@@ -551,3 +551,49 @@ def test_offsets_past_32_bits(cuda_dev):
     ok()
     for x, y in zip(a + c, b + d):
         assert torch.equal(x, y)
+
+
+def test_attn_long_and_ragged_batches_cut_across_blocks(cuda_dev):
+    """Lengths over four orders of magnitude in one batch: pieces of items in many blocks, joined.  Against the
+    fp32 read-back in 64 bits on the GPU, with check_attn's bounds."""
+    rng = np.random.default_rng(15)
+    for D, Hq, Hkv, page, n, lens in ((128, 8, 2, 64, 1, [9000, 1, 0, 40, 3000, 17, 12345]),
+                                      (64, 24, 2, 16, 2, [5, 20000, 33, 2])):
+        B, L = len(lens), max(lens)
+        cache, _, pages = fill(rng, B, L, Hkv, D, page)
+        q = rows(rng, torch.bfloat16, B, n, Hq, D)
+        gl = dev(np.array(lens, np.int32))
+        kr, vr = api.kv4_gather(cache, dev(pages), gl, L, dtype=torch.float32)
+        f32 = torch.empty(B, n, Hq, D, device="cuda")
+        _, lse = api.kv4_attn(dev(q, torch.bfloat16), cache, dev(pages), gl, out=f32)
+        ok()
+        for b in range(B):
+            for j in range(n):
+                m = max(0, lens[b] - n + 1 + j)
+                if not m:
+                    assert (f32[b, j] == 0).all() and (lse[b, :, j] == -math.inf).all()
+                    continue
+                for x in range(Hq):
+                    k, v = (t[b, :m, x * Hkv // Hq].double() for t in (kr, vr))
+                    s = k @ torch.from_numpy(q[b, j, x]).double().cuda() / math.sqrt(D)
+                    z = s.logsumexp(0)
+                    p = (s - z).exp()
+                    tol = (2.0 ** -10 + (m / 16 + 32) * 2.0 ** -23) * (p @ v.abs()) + m * 2.0 ** -25 * v.abs().max()
+                    assert ((f32[b, j, x] - p @ v).abs() <= tol).all()
+                    size = float(np.abs(q[b, j, x]) @ (k.abs().amax(0).cpu().numpy() + 8)) / math.sqrt(D)
+                    assert abs(lse[b, x, j] - z) <= 2.0 ** -19 * size + 2.0 ** -20 * (abs(z) + 1)
+
+
+def test_attn_value_that_is_not_a_number_is_not_lost_between_blocks(cuda_dev):
+    """A whole block of tokens whose keys are NaN: every row that sees it is NaN, wherever the pieces are cut."""
+    rng = np.random.default_rng(16)
+    cache, _, pages = fill(rng, 1, 5000, 1, 128, 16)
+    nan = torch.full((1, 16, 1, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    q = dev(rows(rng, torch.bfloat16, 1, 1, 4, 128), torch.bfloat16)
+    for at in (0, 16, 2048, 4976):
+        trial = cache.clone()
+        api.kv4_append(nan, nan, trial, dev(pages), dev(np.array([at], np.int32)))
+        out, lse = api.kv4_attn(q, trial, dev(pages), dev(np.array([5000], np.int32)))
+        ok()
+        assert out.isnan().all() and lse.isnan().all()
+
