@@ -23,16 +23,14 @@
 #include "tc_helpers.cuh"
 
 // Schedule.  All items' blocks of 16 tokens form one line, batch by batch and
-// item by item, and every CTA of a launch that just fills the GPU takes an equal
+// item by item, and every warp of a grid that just fills the GPU takes an equal
 // stretch of it, whatever the lengths: lengths are read on the device, so a
-// captured step stays balanced as the sequences grow.  A stretch is cut into
-// pieces at the items' ends; a piece that is a whole item is written out, the
-// others leave partial sums that a second kernel joins by log-sum-exp, in the
-// order of the line (no atomics: results repeat bit for bit).  The four warps of
-// a CTA take the blocks of a piece in turn, each with its own ring of shared
-// memory stages filled by bulk copies, so no warp waits for another but at the
-// end of a piece.
-
+// captured step stays balanced as the sequences grow.  An item counts PAD blocks
+// more than it has, for what a warp spends on starting and ending it.  A stretch
+// is cut into pieces at the items' ends; a piece that is a whole item is written
+// out, the others leave partial sums that a second kernel joins by log-sum-exp, in
+// the order of the line (no atomics: results repeat bit for bit).  Warps share
+// nothing: each has its own ring of shared-memory stages filled by bulk copies.
 namespace cp {
 
 namespace {
@@ -426,20 +424,21 @@ struct Part {              // a piece's result in the workspace
     static constexpr int FLOATS = NT * 8 * (D + 2);   // m, l of each row, then the rows
 };
 
-// Blocks in a warp's ring.  12 warps per SM with 4 blocks of 2.5 KB on the way are
-// 120 KB, several times latency x bandwidth (about 46 KB per SM).
+// Blocks in a warp's ring.  12 warps per SM with 5 blocks of 2.5 KB on the way are
+// 150 KB, several times latency x bandwidth (about 46 KB per SM).
 template <int D>
-__host__ __device__ constexpr int stages() { return D == 128 ? 5 : 8; }
+__host__ __device__ constexpr int stages() { return D == 128 ? 6 : 10; }
 
-template <int D, int NT>
+constexpr int PAD = 8;
+
+template <int D>
 struct Smem {
     uint8_t ring[WARPS][stages<D>()][Kv4<D>::BYTES];
-    float o[WARPS][NT * 8][D];
-    float m[WARPS][NT * 8], l[WARPS][NT * 8];
     uint64_t full[WARPS][stages<D>()];
-    int slot[WARPS][stages<D>()];    // first slot of the block; -1: no block
     int64_t scan[WARPS];
-    int64_t found[3];                // sequence, blocks before it, all blocks
+    int64_t before[WARPS];           // blocks before the sequence that a warp's stretch begins in
+    int slot[WARPS][stages<D>()];    // first slot of the block; -1: no block
+    int seq[WARPS];                  // that sequence
     int abort, never;
 };
 
@@ -451,14 +450,14 @@ __device__ __forceinline__ int item_blocks(const Kv4AttnArgs &a, int b)
     return len > 0 ? (len - 1) / KV4_BLOCK + 1 : 1;
 }
 
-// Over the batch, with every thread of the block (blockDim.x = T): all blocks of
-// one item each, and the number before the sequences [upto, B).
+// Over the batch, with every thread of the block (T of them): the extent of one
+// item of every sequence, and of those before sequence `upto`.
 template <int T>
 __device__ __forceinline__ void count_blocks(const Kv4AttnArgs &a, int upto, int64_t &all, int64_t &before, int64_t *red)
 {
     int64_t s = 0, p = 0;
     for (int b = threadIdx.x; b < a.rows.B; b += T) {
-        const int n = item_blocks(a, b);
+        const int n = item_blocks(a, b) + PAD;
         s += n;
         if (b < upto) p += n;
     }
@@ -472,27 +471,26 @@ __device__ __forceinline__ void count_blocks(const Kv4AttnArgs &a, int upto, int
     all = before = 0;
 #pragma unroll
     for (int w = 0; w < T / 32; ++w) all += red[2 * w], before += red[2 * w + 1];
-    __syncthreads();
 }
 
-// Blocks of a CTA's stretch.
-__device__ __forceinline__ int64_t stretch(int64_t all, int ctas, int least)
+// Length of a warp's stretch.
+__device__ __forceinline__ int64_t stretch(int64_t all, int warps, int least)
 {
-    const int64_t per = (all + ctas - 1) / ctas;
+    const int64_t per = (all + warps - 1) / warps;
     return per > least ? per : least;
 }
 
-// A walk over the pieces of a CTA's stretch.
+// A walk over the pieces of a warp's stretch.
 struct Walk {
     int b, i;        // sequence, item of it
     int nb;          // the item's blocks
-    int t0, t1;      // the piece: blocks [t0, t1) of the item
-    int64_t left;    // blocks from t0 to the end of the stretch
+    int t0, t1;      // the piece: blocks [t0, t1) of the item, none if t0 >= t1
+    int64_t left;    // what remains of the stretch, from t0 on
     __device__ __forceinline__ bool valid() const { return left > 0; }
     __device__ __forceinline__ void cut() { t1 = left < nb - t0 ? t0 + (int)left : nb; }
     __device__ __forceinline__ void next(const Kv4AttnArgs &a, int per_batch)
     {
-        left -= t1 - t0;
+        left -= nb + PAD - t0;
         if (left <= 0) return;
         t0 = 0;
         if (++i == per_batch) {
@@ -522,12 +520,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Shape sh, int ctas, int least)
+__global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Shape sh, int warps, int least)
 {
     extern __shared__ __align__(128) uint8_t dyn[];
-    Smem<D, NT> &sm = *reinterpret_cast<Smem<D, NT> *>(dyn);
-    constexpr int NS = stages<D>();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Smem<D> &sm = *reinterpret_cast<Smem<D> *>(dyn);
+    constexpr int NS = stages<D>(), NG = Kv4<D>::NG;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 0) {
         for (int w = 0; w < WARPS; ++w)
@@ -535,12 +533,13 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
         sm.abort = sm.never = 0;
         fence_mbar_init();
     }
-    // where the stretch begins: lane-strided sums, then the one sequence that holds it
+    // where the stretches begin: every thread sums up some sequences, and the one
+    // that holds a warp's beginning looks for it there
     const int B = a.rows.B, chunk = (B + WARPS * 32 - 1) / (WARPS * 32);
     int64_t mine = 0;
     for (int x = 0; x < chunk; ++x) {
         const int b = threadIdx.x * chunk + x;
-        if (b < B) mine += item_blocks(a, b);
+        if (b < B) mine += item_blocks(a, b) + PAD;
     }
     int64_t upto = mine;
 #pragma unroll
@@ -551,46 +550,52 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     if (lane == 31) sm.scan[warp] = upto;
     __syncthreads();
     int64_t all = 0;
+#pragma unroll
     for (int w = 0; w < WARPS; ++w) {
         if (w < warp) upto += sm.scan[w];
         all += sm.scan[w];
     }
     all *= sh.per_batch;
-    const int64_t per = stretch(all, ctas, least), f0 = per * blockIdx.x;
-    if (f0 >= all) return;
-    if (f0 < upto * sh.per_batch && f0 >= (upto - mine) * sh.per_batch) {
-        int b = threadIdx.x * chunk;
-        int64_t before = upto - mine;
-        for (int n; f0 >= (before + (n = item_blocks(a, b))) * sh.per_batch; ++b) before += n;
-        sm.found[0] = b;
-        sm.found[1] = before;
+    const int64_t per = stretch(all, warps, least);
+#pragma unroll 1
+    for (int w = 0; w < WARPS; ++w) {
+        const int64_t f = per * (blockIdx.x * WARPS + w);
+        if (f < upto * sh.per_batch && f >= (upto - mine) * sh.per_batch) {
+            int b = threadIdx.x * chunk;
+            int64_t before = upto - mine;
+            for (int n; f >= (before + (n = item_blocks(a, b) + PAD)) * sh.per_batch; ++b) before += n;
+            sm.seq[w] = b;
+            sm.before[w] = before;
+        }
     }
     __syncthreads();
+    const int64_t self = blockIdx.x * WARPS + warp, f0 = per * self;
+    if (f0 >= all) return;
     Walk at;
-    at.b = (int)sm.found[0];
+    at.b = sm.seq[warp];
     at.nb = item_blocks(a, at.b);
-    const int64_t rest = f0 - sm.found[1] * sh.per_batch;
-    at.i = (int)(rest / at.nb);
-    at.t0 = (int)(rest % at.nb);
+    const int64_t rest = f0 - sm.before[warp] * sh.per_batch;
+    at.i = (int)(rest / (at.nb + PAD));
+    at.t0 = (int)(rest % (at.nb + PAD));
     at.left = min(per, all - f0);
     at.cut();
     Walk ahead = at;                        // the piece that copies are issued for
     const WaitCtl wc{a.pool.err, &sm.abort, a.limit_ns};
     const int ps = a.pool.page_shift, bpp = 1 << (ps - 4);
-    // The issuing side: each lane works out one of the warp's next 32 blocks.
+    // The issuing side: each lane works out one of the next 32 blocks of a piece.
     int batch = 0, batch_n = 0;             // blocks of the batch issued, blocks in it
-    int done_t = ahead.t0 + warp;           // next block of the piece to be worked out
+    int next_t = ahead.t0;                  // next block of the piece to be worked out
     const uint8_t *src = nullptr;
     int src_slot = -1;
     unsigned issued = 0, taken = 0;
     bool dead = false;
-    auto refill = [&]() {                   // false: the stretch has no more blocks for this warp
-        while (ahead.valid() && done_t >= ahead.t1) {
+    auto refill = [&]() {                   // false: the stretch has no more blocks
+        while (ahead.valid() && next_t >= ahead.t1) {
             ahead.next(a, sh.per_batch);
-            done_t = ahead.t0 + warp;
+            next_t = ahead.t0;
         }
         if (!ahead.valid()) return false;
-        const int t = done_t + lane * WARPS;
+        const int t = next_t + lane;
         src = nullptr;
         src_slot = -1;
         if (t < ahead.t1) {
@@ -615,10 +620,10 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
                 }
             }
         }
-        const int n = (ahead.t1 - done_t + WARPS - 1) / WARPS;
+        const int n = ahead.t1 - next_t;
         batch_n = n < 32 ? n : 32;
         batch = 0;
-        done_t += 32 * WARPS;
+        next_t += 32;
         return true;
     };
     auto issue = [&]() {
@@ -640,12 +645,13 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     for (int s = 0; s < NS; ++s) issue();
     __syncwarp();
     for (; at.valid(); at.next(a, sh.per_batch)) {
+        if (at.t0 >= at.t1) continue;
         const Item it = decode_item(sh, a.pool.Hkv, at.b, at.i);
         Rows<D, NT> r;
         load_rows<D, NT>(a, sh, it, kv4_len(a.pool, at.b), r);
         State<D, NT> s;
         s.clear();
-        for (int t = at.t0 + warp; t < at.t1; t += WARPS) {
+        for (int t = at.t0; t < at.t1; ++t) {
             const int st = taken % NS;
             if (!dead && !waitw(smem_u32(&sm.full[warp][st]), (taken / NS) & 1, wc)) dead = true;
             if (dead) break;
@@ -656,8 +662,8 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
             issue();
             __syncwarp();                    // ... and the slot is written before the next round reads it
         }
-        // the warps' sums joined
-        const int g = lane >> 2, c = lane & 3;
+        const bool whole = at.t0 == 0 && at.t1 == at.nb;
+        float *part = static_cast<float *>(a.ws) + (2 * self + (at.t0 == 0 ? 1 : 0)) * Part<D, NT>::FLOATS;
 #pragma unroll
         for (int u = 0; u < NT; ++u)
 #pragma unroll
@@ -665,45 +671,27 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
                 float l = s.l[u][e];
 #pragma unroll
                 for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                const int row = u * 8 + 2 * c + e;
-                if (g == 0) sm.m[warp][row] = s.m[u][e], sm.l[warp][row] = l;
+                const int row = u * 8 + 2 * c + e, rr = it.tile * NT * 8 + row;
+                if (rr >= sh.rows) continue;
+                const float m = s.m[u][e];
+                if (!whole) {
+                    if (g == 0) part[row] = m, part[8 * NT + row] = l;
 #pragma unroll
-                for (int gr = 0; gr < Kv4<D>::NG; ++gr)
-                    *reinterpret_cast<float4 *>(&sm.o[warp][row][32 * gr + 4 * g]) = make_float4(
-                        s.o[u][2 * gr][e], s.o[u][2 * gr][e + 2], s.o[u][2 * gr + 1][e], s.o[u][2 * gr + 1][e + 2]);
-            }
-        __syncthreads();
-        const bool whole = at.t0 == 0 && at.t1 == at.nb;
-        float *part = static_cast<float *>(a.ws) + (2 * (int64_t)blockIdx.x + (at.t0 == 0 ? 1 : 0)) * Part<D, NT>::FLOATS;
-        for (int x = threadIdx.x; x < NT * 8 * (D / 4); x += WARPS * 32) {
-            const int row = x / (D / 4), d4 = x % (D / 4);
-            const int rr = it.tile * NT * 8 + row;
-            if (rr >= sh.rows) continue;
-            float m = -INFINITY, l = 0.f;
+                    for (int gr = 0; gr < NG; ++gr)
+                        *reinterpret_cast<float4 *>(part + 16 * NT + row * D + 32 * gr + 4 * g) = make_float4(
+                            s.o[u][2 * gr][e], s.o[u][2 * gr][e + 2], s.o[u][2 * gr + 1][e], s.o[u][2 * gr + 1][e + 2]);
+                    continue;
+                }
+                const int j = it.j0 + rr / sh.group, head = it.h * sh.group + rr % sh.group;
+                const bool empty = l == 0.f;
+                const float inv = empty ? 0.f : 1.f / l;
+                const int64_t at_out = (((int64_t)it.b * a.rows.n + j) * a.rows.Hq + head) * D;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) m = fmaxf(m, sm.m[w][row]);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const float mw = sm.m[w][row];
-                const float f = mw == m ? 1.f : ex2(mw - m);
-                l = fmaf(f, sm.l[w][row], l);
-                const float4 v = *reinterpret_cast<const float4 *>(&sm.o[w][row][d4 * 4]);
-                o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+                for (int gr = 0; gr < NG; ++gr)
+                    put_out(a, at_out + 32 * gr + 4 * g, make_float4(s.o[u][2 * gr][e] * inv, s.o[u][2 * gr][e + 2] * inv,
+                                                                     s.o[u][2 * gr + 1][e] * inv, s.o[u][2 * gr + 1][e + 2] * inv));
+                if (g == 0) a.lse[((int64_t)it.b * a.rows.Hq + head) * a.rows.n + j] = empty ? -INFINITY : fmaf(m, LN2, logf(l));
             }
-            if (!whole) {
-                *reinterpret_cast<float4 *>(part + 16 * NT + row * D + d4 * 4) = o;
-                if (d4 == 0) part[row] = m, part[8 * NT + row] = l;
-                continue;
-            }
-            const int j = it.j0 + rr / sh.group, head = it.h * sh.group + rr % sh.group;
-            const bool empty = l == 0.f;
-            const float inv = empty ? 0.f : 1.f / l;
-            put_out(a, (((int64_t)it.b * a.rows.n + j) * a.rows.Hq + head) * D + d4 * 4,
-                    make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-            if (d4 == 0) a.lse[((int64_t)it.b * a.rows.Hq + head) * a.rows.n + j] = empty ? -INFINITY : fmaf(m, LN2, logf(l));
-        }
-        __syncthreads();                     // before the next piece writes sm.o
     }
     // after a wait that ran out: copies that were issued land before the block ends
     const WaitCtl drain{a.pool.err, &sm.never, a.drain_ns};
@@ -714,7 +702,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
 constexpr int JOIN_WARPS = 8;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) kv4_join_kernel(Kv4AttnArgs a, Shape sh, int ctas, int least)
+__global__ void __launch_bounds__(JOIN_WARPS * 32) kv4_join_kernel(Kv4AttnArgs a, Shape sh, int warps, int least)
 {
     __shared__ int64_t red[2 * JOIN_WARPS];
     __shared__ float sm_m[JOIN_WARPS], sm_l[JOIN_WARPS];
@@ -727,13 +715,13 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv4_join_kernel(Kv4AttnArgs a
     int64_t all, before;
     count_blocks<JOIN_WARPS * 32>(a, b, all, before, red);
     all *= sh.per_batch;
-    const int64_t per = stretch(all, ctas, least);
+    const int64_t per = stretch(all, warps, least);
     const int nb = item_blocks(a, b);
     // the item of this row: token, row tile, kv head
     const int tile = rr_all / (NT * 8), row = rr_all % (NT * 8);
     const int h = x % a.pool.Hkv, j0 = x / a.pool.Hkv;
     const int i = (j0 * sh.tiles + tile) * a.pool.Hkv + h;
-    const int64_t f = before * sh.per_batch + (int64_t)i * nb;
+    const int64_t f = before * sh.per_batch + (int64_t)i * (nb + PAD);
     const int c0 = (int)(f / per), c1 = (int)((f + nb - 1) / per);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c0 == c1) return;
@@ -779,30 +767,29 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv4_join_kernel(Kv4AttnArgs a
     if (threadIdx.x == 0) a.lse[((int64_t)b * a.rows.Hq + head) * a.rows.n + j] = empty ? -INFINITY : fmaf(m, LN2, logf(l));
 }
 
-constexpr int MAX_CTAS = 640;     // what the workspace has room for
-constexpr int LEAST = 8;          // blocks that a CTA takes at least: two per warp
+constexpr int MAX_ROWS = 2560 * 8;   // rows of warps' parts that the workspace has room for (twice)
+constexpr int LEAST = 4;             // blocks that a warp takes at least
 
 template <int D, int NT>
 int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
 {
-    constexpr int smem = sizeof(Smem<D, NT>);
+    constexpr int smem = sizeof(Smem<D>);
     int resident = 0;
     if (cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kv4_attn_kernel<D, NT>, WARPS * 32, smem) != cudaSuccess ||
         resident < 1)
         return CP_ECUDA;
-    int ctas = resident * sm_count();
-    if (ctas > MAX_CTAS) ctas = MAX_CTAS;
+    const int64_t ctas = min(resident * sm_count(), MAX_ROWS / (NT * 8 * WARPS));
     // an upper bound of the line from the sizes alone
     const int64_t most = a.sel ? (int64_t)a.n_sel << (a.pool.page_shift - 4)
                                : ((int64_t)a.pool.max_pages << (a.pool.page_shift - 4));
-    const int64_t line = (most > 0 ? most : 1) * a.rows.B * sh.per_batch;
-    const int grid = (int)min((int64_t)ctas, (line + LEAST - 1) / LEAST);
+    const int64_t line = ((most > 0 ? most : 1) + PAD) * a.rows.B * sh.per_batch;
+    const int grid = (int)min(ctas, (line + LEAST * WARPS - 1) / (LEAST * WARPS));
     const int64_t joins = (int64_t)a.rows.B * (sh.per_batch / sh.tiles) * sh.rows;
     if (joins > 0x7fffffffLL) return CP_EUNSUPPORTED;
-    kv4_attn_kernel<D, NT><<<grid, WARPS * 32, smem, st>>>(a, sh, grid, LEAST);
+    const int warps = grid * WARPS;
+    kv4_attn_kernel<D, NT><<<grid, WARPS * 32, smem, st>>>(a, sh, warps, LEAST);
     if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
-    if (grid == 1) return CP_OK;             // nothing was cut
     // its blocks start while the first kernel's end, and wait for its results
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)joins);
@@ -813,7 +800,7 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, a, sh, grid, LEAST) == cudaSuccess ? CP_OK : CP_ECUDA;
+    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, a, sh, warps, LEAST) == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 
 }  // namespace
@@ -821,7 +808,7 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
 size_t kv4_attn_workspace_bytes(int D)
 {
     if (D != 64 && D != 128) return 0;
-    return (size_t)2 * MAX_CTAS * 2 * 8 * (D + 2) * sizeof(float);
+    return (size_t)2 * MAX_ROWS * (D + 2) * sizeof(float);
 }
 
 int launch_kv4_attn(const Kv4AttnArgs &a, int D, cudaStream_t st)
