@@ -112,7 +112,9 @@ __device__ __forceinline__ int new_tokens(const Kv4AppendArgs &a, int b)
     return m < 0 ? 0 : m > a.n ? a.n : m;
 }
 
-constexpr float F16_MAX = 65504.f;
+// Largest magnitude that is kept: with the roundings of s (half a step of 8, 15
+// times) and m (half of 32) on top, s code + m still rounds to a finite fp16.
+constexpr float KV4_MAX = 65408.f;
 
 // Codes, scale and minimum of a lane's 8 elements; the group is 4 lanes.
 __device__ __forceinline__ void quantise8(const float (&x)[8], int (&code)[8], __half &s, __half &m)
@@ -122,7 +124,7 @@ __device__ __forceinline__ void quantise8(const float (&x)[8], int (&code)[8], _
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         bad |= !isfinite(x[i]);
-        y[i] = fminf(fmaxf(x[i], -F16_MAX), F16_MAX);
+        y[i] = fminf(fmaxf(x[i], -KV4_MAX), KV4_MAX);
         lo = i ? fminf(lo, y[i]) : y[i];
         hi = i ? fmaxf(hi, y[i]) : y[i];
     }

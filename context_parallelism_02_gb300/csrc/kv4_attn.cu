@@ -48,6 +48,16 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // 8 x 8 transpose of 16-bit elements across the warp.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x)
 {
@@ -212,7 +222,7 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N])
     }
 }
 
-// Scores of one block, in log2 units: x[t][0..1] token g, x[t][2..3] token g + 8.
+// Scores of one block, in the row's units: x[t][0..1] token g, x[t][2..3] token g + 8.
 template <int D, int NT>
 __device__ __forceinline__ void block_scores(const uint8_t *blk, const Rows<D, NT> &r, float (&x)[NT][4])
 {
@@ -225,16 +235,12 @@ __device__ __forceinline__ void block_scores(const uint8_t *blk, const Rows<D, N
     load_words<NG>(blk + Kv4<D>::K_META + (g + 8) * 4 * NG, mb);
     // the minima of group c as both halves of a pair (k = 2c, 2c+1 and 2c+8, 2c+9)
     uint32_t na = 0, nb = 0;
-#pragma unroll
-    for (int gr = 0; gr < NG; ++gr)
-        if (gr == c) na = ma[gr], nb = mb[gr];
-    na = __byte_perm(na, na, 0x3232);
-    nb = __byte_perm(nb, nb, 0x3232);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
-        mma16816(x[t], na, nb, na, nb, r.sum[t][0], r.sum[t][1]);
+    if (NG == 4 || c < NG) {
+        na = *reinterpret_cast<const uint16_t *>(blk + Kv4<D>::K_META + (g * NG + c) * 4 + 2) * 0x10001u;
+        nb = *reinterpret_cast<const uint16_t *>(blk + Kv4<D>::K_META + ((g + 8) * NG + c) * 4 + 2) * 0x10001u;
     }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) mma16816_zero(x[t], na, nb, na, nb, r.sum[t][0], r.sum[t][1]);
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
         __half2 u[4], v[4];
@@ -243,8 +249,8 @@ __device__ __forceinline__ void block_scores(const uint8_t *blk, const Rows<D, N
         const float sa = __low2float(as_h2(ma[gr])), sb = __low2float(as_h2(mb[gr]));
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(acc, h2(u[0]), h2(v[0]), h2(u[1]), h2(v[1]), r.q[t][gr][0], r.q[t][gr][1]);
+            float acc[4];
+            mma16816_zero(acc, h2(u[0]), h2(v[0]), h2(u[1]), h2(v[1]), r.q[t][gr][0], r.q[t][gr][1]);
             mma16816(acc, h2(u[2]), h2(v[2]), h2(u[3]), h2(v[3]), r.q[t][gr][2], r.q[t][gr][3]);
             x[t][0] = fmaf(sa, acc[0], x[t][0]);
             x[t][1] = fmaf(sa, acc[1], x[t][1]);
@@ -252,15 +258,11 @@ __device__ __forceinline__ void block_scores(const uint8_t *blk, const Rows<D, N
             x[t][3] = fmaf(sb, acc[3], x[t][3]);
         }
     }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[t][e] *= r.to_log2[t][e & 1];
 }
 
 // Raises the references m where a score is more than 2^8 above them.
 template <int D, int NT, int NB>
-__device__ __forceinline__ void raise_max(const float (&x)[NB][NT][4], State<D, NT> &s)
+__device__ __forceinline__ void raise_max(const float (&x)[NB][NT][4], const Rows<D, NT> &r, State<D, NT> &s)
 {
     bool high = false;
     float top[NT][2];
@@ -268,11 +270,11 @@ __device__ __forceinline__ void raise_max(const float (&x)[NB][NT][4], State<D, 
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float v = -INFINITY;
+            float v = fmaxf(x[0][t][e], x[0][t][e + 2]);
 #pragma unroll
-            for (int i = 0; i < NB; ++i) v = fmaxf(v, fmaxf(x[i][t][e], x[i][t][e + 2]));
-            top[t][e] = v;
-            high |= v > s.m[t][e] + 8.f;
+            for (int i = 1; i < NB; ++i) v = fmaxf(v, fmaxf(x[i][t][e], x[i][t][e + 2]));
+            top[t][e] = v * r.to_log2[t][e];
+            high |= top[t][e] > s.m[t][e] + 8.f;
         }
     if (!__any_sync(0xffffffffu, high)) return;
 #pragma unroll
@@ -292,7 +294,7 @@ __device__ __forceinline__ void raise_max(const float (&x)[NB][NT][4], State<D, 
 }
 
 // V^T fragments of group gr of a block: f[e][half], e = 0..3 the elements
-// 32 gr + 4 g + e.  Tokens at or past `live` count as 0 whatever the block holds.
+// 32 gr + 4 g + e.
 template <int D>
 __device__ __forceinline__ void value_frags(const uint32_t (&w)[2], const uint2 (&sm)[2], uint32_t (&f)[4][2])
 {
@@ -305,27 +307,45 @@ __device__ __forceinline__ void value_frags(const uint32_t (&w)[2], const uint2 
     }
 }
 
-// O^T += V^T P^T for one block.  p: weights as B operands; live: tokens of the
-// block whose values count (the others are taken as 0, codes and scales may be
-// anything).
-template <int D, int NT>
-__device__ __forceinline__ void block_values(const uint8_t *blk, int live, const uint32_t (&p)[NT][2], State<D, NT> &s)
+// O^T += V^T P^T for one block, p the weights as B operands.  CUT: some row does
+// not see all of the block's tokens.  A token that no row sees (at or past `live`)
+// may hold anything, and one that only some rows see may hold NaN, which 0 times
+// would carry to the others: both count as 0, and the rows that do see a NaN get
+// it afterwards.  rel: the rows' limits from the block's first slot.
+template <int D, int NT, bool CUT>
+__device__ __forceinline__ void block_values(const uint8_t *blk, int live, const int (&rel)[NT][2],
+                                             const uint32_t (&p)[NT][2], State<D, NT> &s)
 {
     constexpr int NG = Kv4<D>::NG;
     const int lane = threadIdx.x & 31, c = lane & 3;
     uint32_t w[2][NG];
     uint2 sm[2][NG];
+    uint32_t nan[NG];   // tokens whose group is NaN
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
         load_words<NG>(blk + Kv4<D>::V_CODES + hf * 128 * NG + lane * 4 * NG, w[hf]);
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr)
-            sm[hf][gr] = *reinterpret_cast<const uint2 *>(blk + Kv4<D>::V_META + ((hf * 4 + c) * NG + gr) * 8);
-        if (live < KV4_BLOCK) {
-            const int k = hf * 8 + 2 * c;
-            const uint32_t keep = (k < live ? 0x0000ffffu : 0u) | (k + 1 < live ? 0xffff0000u : 0u);
+        for (int gr = 0; gr < NG; gr += 2) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(blk + Kv4<D>::V_META + ((hf * 4 + c) * NG + gr) * 8);
+            sm[hf][gr] = make_uint2(v.x, v.y);
+            sm[hf][gr + 1] = make_uint2(v.z, v.w);
+        }
+        if (CUT) {
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) sm[hf][gr].x &= keep, sm[hf][gr].y &= keep;
+            for (int gr = 0; gr < NG; ++gr) {
+                if (hf == 0) nan[gr] = 0;
+                uint2 &v = sm[hf][gr];
+#pragma unroll
+                for (int lo = 0; lo < 2; ++lo) {
+                    const int k = hf * 8 + 2 * c + lo;
+                    const uint32_t half = lo ? 0xffff0000u : 0x0000ffffu, exps = half & 0x7c007c00u;
+                    const bool bad = (v.x & exps) == exps || (v.y & exps) == exps;
+                    if (bad || k >= live) v.x &= ~half, v.y &= ~half;
+                    const unsigned who = __ballot_sync(0xffffffffu, bad && k < live);   // lanes c of every g alike
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) nan[gr] |= (who >> i & 1u) << (hf * 8 + 2 * i + lo);
+                }
+            }
         }
     }
 #pragma unroll
@@ -339,84 +359,72 @@ __device__ __forceinline__ void block_values(const uint8_t *blk, int live, const
             mma16816(s.o[t][2 * gr], f[0][0], f[1][0], f[0][1], f[1][1], p[t][0], p[t][1]);
             mma16816(s.o[t][2 * gr + 1], f[2][0], f[3][0], f[2][1], f[3][1], p[t][0], p[t][1]);
         }
+        if (CUT && nan[gr]) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int n = rel[t][e] < 0 ? 0 : rel[t][e] > 16 ? 16 : rel[t][e];
+                    if (nan[gr] & ((1u << n) - 1u)) s.o[t][2 * gr][e] = s.o[t][2 * gr][e + 2] = s.o[t][2 * gr + 1][e] =
+                        s.o[t][2 * gr + 1][e + 2] = __int_as_float(0x7fffffff);
+                }
+        }
     }
 }
 
-// Whether a block's V scales or minima hold a value that is not finite.
-template <int D>
-__device__ __forceinline__ bool values_bad(const uint8_t *blk)
-{
-    constexpr int NG = Kv4<D>::NG;
-    const int lane = threadIdx.x & 31;
-    bool bad = false;
-    for (int i = lane; i < 16 * NG; i += 32) {   // 16 NG words of two halves
-        const uint32_t w = reinterpret_cast<const uint32_t *>(blk + Kv4<D>::V_META)[i];
-        bad |= (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
-    }
-    return __any_sync(0xffffffffu, bad);
-}
+// First slot of a block that is not there: past every row's limit.
+constexpr int NO_SLOT = 0x7ffffff0;
 
-// One block of 16 tokens whose first slot is `slot`, for the warp's state.
-template <int D, int NT>
-__device__ __forceinline__ void block_step(const uint8_t *blk, int slot, const Rows<D, NT> &r, State<D, NT> &s)
+// NB blocks of 16 tokens, block i beginning at slot[i], for the warp's state.
+template <int D, int NT, int NB>
+__device__ __forceinline__ void blocks_step(const uint8_t *blk, const int (&slot)[NB], const Rows<D, NT> &r, State<D, NT> &s)
 {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    float x[1][NT][4];
-    block_scores<D, NT>(blk, r, x[0]);
-    const bool cut = slot > r.min_limit - KV4_BLOCK;
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    float x[NB][NT][4];
+    bool cut = false;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        block_scores<D, NT>(blk + i * Kv4<D>::BYTES, r, x[i]);
+        cut |= slot[i] > r.min_limit - KV4_BLOCK;
+    }
     if (cut) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (slot + g + (e >> 1) * 8 >= r.limit[t][e & 1]) x[0][t][e] = -INFINITY;
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (slot[i] + g + (e >> 1) * 8 >= r.limit[t][e & 1]) x[i][t][e] = -INFINITY;
     }
-    raise_max<D, NT, 1>(x, s);
-    uint32_t p[NT][2];
+    raise_max<D, NT, NB>(x, r, s);
+    uint32_t p[NB][NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        float w[4];
+        float base[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float m = s.m[t][e & 1];
-            w[e] = ex2(x[0][t][e] - (m == -INFINITY ? 0.f : m));
-            s.l[t][e & 1] += w[e];
-        }
-        p[t][0] = movmatrix(h2(__floats2half2_rn(w[0], w[1])));
-        p[t][1] = movmatrix(h2(__floats2half2_rn(w[2], w[3])));
-    }
-    const int live = r.max_limit - slot;
-    if (cut && live > 0 && r.min_limit < r.max_limit && values_bad<D>(blk)) {
-        // Rows see different tokens of this block and one of its values is not
-        // finite: 0 times it would reach the rows that do not see it.  Row by row.
-#pragma unroll 1
-        for (int q = 0; q < 8; ++q) {
-            uint32_t one[NT][2];
-            int mine = 0;
-#pragma unroll 1
-            for (int t = 0; t < NT; ++t) {
+        for (int e = 0; e < 2; ++e) base[e] = s.m[t][e] == -INFINITY ? 0.f : -s.m[t][e];
 #pragma unroll
-                for (int u = 0; u < NT; ++u) {
-                    const int lim = __shfl_sync(0xffffffffu, (q & 1) ? r.limit[u][1] : r.limit[u][0], q >> 1);
-                    if (u == t) mine = lim - slot;
-                    one[u][0] = u == t && g == q ? p[u][0] : 0u;
-                    one[u][1] = u == t && g == q ? p[u][1] : 0u;
-                }
-                State<D, NT> z;
-                z.clear();
-                block_values<D, NT>(blk, mine, one, z);
+        for (int i = 0; i < NB; ++i) {
+            float w[4];
 #pragma unroll
-                for (int u = 0; u < NT; ++u)
-#pragma unroll
-                    for (int i = 0; i < 2 * Kv4<D>::NG; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (u == t && 2 * c + (e & 1) == q) s.o[u][i][e] += z.o[u][i][e];
+            for (int e = 0; e < 4; ++e) {
+                w[e] = ex2(fmaf(x[i][t][e], r.to_log2[t][e & 1], base[e & 1]));
+                s.l[t][e & 1] += w[e];
             }
+            p[i][t][0] = movmatrix(h2(__floats2half2_rn(w[0], w[1])));
+            p[i][t][1] = movmatrix(h2(__floats2half2_rn(w[2], w[3])));
         }
-        return;
     }
-    block_values<D, NT>(blk, live, p, s);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const uint8_t *b = blk + i * Kv4<D>::BYTES;
+        const int live = r.max_limit - slot[i];
+        int rel[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) rel[t][0] = r.limit[t][0] - slot[i], rel[t][1] = r.limit[t][1] - slot[i];
+        if (!cut) block_values<D, NT, false>(b, live, rel, p[i], s);
+        else if (live > 0) block_values<D, NT, true>(b, live, rel, p[i], s);
+    }
 }
 
 template <int D, int NT>
@@ -424,20 +432,21 @@ struct Part {              // a piece's result in the workspace
     static constexpr int FLOATS = NT * 8 * (D + 2);   // m, l of each row, then the rows
 };
 
-// Blocks in a warp's ring.  12 warps per SM with 5 blocks of 2.5 KB on the way are
-// 150 KB, several times latency x bandwidth (about 46 KB per SM).
+constexpr int NB = 2;      // blocks of a stage, taken together
+
+// Stages of a warp's ring.
 template <int D>
-__host__ __device__ constexpr int stages() { return D == 128 ? 6 : 10; }
+__host__ __device__ constexpr int stages() { return D == 128 ? 3 : 5; }
 
 constexpr int PAD = 8;
 
 template <int D>
 struct Smem {
-    uint8_t ring[WARPS][stages<D>()][Kv4<D>::BYTES];
+    uint8_t ring[WARPS][stages<D>()][NB][Kv4<D>::BYTES];
     uint64_t full[WARPS][stages<D>()];
     int64_t scan[WARPS];
     int64_t before[WARPS];           // blocks before the sequence that a warp's stretch begins in
-    int slot[WARPS][stages<D>()];    // first slot of the block; -1: no block
+    int slot[WARPS][stages<D>()][NB];   // first slot of the block, or NO_SLOT
     int seq[WARPS];                  // that sequence
     int abort, never;
 };
@@ -529,7 +538,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 0) {
         for (int w = 0; w < WARPS; ++w)
-            for (int s = 0; s < NS; ++s) mbar_init(smem_u32(&sm.full[w][s]), 1);
+            for (int s = 0; s < NS; ++s) mbar_init(smem_u32(&sm.full[w][s]), NB);
         sm.abort = sm.never = 0;
         fence_mbar_init();
     }
@@ -583,11 +592,12 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     const WaitCtl wc{a.pool.err, &sm.abort, a.limit_ns};
     const int ps = a.pool.page_shift, bpp = 1 << (ps - 4);
     // The issuing side: each lane works out one of the next 32 blocks of a piece.
-    int batch = 0, batch_n = 0;             // blocks of the batch issued, blocks in it
+    int batch = 0, batch_n = 0;             // blocks of the batch issued, blocks in it (an even number)
     int next_t = ahead.t0;                  // next block of the piece to be worked out
     const uint8_t *src = nullptr;
-    int src_slot = -1;
-    unsigned issued = 0, taken = 0;
+    int src_slot = NO_SLOT;
+    unsigned issued = 0, taken = 0;         // stages
+    int put = 0, get = 0, phase = 0;        // the ring's ends
     bool dead = false;
     auto refill = [&]() {                   // false: the stretch has no more blocks
         while (ahead.valid() && next_t >= ahead.t1) {
@@ -597,7 +607,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
         if (!ahead.valid()) return false;
         const int t = next_t + lane;
         src = nullptr;
-        src_slot = -1;
+        src_slot = NO_SLOT;
         if (t < ahead.t1) {
             const Item it = decode_item(sh, a.pool.Hkv, ahead.b, ahead.i);
             const int len = kv4_len(a.pool, ahead.b);
@@ -621,26 +631,26 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
             }
         }
         const int n = ahead.t1 - next_t;
-        batch_n = n < 32 ? n : 32;
+        batch_n = n < 32 ? (n + NB - 1) / NB * NB : 32;
         batch = 0;
         next_t += 32;
         return true;
     };
     auto issue = [&]() {
         if (dead || (batch == batch_n && !refill())) return;
-        if (lane == batch) {
-            const int s = issued % NS;
-            const uint32_t bar = smem_u32(&sm.full[warp][s]);
-            sm.slot[warp][s] = src_slot;
+        if (lane >= batch && lane < batch + NB) {
+            const uint32_t bar = smem_u32(&sm.full[warp][put]);
+            sm.slot[warp][put][lane - batch] = src_slot;
             if (src) {
                 mbar_arrive_expect_tx(bar, Kv4<D>::BYTES);
-                bulk_load(smem_u32(sm.ring[warp][s]), src, Kv4<D>::BYTES, bar);
+                bulk_load(smem_u32(sm.ring[warp][put][lane - batch]), src, Kv4<D>::BYTES, bar);
             } else {
                 mbar_arrive(bar);
             }
         }
-        ++batch;
+        batch += NB;
         ++issued;
+        if (++put == NS) put = 0;
     };
     for (int s = 0; s < NS; ++s) issue();
     __syncwarp();
@@ -651,16 +661,22 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
         load_rows<D, NT>(a, sh, it, kv4_len(a.pool, at.b), r);
         State<D, NT> s;
         s.clear();
-        for (int t = at.t0; t < at.t1; ++t) {
-            const int st = taken % NS;
-            if (!dead && !waitw(smem_u32(&sm.full[warp][st]), (taken / NS) & 1, wc)) dead = true;
+        for (int t = at.t0; t < at.t1; t += NB) {
+            if (!dead && !waitw(smem_u32(&sm.full[warp][get]), phase, wc)) dead = true;
             if (dead) break;
-            const int slot = sm.slot[warp][st];
-            if (slot >= 0 && slot < r.max_limit) block_step<D, NT>(sm.ring[warp][st], slot, r, s);
+            int slot[NB];
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                slot[i] = sm.slot[warp][get][i];
+                any |= slot[i] < r.max_limit;
+            }
+            if (any) blocks_step<D, NT, NB>(sm.ring[warp][get][0], slot, r, s);
             ++taken;
+            if (++get == NS) get = 0, phase ^= 1;
             __syncwarp();                    // every lane has read the stage
             issue();
-            __syncwarp();                    // ... and the slot is written before the next round reads it
+            __syncwarp();                    // ... and the slots are written before the next round reads them
         }
         const bool whole = at.t0 == 0 && at.t1 == at.nb;
         float *part = static_cast<float *>(a.ws) + (2 * self + (at.t0 == 0 ? 1 : 0)) * Part<D, NT>::FLOATS;
@@ -695,7 +711,10 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     }
     // after a wait that ran out: copies that were issued land before the block ends
     const WaitCtl drain{a.pool.err, &sm.never, a.drain_ns};
-    for (; taken < issued; ++taken) waitw(smem_u32(&sm.full[warp][taken % NS]), (taken / NS) & 1, drain);
+    for (; taken < issued; ++taken) {
+        waitw(smem_u32(&sm.full[warp][get]), phase, drain);
+        if (++get == NS) get = 0, phase ^= 1;
+    }
 }
 
 // Joins the pieces of the items that were cut: one block per output row.

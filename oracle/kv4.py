@@ -39,7 +39,7 @@ def quantise(x):
     x = np.asarray(x, F32)
     g = x.reshape(*x.shape[:-1], -1, 32)
     bad = ~np.isfinite(g).all(-1, keepdims=True)
-    y = np.clip(np.where(bad, F32(0), g), F32(-65504), F32(65504))
+    y = np.clip(np.where(bad, F32(0), g), F32(-65408), F32(65408))
     lo, hi = y.min(-1, keepdims=True), y.max(-1, keepdims=True)
     s = ((hi - lo) / F32(15)).astype(F16)
     m = lo.astype(F16)

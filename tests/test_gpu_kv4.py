@@ -143,9 +143,26 @@ def test_append_values_that_are_not_finite_or_too_large(cuda_dev):
     x = gk[0, :, 0].cpu()
     assert x[0, :32].isnan().all() and (x[0, 32:] == 0).all()
     assert x[1, 32:].isnan().all() and (x[1, :32] == 0).all()
-    assert (x[2, :31] == -65504).all() and x[2].abs().max() <= 65504 + 2 ** 5 and (x[3] == 2.5).all()
+    # -65408 is an fp16 (a multiple of 32); + 15 roundings of the scale, at most 4 each
+    assert (x[2, :31] == -65408).all() and x[2].abs().max() <= 65408 + 15 * 4 + 16 and (x[3] == 2.5).all()
     s = summ[0, 0].float().cpu()               # a key that is not finite opens its elements' range
     assert s[0, 3] == -math.inf and s[1, 3] == math.inf and s[0, 40] == -math.inf and s[1, 40] == math.inf
+
+
+def test_attn_of_the_largest_values_is_finite(cuda_dev):
+    """Values of both signs at the end of the range in one group: s code + m stays below fp16's overflow (65520)."""
+    D = 64
+    v = (torch.ones(1, 8, 1, D, device="cuda") * 1e30).cumprod(-1).clamp(max=1e30)
+    v[..., ::2] *= -1
+    v[0, 1] *= 0.5e-30 * 65408                    # other scales, whose roundings go other ways
+    v[0, 2] = v[0, 0].sign() * 65000
+    cache, lens = api.kv4_cache(1, 1, 16, D), dev(np.array([0], np.int32))
+    pages = dev(np.array([[0]], np.int32))
+    api.kv4_append(torch.zeros_like(v), v, cache, pages, lens)
+    q = torch.zeros(1, 1, 1, D, dtype=torch.bfloat16, device="cuda")
+    out, _ = api.kv4_attn(q, cache, pages, lens + 8)
+    ok()
+    assert torch.isfinite(out).all()
 
 
 GATHER = [(1, 1, 1, 128, 64), (2, 100, 2, 64, 16), (3, 77, 1, 128, 32), (2, 300, 2, 64, 256)]
