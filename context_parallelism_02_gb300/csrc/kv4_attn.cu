@@ -440,6 +440,36 @@ __host__ __device__ constexpr int stages() { return D == 128 ? 3 : 5; }
 
 constexpr int PAD = 8;
 
+// Blocks of one item of sequence b (at least 1, so that every item is written).
+__device__ __forceinline__ int item_blocks(const Kv4AttnArgs &a, int b)
+{
+    if (a.sel) return a.n_sel << (a.pool.page_shift - 4);
+    const int len = kv4_len(a.pool, b);
+    return len > 0 ? (len - 1) / KV4_BLOCK + 1 : 1;
+}
+
+// A walk over the pieces of a warp's stretch.
+struct Walk {
+    int b, i;        // sequence, item of it
+    int nb;          // the item's blocks
+    int t0, t1;      // the piece: blocks [t0, t1) of the item, none if t0 >= t1
+    int64_t left;    // what remains of the stretch, from t0 on
+    __device__ __forceinline__ bool valid() const { return left > 0; }
+    __device__ __forceinline__ void cut() { t1 = left < nb - t0 ? t0 + (int)left : nb; }
+    __device__ __forceinline__ void next(const Kv4AttnArgs &a, int per_batch)
+    {
+        left -= nb + PAD - t0;
+        if (left <= 0) return;
+        t0 = 0;
+        if (++i == per_batch) {
+            i = 0;
+            ++b;
+            nb = item_blocks(a, b);
+        }
+        cut();
+    }
+};
+
 template <int D>
 struct Smem {
     uint8_t ring[WARPS][stages<D>()][NB][Kv4<D>::BYTES];
@@ -448,16 +478,9 @@ struct Smem {
     int64_t before[WARPS];           // blocks before the sequence that a warp's stretch begins in
     int slot[WARPS][stages<D>()][NB];   // first slot of the block, or NO_SLOT
     int seq[WARPS];                  // that sequence
+    Walk ahead[WARPS];               // the piece that a warp's copies are issued for
     int abort, never;
 };
-
-// Blocks of one item of sequence b (at least 1, so that every item is written).
-__device__ __forceinline__ int item_blocks(const Kv4AttnArgs &a, int b)
-{
-    if (a.sel) return a.n_sel << (a.pool.page_shift - 4);
-    const int len = kv4_len(a.pool, b);
-    return len > 0 ? (len - 1) / KV4_BLOCK + 1 : 1;
-}
 
 // Over the batch, with every thread of the block (T of them): the extent of one
 // item of every sequence, and of those before sequence `upto`.
@@ -488,28 +511,6 @@ __device__ __forceinline__ int64_t stretch(int64_t all, int warps, int least)
     const int64_t per = (all + warps - 1) / warps;
     return per > least ? per : least;
 }
-
-// A walk over the pieces of a warp's stretch.
-struct Walk {
-    int b, i;        // sequence, item of it
-    int nb;          // the item's blocks
-    int t0, t1;      // the piece: blocks [t0, t1) of the item, none if t0 >= t1
-    int64_t left;    // what remains of the stretch, from t0 on
-    __device__ __forceinline__ bool valid() const { return left > 0; }
-    __device__ __forceinline__ void cut() { t1 = left < nb - t0 ? t0 + (int)left : nb; }
-    __device__ __forceinline__ void next(const Kv4AttnArgs &a, int per_batch)
-    {
-        left -= nb + PAD - t0;
-        if (left <= 0) return;
-        t0 = 0;
-        if (++i == per_batch) {
-            i = 0;
-            ++b;
-            nb = item_blocks(a, b);
-        }
-        cut();
-    }
-};
 
 // One output row's four elements.
 __device__ __forceinline__ void put_out(const Kv4AttnArgs &a, int64_t at, float4 o)
@@ -588,7 +589,10 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     at.t0 = (int)(rest % (at.nb + PAD));
     at.left = min(per, all - f0);
     at.cut();
-    Walk ahead = at;                        // the piece that copies are issued for
+    Walk &ahead = sm.ahead[warp];           // the same in every lane
+    __syncwarp();
+    ahead = at;
+    __syncwarp();
     const WaitCtl wc{a.pool.err, &sm.abort, a.limit_ns};
     const int ps = a.pool.page_shift, bpp = 1 << (ps - 4);
     // The issuing side: each lane works out one of the next 32 blocks of a piece.
@@ -600,17 +604,21 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     int put = 0, get = 0, phase = 0;        // the ring's ends
     bool dead = false;
     auto refill = [&]() {                   // false: the stretch has no more blocks
-        while (ahead.valid() && next_t >= ahead.t1) {
-            ahead.next(a, sh.per_batch);
-            next_t = ahead.t0;
+        Walk w = ahead;
+        while (w.valid() && next_t >= w.t1) {
+            w.next(a, sh.per_batch);
+            next_t = w.t0;
         }
-        if (!ahead.valid()) return false;
+        __syncwarp();
+        ahead = w;
+        __syncwarp();
+        if (!w.valid()) return false;
         const int t = next_t + lane;
         src = nullptr;
         src_slot = NO_SLOT;
-        if (t < ahead.t1) {
-            const Item it = decode_item(sh, a.pool.Hkv, ahead.b, ahead.i);
-            const int len = kv4_len(a.pool, ahead.b);
+        if (t < w.t1) {
+            const Item it = decode_item(sh, a.pool.Hkv, w.b, w.i);
+            const int len = kv4_len(a.pool, w.b);
             int lp = t >> (ps - 4);
             bool on = true;
             if (a.sel) {
@@ -630,7 +638,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
                 }
             }
         }
-        const int n = ahead.t1 - next_t;
+        const int n = w.t1 - next_t;
         batch_n = n < 32 ? (n + NB - 1) / NB * NB : 32;
         batch = 0;
         next_t += 32;
@@ -717,22 +725,25 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     }
 }
 
-// Joins the pieces of the items that were cut: one block per output row.
-constexpr int JOIN_WARPS = 8;
+// Joins the pieces of the items that were cut: one block per output row.  The
+// parts are read JOIN_DEEP at a time per warp, so that a row of many pieces (one
+// long sequence: up to all warps of the grid) costs a few memory latencies.
+constexpr int JOIN_DEEP = 4;
 
-template <int D, int NT>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) kv4_join_kernel(Kv4AttnArgs a, Shape sh, int warps, int least)
+template <int D, int NT, int JW>
+__global__ void __launch_bounds__(JW * 32) kv4_join_kernel(Kv4AttnArgs a, Shape sh, int warps, int least)
 {
-    __shared__ int64_t red[2 * JOIN_WARPS];
-    __shared__ float sm_m[JOIN_WARPS], sm_l[JOIN_WARPS];
-    __shared__ __align__(16) float sm_o[JOIN_WARPS][D];
+    constexpr int E = D / 32;
+    __shared__ int64_t red[2 * JW];
+    __shared__ float sm_m[JW], sm_l[JW];
+    __shared__ __align__(16) float sm_o[JW][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t item = blockIdx.x / sh.rows;
     const int rr_all = blockIdx.x % sh.rows;
     const int b = (int)(item / (sh.per_batch / sh.tiles));
     const int x = (int)(item % (sh.per_batch / sh.tiles));      // (token, kv head)
     int64_t all, before;
-    count_blocks<JOIN_WARPS * 32>(a, b, all, before, red);
+    count_blocks<JW * 32>(a, b, all, before, red);
     all *= sh.per_batch;
     const int64_t per = stretch(all, warps, least);
     const int nb = item_blocks(a, b);
@@ -744,45 +755,68 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv4_join_kernel(Kv4AttnArgs a
     const int c0 = (int)(f / per), c1 = (int)((f + nb - 1) / per);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c0 == c1) return;
+    const float *ws = static_cast<const float *>(a.ws);
     float m = -INFINITY, l = 0.f;
-    float o[D / 32];
+    float o[E];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-    for (int c = c0 + warp; c <= c1; c += JOIN_WARPS) {
-        const float *part = static_cast<const float *>(a.ws) + (2 * (int64_t)c + (f >= c * per ? 1 : 0)) * Part<D, NT>::FLOATS;
-        const float pm = part[row], pl = part[8 * NT + row];
-        float v[D / 32];
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int c = c0 + warp * JOIN_DEEP; c <= c1; c += JW * JOIN_DEEP) {
+        float pm[JOIN_DEEP], pl[JOIN_DEEP], v[JOIN_DEEP][E], mn = m;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) v[e] = part[16 * NT + row * D + e * 32 + lane];
-        const float mn = fmaxf(m, pm);
-        const float fa = m == mn ? 1.f : ex2(m - mn), fb = pm == mn ? 1.f : ex2(pm - mn);
-        l = fmaf(l, fa, pl * fb);
+        for (int u = 0; u < JOIN_DEEP; ++u) {
+            pm[u] = -INFINITY;
+            pl[u] = 0.f;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[e] = fmaf(o[e], fa, v[e] * fb);
+            for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+            if (c + u > c1) continue;
+            const float *part = ws + (2 * (int64_t)(c + u) + (f >= (c + u) * per ? 1 : 0)) * Part<D, NT>::FLOATS;
+            pm[u] = part[row];
+            pl[u] = part[8 * NT + row];
+            if (E == 4) {
+                const float4 w = *reinterpret_cast<const float4 *>(part + 16 * NT + row * D + lane * 4);
+                v[u][0] = w.x, v[u][1] = w.y, v[u][E - 2] = w.z, v[u][E - 1] = w.w;
+            } else {
+                const float2 w = *reinterpret_cast<const float2 *>(part + 16 * NT + row * D + lane * 2);
+                v[u][0] = w.x, v[u][1] = w.y;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < JOIN_DEEP; ++u) mn = fmaxf(mn, pm[u]);
+        const float fa = m == mn ? 1.f : ex2(m - mn);
+        l *= fa;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= fa;
+#pragma unroll
+        for (int u = 0; u < JOIN_DEEP; ++u) {
+            const float fu = pm[u] == mn ? 1.f : ex2(pm[u] - mn);
+            l = fmaf(pl[u], fu, l);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(v[u][e], fu, o[e]);
+        }
         m = mn;
     }
     if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) sm_o[warp][e * 32 + lane] = o[e];
+    for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = o[e];
     __syncthreads();
-    if (threadIdx.x >= D / 4) return;
+    if (threadIdx.x >= D) return;
     m = -INFINITY;
     l = 0.f;
 #pragma unroll
-    for (int w = 0; w < JOIN_WARPS; ++w) m = fmaxf(m, sm_m[w]);
-    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < JW; ++w) m = fmaxf(m, sm_m[w]);
+    float r = 0.f;
 #pragma unroll
-    for (int w = 0; w < JOIN_WARPS; ++w) {
+    for (int w = 0; w < JW; ++w) {
         const float fw = sm_m[w] == m ? 1.f : ex2(sm_m[w] - m);
         l = fmaf(fw, sm_l[w], l);
-        const float4 v = *reinterpret_cast<const float4 *>(&sm_o[w][threadIdx.x * 4]);
-        r.x = fmaf(fw, v.x, r.x), r.y = fmaf(fw, v.y, r.y), r.z = fmaf(fw, v.z, r.z), r.w = fmaf(fw, v.w, r.w);
+        r = fmaf(fw, sm_o[w][threadIdx.x], r);
     }
     const int j = j0 + rr_all / sh.group, head = h * sh.group + rr_all % sh.group;
     const bool empty = l == 0.f;
-    const float inv = empty ? 0.f : 1.f / l;
-    put_out(a, (((int64_t)b * a.rows.n + j) * a.rows.Hq + head) * D + threadIdx.x * 4,
-            make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv));
+    r *= empty ? 0.f : 1.f / l;
+    const int64_t at = (((int64_t)b * a.rows.n + j) * a.rows.Hq + head) * D + threadIdx.x;
+    if (a.out_f32) static_cast<float *>(a.out)[at] = r;
+    else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(r);
     if (threadIdx.x == 0) a.lse[((int64_t)b * a.rows.Hq + head) * a.rows.n + j] = empty ? -INFINITY : fmaf(m, LN2, logf(l));
 }
 
@@ -809,17 +843,21 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
     const int warps = grid * WARPS;
     kv4_attn_kernel<D, NT><<<grid, WARPS * 32, smem, st>>>(a, sh, warps, LEAST);
     if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
-    // its blocks start while the first kernel's end, and wait for its results
+    // its blocks start while the first kernel's end, and wait for its results;
+    // many warps where a row is cut into many pieces
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)joins);
-    cfg.blockDim = dim3(JOIN_WARPS * 32);
-    cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)joins);
+    cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, a, sh, warps, LEAST) == cudaSuccess ? CP_OK : CP_ECUDA;
+    const bool wide = (int64_t)warps > 32 * (int64_t)a.rows.B * sh.per_batch;
+    cfg.blockDim = dim3(wide ? 1024 : 128);
+    const cudaError_t rc = wide ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 32>, a, sh, warps, LEAST)
+                                : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 4>, a, sh, warps, LEAST);
+    return rc == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 
 }  // namespace
