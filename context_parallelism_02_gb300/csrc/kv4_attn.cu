@@ -152,9 +152,32 @@ __device__ __forceinline__ Item decode_item(const Shape &s, int Hkv, int b, int 
     return it;
 }
 
+// A lane's share of the rows as they are in memory, so that their latency can
+// overlap with other loads.
 template <int D, int NT>
-__device__ __forceinline__ void load_rows(const Kv4AttnArgs &a, const Shape &sh, const Item &it, int len,
-                                          Rows<D, NT> &r)
+struct RawRows {
+    uint4 w[NT][Kv4<D>::NG];
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void fetch_rows(const Kv4AttnArgs &a, const Shape &sh, const Item &it, RawRows<D, NT> &raw)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int row = (it.tile * NT + t) * 8 + g;
+        const bool on = row < sh.rows;
+        const int j = it.j0 + (on ? row / sh.group : 0);
+        const int head = it.h * sh.group + (on ? row % sh.group : 0);
+        const uint4 *p = reinterpret_cast<const uint4 *>(a.q + (((int64_t)it.b * a.rows.n + j) * a.rows.Hq + head) * D);
+#pragma unroll
+        for (int gr = 0; gr < Kv4<D>::NG; ++gr) raw.w[t][gr] = on ? __ldg(p + gr * 4 + c) : make_uint4(0, 0, 0, 0);
+    }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void make_rows(const Kv4AttnArgs &a, const Shape &sh, const Item &it, int len,
+                                          const RawRows<D, NT> &raw, Rows<D, NT> &r)
 {
     constexpr int NG = Kv4<D>::NG;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -164,13 +187,10 @@ __device__ __forceinline__ void load_rows(const Kv4AttnArgs &a, const Shape &sh,
         const int row = (it.tile * NT + t) * 8 + g;
         const bool on = row < sh.rows;
         const int j = it.j0 + (on ? row / sh.group : 0);
-        const int head = it.h * sh.group + (on ? row % sh.group : 0);
-        uint4 w[NG];
+        const uint4(&w)[NG] = raw.w[t];
         float top = 0.f;
-        const uint4 *p = reinterpret_cast<const uint4 *>(a.q + (((int64_t)it.b * a.rows.n + j) * a.rows.Hq + head) * D);
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-            w[gr] = on ? __ldg(p + gr * 4 + c) : make_uint4(0, 0, 0, 0);
             const uint32_t x[4] = {w[gr].x, w[gr].y, w[gr].z, w[gr].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -484,10 +504,7 @@ template <int D>
 struct Smem {
     uint8_t ring[WARPS][stages<D>()][NB][Kv4<D>::BYTES];
     uint64_t full[WARPS][stages<D>()];
-    int64_t scan[WARPS];
-    int64_t before[WARPS];           // blocks before the sequence that a warp's stretch begins in
     int slot[WARPS][stages<D>()][NB];   // first slot of the block, or NO_SLOT
-    int seq[WARPS];                  // that sequence
     Walk ahead[WARPS];               // the piece that a warp's copies are issued for
     int abort, never;
 };
@@ -532,6 +549,12 @@ __device__ __forceinline__ void put_out(const Kv4AttnArgs &a, int64_t at, float4
             make_uint2(tc::pack_bf16(o.x, o.y), tc::pack_bf16(o.z, o.w));
 }
 
+// Line `at` of an array of `bytes` bytes into L2.
+__device__ __forceinline__ void prefetch(const void *p, int64_t at, int64_t bytes)
+{
+    if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p) + at));
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -547,58 +570,61 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     constexpr int NS = stages<D>(), NG = Kv4<D>::NG;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;");
-    if (threadIdx.x == 0) {
-        for (int w = 0; w < WARPS; ++w)
-            for (int s = 0; s < NS; ++s) mbar_init(smem_u32(&sm.full[w][s]), NB);
-        sm.abort = sm.never = 0;
-        fence_mbar_init();
+    {   // what the chain of loads below will need, on its way to L2
+        const int64_t line = ((int64_t)blockIdx.x * (WARPS * 32) + threadIdx.x) * 128;
+        prefetch(a.pool.pages, line, (int64_t)a.rows.B * a.pool.max_pages * 4);
+        prefetch(a.q, line, (int64_t)a.rows.B * a.rows.n * a.rows.Hq * D * 2);
+        if (a.sel) prefetch(a.sel, line, (int64_t)a.rows.B * a.rows.n * a.pool.Hkv * a.n_sel * 4);
     }
-    // where the stretches begin: every thread sums up some sequences, and the one
-    // that holds a warp's beginning looks for it there
-    const int B = a.rows.B, chunk = (B + WARPS * 32 - 1) / (WARPS * 32);
-    int64_t mine = 0;
-    for (int x = 0; x < chunk; ++x) {
-        const int b = threadIdx.x * chunk + x;
-        if (b < B) mine += item_blocks(a, b) + PAD;
-    }
-    int64_t upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    if (lane == 31) sm.scan[warp] = upto;
-    __syncthreads();
+    if (lane < NS) mbar_init(smem_u32(&sm.full[warp][lane]), NB);
+    if (threadIdx.x == 0) sm.abort = sm.never = 0;
+    fence_mbar_init();
+    // where the stretch begins: the extents of all items, then the sequence
+    const int B = a.rows.B;
     int64_t all = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) upto += sm.scan[w];
-        all += sm.scan[w];
+    int one = 0;                              // the lane's sequence of the stretch of 32 in hand
+    for (int b = lane; b < B; b += 32) {
+        one = item_blocks(a, b) + PAD;
+        all += one;
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     all *= sh.per_batch;
     const int64_t per = stretch(all, warps, least);
-#pragma unroll 1
-    for (int w = 0; w < WARPS; ++w) {
-        const int64_t f = per * (blockIdx.x * WARPS + w);
-        if (f < upto * sh.per_batch && f >= (upto - mine) * sh.per_batch) {
-            int b = threadIdx.x * chunk;
-            int64_t before = upto - mine;
-            for (int n; f >= (before + (n = item_blocks(a, b) + PAD)) * sh.per_batch; ++b) before += n;
-            sm.seq[w] = b;
-            sm.before[w] = before;
-        }
-    }
-    __syncthreads();
     const int64_t self = blockIdx.x * WARPS + warp, f0 = per * self;
+    __syncthreads();                          // sm.abort is set
     if (f0 >= all) return;
     Walk at;
-    at.b = sm.seq[warp];
-    at.nb = item_blocks(a, at.b);
-    const int64_t rest = f0 - sm.before[warp] * sh.per_batch;
+    int64_t rest = 0;
+    for (int b0 = 0;; b0 += 32) {
+        const int b = b0 + lane;
+        if (B > 32) one = b < B ? item_blocks(a, b) + PAD : 0;
+        else if (b >= B) one = 0;
+        int64_t upto = one;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const int64_t here = __shfl_sync(0xffffffffu, upto, 31) * sh.per_batch;
+        if (f0 - rest >= here) {
+            rest += here;
+            continue;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, f0 - rest >= upto * sh.per_batch);
+        const int x = __popc(past);           // sequences of these 32 that end before f0
+        at.b = b0 + x;
+        at.nb = __shfl_sync(0xffffffffu, one, x) - PAD;
+        rest = f0 - rest - __shfl_sync(0xffffffffu, upto - one, x) * sh.per_batch;
+        break;
+    }
     at.i = (int)(rest / (at.nb + PAD));
     at.t0 = (int)(rest % (at.nb + PAD));
     at.left = min(per, all - f0);
     at.cut();
+    RawRows<D, NT> raw;
+    bool first = true;
+    fetch_rows<D, NT>(a, sh, decode_item(sh, a.pool.Hkv, at.b, at.i), raw);
     Walk &ahead = sm.ahead[warp];           // the same in every lane
     __syncwarp();
     ahead = at;
@@ -673,10 +699,15 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     for (int s = 0; s < NS; ++s) issue();
     __syncwarp();
     for (; at.valid(); at.next(a, sh.per_batch)) {
-        if (at.t0 >= at.t1) continue;
+        if (at.t0 >= at.t1) {                // the padding of an item that another warp has done
+            first = false;
+            continue;
+        }
         const Item it = decode_item(sh, a.pool.Hkv, at.b, at.i);
         Rows<D, NT> r;
-        load_rows<D, NT>(a, sh, it, kv4_len(a.pool, at.b), r);
+        if (!first) fetch_rows<D, NT>(a, sh, it, raw);
+        first = false;
+        make_rows<D, NT>(a, sh, it, kv4_len(a.pool, at.b), raw, r);
         State<D, NT> s;
         s.clear();
         for (int t = at.t0; t < at.t1; t += NB) {
