@@ -7,7 +7,6 @@ current torch stream (or ``stream``), like the C call.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import numpy as np
@@ -338,20 +337,29 @@ def ulysses_head_to_seq(y: torch.Tensor, N: int, layout: int, x=None, stream=Non
     return x
 
 
-def _kv4_check(**tensors):
-    """Tensors of one call: on the current CUDA device, contiguous, of the given dtype."""
-    for name, (t, dtype) in tensors.items():
-        if t is None:
-            continue
-        _need_cuda_contig(name, t)
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} must be on the current CUDA device")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}")
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _kv4_check(dev, *checks):
+    """(name, tensor or None, dtype) of one call: on ``dev``, contiguous, of that
+    dtype.  A decode step makes these calls once per layer, so the checks are kept
+    to a few attribute reads each."""
+    for name, t, dtype in checks:
+        if t is not None and (t.device != dev or t.dtype != dtype or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor on {dev}")
+
+
+def _kv4_dev(name, t):
+    """The call's device: that of its first tensor, which has to be the current one."""
+    dev = t.device
+    if dev.type != "cuda" or dev.index != _current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return dev
 
 
 def _kv4_shape(name, t, *shape):
-    if t is not None and tuple(t.shape) != shape:
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
 
 
@@ -360,22 +368,27 @@ def _kv4_pool(cache, pages, lens, B):
     if cache.dim() != 4 or cache.shape[3] % 5:
         raise ValueError("cache must have shape [n_pages, Hkv, page, 5 D / 4]")
     P, Hkv, page, w = cache.shape
-    if pages.dim() != 2:
-        raise ValueError("pages must have shape [B, max_pages]")
-    _kv4_shape("pages", pages, B, pages.shape[1])
+    if pages.dim() != 2 or pages.shape[0] != B:
+        raise ValueError(f"pages must have shape [{B}, max_pages]")
     _kv4_shape("lens", lens, B)
     return P, Hkv, page, w // 5 * 4, pages.shape[1]
 
 
-@contextlib.contextmanager
-def _on(stream):
-    """Tensors made inside belong to ``stream``, so that their memory is not handed
-    on while its kernels may still use it."""
+def _kv4_empty(stream, shape, dtype, dev):
+    """A tensor whose memory belongs to ``stream`` (None: the current one), so that it
+    is not handed on while that stream's kernels may still use it."""
     if stream is None:
-        yield
-    else:
-        with torch.cuda.stream(stream):
-            yield
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _kv4_stream(stream, dev):
+    return _raw_stream(dev.index) if stream is None else stream.cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def kv4_cache(n_pages: int, Hkv: int, page: int, D: int, summary: bool = False):
@@ -407,10 +420,7 @@ def kv4_append(k, v, cache, pages, lens, cos=None, sin=None, q=None, q_out=None,
     if k.dtype not in _DT or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
         raise ValueError("q, k, v must share dtype float32 or bfloat16")
     B, n, Hkv, D = k.shape
-    i32 = torch.int32
-    _kv4_check(cache=(cache, torch.uint8), pages=(pages, i32), lens=(lens, i32),
-               cos=(cos, torch.float32), sin=(sin, torch.float32), positions=(positions, i32),
-               n_new=(n_new, i32), summary=(summary, torch.bfloat16), q_out=(q_out, k.dtype))
+    dev, i32, f32 = _kv4_dev("k", k), torch.int32, torch.float32
     P, H, page, Dc, M = _kv4_pool(cache, pages, lens, B)
     if (H, Dc) != (Hkv, D):
         raise ValueError("cache and k must share Hkv and D")
@@ -419,32 +429,36 @@ def kv4_append(k, v, cache, pages, lens, cos=None, sin=None, q=None, q_out=None,
     _kv4_shape("positions", positions, B, n)
     _kv4_shape("n_new", n_new, B)
     _kv4_shape("summary", summary, P, Hkv, 2, D)
+    Hq = 0
     if q is not None:
-        if q.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != D:
+        if q.dim() != 4 or q.shape[0] != B or q.shape[1] != n or q.shape[3] != D:
             raise ValueError("q must have shape [B, n, Hq, D]")
+        Hq = q.shape[2]
         if q_out is None:
-            with _on(stream):
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = _kv4_empty(stream, q.shape, q.dtype, dev)
         _kv4_shape("q_out", q_out, *q.shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    strides = []
-    for name, t in (("k", k), ("v", v), ("q", q)):
-        if t is None:
-            strides += [0, 0, 0]
-            continue
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} must be on the current CUDA device")
-        if t.numel() and t.stride(3) != 1:
-            raise ValueError(f"{name}'s rows must be contiguous")
-        # an axis of one entry is not stepped along: its stride says nothing
-        strides += [0 if t.shape[i] <= 1 else t.stride(i) for i in range(3)]
-    rc = _lib.load().kv4_append(
-        _ptr(k), _ptr(v), _ptr(q), _ptr(q_out), _ptr(cache), _ptr(summary), _ptr(pages), _ptr(lens),
-        _ptr(n_new), _ptr(positions), _ptr(cos), _ptr(sin), (ctypes.c_int64 * 9)(*strides), B, n,
-        0 if q is None else q.shape[2], Hkv, D, P, page, M, 0 if cos is None else 2 * cos.shape[1],
-        int(interleaved), 0 if cos is None else cos.shape[0], _DT[k.dtype],
-        ctypes.c_void_p(_stream(stream)))
+    _kv4_check(dev, ("cache", cache, torch.uint8), ("pages", pages, i32), ("lens", lens, i32), ("cos", cos, f32),
+               ("sin", sin, f32), ("positions", positions, i32), ("n_new", n_new, i32),
+               ("summary", summary, torch.bfloat16), ("q_out", q_out, k.dtype))
+    strides = None
+    if not (k.is_contiguous() and v.is_contiguous() and (q is None or q.is_contiguous())):
+        strides = (ctypes.c_int64 * 9)()
+        for i, (name, t) in enumerate((("k", k), ("v", v), ("q", q))):
+            if t is None:
+                continue
+            if t.numel() and t.stride(3) != 1:
+                raise ValueError(f"{name}'s rows must be contiguous")
+            for x in range(3):   # an axis of one entry is not stepped along: its stride says nothing
+                strides[3 * i + x] = t.stride(x) if t.shape[x] > 1 else 0
+    if v.device != dev or (q is not None and q.device != dev):
+        raise ValueError(f"q, k, v must be on {dev}")
+    rot, max_pos = (0, 0) if cos is None else (2 * cos.shape[1], cos.shape[0])
+    rc = _lib.load().kv4_append(k.data_ptr(), v.data_ptr(), _at(q), _at(q_out), cache.data_ptr(), _at(summary),
+                                pages.data_ptr(), lens.data_ptr(), _at(n_new), _at(positions), _at(cos), _at(sin),
+                                strides, B, n, Hq, Hkv, D, P, page, M, rot, int(interleaved), max_pos, _DT[k.dtype],
+                                _kv4_stream(stream, dev))
     check(rc, "kv4_append")
     return q_out
 
@@ -457,25 +471,32 @@ def kv4_gather(cache, pages, lens, count: int, start=None, dtype=torch.bfloat16,
     if dtype not in _DT:
         raise ValueError("dtype must be float32 or bfloat16")
     B = lens.shape[0]
-    _kv4_check(cache=(cache, torch.uint8), pages=(pages, torch.int32), lens=(lens, torch.int32),
-               start=(start, torch.int32), k=(k, dtype), v=(v, dtype))
+    dev = _kv4_dev("cache", cache)
     P, Hkv, page, D, M = _kv4_pool(cache, pages, lens, B)
     _kv4_shape("start", start, B)
-    with _on(stream):
-        if k is None:
-            k = torch.empty(B, count, Hkv, D, dtype=dtype, device=cache.device)
-        if v is None:
-            v = torch.empty(B, count, Hkv, D, dtype=dtype, device=cache.device)
-    _kv4_shape("k", k, B, count, Hkv, D)
-    _kv4_shape("v", v, B, count, Hkv, D)
-    rc = _lib.load().kv4_gather(_ptr(cache), _ptr(pages), _ptr(lens), _ptr(start), _ptr(k), _ptr(v), B, count,
-                                Hkv, D, P, page, M, _DT[dtype], ctypes.c_void_p(_stream(stream)))
+    shape = (B, count, Hkv, D)
+    if k is None:
+        k = _kv4_empty(stream, shape, dtype, dev)
+    if v is None:
+        v = _kv4_empty(stream, shape, dtype, dev)
+    _kv4_shape("k", k, *shape)
+    _kv4_shape("v", v, *shape)
+    _kv4_check(dev, ("cache", cache, torch.uint8), ("pages", pages, torch.int32), ("lens", lens, torch.int32),
+               ("start", start, torch.int32), ("k", k, dtype), ("v", v, dtype))
+    rc = _lib.load().kv4_gather(cache.data_ptr(), pages.data_ptr(), lens.data_ptr(), _at(start), k.data_ptr(),
+                                v.data_ptr(), B, count, Hkv, D, P, page, M, _DT[dtype], _kv4_stream(stream, dev))
     check(rc, "kv4_gather")
     return k, v
 
 
+_ATTN_WORKSPACE = {}
+
+
 def kv4_attn_workspace(D: int) -> int:
-    return int(_lib.load().kv4_attn_workspace(D))
+    """Bytes of scratch for :func:`kv4_attn` (a constant of D)."""
+    if D not in _ATTN_WORKSPACE:
+        _ATTN_WORKSPACE[D] = int(_lib.load().kv4_attn_workspace(D))
+    return _ATTN_WORKSPACE[D]
 
 
 def kv4_attn(q, cache, pages, lens, vis=None, causal: bool = True, scale: float | None = None, sel=None,
@@ -491,33 +512,32 @@ def kv4_attn(q, cache, pages, lens, vis=None, causal: bool = True, scale: float 
     if q.dim() != 4:
         raise ValueError("q must have shape [B, n, Hq, D]")
     B, n, Hq, D = q.shape
-    with _on(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty(B, Hq, n, dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(max(kv4_attn_workspace(D), 16), dtype=torch.uint8, device=q.device)
+    dev, i32 = _kv4_dev("q", q), torch.int32
+    if out is None:
+        out = _kv4_empty(stream, q.shape, torch.bfloat16, dev)
+    if lse is None:
+        lse = _kv4_empty(stream, (B, Hq, n), torch.float32, dev)
+    if workspace is None:
+        workspace = _kv4_empty(stream, max(kv4_attn_workspace(D), 16), torch.uint8, dev)
     if out.dtype not in _DT:
         raise ValueError("out must be float32 or bfloat16")
-    _kv4_check(q=(q, torch.bfloat16), cache=(cache, torch.uint8), pages=(pages, torch.int32),
-               lens=(lens, torch.int32), vis=(vis, torch.int32), sel=(sel, torch.int32), out=(out, out.dtype),
-               lse=(lse, torch.float32), workspace=(workspace, workspace.dtype))
     P, Hkv, page, Dc, M = _kv4_pool(cache, pages, lens, B)
     if Dc != D:
         raise ValueError("cache and q must share D")
     _kv4_shape("vis", vis, B, n)
     _kv4_shape("out", out, *q.shape)
     _kv4_shape("lse", lse, B, Hq, n)
+    n_sel = 0
     if sel is not None:
-        if sel.dim() != 4:
-            raise ValueError("sel must have shape [B, n, Hkv, n_sel]")
-        _kv4_shape("sel", sel, B, n, Hkv, sel.shape[3])
-    sc = -1.0 if scale is None else float(scale)
-    rc = _lib.load().kv4_attn(_ptr(q), _ptr(cache), _ptr(pages), _ptr(lens), _ptr(vis), _ptr(sel), _ptr(out),
-                              _ptr(lse), B, n, Hq, Hkv, D, P, page, M, 0 if sel is None else sel.shape[3],
-                              int(causal), _DT[out.dtype], sc, _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), ctypes.c_void_p(_stream(stream)))
+        n_sel = sel.shape[-1]
+        _kv4_shape("sel", sel, B, n, Hkv, n_sel)
+    _kv4_check(dev, ("q", q, torch.bfloat16), ("cache", cache, torch.uint8), ("pages", pages, i32), ("lens", lens, i32),
+               ("vis", vis, i32), ("sel", sel, i32), ("out", out, out.dtype), ("lse", lse, torch.float32),
+               ("workspace", workspace, workspace.dtype))
+    rc = _lib.load().kv4_attn(q.data_ptr(), cache.data_ptr(), pages.data_ptr(), lens.data_ptr(), _at(vis), _at(sel),
+                              out.data_ptr(), lse.data_ptr(), B, n, Hq, Hkv, D, P, page, M, n_sel, int(causal),
+                              _DT[out.dtype], -1.0 if scale is None else float(scale), workspace.data_ptr(),
+                              workspace.nbytes, _kv4_stream(stream, dev))
     check(rc, "kv4_attn")
     return out, lse
 
@@ -535,26 +555,24 @@ def kv4_select(q, summary, pages, lens, page: int, n_sel: int, vis=None, causal:
     if q.dim() != 4 or summary.dim() != 4:
         raise ValueError("q must have shape [B, n, Hq, D] and summary [n_pages, Hkv, 2, D]")
     B, n, Hq, D = q.shape
+    dev, i32 = _kv4_dev("q", q), torch.int32
     P, Hkv = summary.shape[:2]
     _kv4_shape("summary", summary, P, Hkv, 2, D)
-    if pages.dim() != 2:
-        raise ValueError("pages must have shape [B, max_pages]")
+    if pages.dim() != 2 or pages.shape[0] != B:
+        raise ValueError(f"pages must have shape [{B}, max_pages]")
     M = pages.shape[1]
-    _kv4_shape("pages", pages, B, M)
     _kv4_shape("lens", lens, B)
     _kv4_shape("vis", vis, B, n)
-    with _on(stream):
-        if sel is None:
-            sel = torch.empty(B, n, Hkv, max(n_sel, 0), dtype=torch.int32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(max(kv4_select_workspace(B, n, Hkv, M), 16), dtype=torch.uint8, device=q.device)
+    if sel is None:
+        sel = _kv4_empty(stream, (B, n, Hkv, max(n_sel, 0)), i32, dev)
+    if workspace is None:
+        workspace = _kv4_empty(stream, max(kv4_select_workspace(B, n, Hkv, M), 16), torch.uint8, dev)
     _kv4_shape("sel", sel, B, n, Hkv, n_sel)
-    _kv4_check(q=(q, torch.bfloat16), summary=(summary, torch.bfloat16), pages=(pages, torch.int32),
-               lens=(lens, torch.int32), vis=(vis, torch.int32), sel=(sel, torch.int32),
-               workspace=(workspace, workspace.dtype))
-    rc = _lib.load().kv4_select(_ptr(q), _ptr(summary), _ptr(pages), _ptr(lens), _ptr(vis), _ptr(sel), B, n, Hq,
-                                Hkv, D, P, page, M, n_sel, int(causal), keep_first, keep_last, _ptr(workspace),
-                                workspace.numel() * workspace.element_size(), ctypes.c_void_p(_stream(stream)))
+    _kv4_check(dev, ("q", q, torch.bfloat16), ("summary", summary, torch.bfloat16), ("pages", pages, i32),
+               ("lens", lens, i32), ("vis", vis, i32), ("sel", sel, i32), ("workspace", workspace, workspace.dtype))
+    rc = _lib.load().kv4_select(q.data_ptr(), summary.data_ptr(), pages.data_ptr(), lens.data_ptr(), _at(vis),
+                                sel.data_ptr(), B, n, Hq, Hkv, D, P, page, M, n_sel, int(causal), keep_first, keep_last,
+                                workspace.data_ptr(), workspace.nbytes, _kv4_stream(stream, dev))
     check(rc, "kv4_select")
     return sel
 

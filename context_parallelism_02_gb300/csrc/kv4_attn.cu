@@ -18,6 +18,8 @@
 // the rows' group sums of q in three fp16 parts.  V's values s n + m are rounded
 // to fp16 (relative 2^-11) and so are the weights P; the row sums are taken over
 // the unrounded fp32 weights.
+#include <atomic>
+
 #include "kernels.h"
 #include "kv4.cuh"
 #include "tc_helpers.cuh"
@@ -767,11 +769,9 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
 }
 
 // Joins the pieces of the items that were cut: one block per output row.  The
-// parts are read JOIN_DEEP at a time per warp, so that a row of many pieces (one
+// parts are read JOIN_DEEP at a time by each of JW warps, so that a row of many pieces (one
 // long sequence: up to all warps of the grid) costs a few memory latencies.
-constexpr int JOIN_DEEP = 4;
-
-template <int D, int NT, int JW>
+template <int D, int NT, int JW, int JOIN_DEEP>
 __global__ void __launch_bounds__(JW * 32) kv4_join_kernel(Kv4AttnArgs a, Shape sh, int warps, int least)
 {
     constexpr int E = D / 32;
@@ -868,12 +868,22 @@ template <int D, int NT>
 int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
 {
     constexpr int smem = sizeof(Smem<D>);
-    int resident = 0;
-    if (cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kv4_attn_kernel<D, NT>, WARPS * 32, smem) != cudaSuccess ||
-        resident < 1)
-        return CP_ECUDA;
-    const int64_t ctas = min(resident * sm_count(), MAX_ROWS / (NT * 8 * WARPS));
+    // blocks of a grid that just fills the device, worked out once per device
+    constexpr int MAX_DEV = 64;
+    static std::atomic<int> fills[MAX_DEV];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEV) return CP_ECUDA;
+    int fill = fills[dev].load(std::memory_order_acquire);
+    if (!fill) {
+        int resident = 0;
+        if (cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kv4_attn_kernel<D, NT>, WARPS * 32, smem) != cudaSuccess ||
+            resident < 1)
+            return CP_ECUDA;
+        fill = resident * sm_count();
+        fills[dev].store(fill, std::memory_order_release);
+    }
+    const int64_t ctas = min(fill, MAX_ROWS / (NT * 8 * WARPS));
     // an upper bound of the line from the sizes alone
     const int64_t most = a.sel ? (int64_t)a.n_sel << (a.pool.page_shift - 4)
                                : ((int64_t)a.pool.max_pages << (a.pool.page_shift - 4));
@@ -894,10 +904,18 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const bool wide = (int64_t)warps > 32 * (int64_t)a.rows.B * sh.per_batch;
-    cfg.blockDim = dim3(wide ? 1024 : 128);
-    const cudaError_t rc = wide ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 32>, a, sh, warps, LEAST)
-                                : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 4>, a, sh, warps, LEAST);
+    const int64_t cuts = warps / ((int64_t)a.rows.B * sh.per_batch);   // pieces of an item, about
+    cudaError_t rc;
+    if (cuts > 64) {
+        cfg.blockDim = dim3(1024);
+        rc = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 32, 4>, a, sh, warps, LEAST);
+    } else if (cuts > 8) {
+        cfg.blockDim = dim3(256);
+        rc = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 8, 8>, a, sh, warps, LEAST);
+    } else {
+        cfg.blockDim = dim3(128);
+        rc = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 4, 2>, a, sh, warps, LEAST);
+    }
     return rc == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 
