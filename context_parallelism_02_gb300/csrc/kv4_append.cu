@@ -286,17 +286,50 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int ch
     }
 }
 
-// One warp per 16-token block and kv head.
+// One warp per 16-token block and kv head.  Lane (g, c) = (lane / 4, lane % 4)
+// takes the words that lie together for it: of K, elements 8 c .. 8 c + 7 of every
+// group of tokens g and g + 8; of V, elements 4 g .. 4 g + 3 of every group of
+// tokens 2 c, 2 c + 1, 8 + 2 c and 9 + 2 c.  All loads are 16 bytes (D = 128) and on
+// their way before the first is used; stores cover 64 bytes of a row or more.
+template <int N>
+__device__ __forceinline__ void words(const uint8_t *p, uint32_t (&w)[N])
+{
+    static_assert(N == 2 || N == 4, "");
+    if (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x, w[1] = v.y, w[N - 2] = v.z, w[N - 1] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x, w[1] = v.y;
+    }
+}
+
+__device__ __forceinline__ float half_of(uint32_t w, int hi)
+{
+    return __half2float(__ushort_as_half((unsigned short)(hi ? w >> 16 : w & 0xffffu)));
+}
+
+__device__ __forceinline__ void store4(float *p, const float (&x)[4])
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&x)[4])
+{
+    *reinterpret_cast<uint2 *>(p) = make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(128) kv4_gather_kernel(Kv4GatherArgs a, int blocks, int64_t warps)
 {
-    constexpr int LPR = D / 8, TPI = 16 / LPR, NG = Kv4<D>::NG;
-    const int lane = threadIdx.x & 31;
+    constexpr int NG = Kv4<D>::NG;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int64_t wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (wid >= warps) return;
-    const int x = (int)(wid % blocks);
-    const int h = (int)(wid / blocks % a.pool.Hkv);
-    const int b = (int)(wid / blocks / a.pool.Hkv);
+    // heads next to each other: their rows are neighbours in k and v
+    const int h = (int)(wid % a.pool.Hkv);
+    const int x = (int)(wid / a.pool.Hkv % blocks);
+    const int b = (int)(wid / a.pool.Hkv / blocks);
     const int len = kv4_len(a.pool, b);
     int64_t first = a.start ? (int64_t)__ldg(a.start + b) : 0;
     if (first < 0) {
@@ -305,44 +338,71 @@ __global__ void __launch_bounds__(128) kv4_gather_kernel(Kv4GatherArgs a, int bl
     }
     const int64_t slot0 = ((first >> 4) + x) << 4;
     const int ps = a.pool.page_shift;
-    const uint8_t *blk = nullptr;
+    uint32_t k[2][NG], km[2][NG], v[2][NG], vm[2][2 * NG];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) k[i][gr] = km[i][gr] = v[i][gr] = vm[i][gr] = vm[i][NG + gr] = 0;
+    }
     if (slot0 < len && slot0 < first + a.count) {
         const int id = kv4_page(a.pool, b, slot0 >> ps);
-        if (id >= 0) blk = kv4_block<D>(a.pool, id, h, (int)((slot0 & ((1 << ps) - 1)) >> 4));
-    }
-    const int sub = lane & (LPR - 1), d0 = sub * 8, gr = sub >> 2, q4 = sub & 3;
-    const bool is_v = (lane / LPR) & 1;
-    for (int t0 = 0; t0 < KV4_BLOCK; t0 += TPI) {
-        const int t = t0 + lane / (2 * LPR);
-        const int64_t slot = slot0 + t, j = slot - first;
-        if (j < 0 || j >= a.count) continue;
-        float y[8] = {};
-        if (blk && slot < len) {
-            float s, m;
-            int code[8];
-            if (!is_v) {
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(blk + t * (D / 2) + (q4 * NG + gr) * 4);
+        if (id >= 0) {
+            const uint8_t *blk = kv4_block<D>(a.pool, id, h, (int)((slot0 & ((1 << ps) - 1)) >> 4));
 #pragma unroll
-                for (int o = 0; o < 8; ++o) code[o] = w >> (4 * ((o >> 1) + 4 * (o & 1))) & 15;
-                const __half2 sm = *reinterpret_cast<const __half2 *>(blk + Kv4<D>::K_META + (t * NG + gr) * 4);
-                s = __low2float(sm), m = __high2float(sm);
-            } else {
+            for (int i = 0; i < 2; ++i) {
+                words<NG>(blk + (g + 8 * i) * (D / 2) + c * 4 * NG, k[i]);
+                words<NG>(blk + Kv4<D>::K_META + (g + 8 * i) * 4 * NG, km[i]);
+                words<NG>(blk + Kv4<D>::V_CODES + i * 128 * NG + lane * 4 * NG, v[i]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t w = *reinterpret_cast<const uint16_t *>(blk + v_code_at<D>(t, gr, 2 * q4 + e));
+                for (int y = 0; y < 2; ++y) {
+                    uint32_t part[NG];
+                    words<NG>(blk + Kv4<D>::V_META + ((i * 4 + c) * 2 + y) * 4 * NG, part);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) code[4 * e + i] = w >> (4 * i) & 15;
+                    for (int gr = 0; gr < NG; ++gr) vm[i][y * NG + gr] = part[gr];
                 }
-                const uint8_t *p = blk + v_meta_at<D>(t, gr);
-                s = __half2float(*reinterpret_cast<const __half *>(p));
-                m = __half2float(*reinterpret_cast<const __half *>(p + 4));
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __fadd_rn(__fmul_rn((float)code[i], s), m);
         }
-        T *to = static_cast<T *>(is_v ? a.v : a.k) + (((int64_t)b * a.count + j) * a.pool.Hkv + h) * D + d0;
-        store8(to, y);
     }
+    const int64_t row0 = (int64_t)b * a.count;
+    const int64_t live = len - slot0;   // tokens of the block below the length; the others are written as 0
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = g + 8 * i;
+        const int64_t j = slot0 + t - first;
+        if (j < 0 || j >= a.count) continue;
+        T *to = static_cast<T *>(a.k) + ((row0 + j) * a.pool.Hkv + h) * D + 8 * c;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+            const float s = half_of(km[i][gr], 0), m = half_of(km[i][gr], 1);
+            float y[8];
+#pragma unroll
+            for (int o = 0; o < 8; ++o) {
+                const int code = k[i][gr] >> (4 * ((o >> 1) + 4 * (o & 1))) & 15;
+                y[o] = t < live ? __fadd_rn(__fmul_rn((float)code, s), m) : 0.f;
+            }
+            store8(to + 32 * gr, y);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int lo = 0; lo < 2; ++lo) {
+            const int t = 8 * i + 2 * c + lo;
+            const int64_t j = slot0 + t - first;
+            if (j < 0 || j >= a.count) continue;
+            T *to = static_cast<T *>(a.v) + ((row0 + j) * a.pool.Hkv + h) * D + 4 * g;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                const float s = half_of(vm[i][2 * gr], lo), m = half_of(vm[i][2 * gr + 1], lo);
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int code = v[i][gr] >> (16 * lo + 4 * e) & 15;
+                    y[e] = t < live ? __fadd_rn(__fmul_rn((float)code, s), m) : 0.f;
+                }
+                store4(to + 32 * gr, y);
+            }
+        }
 }
 
 }  // namespace
