@@ -9,9 +9,13 @@
 // finite is held as NaN.
 //
 // HBM-bound: per token and kv head 2 D elements are read and 1.25 D bytes
-// written.  A lane holds 8 neighbouring elements of a row, so a group's extremes
-// are two shuffles and a K code word is one lane's.  K and V rows of a token sit
-// in one warp (a decode step, one token per sequence, is one pass of one warp).
+// written, next to it the arithmetic of the quantisation (about 25 instructions an
+// element of K).  In K and V a lane holds 8 neighbouring elements of a row, so a
+// group's extremes are two shuffles and a K code word is one lane's; K and V rows
+// of a token sit in one warp (a decode step, one token per sequence, is one pass of
+// one warp).  Blocks of 16 tokens that are written whole are put together in shared
+// memory and leave in 16-byte pieces.  q rows: eight heads of a token per warp, so
+// that a row of the tables is read once for them.
 #include "kernels.h"
 #include "kv4.cuh"
 
@@ -19,22 +23,55 @@ namespace cp {
 
 namespace {
 
+// What a kernel only reads (k, v and the tables, not q, whose rows may be rotated in
+// place) goes through the read-only path, so that loads can move above stores.
 __device__ __forceinline__ void load8(const float *p, float (&x)[8])
 {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
     x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8])
+// 8 elements as they are in memory
+struct Raw16 { uint4 a; };
+struct Raw32 { float4 a, b; };
+__device__ __forceinline__ void fetch8(const __nv_bfloat16 *p, Raw16 &r) { r.a = __ldg(reinterpret_cast<const uint4 *>(p)); }
+__device__ __forceinline__ void fetch8(const float *p, Raw32 &r)
 {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    r.a = __ldg(reinterpret_cast<const float4 *>(p));
+    r.b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+}
+__device__ __forceinline__ void clear(Raw16 &r) { r.a = make_uint4(0, 0, 0, 0); }
+__device__ __forceinline__ void clear(Raw32 &r) { r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f); }
+__device__ __forceinline__ void widen(const Raw16 &r, float (&x)[8])
+{
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[2 * i] = __uint_as_float(w[i] << 16);
         x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+}
+__device__ __forceinline__ void widen(const Raw32 &r, float (&x)[8])
+{
+    x[0] = r.a.x, x[1] = r.a.y, x[2] = r.a.z, x[3] = r.a.w;
+    x[4] = r.b.x, x[5] = r.b.y, x[6] = r.b.z, x[7] = r.b.w;
+}
+template <typename T> struct RawOf;
+template <> struct RawOf<__nv_bfloat16> { using type = Raw16; };
+template <> struct RawOf<float> { using type = Raw32; };
+
+// 4 elements of a q row
+__device__ __forceinline__ void load4(const float *p, float (&x)[4])
+{
+    const float4 a = *reinterpret_cast<const float4 *>(p);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4])
+{
+    const uint2 a = *reinterpret_cast<const uint2 *>(p);
+    x[0] = __uint_as_float(a.x << 16), x[1] = __uint_as_float(a.x & 0xffff0000u);
+    x[2] = __uint_as_float(a.y << 16), x[3] = __uint_as_float(a.y & 0xffff0000u);
 }
 
 __device__ __forceinline__ void store8(float *p, const float (&x)[8])
@@ -52,6 +89,16 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8])
 {
     *reinterpret_cast<uint4 *>(p) = make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
+}
+
+__device__ __forceinline__ void store4(float *p, const float (&x)[4])
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&x)[4])
+{
+    *reinterpret_cast<uint2 *>(p) = make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
 }
 
 // Rotates the 8 elements d0.. of a row spread over consecutive lanes (8 per
@@ -116,17 +163,18 @@ __device__ __forceinline__ int new_tokens(const Kv4AppendArgs &a, int b)
 // times) and m (half of 32) on top, s code + m still rounds to a finite fp16.
 constexpr float KV4_MAX = 65408.f;
 
-// Codes, scale and minimum of a lane's 8 elements; the group is 4 lanes.
-__device__ __forceinline__ void quantise8(const float (&x)[8], int (&code)[8], __half &s, __half &m)
+// Codes (as whole floats), scale and minimum of a lane's 8 elements; the group is
+// 4 lanes.  rint((y - m) / s) is taken from the product with 1 / s, which is off the
+// quotient by less than 4 units in the last place, under 1e-5 at 15; where a lane's
+// product comes that near a half the warp divides.
+__device__ __forceinline__ void quantise8(const float (&x)[8], float (&code)[8], __half &s, __half &m)
 {
-    bool bad = false;
-    float y[8], lo, hi;
+    float lo = x[0], hi = x[0], nan = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        bad |= !isfinite(x[i]);
-        y[i] = fminf(fmaxf(x[i], -KV4_MAX), KV4_MAX);
-        lo = i ? fminf(lo, y[i]) : y[i];
-        hi = i ? fmaxf(hi, y[i]) : y[i];
+        nan = fmaf(x[i], 0.f, nan);   // stays 0 unless an element is not finite
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
     }
 #pragma unroll
     for (int o = 1; o <= 2; o <<= 1) {
@@ -134,15 +182,40 @@ __device__ __forceinline__ void quantise8(const float (&x)[8], int (&code)[8], _
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
     const unsigned group = 0xfu << (threadIdx.x & 28);
-    bad = (__ballot_sync(0xffffffffu, bad) & group) != 0;
+    const bool bad = (__ballot_sync(0xffffffffu, nan != 0.f) & group) != 0;
+    const bool wide = __any_sync(0xffffffffu, !(lo >= -KV4_MAX && hi <= KV4_MAX));
+    lo = fmaxf(lo, -KV4_MAX);
+    hi = fminf(hi, KV4_MAX);
+    lo = fminf(lo, KV4_MAX);
+    hi = fmaxf(hi, -KV4_MAX);
     s = __float2half_rn(bad ? 0.f : __fdiv_rn(hi - lo, 15.f));
     m = bad ? __ushort_as_half(0x7fff) : __float2half_rn(lo);
-    const float sf = __half2float(s), mf = __half2float(m);
+    const float sf = __half2float(s), mf = bad ? 0.f : __half2float(m);
+    const float inv = sf > 0.f ? __frcp_rn(sf) : 0.f;
+    constexpr float ROUND = 12582912.f;   // 1.5 2^23: adding it rounds to a whole number
+    float y[8], off = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float t = sf > 0.f ? rintf(__fdiv_rn(y[i] - mf, sf)) : 0.f;
-        code[i] = (int)fminf(fmaxf(t, 0.f), 15.f);
+        y[i] = wide ? fminf(fmaxf(x[i], -KV4_MAX), KV4_MAX) : x[i];
+        const float r = fminf(fmaxf((y[i] - mf) * inv, 0.f), 15.f);
+        code[i] = __fsub_rn(__fadd_rn(r, ROUND), ROUND);
+        off = fmaxf(off, fabsf(r - code[i]));
     }
+    if (__any_sync(0xffffffffu, off > 0.4999f)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            code[i] = sf > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(y[i] - mf, sf)), 0.f), 15.f) : 0.f;
+    }
+    if (bad) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) code[i] = 0.f;
+    }
+}
+
+// Four codes as the nibbles of 16 bits.
+__device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float d)
+{
+    return __float_as_uint(fmaf(fmaf(fmaf(d, 16.f, c), 16.f, b), 16.f, a) + 8388608.f) & 0xffffu;   // 2^23
 }
 
 // Bytes of a V code word and of its scale for token t, group gr.
@@ -158,36 +231,98 @@ __device__ __forceinline__ int v_meta_at(int t, int gr)
     return Kv4<D>::V_META + (((t >> 3) * 4 + ((t & 7) >> 1)) * Kv4<D>::NG + gr) * 8 + (t & 1) * 2;
 }
 
-// Warps of a block: 4.  The first kv_blocks blocks take (batch, kv head, chunk
-// of max(page, 64) slots), the others 128 / (D / 8) rows of q each.
+// A warp's q rows: token (b, j), heads h0 .. h0 + 7.  A lane holds 4 + 4 elements:
+// the two halves of 4 pairs, 4 pairs that lie together (interleaved), or 8 elements
+// that are not rotated.
 template <int D, typename T>
-__global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int chunk_shift, int chunks, int64_t kv_blocks)
+__device__ __forceinline__ void rotate_q(const Kv4AppendArgs &a, int64_t unit)
+{
+    constexpr int LPR = D / 8, RPP = 32 / LPR, U = 8 / RPP;   // lanes of a row, rows of a pass, passes
+    const int lane = threadIdx.x & 31, l = lane & (LPR - 1);
+    const int hc = (a.Hq + 7) >> 3;
+    const int h0 = (int)(unit % hc) * 8;
+    const int64_t bj = unit / hc;
+    const int j = (int)(bj % a.n), b = (int)(bj / a.n);
+    const bool real = j < new_tokens(a, b);
+    const int64_t pos = real ? position(a, b, j, (int64_t)__ldg(a.pool.lens + b) + j) : -1;
+    const bool on = real && (pos >= 0 || !a.rot);   // rows that are not there, or have no angle, are 0
+    const bool turn = on && 8 * l < a.rot;
+    int da = 8 * l, db = 8 * l + 4;
+    if (!a.interleaved && 8 * l < a.rot) da = 4 * l, db = 4 * l + (a.rot >> 1);
+    float x[U][4], y[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * RPP + lane / LPR;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[u][i] = y[u][i] = 0.f;
+        if (on && h < a.Hq) {
+            const T *p = static_cast<const T *>(a.q) + b * a.qs[0] + j * a.qs[1] + h * a.qs[2];
+            load4(p + da, x[u]);
+            load4(p + db, y[u]);
+        }
+    }
+    float cs[4], sn[4];
+    if (turn) {
+        const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + pos * (a.rot >> 1) + 4 * l));
+        const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + pos * (a.rot >> 1) + 4 * l));
+        cs[0] = cv.x, cs[1] = cv.y, cs[2] = cv.z, cs[3] = cv.w;
+        sn[0] = sv.x, sn[1] = sv.y, sn[2] = sv.z, sn[3] = sv.w;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * RPP + lane / LPR;
+        if (h >= a.Hq) continue;
+        if (turn) {
+            // pairs (x[i], y[i]), or (x[0], x[1]), (x[2], x[3]), (y[0], y[1]), (y[2], y[3])
+            float p[8] = {x[u][0], x[u][1], x[u][2], x[u][3], y[u][0], y[u][1], y[u][2], y[u][3]};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x1 = a.interleaved ? p[2 * i] : p[i], x2 = a.interleaved ? p[2 * i + 1] : p[4 + i];
+                const float r1 = __fsub_rn(__fmul_rn(x1, cs[i]), __fmul_rn(x2, sn[i]));
+                const float r2 = __fadd_rn(__fmul_rn(x2, cs[i]), __fmul_rn(x1, sn[i]));
+                if (a.interleaved) {
+                    if (i < 2) x[u][2 * i] = r1, x[u][2 * i + 1] = r2;
+                    else y[u][2 * i - 4] = r1, y[u][2 * i - 3] = r2;
+                } else {
+                    x[u][i] = r1, y[u][i] = r2;
+                }
+            }
+        }
+        T *to = static_cast<T *>(a.q_out) + (bj * a.Hq + h) * D;
+        store4(to + da, x[u]);
+        store4(to + db, y[u]);
+    }
+}
+
+// Four warps.  kv_blocks of the grid's blocks take (chunk of max(page, 64) slots,
+// kv head) of a sequence each, a warp 16 slots of it at a time; the others q rows.
+// The two kinds alternate (every `every`-th block is a kv block), so that the
+// arithmetic of one and the memory traffic of the other share an SM.
+template <int D, typename T>
+__global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int chunk_shift, int chunks, int64_t kv_blocks,
+                                                         int64_t q_units, int every)
 {
     constexpr int LPR = D / 8;           // lanes of a row
     constexpr int TPI = 16 / LPR;        // tokens of a warp's pass (K and V rows)
+    constexpr int DEEP = sizeof(T) == 2 ? 4 : 2;   // passes whose rows are on their way together
     constexpr int NG = Kv4<D>::NG;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane & (LPR - 1), d0 = sub * 8;
-    if ((int64_t)blockIdx.x >= kv_blocks) {   // q rows
-        const int64_t row = ((int64_t)blockIdx.x - kv_blocks) * (128 / LPR) + threadIdx.x / LPR;
-        const int64_t rows = (int64_t)a.B * a.n * a.Hq;
-        const bool on = row < rows;
-        const int h = on ? (int)(row % a.Hq) : 0;
-        const int64_t bj = on ? row / a.Hq : 0;
-        const int j = (int)(bj % a.n), b = (int)(bj / a.n);
-        const bool real = on && j < new_tokens(a, b);
-        const int64_t pos = real ? position(a, b, j, (int64_t)__ldg(a.pool.lens + b) + j) : -1;
-        float x[8] = {};
-        if (real && (pos >= 0 || !a.rot))   // rows that are not there, or have no angle: 0
-            load8(static_cast<const T *>(a.q) + b * a.qs[0] + j * a.qs[1] + h * a.qs[2] + d0, x);
-        rotate8(x, a, d0, pos, real && a.rot && pos >= 0);
-        if (on) store8(static_cast<T *>(a.q_out) + row * D + d0, x);
+    const int64_t bid = blockIdx.x;
+    // kv blocks at multiples of `every`, as long as there are any
+    const bool is_kv = bid % every == 0 && bid / every < kv_blocks;
+    if (!is_kv) {
+        const int64_t before = (bid + every - 1) / every;   // kv blocks in front
+        const int64_t unit = (bid - (before < kv_blocks ? before : kv_blocks)) * 4 + warp;
+        if (unit < q_units) rotate_q<D, T>(a, unit);
         return;
     }
+    const int64_t kb = bid / every;
     __shared__ float red[4][2][D];
-    const int c = (int)(blockIdx.x % chunks);
-    const int h = (int)(blockIdx.x / chunks % a.pool.Hkv);
-    const int b = (int)(blockIdx.x / chunks / a.pool.Hkv);
+    __shared__ __align__(16) uint8_t stage[4][Kv4<D>::BYTES];
+    const int sub = lane & (LPR - 1), d0 = sub * 8;
+    const int h = (int)(kb % a.pool.Hkv);
+    const int c = (int)(kb / a.pool.Hkv % chunks);
+    const int b = (int)(kb / a.pool.Hkv / chunks);
     const int64_t len = __ldg(a.pool.lens + b);
     if (len < 0) {
         if (threadIdx.x == 0) kv4_report(a.pool.err);
@@ -200,6 +335,7 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int ch
     const int ps = a.pool.page_shift;
     const bool is_v = (lane / LPR) & 1;
     const int tsub = lane / (2 * LPR);
+    const int gr = sub >> 2, q4 = sub & 3;
     float lo[8], hi[8];   // per-d extremes of the K rows that this lane has seen
 #pragma unroll
     for (int i = 0; i < 8; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
@@ -208,53 +344,75 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int ch
         if (slot0 >= end || slot0 + KV4_BLOCK <= len) continue;
         const int id = kv4_page(a.pool, b, slot0 >> ps);
         if (id < 0) continue;
-        uint8_t *blk = kv4_block<D>(a.pool, id, h, (int)((slot0 & ((1 << ps) - 1)) >> 4));
+        uint8_t *const blk = kv4_block<D>(a.pool, id, h, (int)((slot0 & ((1 << ps) - 1)) >> 4));
         const int t_lo = len > slot0 ? (int)(len - slot0) : 0;
         const int t_hi = end - slot0 < KV4_BLOCK ? (int)(end - slot0) : KV4_BLOCK;
-        for (int t0 = t_lo; t0 < t_hi; t0 += TPI) {
-            const int t = t0 + tsub;
-            const int j = (int)(slot0 + t - len);
-            bool on = t < t_hi;
-            const int64_t pos = on ? position(a, b, j, slot0 + t) : -1;
-            if (a.rot) on = on && pos >= 0;
-            float x[8] = {};
-            if (on) {
-                const int64_t *st = is_v ? a.vs : a.ks;
-                load8(static_cast<const T *>(is_v ? a.v : a.k) + b * st[0] + j * st[1] + h * st[2] + d0, x);
+        // lane t: whether token t is written, and its position
+        const bool mine = lane >= t_lo && lane < t_hi;
+        const int64_t at = mine ? position(a, b, (int)(slot0 + lane - len), slot0 + lane) : -1;
+        const unsigned live = __ballot_sync(0xffffffffu, mine && (at >= 0 || !a.rot));
+        const bool full = live == 0xffffu;
+        uint8_t *const to = full ? stage[warp] : blk;
+        for (int t0 = t_lo; t0 < t_hi; t0 += TPI * DEEP) {
+            typename RawOf<T>::type raw[DEEP];
+#pragma unroll
+            for (int u = 0; u < DEEP; ++u) {
+                const int t = t0 + u * TPI + tsub;
+                clear(raw[u]);
+                if (t < t_hi && (live >> t & 1)) {
+                    const int64_t j = slot0 + t - len;
+                    const int64_t st0 = is_v ? a.vs[0] : a.ks[0], st1 = is_v ? a.vs[1] : a.ks[1], st2 = is_v ? a.vs[2] : a.ks[2];
+                    fetch8(static_cast<const T *>(is_v ? a.v : a.k) + b * st0 + j * st1 + h * st2 + d0, raw[u]);
+                }
             }
-            rotate8(x, a, d0, pos, on && a.rot && !is_v);
-            int code[8];
-            __half s, m;
-            quantise8(x, code, s, m);
-            if (!on) continue;
-            const int gr = sub >> 2, q4 = sub & 3;
-            if (!is_v) {
-                uint32_t w = 0;
 #pragma unroll
-                for (int o = 0; o < 8; ++o) w |= (uint32_t)code[o] << (4 * ((o >> 1) + 4 * (o & 1)));
-                *reinterpret_cast<uint32_t *>(blk + t * (D / 2) + (q4 * NG + gr) * 4) = w;
-                if (q4 == 0)
-                    *reinterpret_cast<__half2 *>(blk + Kv4<D>::K_META + (t * NG + gr) * 4) = __halves2half2(s, m);
+            for (int u = 0; u < DEEP; ++u) {
+                if (t0 + u * TPI >= t_hi) break;
+                const int t = t0 + u * TPI + tsub;
+                const bool on = t < t_hi && (live >> t & 1);
+                const int64_t pos = __shfl_sync(0xffffffffu, at, t & 31);
+                float x[8], code[8];
+                widen(raw[u], x);
+                if (a.rot) rotate8(x, a, d0, pos, on && !is_v);
+                __half s, m;
+                quantise8(x, code, s, m);
+                if (!on) continue;
+                if (!is_v) {
+                    *reinterpret_cast<uint32_t *>(to + t * (D / 2) + (q4 * NG + gr) * 4) =
+                        nibbles(code[0], code[2], code[4], code[6]) | nibbles(code[1], code[3], code[5], code[7]) << 16;
+                    if (q4 == 0)
+                        *reinterpret_cast<__half2 *>(to + Kv4<D>::K_META + (t * NG + gr) * 4) = __halves2half2(s, m);
+                    if (a.summary) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const bool fin = isfinite(x[i]);
-                    lo[i] = fminf(lo[i], fin ? x[i] : -INFINITY);
-                    hi[i] = fmaxf(hi[i], fin ? x[i] : INFINITY);
-                }
-            } else {
+                        for (int i = 0; i < 8; ++i) {
+                            const bool fin = isfinite(x[i]);
+                            lo[i] = fminf(lo[i], fin ? x[i] : -INFINITY);
+                            hi[i] = fmaxf(hi[i], fin ? x[i] : INFINITY);
+                        }
+                    }
+                } else {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t w = code[4 * e] | code[4 * e + 1] << 4 | code[4 * e + 2] << 8 | code[4 * e + 3] << 12;
-                    *reinterpret_cast<uint16_t *>(blk + v_code_at<D>(t, gr, 2 * q4 + e)) = (uint16_t)w;
-                }
-                if (q4 == 0) {
-                    uint8_t *p = blk + v_meta_at<D>(t, gr);
-                    *reinterpret_cast<__half *>(p) = s;
-                    *reinterpret_cast<__half *>(p + 4) = m;
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<uint16_t *>(to + v_code_at<D>(t, gr, 2 * q4 + e)) =
+                            (uint16_t)nibbles(code[4 * e], code[4 * e + 1], code[4 * e + 2], code[4 * e + 3]);
+                    if (q4 == 0) {
+                        uint8_t *p = to + v_meta_at<D>(t, gr);
+                        *reinterpret_cast<__half *>(p) = s;
+                        *reinterpret_cast<__half *>(p + 4) = m;
+                    }
                 }
             }
         }
-        // __syncwarp is implied by the warp-wide shuffles of the next block
+        __syncwarp();
+        if (full) {
+#pragma unroll
+            for (int i = 0; i < Kv4<D>::BYTES / 512; ++i)
+                reinterpret_cast<uint4 *>(blk)[i * 32 + lane] = reinterpret_cast<const uint4 *>(stage[warp])[i * 32 + lane];
+            if (Kv4<D>::BYTES % 512 && lane < Kv4<D>::BYTES % 512 / 16)
+                reinterpret_cast<uint4 *>(blk)[Kv4<D>::BYTES / 512 * 32 + lane] =
+                    reinterpret_cast<const uint4 *>(stage[warp])[Kv4<D>::BYTES / 512 * 32 + lane];
+            __syncwarp();
+        }
     }
     if (!a.summary) return;
     // extremes over the warp's token slots (D = 64: two per pass), then over the
@@ -307,16 +465,6 @@ __device__ __forceinline__ void words(const uint8_t *p, uint32_t (&w)[N])
 __device__ __forceinline__ float half_of(uint32_t w, int hi)
 {
     return __half2float(__ushort_as_half((unsigned short)(hi ? w >> 16 : w & 0xffffu)));
-}
-
-__device__ __forceinline__ void store4(float *p, const float (&x)[4])
-{
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&x)[4])
-{
-    *reinterpret_cast<uint2 *>(p) = make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
 }
 
 template <int D, typename T>
@@ -413,12 +561,12 @@ int launch_kv4_append(const Kv4AppendArgs &a, int D, int dtype, cudaStream_t st)
     const int chunk = 1 << chunk_shift;
     const int64_t chunks = ((int64_t)a.n + chunk - 2) / chunk + 1;
     const int64_t kv_blocks = chunks * a.pool.Hkv * a.B;
-    const int64_t q_rows = a.q ? (int64_t)a.B * a.n * a.Hq : 0;
-    const int rpb = 128 / (D / 8);
-    const int64_t blocks = kv_blocks + (q_rows + rpb - 1) / rpb;
+    const int64_t q_units = a.q ? (int64_t)a.B * a.n * ((a.Hq + 7) / 8) : 0;
+    const int64_t blocks = kv_blocks + (q_units + 3) / 4;
     if (blocks > 0x7fffffffLL) return CP_EUNSUPPORTED;
+    const int every = (int)(blocks / kv_blocks);
 #define CP_KV4_APPEND(D_, T_) \
-    kv4_append_kernel<D_, T_><<<(unsigned)blocks, 128, 0, st>>>(a, chunk_shift, (int)chunks, kv_blocks)
+    kv4_append_kernel<D_, T_><<<(unsigned)blocks, 128, 0, st>>>(a, chunk_shift, (int)chunks, kv_blocks, q_units, every)
     if (D == 64) {
         if (dtype == CP_BF16) CP_KV4_APPEND(64, __nv_bfloat16);
         else CP_KV4_APPEND(64, float);
