@@ -103,15 +103,16 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&x)[4])
 
 // Rotates the 8 elements d0.. of a row spread over consecutive lanes (8 per
 // lane).  Every lane of the warp calls it; lanes with turn == false keep x.
+template <bool INTER>
 __device__ __forceinline__ void rotate8(float (&x)[8], const Kv4AppendArgs &a, int d0, int64_t pos, bool turn)
 {
     const int half = a.rot >> 1;
-    const int lane = threadIdx.x & 31;
-    if (a.interleaved) {
-        if (turn && d0 < a.rot) {
+    const bool in = turn && d0 < a.rot;
+    if (INTER) {
+        if (in) {
             const int64_t at = pos * half + (d0 >> 1);
-            const float4 cv = *reinterpret_cast<const float4 *>(a.cos + at);
-            const float4 sv = *reinterpret_cast<const float4 *>(a.sin + at);
+            const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
+            const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
             const float cs[4] = {cv.x, cv.y, cv.z, cv.w}, sn[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -122,22 +123,20 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const Kv4AppendArgs &a, i
         }
         return;
     }
-    const bool in = turn && d0 < a.rot;
+    const int lane = threadIdx.x & 31;
     const bool first = d0 < half;
     const int src = in ? (first ? lane + (half >> 3) : lane - (half >> 3)) : lane;
-    float p[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = __shfl_sync(0xffffffffu, x[i], src);
+    const float sign = first ? -1.f : 1.f;   // x1 cos - x2 sin, x2 cos + x1 sin
+    float cs[8], sn[8];
     if (in) {
-        float cs[8], sn[8];
         const int64_t at = pos * half + (first ? d0 : d0 - half);
         load8(a.cos + at, cs);
         load8(a.sin + at, sn);
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float u = __fmul_rn(x[i], cs[i]), w = __fmul_rn(p[i], sn[i]);
-            x[i] = first ? __fsub_rn(u, w) : __fadd_rn(u, w);
-        }
+    for (int i = 0; i < 8; ++i) {
+        const float p = __shfl_sync(0xffffffffu, x[i], src);
+        if (in) x[i] = __fadd_rn(__fmul_rn(x[i], cs[i]), __fmul_rn(p, sign * sn[i]));
     }
 }
 
@@ -163,59 +162,73 @@ __device__ __forceinline__ int new_tokens(const Kv4AppendArgs &a, int b)
 // times) and m (half of 32) on top, s code + m still rounds to a finite fp16.
 constexpr float KV4_MAX = 65408.f;
 
+// min and max of three that keep a NaN
+__device__ __forceinline__ float min3(float a, float b, float c)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Codes (as whole floats), scale and minimum of a lane's 8 elements; the group is
-// 4 lanes.  rint((y - m) / s) is taken from the product with 1 / s, which is off the
-// quotient by less than 4 units in the last place, under 1e-5 at 15; where a lane's
-// product comes that near a half the warp divides.
+// 4 lanes.  rint((y - m) / s) is taken from a product with 1 / (15 s), held to
+// [0, 1], times 15: off the quotient by less than 6 units in the last place, under
+// 1e-5 at 15; where a lane's product comes that near a half the warp divides.
 __device__ __forceinline__ void quantise8(const float (&x)[8], float (&code)[8], __half &s, __half &m)
 {
-    float lo = x[0], hi = x[0], nan = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        nan = fmaf(x[i], 0.f, nan);   // stays 0 unless an element is not finite
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
+    float lo = min3(min3(x[0], x[1], x[2]), min3(x[3], x[4], x[5]), min3(x[6], x[7], x[7]));
+    float hi = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), max3(x[6], x[7], x[7]));
+    {
+        const float l1 = __shfl_xor_sync(0xffffffffu, lo, 1), h1 = __shfl_xor_sync(0xffffffffu, hi, 1);
+        lo = min3(lo, l1, l1);
+        hi = max3(hi, h1, h1);
+        const float l2 = __shfl_xor_sync(0xffffffffu, lo, 2), h2 = __shfl_xor_sync(0xffffffffu, hi, 2);
+        lo = min3(lo, l2, l2);
+        hi = max3(hi, h2, h2);
     }
+    const bool wide = !(lo >= -KV4_MAX && hi <= KV4_MAX);   // or not a number
+    const bool any_wide = __any_sync(0xffffffffu, wide);
+    bool bad = false;
+    float y[8];
 #pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    for (int i = 0; i < 8; ++i) y[i] = x[i];
+    if (any_wide) {
+        bad = !(fabsf(lo) < INFINITY && fabsf(hi) < INFINITY);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(x[i], -KV4_MAX), KV4_MAX);
+        lo = fminf(fmaxf(lo, -KV4_MAX), KV4_MAX);
+        hi = fminf(fmaxf(hi, -KV4_MAX), KV4_MAX);
     }
-    const unsigned group = 0xfu << (threadIdx.x & 28);
-    const bool bad = (__ballot_sync(0xffffffffu, nan != 0.f) & group) != 0;
-    const bool wide = __any_sync(0xffffffffu, !(lo >= -KV4_MAX && hi <= KV4_MAX));
-    lo = fmaxf(lo, -KV4_MAX);
-    hi = fminf(hi, KV4_MAX);
-    lo = fminf(lo, KV4_MAX);
-    hi = fmaxf(hi, -KV4_MAX);
     s = __float2half_rn(bad ? 0.f : __fdiv_rn(hi - lo, 15.f));
-    m = bad ? __ushort_as_half(0x7fff) : __float2half_rn(lo);
-    const float sf = __half2float(s), mf = bad ? 0.f : __half2float(m);
-    const float inv = sf > 0.f ? __frcp_rn(sf) : 0.f;
+    m = __float2half_rn(lo);
+    const float sf = __half2float(s), mf = __half2float(m);
+    if (bad) m = __ushort_as_half(0x7fff);
+    const float inv = sf > 0.f ? __frcp_rn(sf) * (1.f / 15.f) : 0.f;   // 0: every code is 0
     constexpr float ROUND = 12582912.f;   // 1.5 2^23: adding it rounds to a whole number
-    float y[8], off = 0.f;
+    float off = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        y[i] = wide ? fminf(fmaxf(x[i], -KV4_MAX), KV4_MAX) : x[i];
-        const float r = fminf(fmaxf((y[i] - mf) * inv, 0.f), 15.f);
-        code[i] = __fsub_rn(__fadd_rn(r, ROUND), ROUND);
-        off = fmaxf(off, fabsf(r - code[i]));
+        const float u = __saturatef(__fmul_rn(__fsub_rn(y[i], mf), inv));
+        code[i] = __fsub_rn(__fmaf_rn(u, 15.f, ROUND), ROUND);
+        off = fmaxf(off, fabsf(__fmaf_rn(u, 15.f, -code[i])));
     }
     if (__any_sync(0xffffffffu, off > 0.4999f)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             code[i] = sf > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(y[i] - mf, sf)), 0.f), 15.f) : 0.f;
     }
-    if (bad) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) code[i] = 0.f;
-    }
 }
 
-// Four codes as the nibbles of 16 bits.
+// Four codes as the nibbles of the low 16 bits (what is above them is 2^23's).
 __device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float d)
 {
-    return __float_as_uint(fmaf(fmaf(fmaf(d, 16.f, c), 16.f, b), 16.f, a) + 8388608.f) & 0xffffu;   // 2^23
+    return __float_as_uint(fmaf(fmaf(fmaf(d, 16.f, c), 16.f, b), 16.f, a) + 8388608.f);
 }
 
 // Bytes of a V code word and of its scale for token t, group gr.
@@ -234,7 +247,7 @@ __device__ __forceinline__ int v_meta_at(int t, int gr)
 // A warp's q rows: token (b, j), heads h0 .. h0 + 7.  A lane holds 4 + 4 elements:
 // the two halves of 4 pairs, 4 pairs that lie together (interleaved), or 8 elements
 // that are not rotated.
-template <int D, typename T>
+template <int D, typename T, bool INTER>
 __device__ __forceinline__ void rotate_q(const Kv4AppendArgs &a, int64_t unit)
 {
     constexpr int LPR = D / 8, RPP = 32 / LPR, U = 8 / RPP;   // lanes of a row, rows of a pass, passes
@@ -248,7 +261,7 @@ __device__ __forceinline__ void rotate_q(const Kv4AppendArgs &a, int64_t unit)
     const bool on = real && (pos >= 0 || !a.rot);   // rows that are not there, or have no angle, are 0
     const bool turn = on && 8 * l < a.rot;
     int da = 8 * l, db = 8 * l + 4;
-    if (!a.interleaved && 8 * l < a.rot) da = 4 * l, db = 4 * l + (a.rot >> 1);
+    if (!INTER && 8 * l < a.rot) da = 4 * l, db = 4 * l + (a.rot >> 1);
     float x[U][4], y[U][4];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -277,10 +290,10 @@ __device__ __forceinline__ void rotate_q(const Kv4AppendArgs &a, int64_t unit)
             float p[8] = {x[u][0], x[u][1], x[u][2], x[u][3], y[u][0], y[u][1], y[u][2], y[u][3]};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x1 = a.interleaved ? p[2 * i] : p[i], x2 = a.interleaved ? p[2 * i + 1] : p[4 + i];
+                const float x1 = INTER ? p[2 * i] : p[i], x2 = INTER ? p[2 * i + 1] : p[4 + i];
                 const float r1 = __fsub_rn(__fmul_rn(x1, cs[i]), __fmul_rn(x2, sn[i]));
                 const float r2 = __fadd_rn(__fmul_rn(x2, cs[i]), __fmul_rn(x1, sn[i]));
-                if (a.interleaved) {
+                if (INTER) {
                     if (i < 2) x[u][2 * i] = r1, x[u][2 * i + 1] = r2;
                     else y[u][2 * i - 4] = r1, y[u][2 * i - 3] = r2;
                 } else {
@@ -294,18 +307,67 @@ __device__ __forceinline__ void rotate_q(const Kv4AppendArgs &a, int64_t unit)
     }
 }
 
+// A warp's pass over tokens of K rows (8 elements a lane): rotated,
+// quantised, written to `to` and taken into the elements' extremes (bf16 pairs).
+template <int D, bool INTER>
+__device__ __forceinline__ void k_pass(float (&x)[8], const Kv4AppendArgs &a, int t, int64_t pos, bool on, uint8_t *to,
+                                       __nv_bfloat162 (&lo)[4], __nv_bfloat162 (&hi)[4])
+{
+    constexpr int NG = Kv4<D>::NG;
+    const int sub = threadIdx.x & (D / 8 - 1), gr = sub >> 2, q4 = sub & 3;
+    if (a.rot) rotate8<INTER>(x, a, sub * 8, pos, on);
+    float code[8];
+    __half s, m;
+    quantise8(x, code, s, m);
+    if (!on) return;
+    *reinterpret_cast<uint32_t *>(to + t * (D / 2) + (q4 * NG + gr) * 4) =
+        __byte_perm(nibbles(code[0], code[2], code[4], code[6]), nibbles(code[1], code[3], code[5], code[7]), 0x5410);
+    if (q4 == 0) *reinterpret_cast<__half2 *>(to + Kv4<D>::K_META + (t * NG + gr) * 4) = __halves2half2(s, m);
+    if (!a.summary) return;
+    const bool fine = fabsf(x[0]) + fabsf(x[1]) + fabsf(x[2]) + fabsf(x[3]) + fabsf(x[4]) + fabsf(x[5]) + fabsf(x[6]) +
+                          fabsf(x[7]) < INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]), w = v;
+        if (!fine) {   // a key that is not finite opens its element's range
+            if (!isfinite(x[2 * i])) v.x = __float2bfloat16_rn(-INFINITY), w.x = __float2bfloat16_rn(INFINITY);
+            if (!isfinite(x[2 * i + 1])) v.y = __float2bfloat16_rn(-INFINITY), w.y = __float2bfloat16_rn(INFINITY);
+        }
+        lo[i] = __hmin2(lo[i], v);
+        hi[i] = __hmax2(hi[i], w);
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void v_pass(const float (&x)[8], int t, bool on, uint8_t *to)
+{
+    const int sub = threadIdx.x & (D / 8 - 1), gr = sub >> 2, q4 = sub & 3;
+    float code[8];
+    __half s, m;
+    quantise8(x, code, s, m);
+    if (!on) return;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<uint16_t *>(to + v_code_at<D>(t, gr, 2 * q4 + e)) =
+            (uint16_t)nibbles(code[4 * e], code[4 * e + 1], code[4 * e + 2], code[4 * e + 3]);
+    if (q4 == 0) {
+        uint8_t *p = to + v_meta_at<D>(t, gr);
+        *reinterpret_cast<__half *>(p) = s;
+        *reinterpret_cast<__half *>(p + 4) = m;
+    }
+}
+
 // Four warps.  kv_blocks of the grid's blocks take (chunk of max(page, 64) slots,
 // kv head) of a sequence each, a warp 16 slots of it at a time; the others q rows.
 // The two kinds alternate (every `every`-th block is a kv block), so that the
 // arithmetic of one and the memory traffic of the other share an SM.
-template <int D, typename T>
+template <int D, typename T, bool INTER>
 __global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int chunk_shift, int chunks, int64_t kv_blocks,
                                                          int64_t q_units, int every)
 {
     constexpr int LPR = D / 8;           // lanes of a row
-    constexpr int TPI = 16 / LPR;        // tokens of a warp's pass (K and V rows)
-    constexpr int DEEP = sizeof(T) == 2 ? 4 : 2;   // passes whose rows are on their way together
-    constexpr int NG = Kv4<D>::NG;
+    constexpr int TPP = 32 / LPR;        // tokens of a pass
+    constexpr int DEEP = 2;              // passes whose K and V rows are on their way together
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t bid = blockIdx.x;
     // kv blocks at multiples of `every`, as long as there are any
@@ -313,13 +375,13 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int ch
     if (!is_kv) {
         const int64_t before = (bid + every - 1) / every;   // kv blocks in front
         const int64_t unit = (bid - (before < kv_blocks ? before : kv_blocks)) * 4 + warp;
-        if (unit < q_units) rotate_q<D, T>(a, unit);
+        if (unit < q_units) rotate_q<D, T, INTER>(a, unit);
         return;
     }
     const int64_t kb = bid / every;
-    __shared__ float red[4][2][D];
+    __shared__ __nv_bfloat16 red[4][2][D];
     __shared__ __align__(16) uint8_t stage[4][Kv4<D>::BYTES];
-    const int sub = lane & (LPR - 1), d0 = sub * 8;
+    const int sub = lane & (LPR - 1), d0 = sub * 8, tsub = lane / LPR;
     const int h = (int)(kb % a.pool.Hkv);
     const int c = (int)(kb / a.pool.Hkv % chunks);
     const int b = (int)(kb / a.pool.Hkv / chunks);
@@ -333,12 +395,11 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int ch
     if (c0 >= end) return;
     const int chunk = 1 << chunk_shift;
     const int ps = a.pool.page_shift;
-    const bool is_v = (lane / LPR) & 1;
-    const int tsub = lane / (2 * LPR);
-    const int gr = sub >> 2, q4 = sub & 3;
-    float lo[8], hi[8];   // per-d extremes of the K rows that this lane has seen
+    const T *const k0 = static_cast<const T *>(a.k) + b * a.ks[0] + h * a.ks[2] + d0;
+    const T *const v0 = static_cast<const T *>(a.v) + b * a.vs[0] + h * a.vs[2] + d0;
+    __nv_bfloat162 lo[4], hi[4];   // extremes of the K rows that this lane has seen
 #pragma unroll
-    for (int i = 0; i < 8; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
+    for (int i = 0; i < 4; ++i) lo[i] = __float2bfloat162_rn(INFINITY), hi[i] = __float2bfloat162_rn(-INFINITY);
     for (int s0 = warp * KV4_BLOCK; s0 < chunk; s0 += 4 * KV4_BLOCK) {
         const int64_t slot0 = c0 + s0;
         if (slot0 >= end || slot0 + KV4_BLOCK <= len) continue;
@@ -353,54 +414,31 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int ch
         const unsigned live = __ballot_sync(0xffffffffu, mine && (at >= 0 || !a.rot));
         const bool full = live == 0xffffu;
         uint8_t *const to = full ? stage[warp] : blk;
-        for (int t0 = t_lo; t0 < t_hi; t0 += TPI * DEEP) {
-            typename RawOf<T>::type raw[DEEP];
+#pragma unroll 1
+        for (int t0 = t_lo; t0 < t_hi; t0 += TPP * DEEP) {
+            typename RawOf<T>::type kr[DEEP], vr[DEEP];
 #pragma unroll
             for (int u = 0; u < DEEP; ++u) {
-                const int t = t0 + u * TPI + tsub;
-                clear(raw[u]);
+                const int t = t0 + u * TPP + tsub;
+                clear(kr[u]);
+                clear(vr[u]);
                 if (t < t_hi && (live >> t & 1)) {
                     const int64_t j = slot0 + t - len;
-                    const int64_t st0 = is_v ? a.vs[0] : a.ks[0], st1 = is_v ? a.vs[1] : a.ks[1], st2 = is_v ? a.vs[2] : a.ks[2];
-                    fetch8(static_cast<const T *>(is_v ? a.v : a.k) + b * st0 + j * st1 + h * st2 + d0, raw[u]);
+                    fetch8(k0 + j * a.ks[1], kr[u]);
+                    fetch8(v0 + j * a.vs[1], vr[u]);
                 }
             }
 #pragma unroll
             for (int u = 0; u < DEEP; ++u) {
-                if (t0 + u * TPI >= t_hi) break;
-                const int t = t0 + u * TPI + tsub;
+                if (t0 + u * TPP >= t_hi) break;
+                const int t = t0 + u * TPP + tsub;
                 const bool on = t < t_hi && (live >> t & 1);
                 const int64_t pos = __shfl_sync(0xffffffffu, at, t & 31);
-                float x[8], code[8];
-                widen(raw[u], x);
-                if (a.rot) rotate8(x, a, d0, pos, on && !is_v);
-                __half s, m;
-                quantise8(x, code, s, m);
-                if (!on) continue;
-                if (!is_v) {
-                    *reinterpret_cast<uint32_t *>(to + t * (D / 2) + (q4 * NG + gr) * 4) =
-                        nibbles(code[0], code[2], code[4], code[6]) | nibbles(code[1], code[3], code[5], code[7]) << 16;
-                    if (q4 == 0)
-                        *reinterpret_cast<__half2 *>(to + Kv4<D>::K_META + (t * NG + gr) * 4) = __halves2half2(s, m);
-                    if (a.summary) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const bool fin = isfinite(x[i]);
-                            lo[i] = fminf(lo[i], fin ? x[i] : -INFINITY);
-                            hi[i] = fmaxf(hi[i], fin ? x[i] : INFINITY);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<uint16_t *>(to + v_code_at<D>(t, gr, 2 * q4 + e)) =
-                            (uint16_t)nibbles(code[4 * e], code[4 * e + 1], code[4 * e + 2], code[4 * e + 3]);
-                    if (q4 == 0) {
-                        uint8_t *p = to + v_meta_at<D>(t, gr);
-                        *reinterpret_cast<__half *>(p) = s;
-                        *reinterpret_cast<__half *>(p + 4) = m;
-                    }
-                }
+                float x[8];
+                widen(kr[u], x);
+                k_pass<D, INTER>(x, a, t, pos, on, to, lo, hi);
+                widen(vr[u], x);
+                v_pass<D>(x, t, on, to);
             }
         }
         __syncwarp();
@@ -415,15 +453,19 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int ch
         }
     }
     if (!a.summary) return;
-    // extremes over the warp's token slots (D = 64: two per pass), then over the
-    // warps that share a page
+    // extremes over the lanes that hold the same elements of other tokens, then over
+    // the warps that share a page
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (TPI == 2) {
-            lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], 16));
-            hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], 16));
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int o = LPR; o < 32; o <<= 1) {
+            lo[i] = __hmin2(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+            hi[i] = __hmax2(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
         }
-        if (!is_v && tsub == 0) red[warp][0][d0 + i] = lo[i], red[warp][1][d0 + i] = hi[i];
+        if (tsub == 0) {
+            *reinterpret_cast<__nv_bfloat162 *>(&red[warp][0][d0 + 2 * i]) = lo[i];
+            *reinterpret_cast<__nv_bfloat162 *>(&red[warp][1][d0 + 2 * i]) = hi[i];
+        }
     }
     __syncthreads();
     const int share = (1 << ps) >= 64 ? 4 : (1 << ps) / KV4_BLOCK;   // warps that share a page
@@ -431,16 +473,13 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int ch
         const int p = x / (2 * D), mx = x / D & 1, d = x % D;
         const int64_t p0 = c0 + ((int64_t)p << ps);   // first slot of the page
         if (p0 >= end || p0 + (1 << ps) <= len) continue;
-        float r = red[p * share][mx][d];
-        for (int w = 1; w < share; ++w) r = mx ? fmaxf(r, red[p * share + w][mx][d]) : fminf(r, red[p * share + w][mx][d]);
+        __nv_bfloat16 r = red[p * share][mx][d];
+        for (int w = 1; w < share; ++w) r = mx ? __hmax(r, red[p * share + w][mx][d]) : __hmin(r, red[p * share + w][mx][d]);
         const int id = kv4_page(a.pool, b, p0 >> ps);
         if (id < 0) continue;
         __nv_bfloat16 *to = a.summary + (((int64_t)id * a.pool.Hkv + h) * 2 + mx) * D + d;
-        if (p0 < len) {
-            const float old = __bfloat162float(*to);
-            r = mx ? fmaxf(r, old) : fminf(r, old);
-        }
-        *to = __float2bfloat16_rn(r);
+        if (p0 < len) r = mx ? __hmax(r, *to) : __hmin(r, *to);
+        *to = r;
     }
 }
 
@@ -565,8 +604,11 @@ int launch_kv4_append(const Kv4AppendArgs &a, int D, int dtype, cudaStream_t st)
     const int64_t blocks = kv_blocks + (q_units + 3) / 4;
     if (blocks > 0x7fffffffLL) return CP_EUNSUPPORTED;
     const int every = (int)(blocks / kv_blocks);
-#define CP_KV4_APPEND(D_, T_) \
-    kv4_append_kernel<D_, T_><<<(unsigned)blocks, 128, 0, st>>>(a, chunk_shift, (int)chunks, kv_blocks, q_units, every)
+#define CP_KV4_APPEND(D_, T_)                                                                                         \
+    (a.interleaved ? kv4_append_kernel<D_, T_, true><<<(unsigned)blocks, 128, 0, st>>>(a, chunk_shift, (int)chunks,    \
+                                                                                       kv_blocks, q_units, every)       \
+                   : kv4_append_kernel<D_, T_, false><<<(unsigned)blocks, 128, 0, st>>>(a, chunk_shift, (int)chunks,   \
+                                                                                        kv_blocks, q_units, every))
     if (D == 64) {
         if (dtype == CP_BF16) CP_KV4_APPEND(64, __nv_bfloat16);
         else CP_KV4_APPEND(64, float);
