@@ -244,36 +244,23 @@ __device__ __forceinline__ int v_meta_at(int t, int gr)
     return Kv4<D>::V_META + (((t >> 3) * 4 + ((t & 7) >> 1)) * Kv4<D>::NG + gr) * 8 + (t & 1) * 2;
 }
 
-// A warp's q rows: token (b, j), heads h0 .. h0 + 7.  A lane holds 4 + 4 elements:
-// the two halves of 4 pairs, 4 pairs that lie together (interleaved), or 8 elements
-// that are not rotated.
+// A warp's q rows: `span` eights of heads of one token.  A lane holds 4 + 4 elements
+// of a row: the two halves of 4 pairs, 4 pairs that lie together (interleaved), or 8
+// elements that are not rotated.
 template <int D, typename T, bool INTER>
-__device__ __forceinline__ void rotate_q(const Kv4AppendArgs &a, int64_t unit)
+__device__ __forceinline__ void rotate_q(const Kv4AppendArgs &a, unsigned unit, int span, int spans)
 {
     constexpr int LPR = D / 8, RPP = 32 / LPR, U = 8 / RPP;   // lanes of a row, rows of a pass, passes
     const int lane = threadIdx.x & 31, l = lane & (LPR - 1);
-    const int hc = (a.Hq + 7) >> 3;
-    const int h0 = (int)(unit % hc) * 8;
-    const int64_t bj = unit / hc;
-    const int j = (int)(bj % a.n), b = (int)(bj / a.n);
+    const unsigned bj = unit / (unsigned)spans;
+    const int first = (int)(unit - bj * spans) * span * 8;
+    const int b = (int)(bj / (unsigned)a.n), j = (int)(bj - (unsigned)b * a.n);
     const bool real = j < new_tokens(a, b);
     const int64_t pos = real ? position(a, b, j, (int64_t)__ldg(a.pool.lens + b) + j) : -1;
     const bool on = real && (pos >= 0 || !a.rot);   // rows that are not there, or have no angle, are 0
     const bool turn = on && 8 * l < a.rot;
     int da = 8 * l, db = 8 * l + 4;
     if (!INTER && 8 * l < a.rot) da = 4 * l, db = 4 * l + (a.rot >> 1);
-    float x[U][4], y[U][4];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * RPP + lane / LPR;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[u][i] = y[u][i] = 0.f;
-        if (on && h < a.Hq) {
-            const T *p = static_cast<const T *>(a.q) + b * a.qs[0] + j * a.qs[1] + h * a.qs[2];
-            load4(p + da, x[u]);
-            load4(p + db, y[u]);
-        }
-    }
     float cs[4], sn[4];
     if (turn) {
         const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + pos * (a.rot >> 1) + 4 * l));
@@ -281,29 +268,44 @@ __device__ __forceinline__ void rotate_q(const Kv4AppendArgs &a, int64_t unit)
         cs[0] = cv.x, cs[1] = cv.y, cs[2] = cv.z, cs[3] = cv.w;
         sn[0] = sv.x, sn[1] = sv.y, sn[2] = sv.z, sn[3] = sv.w;
     }
+    const T *p = static_cast<const T *>(a.q) + b * a.qs[0] + j * a.qs[1] + (first + lane / LPR) * a.qs[2];
+    T *to = static_cast<T *>(a.q_out) + ((int64_t)bj * a.Hq + first + lane / LPR) * D;
+    const int64_t step = RPP * a.qs[2];
+    const int last = min(first + span * 8, a.Hq);
+#pragma unroll 1
+    for (int h0 = first + lane / LPR; h0 - lane / LPR < last; h0 += 8) {
+        float x[U][4], y[U][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * RPP + lane / LPR;
-        if (h >= a.Hq) continue;
-        if (turn) {
-            // pairs (x[i], y[i]), or (x[0], x[1]), (x[2], x[3]), (y[0], y[1]), (y[2], y[3])
-            float p[8] = {x[u][0], x[u][1], x[u][2], x[u][3], y[u][0], y[u][1], y[u][2], y[u][3]};
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x1 = INTER ? p[2 * i] : p[i], x2 = INTER ? p[2 * i + 1] : p[4 + i];
-                const float r1 = __fsub_rn(__fmul_rn(x1, cs[i]), __fmul_rn(x2, sn[i]));
-                const float r2 = __fadd_rn(__fmul_rn(x2, cs[i]), __fmul_rn(x1, sn[i]));
-                if (INTER) {
-                    if (i < 2) x[u][2 * i] = r1, x[u][2 * i + 1] = r2;
-                    else y[u][2 * i - 4] = r1, y[u][2 * i - 3] = r2;
-                } else {
-                    x[u][i] = r1, y[u][i] = r2;
-                }
+            for (int i = 0; i < 4; ++i) x[u][i] = y[u][i] = 0.f;
+            if (on && h0 + u * RPP < last) {
+                load4(p + u * step + da, x[u]);
+                load4(p + u * step + db, y[u]);
             }
         }
-        T *to = static_cast<T *>(a.q_out) + (bj * a.Hq + h) * D;
-        store4(to + da, x[u]);
-        store4(to + db, y[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (h0 + u * RPP >= last) break;
+            if (turn) {
+                // pairs (x[i], y[i]), or (x[0], x[1]), (x[2], x[3]), (y[0], y[1]), (y[2], y[3])
+                float r[8] = {x[u][0], x[u][1], x[u][2], x[u][3], y[u][0], y[u][1], y[u][2], y[u][3]};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float &x1 = INTER ? r[2 * i] : r[i], &x2 = INTER ? r[2 * i + 1] : r[4 + i];
+                    const float r1 = __fsub_rn(__fmul_rn(x1, cs[i]), __fmul_rn(x2, sn[i]));
+                    const float r2 = __fadd_rn(__fmul_rn(x2, cs[i]), __fmul_rn(x1, sn[i]));
+                    x1 = r1;
+                    x2 = r2;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[u][i] = r[i], y[u][i] = r[4 + i];
+            }
+            store4(to + u * RPP * D + da, x[u]);
+            store4(to + u * RPP * D + db, y[u]);
+        }
+        p += U * step;
+        to += 8 * D;
     }
 }
 
@@ -362,29 +364,27 @@ __device__ __forceinline__ void v_pass(const float (&x)[8], int t, bool on, uint
 // The two kinds alternate (every `every`-th block is a kv block), so that the
 // arithmetic of one and the memory traffic of the other share an SM.
 template <int D, typename T, bool INTER>
-__global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int chunk_shift, int chunks, int64_t kv_blocks,
-                                                         int64_t q_units, int every)
+__global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int chunk_shift, unsigned chunks, unsigned kv_blocks,
+                                                         unsigned q_units, int span, int spans, unsigned every)
 {
     constexpr int LPR = D / 8;           // lanes of a row
     constexpr int TPP = 32 / LPR;        // tokens of a pass
     constexpr int DEEP = 2;              // passes whose K and V rows are on their way together
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t bid = blockIdx.x;
-    // kv blocks at multiples of `every`, as long as there are any
-    const bool is_kv = bid % every == 0 && bid / every < kv_blocks;
-    if (!is_kv) {
-        const int64_t before = (bid + every - 1) / every;   // kv blocks in front
-        const int64_t unit = (bid - (before < kv_blocks ? before : kv_blocks)) * 4 + warp;
-        if (unit < q_units) rotate_q<D, T, INTER>(a, unit);
+    // kv blocks at multiples of `every`, as long as there are any (32-bit indices: a
+    // 64-bit division is a hundred instructions, as much as a q row's work)
+    const unsigned bid = blockIdx.x, kb = bid / every;
+    if (kb * every != bid || kb >= kv_blocks) {
+        const unsigned before = min(kb + 1, kv_blocks);   // kv blocks in front
+        const unsigned unit = (bid - before) * 4 + warp;
+        if (unit < q_units) rotate_q<D, T, INTER>(a, unit, span, spans);
         return;
     }
-    const int64_t kb = bid / every;
     __shared__ __nv_bfloat16 red[4][2][D];
     __shared__ __align__(16) uint8_t stage[4][Kv4<D>::BYTES];
     const int sub = lane & (LPR - 1), d0 = sub * 8, tsub = lane / LPR;
-    const int h = (int)(kb % a.pool.Hkv);
-    const int c = (int)(kb / a.pool.Hkv % chunks);
-    const int b = (int)(kb / a.pool.Hkv / chunks);
+    const unsigned bc = kb / (unsigned)a.pool.Hkv;
+    const int h = (int)(kb - bc * a.pool.Hkv), b = (int)(bc / chunks), c = (int)(bc - b * chunks);
     const int64_t len = __ldg(a.pool.lens + b);
     if (len < 0) {
         if (threadIdx.x == 0) kv4_report(a.pool.err);
@@ -507,16 +507,15 @@ __device__ __forceinline__ float half_of(uint32_t w, int hi)
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(128) kv4_gather_kernel(Kv4GatherArgs a, int blocks, int64_t warps)
+__global__ void __launch_bounds__(128) kv4_gather_kernel(Kv4GatherArgs a, unsigned blocks, unsigned warps)
 {
     constexpr int NG = Kv4<D>::NG;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int64_t wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const unsigned wid = blockIdx.x * 4 + (threadIdx.x >> 5);
     if (wid >= warps) return;
     // heads next to each other: their rows are neighbours in k and v
-    const int h = (int)(wid % a.pool.Hkv);
-    const int x = (int)(wid / a.pool.Hkv % blocks);
-    const int b = (int)(wid / a.pool.Hkv / blocks);
+    const unsigned bx = wid / (unsigned)a.pool.Hkv;
+    const int h = (int)(wid - bx * a.pool.Hkv), b = (int)(bx / blocks), x = (int)(bx - b * blocks);
     const int len = kv4_len(a.pool, b);
     int64_t first = a.start ? (int64_t)__ldg(a.start + b) : 0;
     if (first < 0) {
@@ -600,15 +599,23 @@ int launch_kv4_append(const Kv4AppendArgs &a, int D, int dtype, cudaStream_t st)
     const int chunk = 1 << chunk_shift;
     const int64_t chunks = ((int64_t)a.n + chunk - 2) / chunk + 1;
     const int64_t kv_blocks = chunks * a.pool.Hkv * a.B;
-    const int64_t q_units = a.q ? (int64_t)a.B * a.n * ((a.Hq + 7) / 8) : 0;
+    // q: a warp takes all heads of a token where there are tokens enough to fill the
+    // GPU, else eight
+    const int64_t tokens = (int64_t)a.B * a.n;
+    const int eights = (a.Hq + 7) / 8;
+    const int span = tokens >= (int64_t)sm_count() * 32 ? eights : 1, spans = (eights + span - 1) / span;
+    const int64_t q_units = a.q ? tokens * spans : 0;
     const int64_t blocks = kv_blocks + (q_units + 3) / 4;
-    if (blocks > 0x7fffffffLL) return CP_EUNSUPPORTED;
-    const int every = (int)(blocks / kv_blocks);
-#define CP_KV4_APPEND(D_, T_)                                                                                         \
-    (a.interleaved ? kv4_append_kernel<D_, T_, true><<<(unsigned)blocks, 128, 0, st>>>(a, chunk_shift, (int)chunks,    \
-                                                                                       kv_blocks, q_units, every)       \
-                   : kv4_append_kernel<D_, T_, false><<<(unsigned)blocks, 128, 0, st>>>(a, chunk_shift, (int)chunks,   \
-                                                                                        kv_blocks, q_units, every))
+    if (blocks > 0x3fffffffLL || q_units > 0x7fffffffLL) return CP_EUNSUPPORTED;
+    const unsigned every = (unsigned)(blocks / kv_blocks);
+#define CP_KV4_LAUNCH(D_, T_, I_)                                                                              \
+    kv4_append_kernel<D_, T_, I_><<<(unsigned)blocks, 128, 0, st>>>(a, chunk_shift, (unsigned)chunks,          \
+                                                                    (unsigned)kv_blocks, (unsigned)q_units, span, spans, every)
+#define CP_KV4_APPEND(D_, T_)                          \
+    do {                                               \
+        if (a.interleaved) CP_KV4_LAUNCH(D_, T_, true); \
+        else CP_KV4_LAUNCH(D_, T_, false);             \
+    } while (0)
     if (D == 64) {
         if (dtype == CP_BF16) CP_KV4_APPEND(64, __nv_bfloat16);
         else CP_KV4_APPEND(64, float);
@@ -617,6 +624,7 @@ int launch_kv4_append(const Kv4AppendArgs &a, int D, int dtype, cudaStream_t st)
         else CP_KV4_APPEND(128, float);
     }
 #undef CP_KV4_APPEND
+#undef CP_KV4_LAUNCH
     return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 
@@ -626,9 +634,9 @@ int launch_kv4_gather(const Kv4GatherArgs &a, int D, int dtype, cudaStream_t st)
     const int64_t blocks = ((int64_t)a.count + KV4_BLOCK - 2) / KV4_BLOCK + 1;
     const int64_t warps = blocks * a.pool.Hkv * a.B;
     const int64_t grid = (warps + 3) / 4;
-    if (grid > 0x7fffffffLL) return CP_EUNSUPPORTED;
+    if (warps > 0x7fffffffLL) return CP_EUNSUPPORTED;
 #define CP_KV4_GATHER(D_, T_) \
-    kv4_gather_kernel<D_, T_><<<(unsigned)grid, 128, 0, st>>>(a, (int)blocks, warps)
+    kv4_gather_kernel<D_, T_><<<(unsigned)grid, 128, 0, st>>>(a, (unsigned)blocks, (unsigned)warps)
     if (D == 64) {
         if (dtype == CP_BF16) CP_KV4_GATHER(64, __nv_bfloat16);
         else CP_KV4_GATHER(64, float);
