@@ -104,13 +104,13 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&x)[4])
 // Rotates the 8 elements d0.. of a row spread over consecutive lanes (8 per
 // lane).  Every lane of the warp calls it; lanes with turn == false keep x.
 template <bool INTER>
-__device__ __forceinline__ void rotate8(float (&x)[8], const Kv4AppendArgs &a, int d0, int64_t pos, bool turn)
+__device__ __forceinline__ void rotate8(float (&x)[8], const Kv4AppendArgs &a, int d0, int pos, bool turn)
 {
     const int half = a.rot >> 1;
     const bool in = turn && d0 < a.rot;
     if (INTER) {
         if (in) {
-            const int64_t at = pos * half + (d0 >> 1);
+            const int64_t at = (int64_t)pos * half + (d0 >> 1);
             const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
             const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
             const float cs[4] = {cv.x, cv.y, cv.z, cv.w}, sn[4] = {sv.x, sv.y, sv.z, sv.w};
@@ -129,7 +129,7 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const Kv4AppendArgs &a, i
     const float sign = first ? -1.f : 1.f;   // x1 cos - x2 sin, x2 cos + x1 sin
     float cs[8], sn[8];
     if (in) {
-        const int64_t at = pos * half + (first ? d0 : d0 - half);
+        const int64_t at = (int64_t)pos * half + (first ? d0 : d0 - half);
         load8(a.cos + at, cs);
         load8(a.sin + at, sn);
     }
@@ -140,15 +140,17 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const Kv4AppendArgs &a, i
     }
 }
 
-// Position of token (b, j); -1 (and CP_ECACHE) outside the rotation table.
-__device__ __forceinline__ int64_t position(const Kv4AppendArgs &a, int b, int j, int64_t slot)
+// Position of token (b, j); -1 (and CP_ECACHE) outside the rotation table, 0 where
+// nothing is rotated.
+__device__ __forceinline__ int position(const Kv4AppendArgs &a, int b, int j, int64_t slot)
 {
+    if (!a.rot) return 0;
     const int64_t p = a.positions ? (int64_t)__ldg(a.positions + (int64_t)b * a.n + j) : slot;
-    if (a.rot && (p < 0 || p >= a.max_pos)) {
+    if (p < 0 || p >= a.max_pos) {
         kv4_report(a.pool.err);
         return -1;
     }
-    return p;
+    return (int)p;
 }
 
 __device__ __forceinline__ int new_tokens(const Kv4AppendArgs &a, int b)
@@ -177,9 +179,9 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 }
 
 // Codes (as whole floats), scale and minimum of a lane's 8 elements; the group is
-// 4 lanes.  rint((y - m) / s) is taken from a product with 1 / (15 s), held to
-// [0, 1], times 15: off the quotient by less than 6 units in the last place, under
-// 1e-5 at 15; where a lane's product comes that near a half the warp divides.
+// 4 lanes.  s is the range times fp32(1 / 15), a = fp32(1 / s) fp32(1 / 15), and a
+// code 15 clamp((y - m) a, 0, 1) rounded: no division but one reciprocal a group, the
+// clamp is the product's own, and the rounding that of adding 1.5 2^23.
 __device__ __forceinline__ void quantise8(const float (&x)[8], float (&code)[8], __half &s, __half &m)
 {
     float lo = min3(min3(x[0], x[1], x[2]), min3(x[3], x[4], x[5]), min3(x[6], x[7], x[7]));
@@ -192,36 +194,22 @@ __device__ __forceinline__ void quantise8(const float (&x)[8], float (&code)[8],
         lo = min3(lo, l2, l2);
         hi = max3(hi, h2, h2);
     }
-    const bool wide = !(lo >= -KV4_MAX && hi <= KV4_MAX);   // or not a number
-    const bool any_wide = __any_sync(0xffffffffu, wide);
-    bool bad = false;
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i];
-    if (any_wide) {
-        bad = !(fabsf(lo) < INFINITY && fabsf(hi) < INFINITY);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(x[i], -KV4_MAX), KV4_MAX);
-        lo = fminf(fmaxf(lo, -KV4_MAX), KV4_MAX);
-        hi = fminf(fmaxf(hi, -KV4_MAX), KV4_MAX);
-    }
-    s = __float2half_rn(bad ? 0.f : __fdiv_rn(hi - lo, 15.f));
+    const bool bad = !(fabsf(lo) < INFINITY && fabsf(hi) < INFINITY);
+    // beyond the largest magnitude: an element's code comes out as its clamped value's
+    lo = fminf(fmaxf(lo, -KV4_MAX), KV4_MAX);
+    hi = fminf(fmaxf(hi, -KV4_MAX), KV4_MAX);
+    constexpr float FIFTEENTH = 1.f / 15.f;
+    s = __float2half_rn(__fmul_rn(hi - lo, FIFTEENTH));
     m = __float2half_rn(lo);
     const float sf = __half2float(s), mf = __half2float(m);
-    if (bad) m = __ushort_as_half(0x7fff);
-    const float inv = sf > 0.f ? __frcp_rn(sf) * (1.f / 15.f) : 0.f;   // 0: every code is 0
+    const float a = sf > 0.f && !bad ? __fmul_rn(__frcp_rn(sf), FIFTEENTH) : 0.f;   // 0: every code is 0
+    if (bad) s = __ushort_as_half(0), m = __ushort_as_half(0x7fff);
     constexpr float ROUND = 12582912.f;   // 1.5 2^23: adding it rounds to a whole number
-    float off = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float u = __saturatef(__fmul_rn(__fsub_rn(y[i], mf), inv));
+        float u;
+        asm("mul.rn.sat.f32 %0, %1, %2;" : "=f"(u) : "f"(__fsub_rn(x[i], mf)), "f"(a));
         code[i] = __fsub_rn(__fmaf_rn(u, 15.f, ROUND), ROUND);
-        off = fmaxf(off, fabsf(__fmaf_rn(u, 15.f, -code[i])));
-    }
-    if (__any_sync(0xffffffffu, off > 0.4999f)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            code[i] = sf > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(y[i] - mf, sf)), 0.f), 15.f) : 0.f;
     }
 }
 
@@ -256,15 +244,15 @@ __device__ __forceinline__ void rotate_q(const Kv4AppendArgs &a, unsigned unit, 
     const int first = (int)(unit - bj * spans) * span * 8;
     const int b = (int)(bj / (unsigned)a.n), j = (int)(bj - (unsigned)b * a.n);
     const bool real = j < new_tokens(a, b);
-    const int64_t pos = real ? position(a, b, j, (int64_t)__ldg(a.pool.lens + b) + j) : -1;
-    const bool on = real && (pos >= 0 || !a.rot);   // rows that are not there, or have no angle, are 0
+    const int pos = real ? position(a, b, j, (int64_t)__ldg(a.pool.lens + b) + j) : -1;
+    const bool on = pos >= 0;                       // rows that are not there, or have no angle, are 0
     const bool turn = on && 8 * l < a.rot;
     int da = 8 * l, db = 8 * l + 4;
     if (!INTER && 8 * l < a.rot) da = 4 * l, db = 4 * l + (a.rot >> 1);
     float cs[4], sn[4];
     if (turn) {
-        const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + pos * (a.rot >> 1) + 4 * l));
-        const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + pos * (a.rot >> 1) + 4 * l));
+        const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + (int64_t)pos * (a.rot >> 1) + 4 * l));
+        const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + (int64_t)pos * (a.rot >> 1) + 4 * l));
         cs[0] = cv.x, cs[1] = cv.y, cs[2] = cv.z, cs[3] = cv.w;
         sn[0] = sv.x, sn[1] = sv.y, sn[2] = sv.z, sn[3] = sv.w;
     }
@@ -309,15 +297,29 @@ __device__ __forceinline__ void rotate_q(const Kv4AppendArgs &a, unsigned unit, 
     }
 }
 
-// A warp's pass over tokens of K rows (8 elements a lane): rotated,
-// quantised, written to `to` and taken into the elements' extremes (bf16 pairs).
+// A warp's pass over tokens of K rows (8 elements a lane): rotated, taken into the
+// elements' extremes (bf16 pairs), quantised and written to `to`.
 template <int D, bool INTER>
-__device__ __forceinline__ void k_pass(float (&x)[8], const Kv4AppendArgs &a, int t, int64_t pos, bool on, uint8_t *to,
+__device__ __forceinline__ void k_pass(float (&x)[8], const Kv4AppendArgs &a, int t, int pos, bool on, uint8_t *to,
                                        __nv_bfloat162 (&lo)[4], __nv_bfloat162 (&hi)[4])
 {
     constexpr int NG = Kv4<D>::NG;
     const int sub = threadIdx.x & (D / 8 - 1), gr = sub >> 2, q4 = sub & 3;
     if (a.rot) rotate8<INTER>(x, a, sub * 8, pos, on);
+    if (a.summary && on) {
+        const float size = fabsf(x[0]) + fabsf(x[1]) + fabsf(x[2]) + fabsf(x[3]) + fabsf(x[4]) + fabsf(x[5]) + fabsf(x[6]) +
+                           fabsf(x[7]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]), w = v;
+            if (!(size < INFINITY)) {   // a key that is not finite opens its element's range
+                if (!isfinite(x[2 * i])) v.x = __float2bfloat16_rn(-INFINITY), w.x = __float2bfloat16_rn(INFINITY);
+                if (!isfinite(x[2 * i + 1])) v.y = __float2bfloat16_rn(-INFINITY), w.y = __float2bfloat16_rn(INFINITY);
+            }
+            lo[i] = __hmin2(lo[i], v);
+            hi[i] = __hmax2(hi[i], w);
+        }
+    }
     float code[8];
     __half s, m;
     quantise8(x, code, s, m);
@@ -325,19 +327,6 @@ __device__ __forceinline__ void k_pass(float (&x)[8], const Kv4AppendArgs &a, in
     *reinterpret_cast<uint32_t *>(to + t * (D / 2) + (q4 * NG + gr) * 4) =
         __byte_perm(nibbles(code[0], code[2], code[4], code[6]), nibbles(code[1], code[3], code[5], code[7]), 0x5410);
     if (q4 == 0) *reinterpret_cast<__half2 *>(to + Kv4<D>::K_META + (t * NG + gr) * 4) = __halves2half2(s, m);
-    if (!a.summary) return;
-    const bool fine = fabsf(x[0]) + fabsf(x[1]) + fabsf(x[2]) + fabsf(x[3]) + fabsf(x[4]) + fabsf(x[5]) + fabsf(x[6]) +
-                          fabsf(x[7]) < INFINITY;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]), w = v;
-        if (!fine) {   // a key that is not finite opens its element's range
-            if (!isfinite(x[2 * i])) v.x = __float2bfloat16_rn(-INFINITY), w.x = __float2bfloat16_rn(INFINITY);
-            if (!isfinite(x[2 * i + 1])) v.y = __float2bfloat16_rn(-INFINITY), w.y = __float2bfloat16_rn(INFINITY);
-        }
-        lo[i] = __hmin2(lo[i], v);
-        hi[i] = __hmax2(hi[i], w);
-    }
 }
 
 template <int D>
@@ -364,12 +353,11 @@ __device__ __forceinline__ void v_pass(const float (&x)[8], int t, bool on, uint
 // The two kinds alternate (every `every`-th block is a kv block), so that the
 // arithmetic of one and the memory traffic of the other share an SM.
 template <int D, typename T, bool INTER>
-__global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int chunk_shift, unsigned chunks, unsigned kv_blocks,
+__global__ void __launch_bounds__(128, 8) kv4_append_kernel(Kv4AppendArgs a, int chunk_shift, unsigned chunks, unsigned kv_blocks,
                                                          unsigned q_units, int span, int spans, unsigned every)
 {
     constexpr int LPR = D / 8;           // lanes of a row
     constexpr int TPP = 32 / LPR;        // tokens of a pass
-    constexpr int DEEP = 2;              // passes whose K and V rows are on their way together
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // kv blocks at multiples of `every`, as long as there are any (32-bit indices: a
     // 64-bit division is a hundred instructions, as much as a q row's work)
@@ -410,36 +398,28 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(Kv4AppendArgs a, int ch
         const int t_hi = end - slot0 < KV4_BLOCK ? (int)(end - slot0) : KV4_BLOCK;
         // lane t: whether token t is written, and its position
         const bool mine = lane >= t_lo && lane < t_hi;
-        const int64_t at = mine ? position(a, b, (int)(slot0 + lane - len), slot0 + lane) : -1;
-        const unsigned live = __ballot_sync(0xffffffffu, mine && (at >= 0 || !a.rot));
+        const int at = mine ? position(a, b, (int)(slot0 + lane - len), slot0 + lane) : -1;
+        const unsigned live = __ballot_sync(0xffffffffu, at >= 0);
         const bool full = live == 0xffffu;
         uint8_t *const to = full ? stage[warp] : blk;
+        int t = t_lo + tsub;
+        const T *kp = k0 + (slot0 + t - len) * a.ks[1], *vp = v0 + (slot0 + t - len) * a.vs[1];
 #pragma unroll 1
-        for (int t0 = t_lo; t0 < t_hi; t0 += TPP * DEEP) {
-            typename RawOf<T>::type kr[DEEP], vr[DEEP];
-#pragma unroll
-            for (int u = 0; u < DEEP; ++u) {
-                const int t = t0 + u * TPP + tsub;
-                clear(kr[u]);
-                clear(vr[u]);
-                if (t < t_hi && (live >> t & 1)) {
-                    const int64_t j = slot0 + t - len;
-                    fetch8(k0 + j * a.ks[1], kr[u]);
-                    fetch8(v0 + j * a.vs[1], vr[u]);
-                }
+        for (int t0 = t_lo; t0 < t_hi; t0 += TPP, t += TPP, kp += TPP * a.ks[1], vp += TPP * a.vs[1]) {
+            typename RawOf<T>::type kr, vr;
+            clear(kr);
+            clear(vr);
+            const bool on = live >> t & 1;   // t < 32
+            if (on) {
+                fetch8(kp, kr);
+                fetch8(vp, vr);
             }
-#pragma unroll
-            for (int u = 0; u < DEEP; ++u) {
-                if (t0 + u * TPP >= t_hi) break;
-                const int t = t0 + u * TPP + tsub;
-                const bool on = t < t_hi && (live >> t & 1);
-                const int64_t pos = __shfl_sync(0xffffffffu, at, t & 31);
-                float x[8];
-                widen(kr[u], x);
-                k_pass<D, INTER>(x, a, t, pos, on, to, lo, hi);
-                widen(vr[u], x);
-                v_pass<D>(x, t, on, to);
-            }
+            const int pos = __shfl_sync(0xffffffffu, at, t);
+            float x[8];
+            widen(kr, x);
+            k_pass<D, INTER>(x, a, t, pos, on, to, lo, hi);
+            widen(vr, x);
+            v_pass<D>(x, t, on, to);
         }
         __syncwarp();
         if (full) {

@@ -41,11 +41,12 @@ def quantise(x):
     bad = ~np.isfinite(g).all(-1, keepdims=True)
     y = np.clip(np.where(bad, F32(0), g), F32(-65408), F32(65408))
     lo, hi = y.min(-1, keepdims=True), y.max(-1, keepdims=True)
-    s = ((hi - lo) / F32(15)).astype(F16)
+    s = ((hi - lo) * F32(1 / 15)).astype(F16)
     m = lo.astype(F16)
     sf, mf = s.astype(F32), m.astype(F32)
-    t = np.rint((y - mf) / np.where(sf > 0, sf, F32(1)))
-    code = np.clip(np.where(sf > 0, t, F32(0)), 0, 15).astype(np.uint8)
+    a = np.where(sf > 0, F32(1) / np.where(sf > 0, sf, F32(1)) * F32(1 / 15), F32(0))
+    u = np.clip((y - mf) * a, F32(0), F32(1))
+    code = np.rint(15.0 * u.astype(np.float64)).astype(np.uint8)
     s, m = np.where(bad, F16(0), s), np.where(bad, F16(np.nan), m)
     code = np.where(bad, np.uint8(0), code)
     shape = x.shape
