@@ -309,15 +309,20 @@ __device__ __forceinline__ void k_pass(float (&x)[8], const Kv4AppendArgs &a, in
     if (a.summary && on) {
         const float size = fabsf(x[0]) + fabsf(x[1]) + fabsf(x[2]) + fabsf(x[3]) + fabsf(x[4]) + fabsf(x[5]) + fabsf(x[6]) +
                            fabsf(x[7]);
+        __nv_bfloat162 v[4], w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = w[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        if (__any_sync(__activemask(), !(size < INFINITY))) {   // a key that is not finite opens its element's range
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (!isfinite(x[2 * i])) v[i].x = __float2bfloat16_rn(-INFINITY), w[i].x = __float2bfloat16_rn(INFINITY);
+                if (!isfinite(x[2 * i + 1])) v[i].y = __float2bfloat16_rn(-INFINITY), w[i].y = __float2bfloat16_rn(INFINITY);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]), w = v;
-            if (!(size < INFINITY)) {   // a key that is not finite opens its element's range
-                if (!isfinite(x[2 * i])) v.x = __float2bfloat16_rn(-INFINITY), w.x = __float2bfloat16_rn(INFINITY);
-                if (!isfinite(x[2 * i + 1])) v.y = __float2bfloat16_rn(-INFINITY), w.y = __float2bfloat16_rn(INFINITY);
-            }
-            lo[i] = __hmin2(lo[i], v);
-            hi[i] = __hmax2(hi[i], w);
+            lo[i] = __hmin2(lo[i], v[i]);
+            hi[i] = __hmax2(hi[i], w[i]);
         }
     }
     float code[8];
@@ -353,7 +358,7 @@ __device__ __forceinline__ void v_pass(const float (&x)[8], int t, bool on, uint
 // The two kinds alternate (every `every`-th block is a kv block), so that the
 // arithmetic of one and the memory traffic of the other share an SM.
 template <int D, typename T, bool INTER>
-__global__ void __launch_bounds__(128, 8) kv4_append_kernel(Kv4AppendArgs a, int chunk_shift, unsigned chunks, unsigned kv_blocks,
+__global__ void __launch_bounds__(128, 7) kv4_append_kernel(Kv4AppendArgs a, int chunk_shift, unsigned chunks, unsigned kv_blocks,
                                                          unsigned q_units, int span, int spans, unsigned every)
 {
     constexpr int LPR = D / 8;           // lanes of a row
@@ -404,21 +409,26 @@ __global__ void __launch_bounds__(128, 8) kv4_append_kernel(Kv4AppendArgs a, int
         uint8_t *const to = full ? stage[warp] : blk;
         int t = t_lo + tsub;
         const T *kp = k0 + (slot0 + t - len) * a.ks[1], *vp = v0 + (slot0 + t - len) * a.vs[1];
+        typename RawOf<T>::type kr, vr;      // the next pass's rows, on their way during this one
+        clear(kr);
+        clear(vr);
+        if (live >> t & 1) {                 // t < 32
+            fetch8(kp, kr);
+            fetch8(vp, vr);
+        }
 #pragma unroll 1
-        for (int t0 = t_lo; t0 < t_hi; t0 += TPP, t += TPP, kp += TPP * a.ks[1], vp += TPP * a.vs[1]) {
-            typename RawOf<T>::type kr, vr;
-            clear(kr);
-            clear(vr);
-            const bool on = live >> t & 1;   // t < 32
-            if (on) {
-                fetch8(kp, kr);
-                fetch8(vp, vr);
-            }
+        for (int t0 = t_lo; t0 < t_hi; t0 += TPP, t += TPP) {
+            const bool on = live >> t & 1;
             const int pos = __shfl_sync(0xffffffffu, at, t);
+            const bool more = t + TPP < KV4_BLOCK && (live >> (t + TPP) & 1);
             float x[8];
             widen(kr, x);
+            kp += TPP * a.ks[1];
+            if (more) fetch8(kp, kr);
             k_pass<D, INTER>(x, a, t, pos, on, to, lo, hi);
             widen(vr, x);
+            vp += TPP * a.vs[1];
+            if (more) fetch8(vp, vr);
             v_pass<D>(x, t, on, to);
         }
         __syncwarp();
