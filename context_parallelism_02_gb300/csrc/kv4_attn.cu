@@ -12,7 +12,9 @@
 // feeds to the tensor core, in registers.
 //
 // Scores: with n the code, s_ij = sum_gr [ s_jgr sum_d n q_d + m_jgr sum_d q_d ].
-// Codes are exact in fp16; q is scaled per row by a power of two into fp16's
+// A masked nibble is an fp16 as it stands: a subnormal, n 2^-24 in the lowest four
+// bits and 16 n 2^-24 in the next four (their elements of q are divided by 16), so
+// unpacking K is one AND a pair.  q is scaled per row by a power of two into fp16's
 // range (bf16's 8 bits fit), so the products are exact and the group's scale
 // multiplies an fp32 sum.  The minima are one more product, m (fp16, exact) with
 // the rows' group sums of q in three fp16 parts.  V's values s n + m are rounded
@@ -81,8 +83,18 @@ __device__ __forceinline__ __half2 pick(uint32_t w, uint32_t mask)
     return as_h2(r);
 }
 
-// The four code pairs of a word (nibbles e, e + 4 of the low and high half) as
-// exact fp16 pairs: a nibble in the low bits of an fp16 of exponent 2^10 reads
+// The four code pairs of a word (nibbles e, e + 4 of the low and high half) as the
+// subnormal fp16 pairs n 2^-24, 16 n 2^-24, n 2^-24, 16 n 2^-24.
+__device__ __forceinline__ void unpack_raw(uint32_t w, uint32_t (&n)[4])
+{
+    const uint32_t u = w >> 8;
+    n[0] = w & 0x000f000fu;
+    n[1] = w & 0x00f000f0u;
+    n[2] = u & 0x000f000fu;
+    n[3] = u & 0x00f000f0u;
+}
+
+// The same as exact fp16 pairs n: a nibble in the low bits of an fp16 of exponent 2^10 reads
 // 1024 + n, in the next four bits 1024 + 16 n.
 __device__ __forceinline__ void unpack(uint32_t w, __half2 (&n)[4])
 {
@@ -102,7 +114,7 @@ __device__ __forceinline__ float ex2(float x) { return tc::ex2(x); }
 template <int D, int NT>
 struct Rows {
     static constexpr int NG = Kv4<D>::NG;
-    uint32_t q[NT][NG][4];     // group gr: elements 8 c + {0,1}, {2,3}, {4,5}, {6,7}
+    uint32_t q[NT][NG][4];     // group gr: elements 8 c + {0,1}, {2,3} / 16, {4,5}, {6,7} / 16
     uint32_t sum[NT][2];       // group c: hi, mid | lo, 0 of the sum of q
     float to_log2[NT][2];      // score -> log2 units, for the lane's two columns
     int limit[NT][2];          // slots that the column's row sees
@@ -212,10 +224,11 @@ __device__ __forceinline__ void make_rows(const Kv4AttnArgs &a, const Shape &sh,
             float part = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const __half2 v = __floats2half2_rn(__uint_as_float(x[i] << 16) * up,
-                                                    __uint_as_float(x[i] & 0xffff0000u) * up);
+                const float f = i & 1 ? up * 0.0625f : up;
+                const __half2 v = __floats2half2_rn(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xffff0000u) * f);
                 r.q[t][gr][i] = h2(v);
-                part += __low2float(v) + __high2float(v);
+                const float both = __low2float(v) + __high2float(v);
+                part += i & 1 ? both * 16.f : both;
             }
             part += __shfl_xor_sync(0xffffffffu, part, 1);
             part += __shfl_xor_sync(0xffffffffu, part, 2);
@@ -227,7 +240,7 @@ __device__ __forceinline__ void make_rows(const Kv4AttnArgs &a, const Shape &sh,
         const __half s2 = __float2half_rn(r1 - __half2float(s1));
         r.sum[t][0] = h2(__halves2half2(s0, s1));
         r.sum[t][1] = h2(__halves2half2(s2, __ushort_as_half(0)));
-        const float back = a.scale * LOG2E / up;
+        const float back = a.scale * LOG2E * (16777216.f / up);   // scores are in units of 2^-24 up
         const int lim = on ? kv4_limit(a.rows, it.b, j, len) : 0;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -272,18 +285,22 @@ __device__ __forceinline__ void block_scores(const uint8_t *blk, const Rows<D, N
         nb = *reinterpret_cast<const uint16_t *>(blk + Kv4<D>::K_META + ((g + 8) * NG + c) * 4 + 2) * 0x10001u;
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) mma16816_zero(x[t], na, nb, na, nb, r.sum[t][0], r.sum[t][1]);
+    for (int t = 0; t < NT; ++t) {
+        mma16816_zero(x[t], na, nb, na, nb, r.sum[t][0], r.sum[t][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[t][e] *= 1.f / 16777216.f;   // the codes' unit, 2^-24
+    }
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
-        __half2 u[4], v[4];
-        unpack(ka[gr], u);
-        unpack(kb[gr], v);
+        uint32_t u[4], v[4];
+        unpack_raw(ka[gr], u);
+        unpack_raw(kb[gr], v);
         const float sa = __low2float(as_h2(ma[gr])), sb = __low2float(as_h2(mb[gr]));
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float acc[4];
-            mma16816_zero(acc, h2(u[0]), h2(v[0]), h2(u[1]), h2(v[1]), r.q[t][gr][0], r.q[t][gr][1]);
-            mma16816(acc, h2(u[2]), h2(v[2]), h2(u[3]), h2(v[3]), r.q[t][gr][2], r.q[t][gr][3]);
+            mma16816_zero(acc, u[0], v[0], u[1], v[1], r.q[t][gr][0], r.q[t][gr][1]);
+            mma16816(acc, u[2], v[2], u[3], v[3], r.q[t][gr][2], r.q[t][gr][3]);
             x[t][0] = fmaf(sa, acc[0], x[t][0]);
             x[t][1] = fmaf(sa, acc[1], x[t][1]);
             x[t][2] = fmaf(sb, acc[2], x[t][2]);
