@@ -73,6 +73,16 @@ __device__ __forceinline__ uint8_t *kv4_block(const Kv4Pool &c, int id, int h, i
     return c.data + ((((int64_t)id * c.Hkv + h) << (c.page_shift - 4)) + blk) * Kv4<D>::BYTES;
 }
 
+// Every kernel of the cache is launched so that its blocks may start while the
+// kernel before it on the stream ends (kv4_launch), and begins with this: its own
+// successor may do the same, and nothing that an earlier kernel wrote is read before
+// that kernel is complete and its writes are visible.
+__device__ __forceinline__ void kv4_begin()
+{
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Length of sequence b, held inside the page table's reach.
 __device__ __forceinline__ int kv4_len(const Kv4Pool &c, int b)
 {
@@ -86,6 +96,22 @@ __device__ __forceinline__ int kv4_len(const Kv4Pool &c, int b)
 }
 
 #endif
+
+template <typename... P, typename... A>
+inline cudaError_t kv4_launch(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 struct Kv4AppendArgs {
     Kv4Pool pool;            // lens: tokens before the append

@@ -366,6 +366,7 @@ __global__ void __launch_bounds__(128, 7) kv4_append_kernel(Kv4AppendArgs a, int
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // kv blocks at multiples of `every`, as long as there are any (32-bit indices: a
     // 64-bit division is a hundred instructions, as much as a q row's work)
+    kv4_begin();
     const unsigned bid = blockIdx.x, kb = bid / every;
     if (kb * every != bid || kb >= kv_blocks) {
         const unsigned before = min(kb + 1, kv_blocks);   // kv blocks in front
@@ -502,6 +503,7 @@ __global__ void __launch_bounds__(128) kv4_gather_kernel(Kv4GatherArgs a, unsign
     constexpr int NG = Kv4<D>::NG;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const unsigned wid = blockIdx.x * 4 + (threadIdx.x >> 5);
+    kv4_begin();
     if (wid >= warps) return;
     // heads next to each other: their rows are neighbours in k and v
     const unsigned bx = wid / (unsigned)a.pool.Hkv;
@@ -598,9 +600,10 @@ int launch_kv4_append(const Kv4AppendArgs &a, int D, int dtype, cudaStream_t st)
     const int64_t blocks = kv_blocks + (q_units + 3) / 4;
     if (blocks > 0x3fffffffLL || q_units > 0x7fffffffLL) return CP_EUNSUPPORTED;
     const unsigned every = (unsigned)(blocks / kv_blocks);
-#define CP_KV4_LAUNCH(D_, T_, I_)                                                                              \
-    kv4_append_kernel<D_, T_, I_><<<(unsigned)blocks, 128, 0, st>>>(a, chunk_shift, (unsigned)chunks,          \
-                                                                    (unsigned)kv_blocks, (unsigned)q_units, span, spans, every)
+    cudaError_t rc;
+#define CP_KV4_LAUNCH(D_, T_, I_)                                                                                     \
+    rc = kv4_launch(kv4_append_kernel<D_, T_, I_>, (unsigned)blocks, 128, 0, st, a, chunk_shift, (unsigned)chunks,    \
+                    (unsigned)kv_blocks, (unsigned)q_units, span, spans, every)
 #define CP_KV4_APPEND(D_, T_)                          \
     do {                                               \
         if (a.interleaved) CP_KV4_LAUNCH(D_, T_, true); \
@@ -615,7 +618,7 @@ int launch_kv4_append(const Kv4AppendArgs &a, int D, int dtype, cudaStream_t st)
     }
 #undef CP_KV4_APPEND
 #undef CP_KV4_LAUNCH
-    return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ECUDA;
+    return rc == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 
 int launch_kv4_gather(const Kv4GatherArgs &a, int D, int dtype, cudaStream_t st)
@@ -625,8 +628,9 @@ int launch_kv4_gather(const Kv4GatherArgs &a, int D, int dtype, cudaStream_t st)
     const int64_t warps = blocks * a.pool.Hkv * a.B;
     const int64_t grid = (warps + 3) / 4;
     if (warps > 0x7fffffffLL) return CP_EUNSUPPORTED;
+    cudaError_t rc;
 #define CP_KV4_GATHER(D_, T_) \
-    kv4_gather_kernel<D_, T_><<<(unsigned)grid, 128, 0, st>>>(a, (unsigned)blocks, (unsigned)warps)
+    rc = kv4_launch(kv4_gather_kernel<D_, T_>, (unsigned)grid, 128, 0, st, a, (unsigned)blocks, (unsigned)warps)
     if (D == 64) {
         if (dtype == CP_BF16) CP_KV4_GATHER(64, __nv_bfloat16);
         else CP_KV4_GATHER(64, float);
@@ -635,7 +639,7 @@ int launch_kv4_gather(const Kv4GatherArgs &a, int D, int dtype, cudaStream_t st)
         else CP_KV4_GATHER(128, float);
     }
 #undef CP_KV4_GATHER
-    return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ECUDA;
+    return rc == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 
 }  // namespace cp

@@ -528,27 +528,21 @@ struct Smem {
     int abort, never;
 };
 
-// Over the batch, with every thread of the block (T of them): the extent of one
-// item of every sequence, and of those before sequence `upto`.
-template <int T>
-__device__ __forceinline__ void count_blocks(const Kv4AttnArgs &a, int upto, int64_t &all, int64_t &before, int64_t *red)
+// Over the batch, by a warp: the extent of one item of every sequence, and of those
+// before sequence `upto`.
+__device__ __forceinline__ void count_blocks(const Kv4AttnArgs &a, int upto, int64_t &all, int64_t &before)
 {
-    int64_t s = 0, p = 0;
-    for (int b = threadIdx.x; b < a.rows.B; b += T) {
+    all = before = 0;
+    for (int b = threadIdx.x & 31; b < a.rows.B; b += 32) {
         const int n = item_blocks(a, b) + PAD;
-        s += n;
-        if (b < upto) p += n;
+        all += n;
+        if (b < upto) before += n;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        p += __shfl_xor_sync(0xffffffffu, p, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
     }
-    if ((threadIdx.x & 31) == 0) red[2 * (threadIdx.x >> 5)] = s, red[2 * (threadIdx.x >> 5) + 1] = p;
-    __syncthreads();
-    all = before = 0;
-#pragma unroll
-    for (int w = 0; w < T / 32; ++w) all += red[2 * w], before += red[2 * w + 1];
 }
 
 // Length of a warp's stretch.
@@ -588,16 +582,16 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     Smem<D> &sm = *reinterpret_cast<Smem<D> *>(dyn);
     constexpr int NS = stages<D>(), NG = Kv4<D>::NG;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    asm volatile("griddepcontrol.launch_dependents;");
+    if (lane < NS) mbar_init(smem_u32(&sm.full[warp][lane]), NB);
+    if (threadIdx.x == 0) sm.abort = sm.never = 0;
+    fence_mbar_init();
+    kv4_begin();
     {   // what the chain of loads below will need, on its way to L2
         const int64_t line = ((int64_t)blockIdx.x * (WARPS * 32) + threadIdx.x) * 128;
         prefetch(a.pool.pages, line, (int64_t)a.rows.B * a.pool.max_pages * 4);
         prefetch(a.q, line, (int64_t)a.rows.B * a.rows.n * a.rows.Hq * D * 2);
         if (a.sel) prefetch(a.sel, line, (int64_t)a.rows.B * a.rows.n * a.pool.Hkv * a.n_sel * 4);
     }
-    if (lane < NS) mbar_init(smem_u32(&sm.full[warp][lane]), NB);
-    if (threadIdx.x == 0) sm.abort = sm.never = 0;
-    fence_mbar_init();
     // where the stretch begins: the extents of all items, then the sequence
     const int B = a.rows.B;
     int64_t all = 0;
@@ -792,16 +786,17 @@ template <int D, int NT, int JW, int JOIN_DEEP>
 __global__ void __launch_bounds__(JW * 32) kv4_join_kernel(Kv4AttnArgs a, Shape sh, int warps, int least)
 {
     constexpr int E = D / 32;
-    __shared__ int64_t red[2 * JW];
     __shared__ float sm_m[JW], sm_l[JW];
     __shared__ __align__(16) float sm_o[JW][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t item = blockIdx.x / sh.rows;
-    const int rr_all = blockIdx.x % sh.rows;
-    const int b = (int)(item / (sh.per_batch / sh.tiles));
-    const int x = (int)(item % (sh.per_batch / sh.tiles));      // (token, kv head)
+    const unsigned item = blockIdx.x / (unsigned)sh.rows, heads = sh.per_batch / sh.tiles;
+    const int rr_all = (int)(blockIdx.x - item * sh.rows);
+    const int b = (int)(item / heads), x = (int)(item - b * heads);   // x: (token, kv head)
+    asm volatile("griddepcontrol.launch_dependents;");
+    // the lengths may be read before the wait: this grid starts when every block of
+    // kv4_attn_kernel has passed its own, so what wrote them is complete
     int64_t all, before;
-    count_blocks<JW * 32>(a, b, all, before, red);
+    count_blocks(a, b, all, before);
     all *= sh.per_batch;
     const int64_t per = stretch(all, warps, least);
     const int nb = item_blocks(a, b);
@@ -909,30 +904,15 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
     const int64_t joins = (int64_t)a.rows.B * (sh.per_batch / sh.tiles) * sh.rows;
     if (joins > 0x7fffffffLL) return CP_EUNSUPPORTED;
     const int warps = grid * WARPS;
-    kv4_attn_kernel<D, NT><<<grid, WARPS * 32, smem, st>>>(a, sh, warps, LEAST);
-    if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
-    // its blocks start while the first kernel's end, and wait for its results;
+    if (kv4_launch(kv4_attn_kernel<D, NT>, (unsigned)grid, WARPS * 32, smem, st, a, sh, warps, LEAST) != cudaSuccess)
+        return CP_ECUDA;
     // many warps where a row is cut into many pieces
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)joins);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     const int64_t cuts = warps / ((int64_t)a.rows.B * sh.per_batch);   // pieces of an item, about
-    cudaError_t rc;
-    if (cuts > 64) {
-        cfg.blockDim = dim3(1024);
-        rc = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 32, 4>, a, sh, warps, LEAST);
-    } else if (cuts > 8) {
-        cfg.blockDim = dim3(256);
-        rc = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 8, 8>, a, sh, warps, LEAST);
-    } else {
-        cfg.blockDim = dim3(128);
-        rc = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 4, 2>, a, sh, warps, LEAST);
-    }
+    const unsigned n = (unsigned)joins;
+    const cudaError_t rc =
+        cuts > 64  ? kv4_launch(kv4_join_kernel<D, NT, 32, 4>, n, 1024, 0, st, a, sh, warps, LEAST)
+        : cuts > 16 ? kv4_launch(kv4_join_kernel<D, NT, 8, 8>, n, 256, 0, st, a, sh, warps, LEAST)
+                    : kv4_launch(kv4_join_kernel<D, NT, 4, 4>, n, 128, 0, st, a, sh, warps, LEAST);
     return rc == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 

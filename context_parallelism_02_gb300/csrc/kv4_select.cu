@@ -36,18 +36,29 @@ __device__ __forceinline__ uint32_t half_line(uint32_t w, bool neg)
 
 // One warp per 16 pages of one (sequence, token, kv head).
 template <int D>
-__global__ void __launch_bounds__(128) kv4_score_kernel(Kv4SelectArgs a, int tiles, int64_t warps)
+__global__ void __launch_bounds__(128) kv4_score_kernel(Kv4SelectArgs a, int tiles, unsigned warps)
 {
     constexpr int NI = D / 16;   // 16-byte pieces of a summary row per lane
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int64_t wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const unsigned wid = blockIdx.x * 4 + (threadIdx.x >> 5);
+    kv4_begin();
     if (wid >= warps) return;
     const int Hkv = a.pool.Hkv, group = a.rows.Hq / Hkv;
-    const int tile = (int)(wid % tiles);
-    const int64_t item = wid / tiles;
-    const int h = (int)(item % Hkv);
-    const int64_t bj = item / Hkv;
-    const int j = (int)(bj % a.rows.n), b = (int)(bj / a.rows.n);
+    const unsigned item = wid / (unsigned)tiles, bj = item / (unsigned)Hkv;
+    const int tile = (int)(wid - item * tiles), h = (int)(item - bj * Hkv);
+    const int b = (int)(bj / (unsigned)a.rows.n), j = (int)(bj - (unsigned)b * a.rows.n);
+    // what does not hang on the length is on its way before it is here: the first
+    // eight heads' q and the tile's page numbers (looked at below the length only)
+    uint4 q0[NI / 2];
+    const uint4 *const qp = reinterpret_cast<const uint4 *>(a.q + ((int64_t)bj * a.rows.Hq + h * group + min(g, group - 1)) * D);
+#pragma unroll
+    for (int i = 0; i < NI / 2; ++i) q0[i] = __ldg(qp + i * 4 + c);
+    int id[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int lp = tile * 16 + r * 8 + g;
+        id[r] = lp < a.pool.max_pages ? __ldg(a.pool.pages + (int64_t)b * a.pool.max_pages + lp) : -1;
+    }
     const int len = kv4_len(a.pool, b);
     const int lim = kv4_limit(a.rows, b, j, len);
     const int ps = a.pool.page_shift;
@@ -57,21 +68,26 @@ __global__ void __launch_bounds__(128) kv4_score_kernel(Kv4SelectArgs a, int til
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int lp = tile * 16 + r * 8 + g;
-        const int id = lp < pages ? kv4_page(a.pool, b, lp) : -1;
-        const uint4 *p = reinterpret_cast<const uint4 *>(a.summary + ((int64_t)(id < 0 ? 0 : id) * Hkv + h) * 2 * D);
+        if (lp >= pages) {
+            id[r] = -1;
+        } else if (id[r] < 0 || id[r] >= a.pool.n_pages) {
+            kv4_report(a.pool.err);
+            id[r] = -1;
+        }
+        const uint4 *p = reinterpret_cast<const uint4 *>(a.summary + ((int64_t)(id[r] < 0 ? 0 : id[r]) * Hkv + h) * 2 * D);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) w[r][i] = id >= 0 ? __ldg(p + i * 4 + c) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < NI; ++i) w[r][i] = id[r] >= 0 ? __ldg(p + i * 4 + c) : make_uint4(0, 0, 0, 0);
     }
     float best[2] = {-INFINITY, -INFINITY};
     bool nan[2] = {false, false};
     for (int h0 = 0; h0 < group; h0 += 8) {
-        const bool on = h0 + g < group;
-        const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (bj * a.rows.Hq + h * group + (on ? h0 + g : 0)) * D);
+        // heads past the group repeat its last one: their columns are not looked at
+        const uint4 *q = reinterpret_cast<const uint4 *>(a.q + ((int64_t)bj * a.rows.Hq + h * group + min(h0 + g, group - 1)) * D);
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const bool neg = i < NI / 2;
-            const uint4 x = __ldg(q + (neg ? i : i - NI / 2) * 4 + c);
+            const uint4 x = h0 == 0 ? q0[neg ? i : i - NI / 2] : __ldg(q + (neg ? i : i - NI / 2) * 4 + c);
             mma16816_bf16(acc, w[0][i].x, w[1][i].x, w[0][i].y, w[1][i].y, half_line(x.x, neg), half_line(x.y, neg));
             mma16816_bf16(acc, w[0][i].z, w[1][i].z, w[0][i].w, w[1][i].w, half_line(x.z, neg), half_line(x.w, neg));
         }
@@ -88,7 +104,7 @@ __global__ void __launch_bounds__(128) kv4_score_kernel(Kv4SelectArgs a, int til
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
         const int lp = tile * 16 + r * 8 + g;
-        if (c == 0 && lp < pages) a.scores[item * a.pool.max_pages + lp] = v;
+        if (c == 0 && lp < pages) a.scores[(int64_t)item * a.pool.max_pages + lp] = v;
     }
 }
 
@@ -102,73 +118,130 @@ __device__ __forceinline__ uint32_t page_key(const Kv4SelectArgs &a, const float
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int SEL_THREADS = 256;
+constexpr int SEL_THREADS = 512;
 
-__device__ __forceinline__ int block_sum(int v, int *red)
+// Sum over the block; red has two halves that calls use in turn, so that one
+// barrier a call is enough.
+__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t (*red)[SEL_THREADS / 32], int &turn)
 {
     v = __reduce_add_sync(0xffffffffu, v);
+    if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = v;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int s = 0;
-#pragma unroll
-    for (int w = 0; w < SEL_THREADS / 32; ++w) s += red[w];
+    const int lane = threadIdx.x & 31;
+    const uint32_t s = __reduce_add_sync(0xffffffffu, lane < SEL_THREADS / 32 ? red[turn][lane] : 0u);
+    turn ^= 1;
     return s;
 }
 
-// One block per (sequence, token, kv head): the n_sel-th largest key bit by bit,
-// then the pages above it and the first of those equal to it, in page order.
+// Two sums behind one barrier.
+__device__ __forceinline__ void block_sum2(uint32_t &v, uint32_t &w, uint32_t (*red)[SEL_THREADS / 32],
+                                           uint32_t (*red2)[SEL_THREADS / 32], int &turn)
+{
+    v = __reduce_add_sync(0xffffffffu, v);
+    w = __reduce_add_sync(0xffffffffu, w);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) red[turn][threadIdx.x >> 5] = v, red2[turn][threadIdx.x >> 5] = w;
+    __syncthreads();
+    v = __reduce_add_sync(0xffffffffu, lane < SEL_THREADS / 32 ? red[turn][lane] : 0u);
+    w = __reduce_add_sync(0xffffffffu, lane < SEL_THREADS / 32 ? red2[turn][lane] : 0u);
+    turn ^= 1;
+}
+
+// Sum over the threads before this one.
+__device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t (*red)[SEL_THREADS / 32], int &turn)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t upto = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t w = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += w;
+    }
+    if (lane == 31) red[turn][warp] = upto;
+    __syncthreads();
+    const uint32_t s = __reduce_add_sync(0xffffffffu, lane < warp ? red[turn][lane] : 0u);
+    turn ^= 1;
+    return s + upto - v;
+}
+
+// The n_sel-th largest key of a row's pages, two bits at a time from the top, then
+// the pages above it and the first of those equal to it, in page order.  A thread has
+// up to K neighbouring pages in registers; K = 0: any number, and the scores are read
+// again for every step.
+template <int K>
+__device__ __forceinline__ void take_top(const Kv4SelectArgs &a, const float *scores, int32_t *sel, int pages,
+                                         uint32_t (*red)[SEL_THREADS / 32], uint32_t (*red2)[SEL_THREADS / 32])
+{
+    int turn = 0;
+    const int each = (pages + SEL_THREADS - 1) / SEL_THREADS;   // at most K, unless K = 0
+    const int first = min((int)threadIdx.x * each, pages), mine = min(each, pages - first);
+    uint32_t key[K > 0 ? K : 1];
+#pragma unroll
+    for (int i = 0; i < K; ++i) key[i] = i < mine ? page_key(a, scores, first + i, pages) : 0u;
+    // number of keys at or above a bound > 0 (no page has key 0: -inf's is 0x007fffff)
+    auto at_least = [&](uint32_t bound) {
+        uint32_t n = 0;
+        if (K > 0) {
+#pragma unroll
+            for (int i = 0; i < K; ++i) n += key[i] >= bound;
+        } else {
+            for (int i = 0; i < mine; ++i) n += page_key(a, scores, first + i, pages) >= bound;
+        }
+        return n;
+    };
+    const uint32_t want = (uint32_t)a.n_sel;
+    uint32_t thr = 0;
+    if (K > 0) {   // fewer than 2^16 pages: three counts in two sums of halves
+        for (int bit = 30; bit >= 0; bit -= 2) {
+            uint32_t s12 = at_least(thr | 1u << bit) | at_least(thr | 2u << bit) << 16, s3 = at_least(thr | 3u << bit);
+            block_sum2(s12, s3, red, red2, turn);
+            if (s3 >= want) thr |= 3u << bit;
+            else if (s12 >> 16 >= want) thr |= 2u << bit;
+            else if ((s12 & 0xffffu) >= want) thr |= 1u << bit;
+        }
+    } else {
+        for (int bit = 31; bit >= 0; --bit)
+            if (block_sum(at_least(thr | 1u << bit), red, turn) >= want) thr |= 1u << bit;
+    }
+    const uint32_t gt = thr == 0xffffffffu ? 0u : at_least(thr + 1), eq = at_least(thr) - gt;
+    const uint32_t ties = want - block_sum(gt, red, turn);   // pages equal to the threshold that are taken
+    uint32_t seen = block_before(eq, red, turn);             // ... that come before this thread's
+    uint32_t at = block_before(gt, red, turn) + min(seen, ties);
+    auto put = [&](uint32_t k, int page) {
+        if (k > thr) sel[at++] = page;
+        else if (k == thr && seen++ < ties) sel[at++] = page;
+    };
+    if (K > 0) {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (i < mine) put(key[i], first + i);
+    } else {
+        for (int i = 0; i < mine; ++i) put(page_key(a, scores, first + i, pages), first + i);
+    }
+}
+
+// One block per (sequence, token, kv head).
 __global__ void __launch_bounds__(SEL_THREADS) kv4_top_kernel(Kv4SelectArgs a)
 {
-    __shared__ int red[SEL_THREADS / 32];
-    const int64_t item = blockIdx.x;
-    const int64_t bj = item / a.pool.Hkv;
-    const int j = (int)(bj % a.rows.n), b = (int)(bj / a.rows.n);
+    __shared__ uint32_t red[2][SEL_THREADS / 32], red2[2][SEL_THREADS / 32];
+    kv4_begin();
+    const unsigned item = blockIdx.x, bj = item / (unsigned)a.pool.Hkv;
+    const int b = (int)(bj / (unsigned)a.rows.n), j = (int)(bj - (unsigned)b * a.rows.n);
     const int len = kv4_len(a.pool, b);
     const int lim = kv4_limit(a.rows, b, j, len);
     const int ps = a.pool.page_shift;
     const int pages = (int)(((int64_t)lim + (1 << ps) - 1) >> ps);
-    const float *scores = a.scores + item * a.pool.max_pages;
-    int32_t *sel = a.sel + item * a.n_sel;
+    const float *scores = a.scores + (int64_t)item * a.pool.max_pages;
+    int32_t *sel = a.sel + (int64_t)item * a.n_sel;
     if (pages <= a.n_sel) {
         for (int i = threadIdx.x; i < a.n_sel; i += SEL_THREADS) sel[i] = i < pages ? i : -1;
         return;
     }
-    uint32_t thr = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t cand = thr | 1u << bit;
-        int n = 0;
-        for (int i = threadIdx.x; i < pages; i += SEL_THREADS) n += page_key(a, scores, i, pages) >= cand;
-        if (block_sum(n, red) >= a.n_sel) thr = cand;
-    }
-    int above = 0;
-    for (int i = threadIdx.x; i < pages; i += SEL_THREADS) above += page_key(a, scores, i, pages) > thr;
-    const int ties = a.n_sel - block_sum(above, red);   // pages equal to the threshold that are taken
-    int done = 0, seen = 0;                             // pages written, ties met, before this stretch
-    for (int i0 = 0; i0 < pages; i0 += SEL_THREADS) {
-        const int i = i0 + threadIdx.x;
-        const uint32_t k = i < pages ? page_key(a, scores, i, pages) : 0u;
-        const bool eq = i < pages && k == thr, gt = i < pages && k > thr;
-        // exclusive counts over the block
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const unsigned be = __ballot_sync(0xffffffffu, eq), bg = __ballot_sync(0xffffffffu, gt);
-        __syncthreads();
-        if (lane == 0) red[warp] = __popc(be) << 16 | __popc(bg);
-        __syncthreads();
-        int pe = 0, pg = 0, te = 0, tg = 0;
-        for (int w = 0; w < SEL_THREADS / 32; ++w) {
-            const int e = red[w] >> 16, q = red[w] & 0xffff;
-            if (w < warp) pe += e, pg += q;
-            te += e, tg += q;
-        }
-        const unsigned below = (1u << lane) - 1u;
-        const int my_e = seen + pe + __popc(be & below);   // ties before this page
-        const int my_g = pg + __popc(bg & below);
-        const int taken_e = min(my_e, ties) - min(seen, ties);
-        if (gt || (eq && my_e < ties)) sel[done + my_g + taken_e] = i;
-        done += tg + min(seen + te, ties) - min(seen, ties);
-        seen += te;
-    }
+    // with two keys a thread a step is its barrier, with 16 its comparisons
+    if (pages <= 2 * SEL_THREADS) take_top<2>(a, scores, sel, pages, red, red2);
+    else if (pages <= 4 * SEL_THREADS) take_top<4>(a, scores, sel, pages, red, red2);
+    else if (pages <= 16 * SEL_THREADS) take_top<16>(a, scores, sel, pages, red, red2);
+    else take_top<0>(a, scores, sel, pages, red, red2);
 }
 
 }  // namespace
@@ -179,12 +252,14 @@ int launch_kv4_select(const Kv4SelectArgs &a, int D, cudaStream_t st)
     const int tiles = (a.pool.max_pages + 15) / 16;
     const int64_t warps = items * tiles;
     const int64_t grid = (warps + 3) / 4;
-    if (items > 0x7fffffffLL || grid > 0x7fffffffLL) return CP_EUNSUPPORTED;
-    if (D == 64) kv4_score_kernel<64><<<(unsigned)grid, 128, 0, st>>>(a, tiles, warps);
-    else kv4_score_kernel<128><<<(unsigned)grid, 128, 0, st>>>(a, tiles, warps);
-    if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
-    kv4_top_kernel<<<(unsigned)items, SEL_THREADS, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ECUDA;
+    if (items > 0x7fffffffLL || warps > 0x7fffffffLL) return CP_EUNSUPPORTED;
+    if (grid > 0) {
+        const cudaError_t rc =
+            D == 64 ? kv4_launch(kv4_score_kernel<64>, (unsigned)grid, 128, 0, st, a, tiles, (unsigned)warps)
+                    : kv4_launch(kv4_score_kernel<128>, (unsigned)grid, 128, 0, st, a, tiles, (unsigned)warps);
+        if (rc != cudaSuccess) return CP_ECUDA;
+    }
+    return kv4_launch(kv4_top_kernel, (unsigned)items, SEL_THREADS, 0, st, a) == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 
 }  // namespace cp
