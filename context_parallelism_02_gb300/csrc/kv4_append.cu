@@ -178,10 +178,20 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
+// One code by division (out of line: eight divisions are a lot of code).
+__device__ __noinline__ float code_by_division(float y, float s)
+{
+    return s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(y, s)), 0.f), 15.f) : 0.f;
+}
+
 // Codes (as whole floats), scale and minimum of a lane's 8 elements; the group is
-// 4 lanes.  s is the range times fp32(1 / 15), a = fp32(1 / s) fp32(1 / 15), and a
-// code 15 clamp((y - m) a, 0, 1) rounded: no division but one reciprocal a group, the
-// clamp is the product's own, and the rounding that of adding 1.5 2^23.
+// 4 lanes.  s is the range times fp32(1 / 15).  rint((y - m) / s) is taken from
+// 15 clamp((y - m) a, 0, 1) with a = fp32(1 / s) fp32(1 / 15): one reciprocal a group,
+// the clamp is the product's own, the rounding that of adding 1.5 2^23.  The factors
+// are off by 2.5 units in the last place together and the quotient by a half:
+// 15 (2.5 2^-23 + 2^-24) < 6e-6.  Where a lane's product comes within 1e-5 of a half the
+// warp divides: bf16 values sit on exact halves of s often enough (4 in 10^4 elements)
+// that the nearest-even rule of the quotient has to hold for them.
 __device__ __forceinline__ void quantise8(const float (&x)[8], float (&code)[8], __half &s, __half &m)
 {
     float lo = min3(min3(x[0], x[1], x[2]), min3(x[3], x[4], x[5]), min3(x[6], x[7], x[7]));
@@ -204,12 +214,21 @@ __device__ __forceinline__ void quantise8(const float (&x)[8], float (&code)[8],
     const float sf = __half2float(s), mf = __half2float(m);
     const float a = sf > 0.f && !bad ? __fmul_rn(__frcp_rn(sf), FIFTEENTH) : 0.f;   // 0: every code is 0
     if (bad) s = __ushort_as_half(0), m = __ushort_as_half(0x7fff);
-    constexpr float ROUND = 12582912.f;   // 1.5 2^23: adding it rounds to a whole number
+    constexpr float ROUND = 12582912.f;
+    float off = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float u;
         asm("mul.rn.sat.f32 %0, %1, %2;" : "=f"(u) : "f"(__fsub_rn(x[i], mf)), "f"(a));
         code[i] = __fsub_rn(__fmaf_rn(u, 15.f, ROUND), ROUND);
+        off = fmaxf(off, fabsf(__fmaf_rn(u, 15.f, -code[i])));
+    }
+    if (__any_sync(0xffffffffu, off > 0.49999f)) {
+        if (off > 0.49999f) {   // a is 0 where the group is constant or not finite: not here
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                code[i] = code_by_division(__fsub_rn(fminf(fmaxf(x[i], -KV4_MAX), KV4_MAX), mf), sf);
+        }
     }
 }
 

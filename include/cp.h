@@ -399,11 +399,9 @@ int ring_attn_bwd_noalloc(const void *q, const void *k, const void *v, const voi
  *   summary [n_pages][Hkv][2][D] bf16 or NULL: per page, the smallest and largest
  *   value of every element of its rotated keys; updated for kv4_select (a page
  *   whose first slot is written starts afresh).
- * Quantisation of a group of 32: s = fp16((max - min) / 15), m = fp16(min),
- * code = rint((y - m) / s) held to 0..15, in fp32 with products in place of the
- * divisions: s from (max - min) fp32(1/15), the code from 15 clamp((y - m) a, 0, 1)
- * with a = fp32(1/s) fp32(1/15).  Values beyond +-65408 count as that, and a group
- * with a value that is not finite is held as NaN.
+ * Quantisation of a group of 32: s = fp16((max - min) fp32(1/15)), m = fp16(min),
+ * code = rint((y - m) / s) held to 0..15, in fp32, halves to even; values beyond
+ * +-65408 count as that, and a group with a value that is not finite is held as NaN.
  * Within one call no two sequences may write the same page.
  * Errors: CP_EINVAL (null pointer, misalignment, sizes, Hq % Hkv), CP_EUNSUPPORTED
  * (D, dtype, page), CP_ECUDA.

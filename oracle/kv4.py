@@ -44,9 +44,8 @@ def quantise(x):
     s = ((hi - lo) * F32(1 / 15)).astype(F16)
     m = lo.astype(F16)
     sf, mf = s.astype(F32), m.astype(F32)
-    a = np.where(sf > 0, F32(1) / np.where(sf > 0, sf, F32(1)) * F32(1 / 15), F32(0))
-    u = np.clip((y - mf) * a, F32(0), F32(1))
-    code = np.rint(15.0 * u.astype(np.float64)).astype(np.uint8)
+    code = np.rint((y - mf) / np.where(sf > 0, sf, F32(1)))
+    code = np.clip(np.where(sf > 0, code, F32(0)), 0, 15).astype(np.uint8)
     s, m = np.where(bad, F16(0), s), np.where(bad, F16(np.nan), m)
     code = np.where(bad, np.uint8(0), code)
     shape = x.shape

@@ -149,6 +149,25 @@ def test_append_values_that_are_not_finite_or_too_large(cuda_dev):
     assert s[0, 3] == -math.inf and s[1, 3] == math.inf and s[0, 40] == -math.inf and s[1, 40] == math.inf
 
 
+def test_append_codes_on_exact_halves(cuda_dev):
+    """Values half way between two codes go to the even one, as the quotient does: bf16 values meet such halves."""
+    rng = np.random.default_rng(18)
+    D, page = 128, 16
+    v = rng.integers(0, 31, (1, 64, 2, D)).astype(np.float32) * 0.5     # s = 1 where 0 and 15 are in the group
+    v[..., ::32], v[..., 1::32] = 0.0, 15.0
+    v *= np.exp2(rng.integers(-6, 7, (1, 64, 2, 1))).astype(np.float32)
+    k = o.bf16(rng.standard_normal((1, 64, 2, D)) * 3)
+    pages, P = table(rng, 1, 4)
+    cache = np.zeros((P, 2, page, D // 4 * 5), np.uint8)
+    gc = dev(cache)
+    api.kv4_append(dev(k, torch.bfloat16), dev(v, torch.bfloat16), gc, dev(pages), dev(np.array([0], np.int32)))
+    ok()
+    for t in range(64):
+        for h in range(2):
+            o.write(cache, pages, 0, h, t, k[0, t, h], v[0, t, h])
+    np.testing.assert_array_equal(gc.cpu().numpy(), cache)
+
+
 def test_attn_of_the_largest_values_is_finite(cuda_dev):
     """Values of both signs at the end of the range in one group: s code + m stays below fp16's overflow (65520)."""
     D = 64
