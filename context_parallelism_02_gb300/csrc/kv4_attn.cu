@@ -485,7 +485,7 @@ constexpr int NB = 2;      // blocks of a stage, taken together
 
 // Stages of a warp's ring.
 template <int D>
-__host__ __device__ constexpr int stages() { return D == 128 ? 3 : 5; }
+__host__ __device__ constexpr int stages() { return 2; }
 
 constexpr int PAD = 8;
 
@@ -545,12 +545,19 @@ __device__ __forceinline__ void count_blocks(const Kv4AttnArgs &a, int upto, int
     }
 }
 
-// Length of a warp's stretch.
-__device__ __forceinline__ int64_t stretch(int64_t all, int warps, int least)
-{
-    const int64_t per = (all + warps - 1) / warps;
-    return per > least ? per : least;
-}
+// The line of `all` blocks in equal stretches: how many there are (a warp takes at
+// least `least` blocks), where stretch c begins, and which one holds position f.
+struct Cuts {
+    int64_t all;
+    int n;
+    __device__ __forceinline__ Cuts(int64_t all_, int warps, int least) : all(all_)
+    {
+        const int64_t most = all / least;
+        n = most < 1 ? 1 : most < warps ? (int)most : warps;
+    }
+    __device__ __forceinline__ int64_t begin(int c) const { return all * c / n; }
+    __device__ __forceinline__ int at(int64_t f) const { return (int)(((f + 1) * n - 1) / all); }
+};
 
 // One output row's four elements.
 __device__ __forceinline__ void put_out(const Kv4AttnArgs &a, int64_t at, float4 o)
@@ -603,10 +610,11 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
 #pragma unroll
     for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     all *= sh.per_batch;
-    const int64_t per = stretch(all, warps, least);
-    const int64_t self = blockIdx.x * WARPS + warp, f0 = per * self;
+    const Cuts cuts(all, warps, least);
+    const int self = blockIdx.x * WARPS + warp;
     __syncthreads();                          // sm.abort is set
-    if (f0 >= all) return;
+    if (self >= cuts.n) return;
+    const int64_t f0 = cuts.begin(self);
     Walk at;
     int64_t rest = 0;
     for (int b0 = 0;; b0 += 32) {
@@ -633,7 +641,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     }
     at.i = (int)(rest / (at.nb + PAD));
     at.t0 = (int)(rest % (at.nb + PAD));
-    at.left = min(per, all - f0);
+    at.left = cuts.begin(self + 1) - f0;
     at.cut();
     RawRows<D, NT> raw;
     bool first = true;
@@ -741,7 +749,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
             __syncwarp();                    // ... and the slots are written before the next round reads them
         }
         const bool whole = at.t0 == 0 && at.t1 == at.nb;
-        float *part = static_cast<float *>(a.ws) + (2 * self + (at.t0 == 0 ? 1 : 0)) * Part<D, NT>::FLOATS;
+        float *part = static_cast<float *>(a.ws) + (2 * (int64_t)self + (at.t0 == 0 ? 1 : 0)) * Part<D, NT>::FLOATS;
 #pragma unroll
         for (int u = 0; u < NT; ++u)
 #pragma unroll
@@ -798,14 +806,14 @@ __global__ void __launch_bounds__(JW * 32) kv4_join_kernel(Kv4AttnArgs a, Shape 
     int64_t all, before;
     count_blocks(a, b, all, before);
     all *= sh.per_batch;
-    const int64_t per = stretch(all, warps, least);
+    const Cuts cuts(all, warps, least);
     const int nb = item_blocks(a, b);
     // the item of this row: token, row tile, kv head
     const int tile = rr_all / (NT * 8), row = rr_all % (NT * 8);
     const int h = x % a.pool.Hkv, j0 = x / a.pool.Hkv;
     const int i = (j0 * sh.tiles + tile) * a.pool.Hkv + h;
     const int64_t f = before * sh.per_batch + (int64_t)i * (nb + PAD);
-    const int c0 = (int)(f / per), c1 = (int)((f + nb - 1) / per);
+    const int c0 = cuts.at(f), c1 = cuts.at(f + nb - 1);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c0 == c1) return;
     const float *ws = static_cast<const float *>(a.ws);
@@ -822,7 +830,7 @@ __global__ void __launch_bounds__(JW * 32) kv4_join_kernel(Kv4AttnArgs a, Shape 
 #pragma unroll
             for (int e = 0; e < E; ++e) v[u][e] = 0.f;
             if (c + u > c1) continue;
-            const float *part = ws + (2 * (int64_t)(c + u) + (f >= (c + u) * per ? 1 : 0)) * Part<D, NT>::FLOATS;
+            const float *part = ws + (2 * (int64_t)(c + u) + (c + u == c0 ? 1 : 0)) * Part<D, NT>::FLOATS;
             pm[u] = part[row];
             pl[u] = part[8 * NT + row];
             if (E == 4) {
