@@ -267,7 +267,7 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N])
     }
 }
 
-// Scores of one block, in the row's units: x[t][0..1] token g, x[t][2..3] token g + 8.
+// Scores of one block, in units of the row's to_log2: x[t][0..1] token g, x[t][2..3] token g + 8.
 template <int D, int NT>
 __device__ __forceinline__ void block_scores(const uint8_t *blk, const Rows<D, NT> &r, float (&x)[NT][4])
 {
@@ -311,7 +311,7 @@ __device__ __forceinline__ void block_scores(const uint8_t *blk, const Rows<D, N
 
 // Raises the references m where a score is more than 2^8 above them.
 template <int D, int NT, int NB>
-__device__ __forceinline__ void raise_max(const float (&x)[NB][NT][4], const Rows<D, NT> &r, State<D, NT> &s)
+__device__ __forceinline__ void raise_max(const float (&x)[NB][NT][4], State<D, NT> &s)
 {
     bool high = false;
     float top[NT][2];
@@ -322,8 +322,8 @@ __device__ __forceinline__ void raise_max(const float (&x)[NB][NT][4], const Row
             float v = fmaxf(x[0][t][e], x[0][t][e + 2]);
 #pragma unroll
             for (int i = 1; i < NB; ++i) v = fmaxf(v, fmaxf(x[i][t][e], x[i][t][e + 2]));
-            top[t][e] = v * r.to_log2[t][e];
-            high |= top[t][e] > s.m[t][e] + 8.f;
+            top[t][e] = v;
+            high |= v > s.m[t][e] + 8.f;
         }
     if (!__any_sync(0xffffffffu, high)) return;
 #pragma unroll
@@ -435,6 +435,12 @@ __device__ __forceinline__ void blocks_step(const uint8_t *blk, const int (&slot
     for (int i = 0; i < NB; ++i) {
         block_scores<D, NT>(blk + i * Kv4<D>::BYTES, r, x[i]);
         cut |= slot[i] > r.min_limit - KV4_BLOCK;
+        // rounded here and not fused with the subtraction of m, which is one of these
+        // products: a difference is then at most 8 however large the scores are
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i][t][e] = __fmul_rn(x[i][t][e], r.to_log2[t][e & 1]);
     }
     if (cut) {
 #pragma unroll
@@ -445,7 +451,7 @@ __device__ __forceinline__ void blocks_step(const uint8_t *blk, const int (&slot
                 for (int e = 0; e < 4; ++e)
                     if (slot[i] + g + (e >> 1) * 8 >= r.limit[t][e & 1]) x[i][t][e] = -INFINITY;
     }
-    raise_max<D, NT, NB>(x, r, s);
+    raise_max<D, NT, NB>(x, s);
     uint32_t p[NB][NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -457,7 +463,7 @@ __device__ __forceinline__ void blocks_step(const uint8_t *blk, const int (&slot
             float w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                w[e] = ex2(fmaf(x[i][t][e], r.to_log2[t][e & 1], base[e & 1]));
+                w[e] = ex2(__fadd_rn(x[i][t][e], base[e & 1]));
                 s.l[t][e & 1] += w[e];
             }
             p[i][t][0] = movmatrix(h2(__floats2half2_rn(w[0], w[1])));

@@ -633,3 +633,240 @@ def test_attn_value_that_is_not_a_number_is_not_lost_between_blocks(cuda_dev):
         ok()
         assert out.isnan().all() and lse.isnan().all()
 
+
+
+def reference(q, kr, vr, limits, scale):
+    """q [B, n, Hq, D], kr and vr [B, L, Hkv, D] fp32, limits [B, n]: out, lse and sum p |v| in 64 bits."""
+    B, n, Hq, D = q.shape
+    L, Hkv = kr.shape[1:3]
+    k, v = (t.double().repeat_interleave(Hq // Hkv, 2) for t in (kr, vr))
+    s = torch.einsum("bnhd,blhd->bhnl", q.double(), k) * scale
+    s = s.masked_fill(torch.arange(L, device=q.device) >= limits.to(q.device)[:, None, :, None], -math.inf)
+    z = s.logsumexp(-1)
+    p = torch.exp(s - z.masked_fill(z == -math.inf, 0.0)[..., None])
+    return torch.einsum("bhnl,blhd->bnhd", p, v), z, torch.einsum("bhnl,blhd->bnhd", p, v.abs())
+
+
+def check_reference(out, lse, q, kr, vr, limits, scale):
+    """The bounds of check_attn, for whole batches."""
+    want, z, a = reference(q, kr, vr, limits, scale)
+    L = kr.shape[1]
+    tol = (2.0 ** -10 + (L / 16 + 32) * 2.0 ** -23) * a + L * 2.0 ** -25 * vr.abs().max().double() + 2.0 ** -25
+    if out.dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * (want.abs() + tol)
+    assert ((out.double() - want).abs() <= tol).all()
+    empty = z == -math.inf
+    assert torch.equal(lse == -math.inf, empty)
+    size = scale * q.double().abs().sum(-1).amax() * (kr.abs().amax() + 8).double()
+    assert ((lse.double() - z).masked_fill(empty, 0.0).abs()
+            <= 2.0 ** -19 * size + 2.0 ** -20 * (z.masked_fill(empty, 0.0).abs() + 1)).all()
+
+
+@pytest.mark.parametrize("B,n,Hq,Hkv,D,page,L", [(70, 1, 4, 2, 64, 16, 300), (300, 1, 2, 1, 128, 32, 90),
+                                                 (1, 200, 8, 2, 64, 64, 700), (3, 33, 10, 5, 128, 16, 150),
+                                                 (2, 1, 128, 1, 128, 64, 900)])
+def test_attn_many_sequences_many_rows(cuda_dev, B, n, Hq, Hkv, D, page, L):
+    rng = np.random.default_rng(B + n)
+    lens = rng.integers(0, L + 1, B).astype(np.int32)
+    lens[-1] = L
+    if B > 40:
+        lens[35:40] = 0
+    M = -(-L // page)
+    pages, P = table(rng, B, M)
+    cache = torch.full((P, Hkv, page, D // 4 * 5), 255, dtype=torch.uint8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k, v = (torch.randn(B, L, Hkv, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    api.kv4_append(k, v, cache, dev(pages), dev(np.zeros(B, np.int32)), n_new=dev(lens))
+    q = torch.randn(B, n, Hq, D, generator=g, device="cuda").bfloat16()
+    out, lse = api.kv4_attn(q, cache, dev(pages), dev(lens))
+    kr, vr = api.kv4_gather(cache, dev(pages), dev(lens), L, dtype=torch.float32)
+    ok()
+    lim = torch.from_numpy(np.maximum(lens[:, None] - (n - 1) + np.arange(n), 0))
+    check_reference(out, lse, q, kr, vr, lim, 1 / math.sqrt(D))
+
+
+def test_attn_sizes_of_scores_and_queries(cuda_dev):
+    """Queries from 2^-100 to 2^40 in one tile, rows of zeros, keys of 2^-10 to 2^8: each row scaled by itself."""
+    rng = np.random.default_rng(19)
+    D, L = 128, 200
+    pages, P = table(rng, 1, 4)
+    cache = torch.full((P, 1, 64, 160), 255, dtype=torch.uint8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(1, L, 1, D, generator=g, device="cuda") for _ in range(2))
+    k *= torch.exp2(torch.randint(-10, 9, (1, L, 1, 1), generator=g, device="cuda").float())
+    lens = dev(np.array([L], np.int32))
+    api.kv4_append(k, v, cache, dev(pages), lens - L)
+    q = torch.randn(1, 1, 8, D, generator=g, device="cuda")
+    for i, e in enumerate((-100, -30, -8, 0, 3, 20, 40)):
+        q[0, 0, i] *= 2.0 ** e
+    q[0, 0, 7] = 0
+    q = q.bfloat16()
+    out, lse = api.kv4_attn(q, cache, dev(pages), lens)
+    kr, vr = api.kv4_gather(cache, dev(pages), lens, L, dtype=torch.float32)
+    ok()
+    for i in range(8):   # by row: the bound of lse is relative to the row's own scores
+        check_reference(out[:, :, i:i + 1], lse[:, i:i + 1], q[:, :, i:i + 1], kr, vr, torch.tensor([[L]]), 1 / math.sqrt(D))
+
+
+def test_append_rotates_q_in_place(cuda_dev):
+    rng = np.random.default_rng(20)
+    cos, sin = (dev(x) for x in rope(64, 128))
+    pages, lens = dev(np.array([[0]], np.int32)), dev(np.array([3], np.int32))
+    q, k = (dev(rows(rng, torch.bfloat16, 1, 20, h, 128), torch.bfloat16) for h in (12, 1))
+    cache = api.kv4_cache(1, 1, 64, 128)
+    want = api.kv4_append(k, k, cache, pages, lens, cos, sin, q=q)
+    got = api.kv4_append(k, k, cache, pages, lens, cos, sin, q=q, q_out=q)
+    ok()
+    assert got is q and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("count,n_sel", [(1030, 100), (2100, 64), (9000, 333), (70000, 50)])
+def test_select_over_many_pages(cuda_dev, count, n_sel):
+    """Every number of keys per thread, ties among them; small integers, so that every bound is exact."""
+    rng = np.random.default_rng(count)
+    box = np.sort(rng.integers(-40, 41, (count, 1, 2, 64)).astype(np.float32), 2)
+    box[rng.integers(0, count, count // 3)] = box[7]
+    pages = rng.permutation(count).astype(np.int32)[None]
+    q = rng.integers(-8, 9, (1, 1, 3, 64)).astype(np.float32)
+    sel = api.kv4_select(dev(q, torch.bfloat16), dev(box, torch.bfloat16), dev(pages),
+                         dev(np.array([count * 16 - 3], np.int32)), 16, n_sel)
+    ok()
+    t = box[pages[0], 0]
+    np.testing.assert_array_equal(sel.cpu().numpy()[0, 0, 0], o.select(q[0, 0], t[:, 0], t[:, 1], n_sel, 1, 1))
+
+
+def test_select_reports_bad_pages_and_lengths(cuda_dev):
+    rng = np.random.default_rng(21)
+    box = dev(np.sort(rng.standard_normal((20, 1, 2, 64)), 2).astype(np.float32), torch.bfloat16)
+    q = dev(rows(rng, torch.bfloat16, 1, 1, 2, 64), torch.bfloat16)
+    pages = np.arange(20, dtype=np.int32)[None].copy()
+    pages[0, 5] = 20
+    sel = api.kv4_select(q, box, dev(pages), dev(np.array([320], np.int32)), 16, 4)
+    torch.cuda.synchronize()
+    assert api.cp_get_error() == _lib.CP_ECACHE
+    assert ((sel >= 0) & (sel < 20)).all()
+    pages[0, 5] = 5
+    for length in (-1, 2 ** 31 - 1):
+        sel = api.kv4_select(q, box, dev(pages), dev(np.array([length], np.int32)), 16, 4)
+        torch.cuda.synchronize()
+        assert api.cp_get_error() == _lib.CP_ECACHE
+        assert (sel < 20).all()
+
+
+def test_calls_on_two_streams_and_two_graphs_at_once(cuda_dev):
+    """Calls that overlap have workspaces of their own (each call takes one, a captured one its graph's)."""
+    rng = np.random.default_rng(22)
+    work = []
+    for i in range(2):
+        cache, summ, pages = fill(rng, 3, 3000, 2, 128, 64)
+        q = dev(rows(rng, torch.bfloat16, 3, 1, 8, 128), torch.bfloat16)
+        lens = dev(np.array([3000, 17, 1234], np.int32))
+
+        def step(q=q, cache=cache, summ=summ, pages=dev(pages), lens=lens):
+            sel = api.kv4_select(q, summ, pages, lens, 64, 5)
+            return [sel, *api.kv4_attn(q, cache, pages, lens), *api.kv4_attn(q, cache, pages, lens, sel=sel)]
+        work.append((step, [t.clone() for t in step()]))
+    ok()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs = []
+    for (step, _), s in zip(work, streams):
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            outs = step()
+        graphs.append((graph, outs))
+    for _ in range(20):
+        got = []
+        for (step, _), s in zip(work, streams):
+            with torch.cuda.stream(s):
+                got.append(step())
+        torch.cuda.synchronize()
+        for (_, want), g in zip(work, got):
+            assert all(torch.equal(x, y) for x, y in zip(want, g))
+        for (graph, outs), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (_, want), (_, outs) in zip(work, graphs):
+            assert all(torch.equal(x, y) for x, y in zip(want, outs))
+    ok()
+
+
+def test_stream_argument(cuda_dev):
+    """Every call on a stream that is not the current one."""
+    rng = np.random.default_rng(23)
+    cache, summ, pages = fill(rng, 1, 500, 1, 64, 32)
+    q = dev(rows(rng, torch.bfloat16, 1, 1, 4, 64), torch.bfloat16)
+    lens, gp = dev(np.array([500], np.int32)), dev(pages)
+    k = dev(rows(rng, torch.bfloat16, 1, 1, 1, 64), torch.bfloat16)
+
+    def step(cache, summ, stream):
+        qr = api.kv4_append(k, k, cache, gp, lens, q=q, summary=summ, stream=stream)
+        sel = api.kv4_select(qr, summ, gp, lens, 32, 3, stream=stream)
+        return [sel, *api.kv4_attn(qr, cache, gp, lens, sel=sel, stream=stream),
+                *api.kv4_gather(cache, gp, lens, 501, stream=stream)]
+    want = step(cache.clone(), summ.clone(), None)
+    ok()
+    side = torch.cuda.Stream()
+    c, s = cache.clone(), summ.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    got = step(c, s, side)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+def test_binding_refusals_on_the_gpu(cuda_dev):
+    D = 64
+    cache, summ = api.kv4_cache(4, 2, 16, D, summary=True)
+    pages, lens = dev(np.array([[0, 1]], np.int32)), dev(np.array([3], np.int32))
+    k = torch.zeros(1, 2, 2, D, device="cuda")
+    q = torch.zeros(1, 1, 4, D, dtype=torch.bfloat16, device="cuda")
+    bad = [
+        lambda: api.kv4_append(k, k, cache, pages, lens.long()),
+        lambda: api.kv4_append(k, k, cache, pages.cpu(), lens),
+        lambda: api.kv4_append(k, k, cache, pages[0], lens),
+        lambda: api.kv4_append(k[:, :, :1], k[:, :, :1], cache, pages, lens),
+        lambda: api.kv4_append(k, k.bfloat16(), cache, pages, lens),
+        lambda: api.kv4_append(k.transpose(2, 3), k.transpose(2, 3), cache, pages, lens),
+        lambda: api.kv4_append(k.transpose(2, 3).contiguous().transpose(2, 3), k, cache, pages, lens),
+        lambda: api.kv4_append(k, k, cache, pages, lens, cos=torch.zeros(5, 32, device="cuda")),
+        lambda: api.kv4_append(k, k, cache, pages, lens, n_new=dev(np.zeros(2, np.int32))),
+        lambda: api.kv4_append(k, k, cache, pages, lens, positions=dev(np.zeros((1, 3), np.int32))),
+        lambda: api.kv4_append(k, k, cache, pages, lens, q_out=k),
+        lambda: api.kv4_append(k, k, cache, pages, lens, summary=summ[:2]),
+        lambda: api.kv4_gather(cache, pages, lens, 4, start=lens.float()),
+        lambda: api.kv4_gather(cache, pages, lens, 4, k=k),
+        lambda: api.kv4_attn(q.float(), cache, pages, lens),
+        lambda: api.kv4_attn(q[..., :32], cache, pages, lens),
+        lambda: api.kv4_attn(q, cache[:, :, ::2], pages, lens),
+        lambda: api.kv4_attn(q, cache, pages, lens, vis=dev(np.zeros((1, 2), np.int32))),
+        lambda: api.kv4_attn(q, cache, pages, lens, sel=dev(np.zeros((1, 1, 1, 2), np.int32))),
+        lambda: api.kv4_attn(q, cache, pages, lens, out=q.half()),
+        lambda: api.kv4_attn(q, cache, pages, lens, lse=torch.zeros(1, 1, 4, device="cuda")),
+        lambda: api.kv4_attn(q, cache, pages, lens, workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
+        lambda: api.kv4_attn(q[:, :, :3].contiguous(), cache, pages, lens),
+        lambda: api.kv4_select(q, summ, pages, lens, 16, 0),
+        lambda: api.kv4_select(q, summ, pages, lens, 16, 2, keep_first=2, keep_last=1),
+        lambda: api.kv4_select(q, summ, pages, lens, 24, 2),
+        lambda: api.kv4_select(q, summ, pages, lens, 16, 2, sel=dev(np.zeros((1, 1, 2, 3), np.int32))),
+    ]
+    before = cache.clone()
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, _lib.CpError)):
+            call()
+            raise AssertionError(i)
+    ok()
+    assert torch.equal(before, cache)
+    # rows that do not start on 16 bytes
+    x = torch.zeros(1, 2, 2 * D + 2, device="cuda", dtype=torch.bfloat16)[..., :2 * D].unflatten(-1, (2, D))
+    with pytest.raises(_lib.CpError):
+        api.kv4_append(x, x, cache, pages, lens)
+    # nothing to do
+    assert api.kv4_append(k[:, :0], k[:, :0], cache, pages, lens) is None
+    out, lse = api.kv4_attn(q[:0], cache, pages[:0], lens[:0])
+    assert out.shape == (0, 1, 4, D) and lse.shape == (0, 4, 1)
+    gk, _ = api.kv4_gather(cache, pages, lens, 0)
+    assert gk.shape == (1, 0, 2, D)
+    out, lse = api.kv4_attn(q, cache, pages[:, :0].contiguous(), lens * 0)      # no pages at all
+    ok()
+    assert (out == 0).all() and lse.isinf().all()
