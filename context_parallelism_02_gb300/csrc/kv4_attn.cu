@@ -529,6 +529,7 @@ template <int D>
 struct Smem {
     uint8_t ring[WARPS][stages<D>()][NB][Kv4<D>::BYTES];
     uint64_t full[WARPS][stages<D>()];
+    uint64_t hold;                   // completed by nobody: what the failure path is tested with
     int slot[WARPS][stages<D>()][NB];   // first slot of the block, or NO_SLOT
     Walk ahead[WARPS];               // the piece that a warp's copies are issued for
     int abort, never;
@@ -596,7 +597,10 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     constexpr int NS = stages<D>(), NG = Kv4<D>::NG;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     if (lane < NS) mbar_init(smem_u32(&sm.full[warp][lane]), NB);
-    if (threadIdx.x == 0) sm.abort = sm.never = 0;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&sm.hold), 1);
+        sm.abort = sm.never = 0;
+    }
     fence_mbar_init();
     kv4_begin();
     {   // what the chain of loads below will need, on its way to L2
@@ -725,6 +729,8 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     };
     for (int s = 0; s < NS; ++s) issue();
     __syncwarp();
+    // a bound this short is the test hook's; the waits below can be met before it
+    if (a.limit_ns < SHORT_WAIT_NS) dead = !waitw(smem_u32(&sm.hold), 0, wc);
     for (; at.valid(); at.next(a, sh.per_batch)) {
         if (at.t0 >= at.t1) {                // the padding of an item that another warp has done
             first = false;

@@ -870,3 +870,23 @@ def test_binding_refusals_on_the_gpu(cuda_dev):
     out, lse = api.kv4_attn(q, cache, pages[:, :0].contiguous(), lens * 0)      # no pages at all
     ok()
     assert (out == 0).all() and lse.isinf().all()
+
+
+def test_attn_bounded_wait(cuda_dev):
+    """A wait that runs out ends the kernel with CP_ETIMEOUT, its copies landed; the next call is whole again."""
+    rng = np.random.default_rng(17)
+    cache, _, pages = fill(rng, 2, 9000, 2, 128, 64)
+    q = dev(rows(rng, torch.bfloat16, 2, 1, 8, 128), torch.bfloat16)
+    lens = dev(np.array([9000, 9000], np.int32))
+    want = api.kv4_attn(q, cache, dev(pages), lens)
+    ok()
+    try:
+        api.cp_debug_set_wait_limit(1)
+        api.kv4_attn(q, cache, dev(pages), lens)
+        torch.cuda.synchronize()
+        assert api.cp_get_error() == _lib.CP_ETIMEOUT
+    finally:
+        api.cp_debug_set_wait_limit(0)
+    got = api.kv4_attn(q, cache, dev(pages), lens)
+    ok()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
