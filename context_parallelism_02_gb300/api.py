@@ -339,38 +339,38 @@ def ulysses_head_to_seq(y: torch.Tensor, N: int, layout: int, x=None, stream=Non
 
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
 
 
-def _kv4_check(dev, *checks):
-    """(name, tensor or None, dtype) of one call: on ``dev``, contiguous, of that
-    dtype.  A decode step makes these calls once per layer, so the checks are kept
-    to a few attribute reads each."""
-    for name, t, dtype in checks:
-        if t is not None and (t.device != dev or t.dtype != dtype or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor on {dev}")
+# A decode step makes the kv4 calls once per layer, so their checks are a few
+# attribute reads per tensor; _kv4_fits says whether a tensor is what it has to be,
+# and _kv4_refuse names the first that is not.
+def _kv4_fits(t, index, dtype):
+    return t.get_device() == index and t.dtype is dtype and t.is_contiguous()
 
 
-def _kv4_dev(name, t):
-    """The call's device: that of its first tensor, which has to be the current one."""
-    dev = t.device
-    if dev.type != "cuda" or dev.index != _current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-    return dev
+def _kv4_refuse(index, *tensors):
+    """Raise for the first of (name, tensor or None, dtype, shape) that is not a
+    contiguous tensor of that dtype and shape on CUDA device ``index``."""
+    if index < 0 or index != _current_device():
+        raise ValueError(f"{tensors[0][0]} must be on the current CUDA device")
+    for name, t, dtype, shape in tensors:
+        if t is None:
+            continue
+        if not _kv4_fits(t, index, dtype):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor on CUDA device {index}")
+        if shape is not None and t.shape != tuple(shape):
+            raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    raise ValueError("kv4: arguments do not fit together")
 
 
-def _kv4_shape(name, t, *shape):
-    if t is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
-
-
-def _kv4_pool(cache, pages, lens, B):
+def _kv4_pool(cache, pages):
     """(n_pages, Hkv, page, D, max_pages) of a pool and a page table."""
     if cache.dim() != 4 or cache.shape[3] % 5:
         raise ValueError("cache must have shape [n_pages, Hkv, page, 5 D / 4]")
+    if pages.dim() != 2:
+        raise ValueError("pages must have shape [B, max_pages]")
     P, Hkv, page, w = cache.shape
-    if pages.dim() != 2 or pages.shape[0] != B:
-        raise ValueError(f"pages must have shape [{B}, max_pages]")
-    _kv4_shape("lens", lens, B)
     return P, Hkv, page, w // 5 * 4, pages.shape[1]
 
 
@@ -383,8 +383,8 @@ def _kv4_empty(stream, shape, dtype, dev):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _kv4_stream(stream, dev):
-    return _raw_stream(dev.index) if stream is None else stream.cuda_stream
+def _kv4_stream(stream, index):
+    return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
 def _at(t):
@@ -417,31 +417,40 @@ def kv4_append(k, v, cache, pages, lens, cos=None, sin=None, q=None, q_out=None,
     """
     if k.dim() != 4 or v.shape != k.shape:
         raise ValueError("k and v must have shape [B, n, Hkv, D]")
-    if k.dtype not in _DT or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    dtype = k.dtype
+    if dtype not in _DT or v.dtype is not dtype or (q is not None and q.dtype is not dtype):
         raise ValueError("q, k, v must share dtype float32 or bfloat16")
     B, n, Hkv, D = k.shape
-    dev, i32, f32 = _kv4_dev("k", k), torch.int32, torch.float32
-    P, H, page, Dc, M = _kv4_pool(cache, pages, lens, B)
-    if (H, Dc) != (Hkv, D):
+    index = k.get_device()
+    P, H, page, Dc, M = _kv4_pool(cache, pages)
+    if H != Hkv or Dc != D:
         raise ValueError("cache and k must share Hkv and D")
     if (cos is None) != (sin is None) or (cos is not None and (cos.dim() != 2 or cos.shape != sin.shape)):
         raise ValueError("cos and sin must share shape [max_pos, rot / 2]")
-    _kv4_shape("positions", positions, B, n)
-    _kv4_shape("n_new", n_new, B)
-    _kv4_shape("summary", summary, P, Hkv, 2, D)
     Hq = 0
     if q is not None:
         if q.dim() != 4 or q.shape[0] != B or q.shape[1] != n or q.shape[3] != D:
             raise ValueError("q must have shape [B, n, Hq, D]")
         Hq = q.shape[2]
-        if q_out is None:
-            q_out = _kv4_empty(stream, q.shape, q.dtype, dev)
-        _kv4_shape("q_out", q_out, *q.shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _kv4_check(dev, ("cache", cache, torch.uint8), ("pages", pages, i32), ("lens", lens, i32), ("cos", cos, f32),
-               ("sin", sin, f32), ("positions", positions, i32), ("n_new", n_new, i32),
-               ("summary", summary, torch.bfloat16), ("q_out", q_out, k.dtype))
+    if not (0 <= index == _current_device() and v.get_device() == index and (q is None or q.get_device() == index)
+            and _kv4_fits(cache, index, _U8) and _kv4_fits(pages, index, _I32) and pages.shape[0] == B
+            and _kv4_fits(lens, index, _I32) and lens.shape == (B,)
+            and (cos is None or (_kv4_fits(cos, index, _F32) and _kv4_fits(sin, index, _F32)))
+            and (positions is None or (_kv4_fits(positions, index, _I32) and positions.shape == (B, n)))
+            and (n_new is None or (_kv4_fits(n_new, index, _I32) and n_new.shape == (B,)))
+            and (summary is None or (_kv4_fits(summary, index, _BF16) and summary.shape == (P, Hkv, 2, D)))
+            and (q_out is None or (_kv4_fits(q_out, index, dtype) and q_out.shape == q.shape))):
+        if v.get_device() != index or (q is not None and q.get_device() != index):
+            raise ValueError(f"q, k, v must be on one device, k's (CUDA device {index})")
+        _kv4_refuse(index, ("k", None, dtype, None), ("cache", cache, _U8, None), ("pages", pages, _I32, (B, M)),
+                    ("lens", lens, _I32, (B,)), ("cos", cos, _F32, None), ("sin", sin, _F32, None),
+                    ("positions", positions, _I32, (B, n)), ("n_new", n_new, _I32, (B,)),
+                    ("summary", summary, _BF16, (P, Hkv, 2, D)),
+                    ("q_out", q_out, dtype, None if q is None else q.shape))
+    if q is not None and q_out is None:
+        q_out = _kv4_empty(stream, q.shape, dtype, k.device)
     strides = None
     if not (k.is_contiguous() and v.is_contiguous() and (q is None or q.is_contiguous())):
         strides = (ctypes.c_int64 * 9)()
@@ -452,14 +461,13 @@ def kv4_append(k, v, cache, pages, lens, cos=None, sin=None, q=None, q_out=None,
                 raise ValueError(f"{name}'s rows must be contiguous")
             for x in range(3):   # an axis of one entry is not stepped along: its stride says nothing
                 strides[3 * i + x] = t.stride(x) if t.shape[x] > 1 else 0
-    if v.device != dev or (q is not None and q.device != dev):
-        raise ValueError(f"q, k, v must be on {dev}")
     rot, max_pos = (0, 0) if cos is None else (2 * cos.shape[1], cos.shape[0])
     rc = _lib.load().kv4_append(k.data_ptr(), v.data_ptr(), _at(q), _at(q_out), cache.data_ptr(), _at(summary),
                                 pages.data_ptr(), lens.data_ptr(), _at(n_new), _at(positions), _at(cos), _at(sin),
-                                strides, B, n, Hq, Hkv, D, P, page, M, rot, int(interleaved), max_pos, _DT[k.dtype],
-                                _kv4_stream(stream, dev))
-    check(rc, "kv4_append")
+                                strides, B, n, Hq, Hkv, D, P, page, M, rot, int(interleaved), max_pos, _DT[dtype],
+                                _kv4_stream(stream, index))
+    if rc:
+        check(rc, "kv4_append")
     return q_out
 
 
@@ -470,22 +478,27 @@ def kv4_gather(cache, pages, lens, count: int, start=None, dtype=torch.bfloat16,
         dtype = k.dtype
     if dtype not in _DT:
         raise ValueError("dtype must be float32 or bfloat16")
+    if lens.dim() != 1:
+        raise ValueError("lens must have shape [B]")
     B = lens.shape[0]
-    dev = _kv4_dev("cache", cache)
-    P, Hkv, page, D, M = _kv4_pool(cache, pages, lens, B)
-    _kv4_shape("start", start, B)
+    index = cache.get_device()
+    P, Hkv, page, D, M = _kv4_pool(cache, pages)
     shape = (B, count, Hkv, D)
+    if not (0 <= index == _current_device() and _kv4_fits(cache, index, _U8)
+            and _kv4_fits(pages, index, _I32) and pages.shape[0] == B and _kv4_fits(lens, index, _I32)
+            and (start is None or (_kv4_fits(start, index, _I32) and start.shape == (B,)))
+            and (k is None or (_kv4_fits(k, index, dtype) and k.shape == shape))
+            and (v is None or (_kv4_fits(v, index, dtype) and v.shape == shape))):
+        _kv4_refuse(index, ("cache", cache, _U8, None), ("pages", pages, _I32, (B, M)), ("lens", lens, _I32, (B,)),
+                    ("start", start, _I32, (B,)), ("k", k, dtype, shape), ("v", v, dtype, shape))
     if k is None:
-        k = _kv4_empty(stream, shape, dtype, dev)
+        k = _kv4_empty(stream, shape, dtype, cache.device)
     if v is None:
-        v = _kv4_empty(stream, shape, dtype, dev)
-    _kv4_shape("k", k, *shape)
-    _kv4_shape("v", v, *shape)
-    _kv4_check(dev, ("cache", cache, torch.uint8), ("pages", pages, torch.int32), ("lens", lens, torch.int32),
-               ("start", start, torch.int32), ("k", k, dtype), ("v", v, dtype))
+        v = _kv4_empty(stream, shape, dtype, cache.device)
     rc = _lib.load().kv4_gather(cache.data_ptr(), pages.data_ptr(), lens.data_ptr(), _at(start), k.data_ptr(),
-                                v.data_ptr(), B, count, Hkv, D, P, page, M, _DT[dtype], _kv4_stream(stream, dev))
-    check(rc, "kv4_gather")
+                                v.data_ptr(), B, count, Hkv, D, P, page, M, _DT[dtype], _kv4_stream(stream, index))
+    if rc:
+        check(rc, "kv4_gather")
     return k, v
 
 
@@ -512,33 +525,38 @@ def kv4_attn(q, cache, pages, lens, vis=None, causal: bool = True, scale: float 
     if q.dim() != 4:
         raise ValueError("q must have shape [B, n, Hq, D]")
     B, n, Hq, D = q.shape
-    dev, i32 = _kv4_dev("q", q), torch.int32
-    if out is None:
-        out = _kv4_empty(stream, q.shape, torch.bfloat16, dev)
-    if lse is None:
-        lse = _kv4_empty(stream, (B, Hq, n), torch.float32, dev)
-    if workspace is None:
-        workspace = _kv4_empty(stream, max(kv4_attn_workspace(D), 16), torch.uint8, dev)
-    if out.dtype not in _DT:
-        raise ValueError("out must be float32 or bfloat16")
-    P, Hkv, page, Dc, M = _kv4_pool(cache, pages, lens, B)
+    index = q.get_device()
+    P, Hkv, page, Dc, M = _kv4_pool(cache, pages)
     if Dc != D:
         raise ValueError("cache and q must share D")
-    _kv4_shape("vis", vis, B, n)
-    _kv4_shape("out", out, *q.shape)
-    _kv4_shape("lse", lse, B, Hq, n)
-    n_sel = 0
-    if sel is not None:
-        n_sel = sel.shape[-1]
-        _kv4_shape("sel", sel, B, n, Hkv, n_sel)
-    _kv4_check(dev, ("q", q, torch.bfloat16), ("cache", cache, torch.uint8), ("pages", pages, i32), ("lens", lens, i32),
-               ("vis", vis, i32), ("sel", sel, i32), ("out", out, out.dtype), ("lse", lse, torch.float32),
-               ("workspace", workspace, workspace.dtype))
+    out_dtype = _BF16 if out is None else out.dtype
+    if out_dtype not in _DT:
+        raise ValueError("out must be float32 or bfloat16")
+    n_sel = 0 if sel is None else sel.shape[-1]
+    if not (0 <= index == _current_device() and _kv4_fits(q, index, _BF16) and _kv4_fits(cache, index, _U8)
+            and _kv4_fits(pages, index, _I32) and pages.shape[0] == B
+            and _kv4_fits(lens, index, _I32) and lens.shape == (B,)
+            and (vis is None or (_kv4_fits(vis, index, _I32) and vis.shape == (B, n)))
+            and (sel is None or (_kv4_fits(sel, index, _I32) and sel.shape == (B, n, Hkv, n_sel)))
+            and (out is None or (_kv4_fits(out, index, out_dtype) and out.shape == q.shape))
+            and (lse is None or (_kv4_fits(lse, index, _F32) and lse.shape == (B, Hq, n)))
+            and (workspace is None or _kv4_fits(workspace, index, workspace.dtype))):
+        _kv4_refuse(index, ("q", q, _BF16, None), ("cache", cache, _U8, None), ("pages", pages, _I32, (B, M)),
+                    ("lens", lens, _I32, (B,)), ("vis", vis, _I32, (B, n)), ("sel", sel, _I32, (B, n, Hkv, n_sel)),
+                    ("out", out, out_dtype, q.shape), ("lse", lse, _F32, (B, Hq, n)),
+                    ("workspace", workspace, None if workspace is None else workspace.dtype, None))
+    if out is None:
+        out = torch.empty_like(q) if stream is None else _kv4_empty(stream, q.shape, _BF16, q.device)
+    if lse is None:
+        lse = _kv4_empty(stream, (B, Hq, n), _F32, q.device)
+    if workspace is None:
+        workspace = _kv4_empty(stream, kv4_attn_workspace(D) or 16, _U8, q.device)
     rc = _lib.load().kv4_attn(q.data_ptr(), cache.data_ptr(), pages.data_ptr(), lens.data_ptr(), _at(vis), _at(sel),
                               out.data_ptr(), lse.data_ptr(), B, n, Hq, Hkv, D, P, page, M, n_sel, int(causal),
-                              _DT[out.dtype], -1.0 if scale is None else float(scale), workspace.data_ptr(),
-                              workspace.nbytes, _kv4_stream(stream, dev))
-    check(rc, "kv4_attn")
+                              _DT[out_dtype], -1.0 if scale is None else float(scale), workspace.data_ptr(),
+                              workspace.nbytes, _kv4_stream(stream, index))
+    if rc:
+        check(rc, "kv4_attn")
     return out, lse
 
 
@@ -555,25 +573,32 @@ def kv4_select(q, summary, pages, lens, page: int, n_sel: int, vis=None, causal:
     if q.dim() != 4 or summary.dim() != 4:
         raise ValueError("q must have shape [B, n, Hq, D] and summary [n_pages, Hkv, 2, D]")
     B, n, Hq, D = q.shape
-    dev, i32 = _kv4_dev("q", q), torch.int32
+    index = q.get_device()
     P, Hkv = summary.shape[:2]
-    _kv4_shape("summary", summary, P, Hkv, 2, D)
-    if pages.dim() != 2 or pages.shape[0] != B:
-        raise ValueError(f"pages must have shape [{B}, max_pages]")
+    if pages.dim() != 2:
+        raise ValueError("pages must have shape [B, max_pages]")
     M = pages.shape[1]
-    _kv4_shape("lens", lens, B)
-    _kv4_shape("vis", vis, B, n)
+    shape = (B, n, Hkv, n_sel)
+    if not (0 <= index == _current_device() and _kv4_fits(q, index, _BF16)
+            and _kv4_fits(summary, index, _BF16) and summary.shape == (P, Hkv, 2, D)
+            and _kv4_fits(pages, index, _I32) and pages.shape[0] == B
+            and _kv4_fits(lens, index, _I32) and lens.shape == (B,)
+            and (vis is None or (_kv4_fits(vis, index, _I32) and vis.shape == (B, n)))
+            and (sel is None or (_kv4_fits(sel, index, _I32) and sel.shape == shape))
+            and (workspace is None or _kv4_fits(workspace, index, workspace.dtype))):
+        _kv4_refuse(index, ("q", q, _BF16, None), ("summary", summary, _BF16, (P, Hkv, 2, D)),
+                    ("pages", pages, _I32, (B, M)), ("lens", lens, _I32, (B,)), ("vis", vis, _I32, (B, n)),
+                    ("sel", sel, _I32, shape),
+                    ("workspace", workspace, None if workspace is None else workspace.dtype, None))
     if sel is None:
-        sel = _kv4_empty(stream, (B, n, Hkv, max(n_sel, 0)), i32, dev)
+        sel = _kv4_empty(stream, (B, n, Hkv, max(n_sel, 0)), _I32, q.device)
     if workspace is None:
-        workspace = _kv4_empty(stream, max(kv4_select_workspace(B, n, Hkv, M), 16), torch.uint8, dev)
-    _kv4_shape("sel", sel, B, n, Hkv, n_sel)
-    _kv4_check(dev, ("q", q, torch.bfloat16), ("summary", summary, torch.bfloat16), ("pages", pages, i32),
-               ("lens", lens, i32), ("vis", vis, i32), ("sel", sel, i32), ("workspace", workspace, workspace.dtype))
+        workspace = _kv4_empty(stream, kv4_select_workspace(B, n, Hkv, M) or 16, _U8, q.device)
     rc = _lib.load().kv4_select(q.data_ptr(), summary.data_ptr(), pages.data_ptr(), lens.data_ptr(), _at(vis),
                                 sel.data_ptr(), B, n, Hq, Hkv, D, P, page, M, n_sel, int(causal), keep_first, keep_last,
-                                workspace.data_ptr(), workspace.nbytes, _kv4_stream(stream, dev))
-    check(rc, "kv4_select")
+                                workspace.data_ptr(), workspace.nbytes, _kv4_stream(stream, index))
+    if rc:
+        check(rc, "kv4_select")
     return sel
 
 
