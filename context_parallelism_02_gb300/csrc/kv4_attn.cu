@@ -159,10 +159,10 @@ __device__ __forceinline__ Item decode_item(const Shape &s, int Hkv, int b, int 
 {
     Item it;
     it.b = b;
-    it.h = i % Hkv;
-    i /= Hkv;
-    it.tile = i % s.tiles;
-    it.j0 = i / s.tiles;
+    const unsigned r = (unsigned)i / (unsigned)Hkv;   // (token, row tile)
+    it.h = i - (int)r * Hkv;
+    it.j0 = s.tiles == 1 ? (int)r : (int)(r / (unsigned)s.tiles);
+    it.tile = (int)r - it.j0 * s.tiles;
     return it;
 }
 
@@ -494,6 +494,7 @@ template <int D>
 __host__ __device__ constexpr int stages() { return 2; }
 
 constexpr int PAD = 8;
+constexpr int LEAST = 4;   // blocks that a warp takes at least
 
 // Blocks of one item of sequence b (at least 1, so that every item is written).
 __device__ __forceinline__ int item_blocks(const Kv4AttnArgs &a, int b)
@@ -552,18 +553,39 @@ __device__ __forceinline__ void count_blocks(const Kv4AttnArgs &a, int upto, int
     }
 }
 
+// a / b, by the 32-bit division (a fifth of the 64-bit one's chain of instructions)
+// where both fit, as they do but for lines of 2^31 blocks.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
+{
+    return (a | b) >> 31 == 0 ? (int64_t)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // The line of `all` blocks in equal stretches: how many there are (a warp takes at
-// least `least` blocks), where stretch c begins, and which one holds position f.
+// least LEAST blocks), where stretch c begins (floor(all c / n)), and which one holds
+// position f.
 struct Cuts {
-    int64_t all;
-    int n;
-    __device__ __forceinline__ Cuts(int64_t all_, int warps, int least) : all(all_)
+    int64_t each;     // all / n
+    int n, over;      // all % n
+    float rate;       // n / all
+    __device__ __forceinline__ Cuts(int64_t all, int warps)
     {
-        const int64_t most = all / least;
+        const int64_t most = all / LEAST;
         n = most < 1 ? 1 : most < warps ? (int)most : warps;
+        each = divide(all, n);
+        over = (int)(all - each * n);
+        rate = (float)n / (float)all;
     }
-    __device__ __forceinline__ int64_t begin(int c) const { return all * c / n; }
-    __device__ __forceinline__ int at(int64_t f) const { return (int)(((f + 1) * n - 1) / all); }
+    __device__ __forceinline__ int64_t begin(int c) const
+    {
+        return each * c + (unsigned)over * (unsigned)c / (unsigned)n;   // n is at most 2560
+    }
+    __device__ __forceinline__ int at(int64_t f) const
+    {
+        int c = min((int)((float)f * rate), n - 1);   // off by one at most
+        while (c > 0 && begin(c) > f) --c;
+        while (c + 1 < n && begin(c + 1) <= f) ++c;
+        return c;
+    }
 };
 
 // One output row's four elements.
@@ -590,7 +612,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Shape sh, int warps, int least)
+__global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Shape sh, int warps)
 {
     extern __shared__ __align__(128) uint8_t dyn[];
     Smem<D> &sm = *reinterpret_cast<Smem<D> *>(dyn);
@@ -620,7 +642,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
 #pragma unroll
     for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     all *= sh.per_batch;
-    const Cuts cuts(all, warps, least);
+    const Cuts cuts(all, warps);
     const int self = blockIdx.x * WARPS + warp;
     __syncthreads();                          // sm.abort is set
     if (self >= cuts.n) return;
@@ -649,8 +671,8 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
         rest = f0 - rest - __shfl_sync(0xffffffffu, upto - one, x) * sh.per_batch;
         break;
     }
-    at.i = (int)(rest / (at.nb + PAD));
-    at.t0 = (int)(rest % (at.nb + PAD));
+    at.i = (int)divide(rest, at.nb + PAD);
+    at.t0 = (int)(rest - (int64_t)at.i * (at.nb + PAD));
     at.left = cuts.begin(self + 1) - f0;
     at.cut();
     RawRows<D, NT> raw;
@@ -803,7 +825,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
 // parts are read JOIN_DEEP at a time by each of JW warps, so that a row of many pieces (one
 // long sequence: up to all warps of the grid) costs a few memory latencies.
 template <int D, int NT, int JW, int JOIN_DEEP>
-__global__ void __launch_bounds__(JW * 32) kv4_join_kernel(Kv4AttnArgs a, Shape sh, int warps, int least)
+__global__ void __launch_bounds__(JW * 32) kv4_join_kernel(Kv4AttnArgs a, Shape sh, int warps)
 {
     constexpr int E = D / 32;
     __shared__ float sm_m[JW], sm_l[JW];
@@ -818,7 +840,7 @@ __global__ void __launch_bounds__(JW * 32) kv4_join_kernel(Kv4AttnArgs a, Shape 
     int64_t all, before;
     count_blocks(a, b, all, before);
     all *= sh.per_batch;
-    const Cuts cuts(all, warps, least);
+    const Cuts cuts(all, warps);
     const int nb = item_blocks(a, b);
     // the item of this row: token, row tile, kv head
     const int tile = rr_all / (NT * 8), row = rr_all % (NT * 8);
@@ -894,7 +916,6 @@ __global__ void __launch_bounds__(JW * 32) kv4_join_kernel(Kv4AttnArgs a, Shape 
 }
 
 constexpr int MAX_ROWS = 2560 * 8;   // rows of warps' parts that the workspace has room for (twice)
-constexpr int LEAST = 4;             // blocks that a warp takes at least
 
 template <int D, int NT>
 int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
@@ -924,15 +945,15 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
     const int64_t joins = (int64_t)a.rows.B * (sh.per_batch / sh.tiles) * sh.rows;
     if (joins > 0x7fffffffLL) return CP_EUNSUPPORTED;
     const int warps = grid * WARPS;
-    if (kv4_launch(kv4_attn_kernel<D, NT>, (unsigned)grid, WARPS * 32, smem, st, a, sh, warps, LEAST) != cudaSuccess)
+    if (kv4_launch(kv4_attn_kernel<D, NT>, (unsigned)grid, WARPS * 32, smem, st, a, sh, warps) != cudaSuccess)
         return CP_ECUDA;
     // many warps where a row is cut into many pieces
     const int64_t cuts = warps / ((int64_t)a.rows.B * sh.per_batch);   // pieces of an item, about
     const unsigned n = (unsigned)joins;
     const cudaError_t rc =
-        cuts > 64  ? kv4_launch(kv4_join_kernel<D, NT, 32, 4>, n, 1024, 0, st, a, sh, warps, LEAST)
-        : cuts > 16 ? kv4_launch(kv4_join_kernel<D, NT, 8, 8>, n, 256, 0, st, a, sh, warps, LEAST)
-                    : kv4_launch(kv4_join_kernel<D, NT, 4, 4>, n, 128, 0, st, a, sh, warps, LEAST);
+        cuts > 64  ? kv4_launch(kv4_join_kernel<D, NT, 32, 4>, n, 1024, 0, st, a, sh, warps)
+        : cuts > 16 ? kv4_launch(kv4_join_kernel<D, NT, 8, 8>, n, 256, 0, st, a, sh, warps)
+                    : kv4_launch(kv4_join_kernel<D, NT, 4, 4>, n, 128, 0, st, a, sh, warps);
     return rc == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 
