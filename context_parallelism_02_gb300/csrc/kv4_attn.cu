@@ -604,11 +604,19 @@ __device__ __forceinline__ void prefetch(const void *p, int64_t at, int64_t byte
     if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p) + at));
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar, uint64_t policy)
 {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ uint64_t policy_evict_normal()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
 }
 
 template <int D, int NT>
@@ -684,6 +692,9 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     __syncwarp();
     const WaitCtl wc{a.pool.err, &sm.abort, a.limit_ns};
     const int ps = a.pool.page_shift, bpp = 1 << (ps - 4);
+    // with one row tile a block is read once and makes way in L2 for what the join
+    // will read (4 x 32k tokens: 39.8 us without, 37.3 us with)
+    const uint64_t policy = sh.tiles == 1 ? tc::policy_evict_first() : policy_evict_normal();
     // The issuing side: each lane works out one of the next 32 blocks of a piece.
     int batch = 0, batch_n = 0;             // blocks of the batch issued, blocks in it (an even number)
     int next_t = ahead.t0;                  // next block of the piece to be worked out
@@ -740,7 +751,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
             sm.slot[warp][put][lane - batch] = src_slot;
             if (src) {
                 mbar_arrive_expect_tx(bar, Kv4<D>::BYTES);
-                bulk_load(smem_u32(sm.ring[warp][put][lane - batch]), src, Kv4<D>::BYTES, bar);
+                bulk_load(smem_u32(sm.ring[warp][put][lane - batch]), src, Kv4<D>::BYTES, bar, policy);
             } else {
                 mbar_arrive(bar);
             }
