@@ -165,6 +165,7 @@ int kv4_attn(const void *q, const void *cache, const int32_t *pages, const int32
     if (out_dtype != CP_F32 && out_dtype != CP_BF16) return CP_EUNSUPPORTED;
     if ((rc = check_rows(q, vis, B, n, Hq, Hkv, causal, a.rows))) return rc;
     if (sel ? n_sel < 1 || !aligned(sel, 4) : n_sel != 0) return CP_EINVAL;
+    if (n_sel > 1 << 26) return CP_EUNSUPPORTED;   // blocks of 16 tokens are counted in 32 bits
     if (isnan(scale)) return CP_EINVAL;
     if (B == 0 || n == 0) return CP_OK;
     if (!out || !lse || !aligned(out, 16) || !aligned(lse, 4)) return CP_EINVAL;

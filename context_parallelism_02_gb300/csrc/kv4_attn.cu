@@ -932,6 +932,9 @@ template <int D, int NT>
 int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
 {
     constexpr int smem = sizeof(Smem<D>);
+    // one block of the join per output row
+    const int64_t joins = (int64_t)a.rows.B * (sh.per_batch / sh.tiles) * sh.rows;
+    if (joins > 0x7fffffffLL) return CP_EUNSUPPORTED;
     // blocks of a grid that just fills the device, worked out once per device
     constexpr int MAX_DEV = 64;
     static std::atomic<int> fills[MAX_DEV];
@@ -953,8 +956,6 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
                                : ((int64_t)a.pool.max_pages << (a.pool.page_shift - 4));
     const int64_t line = ((most > 0 ? most : 1) + PAD) * a.rows.B * sh.per_batch;
     const int grid = (int)min(ctas, (line + LEAST * WARPS - 1) / (LEAST * WARPS));
-    const int64_t joins = (int64_t)a.rows.B * (sh.per_batch / sh.tiles) * sh.rows;
-    if (joins > 0x7fffffffLL) return CP_EUNSUPPORTED;
     const int warps = grid * WARPS;
     if (kv4_launch(kv4_attn_kernel<D, NT>, (unsigned)grid, WARPS * 32, smem, st, a, sh, warps) != cudaSuccess)
         return CP_ECUDA;

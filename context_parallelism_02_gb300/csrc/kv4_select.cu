@@ -30,7 +30,8 @@ __device__ __forceinline__ void mma16816_bf16(float (&d)[4], uint32_t a0, uint32
 // 0 elsewhere.
 __device__ __forceinline__ uint32_t half_line(uint32_t w, bool neg)
 {
-    const uint32_t s = ((w >> 15) & 0x00010001u) * 0xffffu;
+    uint32_t s;   // 0xffff in the halves whose sign is set: prmt that replicates the signs of bytes 1 and 3
+    asm("prmt.b32 %0, %1, %1, 0xBB99;" : "=r"(s) : "r"(w));
     return neg ? w & s : w & ~s;
 }
 

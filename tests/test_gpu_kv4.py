@@ -890,3 +890,47 @@ def test_attn_bounded_wait(cuda_dev):
     got = api.kv4_attn(q, cache, dev(pages), lens)
     ok()
     assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+def test_capture_behind_memsets_copies_and_joined_streams(cuda_dev):
+    """The calls captured behind nodes of every kind: a kernel, a memset, a copy, two streams at once, nothing."""
+    rng = np.random.default_rng(24)
+    cache, summ, pages = fill(rng, 2, 700, 1, 64, 16)
+    q, k = (dev(rows(rng, torch.bfloat16, 2, 1, h, 64), torch.bfloat16) for h in (3, 1))
+    gp, lens = dev(pages), dev(np.array([650, 321], np.int32))
+
+    def call(q):
+        qr = api.kv4_append(k, k, cache, gp, lens, q=q, summary=summ)
+        sel = api.kv4_select(qr, summ, gp, lens, 16, 4)
+        return [qr, sel, *api.kv4_attn(qr, cache, gp, lens, sel=sel), *api.kv4_gather(cache, gp, lens, 60)]
+    want = [t.clone() for t in call(q)]
+    ok()
+    src, buf, side = q.clone(), torch.empty_like(q), torch.cuda.Stream()
+    for kind in ("nothing", "kernel", "memset", "copy", "streams"):
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            x = src
+            if kind == "kernel":
+                x = src + 0
+            if kind == "memset":
+                torch.zeros(1 << 16, device="cuda")
+            if kind == "copy":
+                buf.copy_(src)
+                x = buf
+            if kind == "streams":
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    buf.copy_(src * 1)
+                y = src * 1
+                torch.cuda.current_stream().wait_stream(side)
+                x = buf
+            outs = call(x)
+            if kind == "streams":
+                outs.append(y)
+        for _ in range(3):
+            buf.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(g, w) for g, w in zip(outs, want)), kind
+    ok()

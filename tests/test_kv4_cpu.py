@@ -143,6 +143,7 @@ def test_attn_refusals(cplib):
     assert attn(n_sel=3) == E                       # a count without a list
     assert attn(sel=FAKE, n_sel=0) == E
     assert attn(sel=FAKE + 2, n_sel=3) == E
+    assert attn(sel=FAKE, n_sel=(1 << 26) + 1) == _lib.CP_EUNSUPPORTED
     L = _lib.load()
     assert L.kv4_attn_workspace(96) == 0
     for D in (64, 128):
