@@ -377,6 +377,8 @@ int ring_attn_bwd_noalloc(const void *q, const void *k, const void *v, const voi
  * for them and can be captured in a graph.  An entry outside its range is
  * therefore not an error of the call: the kernels skip what it names and record
  * CP_ECACHE (cp_get_error).
+ * The kernels may be scheduled while the one before them on the stream ends; they
+ * read and write nothing before it is complete.
  */
 
 /*
@@ -437,7 +439,8 @@ int kv4_gather(const void *cache, const int32_t *pages, const int32_t *lens, con
  *   lse [B][Hq][n] fp32, natural log.  A row that sees nothing: (0, -inf).  What a
  *   row does not see has no influence on it, whatever those slots hold.
  *   fp32 sums; K enters exactly, V's values and the softmax weights rounded to
- *   fp16.  scale <= 0 selects 1/sqrt(D).
+ *   fp16.  scale <= 0 selects 1/sqrt(D).  A row of q with a value that is not finite,
+ *   or of 2^110 and more, comes out as NaN.
  *   workspace: device, kv4_attn_workspace(D) bytes, 16-byte aligned, contents
  *   irrelevant; calls that may overlap on the GPU need their own.
  * Errors: as kv4_append, plus a null or too small workspace.
