@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -107,6 +108,31 @@ def load(build_if_missing: bool = False, variant: str | None = None):
                 fn.argtypes = args
             _libs[v] = lib
     return _libs[v]
+
+
+_KV4_CALLS = ("kv4_append", "kv4_gather", "kv4_attn", "kv4_attn_workspace", "kv4_select", "kv4_select_workspace")
+_kv4_module = None
+_kv4_tables = {}           # variant -> the calls' addresses, as the module takes them
+
+
+def kv4():
+    """(module of the paged cache's calls, table of the active library for it)."""
+    global _kv4_module
+    table = _kv4_tables.get(_active)
+    if table is None:
+        lib = load()
+        with _lock:
+            if _kv4_module is None:
+                if not os.path.exists(_build.BINDING):
+                    raise RuntimeError(f"{_build.BINDING} not found; build it with "
+                                       "`python -m context_parallelism_02_gb300.build`")
+                spec = importlib.util.spec_from_file_location("_kv4_binding", _build.BINDING)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                _kv4_module = module
+            table = _kv4_module.table(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _KV4_CALLS))
+            _kv4_tables[_active] = table
+    return _kv4_module, table
 
 
 @contextlib.contextmanager

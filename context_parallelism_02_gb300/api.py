@@ -337,58 +337,18 @@ def ulysses_head_to_seq(y: torch.Tensor, N: int, layout: int, x=None, stream=Non
     return x
 
 
+# The kv4 calls go through the module of csrc/kv4_binding.cpp, which checks the
+# tensors and makes those that are not given: in Python that took longer than the
+# kernels of a decode step.
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
-_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
 
 
-# A decode step makes the kv4 calls once per layer, so their checks are a few
-# attribute reads per tensor; _kv4_fits says whether a tensor is what it has to be,
-# and _kv4_refuse names the first that is not.
-def _kv4_fits(t, index, dtype):
-    return t.get_device() == index and t.dtype is dtype and t.is_contiguous()
-
-
-def _kv4_refuse(index, *tensors):
-    """Raise for the first of (name, tensor or None, dtype, shape) that is not a
-    contiguous tensor of that dtype and shape on CUDA device ``index``."""
-    if index < 0 or index != _current_device():
-        raise ValueError(f"{tensors[0][0]} must be on the current CUDA device")
-    for name, t, dtype, shape in tensors:
-        if t is None:
-            continue
-        if not _kv4_fits(t, index, dtype):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor on CUDA device {index}")
-        if shape is not None and t.shape != tuple(shape):
-            raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
-    raise ValueError("kv4: arguments do not fit together")
-
-
-def _kv4_pool(cache, pages):
-    """(n_pages, Hkv, page, D, max_pages) of a pool and a page table."""
-    if cache.dim() != 4 or cache.shape[3] % 5:
-        raise ValueError("cache must have shape [n_pages, Hkv, page, 5 D / 4]")
-    if pages.dim() != 2:
-        raise ValueError("pages must have shape [B, max_pages]")
-    P, Hkv, page, w = cache.shape
-    return P, Hkv, page, w // 5 * 4, pages.shape[1]
-
-
-def _kv4_empty(stream, shape, dtype, dev):
-    """A tensor whose memory belongs to ``stream`` (None: the current one), so that it
-    is not handed on while that stream's kernels may still use it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-
-def _kv4_stream(stream, index):
-    return _raw_stream(index) if stream is None else stream.cuda_stream
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _kv4_device(name, t):
+    """The call's device: that of its first tensor, which has to be the current one."""
+    if not t.is_cuda or t.get_device() != _current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return t.get_device()
 
 
 def kv4_cache(n_pages: int, Hkv: int, page: int, D: int, summary: bool = False):
@@ -415,101 +375,39 @@ def kv4_append(k, v, cache, pages, lens, cos=None, sin=None, q=None, q_out=None,
     slots); n_new int32 ``[B]``: real tokens of a padded batch; summary: the pool's
     key ranges, kept for :func:`kv4_select`.
     """
-    if k.dim() != 4 or v.shape != k.shape:
-        raise ValueError("k and v must have shape [B, n, Hkv, D]")
-    dtype = k.dtype
-    if dtype not in _DT or v.dtype is not dtype or (q is not None and q.dtype is not dtype):
-        raise ValueError("q, k, v must share dtype float32 or bfloat16")
-    B, n, Hkv, D = k.shape
-    index = k.get_device()
-    P, H, page, Dc, M = _kv4_pool(cache, pages)
-    if H != Hkv or Dc != D:
-        raise ValueError("cache and k must share Hkv and D")
-    if (cos is None) != (sin is None) or (cos is not None and (cos.dim() != 2 or cos.shape != sin.shape)):
-        raise ValueError("cos and sin must share shape [max_pos, rot / 2]")
-    Hq = 0
-    if q is not None:
-        if q.dim() != 4 or q.shape[0] != B or q.shape[1] != n or q.shape[3] != D:
-            raise ValueError("q must have shape [B, n, Hq, D]")
-        Hq = q.shape[2]
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if not (0 <= index == _current_device() and v.get_device() == index and (q is None or q.get_device() == index)
-            and _kv4_fits(cache, index, _U8) and _kv4_fits(pages, index, _I32) and pages.shape[0] == B
-            and _kv4_fits(lens, index, _I32) and lens.shape == (B,)
-            and (cos is None or (_kv4_fits(cos, index, _F32) and _kv4_fits(sin, index, _F32)))
-            and (positions is None or (_kv4_fits(positions, index, _I32) and positions.shape == (B, n)))
-            and (n_new is None or (_kv4_fits(n_new, index, _I32) and n_new.shape == (B,)))
-            and (summary is None or (_kv4_fits(summary, index, _BF16) and summary.shape == (P, Hkv, 2, D)))
-            and (q_out is None or (_kv4_fits(q_out, index, dtype) and q_out.shape == q.shape))):
-        if v.get_device() != index or (q is not None and q.get_device() != index):
-            raise ValueError(f"q, k, v must be on one device, k's (CUDA device {index})")
-        _kv4_refuse(index, ("k", None, dtype, None), ("cache", cache, _U8, None), ("pages", pages, _I32, (B, M)),
-                    ("lens", lens, _I32, (B,)), ("cos", cos, _F32, None), ("sin", sin, _F32, None),
-                    ("positions", positions, _I32, (B, n)), ("n_new", n_new, _I32, (B,)),
-                    ("summary", summary, _BF16, (P, Hkv, 2, D)),
-                    ("q_out", q_out, dtype, None if q is None else q.shape))
-    if q is not None and q_out is None:
-        q_out = _kv4_empty(stream, q.shape, dtype, k.device)
-    strides = None
-    if not (k.is_contiguous() and v.is_contiguous() and (q is None or q.is_contiguous())):
-        strides = (ctypes.c_int64 * 9)()
-        for i, (name, t) in enumerate((("k", k), ("v", v), ("q", q))):
-            if t is None:
-                continue
-            if t.numel() and t.stride(3) != 1:
-                raise ValueError(f"{name}'s rows must be contiguous")
-            for x in range(3):   # an axis of one entry is not stepped along: its stride says nothing
-                strides[3 * i + x] = t.stride(x) if t.shape[x] > 1 else 0
-    rot, max_pos = (0, 0) if cos is None else (2 * cos.shape[1], cos.shape[0])
-    rc = _lib.load().kv4_append(k.data_ptr(), v.data_ptr(), _at(q), _at(q_out), cache.data_ptr(), _at(summary),
-                                pages.data_ptr(), lens.data_ptr(), _at(n_new), _at(positions), _at(cos), _at(sin),
-                                strides, B, n, Hq, Hkv, D, P, page, M, rot, int(interleaved), max_pos, _DT[dtype],
-                                _kv4_stream(stream, index))
-    if rc:
-        check(rc, "kv4_append")
-    return q_out
+    if stream is not None:   # what is allocated belongs to the stream that uses it
+        with torch.cuda.stream(stream):
+            return kv4_append(k, v, cache, pages, lens, cos, sin, q, q_out, positions, n_new, summary, interleaved)
+    index = _kv4_device("k", k)
+    module, table = _lib.kv4()
+    got = module.append(table, k, v, cache, pages, lens, cos, sin, q, q_out, positions, n_new, summary, interleaved, index,
+                        _raw_stream(index))
+    if type(got) is int:
+        check(got, "kv4_append")
+    return got if q_out is None else q_out
 
 
 def kv4_gather(cache, pages, lens, count: int, start=None, dtype=torch.bfloat16, k=None, v=None, stream=None):
     """Cached tokens back as rows: (k, v) ``[B, count, Hkv, D]`` with row (b, j) the slot
     ``start[b] + j`` (start int32 ``[B]``, None: 0); rows at or past ``lens[b]`` are 0."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv4_gather(cache, pages, lens, count, start, dtype, k, v)
     if k is not None:
         dtype = k.dtype
     if dtype not in _DT:
         raise ValueError("dtype must be float32 or bfloat16")
-    if lens.dim() != 1:
-        raise ValueError("lens must have shape [B]")
-    B = lens.shape[0]
-    index = cache.get_device()
-    P, Hkv, page, D, M = _kv4_pool(cache, pages)
-    shape = (B, count, Hkv, D)
-    if not (0 <= index == _current_device() and _kv4_fits(cache, index, _U8)
-            and _kv4_fits(pages, index, _I32) and pages.shape[0] == B and _kv4_fits(lens, index, _I32)
-            and (start is None or (_kv4_fits(start, index, _I32) and start.shape == (B,)))
-            and (k is None or (_kv4_fits(k, index, dtype) and k.shape == shape))
-            and (v is None or (_kv4_fits(v, index, dtype) and v.shape == shape))):
-        _kv4_refuse(index, ("cache", cache, _U8, None), ("pages", pages, _I32, (B, M)), ("lens", lens, _I32, (B,)),
-                    ("start", start, _I32, (B,)), ("k", k, dtype, shape), ("v", v, dtype, shape))
-    if k is None:
-        k = _kv4_empty(stream, shape, dtype, cache.device)
-    if v is None:
-        v = _kv4_empty(stream, shape, dtype, cache.device)
-    rc = _lib.load().kv4_gather(cache.data_ptr(), pages.data_ptr(), lens.data_ptr(), _at(start), k.data_ptr(),
-                                v.data_ptr(), B, count, Hkv, D, P, page, M, _DT[dtype], _kv4_stream(stream, index))
-    if rc:
-        check(rc, "kv4_gather")
-    return k, v
-
-
-_ATTN_WORKSPACE = {}
+    index = _kv4_device("cache", cache)
+    module, table = _lib.kv4()
+    got = module.gather(table, cache, pages, lens, count, start, dtype is torch.bfloat16, k, v, index, _raw_stream(index))
+    if type(got) is int:
+        check(got, "kv4_gather")
+    return got
 
 
 def kv4_attn_workspace(D: int) -> int:
     """Bytes of scratch for :func:`kv4_attn` (a constant of D)."""
-    if D not in _ATTN_WORKSPACE:
-        _ATTN_WORKSPACE[D] = int(_lib.load().kv4_attn_workspace(D))
-    return _ATTN_WORKSPACE[D]
+    return int(_lib.load().kv4_attn_workspace(D))
 
 
 def kv4_attn(q, cache, pages, lens, vis=None, causal: bool = True, scale: float | None = None, sel=None,
@@ -522,42 +420,16 @@ def kv4_attn(q, cache, pages, lens, vis=None, causal: bool = True, scale: float 
     causal, else below ``lens[b]``.  ``sel`` int32 ``[B, n, Hkv, n_sel]``
     (:func:`kv4_select`): only the slots of these pages.
     """
-    if q.dim() != 4:
-        raise ValueError("q must have shape [B, n, Hq, D]")
-    B, n, Hq, D = q.shape
-    index = q.get_device()
-    P, Hkv, page, Dc, M = _kv4_pool(cache, pages)
-    if Dc != D:
-        raise ValueError("cache and q must share D")
-    out_dtype = _BF16 if out is None else out.dtype
-    if out_dtype not in _DT:
-        raise ValueError("out must be float32 or bfloat16")
-    n_sel = 0 if sel is None else sel.shape[-1]
-    if not (0 <= index == _current_device() and _kv4_fits(q, index, _BF16) and _kv4_fits(cache, index, _U8)
-            and _kv4_fits(pages, index, _I32) and pages.shape[0] == B
-            and _kv4_fits(lens, index, _I32) and lens.shape == (B,)
-            and (vis is None or (_kv4_fits(vis, index, _I32) and vis.shape == (B, n)))
-            and (sel is None or (_kv4_fits(sel, index, _I32) and sel.shape == (B, n, Hkv, n_sel)))
-            and (out is None or (_kv4_fits(out, index, out_dtype) and out.shape == q.shape))
-            and (lse is None or (_kv4_fits(lse, index, _F32) and lse.shape == (B, Hq, n)))
-            and (workspace is None or _kv4_fits(workspace, index, workspace.dtype))):
-        _kv4_refuse(index, ("q", q, _BF16, None), ("cache", cache, _U8, None), ("pages", pages, _I32, (B, M)),
-                    ("lens", lens, _I32, (B,)), ("vis", vis, _I32, (B, n)), ("sel", sel, _I32, (B, n, Hkv, n_sel)),
-                    ("out", out, out_dtype, q.shape), ("lse", lse, _F32, (B, Hq, n)),
-                    ("workspace", workspace, None if workspace is None else workspace.dtype, None))
-    if out is None:
-        out = torch.empty_like(q) if stream is None else _kv4_empty(stream, q.shape, _BF16, q.device)
-    if lse is None:
-        lse = _kv4_empty(stream, (B, Hq, n), _F32, q.device)
-    if workspace is None:
-        workspace = _kv4_empty(stream, kv4_attn_workspace(D) or 16, _U8, q.device)
-    rc = _lib.load().kv4_attn(q.data_ptr(), cache.data_ptr(), pages.data_ptr(), lens.data_ptr(), _at(vis), _at(sel),
-                              out.data_ptr(), lse.data_ptr(), B, n, Hq, Hkv, D, P, page, M, n_sel, int(causal),
-                              _DT[out_dtype], -1.0 if scale is None else float(scale), workspace.data_ptr(),
-                              workspace.nbytes, _kv4_stream(stream, index))
-    if rc:
-        check(rc, "kv4_attn")
-    return out, lse
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv4_attn(q, cache, pages, lens, vis, causal, scale, sel, out, lse, workspace)
+    index = _kv4_device("q", q)
+    module, table = _lib.kv4()
+    got = module.attn(table, q, cache, pages, lens, vis, causal, -1.0 if scale is None else scale, sel, out, lse, workspace,
+                      index, _raw_stream(index))
+    if type(got) is int:
+        check(got, "kv4_attn")
+    return got
 
 
 def kv4_select_workspace(B: int, n: int, Hkv: int, max_pages: int) -> int:
@@ -570,36 +442,16 @@ def kv4_select(q, summary, pages, lens, page: int, n_sel: int, vis=None, causal:
     ``[B, n, Hkv, n_sel]``, ascending, then -1.  q as :func:`kv4_attn`; summary as
     :func:`kv4_cache`; ``page``: tokens of a page.  The first ``keep_first`` and last
     ``keep_last`` pages that the row sees are always among them."""
-    if q.dim() != 4 or summary.dim() != 4:
-        raise ValueError("q must have shape [B, n, Hq, D] and summary [n_pages, Hkv, 2, D]")
-    B, n, Hq, D = q.shape
-    index = q.get_device()
-    P, Hkv = summary.shape[:2]
-    if pages.dim() != 2:
-        raise ValueError("pages must have shape [B, max_pages]")
-    M = pages.shape[1]
-    shape = (B, n, Hkv, n_sel)
-    if not (0 <= index == _current_device() and _kv4_fits(q, index, _BF16)
-            and _kv4_fits(summary, index, _BF16) and summary.shape == (P, Hkv, 2, D)
-            and _kv4_fits(pages, index, _I32) and pages.shape[0] == B
-            and _kv4_fits(lens, index, _I32) and lens.shape == (B,)
-            and (vis is None or (_kv4_fits(vis, index, _I32) and vis.shape == (B, n)))
-            and (sel is None or (_kv4_fits(sel, index, _I32) and sel.shape == shape))
-            and (workspace is None or _kv4_fits(workspace, index, workspace.dtype))):
-        _kv4_refuse(index, ("q", q, _BF16, None), ("summary", summary, _BF16, (P, Hkv, 2, D)),
-                    ("pages", pages, _I32, (B, M)), ("lens", lens, _I32, (B,)), ("vis", vis, _I32, (B, n)),
-                    ("sel", sel, _I32, shape),
-                    ("workspace", workspace, None if workspace is None else workspace.dtype, None))
-    if sel is None:
-        sel = _kv4_empty(stream, (B, n, Hkv, max(n_sel, 0)), _I32, q.device)
-    if workspace is None:
-        workspace = _kv4_empty(stream, kv4_select_workspace(B, n, Hkv, M) or 16, _U8, q.device)
-    rc = _lib.load().kv4_select(q.data_ptr(), summary.data_ptr(), pages.data_ptr(), lens.data_ptr(), _at(vis),
-                                sel.data_ptr(), B, n, Hq, Hkv, D, P, page, M, n_sel, int(causal), keep_first, keep_last,
-                                workspace.data_ptr(), workspace.nbytes, _kv4_stream(stream, index))
-    if rc:
-        check(rc, "kv4_select")
-    return sel
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv4_select(q, summary, pages, lens, page, n_sel, vis, causal, keep_first, keep_last, sel, workspace)
+    index = _kv4_device("q", q)
+    module, table = _lib.kv4()
+    got = module.select(table, q, summary, pages, lens, page, n_sel, vis, causal, keep_first, keep_last, sel, workspace,
+                        index, _raw_stream(index))
+    if type(got) is int:
+        check(got, "kv4_select")
+    return got
 
 
 def cp_get_error(stream=None) -> int:

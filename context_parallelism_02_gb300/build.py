@@ -2,7 +2,8 @@
 
 Each ``csrc/*.cu`` is compiled in parallel to an object file, then linked
 into ``context_parallelism_02_gb300/_build/libcp.so`` with the CUDA runtime
-linked statically, so the library needs only the driver at load time.
+linked statically, so the library needs only the driver at load time.  Next to
+it, ``csrc/kv4_binding.cpp`` becomes the Python module of the cache's calls.
 
 Usage: ``python -m context_parallelism_02_gb300.build`` (or ``build()``).
 
@@ -15,10 +16,12 @@ of range (no trap).  Tests select it with ``_lib.variant("debug_bounds")``.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -27,6 +30,12 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libcp.so")
 LIB_DEBUG_BOUNDS = os.path.join(BUILD, "debug_bounds", "libcp.so")
+try:   # the module belongs to the torch it was compiled against
+    _TORCH = importlib.metadata.version("torch")
+except importlib.metadata.PackageNotFoundError:
+    _TORCH = "none"
+BINDING = os.path.join(BUILD, f"_kv4_binding-{_TORCH}.so")
+BINDING_SRC = "kv4_binding.cpp"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC,
@@ -45,7 +54,28 @@ def _sources():
 
 
 def _deps():
-    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "cp.h")]
+    return [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != BINDING_SRC] + [os.path.join(INCLUDE, "cp.h")]
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the Python module of the cache's calls against torch's headers (g++); returns its path."""
+    deps = [os.path.join(CSRC, BINDING_SRC), os.path.join(INCLUDE, "cp.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return BINDING
+    import torch
+    home = os.path.dirname(torch.__file__)
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", os.path.join(home, "include"), "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], deps[0], "-o", tmp, "-L" + os.path.join(home, "lib"),
+           "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def up_to_date(lib: str = LIB) -> bool:
@@ -60,6 +90,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(),
     """Compile and link libcp.so (or its debug-bounds variant); returns its path."""
     lib = LIB_DEBUG_BOUNDS if debug_bounds else LIB
     if not force and up_to_date(lib):
+        build_binding()
         return lib
     out_dir = os.path.dirname(lib)
     os.makedirs(out_dir, exist_ok=True)
@@ -78,8 +109,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(),
         return obj
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(build_binding, force)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -708,6 +708,24 @@ def test_attn_sizes_of_scores_and_queries(cuda_dev):
         check_reference(out[:, :, i:i + 1], lse[:, i:i + 1], q[:, :, i:i + 1], kr, vr, torch.tensor([[L]]), 1 / math.sqrt(D))
 
 
+def test_attn_query_rows_that_are_not_finite(cuda_dev):
+    """A row of q with an infinity, a NaN or a magnitude beyond 2^110 is NaN; the other rows of its tile are what they were."""
+    rng = np.random.default_rng(25)
+    cache, _, pages = fill(rng, 1, 300, 1, 128, 64)
+    q = dev(rows(rng, torch.bfloat16, 1, 1, 8, 128), torch.bfloat16)
+    lens = dev(np.array([300], np.int32))
+    want, wlse = api.kv4_attn(q, cache, dev(pages), lens)
+    bad = q.clone()
+    bad[0, 0, 1, 5], bad[0, 0, 4, 100], bad[0, 0, 6] = math.inf, math.nan, 2.0 ** 112
+    out, lse = api.kv4_attn(bad, cache, dev(pages), lens)
+    ok()
+    for i in range(8):
+        if i in (1, 4, 6):
+            assert out[0, 0, i].isnan().all() and lse[0, i].isnan().all()
+        else:
+            assert torch.equal(out[0, 0, i], want[0, 0, i]) and torch.equal(lse[0, i], wlse[0, i])
+
+
 def test_append_rotates_q_in_place(cuda_dev):
     rng = np.random.default_rng(20)
     cos, sin = (dev(x) for x in rope(64, 128))
@@ -857,6 +875,15 @@ def test_binding_refusals_on_the_gpu(cuda_dev):
             raise AssertionError(i)
     ok()
     assert torch.equal(before, cache)
+    for call, error in ((lambda: api.kv4_gather(cache, pages, lens, "4"), TypeError),
+                        (lambda: api.kv4_gather(cache, pages, lens, 1 << 40), ValueError),
+                        (lambda: api.kv4_gather(cache, pages, lens, -1), _lib.CpError),
+                        (lambda: api.kv4_attn(q, cache, pages, lens, scale="x"), TypeError),
+                        (lambda: api.kv4_attn(q, cache, pages, lens, vis=3), ValueError),
+                        (lambda: api.kv4_attn(q, cache, pages, None), ValueError),
+                        (lambda: api.kv4_select(q, summ, pages, lens, 16, 1 << 33), ValueError)):
+        with pytest.raises(error):
+            call()
     # rows that do not start on 16 bytes
     x = torch.zeros(1, 2, 2 * D + 2, device="cuda", dtype=torch.bfloat16)[..., :2 * D].unflatten(-1, (2, D))
     with pytest.raises(_lib.CpError):
