@@ -502,7 +502,7 @@ __host__ __device__ constexpr int stages() { return 2; }
 // What an item costs beyond its blocks, in blocks: with 4, 64 ragged sequences up to
 // 8192 tokens take 38 us instead of 33, with 16 34.
 constexpr int PAD = 8;
-constexpr int LEAST = 4;   // blocks that a warp takes at least
+constexpr int LEAST = 2;   // blocks that a warp takes at least: a stage (512 tokens: 8.5 us, with 4 9.0)
 
 // Blocks of one item of sequence b (at least 1, so that every item is written).
 __device__ __forceinline__ int item_blocks(const Kv4AttnArgs &a, int b)
@@ -971,7 +971,7 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
     const int64_t cuts = warps / ((int64_t)a.rows.B * sh.per_batch);   // pieces of an item, about
     const unsigned n = (unsigned)joins;
     const cudaError_t rc =
-        cuts > 64  ? kv4_launch(kv4_join_kernel<D, NT, 32, 4>, n, 1024, 0, st, a, sh, warps)
+        cuts > 64  ? kv4_launch(kv4_join_kernel<D, NT, 16, 4>, n, 512, 0, st, a, sh, warps)
         : cuts > 16 ? kv4_launch(kv4_join_kernel<D, NT, 8, 8>, n, 256, 0, st, a, sh, warps)
                     : kv4_launch(kv4_join_kernel<D, NT, 4, 4>, n, 128, 0, st, a, sh, warps);
     return rc == cudaSuccess ? CP_OK : CP_ECUDA;
