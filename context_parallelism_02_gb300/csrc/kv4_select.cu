@@ -35,77 +35,103 @@ __device__ __forceinline__ uint32_t half_line(uint32_t w, bool neg)
     return neg ? w & s : w & ~s;
 }
 
-// One warp per 16 pages of one (sequence, token, kv head).
+// A warp takes 16 pages of one (sequence, token, kv head) at a time; the page numbers
+// of its next ones are on their way while it works.
 template <int D>
-__global__ void __launch_bounds__(128) kv4_score_kernel(Kv4SelectArgs a, int tiles, unsigned warps)
+__global__ void __launch_bounds__(128) kv4_score_kernel(Kv4SelectArgs a, int tiles, unsigned units)
 {
     constexpr int NI = D / 16;   // 16-byte pieces of a summary row per lane
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const unsigned wid = blockIdx.x * 4 + (threadIdx.x >> 5);
     kv4_begin();
-    if (wid >= warps) return;
-    const int Hkv = a.pool.Hkv, group = a.rows.Hq / Hkv;
-    const unsigned item = wid / (unsigned)tiles, bj = item / (unsigned)Hkv;
-    const int tile = (int)(wid - item * tiles), h = (int)(item - bj * Hkv);
-    const int b = (int)(bj / (unsigned)a.rows.n), j = (int)(bj - (unsigned)b * a.rows.n);
-    // what does not hang on the length is on its way before it is here: the first
-    // eight heads' q and the tile's page numbers (looked at below the length only)
-    uint4 q0[NI / 2];
-    const uint4 *const qp = reinterpret_cast<const uint4 *>(a.q + ((int64_t)bj * a.rows.Hq + h * group + min(g, group - 1)) * D);
+    const int Hkv = a.pool.Hkv, group = a.rows.Hq / Hkv, ps = a.pool.page_shift;
+    const unsigned step = gridDim.x * 4;
+    // a unit's place, and the page numbers of its tile (looked at below the length only)
+    struct Place {
+        unsigned item, bj;
+        int tile, h, b, j, id[2];
+    };
+    auto place = [&](unsigned unit) {
+        Place p;
+        p.item = unit / (unsigned)tiles;
+        p.bj = p.item / (unsigned)Hkv;
+        p.tile = (int)(unit - p.item * tiles);
+        p.h = (int)(p.item - p.bj * Hkv);
+        p.b = (int)(p.bj / (unsigned)a.rows.n);
+        p.j = (int)(p.bj - (unsigned)p.b * a.rows.n);
 #pragma unroll
-    for (int i = 0; i < NI / 2; ++i) q0[i] = __ldg(qp + i * 4 + c);
-    int id[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int lp = tile * 16 + r * 8 + g;
-        id[r] = lp < a.pool.max_pages ? __ldg(a.pool.pages + (int64_t)b * a.pool.max_pages + lp) : -1;
-    }
-    const int len = kv4_len(a.pool, b);
-    const int lim = kv4_limit(a.rows, b, j, len);
-    const int ps = a.pool.page_shift;
-    const int pages = (int)(((int64_t)lim + (1 << ps) - 1) >> ps);
-    if (tile * 16 >= pages) return;
-    uint4 w[2][NI];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int lp = tile * 16 + r * 8 + g;
-        if (lp >= pages) {
-            id[r] = -1;
-        } else if (id[r] < 0 || id[r] >= a.pool.n_pages) {
-            kv4_report(a.pool.err);
-            id[r] = -1;
+        for (int r = 0; r < 2; ++r) {
+            const int lp = p.tile * 16 + r * 8 + g;
+            p.id[r] = lp < a.pool.max_pages ? __ldg(a.pool.pages + (int64_t)p.b * a.pool.max_pages + lp) : -1;
         }
-        const uint4 *p = reinterpret_cast<const uint4 *>(a.summary + ((int64_t)(id[r] < 0 ? 0 : id[r]) * Hkv + h) * 2 * D);
+        return p;
+    };
+    unsigned unit = blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (unit >= units) return;
+    Place p = place(unit);
+    for (;;) {
+        const int len = kv4_len(a.pool, p.b);
+        const int lim = kv4_limit(a.rows, p.b, p.j, len);
+        const int pages = (int)(((int64_t)lim + (1 << ps) - 1) >> ps);
+        const bool any = p.tile * 16 < pages;
+        uint4 w[2][NI];
+        const uint4 *const q =
+            reinterpret_cast<const uint4 *>(a.q + ((int64_t)p.bj * a.rows.Hq + p.h * group + min(g, group - 1)) * D);
+        uint4 q0[NI / 2];
+        if (any) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) w[r][i] = id[r] >= 0 ? __ldg(p + i * 4 + c) : make_uint4(0, 0, 0, 0);
-    }
-    float best[2] = {-INFINITY, -INFINITY};
-    bool nan[2] = {false, false};
-    for (int h0 = 0; h0 < group; h0 += 8) {
-        // heads past the group repeat its last one: their columns are not looked at
-        const uint4 *q = reinterpret_cast<const uint4 *>(a.q + ((int64_t)bj * a.rows.Hq + h * group + min(h0 + g, group - 1)) * D);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < NI / 2; ++i) q0[i] = __ldg(q + i * 4 + c);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const bool neg = i < NI / 2;
-            const uint4 x = h0 == 0 ? q0[neg ? i : i - NI / 2] : __ldg(q + (neg ? i : i - NI / 2) * 4 + c);
-            mma16816_bf16(acc, w[0][i].x, w[1][i].x, w[0][i].y, w[1][i].y, half_line(x.x, neg), half_line(x.y, neg));
-            mma16816_bf16(acc, w[0][i].z, w[1][i].z, w[0][i].w, w[1][i].w, half_line(x.z, neg), half_line(x.w, neg));
-        }
+            for (int r = 0; r < 2; ++r) {
+                const int lp = p.tile * 16 + r * 8 + g;
+                int id = p.id[r];
+                if (lp >= pages) {
+                    id = -1;
+                } else if (id < 0 || id >= a.pool.n_pages) {
+                    kv4_report(a.pool.err);
+                    id = -1;
+                }
+                const uint4 *s = reinterpret_cast<const uint4 *>(a.summary + ((int64_t)(id < 0 ? 0 : id) * Hkv + p.h) * 2 * D);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (h0 + 2 * c + (e & 1) < group) {
-                best[e >> 1] = fmaxf(best[e >> 1], acc[e]);
-                nan[e >> 1] |= isnan(acc[e]);
+                for (int i = 0; i < NI; ++i) w[r][i] = id >= 0 ? __ldg(s + i * 4 + c) : make_uint4(0, 0, 0, 0);
             }
-    }
+        }
+        const Place now = p;
+        unit += step;
+        const bool more = unit < units;
+        if (more) p = place(unit);
+        if (any) {
+            float best[2] = {-INFINITY, -INFINITY};
+            bool nan[2] = {false, false};
+            for (int h0 = 0; h0 < group; h0 += 8) {
+                // heads past the group repeat its last one: their columns are not looked at
+                const uint4 *qh = q + (int64_t)(min(h0 + g, group - 1) - min(g, group - 1)) * (D / 8);
+                float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};   // two chains
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        float v = nan[r] ? INFINITY : best[r];   // a page whose bound is not a number comes first
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-        const int lp = tile * 16 + r * 8 + g;
-        if (c == 0 && lp < pages) a.scores[(int64_t)item * a.pool.max_pages + lp] = v;
+                for (int i = 0; i < NI; ++i) {
+                    const bool neg = i < NI / 2;
+                    const int x4 = neg ? i : i - NI / 2;
+                    const uint4 x = h0 == 0 ? q0[x4] : __ldg(qh + x4 * 4 + c);
+                    mma16816_bf16(acc, w[0][i].x, w[1][i].x, w[0][i].y, w[1][i].y, half_line(x.x, neg), half_line(x.y, neg));
+                    mma16816_bf16(acc2, w[0][i].z, w[1][i].z, w[0][i].w, w[1][i].w, half_line(x.z, neg), half_line(x.w, neg));
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (h0 + 2 * c + (e & 1) < group) {
+                        const float sum = acc[e] + acc2[e];
+                        best[e >> 1] = fmaxf(best[e >> 1], sum);
+                        nan[e >> 1] |= isnan(sum);
+                    }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float v = nan[r] ? INFINITY : best[r];   // a page whose bound is not a number comes first
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                const int lp = now.tile * 16 + r * 8 + g;
+                if (c == 0 && lp < pages) a.scores[(int64_t)now.item * a.pool.max_pages + lp] = v;
+            }
+        }
+        if (!more) return;
     }
 }
 
@@ -119,7 +145,7 @@ __device__ __forceinline__ uint32_t page_key(const Kv4SelectArgs &a, const float
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int SEL_THREADS = 512;
+constexpr int SEL_THREADS = 256;   // 2048 pages: 9.3 us for the two kernels, with 512 9.9
 
 // Sum over the block; red has two halves that calls use in turn, so that one
 // barrier a call is enough.
@@ -191,20 +217,24 @@ __device__ __forceinline__ void take_top(const Kv4SelectArgs &a, const float *sc
         return n;
     };
     const uint32_t want = (uint32_t)a.n_sel;
-    uint32_t thr = 0;
+    uint32_t thr = 0, have = pages;   // pages at or above thr: once that is what is wanted, the bits below do not matter
     if (K > 0) {   // fewer than 2^16 pages: three counts in two sums of halves
-        for (int bit = 30; bit >= 0; bit -= 2) {
+        for (int bit = 30; bit >= 0 && have != want; bit -= 2) {
             uint32_t s12 = at_least(thr | 1u << bit) | at_least(thr | 2u << bit) << 16, s3 = at_least(thr | 3u << bit);
             block_sum2(s12, s3, red, red2, turn);
-            if (s3 >= want) thr |= 3u << bit;
-            else if (s12 >> 16 >= want) thr |= 2u << bit;
-            else if ((s12 & 0xffffu) >= want) thr |= 1u << bit;
+            if (s3 >= want) thr |= 3u << bit, have = s3;
+            else if (s12 >> 16 >= want) thr |= 2u << bit, have = s12 >> 16;
+            else if ((s12 & 0xffffu) >= want) thr |= 1u << bit, have = s12 & 0xffffu;
         }
     } else {
-        for (int bit = 31; bit >= 0; --bit)
-            if (block_sum(at_least(thr | 1u << bit), red, turn) >= want) thr |= 1u << bit;
+        for (int bit = 31; bit >= 0 && have != want; --bit) {
+            const uint32_t s = block_sum(at_least(thr | 1u << bit), red, turn);
+            if (s >= want) thr |= 1u << bit, have = s;
+        }
     }
-    const uint32_t gt = thr == 0xffffffffu ? 0u : at_least(thr + 1), eq = at_least(thr) - gt;
+    // with as many pages at or above thr as are wanted, all of them count as above
+    if (have == want) --thr;
+    const uint32_t gt = thr == 0xffffffffu ? 0u : at_least(thr + 1), eq = have == want ? 0u : at_least(thr) - gt;
     const uint32_t ties = want - block_sum(gt, red, turn);   // pages equal to the threshold that are taken
     uint32_t seen = block_before(eq, red, turn);             // ... that come before this thread's
     uint32_t at = block_before(gt, red, turn) + min(seen, ties);
@@ -238,10 +268,10 @@ __global__ void __launch_bounds__(SEL_THREADS) kv4_top_kernel(Kv4SelectArgs a)
         for (int i = threadIdx.x; i < a.n_sel; i += SEL_THREADS) sel[i] = i < pages ? i : -1;
         return;
     }
-    // with two keys a thread a step is its barrier, with 16 its comparisons
+    // with two keys a thread a step is its barrier, with 32 its comparisons
     if (pages <= 2 * SEL_THREADS) take_top<2>(a, scores, sel, pages, red, red2);
-    else if (pages <= 4 * SEL_THREADS) take_top<4>(a, scores, sel, pages, red, red2);
-    else if (pages <= 16 * SEL_THREADS) take_top<16>(a, scores, sel, pages, red, red2);
+    else if (pages <= 8 * SEL_THREADS) take_top<8>(a, scores, sel, pages, red, red2);
+    else if (pages <= 32 * SEL_THREADS) take_top<32>(a, scores, sel, pages, red, red2);
     else take_top<0>(a, scores, sel, pages, red, red2);
 }
 
@@ -252,8 +282,10 @@ int launch_kv4_select(const Kv4SelectArgs &a, int D, cudaStream_t st)
     const int64_t items = (int64_t)a.rows.B * a.rows.n * a.pool.Hkv;
     const int tiles = (a.pool.max_pages + 15) / 16;
     const int64_t warps = items * tiles;
-    const int64_t grid = (warps + 3) / 4;
-    if (items > 0x7fffffffLL || warps > 0x7fffffffLL) return CP_EUNSUPPORTED;
+    if (items > 0x7fffffffLL || warps > 0x3fffffffLL) return CP_EUNSUPPORTED;
+    // four waves of blocks (16 sequences of up to 1024 pages: both kernels 16.0 us; one
+    // wave, whose warps loop more, 17.9: ragged lengths leave some with little to do)
+    const int64_t grid = min((warps + 3) / 4, (int64_t)sm_count() * 16);
     if (grid > 0) {
         const cudaError_t rc =
             D == 64 ? kv4_launch(kv4_score_kernel<64>, (unsigned)grid, 128, 0, st, a, tiles, (unsigned)warps)
