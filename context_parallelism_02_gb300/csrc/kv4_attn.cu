@@ -40,6 +40,7 @@
 // out, the others leave partial sums that a second kernel joins by log-sum-exp, in
 // the order of the line (no atomics: results repeat bit for bit).  Warps share
 // nothing: each has its own ring of shared-memory stages filled by bulk copies.
+// Short tables of few items take a block per item instead (ALONE).
 namespace cp {
 
 namespace {
@@ -534,13 +535,13 @@ struct Walk {
     }
 };
 
-template <int D>
+template <int D, int W>
 struct Smem {
-    uint8_t ring[WARPS][stages<D>()][NB][Kv4<D>::BYTES];
-    uint64_t full[WARPS][stages<D>()];
+    uint8_t ring[W][stages<D>()][NB][Kv4<D>::BYTES];
+    uint64_t full[W][stages<D>()];
     uint64_t hold;                   // completed by nobody: what the failure path is tested with
-    int slot[WARPS][stages<D>()][NB];   // first slot of the block, or NO_SLOT
-    Walk ahead[WARPS];               // the piece that a warp's copies are issued for
+    int slot[W][stages<D>()][NB];   // first slot of the block, or NO_SLOT
+    Walk ahead[W];               // the piece that a warp's copies are issued for
     int abort, never;
 };
 
@@ -627,11 +628,21 @@ __device__ __forceinline__ uint64_t policy_evict_normal()
     return p;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Shape sh, int warps)
+// The warps' states of a block that has an item to itself.
+template <int D, int NT, int W>
+struct Joined {
+    float o[W][NT * 8][D];
+    float m[W][NT * 8], l[W][NT * 8];
+};
+
+// ALONE: a block per item, its W warps share the item's blocks evenly and join in
+// shared memory, and there is no second kernel (short tables); else the schedule at the
+// top of this file.
+template <int D, int NT, int W, bool ALONE>
+__global__ void __launch_bounds__(W * 32) kv4_attn_kernel(Kv4AttnArgs a, Shape sh, int warps)
 {
     extern __shared__ __align__(128) uint8_t dyn[];
-    Smem<D> &sm = *reinterpret_cast<Smem<D> *>(dyn);
+    Smem<D, W> &sm = *reinterpret_cast<Smem<D, W> *>(dyn);
     constexpr int NS = stages<D>(), NG = Kv4<D>::NG;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     if (lane < NS) mbar_init(smem_u32(&sm.full[warp][lane]), NB);
@@ -642,55 +653,67 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     fence_mbar_init();
     kv4_begin();
     {   // what the chain of loads below will need, on its way to L2
-        const int64_t line = ((int64_t)blockIdx.x * (WARPS * 32) + threadIdx.x) * 128;
+        const int64_t line = ((int64_t)blockIdx.x * (W * 32) + threadIdx.x) * 128;
         prefetch(a.pool.pages, line, (int64_t)a.rows.B * a.pool.max_pages * 4);
         prefetch(a.q, line, (int64_t)a.rows.B * a.rows.n * a.rows.Hq * D * 2);
         if (a.sel) prefetch(a.sel, line, (int64_t)a.rows.B * a.rows.n * a.pool.Hkv * a.n_sel * 4);
     }
-    // where the stretch begins: the extents of all items, then the sequence
-    const int B = a.rows.B;
-    int64_t all = 0;
-    int one = 0;                              // the lane's sequence of the stretch of 32 in hand
-    for (int b = lane; b < B; b += 32) {
-        one = item_blocks(a, b) + PAD;
-        all += one;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    all *= sh.per_batch;
-    const Cuts cuts(all, warps);
-    const int self = blockIdx.x * WARPS + warp;
-    __syncthreads();                          // sm.abort is set
-    if (self >= cuts.n) return;
-    const int64_t f0 = cuts.begin(self);
     Walk at;
-    int64_t rest = 0;
-    for (int b0 = 0;; b0 += 32) {
-        const int b = b0 + lane;
-        if (B > 32) one = b < B ? item_blocks(a, b) + PAD : 0;
-        else if (b >= B) one = 0;
-        int64_t upto = one;
+    int self = 0;
+    if constexpr (ALONE) {
+        at.b = blockIdx.x / (unsigned)sh.per_batch;
+        at.i = blockIdx.x - at.b * sh.per_batch;
+        at.nb = item_blocks(a, at.b);
+        const int stagesful = (at.nb + NB - 1) / NB;
+        at.t0 = stagesful * warp / W * NB;
+        at.t1 = min(stagesful * (warp + 1) / W * NB, at.nb);
+        at.left = at.t1 - at.t0;
+        __syncthreads();                      // sm.abort is set
+    } else {
+        // where the stretch begins: the extents of all items, then the sequence
+        const int B = a.rows.B;
+        int64_t all = 0;
+        int one = 0;                              // the lane's sequence of the stretch of 32 in hand
+        for (int b = lane; b < B; b += 32) {
+            one = item_blocks(a, b) + PAD;
+            all += one;
+        }
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
+        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        all *= sh.per_batch;
+        const Cuts cuts(all, warps);
+        self = blockIdx.x * W + warp;
+        __syncthreads();                          // sm.abort is set
+        if (self >= cuts.n) return;
+        const int64_t f0 = cuts.begin(self);
+        int64_t rest = 0;
+        for (int b0 = 0;; b0 += 32) {
+            const int b = b0 + lane;
+            if (B > 32) one = b < B ? item_blocks(a, b) + PAD : 0;
+            else if (b >= B) one = 0;
+            int64_t upto = one;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const int64_t here = __shfl_sync(0xffffffffu, upto, 31) * sh.per_batch;
+            if (f0 - rest >= here) {
+                rest += here;
+                continue;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, f0 - rest >= upto * sh.per_batch);
+            const int x = __popc(past);           // sequences of these 32 that end before f0
+            at.b = b0 + x;
+            at.nb = __shfl_sync(0xffffffffu, one, x) - PAD;
+            rest = f0 - rest - __shfl_sync(0xffffffffu, upto - one, x) * sh.per_batch;
+            break;
         }
-        const int64_t here = __shfl_sync(0xffffffffu, upto, 31) * sh.per_batch;
-        if (f0 - rest >= here) {
-            rest += here;
-            continue;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, f0 - rest >= upto * sh.per_batch);
-        const int x = __popc(past);           // sequences of these 32 that end before f0
-        at.b = b0 + x;
-        at.nb = __shfl_sync(0xffffffffu, one, x) - PAD;
-        rest = f0 - rest - __shfl_sync(0xffffffffu, upto - one, x) * sh.per_batch;
-        break;
+        at.i = (int)divide(rest, at.nb + PAD);
+        at.t0 = (int)(rest - (int64_t)at.i * (at.nb + PAD));
+        at.left = cuts.begin(self + 1) - f0;
+        at.cut();
     }
-    at.i = (int)divide(rest, at.nb + PAD);
-    at.t0 = (int)(rest - (int64_t)at.i * (at.nb + PAD));
-    at.left = cuts.begin(self + 1) - f0;
-    at.cut();
     RawRows<D, NT> raw;
     bool first = true;
     fetch_rows<D, NT>(a, sh, decode_item(sh, a.pool.Hkv, at.b, at.i), raw);
@@ -772,19 +795,8 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
     __syncwarp();
     // a bound this short is the test hook's; the waits below can be met before it
     if (a.limit_ns < SHORT_WAIT_NS) dead = !waitw(smem_u32(&sm.hold), 0, wc);
-    for (; at.valid(); at.next(a, sh.per_batch)) {
-        if (at.t0 >= at.t1) {                // the padding of an item that another warp has done
-            first = false;
-            continue;
-        }
-        const Item it = decode_item(sh, a.pool.Hkv, at.b, at.i);
-        Rows<D, NT> r;
-        if (!first) fetch_rows<D, NT>(a, sh, it, raw);
-        first = false;
-        make_rows<D, NT>(a, sh, it, kv4_len(a.pool, at.b), raw, r);
-        State<D, NT> s;
-        s.clear();
-        for (int t = at.t0; t < at.t1; t += NB) {
+    auto take = [&](const Rows<D, NT> &r, State<D, NT> &s, int blocks) {   // the next blocks of the ring
+        for (int t = 0; t < blocks; t += NB) {
             if (!dead && !waitw(smem_u32(&sm.full[warp][get]), phase, wc)) dead = true;
             if (dead) break;
             int slot[NB];
@@ -801,6 +813,75 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
             issue();
             __syncwarp();                    // ... and the slots are written before the next round reads them
         }
+    };
+    // after a wait that ran out: copies that were issued land before the block ends
+    auto drain = [&] {
+        const WaitCtl last{a.pool.err, &sm.never, a.drain_ns};
+        for (; taken < issued; ++taken) {
+            waitw(smem_u32(&sm.full[warp][get]), phase, last);
+            if (++get == NS) get = 0, phase ^= 1;
+        }
+    };
+    if constexpr (ALONE) {
+        Joined<D, NT, W> &jn = *reinterpret_cast<Joined<D, NT, W> *>(dyn + (sizeof(Smem<D, W>) + 15) / 16 * 16);
+        const Item it = decode_item(sh, a.pool.Hkv, at.b, at.i);
+        Rows<D, NT> r;
+        make_rows<D, NT>(a, sh, it, kv4_len(a.pool, at.b), raw, r);
+        State<D, NT> s;
+        s.clear();
+        take(r, s, at.t1 - at.t0);
+        drain();
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = s.l[u][e];
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                const int row = u * 8 + 2 * c + e;
+                if (g == 0) jn.m[warp][row] = s.m[u][e], jn.l[warp][row] = l;
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr)
+                    *reinterpret_cast<float4 *>(&jn.o[warp][row][32 * gr + 4 * g]) = make_float4(
+                        s.o[u][2 * gr][e], s.o[u][2 * gr][e + 2], s.o[u][2 * gr + 1][e], s.o[u][2 * gr + 1][e + 2]);
+            }
+        __syncthreads();
+        for (int x = threadIdx.x; x < NT * 8 * (D / 4); x += W * 32) {
+            const int row = x / (D / 4), d4 = x % (D / 4), rr = it.tile * NT * 8 + row;
+            if (rr >= sh.rows) continue;
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) m = fmaxf(m, jn.m[w][row]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float f = jn.m[w][row] == m ? 1.f : ex2(jn.m[w][row] - m);
+                l = fmaf(f, jn.l[w][row], l);
+                const float4 v = *reinterpret_cast<const float4 *>(&jn.o[w][row][d4 * 4]);
+                o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+            }
+            const int j = it.j0 + rr / sh.group, head = it.h * sh.group + rr % sh.group;
+            const bool empty = l == 0.f;
+            const float inv = empty ? 0.f : 1.f / l;
+            put_out(a, (((int64_t)it.b * a.rows.n + j) * a.rows.Hq + head) * D + d4 * 4,
+                    make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+            if (d4 == 0) a.lse[((int64_t)it.b * a.rows.Hq + head) * a.rows.n + j] = empty ? -INFINITY : fmaf(m, LN2, logf(l));
+        }
+        return;
+    }
+    for (; at.valid(); at.next(a, sh.per_batch)) {
+        if (at.t0 >= at.t1) {                // the padding of an item that another warp has done
+            first = false;
+            continue;
+        }
+        const Item it = decode_item(sh, a.pool.Hkv, at.b, at.i);
+        Rows<D, NT> r;
+        if (!first) fetch_rows<D, NT>(a, sh, it, raw);
+        first = false;
+        make_rows<D, NT>(a, sh, it, kv4_len(a.pool, at.b), raw, r);
+        State<D, NT> s;
+        s.clear();
+        take(r, s, at.t1 - at.t0);
         const bool whole = at.t0 == 0 && at.t1 == at.nb;
         float *part = static_cast<float *>(a.ws) + (2 * (int64_t)self + (at.t0 == 0 ? 1 : 0)) * Part<D, NT>::FLOATS;
 #pragma unroll
@@ -832,12 +913,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_attn_kernel(Kv4AttnArgs a, Sha
                 if (g == 0) a.lse[((int64_t)it.b * a.rows.Hq + head) * a.rows.n + j] = empty ? -INFINITY : fmaf(m, LN2, logf(l));
             }
     }
-    // after a wait that ran out: copies that were issued land before the block ends
-    const WaitCtl drain{a.pool.err, &sm.never, a.drain_ns};
-    for (; taken < issued; ++taken) {
-        waitw(smem_u32(&sm.full[warp][get]), phase, drain);
-        if (++get == NS) get = 0, phase ^= 1;
-    }
+    drain();
 }
 
 // Joins the pieces of the items that were cut: one block per output row.  The
@@ -934,12 +1010,17 @@ __global__ void __launch_bounds__(JW * 32) kv4_join_kernel(Kv4AttnArgs a, Shape 
     if (threadIdx.x == 0) a.lse[((int64_t)b * a.rows.Hq + head) * a.rows.n + j] = empty ? -INFINITY : fmaf(m, LN2, logf(l));
 }
 
+// Short tables: a block per item where the items fit the SMs at once.  8 items of 512
+// tokens take 7.0 us (by stretches and join 8.4), of 1024 9.4 (8.5); 128 items of 512
+// 7.3 us (14.0), of 1024 9.9 (15.3), of 2048 14.7 (18.5).
+constexpr int ALONE_WARPS = 8, ALONE_BLOCKS = 48, ALONE_BLOCKS_MANY = 128;
 constexpr int MAX_ROWS = 2560 * 8;   // rows of warps' parts that the workspace has room for (twice)
 
 template <int D, int NT>
 int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
 {
-    constexpr int smem = sizeof(Smem<D>);
+    constexpr int smem = sizeof(Smem<D, WARPS>);
+    constexpr int alone = (sizeof(Smem<D, ALONE_WARPS>) + 15) / 16 * 16 + sizeof(Joined<D, NT, ALONE_WARPS>);
     // one block of the join per output row
     const int64_t joins = (int64_t)a.rows.B * (sh.per_batch / sh.tiles) * sh.rows;
     if (joins > 0x7fffffffLL) return CP_EUNSUPPORTED;
@@ -951,9 +1032,11 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
     int fill = fills[dev].load(std::memory_order_acquire);
     if (!fill) {
         int resident = 0;
-        if (cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kv4_attn_kernel<D, NT>, WARPS * 32, smem) != cudaSuccess ||
-            resident < 1)
+        if (cudaFuncSetAttribute(kv4_attn_kernel<D, NT, WARPS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kv4_attn_kernel<D, NT, WARPS, false>, WARPS * 32, smem) != cudaSuccess ||
+            resident < 1 ||
+            cudaFuncSetAttribute(kv4_attn_kernel<D, NT, ALONE_WARPS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, alone) !=
+                cudaSuccess)
             return CP_ECUDA;
         fill = resident * sm_count();
         fills[dev].store(fill, std::memory_order_release);
@@ -962,10 +1045,16 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
     // an upper bound of the line from the sizes alone
     const int64_t most = a.sel ? (int64_t)a.n_sel << (a.pool.page_shift - 4)
                                : ((int64_t)a.pool.max_pages << (a.pool.page_shift - 4));
-    const int64_t line = ((most > 0 ? most : 1) + PAD) * a.rows.B * sh.per_batch;
+    const int64_t items = (int64_t)a.rows.B * sh.per_batch;
+    if (items <= sm_count() && most <= (2 * items >= sm_count() ? ALONE_BLOCKS_MANY : ALONE_BLOCKS)) {
+        const cudaError_t rc = kv4_launch(kv4_attn_kernel<D, NT, ALONE_WARPS, true>, (unsigned)items,
+                                          ALONE_WARPS * 32, alone, st, a, sh, 0);
+        return rc == cudaSuccess ? CP_OK : CP_ECUDA;
+    }
+    const int64_t line = ((most > 0 ? most : 1) + PAD) * items;
     const int grid = (int)min(ctas, (line + LEAST * WARPS - 1) / (LEAST * WARPS));
     const int warps = grid * WARPS;
-    if (kv4_launch(kv4_attn_kernel<D, NT>, (unsigned)grid, WARPS * 32, smem, st, a, sh, warps) != cudaSuccess)
+    if (kv4_launch(kv4_attn_kernel<D, NT, WARPS, false>, (unsigned)grid, WARPS * 32, smem, st, a, sh, warps) != cudaSuccess)
         return CP_ECUDA;
     // many warps where a row is cut into many pieces
     const int64_t cuts = warps / ((int64_t)a.rows.B * sh.per_batch);   // pieces of an item, about

@@ -685,6 +685,37 @@ def test_attn_many_sequences_many_rows(cuda_dev, B, n, Hq, Hkv, D, page, L):
     check_reference(out, lse, q, kr, vr, lim, 1 / math.sqrt(D))
 
 
+@pytest.mark.parametrize("B,Hkv,pages_of_64", [(1, 1, 11), (1, 1, 13), (19, 4, 30), (19, 4, 33), (160, 1, 2)])
+def test_attn_on_both_sides_of_a_block_per_item(cuda_dev, B, Hkv, pages_of_64):
+    """Table sizes and item counts around the choice between a block per item and stretches, ragged lengths in both;
+    a bounded wait in a block that joins in shared memory."""
+    L = pages_of_64 * 64
+    rng = np.random.default_rng(L)
+    lens = rng.integers(0, L + 1, B).astype(np.int32)
+    lens[0] = L
+    pages, P = table(rng, B, pages_of_64)
+    cache = torch.full((P, Hkv, 64, 160), 255, dtype=torch.uint8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(L)
+    k, v = (torch.randn(B, L, Hkv, 128, generator=g, device="cuda").bfloat16() for _ in range(2))
+    api.kv4_append(k, v, cache, dev(pages), dev(np.zeros(B, np.int32)), n_new=dev(lens))
+    q = torch.randn(B, 2, 3 * Hkv, 128, generator=g, device="cuda").bfloat16()
+    out, lse = api.kv4_attn(q, cache, dev(pages), dev(lens))
+    kr, vr = api.kv4_gather(cache, dev(pages), dev(lens), L, dtype=torch.float32)
+    ok()
+    lim = torch.from_numpy(np.maximum(lens[:, None] - 1 + np.arange(2), 0))
+    check_reference(out, lse, q, kr, vr, lim, 1 / math.sqrt(128))
+    try:
+        api.cp_debug_set_wait_limit(1)
+        api.kv4_attn(q, cache, dev(pages), dev(lens))
+        torch.cuda.synchronize()
+        assert api.cp_get_error() == _lib.CP_ETIMEOUT
+    finally:
+        api.cp_debug_set_wait_limit(0)
+    again, _ = api.kv4_attn(q, cache, dev(pages), dev(lens))
+    ok()
+    assert torch.equal(out, again)
+
+
 def test_attn_sizes_of_scores_and_queries(cuda_dev):
     """Queries from 2^-100 to 2^40 in one tile, rows of zeros, keys of 2^-10 to 2^8: each row scaled by itself."""
     rng = np.random.default_rng(19)
