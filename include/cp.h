@@ -403,7 +403,8 @@ int ring_attn_bwd_noalloc(const void *q, const void *k, const void *v, const voi
  *   whose first slot is written starts afresh).
  * Quantisation of a group of 32: s = fp16((max - min) fp32(1/15)), m = fp16(min),
  * code = rint((y - m) / s) held to 0..15, in fp32, halves to even; values beyond
- * +-65408 count as that, and a group with a value that is not finite is held as NaN.
+ * +-65408 count as that, a group with a value that is not finite is held as NaN,
+ * and differences below fp16's smallest step (6e-8) are lost.
  * Within one call no two sequences may write the same page.
  * Errors: CP_EINVAL (null pointer, misalignment, sizes, Hq % Hkv), CP_EUNSUPPORTED
  * (D, dtype, page), CP_ECUDA.
