@@ -1012,8 +1012,10 @@ __global__ void __launch_bounds__(JW * 32) kv4_join_kernel(Kv4AttnArgs a, Shape 
 
 // Short tables: a block per item where the items fit the SMs at once.  8 items of 512
 // tokens take 7.0 us (by stretches and join 8.4), of 1024 9.4 (8.5); 128 items of 512
-// 7.3 us (14.0), of 1024 9.9 (15.3), of 2048 14.7 (18.5).
-constexpr int ALONE_WARPS = 8, ALONE_BLOCKS = 48, ALONE_BLOCKS_MANY = 128;
+// 7.3 us (14.0), of 1024 9.9 (15.3), of 2048 14.7 (18.5).  More items than SMs: blocks
+// of four warps as long as they fit at once; 256 items of 512 tokens 11.3 us (15.6), of
+// 1024 17.1 (19.9), of 2048 29.0 (25.1), 448 of 1024 18.3 (26.7).
+constexpr int ALONE_WARPS = 8, ALONE_BLOCKS = 48, ALONE_BLOCKS_MANY = 128, ALONE_BLOCKS_FULL = 64;
 constexpr int MAX_ROWS = 2560 * 8;   // rows of warps' parts that the workspace has room for (twice)
 
 template <int D, int NT>
@@ -1021,24 +1023,30 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
 {
     constexpr int smem = sizeof(Smem<D, WARPS>);
     constexpr int alone = (sizeof(Smem<D, ALONE_WARPS>) + 15) / 16 * 16 + sizeof(Joined<D, NT, ALONE_WARPS>);
+    constexpr int alone4 = (sizeof(Smem<D, WARPS>) + 15) / 16 * 16 + sizeof(Joined<D, NT, WARPS>);
     // one block of the join per output row
     const int64_t joins = (int64_t)a.rows.B * (sh.per_batch / sh.tiles) * sh.rows;
     if (joins > 0x7fffffffLL) return CP_EUNSUPPORTED;
     // blocks of a grid that just fills the device, worked out once per device
     constexpr int MAX_DEV = 64;
-    static std::atomic<int> fills[MAX_DEV];
+    static std::atomic<int> fills[MAX_DEV], fills4[MAX_DEV];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEV) return CP_ECUDA;
     int fill = fills[dev].load(std::memory_order_acquire);
     if (!fill) {
-        int resident = 0;
+        int resident = 0, resident4 = 0;
         if (cudaFuncSetAttribute(kv4_attn_kernel<D, NT, WARPS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kv4_attn_kernel<D, NT, WARPS, false>, WARPS * 32, smem) != cudaSuccess ||
             resident < 1 ||
             cudaFuncSetAttribute(kv4_attn_kernel<D, NT, ALONE_WARPS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, alone) !=
+                cudaSuccess ||
+            cudaFuncSetAttribute(kv4_attn_kernel<D, NT, WARPS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, alone4) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident4, kv4_attn_kernel<D, NT, WARPS, true>, WARPS * 32, alone4) !=
                 cudaSuccess)
             return CP_ECUDA;
         fill = resident * sm_count();
+        fills4[dev].store(resident4 * sm_count(), std::memory_order_relaxed);
         fills[dev].store(fill, std::memory_order_release);
     }
     const int64_t ctas = min(fill, MAX_ROWS / (NT * 8 * WARPS));
@@ -1049,6 +1057,11 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
     if (items <= sm_count() && most <= (2 * items >= sm_count() ? ALONE_BLOCKS_MANY : ALONE_BLOCKS)) {
         const cudaError_t rc = kv4_launch(kv4_attn_kernel<D, NT, ALONE_WARPS, true>, (unsigned)items,
                                           ALONE_WARPS * 32, alone, st, a, sh, 0);
+        return rc == cudaSuccess ? CP_OK : CP_ECUDA;
+    }
+    if (items > sm_count() && items <= fills4[dev].load(std::memory_order_relaxed) && most <= ALONE_BLOCKS_FULL) {
+        const cudaError_t rc =
+            kv4_launch(kv4_attn_kernel<D, NT, WARPS, true>, (unsigned)items, WARPS * 32, alone4, st, a, sh, 0);
         return rc == cudaSuccess ? CP_OK : CP_ECUDA;
     }
     const int64_t line = ((most > 0 ? most : 1) + PAD) * items;

@@ -685,8 +685,9 @@ def test_attn_many_sequences_many_rows(cuda_dev, B, n, Hq, Hkv, D, page, L):
     check_reference(out, lse, q, kr, vr, lim, 1 / math.sqrt(D))
 
 
-@pytest.mark.parametrize("B,Hkv,pages_of_64", [(1, 1, 11), (1, 1, 13), (19, 4, 30), (19, 4, 33), (160, 1, 2)])
-def test_attn_on_both_sides_of_a_block_per_item(cuda_dev, B, Hkv, pages_of_64):
+@pytest.mark.parametrize("B,Hkv,pages_of_64,n", [(1, 1, 11, 2), (1, 1, 13, 2), (19, 4, 30, 2), (19, 4, 33, 2), (160, 1, 2, 2),
+                                                 (40, 4, 16, 2), (40, 4, 17, 2), (50, 4, 9, 5), (90, 4, 3, 5), (230, 2, 3, 1)])
+def test_attn_on_both_sides_of_a_block_per_item(cuda_dev, B, Hkv, pages_of_64, n):
     """Table sizes and item counts around the choice between a block per item and stretches, ragged lengths in both;
     a bounded wait in a block that joins in shared memory."""
     L = pages_of_64 * 64
@@ -698,11 +699,11 @@ def test_attn_on_both_sides_of_a_block_per_item(cuda_dev, B, Hkv, pages_of_64):
     g = torch.Generator(device="cuda").manual_seed(L)
     k, v = (torch.randn(B, L, Hkv, 128, generator=g, device="cuda").bfloat16() for _ in range(2))
     api.kv4_append(k, v, cache, dev(pages), dev(np.zeros(B, np.int32)), n_new=dev(lens))
-    q = torch.randn(B, 2, 3 * Hkv, 128, generator=g, device="cuda").bfloat16()
+    q = torch.randn(B, n, 3 * Hkv, 128, generator=g, device="cuda").bfloat16()
     out, lse = api.kv4_attn(q, cache, dev(pages), dev(lens))
     kr, vr = api.kv4_gather(cache, dev(pages), dev(lens), L, dtype=torch.float32)
     ok()
-    lim = torch.from_numpy(np.maximum(lens[:, None] - 1 + np.arange(2), 0))
+    lim = torch.from_numpy(np.maximum(lens[:, None] - (n - 1) + np.arange(n), 0))
     check_reference(out, lse, q, kr, vr, lim, 1 / math.sqrt(128))
     try:
         api.cp_debug_set_wait_limit(1)
