@@ -74,20 +74,28 @@ __device__ __forceinline__ uint8_t *kv4_block(const Kv4Pool &c, int id, int h, i
 }
 
 // Every kernel of the cache is launched so that its blocks may start while the
-// kernel before it on the stream ends (kv4_launch), and begins with this: its own
-// successor may do the same, and nothing that an earlier kernel wrote is read before
-// that kernel is complete and its writes are visible.
+// kernel before it on the stream ends (kv4_launch).  kv4_trigger lets its own successor
+// do the same, as soon as every block has called it; behind kv4_wait the kernel before
+// it is complete and its writes are visible.  A kernel that triggers first says nothing
+// about its predecessors: its successor must wait before it reads anything.
+__device__ __forceinline__ void kv4_trigger() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void kv4_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void kv4_begin()
 {
-    asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    kv4_trigger();
+    kv4_wait();
 }
 
-// Length of sequence b, held inside the page table's reach.
+// Length of sequence b, held inside the page table's reach.  EARLY: by a kernel that has
+// not waited yet, whose predecessor triggered behind its own wait.
+template <bool EARLY = false>
 __device__ __forceinline__ int kv4_len(const Kv4Pool &c, int b)
 {
     const int64_t cap = (int64_t)c.max_pages << c.page_shift;
-    int64_t len = __ldg(c.lens + b);
+    int got;
+    if (EARLY) asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(got) : "l"(c.lens + b) : "memory");
+    else got = __ldg(c.lens + b);
+    int64_t len = got;
     if (len < 0 || len > cap) {
         kv4_report(c.err);
         len = len < 0 ? 0 : cap;

@@ -377,8 +377,8 @@ int ring_attn_bwd_noalloc(const void *q, const void *k, const void *v, const voi
  * for them and can be captured in a graph.  An entry outside its range is
  * therefore not an error of the call: the kernels skip what it names and record
  * CP_ECACHE (cp_get_error).
- * The kernels may be scheduled while the one before them on the stream ends; they
- * read and write nothing before it is complete.
+ * A call's kernels may be scheduled while what is before the call on the stream ends;
+ * they read and write nothing before that is complete.
  */
 
 /*
