@@ -58,7 +58,7 @@ __device__ __forceinline__ void kv4_report(unsigned *err) { atomicCAS(err, 0u, E
 __device__ __forceinline__ int kv4_page(const Kv4Pool &c, int b, int64_t lp)
 {
     int id = -1;
-    if (lp >= 0 && lp < c.max_pages) id = __ldg(c.pages + (int64_t)b * c.max_pages + lp);
+    if (lp >= 0 && lp < c.max_pages) id = c.pages[(int64_t)b * c.max_pages + lp];
     if (id < 0 || id >= c.n_pages) {
         kv4_report(c.err);
         return -1;
@@ -78,6 +78,9 @@ __device__ __forceinline__ uint8_t *kv4_block(const Kv4Pool &c, int id, int h, i
 // do the same, as soon as every block has called it; behind kv4_wait the kernel before
 // it is complete and its writes are visible.  A kernel that triggers first says nothing
 // about its predecessors: its successor must wait before it reads anything.
+// What the kernels read may be written while they are already resident, so no load takes
+// the read-only path (ld.global.nc asks for data that nobody writes while the kernel
+// lives, and is not ordered behind the wait); plain loads are.
 __device__ __forceinline__ void kv4_trigger() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void kv4_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void kv4_begin()
@@ -94,7 +97,7 @@ __device__ __forceinline__ int kv4_len(const Kv4Pool &c, int b)
     const int64_t cap = (int64_t)c.max_pages << c.page_shift;
     int got;
     if (EARLY) asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(got) : "l"(c.lens + b) : "memory");
-    else got = __ldg(c.lens + b);
+    else got = c.lens[b];
     int64_t len = got;
     if (len < 0 || len > cap) {
         kv4_report(c.err);
@@ -152,7 +155,7 @@ struct Kv4Rows {
 __device__ __forceinline__ int kv4_limit(const Kv4Rows &r, int b, int j, int len)
 {
     int64_t lim = len;
-    if (r.vis) lim = __ldg(r.vis + (int64_t)b * r.n + j);
+    if (r.vis) lim = r.vis[(int64_t)b * r.n + j];
     else if (r.causal) lim = (int64_t)len - (r.n - 1) + j;
     return (int)(lim < 0 ? 0 : lim > len ? len : lim);
 }

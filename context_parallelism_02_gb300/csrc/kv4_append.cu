@@ -26,11 +26,9 @@ namespace cp {
 
 namespace {
 
-// What a kernel only reads (k, v and the tables, not q, whose rows may be rotated in
-// place) goes through the read-only path, so that loads can move above stores.
 __device__ __forceinline__ void load8(const float *p, float (&x)[8])
 {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
     x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
@@ -38,11 +36,11 @@ __device__ __forceinline__ void load8(const float *p, float (&x)[8])
 // 8 elements as they are in memory
 struct Raw16 { uint4 a; };
 struct Raw32 { float4 a, b; };
-__device__ __forceinline__ void fetch8(const __nv_bfloat16 *p, Raw16 &r) { r.a = __ldg(reinterpret_cast<const uint4 *>(p)); }
+__device__ __forceinline__ void fetch8(const __nv_bfloat16 *p, Raw16 &r) { r.a = *reinterpret_cast<const uint4 *>(p); }
 __device__ __forceinline__ void fetch8(const float *p, Raw32 &r)
 {
-    r.a = __ldg(reinterpret_cast<const float4 *>(p));
-    r.b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    r.a = reinterpret_cast<const float4 *>(p)[0];
+    r.b = reinterpret_cast<const float4 *>(p)[1];
 }
 __device__ __forceinline__ void clear(Raw16 &r) { r.a = make_uint4(0, 0, 0, 0); }
 __device__ __forceinline__ void clear(Raw32 &r) { r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f); }
@@ -114,8 +112,8 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const Kv4AppendArgs &a, i
     if (INTER) {
         if (in) {
             const int64_t at = (int64_t)pos * half + (d0 >> 1);
-            const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
-            const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
+            const float4 cv = *reinterpret_cast<const float4 *>(a.cos + at);
+            const float4 sv = *reinterpret_cast<const float4 *>(a.sin + at);
             const float cs[4] = {cv.x, cv.y, cv.z, cv.w}, sn[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -148,7 +146,7 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const Kv4AppendArgs &a, i
 __device__ __forceinline__ int position(const Kv4AppendArgs &a, int b, int j, int64_t slot)
 {
     if (!a.rot) return 0;
-    const int64_t p = a.positions ? (int64_t)__ldg(a.positions + (int64_t)b * a.n + j) : slot;
+    const int64_t p = a.positions ? (int64_t)a.positions[(int64_t)b * a.n + j] : slot;
     if (p < 0 || p >= a.max_pos) {
         kv4_report(a.pool.err);
         return -1;
@@ -159,7 +157,7 @@ __device__ __forceinline__ int position(const Kv4AppendArgs &a, int b, int j, in
 __device__ __forceinline__ int new_tokens(const Kv4AppendArgs &a, int b)
 {
     if (!a.n_new) return a.n;
-    const int m = __ldg(a.n_new + b);
+    const int m = a.n_new[b];
     return m < 0 ? 0 : m > a.n ? a.n : m;
 }
 
@@ -266,15 +264,15 @@ __device__ __forceinline__ void rotate_q(const Kv4AppendArgs &a, unsigned unit, 
     const int first = (int)(unit - bj * spans) * span * 8;
     const int b = (int)(bj / (unsigned)a.n), j = (int)(bj - (unsigned)b * a.n);
     const bool real = j < new_tokens(a, b);
-    const int pos = real ? position(a, b, j, (int64_t)__ldg(a.pool.lens + b) + j) : -1;
+    const int pos = real ? position(a, b, j, (int64_t)a.pool.lens[b] + j) : -1;
     const bool on = pos >= 0;                       // rows that are not there, or have no angle, are 0
     const bool turn = on && 8 * l < a.rot;
     int da = 8 * l, db = 8 * l + 4;
     if (!INTER && 8 * l < a.rot) da = 4 * l, db = 4 * l + (a.rot >> 1);
     float cs[4], sn[4];
     if (turn) {
-        const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + (int64_t)pos * (a.rot >> 1) + 4 * l));
-        const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + (int64_t)pos * (a.rot >> 1) + 4 * l));
+        const float4 cv = *reinterpret_cast<const float4 *>(a.cos + (int64_t)pos * (a.rot >> 1) + 4 * l);
+        const float4 sv = *reinterpret_cast<const float4 *>(a.sin + (int64_t)pos * (a.rot >> 1) + 4 * l);
         cs[0] = cv.x, cs[1] = cv.y, cs[2] = cv.z, cs[3] = cv.w;
         sn[0] = sv.x, sn[1] = sv.y, sn[2] = sv.z, sn[3] = sv.w;
     }
@@ -401,7 +399,7 @@ __global__ void __launch_bounds__(128, 7) kv4_append_kernel(Kv4AppendArgs a, int
     const int sub = lane & (LPR - 1), d0 = sub * 8, tsub = lane / LPR;
     const unsigned bc = kb / (unsigned)a.pool.Hkv;
     const int h = (int)(kb - bc * a.pool.Hkv), b = (int)(bc / chunks), c = (int)(bc - b * chunks);
-    const int64_t len = __ldg(a.pool.lens + b);
+    const int64_t len = a.pool.lens[b];
     if (len < 0) {
         if (threadIdx.x == 0) kv4_report(a.pool.err);
         return;
@@ -531,7 +529,7 @@ __global__ void __launch_bounds__(128) kv4_gather_kernel(Kv4GatherArgs a, unsign
     const unsigned bx = wid / (unsigned)a.pool.Hkv;
     const int h = (int)(wid - bx * a.pool.Hkv), b = (int)(bx / blocks), x = (int)(bx - b * blocks);
     const int len = kv4_len(a.pool, b);
-    int64_t first = a.start ? (int64_t)__ldg(a.start + b) : 0;
+    int64_t first = a.start ? (int64_t)a.start[b] : 0;
     if (first < 0) {
         if (lane == 0) kv4_report(a.pool.err);
         first = len;   // no slot to read: every row is written as 0

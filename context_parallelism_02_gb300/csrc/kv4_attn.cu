@@ -190,7 +190,7 @@ __device__ __forceinline__ void fetch_rows(const Kv4AttnArgs &a, const Shape &sh
         const int head = it.h * sh.group + (on ? row % sh.group : 0);
         const uint4 *p = reinterpret_cast<const uint4 *>(a.q + (((int64_t)it.b * a.rows.n + j) * a.rows.Hq + head) * D);
 #pragma unroll
-        for (int gr = 0; gr < Kv4<D>::NG; ++gr) raw.w[t][gr] = on ? __ldg(p + gr * 4 + c) : make_uint4(0, 0, 0, 0);
+        for (int gr = 0; gr < Kv4<D>::NG; ++gr) raw.w[t][gr] = on ? p[gr * 4 + c] : make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(W * 32) kv4_attn_kernel(Kv4AttnArgs a, Shape s
             int lp = t >> (ps - 4);
             bool on = true;
             if (a.sel) {
-                lp = __ldg(a.sel + (((int64_t)it.b * a.rows.n + it.j0) * a.pool.Hkv + it.h) * a.n_sel + lp);
+                lp = a.sel[(((int64_t)it.b * a.rows.n + it.j0) * a.pool.Hkv + it.h) * a.n_sel + lp];
                 on = lp >= 0;
                 if (on && lp > (len - 1) >> ps) {   // len 0: -1 >> ps is -1
                     kv4_report(a.pool.err);

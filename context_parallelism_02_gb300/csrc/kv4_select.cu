@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(128) kv4_score_kernel(Kv4SelectArgs a, int til
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int lp = p.tile * 16 + r * 8 + g;
-            p.id[r] = lp < a.pool.max_pages ? __ldg(a.pool.pages + (int64_t)p.b * a.pool.max_pages + lp) : -1;
+            p.id[r] = lp < a.pool.max_pages ? a.pool.pages[(int64_t)p.b * a.pool.max_pages + lp] : -1;
         }
         return p;
     };
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(128) kv4_score_kernel(Kv4SelectArgs a, int til
         uint4 q0[NI / 2];
         if (any) {
 #pragma unroll
-            for (int i = 0; i < NI / 2; ++i) q0[i] = __ldg(q + i * 4 + c);
+            for (int i = 0; i < NI / 2; ++i) q0[i] = q[i * 4 + c];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int lp = p.tile * 16 + r * 8 + g;
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(128) kv4_score_kernel(Kv4SelectArgs a, int til
                 }
                 const uint4 *s = reinterpret_cast<const uint4 *>(a.summary + ((int64_t)(id < 0 ? 0 : id) * Hkv + p.h) * 2 * D);
 #pragma unroll
-                for (int i = 0; i < NI; ++i) w[r][i] = id >= 0 ? __ldg(s + i * 4 + c) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < NI; ++i) w[r][i] = id >= 0 ? s[i * 4 + c] : make_uint4(0, 0, 0, 0);
             }
         }
         const Place now = p;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(128) kv4_score_kernel(Kv4SelectArgs a, int til
                 for (int i = 0; i < NI; ++i) {
                     const bool neg = i < NI / 2;
                     const int x4 = neg ? i : i - NI / 2;
-                    const uint4 x = h0 == 0 ? q0[x4] : __ldg(qh + x4 * 4 + c);
+                    const uint4 x = h0 == 0 ? q0[x4] : qh[x4 * 4 + c];
                     mma16816_bf16(acc, w[0][i].x, w[1][i].x, w[0][i].y, w[1][i].y, half_line(x.x, neg), half_line(x.y, neg));
                     mma16816_bf16(acc2, w[0][i].z, w[1][i].z, w[0][i].w, w[1][i].w, half_line(x.z, neg), half_line(x.w, neg));
                 }
