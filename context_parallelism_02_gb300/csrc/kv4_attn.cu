@@ -328,7 +328,8 @@ __device__ __forceinline__ void raise_max(const float (&x)[NB][NT][4], State<D, 
 #pragma unroll
             for (int i = 1; i < NB; ++i) v = fmaxf(v, fmaxf(x[i][t][e], x[i][t][e + 2]));
             top[t][e] = v;
-            high |= v > s.m[t][e] + 8.f;
+            // the difference, exact for neighbours: m + 8 rounds up to m + 16 where floats lie 16 apart
+            high |= v - s.m[t][e] > 8.f;
         }
     if (!__any_sync(0xffffffffu, high)) return;
 #pragma unroll
