@@ -18,8 +18,12 @@
 // range (bf16's 8 bits fit), so the products are exact and the group's scale
 // multiplies an fp32 sum.  The minima are one more product, m (fp16, exact) with
 // the rows' group sums of q in three fp16 parts.  V's values s n + m are rounded
-// to fp16 (relative 2^-11) and so are the weights P; the row sums are taken over
-// the unrounded fp32 weights.
+// to fp16 (relative 2^-11, below 2^-14 absolute 2^-25) and so are the weights P; the row
+// sums are taken over the unrounded fp32 weights.  Weights are taken relative to a
+// reference at least 7 (in powers of two) below the largest score of the stretch so far, so
+// that the largest is 2^7 to 2^15 and a small one is off by 2^-11 of itself or 2^-32 of
+// the largest: a long tail behind one large score is not lost from O while it
+// counts in the sums.
 //
 // Measured (Hq = 32, Hkv = 8, D = 128): 16 x 32768 tokens 119.8 us, 5.6 TB/s of cache,
 // 108 without the arithmetic; 4 x 32768 37.4 us; 1 x 512 (a block per item) 6.9 us.  Per block 339
@@ -126,7 +130,7 @@ struct Rows {
     int min_limit, max_limit;  // over the tile
 };
 
-// Running state of a warp: m in log2 units (a lazily raised reference, not the
+// Running state of a warp: m in log2 units (a lazily raised reference, 7 to 15 below the
 // maximum), l per lane (its own tokens), O^T accumulators.
 template <int D, int NT>
 struct State {
@@ -314,7 +318,10 @@ __device__ __forceinline__ void block_scores(const uint8_t *blk, const Rows<D, N
     }
 }
 
-// Raises the references m where a score is more than 2^8 above them.
+// The references m lie this far below the largest score when they are raised, and are
+// raised where a score passes them by more than 15: 2^15 is an fp16.
+constexpr float BELOW = 7.f, LAG = 15.f;
+
 template <int D, int NT, int NB>
 __device__ __forceinline__ void raise_max(const float (&x)[NB][NT][4], State<D, NT> &s)
 {
@@ -328,8 +335,8 @@ __device__ __forceinline__ void raise_max(const float (&x)[NB][NT][4], State<D, 
 #pragma unroll
             for (int i = 1; i < NB; ++i) v = fmaxf(v, fmaxf(x[i][t][e], x[i][t][e + 2]));
             top[t][e] = v;
-            // the difference, exact for neighbours: m + 8 rounds up to m + 16 where floats lie 16 apart
-            high |= v - s.m[t][e] > 8.f;
+            // the difference, exact for neighbours: m + 15 rounds up to m + 16 where floats lie 16 apart
+            high |= v - s.m[t][e] > LAG;
         }
     if (!__any_sync(0xffffffffu, high)) return;
 #pragma unroll
@@ -339,7 +346,7 @@ __device__ __forceinline__ void raise_max(const float (&x)[NB][NT][4], State<D, 
             float v = top[t][e];
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-            const float m = fmaxf(s.m[t][e], v);
+            const float m = fmaxf(s.m[t][e], v - BELOW);
             const float f = m == -INFINITY ? 1.f : ex2(s.m[t][e] - m);
             s.m[t][e] = m;
             s.l[t][e] *= f;
@@ -442,7 +449,7 @@ __device__ __forceinline__ void blocks_step(const uint8_t *blk, const int (&slot
         block_scores<D, NT>(blk + i * Kv4<D>::BYTES, r, x[i]);
         cut |= slot[i] > r.min_limit - KV4_BLOCK;
         // rounded here and not fused with the subtraction of m, which is one of these
-        // products: a difference is then at most 8 however large the scores are
+        // products: a difference is then at most LAG however large the scores are
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
