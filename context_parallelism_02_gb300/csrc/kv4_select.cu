@@ -1,9 +1,12 @@
 // kv4_select.cu -- the pages that a query attends to, by a bound on its scores.
 //
-// A page's summary holds, per kv head, the smallest and largest value of every
-// element of its keys.  For any key k of the page and a query row q
+// A page's summary holds, per kv head, the smallest and largest value lo_d, hi_d of every
+// element of its keys.  For any key k within them and a query row q
 //   q.k <= sum_d max(q_d lo_d, q_d hi_d) = sum_d min(q_d, 0) lo_d + max(q_d, 0) hi_d,
-// one product of length 2 D; a page's score is the largest bound of the query
+// one product of length 2 D.  The summary is of the keys before quantisation, rounded to
+// the nearest bf16, so the keys that attention reads may lie 2^-8 of the extremes and half
+// a step of their groups outside: the bound ranks pages, it does not rule any out.
+// A page's score is the largest bound of the query
 // heads that share the kv head.  The n_sel best pages are kept, ties to the lower
 // page, with the first and last pages of the sequence always among them.
 //

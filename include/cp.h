@@ -399,7 +399,8 @@ int ring_attn_bwd_noalloc(const void *q, const void *k, const void *v, const voi
  *   n_new [B] int32 or NULL: tokens of each sequence that are real (a padded
  *   batch; clamped to [0, n]).  The others are not written; their q_out is 0.
  *   summary [n_pages][Hkv][2][D] bf16 or NULL: per page, the smallest and largest
- *   value of every element of its rotated keys; updated for kv4_select (a page
+ *   value of every element of its rotated keys (before quantisation, rounded to
+ *   the nearest bf16); updated for kv4_select (a page
  *   whose first slot is written starts afresh).
  * Quantisation of a group of 32: s = fp16((max - min) fp32(1/15)), m = fp16(min),
  * code = rint((y - m) / s) held to 0..15, in fp32, halves to even; values beyond
@@ -459,7 +460,11 @@ size_t kv4_attn_workspace(int D);
  * kv4_select -- per (b, j, kv head) the n_sel pages that kv4_attn should read.
  * A page's score is max over the kv head's query heads of
  *   sum_d max(q_d lo_d, q_d hi_d)
- * with (lo, hi) its summary: no key of the page has a larger q.k.  Among the pages
+ * with (lo, hi) its summary.  It bounds q.k from above for the page's keys as they were
+ * appended, but for the rounding of (lo, hi) to the nearest bf16: a key's q.k may pass it
+ * by 2^-8 sum_d |q_d| max(|lo_d|, |hi_d|).  The keys that kv4_attn reads are the quantised
+ * ones, and each of their elements may lie half a step of its group, s / 2 (and 2^-11 of
+ * the group's largest magnitudes for the roundings of s and m), further out.  Among the pages
  * that hold a slot the row sees, the first keep_first and the last keep_last are
  * always taken, then the best scores, ties to the lower page (a score that is not
  * a number comes first).

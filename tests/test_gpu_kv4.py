@@ -993,3 +993,37 @@ def test_capture_behind_memsets_copies_and_joined_streams(cuda_dev):
             torch.cuda.synchronize()
             assert all(torch.equal(g, w) for g, w in zip(outs, want)), kind
     ok()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D,page,inter", [(64, 16, False), (128, 64, True)])
+def test_page_ranges_bound_the_scores(cuda_dev, D, page, inter, dtype):
+    """The largest q.k that a page's range allows, against the keys that attention reads: they pass it at most by the
+    bf16 rounding of the range (2^-8 of an element's extremes) and by the quantisation of the key (half a step; the scale's
+    rounding, 15 codes of 2^-11 of it; the minimum's, 2^-11 of it; below fp16's normal range 2^-25 in place of 2^-11)."""
+    rng = np.random.default_rng(26)
+    L, H, rot = 5 * page, 2, D
+    pages, P = table(rng, 1, 5)
+    k = rng.standard_normal((1, L, H, D)) * np.exp2(rng.integers(-6, 7, (1, L, H, 1))) + rng.standard_normal((1, 1, H, D)) * 8
+    k = k.astype(np.float32)
+    k = o.bf16(k) if dtype == torch.bfloat16 else k
+    cos, sin = rope(L, rot)
+    cache, summ = api.kv4_cache(P, H, page, D, summary=True)
+    zero = dev(np.array([0], np.int32))
+    api.kv4_append(dev(k, dtype), dev(k, dtype), cache, dev(pages), zero, dev(cos), dev(sin), summary=summ, interleaved=inter)
+    kr, _ = api.kv4_gather(cache, dev(pages), zero + L, L, dtype=torch.float32)
+    ok()
+    turned = o.rotate(k[0], cos[:, None], sin[:, None], inter)                           # [L, H, D] fp32, as the append has it
+    _, s, m = (x.astype(np.float64) for x in o.quantise(turned))
+    slack = s * (0.5 + 15 * 2.0 ** -11) + 2.0 ** -11 * np.abs(m) + 16 * 2.0 ** -25 + 2.0 ** -22 * np.abs(turned)
+    q = rng.standard_normal((200, D))
+    box = summ.double().cpu().numpy()[pages[0]]                                            # [5, H, 2, D]
+    read = kr[0].double().cpu().numpy().reshape(5, page, H, D)
+    slack, turned = slack.reshape(5, page, H, D), turned.astype(np.float64).reshape(5, page, H, D)
+    for p in range(5):
+        for h in range(H):
+            lo, hi = box[p, h]
+            bound = np.maximum(q * lo, q * hi).sum(-1)                                     # [200]
+            edge = np.abs(q) @ (2.0 ** -8 * np.maximum(np.abs(lo), np.abs(hi)))
+            assert (q @ turned[p, :, h].T <= (bound + edge)[:, None]).all()
+            assert (q @ read[p, :, h].T <= (bound + edge)[:, None] + np.abs(q) @ slack[p, :, h].T).all()
