@@ -125,7 +125,8 @@ def kv4():
             if _kv4_module is None:
                 if not os.path.exists(_build.BINDING):
                     raise RuntimeError(f"{_build.BINDING} not found; build it with "
-                                       "`python -m context_parallelism_02_gb300.build`")
+                                       "`python -m context_parallelism_02_gb300.build` (this needs the headers of "
+                                       "Python and torch)")
                 spec = importlib.util.spec_from_file_location("_kv4_binding", _build.BINDING)
                 module = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(module)

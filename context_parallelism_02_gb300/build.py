@@ -3,7 +3,9 @@
 Each ``csrc/*.cu`` is compiled in parallel to an object file, then linked
 into ``context_parallelism_02_gb300/_build/libcp.so`` with the CUDA runtime
 linked statically, so the library needs only the driver at load time.  Next to
-it, ``csrc/kv4_binding.cpp`` becomes the Python module of the cache's calls.
+it, ``csrc/kv4_binding.cpp`` becomes the Python module of the cache's calls; the
+library does not need it, and where torch or Python's headers are missing it is
+left out with a warning.
 
 Usage: ``python -m context_parallelism_02_gb300.build`` (or ``build()``).
 
@@ -22,6 +24,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -57,19 +60,27 @@ def _deps():
     return [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != BINDING_SRC] + [os.path.join(INCLUDE, "cp.h")]
 
 
-def build_binding(force: bool = False) -> str:
-    """Compile the Python module of the cache's calls against torch's headers (g++); returns its path."""
+def build_binding(force: bool = False) -> str | None:
+    """Compile the Python module of the cache's calls against torch's headers (g++); returns its path,
+    or None where there is no torch or no Python header to compile it against."""
     deps = [os.path.join(CSRC, BINDING_SRC), os.path.join(INCLUDE, "cp.h")]
     if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
         return BINDING
-    import torch
+    include = sysconfig.get_paths()["include"]
+    try:
+        import torch
+        if not os.path.exists(os.path.join(include, "Python.h")):
+            raise ImportError(f"no Python.h in {include}")
+    except ImportError as e:
+        warnings.warn(f"{BINDING_SRC} is not compiled, so the kv4 calls are missing from the Python package: {e}")
+        return None
     home = os.path.dirname(torch.__file__)
     os.makedirs(BUILD, exist_ok=True)
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
            "-isystem", os.path.join(home, "include"), "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_paths()["include"], deps[0], "-o", tmp, "-L" + os.path.join(home, "lib"),
+           "-isystem", include, deps[0], "-o", tmp, "-L" + os.path.join(home, "lib"),
            "-lc10", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -112,13 +123,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(),
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
         binding = ex.submit(build_binding, force)
         objs = list(ex.map(compile_one, srcs))
-        binding.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
+    binding.result()   # raises what the module's compilation raised; the library is there
     return lib
 
 
