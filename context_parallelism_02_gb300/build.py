@@ -33,11 +33,11 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libcp.so")
 LIB_DEBUG_BOUNDS = os.path.join(BUILD, "debug_bounds", "libcp.so")
-try:   # the module belongs to the torch it was compiled against
+try:   # the module belongs to the torch and the Python it was compiled against
     _TORCH = importlib.metadata.version("torch")
 except importlib.metadata.PackageNotFoundError:
     _TORCH = "none"
-BINDING = os.path.join(BUILD, f"_kv4_binding-{_TORCH}.so")
+BINDING = os.path.join(BUILD, f"_kv4_binding-{_TORCH}{sysconfig.get_config_var('EXT_SUFFIX') or '.so'}")
 BINDING_SRC = "kv4_binding.cpp"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -2,6 +2,7 @@
 import os
 import subprocess
 import sys
+import sysconfig
 import types
 
 import pytest
@@ -53,6 +54,10 @@ def test_binding_is_compiled_beside_the_library(tree):
     tree.binding.write_text('#include <Python.h>\n#include <torch/csrc/Exceptions.h>\nextern "C" int two() { return 2; }\n')
     assert build.build() == str(tree.lib)
     assert tree.lib.exists() and tree.so.exists()
+
+
+def test_binding_file_belongs_to_this_python():
+    assert build.BINDING.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
 
 
 def test_missing_binding_is_named(cplib, monkeypatch):
