@@ -340,13 +340,13 @@ def ulysses_head_to_seq(y: torch.Tensor, N: int, layout: int, x=None, stream=Non
 # The kv4 calls go through the module of csrc/kv4_binding.cpp, which checks the
 # tensors and makes those that are not given: in Python that took longer than the
 # kernels of a decode step.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _raw_stream(index):   # looked up at the call: a torch without CUDA has no such function
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _kv4_device(name, t):
     """The call's device: that of its first tensor, which has to be the current one."""
-    if not t.is_cuda or t.get_device() != _current_device():
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current CUDA device")
     return t.get_device()
 

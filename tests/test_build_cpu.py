@@ -66,3 +66,23 @@ def test_missing_binding_is_named(cplib, monkeypatch):
     monkeypatch.setattr(build, "BINDING", build.BINDING + ".none")
     with pytest.raises(RuntimeError, match="needs the headers"):
         _lib.kv4()
+
+
+def test_import_with_a_torch_without_cuda(cplib):
+    """The host calls (shard maps, schedules) need no CUDA build of torch, and the cache's refuse host tensors there."""
+    code = """
+import torch
+for name in [n for n in dir(torch._C) if n.startswith("_cuda_")]:
+    delattr(torch._C, name)
+from context_parallelism_02_gb300 import api
+assert api.cp_shard_map(16, 4, 1).shape == (4, 4)
+assert api.cp_schedule_pairs(256, 2, 0, True)[0].sum() == 256 * 257 // 2
+x = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+i = torch.zeros(1, 1, dtype=torch.int32)
+try:
+    api.kv4_attn(x, torch.zeros(1, 1, 16, 80, dtype=torch.uint8), i, i[0])
+except ValueError:
+    print("refused")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
