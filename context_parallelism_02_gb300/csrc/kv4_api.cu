@@ -66,9 +66,17 @@ int set_strides(const int64_t *given, int n, int H, int D, int elem, int64_t (&s
     return CP_OK;
 }
 
+// Whether [B][n][heads] rows are more than the launches count in 64 bits (far more than any
+// memory holds: rows with strides of 0 need none).
+bool too_many(int B, int n, int heads)
+{
+    return (unsigned __int128)(unsigned)B * (unsigned)n * (unsigned)heads > (unsigned __int128)1 << 48;
+}
+
 int check_rows(const void *q, const int32_t *vis, int B, int n, int Hq, int Hkv, int causal, Kv4Rows &r)
 {
     if (B < 0 || n < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (causal != 0 && causal != 1)) return CP_EINVAL;
+    if (too_many(B, n, Hq)) return CP_EUNSUPPORTED;
     if (B > 0 && n > 0 && (!q || !aligned(q, 16) || !aligned(vis, 4))) return CP_EINVAL;
     r.vis = vis;
     r.B = B;
@@ -100,6 +108,7 @@ int kv4_append(const void *k, const void *v, const void *q, void *q_out, void *c
     if (n < 0 || (!q) != (!q_out) || (q && Hq < 1) || (interleaved != 0 && interleaved != 1)) return CP_EINVAL;
     if (q && Hq % Hkv) return CP_EINVAL;
     if (rot < 0 || rot > D || rot % 16 || max_pos < 0) return CP_EINVAL;
+    if (too_many(B, n, Hkv) || (q && too_many(B, n, Hq))) return CP_EUNSUPPORTED;
     if (B == 0 || n == 0) return CP_OK;
     if (!k || !v || !cache) return CP_EINVAL;
     if (rot && (!cosine || !sine || !aligned(cosine, 16) || !aligned(sine, 16))) return CP_EINVAL;
@@ -140,6 +149,7 @@ int kv4_gather(const void *cache, const int32_t *pages, const int32_t *lens, con
     if (rc) return rc;
     if (dtype != CP_F32 && dtype != CP_BF16) return CP_EUNSUPPORTED;
     if (count < 0) return CP_EINVAL;
+    if (too_many(B, count, Hkv)) return CP_EUNSUPPORTED;
     if (B == 0 || count == 0) return CP_OK;
     if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4)) return CP_EINVAL;
     a.start = start;

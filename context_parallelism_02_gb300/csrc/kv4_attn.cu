@@ -1064,9 +1064,9 @@ int launch(const Kv4AttnArgs &a, const Shape &sh, cudaStream_t st)
         fills[dev].store(fill, std::memory_order_release);
     }
     const int64_t ctas = min(fill, MAX_ROWS / (NT * 8 * WARPS));
-    // an upper bound of the line from the sizes alone
+    // an upper bound of the line from the sizes alone (a length is below 2^31: 2^27 blocks)
     const int64_t most = a.sel ? (int64_t)a.n_sel << (a.pool.page_shift - 4)
-                               : ((int64_t)a.pool.max_pages << (a.pool.page_shift - 4));
+                               : min((int64_t)a.pool.max_pages << (a.pool.page_shift - 4), (int64_t)1 << 27);
     const int64_t items = (int64_t)a.rows.B * sh.per_batch;
     if (items <= sm_count() && most <= (2 * items >= sm_count() ? ALONE_BLOCKS_MANY : ALONE_BLOCKS)) {
         const cudaError_t rc = kv4_launch(kv4_attn_kernel<D, NT, ALONE_WARPS, true>, (unsigned)items,

@@ -408,7 +408,7 @@ int ring_attn_bwd_noalloc(const void *q, const void *k, const void *v, const voi
  * and differences below fp16's smallest step (6e-8) are lost.
  * Within one call no two sequences may write the same page.
  * Errors: CP_EINVAL (null pointer, misalignment, sizes, Hq % Hkv), CP_EUNSUPPORTED
- * (D, dtype, page), CP_ECUDA.
+ * (D, dtype, page, more rows than a launch counts), CP_ECUDA.
  */
 int kv4_append(const void *k, const void *v, const void *q, void *q_out, void *cache, void *summary,
                const int32_t *pages, const int32_t *lens, const int32_t *n_new,

@@ -196,3 +196,16 @@ def test_binding_refuses_host_tensors_and_bad_shapes():
     for D, page in ((96, 16), (64, 24)):
         with pytest.raises(_lib.CpError):
             api.kv4_cache(4, 2, page, D)
+
+
+def test_sizes_whose_products_pass_64_bits_are_refused(cplib):
+    """Rows with strides of 0 and an empty pool need no memory, so sizes alone must not wrap a launch's counts."""
+    U, most = _lib.CP_EUNSUPPORTED, 2 ** 31 - 1
+    zero = ctypes.cast((ctypes.c_int64 * 9)(), ctypes.c_void_p)
+    for B, n, H in ((most, most, most), (1 << 20, most, most), (most, 1, most), (256, (1 << 31) - 128, 1 << 30)):
+        assert append(B=B, n=n, Hkv=H, q=None, q_out=None, strides=zero, P=0) == U
+        assert append(B=B, n=n, Hkv=1, Hq=H, strides=zero, P=0) == U
+        assert gather(B=B, count=n, Hkv=H, P=0) == U
+        assert attn(B=B, n=n, Hkv=H, Hq=H, P=0) == U
+        assert attn(B=B, n=n, Hkv=1, Hq=H, P=0, sel=FAKE, n_sel=4) == U
+        assert select(B=B, n=n, Hkv=H, Hq=H, P=0) == U
