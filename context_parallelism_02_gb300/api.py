@@ -374,6 +374,9 @@ def kv4_append(k, v, cache, pages, lens, cos=None, sin=None, q=None, q_out=None,
     ``[max_pos, rot / 2]`` (None: no rotation); positions int32 ``[B, n]`` (None: the
     slots); n_new int32 ``[B]``: real tokens of a padded batch; summary: the pool's
     key ranges, kept for :func:`kv4_select`.
+
+    The cache is for serving: none of the kv4 calls has a gradient.  What they return
+    requires none, also where k, v or q do.
     """
     if stream is not None:   # what is allocated belongs to the stream that uses it
         with torch.cuda.stream(stream):
@@ -389,7 +392,8 @@ def kv4_append(k, v, cache, pages, lens, cos=None, sin=None, q=None, q_out=None,
 
 def kv4_gather(cache, pages, lens, count: int, start=None, dtype=torch.bfloat16, k=None, v=None, stream=None):
     """Cached tokens back as rows: (k, v) ``[B, count, Hkv, D]`` with row (b, j) the slot
-    ``start[b] + j`` (start int32 ``[B]``, None: 0); rows at or past ``lens[b]`` are 0."""
+    ``start[b] + j`` (start int32 ``[B]``, None: 0); rows at or past ``lens[b]`` are 0.
+    No gradient."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return kv4_gather(cache, pages, lens, count, start, dtype, k, v)
@@ -418,7 +422,8 @@ def kv4_attn(q, cache, pages, lens, vis=None, causal: bool = True, scale: float 
     :func:`lse_merge` takes it), lse ``[B, Hq, n]`` fp32.  Row (b, j) sees the slots
     below ``vis[b, j]`` (int32 ``[B, n]``), else below ``lens[b] - (n - 1) + j`` if
     causal, else below ``lens[b]``.  ``sel`` int32 ``[B, n, Hkv, n_sel]``
-    (:func:`kv4_select`): only the slots of these pages.
+    (:func:`kv4_select`): only the slots of these pages.  No gradient: training runs
+    :func:`ring_attn_fwd` and :func:`ring_attn_bwd` on rows that are not quantised.
     """
     if stream is not None:
         with torch.cuda.stream(stream):

@@ -361,7 +361,7 @@ int ring_attn_bwd_noalloc(const void *q, const void *k, const void *v, const voi
  * kv4_attn (attention of a few query tokens over the cache; its (out, lse) are
  * partials that lse_merge joins when the ranks of a context-parallel group each
  * hold a part of the sequence) and kv4_select (the pages that a query attends
- * to, for kv4_attn).
+ * to, for kv4_attn).  They serve; none of them has a backward pass.
  *
  * Pool: cache [n_pages][Hkv][page][5 D / 4] bytes, 16-byte aligned; page in
  * {16, 32, 64, 128, 256}, D in {64, 128}.  A page holds `page` tokens of one
@@ -435,7 +435,7 @@ int kv4_gather(const void *cache, const int32_t *pages, const int32_t *lens, con
  *   below lens[b] - (n - 1) + j if causal (the n tokens are the last of the
  *   cache), else below lens[b]; in any case below lens[b].
  *   sel [B][n][Hkv][n_sel] int32 or NULL: row (b, j) and kv head h attend only to
- *   the slots that they see in these pages (numbers within the sequence; -1: no
+ *   the slots that they see in these pages (numbers within the sequence; negative: no
  *   page; a page named twice counts twice).
  *   out [B][n][Hq][D]: bf16 (rounded to nearest even) or fp32 by out_dtype;
  *   lse [B][Hq][n] fp32, natural log.  A row that sees nothing: (0, -inf).  What a

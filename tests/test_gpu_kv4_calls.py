@@ -167,3 +167,16 @@ def test_calls_from_two_threads(cuda_dev):
     assert not errors
     for i in range(2):
         assert all(torch.equal(x, y) for x, y in zip(want[i], got[i]))
+
+
+def test_no_gradient(cuda_dev):
+    """Inputs that require gradients are taken; what comes back requires none, as the documentation says."""
+    cache, summ, pages, g = pool(5, 1, 100, 1, 64, 16)
+    k, q = (torch.randn(1, 1, h, 64, generator=g, device="cuda").bfloat16().requires_grad_() for h in (1, 2))
+    lens = torch.tensor([40], **I32)
+    qr = api.kv4_append(k, k, cache, pages, lens, q=q, summary=summ)
+    out, lse = api.kv4_attn(q, cache, pages, lens)
+    done()
+    assert torch.equal(qr, q) and not (qr.requires_grad or out.requires_grad or lse.requires_grad)
+    for f in (api.kv4_append, api.kv4_gather, api.kv4_attn):
+        assert "radient" in f.__doc__
