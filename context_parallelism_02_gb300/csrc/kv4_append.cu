@@ -8,11 +8,13 @@
 // code = clamp(rint((y - m) / s), 0, 15); a group with a value that is not
 // finite is held as NaN.
 //
-// HBM-bound in principle: per token and kv head 2 D elements are read and 1.25 D
-// bytes written.  The arithmetic of the quantisation is as long: about 600
-// instructions for the K and V rows of two tokens and a head.  32768 tokens of 8 kv
-// and 32 q heads take 149 us, 713 MB at 4.8 TB/s: 66 % of the issue slots, 59 % of
-// DRAM; the k and v rows alone 84 to 96 us, the q rows alone 92.
+// Per token and kv head 2 D elements are read and 1.25 D bytes written.  The q rows are
+// bound by that traffic; the k and v rows are not: the quantisation takes about 600
+// instructions for the K and V rows of two tokens and a head, in one dependent chain a
+// pass.  32768 tokens of 8 kv and 32 q heads take 151 us, 713 MB at 4.7 TB/s: 66 % of the
+// issue slots, 59 % of DRAM, and warps that mostly wait for their rows (4.2 of 10 cycles a
+// warp and instruction); the k and v rows alone 84 to 96 us, of which their bytes
+// are 26, the q rows alone 92.
 // In K and V a lane holds 8 neighbouring elements of a row, so a group's extremes are
 // two shuffles and a K code word is one lane's; a warp's pass takes the K rows of
 // 256 / D tokens, the next their V rows (one pass over both left lanes idle in the

@@ -15,18 +15,22 @@
 // A masked nibble is an fp16 as it stands: a subnormal, n 2^-24 in the lowest four
 // bits and 16 n 2^-24 in the next four (their elements of q are divided by 16), so
 // unpacking K is one AND a pair.  q is scaled per row by a power of two into fp16's
-// range (bf16's 8 bits fit), so the products are exact and the group's scale
-// multiplies an fp32 sum.  The minima are one more product, m (fp16, exact) with
-// the rows' group sums of q in three fp16 parts.  V's values s n + m are rounded
-// to fp16 (relative 2^-11, below 2^-14 absolute 2^-25) and so are the weights P; the row
-// sums are taken over the unrounded fp32 weights.  Weights are taken relative to a
-// reference at least 7 (in powers of two) below the largest score of the stretch so far, so
-// that the largest is 2^7 to 2^15 and a small one is off by 2^-11 of itself or 2^-32 of
-// the largest: a long tail behind one large score is not lost from O while it
-// counts in the sums.
+// range: its largest element comes to 2^8 (2^4 where it is divided by 16), bf16's 8 bits
+// fit down to 2^-21 of it, and the products are exact; smaller elements are off by up to
+// 2^-29 of the largest.  The group's scale multiplies an fp32 sum.  The minima are one
+// more product, m (fp16, exact) with the rows' group sums of q in three fp16 parts.
+// V's values s n + m are rounded to fp16 (relative 2^-11, below 2^-14 absolute 2^-25)
+// and so are the weights P; the row sums are taken over the unrounded fp32 weights.
+// Weights are relative to a reference 7 to 15 powers of two below the largest score of the
+// stretch so far, so that the largest weight is 2^7 to 2^15 and a small one is off by 2^-11
+// of itself or 2^-32 of the largest: a long tail behind one large score is not lost from
+// O while it counts in the sums.  V and P in one fp16 part each are a choice: a second
+// part of either doubles the 8 products of a block in a kernel that is short of issue slots,
+// and what it would mend is below the output's own bf16 step (error against 64 bits 0.0017
+// of the outputs' norm either way; one output in 8 falls on the other side of a bf16 step).
 //
-// Measured (Hq = 32, Hkv = 8, D = 128): 16 x 32768 tokens 119.8 us, 5.6 TB/s of cache,
-// 108 without the arithmetic; 4 x 32768 37.4 us; 1 x 512 (a block per item) 6.9 us.  Per block 339
+// Measured (Hq = 32, Hkv = 8, D = 128): 16 x 32768 tokens 119.5 us, 5.6 TB/s of cache,
+// 108 without the arithmetic; 4 x 32768 37.6 us; 1 x 512 (a block per item) 7.0 us.  Per block 340
 // instructions: the integer pipe and the heavy half of the FMA pipe take 60 cycles of
 // an SM each, issue 85, HBM at its copy rate 112.
 #include <atomic>

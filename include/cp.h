@@ -440,11 +440,14 @@ int kv4_gather(const void *cache, const int32_t *pages, const int32_t *lens, con
  *   out [B][n][Hq][D]: bf16 (rounded to nearest even) or fp32 by out_dtype;
  *   lse [B][Hq][n] fp32, natural log.  A row that sees nothing: (0, -inf).  What a
  *   row does not see has no influence on it, whatever those slots hold.
- *   fp32 sums; K enters exactly, V's values and the softmax weights rounded to
- *   fp16 (2^-11 of themselves; a weight at worst 2^-32 of the row's largest).  scale <= 0 selects 1/sqrt(D).  A row of q with a value that is not finite,
+ *   fp32 sums; K and q enter exactly (an element of q below 2^-21 of its row's largest
+ *   is rounded, by up to 2^-29 of the largest), V's values and the softmax weights rounded
+ *   to fp16 (2^-11 of themselves; a weight at worst 2^-32 of the row's largest).  scale <= 0 selects 1/sqrt(D).  A row of q with a value that is not finite,
  *   or of 2^110 and more, comes out as NaN.
  *   workspace: device, kv4_attn_workspace(D) bytes, 16-byte aligned, contents
  *   irrelevant; calls that may overlap on the GPU need their own.
+ *   Which kernels run goes by the sizes alone, max_pages among them: a page table no
+ *   wider than the sequences need is the faster one for short ones.
  * Errors: as kv4_append, plus a null or too small workspace.
  */
 int kv4_attn(const void *q, const void *cache, const int32_t *pages, const int32_t *lens,
