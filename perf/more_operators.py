@@ -78,7 +78,9 @@ def draw(rng):
         Sk = _log(rng, 16, most // B)
         Sq = rng.choice([Sk, Sk, max(1, Sk // 3), _log(rng, 1, Sk)]) if op == "fwd" else Sk
         pairs = (1 << 26) if f32 else (1 << 32) if op == "fwd" else (1 << 28)
-        window = _log(rng, 1, max(1, min(2 * Sk, pairs // (B * Sq * Hq))))
+        # a row that sees itself alone has no gradient of q and k: nothing to compare
+        least = 1 if op == "fwd" else 2
+        window = _log(rng, least, max(least, min(2 * Sk, pairs // (B * Sq * Hq))))
         return dict(op=op, B=B, Sq=Sq, Sk=Sk, Hq=Hq, Hkv=Hkv, D=D, window=window,
                     sinks=rng.choice([0, 1, 4, 4, 7, 64, 200]), dtype="f32" if f32 else "bf16")
     if op == "append":
