@@ -59,6 +59,9 @@ SIGNATURES = {
     "lse_merge_n": (_I, [_P, _P, _I, _L, _I, _P, _P, _P]),
     "ulysses_seq_to_head": (_I, [_P, _P, _I, _L, _I, _I, _I, _I, _I, _P]),
     "ulysses_head_to_seq": (_I, [_P, _P, _I, _L, _I, _I, _I, _I, _I, _P]),
+    "window_attn_fwd": (_I, [_P] * 5 + [_I] * 3 + [_L, _L, _I, _L, _L, _I, _F, _P]),
+    "window_attn_bwd": (_I, [_P] * 9 + [_I] * 3 + [_L, _L, _I, _L, _L, _I, _F, _P, ctypes.c_size_t, _P]),
+    "window_attn_bwd_workspace": (ctypes.c_size_t, [_I] * 3 + [_L, _L, _I, _L, _L, _I]),
     "kv4_append": (_I, [_P] * 13 + [_I] * 12 + [_P]),
     "kv4_gather": (_I, [_P] * 6 + [_I] * 8 + [_P]),
     "kv4_attn": (_I, [_P] * 8 + [_I] * 11 + [_F, _P, ctypes.c_size_t, _P]),

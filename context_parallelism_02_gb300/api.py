@@ -271,6 +271,93 @@ def ring_attn_bwd_noalloc(q, k, v, out, lse, dout, N: int, layout: int, causal: 
     return dq, dk, dv
 
 
+def _window_sizes(q, k, v):
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _need_cuda_contig(name, t)
+        if t.dim() != 4:
+            raise ValueError(f"{name} must have shape [B, S, H, D]")
+        if t.device != q.device:
+            raise ValueError(f"{name} must be on q's device")
+    if q.device.index != torch.cuda.current_device():
+        raise ValueError("q must be on the current CUDA device")
+    if q.dtype not in _DT or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k, v must share dtype float32 or bfloat16")
+    B, Sq, Hq, D = q.shape
+    Sk, Hkv = k.shape[1], k.shape[2]
+    if k.shape != (B, Sk, Hkv, D) or v.shape != k.shape:
+        raise ValueError("k and v must have shape [B, Sk, Hkv, D] with q's B and D")
+    return B, Sq, Sk, Hq, Hkv, D
+
+
+def _window_like(name, t, like, dtype=None):
+    """An output or saved tensor of ``like``'s shape, device and (unless given) dtype."""
+    _need_cuda_contig(name, t)
+    if tuple(t.shape) != tuple(like.shape) or t.device != like.device or t.dtype != (dtype or like.dtype):
+        raise ValueError(f"{name} must be {dtype or like.dtype} {list(like.shape)} on {like.device}")
+    return t
+
+
+def window_attn_fwd(q, k, v, window: int, sinks: int = 0, scale: float | None = None, out=None, lse=None, stream=None):
+    """Causal attention with a sliding window and first tokens that stay visible; returns
+    (out, lse).
+
+    q ``[B, Sq, Hq, D]``, k/v ``[B, Sk, Hkv, D]`` (fp32 or bf16), Sq <= Sk: row i stands at
+    position ``p = i + Sk - Sq`` and sees key j iff ``j <= p and (j > p - window or
+    j < sinks)``.  out like q, lse ``[B, Hq, Sq]`` fp32.  A chunk of a prompt, or the shard
+    of a context-parallel rank, passes its own rows as q and as k and v the sinks' rows,
+    ``window - 1`` rows before the shard and the shard (all rows from 0 on where these
+    meet).  Gradients: :func:`window_attn_bwd`.
+    """
+    if stream is not None:   # what is allocated belongs to the stream that uses it
+        with torch.cuda.stream(stream):
+            return window_attn_fwd(q, k, v, window, sinks, scale, out, lse)
+    B, Sq, Sk, Hq, Hkv, D = _window_sizes(q, k, v)
+    out = torch.empty_like(q) if out is None else _window_like("out", out, q)
+    stat = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
+    if lse is not None and (lse.shape != (B, Hq, Sq) or lse.dtype != torch.float32 or lse.device != q.device
+                            or not lse.is_contiguous()):
+        raise ValueError(f"lse must be contiguous float32 {[B, Hq, Sq]} on {q.device}")
+    rc = _lib.load().window_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(stat), B, Hq, Hkv, Sq, Sk, D, window,
+                                     sinks, _DT[q.dtype], -1.0 if scale is None else float(scale),
+                                     ctypes.c_void_p(_stream(None)))
+    check(rc, "window_attn_fwd")
+    return out, stat
+
+
+def window_attn_bwd_workspace(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: int, window: int, sinks: int = 0,
+                              dtype=torch.bfloat16) -> int:
+    """Bytes of scratch for :func:`window_attn_bwd`."""
+    return int(_lib.load().window_attn_bwd_workspace(B, Hq, Hkv, Sq, Sk, D, window, sinks, _DT.get(dtype, -1)))
+
+
+def window_attn_bwd(q, k, v, out, lse, dout, window: int, sinks: int = 0, scale: float | None = None, dq=None, dk=None,
+                    dv=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of sum(dout * out) for :func:`window_attn_fwd`, whose out and
+    lse are passed in."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return window_attn_bwd(q, k, v, out, lse, dout, window, sinks, scale, dq, dk, dv, workspace)
+    B, Sq, Sk, Hq, Hkv, D = _window_sizes(q, k, v)
+    _window_like("out", out, q)
+    _window_like("dout", dout, q)
+    if lse.shape != (B, Hq, Sq) or lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous float32 {[B, Hq, Sq]} on {q.device}")
+    dq = torch.empty_like(q) if dq is None else _window_like("dq", dq, q)
+    dk = torch.empty_like(k) if dk is None else _window_like("dk", dk, k)
+    dv = torch.empty_like(v) if dv is None else _window_like("dv", dv, v)
+    if workspace is None:
+        workspace = torch.empty(window_attn_bwd_workspace(B, Hq, Hkv, Sq, Sk, D, window, sinks, q.dtype),
+                                dtype=torch.uint8, device=q.device)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {q.device}")
+    rc = _lib.load().window_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
+                                     _ptr(dv), B, Hq, Hkv, Sq, Sk, D, window, sinks, _DT[q.dtype],
+                                     -1.0 if scale is None else float(scale), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), ctypes.c_void_p(_stream(None)))
+    check(rc, "window_attn_bwd")
+    return dq, dk, dv
+
+
 def lse_merge(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=None):
     """Merge two fp32 partials over disjoint key sets; returns (out, lse)."""
     for name, t in (("out_a", out_a), ("lse_a", lse_a), ("out_b", out_b), ("lse_b", lse_b)):

@@ -35,10 +35,14 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <type_traits>
+
 #include "cp_common.cuh"
 #include "kernels.h"
 #include "tc_helpers.cuh"
 #include "tmem_io.cuh"
+#include "window_sinks.cuh"
 
 namespace cp {
 
@@ -215,17 +219,31 @@ struct BwdArgs {
     unsigned *err;
     uint64_t limit_ns;   // pipeline waits
     uint64_t drain_ns;   // waits that drain copies and MMAs before exit
+    int Sk;              // windowed attention: keys (S counts query rows)
+    Window win;          // windowed attention
+    SinkPlan sp;
+    float *part;         // the sinks' partial gradients (window_sinks.cuh)
 };
 
-template <int D>
+// WIN: windowed attention with sinks, the walks of WinIter and WinQIter.  The dQ
+// kernel's packed first tile has boxes of its own, as the forward's.
+struct PackMaps {
+    CUtensorMap k_sinks, k_rest, v_sinks, v_rest;
+};
+struct NoMaps {
+};
+
+template <int D, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                   const BwdArgs a, const float *__restrict__ lse,
                   const float *__restrict__ delta, __nv_bfloat16 *__restrict__ dq,
-                  const __nv_bfloat16 *__restrict__ dout)
+                  const __nv_bfloat16 *__restrict__ dout,
+                  const __grid_constant__ std::conditional_t<WIN, PackMaps, NoMaps> pm)
 {
     using C = DqCfg<D>;
+    using Walk = std::conditional_t<WIN, WinIter<T>, KvIter<T>>;
     constexpr int TB = C::TB;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
@@ -243,9 +261,38 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const Geom g = make_geom(a.S, a.N, a.layout, a.causal);
     const Unit w = decode_unit_grouped(g, a.B, a.Hq, a.upc, T, blockIdx.x);
     const int kvh = w.h / (a.Hq / a.Hkv);
-    const int n = KvIter<T>::count(g, w.r, w.qmax);
+    auto start_walk = [&](Walk &it) {
+        if constexpr (WIN) it.begin(a.win, w.q0 + a.win.off, w.qmax + a.win.off);
+        else it.begin(g, w.r, w.qmax);
+    };
+    int n;
+    if constexpr (WIN) n = WinIter<T>::count(a.win, w.q0 + a.win.off, w.qmax + a.win.off);
+    else n = KvIter<T>::count(g, w.r, w.qmax);
     // extents of the tensor maps' (rank, row) dimensions, for the debug-bounds build
     const int map_r = striped(g) ? g.N : 1, map_rows = a.S / map_r;
+    // a tile of K or V into shared memory
+    auto load_tile = [&](const Walk &it, uint32_t dst, const CUtensorMap *map, const CUtensorMap *sinks,
+                         const CUtensorMap *rest, uint32_t bar, uint64_t policy) {
+        if constexpr (WIN) {
+            if (it.packed()) {
+                for (int bx = 0; bx < D / 64; ++bx) {
+                    tma_load5(dst + bx * 16384, sinks, bar, bx * 64, kvh, 0, 0, w.b, policy);
+                    tma_load5(dst + bx * 16384 + it.pk * 128, rest, bar, bx * 64, kvh, 0,
+                              dbg_coord(a.err, it.start() + it.pk, a.Sk), w.b, policy);
+                }
+                return;
+            }
+            const int row = dbg_coord(a.err, it.start(), a.Sk);
+            for (int bx = 0; bx < D / 64; ++bx)
+                tma_load5(dst + bx * 16384, map, bar, bx * 64, kvh, 0, row, w.b, policy);
+        } else {
+            const int mr = dbg_coord(a.err, it.mrank(), map_r), mw = dbg_coord(a.err, it.mrow(), map_rows);
+            for (int bx = 0; bx < D / 64; ++bx)
+                tma_load5(dst + bx * 16384, map, bar, bx * 64, kvh, mr, mw, w.b, policy);
+        }
+    };
+    const CUtensorMap *pks = nullptr, *pkr = nullptr, *pvs = nullptr, *pvr = nullptr;
+    if constexpr (WIN) pks = &pm.k_sinks, pkr = &pm.k_rest, pvs = &pm.v_sinks, pvr = &pm.v_rest;
 
     if (threadIdx.x == 0) {
         mbar_init(BAR(Q_QTM), 1);
@@ -286,17 +333,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (warp == 0 && lane == 0) {
             // ------------------------------------------------------------ K producer
             const uint64_t pol_kv = policy_evict_last();
-            KvIter<T> it;
-            it.begin(g, w.r, w.qmax);
+            Walk it;
+            start_walk(it);
             int nk = 0;
             Ring<Q_KST> kr;
             for (int j = 0; j < n; ++j, it.next(), kr.next()) {
                 if (j >= Q_KST && !wait1(BAR(Q_KEMPTY + kr.st), kr.ph ^ 1, wc)) break;
                 mbar_arrive_expect_tx(BAR(Q_KFULL + kr.st), TB);
-                const int kmr = dbg_coord(a.err, it.mrank(), map_r), kmw = dbg_coord(a.err, it.mrow(), map_rows);
-                for (int bx = 0; bx < D / 64; ++bx)
-                    tma_load5(sK + kr.st * TB + bx * 16384, &tmK, BAR(Q_KFULL + kr.st), bx * 64, kvh,
-                              kmr, kmw, w.b, pol_kv);
+                load_tile(it, sK + kr.st * TB, &tmK, pks, pkr, BAR(Q_KFULL + kr.st), pol_kv);
                 ++nk;
             }
             {
@@ -316,17 +360,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_arrive_expect_tx(BAR(Q_QTM), TB);
             for (int bx = 0; bx < D / 64; ++bx)
                 tma_load5(sQ + bx * 16384, &tmQ, BAR(Q_QTM), bx * 64, w.h, qmr, qmw, w.b, pol_q);
-            KvIter<T> it;
-            it.begin(g, w.r, w.qmax);
+            Walk it;
+            start_walk(it);
             int nv = 0;
             for (int j = 0; j < n; ++j, it.next()) {
                 const int sv = j & 1;
                 if (j >= 2 && !wait1(BAR(Q_VEMPTY + sv), ((j >> 1) - 1) & 1, wc)) break;
                 mbar_arrive_expect_tx(BAR(Q_VFULL + sv), TB);
-                const int vmr = dbg_coord(a.err, it.mrank(), map_r), vmw = dbg_coord(a.err, it.mrow(), map_rows);
-                for (int bx = 0; bx < D / 64; ++bx)
-                    tma_load5(sV + sv * TB + bx * 16384, &tmV, BAR(Q_VFULL + sv), bx * 64, kvh,
-                              vmr, vmw, w.b, pol_kv);
+                load_tile(it, sV + sv * TB, &tmV, pvs, pvr, BAR(Q_VFULL + sv), pol_kv);
                 ++nv;
             }
             {
@@ -460,14 +501,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (lane == 0) mbar_arrive(BAR(Q_DOFULL));
         }
         bool ok = true;
-        KvIter<T> it;
-        it.begin(g, w.r, w.qmax);
+        Walk it;
+        start_walk(it);
         for (int j = 0; j < n; ++j, it.next()) {
             const int ks = it.start(), kl = it.len();
             int lim = kl;                              // visible columns [0, lim) of the tile
-            if (a.causal) {
-                const int c = qpos - ks + 1 + it.shift;
-                lim = c < lim ? c : lim;
+            uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;   // WIN: visible columns, 32 each
+            bool all = false;
+            if constexpr (WIN) {
+                const int p0 = w.q0 + a.win.off, p = qpos + a.win.off;
+                all = it.full(a.win, p0, w.qmax + a.win.off);
+                if (!all) {
+                    const int hi = (p - ks + 1 < kl ? p - ks + 1 : kl) - 64 * half;
+                    const int lo = it.window_col(a.win, p) - 64 * half, sc = it.sink_cols() - 64 * half;
+                    see0 = visible_bits(0, hi, lo, sc);
+                    see1 = visible_bits(32, hi, lo, sc);
+                }
+            } else {
+                if (a.causal) {
+                    const int c = qpos - ks + 1 + it.shift;
+                    lim = c < lim ? c : lim;
+                }
             }
             lim -= 64 * half;                          // in this half's local columns
             if (!waitw(BAR(Q_SDONE), j & 1, wc)) {
@@ -482,7 +536,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (lane == 0) mbar_arrive(BAR(Q_SFREE));   // S(j+1) may be issued
             // P = exp2(S sl2 - lse2); the per-element mask only where some row of
             // the warp does not see the whole half tile
-            const bool full = __all_sync(0xffffffffu, lim >= 64);
+            const bool full = WIN ? all : __all_sync(0xffffffffu, lim >= 64);
             float p[64];
 #pragma unroll
             for (int e = 0; e < 64; e += 2) {
@@ -492,7 +546,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             if (!full) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e) p[e] = e < lim ? p[e] : 0.f;
+                for (int e = 0; e < 64; ++e) {
+                    if constexpr (WIN) p[e] = (e < 32 ? see0 : see1) >> (e & 31) & 1u ? p[e] : 0.f;
+                    else p[e] = e < lim ? p[e] : 0.f;
+                }
             }
             if (!waitw(BAR(Q_PDONE), j & 1, wc)) {
                 ok = false;
@@ -612,7 +669,7 @@ struct DkvCfg {
     static_assert(TM_DK + D <= 512, "dK/dV kernel tensor memory");
 };
 
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQh, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDOh,
@@ -635,12 +692,47 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem_raw + C::OFF_MISC + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Geom g = make_geom(a.S, a.N, a.layout, a.causal);
-    const KvUnit w = decode_kv_unit<T>(g, a.B, a.Hkv, a.tpc, blockIdx.x);
     const int grp = a.Hq / a.Hkv;
+    const Geom g = make_geom(a.S, a.N, a.layout, a.causal);
+    using Walk = std::conditional_t<WIN, WinQIter<T>, QIter<T>>;
+    KvUnit w;
+    int piece = 0;       // WIN: 0 a window unit, else 1 + the piece of a tile of sinks
+    if constexpr (WIN) {
+        const Geom gk = make_geom(a.Sk, 1, CP_LAYOUT_CONTIGUOUS, 1);
+        const int windows = a.tpc * a.B * a.Hkv;
+        if ((int)blockIdx.x < windows) {
+            w = decode_kv_unit<T>(gk, a.B, a.Hkv, a.tpc, blockIdx.x);
+        } else {
+            unsigned x = blockIdx.x - windows;
+            piece = 1 + (int)(x % (unsigned)a.sp.pieces);
+            x /= (unsigned)a.sp.pieces;
+            const unsigned t = x % (unsigned)a.sp.tiles;
+            x /= (unsigned)a.sp.tiles;
+            w.g = (int)(x % (unsigned)a.Hkv);
+            w.b = (int)(x / (unsigned)a.Hkv);
+            w.src = 0;
+            w.ks = (int)t * T;
+            w.kcend = a.Sk;
+            w.kl = a.Sk - w.ks < T ? a.Sk - w.ks : T;
+        }
+    } else {
+        w = decode_kv_unit<T>(g, a.B, a.Hkv, a.tpc, blockIdx.x);
+    }
+    auto start_walk = [&](Walk &it) {
+        if constexpr (!WIN) it.begin(g, w.src, w.ks, w.g * grp, grp);
+        else if (piece == 0) it.window(a.win, a.S, w.ks, w.kl, w.g * grp, grp);
+        else it.sinks(a.win, a.S, w.ks, w.g * grp, grp, piece - 1, a.sp.each);
+    };
     // extents of the tensor maps' (rank, row) dimensions, for the debug-bounds build
     const int map_r = striped(g) ? g.N : 1, map_rows = a.S / map_r;
-    const int ns = 2 * QIter<T>::count(g, w.src, w.ks, grp);   // half steps
+    int ns;   // half steps
+    if constexpr (WIN) {
+        Walk it;
+        start_walk(it);
+        ns = 2 * it.count();
+    } else {
+        ns = 2 * QIter<T>::count(g, w.src, w.ks, grp);
+    }
 
     if (threadIdx.x == 0) {
         mbar_init(BAR(K_KVFULL), 1);
@@ -679,16 +771,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // ------------------------------------------------------------ producer (whole warp)
             const uint64_t pol_kv = policy_evict_first(), pol_q = policy_evict_last();
             if (lane == 0) {
-                const int kmr = dbg_coord(a.err, slot_mrank(g, w.ks), map_r);
-                const int kmw = dbg_coord(a.err, slot_mrow(g, w.ks), map_rows);
+                const int kmr = WIN ? 0 : dbg_coord(a.err, slot_mrank(g, w.ks), map_r);
+                const int kmw = WIN ? dbg_coord(a.err, w.ks, a.Sk) : dbg_coord(a.err, slot_mrow(g, w.ks), map_rows);
                 mbar_arrive_expect_tx(BAR(K_KVFULL), 2 * TB);
                 for (int bx = 0; bx < D / 64; ++bx) {
                     tma_load5(sK + bx * 16384, &tmK, BAR(K_KVFULL), bx * 64, w.g, kmr, kmw, w.b, pol_kv);
                     tma_load5(sV + bx * 16384, &tmV, BAR(K_KVFULL), bx * 64, w.g, kmr, kmw, w.b, pol_kv);
                 }
             }
-            QIter<T> it;
-            it.begin(g, w.src, w.ks, w.g * grp, grp);
+            Walk it;
+            start_walk(it);
             int issued = 0;
             Ring<K_QST> qr;
             for (int s = 0; s < ns; ++s, qr.next()) {
@@ -697,8 +789,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const int qa = it.start() + 64 * hs, ql = it.len() - 64 * hs, h = it.head();
                 // map coordinates; the second half-tile may start past the end of
                 // the map (a short last tile): the copy then reads the fill value
-                const int qr_rank = dbg_coord(a.err, it.mrank(), map_r);
-                const int qr_row = dbg_coord(a.err, it.mrow(), map_rows) + 64 * hs;
+                int qr_rank = 0, qr_row;
+                if constexpr (WIN) {
+                    qr_row = dbg_coord(a.err, it.start(), a.S) + 64 * hs;
+                } else {
+                    qr_rank = dbg_coord(a.err, it.mrank(), map_r);
+                    qr_row = dbg_coord(a.err, it.mrow(), map_rows) + 64 * hs;
+                }
                 // per-row statistics of the half tile, negated: -lse (log2 units), -Delta
                 float *ls = stat + qr.st * 128, *dl = ls + 64;
                 for (int e = lane; e < 64; e += 32) {
@@ -827,12 +924,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int kpos = w.ks + row;
         const float sl2 = a.scale * LOG2E;
         bool ok = true;
-        QIter<T> it;
-        it.begin(g, w.src, w.ks, w.g * grp, grp);
+        Walk it;
+        start_walk(it);
         Ring<K_QST> qr;
         if (half) qr.next();
         for (int i = 0; 2 * i + half < ns; ++i, it.next(), qr.next(), qr.next()) {
-            const int qa = it.start() + 64 * half, ql = it.len() - 64 * half, sh = it.shift;
+            const int qa = it.start() + 64 * half, ql = it.len() - 64 * half;
+            int sh = 0;
+            if constexpr (!WIN) sh = it.shift;
             if (!waitw(BAR(K_S + half), i & 1, wc) || !waitw(BAR(K_QFULL + qr.st), qr.ph, wc)) {
                 ok = false;
                 break;
@@ -841,11 +940,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             uint32_t sr[64], pr[64];
             tmem_ld_x64(tb, sr);
             // visible query columns c: c < ql and (not causal or qa + c >= kpos)
-            const int lo = a.causal ? kpos - sh - qa : 0;
+            int lo = a.causal ? kpos - sh - qa : 0, hi = ql;
+            if constexpr (WIN) {
+                // the query of column c stands at position qa + c + off; a window unit's
+                // keys are seen up to window - 1 behind them, a piece's sinks from there on
+                lo = kpos - a.win.off - qa;
+                if (piece == 0) hi = a.win.window - 1 < ql - 1 - lo ? lo + a.win.window : ql;
+                else lo = kpos < a.win.sinks && a.win.window <= 64 - lo ? lo + a.win.window : 64;
+            }
             const float4 *ls4 = reinterpret_cast<const float4 *>(stat + qr.st * 128);   // -lse2
             const float4 *dl4 = ls4 + 16;                                               // -Delta
             // most tiles are visible to the whole warp: no per-element mask there
-            const bool full = __all_sync(0xffffffffu, lo <= 0 && ql >= 64);
+            const bool full = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
             // P^T (fp32, kept in place of S^T for dS^T) and its bf16 pairs, stored
             // at once so that their registers are free for dS^T
             {
@@ -862,10 +968,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     p2 = ex2(p2);
                     p3 = ex2(p3);
                     if (!full) {
-                        p0 = (c >= lo && c < ql) ? p0 : 0.f;
-                        p1 = (c + 1 >= lo && c + 1 < ql) ? p1 : 0.f;
-                        p2 = (c + 2 >= lo && c + 2 < ql) ? p2 : 0.f;
-                        p3 = (c + 3 >= lo && c + 3 < ql) ? p3 : 0.f;
+                        p0 = (c >= lo && c < hi) ? p0 : 0.f;
+                        p1 = (c + 1 >= lo && c + 1 < hi) ? p1 : 0.f;
+                        p2 = (c + 2 >= lo && c + 2 < hi) ? p2 : 0.f;
+                        p3 = (c + 3 >= lo && c + 3 < hi) ? p3 : 0.f;
                     }
                     sr[c] = __float_as_uint(p0);
                     sr[c + 1] = __float_as_uint(p1);
@@ -911,15 +1017,37 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (ok && waitw(BAR(K_FIN), 0, wc)) {
             tc_fence_after();
             // half 0 writes dV, half 1 writes dK (times scale)
-            const bool valid = row < w.kl;
+            bool valid = row < w.kl;
             const float f = half ? a.scale : 1.f;
             const uint32_t tAcc = tmem + lane_off + (half ? C::TM_DK : C::TM_DV);
-            __nv_bfloat16 *orow =
-                (half ? dk : dv) + (((int64_t)w.b * a.S + dbg_coord(a.err, valid ? slot_pos(g, kpos) : 0, a.S)) * a.Hkv + w.g) * D;
+            const int krow = WIN ? dbg_coord(a.err, valid ? kpos : 0, a.Sk)
+                                 : dbg_coord(a.err, valid ? slot_pos(g, kpos) : 0, a.S);
+            __nv_bfloat16 *orow = (half ? dk : dv) + (((int64_t)w.b * (WIN ? a.Sk : a.S) + krow) * a.Hkv + w.g) * D;
+            float *prow = nullptr;   // WIN: a sink's partial gradient
+            if constexpr (WIN) {
+                const bool sink = valid && a.sp.pieces > 0 && kpos < a.win.sinks;
+                if (sink)
+                    prow = a.part + (((int64_t)w.b * a.Hkv + w.g) * window_part_rows(a.win, a.sp) +
+                                     ((int64_t)piece * 2 + (half ? 0 : 1)) * a.win.sinks + kpos) * D;
+                valid = valid && !sink && piece == 0;
+            }
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld_x32(tAcc + 32u * c, o);
+                if constexpr (WIN) {
+                    if (ns == 0) {           // keys that no row reaches: the accumulators hold nothing
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    }
+                    if (prow) {
+                        float4 *dst = reinterpret_cast<float4 *>(prow + 32 * c);
+#pragma unroll
+                        for (int v4 = 0; v4 < 8; ++v4)
+                            dst[v4] = make_float4(__uint_as_float(o[4 * v4]) * f, __uint_as_float(o[4 * v4 + 1]) * f,
+                                                  __uint_as_float(o[4 * v4 + 2]) * f, __uint_as_float(o[4 * v4 + 3]) * f);
+                    }
+                }
                 if (valid) {
                     uint4 *dst = reinterpret_cast<uint4 *>(orow + 32 * c);
 #pragma unroll
@@ -942,6 +1070,65 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #undef BAR
 }
 
+// Delta = rowsum(dO * out) into the workspace
+int launch_delta(const BwdPtrs &p, const BwdArgs &a, int D, cudaStream_t st)
+{
+    const int64_t rows = (int64_t)a.B * a.S * a.Hq;
+    int64_t blocks = (rows + 7) / 8;
+    const int64_t cap = (int64_t)sm_count() * 8;
+    if (blocks > cap) blocks = cap;
+    bwd_delta_kernel<<<(unsigned)blocks, 256, 0, st>>>(
+        static_cast<const __nv_bfloat16 *>(p.out), static_cast<const __nv_bfloat16 *>(p.dout),
+        static_cast<float *>(p.workspace), a.S, a.Hq, D, rows);
+    return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ECUDA;
+}
+
+template <int D>
+int launch_window_d(const BwdPtrs &p, BwdArgs a, cudaStream_t st)
+{
+    CUtensorMap mk, mv, mq, mq64, mdo64;
+    PackMaps pm;
+    const int pack = a.win.pack, box = pack ? pack : 16;
+    if (!make_map(&mk, p.k, a.B, a.Sk, a.Hkv, D, 128) || !make_map(&mv, p.v, a.B, a.Sk, a.Hkv, D, 128) ||
+        !make_map(&mq, p.q, a.B, a.S, a.Hq, D, 128) || !make_map(&mq64, p.q, a.B, a.S, a.Hq, D, 64) ||
+        !make_map(&mdo64, p.dout, a.B, a.S, a.Hq, D, 64) ||
+        !make_map(&pm.k_sinks, p.k, a.B, a.Sk, a.Hkv, D, box) ||
+        !make_map(&pm.k_rest, p.k, a.B, a.Sk, a.Hkv, D, 128 - pack) ||
+        !make_map(&pm.v_sinks, p.v, a.B, a.Sk, a.Hkv, D, box) ||
+        !make_map(&pm.v_rest, p.v, a.B, a.Sk, a.Hkv, D, 128 - pack))
+        return CP_ECUDA;
+    static std::atomic<bool> attr_done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return CP_ECUDA;
+    if (dev >= 64 || !attr_done[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(bwd_dq_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 DqCfg<D>::SMEM) != cudaSuccess ||
+            cudaFuncSetAttribute(bwd_dkdv_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 DkvCfg<D>::SMEM) != cudaSuccess)
+            return CP_ECUDA;
+        if (dev < 64) attr_done[dev].store(true, std::memory_order_release);
+    }
+    a.upc = (a.S + T - 1) / T;
+    a.tpc = (a.Sk + T - 1) / T;
+    a.sp = sink_plan<T>(a.win, a.S, a.Sk, a.Hq / a.Hkv);
+    const int64_t qunits = (int64_t)a.upc * a.B * a.Hq;
+    const int64_t kunits = ((int64_t)a.tpc + (int64_t)a.sp.tiles * a.sp.pieces) * a.B * a.Hkv;
+    if (qunits > 0x7fffffffLL || kunits > 0x7fffffffLL) return CP_EUNSUPPORTED;
+    const int rc = launch_delta(p, a, D, st);
+    if (rc) return rc;
+    float *delta = static_cast<float *>(p.workspace);
+    a.part = delta + bwd_workspace_bytes(a.B, a.Hq, a.S) / 4;
+    __nv_bfloat16 *dk = static_cast<__nv_bfloat16 *>(p.dk), *dv = static_cast<__nv_bfloat16 *>(p.dv);
+    bwd_dq_kernel<D, true><<<(unsigned)qunits, NTHREADS, DqCfg<D>::SMEM, st>>>(
+        mq, mk, mv, mdo64, a, p.lse, delta, static_cast<__nv_bfloat16 *>(p.dq),
+        static_cast<const __nv_bfloat16 *>(p.dout), pm);
+    if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
+    bwd_dkdv_kernel<D, true><<<(unsigned)kunits, NTHREADS, DkvCfg<D>::SMEM, st>>>(mq64, mk, mv, mdo64, a, p.lse, delta,
+                                                                                  dk, dv);
+    if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
+    return launch_window_sinks<D>(a.part, a.win, a.sp, a.B, a.Hkv, a.Sk, dk, dv, st);
+}
+
 template <int D>
 int launch_bwd_d(const BwdPtrs &p, BwdArgs a, cudaStream_t st)
 {
@@ -955,36 +1142,28 @@ int launch_bwd_d(const BwdPtrs &p, BwdArgs a, cudaStream_t st)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return CP_ECUDA;
     if (dev < 64 && !attr_done[dev]) {
-        if (cudaFuncSetAttribute(bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(bwd_dq_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  DqCfg<D>::SMEM) != cudaSuccess ||
-            cudaFuncSetAttribute(bwd_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            cudaFuncSetAttribute(bwd_dkdv_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  DkvCfg<D>::SMEM) != cudaSuccess)
             return CP_ECUDA;
         attr_done[dev] = true;
     }
     const Geom g = make_geom(a.S, a.N, a.layout, a.causal);
     float *delta = static_cast<float *>(p.workspace);
-
-    // Delta = rowsum(dO * out)
-    const int64_t rows = (int64_t)a.B * a.S * a.Hq;
-    int64_t blocks = (rows + 7) / 8;
-    const int64_t cap = (int64_t)sm_count() * 8;
-    if (blocks > cap) blocks = cap;
-    bwd_delta_kernel<<<(unsigned)blocks, 256, 0, st>>>(
-        static_cast<const __nv_bfloat16 *>(p.out), static_cast<const __nv_bfloat16 *>(p.dout), delta,
-        a.S, a.Hq, D, rows);
-    if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
+    const int rc = launch_delta(p, a, D, st);
+    if (rc) return rc;
 
     a.upc = (g.clen + T - 1) / T;
     a.tpc = (g.clen + T - 1) / T;
     const int64_t qunits = (int64_t)g.N * g.cpr * a.upc * a.B * a.Hq;
     const int64_t kunits = (int64_t)g.N * g.cpr * a.tpc * a.B * a.Hkv;
     if (qunits > 0x7fffffffLL || kunits > 0x7fffffffLL) return CP_EUNSUPPORTED;
-    bwd_dq_kernel<D><<<(unsigned)qunits, NTHREADS, DqCfg<D>::SMEM, st>>>(
+    bwd_dq_kernel<D, false><<<(unsigned)qunits, NTHREADS, DqCfg<D>::SMEM, st>>>(
         mq, mk, mv, mdo, a, p.lse, delta,
-        static_cast<__nv_bfloat16 *>(p.dq), static_cast<const __nv_bfloat16 *>(p.dout));
+        static_cast<__nv_bfloat16 *>(p.dq), static_cast<const __nv_bfloat16 *>(p.dout), NoMaps{});
     if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
-    bwd_dkdv_kernel<D><<<(unsigned)kunits, NTHREADS, DkvCfg<D>::SMEM, st>>>(
+    bwd_dkdv_kernel<D, false><<<(unsigned)kunits, NTHREADS, DkvCfg<D>::SMEM, st>>>(
         mq64, mk, mv, mdo64, a, p.lse, delta, static_cast<__nv_bfloat16 *>(p.dk),
         static_cast<__nv_bfloat16 *>(p.dv));
     return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ECUDA;
@@ -999,7 +1178,18 @@ size_t bwd_workspace_bytes(int B, int Hq, int64_t S)
     return (b + 255u) & ~(size_t)255u;
 }
 
-int launch_bwd_bf16(const BwdPtrs &p, const FwdArgs &f, cudaStream_t st)
+size_t window_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, int dtype, const Window &w)
+{
+    const int grp = Hq / Hkv, Sk = Sq + w.off;
+    const SinkPlan sp = dtype == CP_BF16 ? sink_plan<T>(w, Sq, Sk, grp) : sink_plan<WINDOW_F32_TILE>(w, Sq, Sk, grp);
+    size_t b = bwd_workspace_bytes(B, Hq, Sq);
+    if (sp.pieces) b += (size_t)B * Hkv * (size_t)window_part_rows(w, sp) * D * sizeof(float);
+    return (b + 255u) & ~(size_t)255u;
+}
+
+namespace {
+
+BwdArgs bwd_args(const FwdArgs &f)
 {
     BwdArgs a;
     a.B = f.B;
@@ -1015,6 +1205,25 @@ int launch_bwd_bf16(const BwdPtrs &p, const FwdArgs &f, cudaStream_t st)
     a.err = f.err;
     a.limit_ns = f.limit_ns;
     a.drain_ns = f.drain_ns;
+    a.Sk = f.Sk;
+    a.win = f.win;
+    a.sp = SinkPlan{0, 0, 1};
+    a.part = nullptr;
+    return a;
+}
+
+}  // namespace
+
+int launch_window_bwd_bf16(const BwdPtrs &p, const FwdArgs &f, cudaStream_t st)
+{
+    if (f.D == 64) return launch_window_d<64>(p, bwd_args(f), st);
+    if (f.D == 128) return launch_window_d<128>(p, bwd_args(f), st);
+    return CP_EUNSUPPORTED;
+}
+
+int launch_bwd_bf16(const BwdPtrs &p, const FwdArgs &f, cudaStream_t st)
+{
+    const BwdArgs a = bwd_args(f);
     if (f.D == 64) return launch_bwd_d<64>(p, a, st);
     if (f.D == 128) return launch_bwd_d<128>(p, a, st);
     return CP_EUNSUPPORTED;

@@ -265,6 +265,155 @@ struct KvIter {
     }
 };
 
+// What a query row sees of a windowed attention: key j is visible at position p
+// iff j <= p and (j > p - window or j < sinks).  Query row i of Sq stands at
+// position i + off (off = Sk - Sq: the rows are the last of the Sk keys).
+struct Window {
+    int off, window, sinks;
+    int pack;   // columns of a first tile that hold the sinks (a multiple of 16, at least sinks), or 0
+};
+
+// Walks the key tiles of a run of query rows at positions [p0, p1]: the sinks,
+// then the keys from the first row's window to the last row.  A few sinks in a
+// tile of their own would cost as much as TILE keys, so with pack > 0 they share
+// the first tile: its first `pk` columns are keys 0, 1, ..., the others go on from
+// lo.  Where sinks and window meet, the walk is one run of keys from 0.
+template <int TILE>
+struct WinIter {
+    int lo, end;      // keys [lo, end): those that some row has in its window
+    int se, pk;       // sinks outside that run; columns that they take in the first tile
+    int ns, nt, t;    // tiles of sinks alone, tiles, the current one
+    int sinks;
+
+    CP_HD void begin(const Window &w, int p0, int p1)
+    {
+        lo = p0 - w.window + 1 > 0 ? p0 - w.window + 1 : 0;
+        end = p1 + 1;
+        sinks = w.sinks;
+        se = pk = ns = t = 0;
+        if (sinks > 0 && lo > 0) {
+            if (sinks >= lo || w.pack >= lo) {
+                lo = 0;
+            } else {
+                se = sinks;
+                pk = w.pack;
+                if (!pk) ns = (se + TILE - 1) / TILE;
+            }
+        }
+        nt = ns + (end - lo + pk + TILE - 1) / TILE;
+    }
+    CP_HD bool valid() const { return t < nt; }
+    CP_HD bool packed() const { return pk > 0 && t == 0; }
+    // the key of column c is start() + c (but for the sinks of a packed tile)
+    CP_HD int start() const { return t < ns ? t * TILE : lo - pk + (t - ns) * TILE; }
+    CP_HD int len() const
+    {
+        const int l = (t < ns ? se : end) - start();
+        return l < TILE ? l : TILE;
+    }
+    // columns [0, sink_cols()) are sinks, visible to every row that is not before them
+    CP_HD int sink_cols() const { return packed() ? se : sinks - start(); }
+    // the first column of a row at position p's window
+    CP_HD int window_col(const Window &w, int p) const
+    {
+        const int c = p - w.window + 1 - start();
+        return packed() && c < pk ? pk : c;
+    }
+    // whether every row of [p0, p1] sees all TILE columns
+    CP_HD bool full(const Window &w, int p0, int p1) const
+    {
+        return len() == TILE && start() + TILE - 1 <= p0 && !packed() &&
+               (start() > p1 - w.window || sink_cols() >= TILE);
+    }
+    CP_HD void next() { ++t; }
+    CP_HD static int count(const Window &w, int p0, int p1)
+    {
+        WinIter it;
+        it.begin(w, p0, p1);
+        return it.nt;
+    }
+};
+
+// Windowed attention's key-stationary walk: the query tiles (per head of the GQA
+// group) that see the TILE keys from ks on.  Two kinds of unit:
+//   window  rows whose window reaches one of the keys;
+//   sinks   rows behind the window of a tile's sinks, in pieces of `each` tiles: a
+//           few keys that every later row sees, too long a walk for one block.
+template <int TILE>
+struct WinQIter {
+    int i0, i1;          // rows [i0, i1) that the unit's keys reach
+    int h0, per;         // first head of the group, tiles per head
+    int left;            // tiles to go
+    int hh, t;           // the current one: head of the group, tile of its rows
+
+    CP_HD void window(const Window &w, int Sq, int ks, int kl, int h0_, int grp)
+    {
+        const int64_t last = (int64_t)ks + kl - 1 + w.window - 1 - w.off;
+        set(ks - w.off, last + 1 < Sq ? (int)(last + 1) : Sq, h0_);
+        left = grp * per;
+        hh = t = 0;
+    }
+    CP_HD void sinks(const Window &w, int Sq, int ks, int h0_, int grp, int piece, int each)
+    {
+        const int64_t first = (int64_t)ks + w.window - w.off;
+        set(first < Sq ? (int)first : Sq, Sq, h0_);
+        const int all = grp * per, u = piece * each < all ? piece * each : all;
+        left = each < all - u ? each : all - u;
+        hh = per ? u / per : 0;
+        t = u - hh * per;
+    }
+    CP_HD void set(int a, int b, int h0_)
+    {
+        i0 = a > 0 ? a : 0;
+        i1 = b > i0 ? b : i0;
+        h0 = h0_;
+        per = (i1 - i0 + TILE - 1) / TILE;
+    }
+    CP_HD int count() const { return left; }
+    CP_HD int head() const { return h0 + hh; }
+    CP_HD int start() const { return i0 + t * TILE; }
+    CP_HD int len() const
+    {
+        const int l = i1 - start();
+        return l < TILE ? l : TILE;
+    }
+    CP_HD void next()
+    {
+        --left;
+        if (++t == per) t = 0, ++hh;
+    }
+};
+
+// How the sinks' walk is cut: tiles of sink keys, pieces per (batch, kv head, tile)
+// and query tiles of a piece -- as many as a window unit has, but not below 16.
+struct SinkPlan {
+    int tiles, pieces, each;
+};
+template <int TILE>
+CP_HD SinkPlan sink_plan(const Window &w, int Sq, int Sk, int grp)
+{
+    SinkPlan s{0, 0, 1};
+    const int64_t rows = (int64_t)Sq - ((int64_t)w.window - w.off > 0 ? (int64_t)w.window - w.off : 0);
+    if (w.sinks == 0 || rows <= 0) return s;     // no row is behind its window's first key
+    const int sinks = w.sinks < Sk ? w.sinks : Sk;
+    s.tiles = (sinks + TILE - 1) / TILE;
+    const int64_t all = (rows + TILE - 1) / TILE * grp;
+    int64_t each = ((int64_t)w.window / TILE + 2) * grp;
+    each = each < 16 ? 16 : each;
+    s.each = (int)(each < all ? each : all);
+    s.pieces = (int)((all + s.each - 1) / s.each);
+    return s;
+}
+
+// The low n bits.
+CP_HD uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// Of columns c0 .. c0 + 31, those that a row sees: below hi, and from lo on or below sc.
+CP_HD uint32_t visible_bits(int c0, int hi, int lo, int sc)
+{
+    return low_bits(hi - c0) & (~low_bits(lo - c0) | low_bits(sc - c0));
+}
+
 // A unit of work: `qrows` consecutive query rows of one chunk, for one
 // (batch, query head).  Units are numbered heads fastest, then batch, then by
 // descending position.

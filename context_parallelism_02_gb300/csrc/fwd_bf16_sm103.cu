@@ -52,6 +52,9 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <type_traits>
+
 #include "cp_common.cuh"
 #include "kernels.h"
 #include "tc_helpers.cuh"
@@ -152,7 +155,21 @@ __device__ __forceinline__ void issue_pv_seq(uint32_t tO, uint32_t tP, uint64_t 
 //               block's result is merged into the running state (stp.out_acc,
 //               stp.lse_acc) with the log-sum-exp form of the online-softmax
 //               rescaling, and optionally written rounded to bf16.
-enum { MODE_RING = 0, MODE_SPLIT = 1, MODE_STEP = 2 };
+//   MODE_WINDOW attention of the last a.S of a.Sk tokens with a sliding window and
+//               sinks (WinIter's walk).  The walk of a unit is short (window + 127
+//               keys), so it starts exactly at the first row's window, and a few
+//               sinks share its first tile by copies of their own.
+enum { MODE_RING = 0, MODE_SPLIT = 1, MODE_STEP = 2, MODE_WINDOW = 3 };
+
+// MODE_WINDOW's packed first tile: boxes of win.pack rows for the sinks and of
+// what is left of K's 256 and of V's 128 rows.
+struct PackMaps {
+    CUtensorMap k_sinks, k_rest, v_sinks, v_rest;
+};
+struct NoMaps {
+};
+template <int MODE>
+using ModeMaps = std::conditional_t<MODE == MODE_WINDOW, PackMaps, NoMaps>;
 
 // PERSIST: the block runs several work items in turn (fewer blocks than
 // items); otherwise it runs item blockIdx.x alone and its item loops run once,
@@ -162,10 +179,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdArgs a, const float sl2,
                     __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, const SplitOut so,
-                    const StepOut stp)
+                    const StepOut stp, const __grid_constant__ ModeMaps<MODE> pm_maps)
 {
     constexpr bool SPLIT = MODE == MODE_SPLIT;
     constexpr bool STEP = MODE == MODE_STEP;
+    constexpr bool WIN = MODE == MODE_WINDOW;
+    using Walk = std::conditional_t<WIN, WinIter<KT>, KvIter<KT>>;
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
@@ -187,6 +206,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // extents of the tensor maps' (rank, row) dimensions, for the debug-bounds build
     const int map_r = (!STEP && striped(g)) ? g.N : 1;
     const int map_rows = STEP ? C_loc : a.S / map_r;
+    const int map_keys = WIN ? a.Sk : map_rows;
+    auto start_walk = [&](Walk &it, const Unit &w) {
+        if constexpr (WIN) it.begin(a.win, w.q0 + a.win.off, w.qmax + a.win.off);
+        else if constexpr (STEP) it.begin_steps(g, w.r, w.qmax, stp.step_k, stp.step_k + 1);
+        else it.begin(g, w.r, w.qmax);
+    };
     // Work items: the launch's units (times the splits).  Split index slowest:
     // the blocks in flight run the same split of consecutive units, which walk
     // the same key tiles (as in an unsplit launch) and share them in L2;
@@ -216,8 +241,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         x.w = a.head_grouped ? decode_unit_grouped(g, a.B, a.Hq, a.upc, QT, ublk)
                              : decode_unit(g, a.B, a.Hq, a.rank_lo, a.rank_hi, a.upc, QT, ublk);
         x.kvh = x.w.h / (a.Hq / a.Hkv);
-        const int n_all = STEP ? KvIter<KT>::count(g, x.w.r, x.w.qmax, stp.step_k, stp.step_k + 1)
-                               : KvIter<KT>::count(g, x.w.r, x.w.qmax);
+        int n_all;
+        if constexpr (WIN) n_all = WinIter<KT>::count(a.win, x.w.q0 + a.win.off, x.w.qmax + a.win.off);
+        else n_all = STEP ? KvIter<KT>::count(g, x.w.r, x.w.qmax, stp.step_k, stp.step_k + 1)
+                          : KvIter<KT>::count(g, x.w.r, x.w.qmax);
         x.j0 = SPLIT ? (int)((int64_t)n_all * x.sp / so.n) : 0;
         x.n = SPLIT ? (int)((int64_t)n_all * (x.sp + 1) / so.n) - x.j0 : n_all;
         return x;
@@ -299,20 +326,34 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 int it2 = it + 1;
                 Item y = x;
                 // K runs one tile ahead of V; the V loads reuse the K tile starts
-                KvIter<KT> itk;
-                if (STEP)
-                    itk.begin_steps(g, x.w.r, x.w.qmax, stp.step_k, stp.step_k + 1);
-                else
-                    itk.begin(g, x.w.r, x.w.qmax);
-                if (SPLIT) itk.skip(x.j0);
+                Walk itk;
+                start_walk(itk, x.w);
+                if constexpr (SPLIT) itk.skip(x.j0);
                 int kr_cur = 0, kw_cur = 0, kr_next = 0, kw_next = 0;   // map coordinates (rank, row)
                 const int kvh = dbg_coord(a.err, x.kvh, a.Hkv), qb = dbg_coord(a.err, x.w.b, a.B);
                 auto load_k = [&]() -> bool {   // the next K tile, global index nk
                     const int st = nk & 1;
                     if (nk >= 2 && !wait1(BAR(B_KEMPTY + st), ((nk >> 1) - 1) & 1, wc)) return false;
                     mbar_arrive_expect_tx(BAR(B_KFULL + st), C::KBYTES);
-                    kr_next = dbg_coord(a.err, STEP ? 0 : itk.mrank(), map_r);
-                    kw_next = dbg_coord(a.err, STEP ? itk.lrow() : itk.mrow(), map_rows);
+                    if constexpr (WIN) {
+                        kw_next = itk.start();
+                        if (itk.packed()) {
+                            const int row = dbg_coord(a.err, kw_next + itk.pk, map_keys);
+                            for (int bx = 0; bx < D / 64; ++bx) {
+                                const uint32_t dst = sK + st * C::KBYTES + bx * C::KBOX;
+                                tma_load5(dst, &pm_maps.k_sinks, BAR(B_KFULL + st), bx * 64, kvh, 0, 0, qb, pol_kv);
+                                tma_load5(dst + itk.pk * 128, &pm_maps.k_rest, BAR(B_KFULL + st), bx * 64, kvh, 0,
+                                          row, qb, pol_kv);
+                            }
+                            itk.next();
+                            ++nk;
+                            return true;
+                        }
+                        kw_next = dbg_coord(a.err, kw_next, map_keys);
+                    } else {
+                        kr_next = dbg_coord(a.err, STEP ? 0 : itk.mrank(), map_r);
+                        kw_next = dbg_coord(a.err, STEP ? itk.lrow() : itk.mrow(), map_rows);
+                    }
                     for (int bx = 0; bx < D / 64; ++bx)
                         tma_load5(sK + st * C::KBYTES + bx * C::KBOX, &tmK, BAR(B_KFULL + st), bx * 64,
                                   kvh, kr_next, kw_next, qb, pol_kv);
@@ -320,6 +361,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     ++nk;
                     return true;
                 };
+                int pk = 0;   // columns of a packed first tile that hold the sinks
+                if constexpr (WIN) pk = itk.pk;
                 ok = load_k();
                 const bool have2 = PERSIST && next_busy(it2, y);
                 for (int j = 0; ok && j < x.n; ++j) {
@@ -337,6 +380,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             break;
                         }
                         mbar_arrive_expect_tx(BAR(B_VFULL + hh), C::VBYTES);
+                        if constexpr (WIN) {
+                            if (hh == 0 && j == 0 && pk > 0) {   // the packed tile's first half
+                                for (int bx = 0; bx < D / 64; ++bx) {
+                                    const uint32_t dst = sV + bx * 16384;
+                                    tma_load5(dst, &pm_maps.v_sinks, BAR(B_VFULL), bx * 64, kvh, 0, 0, qb, pol_kv);
+                                    tma_load5(dst + pk * 128, &pm_maps.v_rest, BAR(B_VFULL), bx * 64, kvh, 0,
+                                              dbg_coord(a.err, kw_cur + pk, map_keys), qb, pol_kv);
+                                }
+                                ++nv;
+                                continue;
+                            }
+                        }
                         for (int bx = 0; bx < D / 64; ++bx)
                             tma_load5(sV + hh * C::VBYTES + bx * 16384, &tmV, BAR(B_VFULL + hh), bx * 64,
                                       kvh, kr_cur, kw_cur + 128 * hh, qb, pol_kv);
@@ -532,12 +587,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             float m_run = NEG_INF, l_run = 0.f;      // l_run: this half's share of the row sum
 
-            KvIter<KT> kit;
-            if (STEP)
-                kit.begin_steps(g, w.r, w.qmax, stp.step_k, stp.step_k + 1);
-            else
-                kit.begin(g, w.r, w.qmax);
-            if (SPLIT) kit.skip(x.j0);
+            Walk kit;
+            start_walk(kit, w);
+            if constexpr (SPLIT) kit.skip(x.j0);
             for (int j = 0; j < n; ++j, ++nt, ++nx, kit.next()) {
                 if (!waitw(BAR(B_SFULL), nt & 1, wc)) {
                     ok = false;
@@ -554,7 +606,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 float *s = reinterpret_cast<float *>(sr);
                 const int ks = kit.start();
                 const int kl = kit.len();
-                if (kl < KT || (a.causal && ks + kl - 1 > w.q0 + kit.shift)) {
+                if constexpr (WIN) {
+                    const int p0 = w.q0 + a.win.off;
+                    if (!kit.full(a.win, p0, w.qmax + a.win.off)) {
+                        const int p = qpos + a.win.off;
+                        const int hi = (p - ks + 1 < kl ? p - ks + 1 : kl) - 128 * half;
+                        const int lo = kit.window_col(a.win, p) - 128 * half;
+                        const int sc = kit.sink_cols() - 128 * half;
+#pragma unroll
+                        for (int c0 = 0; c0 < 128; c0 += 32) {
+                            const uint32_t see = visible_bits(c0, hi, lo, sc);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(see >> c & 1u)) s[c0 + c] = NEG_INF;
+                        }
+                    }
+                } else if (kl < KT || (a.causal && ks + kl - 1 > w.q0 + kit.shift)) {
                     // partial tile: key columns [0, lim) of the 256 are visible to this row
                     int lim = kl;
                     if (a.causal) {
@@ -864,6 +931,7 @@ template <int D, int MODE>
 int launch_d(const void *q, const void *k, const void *v, void *out, float *lse, FwdArgs a,
              const SplitOut &so, const StepOut &stp, cudaStream_t st)
 {
+    static_assert(MODE != MODE_WINDOW, "launch_window_d");
     CUtensorMap mq, mk, mv;
     const Geom g = make_geom(a.S, a.N, a.layout, a.causal);
     if (MODE == MODE_STEP) {
@@ -926,14 +994,64 @@ int launch_d(const void *q, const void *k, const void *v, void *out, float *lse,
     const float sl2 = a.scale * 1.4426950408889634f;
     if (blocks < items)
         fwd_bf16_kernel<D, MODE, true><<<(unsigned)blocks, NTHREADS, Cfg<D>::SMEM, st>>>(
-            mq, mk, mv, a, sl2, reinterpret_cast<__nv_bfloat16 *>(out), lse, so, stp);
+            mq, mk, mv, a, sl2, reinterpret_cast<__nv_bfloat16 *>(out), lse, so, stp, NoMaps{});
     else
         fwd_bf16_kernel<D, MODE, false><<<(unsigned)blocks, NTHREADS, Cfg<D>::SMEM, st>>>(
-            mq, mk, mv, a, sl2, reinterpret_cast<__nv_bfloat16 *>(out), lse, so, stp);
+            mq, mk, mv, a, sl2, reinterpret_cast<__nv_bfloat16 *>(out), lse, so, stp, NoMaps{});
+    return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ECUDA;
+}
+
+// Windowed attention.  Units differ little in work (all but those of the first
+// window walk window + 127 keys) and are short, so one persistent block per SM
+// takes them in turn, whatever their number.
+template <int D>
+int launch_window_d(const void *q, const void *k, const void *v, void *out, float *lse, FwdArgs a, cudaStream_t st)
+{
+    CUtensorMap mq, mk, mv;
+    PackMaps pm;
+    const int pack = a.win.pack;
+    if (!make_map(&mq, q, a.B, a.S, a.Hq, D, 128) || !make_map(&mk, k, a.B, a.Sk, a.Hkv, D, KT) ||
+        !make_map(&mv, v, a.B, a.Sk, a.Hkv, D, 128))
+        return CP_ECUDA;
+    if (!make_map(&pm.k_sinks, k, a.B, a.Sk, a.Hkv, D, pack ? pack : 16) ||
+        !make_map(&pm.k_rest, k, a.B, a.Sk, a.Hkv, D, KT - pack) ||
+        !make_map(&pm.v_sinks, v, a.B, a.Sk, a.Hkv, D, pack ? pack : 16) ||
+        !make_map(&pm.v_rest, v, a.B, a.Sk, a.Hkv, D, 128 - pack))
+        return CP_ECUDA;
+    auto kernel = fwd_bf16_kernel<D, MODE_WINDOW, true>;
+    static std::atomic<bool> attr_done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return CP_ECUDA;
+    if (dev >= 64 || !attr_done[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM) != cudaSuccess)
+            return CP_ECUDA;
+        if (dev < 64) attr_done[dev].store(true, std::memory_order_release);
+    }
+    a.upc = (a.S + QT - 1) / QT;
+    a.head_grouped = 0;
+    const int64_t units = (int64_t)a.upc * a.B * a.Hq;
+    if (units > 0x7fffffffLL) return CP_EUNSUPPORTED;
+    a.n_units = (int)units;
+    int64_t blocks = sm_count();
+    const int cap = fwd_grid_limit();   // test hook
+    if (cap > 0) blocks = cap;
+    if (blocks > units) blocks = units;
+    const SplitOut none{1, nullptr, nullptr};
+    const StepOut nostep{0, 0, nullptr, nullptr, nullptr};
+    kernel<<<(unsigned)blocks, NTHREADS, Cfg<D>::SMEM, st>>>(mq, mk, mv, a, a.scale * 1.4426950408889634f,
+                                                             static_cast<__nv_bfloat16 *>(out), lse, none, nostep, pm);
     return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 
 }  // namespace
+
+int launch_window_fwd_bf16(const void *q, const void *k, const void *v, void *out, float *lse, FwdArgs a,
+                           cudaStream_t st)
+{
+    if (a.D == 64) return launch_window_d<64>(q, k, v, out, lse, a, st);
+    if (a.D == 128) return launch_window_d<128>(q, k, v, out, lse, a, st);
+    return CP_EUNSUPPORTED;
+}
 
 int launch_fwd_bf16(const void *q, const void *k, const void *v, void *out, float *lse,
                     FwdArgs a, cudaStream_t st)

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "cp_common.cuh"
+
 namespace cp {
 
 struct FwdArgs {
@@ -19,6 +21,8 @@ struct FwdArgs {
     unsigned *err;        // device error word
     uint64_t limit_ns;    // bound of every pipeline wait
     uint64_t drain_ns;    // bound of the waits that drain copies and MMAs before exit
+    int Sk;               // windowed attention: keys (S counts query rows)
+    Window win;           // windowed attention
 };
 
 // Partial results of a split forward (fp32, normalised): n splits of every
@@ -51,6 +55,11 @@ int launch_fwd_bf16(const void *q, const void *k, const void *v, void *out, floa
                     FwdArgs a, cudaStream_t st);
 int launch_fwd_bf16_split(const void *q, const void *k, const void *v, FwdArgs a,
                           const SplitOut &so, cudaStream_t st);
+// Windowed attention (a.S query rows, a.Sk keys, a.win; N 1, contiguous, causal).
+int launch_window_fwd_bf16(const void *q, const void *k, const void *v, void *out, float *lse,
+                           FwdArgs a, cudaStream_t st);
+int launch_window_fwd_f32(const float *q, const float *k, const float *v, float *out, float *lse,
+                          const FwdArgs &a, cudaStream_t st);
 // Merge the so.n partials of the rows of ranks [a.rank_lo, a.rank_hi) into
 // out (bf16, [B][S][Hq][D]) and lse ([B][Hq][S]).
 int launch_fwd_split_combine(const FwdArgs &a, const SplitOut &so, void *out, float *lse,
@@ -79,6 +88,13 @@ int launch_bwd_bf16(const BwdPtrs &p, const FwdArgs &a, cudaStream_t st);
 // fp32 inputs/outputs, fp64 arithmetic; does not touch p.workspace
 int launch_bwd_f32(const BwdPtrs &p, const FwdArgs &a, cudaStream_t st);
 size_t bwd_workspace_bytes(int B, int Hq, int64_t S);
+// Windowed attention's gradients; the workspace is window_bwd_workspace_bytes() bytes.
+int launch_window_bwd_bf16(const BwdPtrs &p, const FwdArgs &a, cudaStream_t st);
+int launch_window_bwd_f32(const BwdPtrs &p, const FwdArgs &a, cudaStream_t st);
+size_t window_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, int dtype, const Window &w);
+// Columns of a first tile that hold the sinks, a multiple of 16; 0: too many to share one.
+constexpr int WINDOW_MAX_PACK = 64;
+inline int window_pack(int sinks) { return sinks <= WINDOW_MAX_PACK ? (sinks + 15) / 16 * 16 : 0; }
 
 // Number of SMs of the current device (cached per device).
 int sm_count();

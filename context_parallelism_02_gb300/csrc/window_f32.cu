@@ -1,0 +1,485 @@
+// window_f32.cu -- windowed attention with sinks on fp32 tensors, forward and backward,
+// on the CUDA cores in fp32 arithmetic (bounded by the FMA pipe: no tensor-core kind
+// holds fp32's 24 bits).
+//
+// Tiles of 64 rows by 64 keys, 256 threads as 16 x 16, each with a 4 x 4 part of the
+// scores (rows ty + 16 i, columns tx + 16 j) and of the 64 x D products 4 rows by D / 16
+// columns (4 tx + 64 j).  Per four elements of the inner axis a thread reads 8 x 16 bytes
+// of shared memory for 64 FMAs.  The walks are those of the bf16 kernels: WinIter for the
+// query-stationary kernels, WinQIter and the sinks' pieces for dK and dV; every output
+// element is written once.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "cp_common.cuh"
+#include "kernels.h"
+#include "window_sinks.cuh"
+
+namespace cp {
+
+namespace {
+
+constexpr int T = WINDOW_F32_TILE;
+constexpr int THREADS = 256;
+constexpr int PS = T + 4;             // row stride of a T x T tile in shared memory
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994530942f;
+
+template <int D>
+struct Rows {
+    static constexpr int STRIDE = D + 4;        // a warp's 8 rows of 16 bytes fall on 32 banks
+    static constexpr int FLOATS = T * STRIDE;
+};
+
+struct Args {
+    const float *q, *k, *v, *out, *dout, *lse;
+    float *delta, *part;
+    int B, Hq, Hkv, Sq, Sk;
+    float scale;
+    Window win;
+    SinkPlan sp;
+};
+
+// n rows of x [B][S][H][D] (head h, from row r0) into shared memory, the rest 0.
+template <int D>
+__device__ __forceinline__ void load_rows(float *dst, const float *x, int64_t b, int S, int H, int h, int r0, int n)
+{
+    for (int i = threadIdx.x; i < T * (D / 4); i += THREADS) {
+        const int r = i / (D / 4), c = i % (D / 4);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < n) v = *reinterpret_cast<const float4 *>(x + ((b * S + r0 + r) * H + h) * D + c * 4);
+        *reinterpret_cast<float4 *>(dst + r * Rows<D>::STRIDE + c * 4) = v;
+    }
+}
+
+// acc[i][j] = A[ty + 16 i] . B[tx + 16 j]
+template <int D>
+__device__ __forceinline__ void dots(const float *A, const float *B, float (&acc)[4][4])
+{
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = *reinterpret_cast<const float4 *>(A + (ty + 16 * i) * Rows<D>::STRIDE + d);
+            b[i] = *reinterpret_cast<const float4 *>(B + (tx + 16 * i) * Rows<D>::STRIDE + d);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
+                acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
+                acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
+                acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+            }
+    }
+}
+
+// acc[i][4 j + e] += sum_k P[ty + 16 i][k] B[k][4 tx + 64 j + e]
+template <int D>
+__device__ __forceinline__ void product(const float *P, const float *B, float (&acc)[4][D / 16])
+{
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 2
+    for (int k = 0; k < T; k += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(P + (ty + 16 * i) * PS + k);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const float4 b = *reinterpret_cast<const float4 *>(B + (k + kk) * Rows<D>::STRIDE + 4 * tx + 64 * j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                    acc[i][4 * j + 0] = fmaf(x, b.x, acc[i][4 * j + 0]);
+                    acc[i][4 * j + 1] = fmaf(x, b.y, acc[i][4 * j + 1]);
+                    acc[i][4 * j + 2] = fmaf(x, b.z, acc[i][4 * j + 2]);
+                    acc[i][4 * j + 3] = fmaf(x, b.w, acc[i][4 * j + 3]);
+                }
+            }
+    }
+}
+
+// What thread row i of the walk's current tile sees: columns [lo, hi) and [0, sc).
+struct Seen {
+    int lo, hi, sc;
+    __device__ __forceinline__ Seen(const WinIter<T> &it, const Window &w, int p)
+    {
+        const int kl = it.len(), ks = it.start();
+        hi = p - ks + 1 < kl ? p - ks + 1 : kl;
+        lo = it.window_col(w, p);
+        sc = it.sink_cols();
+    }
+    __device__ __forceinline__ bool at(int c) const { return c < hi && (c >= lo || c < sc); }
+};
+
+__device__ __forceinline__ float row_max(float x)   // over the 16 threads of a row
+{
+#pragma unroll
+    for (int o = 8; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+__device__ __forceinline__ float row_sum(float x)
+{
+#pragma unroll
+    for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// The unit's 64 query rows: heads fastest, so that the heads of a group share K and V in L2.
+struct QUnit {
+    int b, h, kvh, q0, rows;
+    __device__ __forceinline__ QUnit(const Args &a)
+    {
+        unsigned u = blockIdx.x;
+        h = (int)(u % (unsigned)a.Hq);
+        u /= (unsigned)a.Hq;
+        b = (int)(u % (unsigned)a.B);
+        q0 = (int)(u / (unsigned)a.B) * T;
+        kvh = h / (a.Hq / a.Hkv);
+        rows = a.Sq - q0 < T ? a.Sq - q0 : T;
+    }
+};
+
+// Rows of K or V for the walk's current tile.  No packed tiles here (win.pack is 0).
+template <int D>
+__device__ __forceinline__ void load_keys(float *dst, const float *x, const Args &a, const QUnit &u, const WinIter<T> &it)
+{
+    load_rows<D>(dst, x, u.b, a.Sk, a.Hkv, u.kvh, it.start(), it.len());
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS) window_f32_fwd_kernel(const Args a, float *__restrict__ out, float *__restrict__ lse)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *Q = sm, *K = Q + Rows<D>::FLOATS, *V = K + Rows<D>::FLOATS, *P = V + Rows<D>::FLOATS;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const QUnit u(a);
+    load_rows<D>(Q, a.q, u.b, a.Sq, a.Hq, u.h, u.q0, u.rows);
+    const float sl2 = a.scale * LOG2E;
+    float o[4][D / 16], m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) o[i][j] = 0.f;
+    }
+    const int p0 = u.q0 + a.win.off, p1 = p0 + u.rows - 1;
+    WinIter<T> it;
+    for (it.begin(a.win, p0, p1); it.valid(); it.next()) {
+        __syncthreads();
+        load_keys<D>(K, a.k, a, u, it);
+        load_keys<D>(V, a.v, a, u, it);
+        __syncthreads();
+        float x[4][4];
+        dots<D>(Q, K, x);
+        const bool full = it.full(a.win, p0, p1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Seen see(it, a.win, p0 + ty + 16 * i);
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[i][j] = full || see.at(tx + 16 * j) ? x[i][j] * sl2 : -INFINITY;
+                top = fmaxf(top, x[i][j]);
+            }
+            const float mn = fmaxf(m[i], row_max(top)), base = mn == -INFINITY ? 0.f : mn;
+            const float f = exp2f(m[i] - base);   // 0 where nothing was seen before
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[i][j] = exp2f(x[i][j] - base);
+                sum += x[i][j];
+                P[(ty + 16 * i) * PS + tx + 16 * j] = x[i][j];
+            }
+            l[i] = l[i] * f + row_sum(sum);
+            m[i] = mn;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) o[i][j] *= f;
+        }
+        __syncthreads();
+        product<D>(P, V, o);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty + 16 * i;
+        if (r >= u.rows) continue;
+        const float inv = l[i] > 0.f ? 1.f / l[i] : l[i];
+        float *row = out + (((int64_t)u.b * a.Sq + u.q0 + r) * a.Hq + u.h) * D;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+            *reinterpret_cast<float4 *>(row + 4 * tx + 64 * j) =
+                make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv);
+        if (tx == 0) lse[((int64_t)u.b * a.Hq + u.h) * a.Sq + u.q0 + r] = l[i] > 0.f ? fmaf(m[i], LN2, logf(l[i])) : -INFINITY;
+    }
+}
+
+// Delta = rowsum(dO * out), a warp a row.
+template <int D>
+__global__ void __launch_bounds__(THREADS) window_f32_delta_kernel(const Args a)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = (int64_t)a.B * a.Sq * a.Hq, step = (int64_t)gridDim.x * (THREADS / 32);
+    for (int64_t r = (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5); r < rows; r += step) {
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) s = fmaf(a.dout[r * D + lane + 32 * e], a.out[r * D + lane + 32 * e], s);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const int64_t bs = r / a.Hq, h = r % a.Hq, b = bs / a.Sq;
+        if (lane == 0) a.delta[(b * a.Hq + h) * a.Sq + bs % a.Sq] = s;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS) window_f32_dq_kernel(const Args a, float *__restrict__ dq)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *Q = sm, *G = Q + Rows<D>::FLOATS, *K = G + Rows<D>::FLOATS, *V = K + Rows<D>::FLOATS, *P = V + Rows<D>::FLOATS;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const QUnit u(a);
+    load_rows<D>(Q, a.q, u.b, a.Sq, a.Hq, u.h, u.q0, u.rows);
+    load_rows<D>(G, a.dout, u.b, a.Sq, a.Hq, u.h, u.q0, u.rows);
+    const float sl2 = a.scale * LOG2E;
+    float acc[4][D / 16], lse2[4], delta[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty + 16 * i;
+        const int64_t at = ((int64_t)u.b * a.Hq + u.h) * a.Sq + u.q0 + r;
+        lse2[i] = r < u.rows ? a.lse[at] * LOG2E : 0.f;
+        delta[i] = r < u.rows ? a.delta[at] : 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) acc[i][j] = 0.f;
+    }
+    const int p0 = u.q0 + a.win.off, p1 = p0 + u.rows - 1;
+    WinIter<T> it;
+    for (it.begin(a.win, p0, p1); it.valid(); it.next()) {
+        __syncthreads();
+        load_keys<D>(K, a.k, a, u, it);
+        load_keys<D>(V, a.v, a, u, it);
+        __syncthreads();
+        float x[4][4], g[4][4];
+        dots<D>(Q, K, x);
+        dots<D>(G, V, g);
+        const bool full = it.full(a.win, p0, p1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Seen see(it, a.win, p0 + ty + 16 * i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool on = full || see.at(tx + 16 * j);
+                P[(ty + 16 * i) * PS + tx + 16 * j] = on ? exp2f(fmaf(x[i][j], sl2, -lse2[i])) * (g[i][j] - delta[i]) : 0.f;
+            }
+        }
+        __syncthreads();
+        product<D>(P, K, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty + 16 * i;
+        if (r >= u.rows) continue;
+        float *row = dq + (((int64_t)u.b * a.Sq + u.q0 + r) * a.Hq + u.h) * D;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+            *reinterpret_cast<float4 *>(row + 4 * tx + 64 * j) =
+                make_float4(acc[i][4 * j] * a.scale, acc[i][4 * j + 1] * a.scale, acc[i][4 * j + 2] * a.scale,
+                            acc[i][4 * j + 3] * a.scale);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS) window_f32_dkdv_kernel(const Args a, float *__restrict__ dk, float *__restrict__ dv)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *K = sm, *V = K + Rows<D>::FLOATS, *Q = V + Rows<D>::FLOATS, *G = Q + Rows<D>::FLOATS;
+    float *P = G + Rows<D>::FLOATS, *S = P + T * PS, *lse2 = S + T * PS, *delta = lse2 + T;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, grp = a.Hq / a.Hkv;
+    const int tpc = (a.Sk + T - 1) / T;
+    // window units, then the pieces of the tiles of sinks
+    int piece = 0, t, kvh, b;
+    unsigned x = blockIdx.x;
+    if (x < (unsigned)tpc * a.B * a.Hkv) {
+        t = (int)(x % (unsigned)tpc);
+        x /= (unsigned)tpc;
+    } else {
+        x -= (unsigned)tpc * a.B * a.Hkv;
+        piece = 1 + (int)(x % (unsigned)a.sp.pieces);
+        x /= (unsigned)a.sp.pieces;
+        t = (int)(x % (unsigned)a.sp.tiles);
+        x /= (unsigned)a.sp.tiles;
+    }
+    kvh = (int)(x % (unsigned)a.Hkv);
+    b = (int)(x / (unsigned)a.Hkv);
+    const int ks = t * T, kl = a.Sk - ks < T ? a.Sk - ks : T;
+    load_rows<D>(K, a.k, b, a.Sk, a.Hkv, kvh, ks, kl);
+    load_rows<D>(V, a.v, b, a.Sk, a.Hkv, kvh, ks, kl);
+    float adk[4][D / 16], adv[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) adk[i][j] = adv[i][j] = 0.f;
+    const float sl2 = a.scale * LOG2E;
+    WinQIter<T> it;
+    if (piece == 0) it.window(a.win, a.Sq, ks, kl, kvh * grp, grp);
+    else it.sinks(a.win, a.Sq, ks, kvh * grp, grp, piece - 1, a.sp.each);
+    for (; it.count() > 0; it.next()) {
+        const int h = it.head(), qa = it.start(), ql = it.len();
+        __syncthreads();
+        load_rows<D>(Q, a.q, b, a.Sq, a.Hq, h, qa, ql);
+        load_rows<D>(G, a.dout, b, a.Sq, a.Hq, h, qa, ql);
+        if (threadIdx.x < T) {
+            const int64_t at = ((int64_t)b * a.Hq + h) * a.Sq + qa + threadIdx.x;
+            lse2[threadIdx.x] = threadIdx.x < ql ? a.lse[at] * LOG2E : 0.f;
+            delta[threadIdx.x] = threadIdx.x < ql ? a.delta[at] : 0.f;
+        }
+        __syncthreads();
+        float s[4][4], g[4][4];
+        dots<D>(K, Q, s);
+        dots<D>(V, G, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int kpos = ks + ty + 16 * i;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = tx + 16 * j, back = qa + c + a.win.off - kpos;   // how far the key lies behind the row
+                const bool on = c < ql && (piece == 0 ? back >= 0 && back < a.win.window
+                                                      : kpos < a.win.sinks && back >= a.win.window);
+                const float p = on ? exp2f(fmaf(s[i][j], sl2, -lse2[c])) : 0.f;
+                P[(ty + 16 * i) * PS + c] = p;
+                S[(ty + 16 * i) * PS + c] = on ? p * (g[i][j] - delta[c]) : 0.f;
+            }
+        }
+        __syncthreads();
+        product<D>(P, G, adv);
+        product<D>(S, Q, adk);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty + 16 * i, kpos = ks + r;
+        if (r >= kl) continue;
+        const bool sink = a.sp.pieces > 0 && kpos < a.win.sinks;
+        if (!sink && piece != 0) continue;
+        const int64_t at = (((int64_t)b * a.Sk + kpos) * a.Hkv + kvh) * D;
+        float *slot = a.part + (((int64_t)b * a.Hkv + kvh) * window_part_rows(a.win, a.sp) + (int64_t)piece * 2 * a.win.sinks + kpos) * D;
+        float *rk = sink ? slot : dk + at, *rv = sink ? slot + (int64_t)a.win.sinks * D : dv + at;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            const int c = 4 * tx + 64 * j;
+            *reinterpret_cast<float4 *>(rk + c) = make_float4(adk[i][4 * j] * a.scale, adk[i][4 * j + 1] * a.scale,
+                                                             adk[i][4 * j + 2] * a.scale, adk[i][4 * j + 3] * a.scale);
+            *reinterpret_cast<float4 *>(rv + c) = make_float4(adv[i][4 * j], adv[i][4 * j + 1], adv[i][4 * j + 2], adv[i][4 * j + 3]);
+        }
+    }
+}
+
+template <int D>
+constexpr int SMEM_FWD = (3 * Rows<D>::FLOATS + T * PS) * 4;
+template <int D>
+constexpr int SMEM_DQ = (4 * Rows<D>::FLOATS + T * PS) * 4;
+template <int D>
+constexpr int SMEM_DKDV = (4 * Rows<D>::FLOATS + 2 * T * PS + 2 * T) * 4;
+
+template <int D>
+int prepare()   // the kernels' shared memory, once per device
+{
+    static_assert(SMEM_DKDV<D> <= 232448, "shared memory");
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return CP_ECUDA;
+    if (dev < 64 && done[dev].load(std::memory_order_acquire)) return CP_OK;
+    const cudaFuncAttribute what = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if (cudaFuncSetAttribute(window_f32_fwd_kernel<D>, what, SMEM_FWD<D>) != cudaSuccess ||
+        cudaFuncSetAttribute(window_f32_dq_kernel<D>, what, SMEM_DQ<D>) != cudaSuccess ||
+        cudaFuncSetAttribute(window_f32_dkdv_kernel<D>, what, SMEM_DKDV<D>) != cudaSuccess)
+        return CP_ECUDA;
+    if (dev < 64) done[dev].store(true, std::memory_order_release);
+    return CP_OK;
+}
+
+Args make_args(const FwdArgs &f)
+{
+    Args a{};
+    a.B = f.B;
+    a.Hq = f.Hq;
+    a.Hkv = f.Hkv;
+    a.Sq = f.S;
+    a.Sk = f.Sk;
+    a.scale = f.scale;
+    a.win = f.win;
+    a.win.pack = 0;
+    a.sp = sink_plan<T>(a.win, a.Sq, a.Sk, a.Hq / a.Hkv);
+    return a;
+}
+
+template <int D>
+int forward(const Args &a, float *out, float *lse, cudaStream_t st)
+{
+    const int rc = prepare<D>();
+    if (rc) return rc;
+    const int64_t units = (int64_t)((a.Sq + T - 1) / T) * a.B * a.Hq;
+    if (units > 0x7fffffffLL) return CP_EUNSUPPORTED;
+    window_f32_fwd_kernel<D><<<(unsigned)units, THREADS, SMEM_FWD<D>, st>>>(a, out, lse);
+    return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ECUDA;
+}
+
+template <int D>
+int backward(const Args &a, float *dq, float *dk, float *dv, cudaStream_t st)
+{
+    const int rc = prepare<D>();
+    if (rc) return rc;
+    const int64_t units = (int64_t)((a.Sq + T - 1) / T) * a.B * a.Hq;
+    const int64_t kunits = ((int64_t)((a.Sk + T - 1) / T) + (int64_t)a.sp.tiles * a.sp.pieces) * a.B * a.Hkv;
+    if (units > 0x7fffffffLL || kunits > 0x7fffffffLL) return CP_EUNSUPPORTED;
+    const int64_t rows = (int64_t)a.B * a.Sq * a.Hq, cap = (int64_t)sm_count() * 8;
+    const int64_t blocks = (rows + 7) / 8 < cap ? (rows + 7) / 8 : cap;
+    window_f32_delta_kernel<D><<<(unsigned)blocks, THREADS, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
+    window_f32_dq_kernel<D><<<(unsigned)units, THREADS, SMEM_DQ<D>, st>>>(a, dq);
+    if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
+    window_f32_dkdv_kernel<D><<<(unsigned)kunits, THREADS, SMEM_DKDV<D>, st>>>(a, dk, dv);
+    if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
+    return launch_window_sinks<D>(a.part, a.win, a.sp, a.B, a.Hkv, a.Sk, dk, dv, st);
+}
+
+}  // namespace
+
+int launch_window_fwd_f32(const float *q, const float *k, const float *v, float *out, float *lse, const FwdArgs &f,
+                          cudaStream_t st)
+{
+    Args a = make_args(f);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    if (f.D == 64) return forward<64>(a, out, lse, st);
+    if (f.D == 128) return forward<128>(a, out, lse, st);
+    return CP_EUNSUPPORTED;
+}
+
+int launch_window_bwd_f32(const BwdPtrs &p, const FwdArgs &f, cudaStream_t st)
+{
+    Args a = make_args(f);
+    a.q = static_cast<const float *>(p.q);
+    a.k = static_cast<const float *>(p.k);
+    a.v = static_cast<const float *>(p.v);
+    a.out = static_cast<const float *>(p.out);
+    a.dout = static_cast<const float *>(p.dout);
+    a.lse = p.lse;
+    a.delta = static_cast<float *>(p.workspace);
+    a.part = a.delta + bwd_workspace_bytes(a.B, a.Hq, a.Sq) / 4;
+    float *dq = static_cast<float *>(p.dq), *dk = static_cast<float *>(p.dk), *dv = static_cast<float *>(p.dv);
+    if (f.D == 64) return backward<64>(a, dq, dk, dv, st);
+    if (f.D == 128) return backward<128>(a, dq, dk, dv, st);
+    return CP_EUNSUPPORTED;
+}
+
+}  // namespace cp

@@ -355,6 +355,50 @@ int ring_attn_bwd_noalloc(const void *q, const void *k, const void *v, const voi
                           int dtype, float scale, void *stream);
 
 /*
+ * window_attn_fwd -- causal attention with a sliding window and a few first tokens
+ * that stay visible (sinks).  Query row i stands at position p = i + Sk - Sq, the rows
+ * being the last Sq of the Sk tokens, and sees key j iff
+ *   j <= p and (j > p - window or j < sinks):
+ * itself, the window - 1 tokens before it and the first `sinks` tokens.  Sq = Sk is a
+ * whole prompt or a training step; Sq < Sk a chunk behind earlier tokens, or the shard of
+ * a context-parallel rank behind its halo: the rank's k and v are then the sinks' rows,
+ * the window - 1 rows before its shard and its own, since only distances inside the
+ * window and the number of the sinks matter (a rank whose halo reaches the sinks passes
+ * all rows from 0 on).
+ *   q [B][Sq][Hq][D], k, v [B][Sk][Hkv][D], out [B][Sq][Hq][D]: device, dtype CP_BF16 or
+ *   CP_F32; lse [B][Hq][Sq] fp32, natural log.  D in {64, 128}; Hq % Hkv == 0.
+ *   window >= 1 (Sk and more: no limit), sinks >= 0; scale <= 0 selects 1/sqrt(D).
+ *   CP_BF16 runs on the tensor cores (bf16 operands and weights, fp32 accumulation),
+ *   CP_F32 on the CUDA cores in fp32 arithmetic.
+ * Work goes with the visible pairs: tiles that no row of a query tile sees are not read.
+ * Errors: CP_EINVAL (null pointer, misalignment, Sq > Sk, window, sinks, Hq % Hkv),
+ * CP_EUNSUPPORTED (D, dtype, Sk beyond 2^31 - 1025), CP_ECUDA.
+ */
+int window_attn_fwd(const void *q, const void *k, const void *v, void *out, float *lse, int B, int Hq, int Hkv,
+                    int64_t Sq, int64_t Sk, int D, int64_t window, int64_t sinks, int dtype, float scale,
+                    void *stream);
+
+/*
+ * window_attn_bwd -- gradients of L = sum(dout * out) for window_attn_fwd: the formulas of
+ * ring_attn_bwd over the visible pairs, with the forward's lse.
+ *   q, out, dout, dq [B][Sq][Hq][D]; k, v, dk, dv [B][Sk][Hkv][D]; lse [B][Hq][Sq].
+ *   Every element of dq, dk and dv is written (0 for keys that no row sees).
+ *   workspace: device, window_attn_bwd_workspace(...) bytes, 16-byte aligned, contents
+ *   irrelevant; calls that may overlap on the GPU need their own.
+ * No atomics: results repeat bit for bit.
+ * Errors: as window_attn_fwd, plus a null, misaligned or too small workspace.
+ */
+int window_attn_bwd(const void *q, const void *k, const void *v, const void *out, const float *lse, const void *dout,
+                    void *dq, void *dk, void *dv, int B, int Hq, int Hkv, int64_t Sq, int64_t Sk, int D,
+                    int64_t window, int64_t sinks, int dtype, float scale, void *workspace, size_t ws_bytes,
+                    void *stream);
+
+/* window_attn_bwd_workspace -- bytes of scratch window_attn_bwd needs (Delta, and the
+ * sinks' partial gradients); 0 for arguments that it refuses.  Host only. */
+size_t window_attn_bwd_workspace(int B, int Hq, int Hkv, int64_t Sq, int64_t Sk, int D, int64_t window, int64_t sinks,
+                                 int dtype);
+
+/*
  * The paged 4-bit key/value cache: what a long prompt leaves behind for
  * decoding.  Four calls: kv4_append (rotate, quantise, write), kv4_gather (read
  * slots back as BSHD, for ring_attn_fwd or flash_block_step on the next chunk),
