@@ -68,6 +68,11 @@ SIGNATURES = {
     "kv4_attn_workspace": (ctypes.c_size_t, [_I]),
     "kv4_select": (_I, [_P] * 6 + [_I] * 12 + [_P, ctypes.c_size_t, _P]),
     "kv4_select_workspace": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "kv8_append": (_I, [_P] * 8 + [_I] * 8 + [_P]),
+    "kv8_gather": (_I, [_P] * 7 + [_I] * 8 + [_P]),
+    "kv8_attn": (_I, [_P] * 9 + [_I] * 8 + [_L, _L, _I, _I, _F, _P, ctypes.c_size_t, _P]),
+    "kv8_attn_workspace": (ctypes.c_size_t, [_I] * 7),
+    "kv8_evict": (_I, [_P] * 9 + [_I] * 10 + [_P]),
     "cp_get_error": (_I, [_P]),
     "cp_strerror": (ctypes.c_char_p, [_I]),
     "cp_debug_wait_timeout": (_I, [ctypes.c_uint64, _P]),
@@ -113,13 +118,15 @@ def load(build_if_missing: bool = False, variant: str | None = None):
     return _libs[v]
 
 
-_KV4_CALLS = ("kv4_append", "kv4_gather", "kv4_attn", "kv4_attn_workspace", "kv4_select", "kv4_select_workspace")
+_KV4_CALLS = ("kv4_append", "kv4_gather", "kv4_attn", "kv4_attn_workspace", "kv4_select", "kv4_select_workspace",
+              "kv8_append", "kv8_gather", "kv8_attn", "kv8_attn_workspace", "kv8_evict",
+              "window_attn_fwd", "window_attn_bwd", "window_attn_bwd_workspace")
 _kv4_module = None
 _kv4_tables = {}           # variant -> the calls' addresses, as the module takes them
 
 
 def kv4():
-    """(module of the paged cache's calls, table of the active library for it)."""
+    """(module of the paged caches' and the windowed calls, table of the active library for it)."""
     global _kv4_module
     table = _kv4_tables.get(_active)
     if table is None:

@@ -271,93 +271,6 @@ def ring_attn_bwd_noalloc(q, k, v, out, lse, dout, N: int, layout: int, causal: 
     return dq, dk, dv
 
 
-def _window_sizes(q, k, v):
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _need_cuda_contig(name, t)
-        if t.dim() != 4:
-            raise ValueError(f"{name} must have shape [B, S, H, D]")
-        if t.device != q.device:
-            raise ValueError(f"{name} must be on q's device")
-    if q.device.index != torch.cuda.current_device():
-        raise ValueError("q must be on the current CUDA device")
-    if q.dtype not in _DT or k.dtype != q.dtype or v.dtype != q.dtype:
-        raise ValueError("q, k, v must share dtype float32 or bfloat16")
-    B, Sq, Hq, D = q.shape
-    Sk, Hkv = k.shape[1], k.shape[2]
-    if k.shape != (B, Sk, Hkv, D) or v.shape != k.shape:
-        raise ValueError("k and v must have shape [B, Sk, Hkv, D] with q's B and D")
-    return B, Sq, Sk, Hq, Hkv, D
-
-
-def _window_like(name, t, like, dtype=None):
-    """An output or saved tensor of ``like``'s shape, device and (unless given) dtype."""
-    _need_cuda_contig(name, t)
-    if tuple(t.shape) != tuple(like.shape) or t.device != like.device or t.dtype != (dtype or like.dtype):
-        raise ValueError(f"{name} must be {dtype or like.dtype} {list(like.shape)} on {like.device}")
-    return t
-
-
-def window_attn_fwd(q, k, v, window: int, sinks: int = 0, scale: float | None = None, out=None, lse=None, stream=None):
-    """Causal attention with a sliding window and first tokens that stay visible; returns
-    (out, lse).
-
-    q ``[B, Sq, Hq, D]``, k/v ``[B, Sk, Hkv, D]`` (fp32 or bf16), Sq <= Sk: row i stands at
-    position ``p = i + Sk - Sq`` and sees key j iff ``j <= p and (j > p - window or
-    j < sinks)``.  out like q, lse ``[B, Hq, Sq]`` fp32.  A chunk of a prompt, or the shard
-    of a context-parallel rank, passes its own rows as q and as k and v the sinks' rows,
-    ``window - 1`` rows before the shard and the shard (all rows from 0 on where these
-    meet).  Gradients: :func:`window_attn_bwd`.
-    """
-    if stream is not None:   # what is allocated belongs to the stream that uses it
-        with torch.cuda.stream(stream):
-            return window_attn_fwd(q, k, v, window, sinks, scale, out, lse)
-    B, Sq, Sk, Hq, Hkv, D = _window_sizes(q, k, v)
-    out = torch.empty_like(q) if out is None else _window_like("out", out, q)
-    stat = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
-    if lse is not None and (lse.shape != (B, Hq, Sq) or lse.dtype != torch.float32 or lse.device != q.device
-                            or not lse.is_contiguous()):
-        raise ValueError(f"lse must be contiguous float32 {[B, Hq, Sq]} on {q.device}")
-    rc = _lib.load().window_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(stat), B, Hq, Hkv, Sq, Sk, D, window,
-                                     sinks, _DT[q.dtype], -1.0 if scale is None else float(scale),
-                                     ctypes.c_void_p(_stream(None)))
-    check(rc, "window_attn_fwd")
-    return out, stat
-
-
-def window_attn_bwd_workspace(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: int, window: int, sinks: int = 0,
-                              dtype=torch.bfloat16) -> int:
-    """Bytes of scratch for :func:`window_attn_bwd`."""
-    return int(_lib.load().window_attn_bwd_workspace(B, Hq, Hkv, Sq, Sk, D, window, sinks, _DT.get(dtype, -1)))
-
-
-def window_attn_bwd(q, k, v, out, lse, dout, window: int, sinks: int = 0, scale: float | None = None, dq=None, dk=None,
-                    dv=None, workspace=None, stream=None):
-    """Gradients (dq, dk, dv) of sum(dout * out) for :func:`window_attn_fwd`, whose out and
-    lse are passed in."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return window_attn_bwd(q, k, v, out, lse, dout, window, sinks, scale, dq, dk, dv, workspace)
-    B, Sq, Sk, Hq, Hkv, D = _window_sizes(q, k, v)
-    _window_like("out", out, q)
-    _window_like("dout", dout, q)
-    if lse.shape != (B, Hq, Sq) or lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous():
-        raise ValueError(f"lse must be contiguous float32 {[B, Hq, Sq]} on {q.device}")
-    dq = torch.empty_like(q) if dq is None else _window_like("dq", dq, q)
-    dk = torch.empty_like(k) if dk is None else _window_like("dk", dk, k)
-    dv = torch.empty_like(v) if dv is None else _window_like("dv", dv, v)
-    if workspace is None:
-        workspace = torch.empty(window_attn_bwd_workspace(B, Hq, Hkv, Sq, Sk, D, window, sinks, q.dtype),
-                                dtype=torch.uint8, device=q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {q.device}")
-    rc = _lib.load().window_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
-                                     _ptr(dv), B, Hq, Hkv, Sq, Sk, D, window, sinks, _DT[q.dtype],
-                                     -1.0 if scale is None else float(scale), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(), ctypes.c_void_p(_stream(None)))
-    check(rc, "window_attn_bwd")
-    return dq, dk, dv
-
-
 def lse_merge(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=None):
     """Merge two fp32 partials over disjoint key sets; returns (out, lse)."""
     for name, t in (("out_a", out_a), ("lse_a", lse_a), ("out_b", out_b), ("lse_b", lse_b)):
@@ -424,7 +337,7 @@ def ulysses_head_to_seq(y: torch.Tensor, N: int, layout: int, x=None, stream=Non
     return x
 
 
-# The kv4 calls go through the module of csrc/kv4_binding.cpp, which checks the
+# The calls from here on go through the module of csrc/kv4_binding.cpp, which checks the
 # tensors and makes those that are not given: in Python that took longer than the
 # kernels of a decode step.
 def _raw_stream(index):   # looked up at the call: a torch without CUDA has no such function
@@ -543,6 +456,154 @@ def kv4_select(q, summary, pages, lens, page: int, n_sel: int, vis=None, causal:
                         index, _raw_stream(index))
     if type(got) is int:
         check(got, "kv4_select")
+    return got
+
+
+def kv8_cache(n_pages: int, Hkv: int, page: int, D: int):
+    """An empty pool for :func:`kv8_append` on the current device: codes uint8
+    ``[n_pages, Hkv, 2, page, D]`` (K, V; ``view(torch.float8_e4m3fn)`` shows them as values)
+    and scales fp32 ``[n_pages, Hkv, 2, page / 16]``."""
+    if D not in (64, 128) or page not in (16, 32, 64, 128, 256):
+        raise CpError(_lib.CP_EUNSUPPORTED, "kv8_cache")
+    cache = torch.empty(n_pages, Hkv, 2, page, D, dtype=torch.uint8, device="cuda")
+    return cache, torch.empty(n_pages, Hkv, 2, page // 16, dtype=torch.float32, device="cuda")
+
+
+def kv8_append(k, v, cache, scales, pages, lens, n_new=None, stream=None):
+    """Write new tokens into the paged 8-bit cache, token (b, j) into slot ``lens[b] + j``.
+
+    k, v ``[B, n, Hkv, D]`` (fp32 or bf16), as the attention takes them, may be strided views
+    whose rows are contiguous.  cache, scales as :func:`kv8_cache`, pages int32
+    ``[B, max_pages]``, lens int32 ``[B]``: tokens cached before the call, which does not
+    change it; n_new int32 ``[B]``: real tokens of a padded batch.
+
+    The cache is for serving: none of the kv8 calls has a gradient.
+    """
+    if stream is not None:   # what is allocated belongs to the stream that uses it
+        with torch.cuda.stream(stream):
+            return kv8_append(k, v, cache, scales, pages, lens, n_new)
+    index = _kv4_device("k", k)
+    module, table = _lib.kv4()
+    got = module.append8(table, k, v, cache, scales, pages, lens, n_new, index, _raw_stream(index))
+    if type(got) is int:
+        check(got, "kv8_append")
+
+
+def kv8_gather(cache, scales, pages, lens, count: int, start=None, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """Cached tokens back as rows: (k, v) ``[B, count, Hkv, D]`` with row (b, j) the slot
+    ``start[b] + j`` (start int32 ``[B]``, None: 0); rows at or past ``lens[b]`` are 0.  For
+    :func:`window_attn_fwd` or ring attention on the next chunk.  No gradient."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_gather(cache, scales, pages, lens, count, start, dtype, k, v)
+    if k is not None:
+        dtype = k.dtype
+    if dtype not in _DT:
+        raise ValueError("dtype must be float32 or bfloat16")
+    index = _kv4_device("cache", cache)
+    module, table = _lib.kv4()
+    got = module.gather8(table, cache, scales, pages, lens, count, start, dtype is torch.bfloat16, k, v, index,
+                         _raw_stream(index))
+    if type(got) is int:
+        check(got, "kv8_gather")
+    return got
+
+
+def kv8_attn_workspace(B: int, n: int, Hq: int, D: int, page: int, max_pages: int, mass: bool = False) -> int:
+    """Bytes of scratch for :func:`kv8_attn`."""
+    return int(_lib.load().kv8_attn_workspace(B, n, Hq, D, page, max_pages, int(mass)))
+
+
+def kv8_attn(q, cache, scales, pages, lens, window: int = 0, sinks: int = 0, vis=None, causal: bool = True,
+             scale: float | None = None, mass=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of query tokens over the paged 8-bit cache; returns (out, lse).
+
+    q ``[B, n, Hq, D]`` bf16; out like q (or fp32, if given so, as :func:`lse_merge` takes
+    it), lse ``[B, Hq, n]`` fp32.  Row (b, j)'s limit is ``vis[b, j]`` (int32 ``[B, n]``), else
+    ``lens[b] - (n - 1) + j`` if causal, else ``lens[b]``.  It sees the slots below its limit;
+    with ``window`` the last ``window`` of them and the first ``sinks``, as
+    :func:`window_attn_fwd` (pages between them may be reused).  ``mass`` fp32
+    ``[B, Hkv, max_pages * page]``: each slot's attention weight, summed over the rows of its
+    kv head, is added to it, for :func:`kv8_evict`.  No gradient.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_attn(q, cache, scales, pages, lens, window, sinks, vis, causal, scale, mass, out, lse, workspace)
+    index = _kv4_device("q", q)
+    module, table = _lib.kv4()
+    got = module.attn8(table, q, cache, scales, pages, lens, window, sinks, vis, causal, -1.0 if scale is None else scale,
+                       mass, out, lse, workspace, index, _raw_stream(index))
+    if type(got) is int:
+        check(got, "kv8_attn")
+    return got
+
+
+def kv8_evict(cache, scales, pages, lens, mass, pages_to, budget: int, keep_first: int = 0, keep_last: int = 0, kept=None,
+              lens_to=None, mass_to=None, stream=None):
+    """Move the tokens with the largest mass into other pages; returns (kept, lens_to, mass_to).
+
+    Per sequence and kv head the ``min(lens[b], budget)`` slots to keep are the first
+    ``keep_first``, the last ``keep_last``, then those of the largest ``mass`` (fp32
+    ``[B, Hkv, max_pages * page]``; ties to the lower slot).  They become slots 0, 1, ... of the
+    pages ``pages_to`` (int32 ``[B, max_to]``, of the same pool; none of them in use), in
+    ascending order.  kept int32 ``[B, Hkv, budget]`` names them (then -1), lens_to int32
+    ``[B]`` and mass_to ``[B, Hkv, max_to * page]`` go with ``pages_to`` from there on.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_evict(cache, scales, pages, lens, mass, pages_to, budget, keep_first, keep_last, kept, lens_to, mass_to)
+    index = _kv4_device("cache", cache)
+    module, table = _lib.kv4()
+    got = module.evict8(table, cache, scales, pages, lens, mass, pages_to, budget, keep_first, keep_last, kept, lens_to,
+                        mass_to, index, _raw_stream(index))
+    if type(got) is int:
+        check(got, "kv8_evict")
+    return got
+
+
+def window_attn_fwd(q, k, v, window: int, sinks: int = 0, scale: float | None = None, out=None, lse=None, stream=None):
+    """Causal attention with a sliding window and first tokens that stay visible; returns
+    (out, lse).
+
+    q ``[B, Sq, Hq, D]``, k/v ``[B, Sk, Hkv, D]`` (fp32 or bf16), Sq <= Sk: row i stands at
+    position ``p = i + Sk - Sq`` and sees key j iff ``j <= p and (j > p - window or
+    j < sinks)``.  out like q, lse ``[B, Hq, Sq]`` fp32.  A chunk of a prompt, or the shard
+    of a context-parallel rank, passes its own rows as q and as k and v the sinks' rows,
+    ``window - 1`` rows before the shard and the shard (all rows from 0 on where these
+    meet).  Its single-token form over a cache is :func:`kv8_attn`; its gradients
+    :func:`window_attn_bwd`.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return window_attn_fwd(q, k, v, window, sinks, scale, out, lse)
+    index = _kv4_device("q", q)
+    module, table = _lib.kv4()
+    got = module.window_fwd(table, q, k, v, window, sinks, -1.0 if scale is None else scale, out, lse, index,
+                            _raw_stream(index))
+    if type(got) is int:
+        check(got, "window_attn_fwd")
+    return got
+
+
+def window_attn_bwd_workspace(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: int, window: int, sinks: int = 0,
+                              dtype=torch.bfloat16) -> int:
+    """Bytes of scratch for :func:`window_attn_bwd`."""
+    return int(_lib.load().window_attn_bwd_workspace(B, Hq, Hkv, Sq, Sk, D, window, sinks, _DT.get(dtype, -1)))
+
+
+def window_attn_bwd(q, k, v, out, lse, dout, window: int, sinks: int = 0, scale: float | None = None, dq=None, dk=None,
+                    dv=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of sum(dout * out) for :func:`window_attn_fwd`, whose out and
+    lse are passed in."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return window_attn_bwd(q, k, v, out, lse, dout, window, sinks, scale, dq, dk, dv, workspace)
+    index = _kv4_device("q", q)
+    module, table = _lib.kv4()
+    got = module.window_bwd(table, q, k, v, out, lse, dout, window, sinks, -1.0 if scale is None else scale, dq, dk, dv,
+                            workspace, index, _raw_stream(index))
+    if type(got) is int:
+        check(got, "window_attn_bwd")
     return got
 
 

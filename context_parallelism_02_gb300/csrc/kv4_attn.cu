@@ -521,49 +521,8 @@ __global__ void __launch_bounds__(W * 32) kv4_attn_kernel(Kv4AttnArgs a, Shape s
         at.left = at.t1 - at.t0;
         __syncthreads();                      // sm.abort is set
     } else {
-        // where the stretch begins: the extents of all items, then the sequence
-        const int B = a.rows.B;
-        int64_t all = 0;
-        int one = 0;                              // the lane's sequence of the stretch of 32 in hand
-        for (int b = lane; b < B; b += 32) {
-            one = item_blocks(a, b) + PAD;
-            all += one;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        all *= sh.per_batch;
-        const Cuts cuts(all, warps, LEAST);
         self = blockIdx.x * W + warp;
-        __syncthreads();                          // sm.abort is set
-        if (self >= cuts.n) return;
-        const int64_t f0 = cuts.begin(self);
-        int64_t rest = 0;
-        for (int b0 = 0;; b0 += 32) {
-            const int b = b0 + lane;
-            if (B > 32) one = b < B ? item_blocks(a, b) + PAD : 0;
-            else if (b >= B) one = 0;
-            int64_t upto = one;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += v;
-            }
-            const int64_t here = __shfl_sync(0xffffffffu, upto, 31) * sh.per_batch;
-            if (f0 - rest >= here) {
-                rest += here;
-                continue;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, f0 - rest >= upto * sh.per_batch);
-            const int x = __popc(past);           // sequences of these 32 that end before f0
-            at.b = b0 + x;
-            at.nb = __shfl_sync(0xffffffffu, one, x) - PAD;
-            rest = f0 - rest - __shfl_sync(0xffffffffu, upto - one, x) * sh.per_batch;
-            break;
-        }
-        at.i = (int)divide(rest, at.nb + PAD);
-        at.t0 = (int)(rest - (int64_t)at.i * (at.nb + PAD));
-        at.left = cuts.begin(self + 1) - f0;
-        at.cut();
+        if (!start_of_stretch(a, sh, warps, self, at)) return;   // behind it sm.abort is set
     }
     RawRows<D, NT> raw;
     bool first = true;

@@ -1,5 +1,5 @@
-// kv4_binding.cpp -- Python module _kv4_binding: the calls of the paged 4-bit cache on
-// torch tensors.  It checks tensors, allocates what the caller did not give and calls
+// kv4_binding.cpp -- Python module _kv4_binding: the calls of the paged caches (kv4_*, kv8_*)
+// and of windowed attention on torch tensors.  It checks tensors, allocates what the caller did not give and calls
 // libcp's entry points; it holds no arithmetic.  A decode step makes these calls
 // once per layer, and in Python their checks and allocations took longer than the
 // kernels (21 us of host time for an attention call of 9 us; 11 here).
@@ -14,6 +14,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <limits.h>
+#include <string.h>
 
 #include "cp.h"
 
@@ -26,7 +27,16 @@ struct Table {
     decltype(&kv4_attn_workspace) attn_workspace;
     decltype(&kv4_select) select;
     decltype(&kv4_select_workspace) select_workspace;
+    decltype(&kv8_append) append8;
+    decltype(&kv8_gather) gather8;
+    decltype(&kv8_attn) attn8;
+    decltype(&kv8_attn_workspace) attn8_workspace;
+    decltype(&kv8_evict) evict8;
+    decltype(&window_attn_fwd) window_fwd;
+    decltype(&window_attn_bwd) window_bwd;
+    decltype(&window_attn_bwd_workspace) window_bwd_workspace;
 };
+constexpr int CALLS = 14;
 
 constexpr const char *TABLE = "libcp.kv4";
 
@@ -312,21 +322,250 @@ PyObject *select(PyObject *const *args, Py_ssize_t n_args)
     return THPVariable_Wrap(s);
 }
 
-// (append, gather, attn, attn_workspace, select, select_workspace): addresses in libcp
+Pool check_pool8(const Args &a, const at::Tensor &cache, const at::Tensor &scales, const at::Tensor &pages,
+                 const at::Tensor &lens, int64_t B)
+{
+    a.check("cache", &cache, at::kByte);
+    if (cache.dim() != 5 || cache.size(2) != 2) refuse("cache must have shape [n_pages, Hkv, 2, page, D], not ", cache.sizes());
+    a.check("scales", &scales, at::kFloat, {cache.size(0), cache.size(1), 2, cache.size(3) / 16});
+    a.check("pages", &pages, at::kInt);
+    if (pages.dim() != 2 || pages.size(0) != B) refuse("pages must have shape [", B, ", max_pages], not ", pages.sizes());
+    a.check("lens", &lens, at::kInt, {B});
+    return {status("n_pages", cache.size(0)), status("Hkv", cache.size(1)), status("page", cache.size(3)),
+            status("D", cache.size(4)), status("max_pages", pages.size(1))};
+}
+
+// Element strides of [B, n, H, D] rows; an axis of one entry is not stepped along.
+void row_strides(const Args &a, const char *name, const at::Tensor &t, int64_t *strides)
+{
+    a.on_device(name, t);
+    if (t.numel() && t.stride(3) != 1) refuse(name, "'s rows must be contiguous");
+    for (int x = 0; x < 3; ++x) strides[x] = t.size(x) > 1 ? t.stride(x) : 0;
+}
+
+// (table, k, v, cache, scales, pages, lens, n_new, device, stream)
+PyObject *append8(PyObject *const *args, Py_ssize_t n_args)
+{
+    Args a(args, n_args, 10);
+    const at::Tensor &k = a.needed("k"), &v = a.needed("v"), &cache = a.needed("cache"), &scales = a.needed("scales"),
+                     &pages = a.needed("pages"), &lens = a.needed("lens");
+    const at::Tensor *n_new = a.tensor("n_new");
+    a.index = a.integer();
+    void *stream = a.stream();
+    if (k.dim() != 4 || v.sizes() != k.sizes()) refuse("k and v must have shape [B, n, Hkv, D]");
+    const at::ScalarType type = k.scalar_type();
+    if (code_of(type) < 0 || v.scalar_type() != type) refuse("k and v must share dtype float32 or bfloat16");
+    const int64_t B = k.size(0);
+    const Pool p = check_pool8(a, cache, scales, pages, lens, B);
+    if (p.heads != k.size(2) || p.D != k.size(3)) refuse("cache and k must share Hkv and D");
+    a.check("n_new", n_new, at::kInt, {B});
+    int64_t strides[6];
+    row_strides(a, "k", k, strides);
+    row_strides(a, "v", v, strides + 3);
+    const int b = status("B", B), n = status("n", k.size(1));
+    const int rc = run([&] {
+        return a.table->append8(ptr(k), ptr(v), ptr(cache), static_cast<float *>(ptr(scales)), ints(pages), ints(lens),
+                                ints(n_new), strides, b, n, p.heads, p.D, p.n_pages, p.page, p.max_pages, code_of(type), stream);
+    });
+    if (rc) return PyLong_FromLong(rc);
+    Py_RETURN_NONE;
+}
+
+// (table, cache, scales, pages, lens, count, start, bf16, k, v, device, stream)
+PyObject *gather8(PyObject *const *args, Py_ssize_t n_args)
+{
+    Args a(args, n_args, 12);
+    const at::Tensor &cache = a.needed("cache"), &scales = a.needed("scales"), &pages = a.needed("pages"), &lens = a.needed("lens");
+    const int count = a.small("count");
+    const at::Tensor *start = a.tensor("start");
+    const at::ScalarType type = a.truth() ? at::kBFloat16 : at::kFloat;
+    const at::Tensor *k = a.tensor("k"), *v = a.tensor("v");
+    a.index = a.integer();
+    void *stream = a.stream();
+    if (lens.dim() != 1) refuse("lens must have shape [B]");
+    if (count < 0) return PyLong_FromLong(CP_EINVAL);
+    const int64_t B = lens.size(0);
+    const Pool p = check_pool8(a, cache, scales, pages, lens, B);
+    const int64_t shape[4] = {B, count, p.heads, p.D};
+    a.check("start", start, at::kInt, {B});
+    a.check("k", k, type, shape);
+    a.check("v", v, type, shape);
+    const auto options = cache.options().dtype(type);
+    const at::Tensor ko = k ? *k : at::empty(shape, options), vo = v ? *v : at::empty(shape, options);
+    const int b = status("B", B);
+    const int rc = run([&] {
+        return a.table->gather8(ptr(cache), floats(&scales), ints(pages), ints(lens), ints(start), ptr(ko), ptr(vo), b, count,
+                                p.heads, p.D, p.n_pages, p.page, p.max_pages, code_of(type), stream);
+    });
+    if (rc) return PyLong_FromLong(rc);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(ko), THPVariable_Wrap(vo));
+}
+
+// (table, q, cache, scales, pages, lens, window, sinks, vis, causal, scale, mass, out, lse, workspace, device, stream)
+PyObject *attn8(PyObject *const *args, Py_ssize_t n_args)
+{
+    Args a(args, n_args, 17);
+    const at::Tensor &q = a.needed("q"), &cache = a.needed("cache"), &scales = a.needed("scales"), &pages = a.needed("pages"),
+                     &lens = a.needed("lens");
+    const int64_t window = a.integer(), sinks = a.integer();
+    const at::Tensor *vis = a.tensor("vis");
+    const bool causal = a.truth();
+    const float scale = a.number();
+    const at::Tensor *mass = a.tensor("mass"), *out = a.tensor("out"), *lse = a.tensor("lse"), *ws = a.tensor("workspace");
+    a.index = a.integer();
+    void *stream = a.stream();
+    if (q.dim() != 4) refuse("q must have shape [B, n, Hq, D]");
+    a.check("q", &q, at::kBFloat16);
+    const int64_t B = q.size(0), n = q.size(1), Hq = q.size(2), D = q.size(3);
+    const Pool p = check_pool8(a, cache, scales, pages, lens, B);
+    if (p.D != D) refuse("cache and q must share D");
+    a.check("vis", vis, at::kInt, {B, n});
+    a.check("mass", mass, at::kFloat, {B, p.heads, (int64_t)p.max_pages * p.page});
+    const at::ScalarType type = out ? out->scalar_type() : at::kBFloat16;
+    if (code_of(type) < 0) refuse("out must be float32 or bfloat16");
+    a.check("out", out, type, q.sizes());
+    a.check("lse", lse, at::kFloat, {B, Hq, n});
+    if (ws) a.check("workspace", ws, ws->scalar_type());
+    const int b = status("B", B), nn = status("n", n), hq = status("Hq", Hq);
+    const at::Tensor o = out ? *out : at::empty(q.sizes(), q.options());
+    const at::Tensor z = lse ? *lse : at::empty({B, Hq, n}, q.options().dtype(at::kFloat));
+    const at::Tensor w = ws ? *ws
+                            : at::empty({(int64_t)a.table->attn8_workspace(b, nn, hq, p.D, p.page, p.max_pages, mass != nullptr)},
+                                        q.options().dtype(at::kByte));
+    const int rc = run([&] {
+        return a.table->attn8(ptr(q), ptr(cache), floats(&scales), ints(pages), ints(lens), ints(vis), ptr(o),
+                              static_cast<float *>(ptr(z)), static_cast<float *>(ptr(mass)), b, nn, hq, p.heads, p.D, p.n_pages,
+                              p.page, p.max_pages, window, sinks, causal, code_of(type), scale, ptr(w), w.nbytes(), stream);
+    });
+    if (rc) return PyLong_FromLong(rc);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(o), THPVariable_Wrap(z));
+}
+
+// (table, cache, scales, pages, lens, mass, pages_to, budget, keep_first, keep_last, kept, lens_to, mass_to, device, stream)
+PyObject *evict8(PyObject *const *args, Py_ssize_t n_args)
+{
+    Args a(args, n_args, 15);
+    const at::Tensor &cache = a.needed("cache"), &scales = a.needed("scales"), &pages = a.needed("pages"), &lens = a.needed("lens"),
+                     &mass = a.needed("mass"), &to = a.needed("pages_to");
+    const int budget = a.small("budget"), first = a.small("keep_first"), last = a.small("keep_last");
+    const at::Tensor *kept = a.tensor("kept"), *lens_to = a.tensor("lens_to"), *mass_to = a.tensor("mass_to");
+    a.index = a.integer();
+    void *stream = a.stream();
+    if (lens.dim() != 1) refuse("lens must have shape [B]");
+    const int64_t B = lens.size(0);
+    const Pool p = check_pool8(a, cache, scales, pages, lens, B);
+    a.check("mass", &mass, at::kFloat, {B, p.heads, (int64_t)p.max_pages * p.page});
+    a.check("pages_to", &to, at::kInt);
+    if (to.dim() != 2 || to.size(0) != B) refuse("pages_to must have shape [", B, ", max_to], not ", to.sizes());
+    const int max_to = status("max_to", to.size(1));
+    if (budget < 1) return PyLong_FromLong(CP_EINVAL);
+    a.check("kept", kept, at::kInt, {B, p.heads, budget});
+    a.check("lens_to", lens_to, at::kInt, {B});
+    const int64_t slots[3] = {B, p.heads, (int64_t)max_to * p.page};
+    a.check("mass_to", mass_to, at::kFloat, slots);
+    const at::Tensor k = kept ? *kept : at::empty({B, p.heads, budget}, lens.options());
+    const at::Tensor l = lens_to ? *lens_to : at::empty({B}, lens.options());
+    const at::Tensor m = mass_to ? *mass_to : at::empty(slots, mass.options());
+    const int b = status("B", B);
+    const int rc = run([&] {
+        return a.table->evict8(ptr(cache), static_cast<float *>(ptr(scales)), ints(pages), ints(lens), floats(&mass), ints(to),
+                               static_cast<int32_t *>(ptr(k)), static_cast<int32_t *>(ptr(l)), static_cast<float *>(ptr(m)), b,
+                               p.heads, p.D, p.n_pages, p.page, p.max_pages, max_to, budget, first, last, stream);
+    });
+    if (rc) return PyLong_FromLong(rc);
+    return Py_BuildValue("(NNN)", THPVariable_Wrap(k), THPVariable_Wrap(l), THPVariable_Wrap(m));
+}
+
+// What the windowed calls are given: q, k, v.
+struct Window {
+    int B, Hq, Hkv, D, type;
+    int64_t Sq, Sk;
+    Window(const Args &a, const at::Tensor &q, const at::Tensor &k, const at::Tensor &v)
+    {
+        if (q.dim() != 4 || k.dim() != 4) refuse("q and k must have shape [B, S, H, D]");
+        const at::ScalarType t = q.scalar_type();
+        type = code_of(t);
+        if (type < 0 || k.scalar_type() != t || v.scalar_type() != t) refuse("q, k, v must share dtype float32 or bfloat16");
+        a.check("q", &q, t);
+        a.check("k", &k, t, {q.size(0), k.size(1), k.size(2), q.size(3)});
+        a.check("v", &v, t, k.sizes());
+        B = status("B", q.size(0)), Hq = status("Hq", q.size(2)), Hkv = status("Hkv", k.size(2)), D = status("D", q.size(3));
+        Sq = q.size(1), Sk = k.size(1);
+    }
+};
+
+// (table, q, k, v, window, sinks, scale, out, lse, device, stream)
+PyObject *window_fwd(PyObject *const *args, Py_ssize_t n_args)
+{
+    Args a(args, n_args, 11);
+    const at::Tensor &q = a.needed("q"), &k = a.needed("k"), &v = a.needed("v");
+    const int64_t window = a.integer(), sinks = a.integer();
+    const float scale = a.number();
+    const at::Tensor *out = a.tensor("out"), *lse = a.tensor("lse");
+    a.index = a.integer();
+    void *stream = a.stream();
+    const Window w(a, q, k, v);
+    a.check("out", out, q.scalar_type(), q.sizes());
+    a.check("lse", lse, at::kFloat, {w.B, w.Hq, w.Sq});
+    const at::Tensor o = out ? *out : at::empty(q.sizes(), q.options());
+    const at::Tensor z = lse ? *lse : at::empty({w.B, w.Hq, w.Sq}, q.options().dtype(at::kFloat));
+    const int rc = run([&] {
+        return a.table->window_fwd(ptr(q), ptr(k), ptr(v), ptr(o), static_cast<float *>(ptr(z)), w.B, w.Hq, w.Hkv, w.Sq, w.Sk,
+                                   w.D, window, sinks, w.type, scale, stream);
+    });
+    if (rc) return PyLong_FromLong(rc);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(o), THPVariable_Wrap(z));
+}
+
+// (table, q, k, v, out, lse, dout, window, sinks, scale, dq, dk, dv, workspace, device, stream)
+PyObject *window_bwd(PyObject *const *args, Py_ssize_t n_args)
+{
+    Args a(args, n_args, 16);
+    const at::Tensor &q = a.needed("q"), &k = a.needed("k"), &v = a.needed("v"), &out = a.needed("out"), &lse = a.needed("lse"),
+                     &dout = a.needed("dout");
+    const int64_t window = a.integer(), sinks = a.integer();
+    const float scale = a.number();
+    const at::Tensor *dq = a.tensor("dq"), *dk = a.tensor("dk"), *dv = a.tensor("dv"), *ws = a.tensor("workspace");
+    a.index = a.integer();
+    void *stream = a.stream();
+    const Window w(a, q, k, v);
+    const at::ScalarType t = q.scalar_type();
+    a.check("out", &out, t, q.sizes());
+    a.check("dout", &dout, t, q.sizes());
+    a.check("lse", &lse, at::kFloat, {w.B, w.Hq, w.Sq});
+    a.check("dq", dq, t, q.sizes());
+    a.check("dk", dk, t, k.sizes());
+    a.check("dv", dv, t, k.sizes());
+    if (ws) a.check("workspace", ws, ws->scalar_type());
+    const at::Tensor x = dq ? *dq : at::empty(q.sizes(), q.options()), y = dk ? *dk : at::empty(k.sizes(), k.options()),
+                     z = dv ? *dv : at::empty(k.sizes(), k.options());
+    const at::Tensor s = ws ? *ws
+                            : at::empty({(int64_t)a.table->window_bwd_workspace(w.B, w.Hq, w.Hkv, w.Sq, w.Sk, w.D, window, sinks,
+                                                                                w.type)},
+                                        q.options().dtype(at::kByte));
+    const int rc = run([&] {
+        return a.table->window_bwd(ptr(q), ptr(k), ptr(v), ptr(out), floats(&lse), ptr(dout), ptr(x), ptr(y), ptr(z), w.B, w.Hq,
+                                   w.Hkv, w.Sq, w.Sk, w.D, window, sinks, w.type, scale, ptr(s), s.nbytes(), stream);
+    });
+    if (rc) return PyLong_FromLong(rc);
+    return Py_BuildValue("(NNN)", THPVariable_Wrap(x), THPVariable_Wrap(y), THPVariable_Wrap(z));
+}
+
+// The calls' addresses in libcp, in Table's order
 PyObject *table(PyObject *const *args, Py_ssize_t n_args)
 {
-    if (n_args != 6) refuse("kv4: six addresses expected");
-    void *f[6];
-    for (int i = 0; i < 6; ++i) {
+    if (n_args != CALLS) refuse("kv4: ", CALLS, " addresses expected");
+    void *f[CALLS];
+    for (int i = 0; i < CALLS; ++i) {
         f[i] = PyLong_AsVoidPtr(args[i]);
         if (!f[i]) {
             if (PyErr_Occurred()) throw python_error();
             refuse("kv4: null address");
         }
     }
-    Table *t = new Table{reinterpret_cast<decltype(&kv4_append)>(f[0]),          reinterpret_cast<decltype(&kv4_gather)>(f[1]),
-                         reinterpret_cast<decltype(&kv4_attn)>(f[2]),            reinterpret_cast<decltype(&kv4_attn_workspace)>(f[3]),
-                         reinterpret_cast<decltype(&kv4_select)>(f[4]),          reinterpret_cast<decltype(&kv4_select_workspace)>(f[5])};
+    Table *t = new Table;
+    static_assert(sizeof(Table) == sizeof(f), "Table holds the addresses and nothing else");
+    memcpy(static_cast<void *>(t), f, sizeof(f));
     return PyCapsule_New(t, TABLE, [](PyObject *c) { delete static_cast<Table *>(PyCapsule_GetPointer(c, TABLE)); });
 }
 
@@ -345,7 +584,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 }
 
 #define CP_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&entry<name>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {CP_METHOD(append), CP_METHOD(gather), CP_METHOD(attn), CP_METHOD(select), CP_METHOD(table),
+PyMethodDef methods[] = {CP_METHOD(append), CP_METHOD(gather), CP_METHOD(attn), CP_METHOD(select), CP_METHOD(append8),
+                         CP_METHOD(gather8), CP_METHOD(attn8), CP_METHOD(evict8), CP_METHOD(window_fwd), CP_METHOD(window_bwd), CP_METHOD(table),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kv4_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -531,6 +531,103 @@ int kv4_select(const void *q, const void *summary, const int32_t *pages, const i
 size_t kv4_select_workspace(int B, int n, int Hkv, int max_pages);
 
 /*
+ * The paged 8-bit key/value cache: twice the bytes of the 4-bit one and eight times its
+ * precision, for contexts whose growth is bounded: kv8_attn takes a sliding window with
+ * sinks (window_attn_fwd's single-token form) or accumulates the weight that every cached
+ * token got, and kv8_evict cuts the cache down to the tokens of the largest weight.  Its
+ * calls take rows as the attention takes them (rotated, where the model rotates).  They
+ * serve; none of them has a backward pass.
+ *
+ * Pool: cache [n_pages][Hkv][2 (K, V)][page][D] bytes, 16-byte aligned, e4m3 codes (sign,
+ * four bits of exponent, three of mantissa), and scales [n_pages][Hkv][2][page / 16] fp32;
+ * page in {16, 32, 64, 128, 256}, D in {64, 128}.  The 16 tokens of a block share a scale,
+ * 2^e with e the smallest integer in [-40, 60] such that amax <= 448 2^e over the block's
+ * tokens; a value is code * scale.  Cache and scales may start uninitialised.
+ * pages, lens, page numbers out of range and scheduling: as the 4-bit cache.
+ * max_pages * page at most 2^31 - 1025.
+ */
+
+/*
+ * kv8_append -- writes new tokens behind the cached ones: token (b, j) goes to slot
+ * lens[b] + j.
+ *   k, v [B][n][Hkv][D]: device, dtype CP_BF16 or CP_F32, rows contiguous and 16-byte
+ *   aligned; strides: HOST array of six element strides (batch, token, head of k, then of
+ *   v), NULL for contiguous tensors.
+ *   n_new [B] int32 or NULL: tokens of each sequence that are real (clamped to [0, n]).
+ * A block whose first slot is written starts afresh; a block that new tokens join takes
+ * the larger of its scale and theirs, and where that grows, the older tokens' codes are
+ * rounded to it (nothing is lost of codes that stay in e4m3's normal range).  Codes are
+ * nearest even; magnitudes beyond 448 2^60 count as that, infinities and NaN are held as
+ * NaN and do not count for the scale.
+ * Within one call no two sequences may write the same page.
+ * Errors: CP_EINVAL (null pointer, misalignment, sizes), CP_EUNSUPPORTED (D, dtype, page,
+ * more rows or slots than a launch counts), CP_ECUDA.
+ */
+int kv8_append(const void *k, const void *v, void *cache, float *scales, const int32_t *pages, const int32_t *lens,
+               const int32_t *n_new, const int64_t *strides, int B, int n, int Hkv, int D, int n_pages, int page,
+               int max_pages, int dtype, void *stream);
+
+/*
+ * kv8_gather -- cached tokens back as rows: row (b, j) of k and v [B][count][Hkv][D] (dtype
+ * CP_BF16 or CP_F32, both exact) is slot start[b] + j; rows at or past lens[b] are 0.
+ *   start [B] int32 or NULL (0).
+ * Errors: as kv8_append.
+ */
+int kv8_gather(const void *cache, const float *scales, const int32_t *pages, const int32_t *lens, const int32_t *start,
+               void *k, void *v, int B, int count, int Hkv, int D, int n_pages, int page, int max_pages, int dtype,
+               void *stream);
+
+/*
+ * kv8_attn -- attention of query tokens over the cache.
+ *   q [B][n][Hq][D] bf16, contiguous; query head h reads kv head h / (Hq / Hkv).
+ *   Row (b, j)'s limit is vis[b][j] if vis [B][n] (int32) is given, else lens[b] - (n - 1)
+ *   + j if causal (the n tokens are the last of the cache), else lens[b]; in any case at
+ *   most lens[b].  It sees the slots below its limit; with window > 0 only the last
+ *   `window` of them and the first `sinks` (window 0: no window).  Pages that neither
+ *   reaches are not read (but with vis, where every page up to lens[b] is).  Window and
+ *   sinks count slots: behind kv8_evict they are no longer positions.
+ *   out [B][n][Hq][D]: bf16 (rounded to nearest even) or fp32 by out_dtype; lse [B][Hq][n]
+ *   fp32, natural log.  A row that sees nothing: (0, -inf).  What a row does not see has no
+ *   influence on it, whatever those slots hold.
+ *   mass [B][Hkv][max_pages page] fp32 or NULL: += the weights e^(s - lse) that each slot
+ *   got, summed over the rows of its kv head; slots that no row sees stay as they are.
+ *   fp32 sums; K, V and q enter exactly (an element of q below 2^-31 of its row's largest is
+ *   rounded); the product of a weight and its block's V scale is rounded to fp16 (2^-11 of
+ *   itself, or 2^-32 of the row's largest such product).  scale <= 0 selects 1/sqrt(D).  A row
+ *   of q with a value that is not finite comes out as NaN.
+ *   workspace: device, kv8_attn_workspace(...) bytes, 16-byte aligned, contents irrelevant;
+ *   calls that may overlap on the GPU need their own.
+ * No atomics: results repeat bit for bit.
+ * Errors: as kv8_append, plus CP_EINVAL for window, sinks and a null or too small workspace.
+ */
+int kv8_attn(const void *q, const void *cache, const float *scales, const int32_t *pages, const int32_t *lens,
+             const int32_t *vis, void *out, float *lse, float *mass, int B, int n, int Hq, int Hkv, int D, int n_pages,
+             int page, int max_pages, int64_t window, int64_t sinks, int causal, int out_dtype, float scale,
+             void *workspace, size_t ws_bytes, void *stream);
+
+/* kv8_attn_workspace -- bytes of scratch kv8_attn needs: a constant of D, and with mass (not
+ * 0) the scores, B n Hq page max_pages fp32; 0 for sizes that are not built.  Host only. */
+size_t kv8_attn_workspace(int B, int n, int Hq, int D, int page, int max_pages, int mass);
+
+/*
+ * kv8_evict -- the tokens with the largest mass into other pages.  Per sequence and kv head
+ * the min(lens[b], budget) slots to keep are the first keep_first, the last keep_last, then
+ * those of the largest mass [B][Hkv][max_pages page] (ties to the lower slot; NaN counts as
+ * the largest), moved in ascending order into slots 0, 1, ... of the pages
+ * pages_to [B][max_to] of the same pool.  A new block's scale is the largest of its tokens'
+ * scales; the codes of the others are rounded to it as in kv8_append.
+ *   kept [B][Hkv][budget] int32: the slots that were kept, then -1.
+ *   lens_to [B] int32: min(lens[b], budget).
+ *   mass_to [B][Hkv][max_to page] fp32 or NULL: the kept slots' mass, then 0.
+ *   max_to page >= budget >= 1; keep_first + keep_last <= budget.
+ * The source pages stay as they are; pages_to must not name one of them, nor a page twice.
+ * Errors: as kv8_append.
+ */
+int kv8_evict(void *cache, float *scales, const int32_t *pages, const int32_t *lens, const float *mass,
+              const int32_t *pages_to, int32_t *kept, int32_t *lens_to, float *mass_to, int B, int Hkv, int D, int n_pages,
+              int page, int max_pages, int max_to, int budget, int keep_first, int keep_last, void *stream);
+
+/*
  * cp_get_error -- synchronise `stream`, then read and clear the calling
  * device's error word.  Returns CP_OK, CP_ETIMEOUT (a kernel's bounded wait
  * ran out and the kernel returned early; its outputs are undefined),
