@@ -116,34 +116,50 @@ __global__ void __launch_bounds__(256) bwd_delta_kernel(const __nv_bfloat16 *__r
                                                         float *__restrict__ delta, int S, int Hq,
                                                         int D, int64_t rows)
 {
-    // one warp per (b, s, h) row, rows in BSHD order
+    // one warp per (b, s, h) row, rows in BSHD order, ROWS of them at a time (one at a
+    // time left the loads' latency exposed: 268 MB in 58 us)
+    constexpr int ROWS = 4;
     const int lane = threadIdx.x & 31;
     const int64_t wid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int64_t nw = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    for (int64_t r = wid; r < rows; r += nw) {
-        const __nv_bfloat16 *o = out + r * D;
-        const __nv_bfloat16 *g = dout + r * D;
-        float acc = 0.f;
-        for (int d = lane * 4; d < D; d += 128) {
-            const uint2 ov = *reinterpret_cast<const uint2 *>(o + d);
-            const uint2 gv = *reinterpret_cast<const uint2 *>(g + d);
-            const __nv_bfloat162 *o2 = reinterpret_cast<const __nv_bfloat162 *>(&ov);
-            const __nv_bfloat162 *g2 = reinterpret_cast<const __nv_bfloat162 *>(&gv);
+    for (int64_t r0 = wid * ROWS; r0 < rows; r0 += nw * ROWS) {
+        float acc[ROWS];
+        uint2 ov[ROWS], gv[ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            ov[i] = gv[i] = make_uint2(0, 0);
+            acc[i] = 0.f;
+            if (r0 + i < rows && lane * 4 < D) {
+                ov[i] = *reinterpret_cast<const uint2 *>(out + (r0 + i) * D + lane * 4);
+                gv[i] = *reinterpret_cast<const uint2 *>(dout + (r0 + i) * D + lane * 4);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const __nv_bfloat162 *o2 = reinterpret_cast<const __nv_bfloat162 *>(&ov[i]);
+            const __nv_bfloat162 *g2 = reinterpret_cast<const __nv_bfloat162 *>(&gv[i]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float2 a = __bfloat1622float2(o2[e]);
                 const float2 b = __bfloat1622float2(g2[e]);
-                acc = fmaf(a.x, b.x, acc);
-                acc = fmaf(a.y, b.y, acc);
+                acc[i] = fmaf(a.x, b.x, acc[i]);
+                acc[i] = fmaf(a.y, b.y, acc[i]);
             }
         }
 #pragma unroll
-        for (int off = 16; off; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-        if (lane == 0) {
+        for (int off = 16; off; off >>= 1)
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+        // lane i writes row i's
+        float mine = acc[0];
+#pragma unroll
+        for (int i = 1; i < ROWS; ++i) mine = lane == i ? acc[i] : mine;
+        const int64_t r = r0 + lane;
+        if (lane < ROWS && r < rows) {
             const int64_t h = r % Hq;
             const int64_t bs = r / Hq;   // b * S + s
             const int64_t b = bs / S, s = bs % S;
-            delta[(b * Hq + h) * S + s] = acc;
+            delta[(b * Hq + h) * S + s] = mine;
         }
     }
 }
@@ -1074,7 +1090,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 int launch_delta(const BwdPtrs &p, const BwdArgs &a, int D, cudaStream_t st)
 {
     const int64_t rows = (int64_t)a.B * a.S * a.Hq;
-    int64_t blocks = (rows + 7) / 8;
+    int64_t blocks = (rows + 31) / 32;
     const int64_t cap = (int64_t)sm_count() * 8;
     if (blocks > cap) blocks = cap;
     bwd_delta_kernel<<<(unsigned)blocks, 256, 0, st>>>(
@@ -1110,7 +1126,7 @@ int launch_window_d(const BwdPtrs &p, BwdArgs a, cudaStream_t st)
     }
     a.upc = (a.S + T - 1) / T;
     a.tpc = (a.Sk + T - 1) / T;
-    a.sp = sink_plan<T>(a.win, a.S, a.Sk, a.Hq / a.Hkv);
+    a.sp = sink_plan<T, T>(a.win, a.S, a.Sk, a.Hq / a.Hkv);
     const int64_t qunits = (int64_t)a.upc * a.B * a.Hq;
     const int64_t kunits = ((int64_t)a.tpc + (int64_t)a.sp.tiles * a.sp.pieces) * a.B * a.Hkv;
     if (qunits > 0x7fffffffLL || kunits > 0x7fffffffLL) return CP_EUNSUPPORTED;
@@ -1180,8 +1196,7 @@ size_t bwd_workspace_bytes(int B, int Hq, int64_t S)
 
 size_t window_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, int dtype, const Window &w)
 {
-    const int grp = Hq / Hkv, Sk = Sq + w.off;
-    const SinkPlan sp = dtype == CP_BF16 ? sink_plan<T>(w, Sq, Sk, grp) : sink_plan<WINDOW_F32_TILE>(w, Sq, Sk, grp);
+    const SinkPlan sp = dtype == CP_BF16 ? sink_plan<T, T>(w, Sq, Sq + w.off, Hq / Hkv) : window_f32_plan(w, Sq, Hq / Hkv);
     size_t b = bwd_workspace_bytes(B, Hq, Sq);
     if (sp.pieces) b += (size_t)B * Hkv * (size_t)window_part_rows(w, sp) * D * sizeof(float);
     return (b + 255u) & ~(size_t)255u;

@@ -384,21 +384,21 @@ struct WinQIter {
     }
 };
 
-// How the sinks' walk is cut: tiles of sink keys, pieces per (batch, kv head, tile)
-// and query tiles of a piece -- as many as a window unit has, but not below 16.
+// How the sinks' walk is cut: tiles of KEYS sink keys, pieces per (batch, kv head, tile)
+// and tiles of QUERIES rows of a piece -- as many as a window unit has, but not below 16.
 struct SinkPlan {
     int tiles, pieces, each;
 };
-template <int TILE>
+template <int KEYS, int QUERIES>
 CP_HD SinkPlan sink_plan(const Window &w, int Sq, int Sk, int grp)
 {
     SinkPlan s{0, 0, 1};
     const int64_t rows = (int64_t)Sq - ((int64_t)w.window - w.off > 0 ? (int64_t)w.window - w.off : 0);
     if (w.sinks == 0 || rows <= 0) return s;     // no row is behind its window's first key
     const int sinks = w.sinks < Sk ? w.sinks : Sk;
-    s.tiles = (sinks + TILE - 1) / TILE;
-    const int64_t all = (rows + TILE - 1) / TILE * grp;
-    int64_t each = ((int64_t)w.window / TILE + 2) * grp;
+    s.tiles = (sinks + KEYS - 1) / KEYS;
+    const int64_t all = (rows + QUERIES - 1) / QUERIES * grp;
+    int64_t each = ((int64_t)w.window / QUERIES + 2) * grp;
     each = each < 16 ? 16 : each;
     s.each = (int)(each < all ? each : all);
     s.pieces = (int)((all + s.each - 1) / s.each);

@@ -527,6 +527,34 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const float NEG_INF = -INFINITY;
         bool ok = true;
         int nu = 0, nt = 0, nx = 0;   // units finished, tiles done, row-max exchanges so far
+        // MODE_WINDOW: a unit's output waits until the next unit's first P is computed, so that
+        // the unit's last PV, and then this epilogue, run beside the next unit's first products.
+        bool pend = false, p_valid = false;
+        float p_m = 0.f, p_l = 0.f;   // the unit's reference and row sum
+        __nv_bfloat16 *p_row = nullptr;
+        float *p_lse = nullptr;
+        auto put_unit = [&]() {
+            const float inv = p_l > 0.f ? 1.f / p_l : 0.f;
+            const bool a32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+#pragma unroll
+            for (int pc = 0; pc < D / 64; ++pc) {   // 32 columns at a time: P's registers are live here
+                uint32_t o[32], pk[16];
+                tmem_ld_x32(tO + 32u * pc, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    pk[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                if (a32) {
+                    store_warp_rows<16>(p_row + 32 * pc, p_valid, pk, lane);
+                } else if (p_valid) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p_row + 32 * pc);
+#pragma unroll
+                    for (int v4 = 0; v4 < 4; ++v4)
+                        dst[v4] = make_uint4(pk[4 * v4], pk[4 * v4 + 1], pk[4 * v4 + 2], pk[4 * v4 + 3]);
+                }
+            }
+            if (p_valid && half == 0) *p_lse = p_l > 0.f ? (p_m + lg2(p_l)) * 0.69314718055994531f : NEG_INF;
+            pend = false;
+        };
 
         // Every item, empty ones included, decoded one ahead: the next one is
         // decoded while this unit's last PV completes.
@@ -645,6 +673,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 mx0 = fmax3(mx0, s[124], s[125]);
                 mx1 = fmax3(mx1, s[126], s[127]);
                 mx0 = fmax3(mx0, mx2, mx3);
+                if constexpr (WIN) {   // the previous unit's row sums, before their buffer is written again
+                    if (j == 0 && pend) {
+                        if (!waitw(BAR(B_MX), (nx - 1) & 1, wc)) {
+                            ok = false;
+                            break;
+                        }
+                        const float *pl = pm + ((nx - 1) & 1) * 256;
+                        p_l = pl[row] + pl[128 + row];
+                    }
+                }
                 // Publish this half's row maximum (double-buffered by exchange
                 // parity; the barrier's phase completes once all 256 threads
                 // published theirs).
@@ -714,6 +752,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     break;
                 }
                 tc_fence_after();
+                if constexpr (WIN) {
+                    if (j == 0 && pend) put_unit();
+                }
                 if (j > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c) {
@@ -731,6 +772,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(B_PFULL));
+            }
+            if constexpr (WIN) {
+                if (!ok) break;
+                float *pmn = pm + (nx & 1) * 256;   // this half's share of the row sums
+                pmn[half * 128 + row] = l_run;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(B_MX));
+                ++nx;
+                pend = true;
+                p_m = m_run;
+                p_valid = valid;
+                const int r = dbg_coord(a.err, valid ? qpos : 0, a.S);
+                p_row = out + (((int64_t)w.b * a.S + r) * a.Hq + w.h) * D + (D / 2) * half;
+                p_lse = lse + ((int64_t)w.b * a.Hq + w.h) * a.S + r;
+                advance(it);
+                continue;
             }
             advance(it);
             if (!ok || !waitw(BAR(B_OFIN), nu & 1, wc)) {
@@ -916,6 +973,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         l_tot > 0.f ? (m_run + lg2(l_tot)) * 0.69314718055994531f : NEG_INF;
             }
             ++nu;
+        }
+        if constexpr (WIN) {   // the last unit's output
+            if (ok && pend && waitw(BAR(B_MX), (nx - 1) & 1, wc) && waitw(BAR(B_PFREE), (nt - 1) & 1, wc)) {
+                tc_fence_after();
+                const float *pl = pm + ((nx - 1) & 1) * 256;
+                p_l = pl[row] + pl[128 + row];
+                put_unit();
+            }
         }
         __syncwarp();
         tc_fence_before();

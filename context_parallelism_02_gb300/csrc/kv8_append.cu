@@ -97,24 +97,23 @@ __global__ void __launch_bounds__(WARPS * 32) kv8_append_kernel(Kv8AppendArgs a,
     const int n = a.n_new ? max(0, min(a.n_new[b], a.n)) : a.n;
     const int64_t slot0 = (len / KV8_BLOCK + t) * KV8_BLOCK;    // the block's first slot
     if (slot0 >= len + n) return;
-    const int64_t lp = slot0 >> a.pool.page_shift;
-    const int id = kv4_page(a.pool, b, lp);
-    if (id < 0) return;
-    const int at = (int)(slot0 & ((1 << a.pool.page_shift) - 1));
     const int lo = slot0 < len ? (int)(len - slot0) : 0;        // rows [lo, hi) of the block are new
     const int hi = (int)(len + n - slot0 < KV8_BLOCK ? len + n - slot0 : KV8_BLOCK);
     const int64_t *st = which ? a.vs : a.ks;
     const T *src = static_cast<const T *>(which ? a.v : a.k) + b * st[0] + h * st[2] + lane % L::LANES * L::EPL;
     const int j0 = (int)(slot0 - len);                          // new token of row 0 (negative: an older one)
     const int r0 = lane / L::LANES;
-    float *sp = kv8_scale(a.pool, id, h, which, at);
-    const float held = lo > 0 ? *sp : 0.f;
-    uint4 x[L::N];
+    uint4 x[L::N];                                              // on their way while the page is looked up
 #pragma unroll
     for (int i = 0; i < L::N; ++i) {
         const int r = r0 + i * L::ROWS;
         x[i] = r >= lo && r < hi ? *reinterpret_cast<const uint4 *>(src + (int64_t)(j0 + r) * st[1]) : make_uint4(0, 0, 0, 0);
     }
+    const int id = kv4_page(a.pool, b, slot0 >> a.pool.page_shift);
+    if (id < 0) return;
+    const int at = (int)(slot0 & ((1 << a.pool.page_shift) - 1));
+    float *sp = kv8_scale(a.pool, id, h, which, at);
+    const float held = lo > 0 ? *sp : 0.f;
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < L::N; ++i) top = max(top, top_bits<T>(x[i]));
@@ -145,11 +144,11 @@ __global__ void __launch_bounds__(WARPS * 32) kv8_append_kernel(Kv8AppendArgs a,
     if (lane == 0 && (lo == 0 || scale > held)) *sp = scale;
 }
 
-// 16 rows of one head: 16 codes a lane.
+// 16 rows of one head: 8 codes a lane, so that reads and writes cover whole rows.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(WARPS * 32) kv8_gather_kernel(Kv8GatherArgs a, int blocks, int64_t units)
 {
-    constexpr int LANES = D / 16, ROWS = 32 / LANES, N = 16 / ROWS;
+    constexpr int LANES = D / 8, ROWS = 32 / LANES, N = 16 / ROWS;
     const int lane = threadIdx.x & 31;
     kv4_begin();
     const int64_t unit = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
@@ -160,47 +159,50 @@ __global__ void __launch_bounds__(WARPS * 32) kv8_gather_kernel(Kv8GatherArgs a,
     rest /= a.pool.Hkv;
     const int t = (int)(rest % blocks), b = (int)(rest / blocks);
     const int64_t len = kv4_len(a.pool, b), start = a.start ? a.start[b] : 0;
-    uint4 x[N];
-    float scale[N];
+    // lane r < 16: where row r comes from
+    const uint8_t *src = nullptr;
+    float scale = 0.f;
+    {
+        const int j = t * 16 + lane;
+        const int64_t slot = start + j;
+        if (lane < 16 && j < a.count && slot < len) {
+            if (slot < 0) {
+                kv4_report(a.pool.err);
+            } else {
+                const int id = kv4_page(a.pool, b, slot >> a.pool.page_shift);
+                const int at = (int)(slot & ((1 << a.pool.page_shift) - 1));
+                if (id >= 0) {
+                    src = kv8_row<D>(a.pool, id, h, which, at);
+                    scale = *kv8_scale(a.pool, id, h, which, at);
+                }
+            }
+        }
+    }
+    uint2 x[N];
+    float f[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int j = t * 16 + lane / LANES + i * ROWS;
-        const int64_t slot = start + j;
-        x[i] = make_uint4(0, 0, 0, 0);
-        scale[i] = 0.f;
-        if (j >= a.count || slot >= len) continue;
-        if (slot < 0) {
-            kv4_report(a.pool.err);
-            continue;
-        }
-        const int id = kv4_page(a.pool, b, slot >> a.pool.page_shift);
-        if (id < 0) continue;
-        const int at = (int)(slot & ((1 << a.pool.page_shift) - 1));
-        x[i] = *reinterpret_cast<const uint4 *>(kv8_row<D>(a.pool, id, h, which, at) + lane % LANES * 16);
-        scale[i] = *kv8_scale(a.pool, id, h, which, at);
+        const int r = lane / LANES + i * ROWS;
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
+        x[i] = p ? *reinterpret_cast<const uint2 *>(p + lane % LANES * 8) : make_uint2(0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __shfl_sync(0xffffffffu, scale, lane / LANES + i * ROWS);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int j = t * 16 + lane / LANES + i * ROWS;
         if (j >= a.count) continue;
-        const int64_t at = (((int64_t)b * a.count + j) * a.pool.Hkv + h) * D + lane % LANES * 16;
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        float4 f[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            f[e] = kv8_floats(w[e]);
-            f[e].x *= scale[i], f[e].y *= scale[i], f[e].z *= scale[i], f[e].w *= scale[i];
-        }
+        const int64_t at = (((int64_t)b * a.count + j) * a.pool.Hkv + h) * D + lane % LANES * 8;
+        float4 u = kv8_floats(x[i].x), v = kv8_floats(x[i].y);
+        u.x *= f[i], u.y *= f[i], u.z *= f[i], u.w *= f[i];
+        v.x *= f[i], v.y *= f[i], v.z *= f[i], v.w *= f[i];
         if (BF16) {
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(which ? a.v : a.k) + at);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                dst[e] = make_uint4(tc::pack_bf16(f[2 * e].x, f[2 * e].y), tc::pack_bf16(f[2 * e].z, f[2 * e].w),
-                                    tc::pack_bf16(f[2 * e + 1].x, f[2 * e + 1].y), tc::pack_bf16(f[2 * e + 1].z, f[2 * e + 1].w));
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(which ? a.v : a.k) + at) =
+                make_uint4(tc::pack_bf16(u.x, u.y), tc::pack_bf16(u.z, u.w), tc::pack_bf16(v.x, v.y), tc::pack_bf16(v.z, v.w));
         } else {
             float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(which ? a.v : a.k) + at);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = f[e];
+            dst[0] = u;
+            dst[1] = v;
         }
     }
 }

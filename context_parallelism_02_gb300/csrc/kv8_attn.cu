@@ -733,11 +733,20 @@ __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, 
             }
             __syncthreads();
             if (slot >= len) continue;
-            for (int r = 0; r < n; ++r)
+            auto add = [&](float s, int r) {
                 if (slot < limit[r] && (slot >= low[r] || slot < a.sinks)) {
-                    sum += ex2(x[r0 + r] - lse2[r]);
+                    sum += ex2(s - lse2[r]);
                     any = true;
                 }
+            };
+            if (sh.rows % 4 == 0) {          // n is a multiple of 4 too
+                for (int r = 0; r < n; r += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(x + r0 + r);
+                    add(v.x, r), add(v.y, r + 1), add(v.z, r + 2), add(v.w, r + 3);
+                }
+            } else {
+                for (int r = 0; r < n; ++r) add(x[r0 + r], r);
+            }
         }
         if (any) a.mass[(int64_t)bh * cap + slot] += sum;
     }

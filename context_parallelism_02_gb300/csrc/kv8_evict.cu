@@ -101,8 +101,19 @@ __global__ void __launch_bounds__(THREADS) kv8_select_kernel(Kv8EvictArgs a, int
         return key_of(mass[s]);
     };
     auto key = [&](int s) -> uint32_t { return in_shared ? keys[s - s0] : key_at(s); };
-    if (in_shared)
-        for (int s = s0 + threadIdx.x; s < s1; s += THREADS) keys[s - s0] = key_at(s);
+    if (in_shared) {
+        constexpr int BATCH = 8;                             // loads in flight of a thread
+        for (int t = s0 + threadIdx.x; t < s1; t += BATCH * THREADS) {
+            float x[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) x[i] = t + i * THREADS < s1 ? mass[t + i * THREADS] : 0.f;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int s = t + i * THREADS;
+                if (s < s1) keys[s - s0] = s < a.first || s >= len - a.last ? 0xffffffffu : key_of(x[i]);
+            }
+        }
+    }
     if (threadIdx.x == 0) sm.prefix = 0, sm.want = (uint32_t)n;
     if (threadIdx.x < 256) sm.hist[0][threadIdx.x] = sm.hist[1][threadIdx.x] = 0;
     __syncthreads();
@@ -110,6 +121,7 @@ __global__ void __launch_bounds__(THREADS) kv8_select_kernel(Kv8EvictArgs a, int
         const int shift = 24 - 8 * round;
         uint32_t *hist = sm.hist[round & 1];
         const uint32_t prefix = sm.prefix, want = sm.want;
+#pragma unroll 4
         for (int s = s0 + threadIdx.x; s < s1; s += THREADS) {
             const uint32_t k = key(s);
             if (round == 0 || k >> (shift + 8) == prefix) atomicAdd(&hist[k >> shift & 255u], 1u);
@@ -117,7 +129,9 @@ __global__ void __launch_bounds__(THREADS) kv8_select_kernel(Kv8EvictArgs a, int
         cl.sync();
         if (threadIdx.x < 256) {
             uint32_t t = 0;
-            for (int r = 0; r < C; ++r) t += cl.map_shared_rank(hist, r)[threadIdx.x];
+#pragma unroll
+            for (int r = 0; r < MAX_CLUSTER; ++r)            // all loads in flight
+                if (r < C) t += cl.map_shared_rank(hist, r)[threadIdx.x];
             sm.total[threadIdx.x] = t;
             if (round >= 1) sm.hist[(round + 1) & 1][threadIdx.x] = 0;   // read by the cluster a round ago
         }

@@ -2,12 +2,16 @@
 // on the CUDA cores in fp32 arithmetic (bounded by the FMA pipe: no tensor-core kind
 // holds fp32's 24 bits).
 //
-// Tiles of 64 rows by 64 keys, 256 threads as 16 x 16, each with a 4 x 4 part of the
-// scores (rows ty + 16 i, columns tx + 16 j) and of the 64 x D products 4 rows by D / 16
+// Tiles of 32 rows by 64 columns, 128 threads as 8 x 16, each with a 4 x 4 part of the
+// scores (rows ty + 8 i, columns tx + 16 j) and of the 32 x D products 4 rows by D / 16
 // columns (4 tx + 64 j).  Per four elements of the inner axis a thread reads 8 x 16 bytes
-// of shared memory for 64 FMAs.  The walks are those of the bf16 kernels: WinIter for the
-// query-stationary kernels, WinQIter and the sinks' pieces for dK and dV; every output
-// element is written once.
+// of shared memory for 64 FMAs.  Small blocks, several to an SM, cover each other's loads
+// and leave less behind the mask than 64 x 64 tiles of 256 threads (which took 318 us where
+// these take 212 for a step of 2 x 1001 rows, 6 heads on 2, D = 64, window 200).  The walks are those
+// of the bf16 kernels: WinIter for the query-stationary kernels, WinQIter and the sinks'
+// pieces for dK and dV, whose heads of a group go to the blocks of a cluster and are added
+// up in order through distributed shared memory; every output element is written once.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -21,15 +25,17 @@ namespace cp {
 
 namespace {
 
-constexpr int T = WINDOW_F32_TILE;
-constexpr int THREADS = 256;
-constexpr int PS = T + 4;             // row stride of a T x T tile in shared memory
+namespace cg = cooperative_groups;
+
+constexpr int R = WINDOW_F32_ROWS, T = WINDOW_F32_COLS;
+constexpr int THREADS = 128;
+constexpr int PS = T + 4;             // row stride of an R x T tile in shared memory
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994530942f;
 
 template <int D>
 struct Rows {
     static constexpr int STRIDE = D + 4;        // a warp's 8 rows of 16 bytes fall on 32 banks
-    static constexpr int FLOATS = T * STRIDE;
+    static constexpr int FEW = R * STRIDE, FLOATS = T * STRIDE;
 };
 
 struct Args {
@@ -41,11 +47,12 @@ struct Args {
     SinkPlan sp;
 };
 
-// n rows of x [B][S][H][D] (head h, from row r0) into shared memory, the rest 0.
-template <int D>
+// n rows of x [B][S][H][D] (head h, from row r0) into COUNT rows of shared memory, the rest 0.
+template <int D, int COUNT>
 __device__ __forceinline__ void load_rows(float *dst, const float *x, int64_t b, int S, int H, int h, int r0, int n)
 {
-    for (int i = threadIdx.x; i < T * (D / 4); i += THREADS) {
+#pragma unroll 8
+    for (int i = threadIdx.x; i < COUNT * (D / 4); i += THREADS) {
         const int r = i / (D / 4), c = i % (D / 4);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < n) v = *reinterpret_cast<const float4 *>(x + ((b * S + r0 + r) * H + h) * D + c * 4);
@@ -53,7 +60,7 @@ __device__ __forceinline__ void load_rows(float *dst, const float *x, int64_t b,
     }
 }
 
-// acc[i][j] = A[ty + 16 i] . B[tx + 16 j]
+// acc[i][j] = A[ty + 8 i] . B[tx + 16 j]
 template <int D>
 __device__ __forceinline__ void dots(const float *A, const float *B, float (&acc)[4][4])
 {
@@ -67,7 +74,7 @@ __device__ __forceinline__ void dots(const float *A, const float *B, float (&acc
         float4 a[4], b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            a[i] = *reinterpret_cast<const float4 *>(A + (ty + 16 * i) * Rows<D>::STRIDE + d);
+            a[i] = *reinterpret_cast<const float4 *>(A + (ty + 8 * i) * Rows<D>::STRIDE + d);
             b[i] = *reinterpret_cast<const float4 *>(B + (tx + 16 * i) * Rows<D>::STRIDE + d);
         }
 #pragma unroll
@@ -82,7 +89,7 @@ __device__ __forceinline__ void dots(const float *A, const float *B, float (&acc
     }
 }
 
-// acc[i][4 j + e] += sum_k P[ty + 16 i][k] B[k][4 tx + 64 j + e]
+// acc[i][4 j + e] += sum_k P[ty + 8 i][k] B[k][4 tx + 64 j + e]
 template <int D>
 __device__ __forceinline__ void product(const float *P, const float *B, float (&acc)[4][D / 16])
 {
@@ -91,7 +98,7 @@ __device__ __forceinline__ void product(const float *P, const float *B, float (&
     for (int k = 0; k < T; k += 4) {
         float4 p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(P + (ty + 16 * i) * PS + k);
+        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(P + (ty + 8 * i) * PS + k);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -135,7 +142,7 @@ __device__ __forceinline__ float row_sum(float x)
     return x;
 }
 
-// The unit's 64 query rows: heads fastest, so that the heads of a group share K and V in L2.
+// The unit's query rows: heads fastest, so that the heads of a group share K and V in L2.
 struct QUnit {
     int b, h, kvh, q0, rows;
     __device__ __forceinline__ QUnit(const Args &a)
@@ -144,9 +151,9 @@ struct QUnit {
         h = (int)(u % (unsigned)a.Hq);
         u /= (unsigned)a.Hq;
         b = (int)(u % (unsigned)a.B);
-        q0 = (int)(u / (unsigned)a.B) * T;
+        q0 = (int)(u / (unsigned)a.B) * R;
         kvh = h / (a.Hq / a.Hkv);
-        rows = a.Sq - q0 < T ? a.Sq - q0 : T;
+        rows = a.Sq - q0 < R ? a.Sq - q0 : R;
     }
 };
 
@@ -154,17 +161,17 @@ struct QUnit {
 template <int D>
 __device__ __forceinline__ void load_keys(float *dst, const float *x, const Args &a, const QUnit &u, const WinIter<T> &it)
 {
-    load_rows<D>(dst, x, u.b, a.Sk, a.Hkv, u.kvh, it.start(), it.len());
+    load_rows<D, T>(dst, x, u.b, a.Sk, a.Hkv, u.kvh, it.start(), it.len());
 }
 
 template <int D>
 __global__ void __launch_bounds__(THREADS) window_f32_fwd_kernel(const Args a, float *__restrict__ out, float *__restrict__ lse)
 {
     extern __shared__ __align__(16) float sm[];
-    float *Q = sm, *K = Q + Rows<D>::FLOATS, *V = K + Rows<D>::FLOATS, *P = V + Rows<D>::FLOATS;
+    float *Q = sm, *K = Q + Rows<D>::FEW, *V = K + Rows<D>::FLOATS, *P = V + Rows<D>::FLOATS;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const QUnit u(a);
-    load_rows<D>(Q, a.q, u.b, a.Sq, a.Hq, u.h, u.q0, u.rows);
+    load_rows<D, R>(Q, a.q, u.b, a.Sq, a.Hq, u.h, u.q0, u.rows);
     const float sl2 = a.scale * LOG2E;
     float o[4][D / 16], m[4], l[4];
 #pragma unroll
@@ -186,7 +193,7 @@ __global__ void __launch_bounds__(THREADS) window_f32_fwd_kernel(const Args a, f
         const bool full = it.full(a.win, p0, p1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const Seen see(it, a.win, p0 + ty + 16 * i);
+            const Seen see(it, a.win, p0 + ty + 8 * i);
             float top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(THREADS) window_f32_fwd_kernel(const Args a, f
             for (int j = 0; j < 4; ++j) {
                 x[i][j] = exp2f(x[i][j] - base);
                 sum += x[i][j];
-                P[(ty + 16 * i) * PS + tx + 16 * j] = x[i][j];
+                P[(ty + 8 * i) * PS + tx + 16 * j] = x[i][j];
             }
             l[i] = l[i] * f + row_sum(sum);
             m[i] = mn;
@@ -212,7 +219,7 @@ __global__ void __launch_bounds__(THREADS) window_f32_fwd_kernel(const Args a, f
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
+        const int r = ty + 8 * i;
         if (r >= u.rows) continue;
         const float inv = l[i] > 0.f ? 1.f / l[i] : l[i];
         float *row = out + (((int64_t)u.b * a.Sq + u.q0 + r) * a.Hq + u.h) * D;
@@ -245,16 +252,16 @@ template <int D>
 __global__ void __launch_bounds__(THREADS) window_f32_dq_kernel(const Args a, float *__restrict__ dq)
 {
     extern __shared__ __align__(16) float sm[];
-    float *Q = sm, *G = Q + Rows<D>::FLOATS, *K = G + Rows<D>::FLOATS, *V = K + Rows<D>::FLOATS, *P = V + Rows<D>::FLOATS;
+    float *Q = sm, *G = Q + Rows<D>::FEW, *K = G + Rows<D>::FEW, *V = K + Rows<D>::FLOATS, *P = V + Rows<D>::FLOATS;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const QUnit u(a);
-    load_rows<D>(Q, a.q, u.b, a.Sq, a.Hq, u.h, u.q0, u.rows);
-    load_rows<D>(G, a.dout, u.b, a.Sq, a.Hq, u.h, u.q0, u.rows);
+    load_rows<D, R>(Q, a.q, u.b, a.Sq, a.Hq, u.h, u.q0, u.rows);
+    load_rows<D, R>(G, a.dout, u.b, a.Sq, a.Hq, u.h, u.q0, u.rows);
     const float sl2 = a.scale * LOG2E;
     float acc[4][D / 16], lse2[4], delta[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
+        const int r = ty + 8 * i;
         const int64_t at = ((int64_t)u.b * a.Hq + u.h) * a.Sq + u.q0 + r;
         lse2[i] = r < u.rows ? a.lse[at] * LOG2E : 0.f;
         delta[i] = r < u.rows ? a.delta[at] : 0.f;
@@ -274,11 +281,11 @@ __global__ void __launch_bounds__(THREADS) window_f32_dq_kernel(const Args a, fl
         const bool full = it.full(a.win, p0, p1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const Seen see(it, a.win, p0 + ty + 16 * i);
+            const Seen see(it, a.win, p0 + ty + 8 * i);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bool on = full || see.at(tx + 16 * j);
-                P[(ty + 16 * i) * PS + tx + 16 * j] = on ? exp2f(fmaf(x[i][j], sl2, -lse2[i])) * (g[i][j] - delta[i]) : 0.f;
+                P[(ty + 8 * i) * PS + tx + 16 * j] = on ? exp2f(fmaf(x[i][j], sl2, -lse2[i])) * (g[i][j] - delta[i]) : 0.f;
             }
         }
         __syncthreads();
@@ -286,7 +293,7 @@ __global__ void __launch_bounds__(THREADS) window_f32_dq_kernel(const Args a, fl
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
+        const int r = ty + 8 * i;
         if (r >= u.rows) continue;
         float *row = dq + (((int64_t)u.b * a.Sq + u.q0 + r) * a.Hq + u.h) * D;
 #pragma unroll
@@ -301,13 +308,15 @@ template <int D>
 __global__ void __launch_bounds__(THREADS) window_f32_dkdv_kernel(const Args a, float *__restrict__ dk, float *__restrict__ dv)
 {
     extern __shared__ __align__(16) float sm[];
-    float *K = sm, *V = K + Rows<D>::FLOATS, *Q = V + Rows<D>::FLOATS, *G = Q + Rows<D>::FLOATS;
-    float *P = G + Rows<D>::FLOATS, *S = P + T * PS, *lse2 = S + T * PS, *delta = lse2 + T;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, grp = a.Hq / a.Hkv;
-    const int tpc = (a.Sk + T - 1) / T;
+    float *K = sm, *V = K + Rows<D>::FEW, *Q = V + Rows<D>::FEW, *G = Q + Rows<D>::FLOATS;
+    float *P = G + Rows<D>::FLOATS, *S = P + R * PS, *lse2 = S + R * PS, *delta = lse2 + T;
+    cg::cluster_group cl = cg::this_cluster();
+    const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, grp = a.Hq / a.Hkv / C;   // heads of this block
+    const int tpc = (a.Sk + R - 1) / R;
     // window units, then the pieces of the tiles of sinks
     int piece = 0, t, kvh, b;
-    unsigned x = blockIdx.x;
+    unsigned x = blockIdx.x / (unsigned)C;
     if (x < (unsigned)tpc * a.B * a.Hkv) {
         t = (int)(x % (unsigned)tpc);
         x /= (unsigned)tpc;
@@ -320,9 +329,10 @@ __global__ void __launch_bounds__(THREADS) window_f32_dkdv_kernel(const Args a, 
     }
     kvh = (int)(x % (unsigned)a.Hkv);
     b = (int)(x / (unsigned)a.Hkv);
-    const int ks = t * T, kl = a.Sk - ks < T ? a.Sk - ks : T;
-    load_rows<D>(K, a.k, b, a.Sk, a.Hkv, kvh, ks, kl);
-    load_rows<D>(V, a.v, b, a.Sk, a.Hkv, kvh, ks, kl);
+    const int h0 = (kvh * C + rank) * grp;
+    const int ks = t * R, kl = a.Sk - ks < R ? a.Sk - ks : R;
+    load_rows<D, R>(K, a.k, b, a.Sk, a.Hkv, kvh, ks, kl);
+    load_rows<D, R>(V, a.v, b, a.Sk, a.Hkv, kvh, ks, kl);
     float adk[4][D / 16], adv[4][D / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -330,13 +340,13 @@ __global__ void __launch_bounds__(THREADS) window_f32_dkdv_kernel(const Args a, 
         for (int j = 0; j < D / 16; ++j) adk[i][j] = adv[i][j] = 0.f;
     const float sl2 = a.scale * LOG2E;
     WinQIter<T> it;
-    if (piece == 0) it.window(a.win, a.Sq, ks, kl, kvh * grp, grp);
-    else it.sinks(a.win, a.Sq, ks, kvh * grp, grp, piece - 1, a.sp.each);
+    if (piece == 0) it.window(a.win, a.Sq, ks, kl, h0, grp);
+    else it.sinks(a.win, a.Sq, ks, h0, grp, piece - 1, a.sp.each);
     for (; it.count() > 0; it.next()) {
         const int h = it.head(), qa = it.start(), ql = it.len();
         __syncthreads();
-        load_rows<D>(Q, a.q, b, a.Sq, a.Hq, h, qa, ql);
-        load_rows<D>(G, a.dout, b, a.Sq, a.Hq, h, qa, ql);
+        load_rows<D, T>(Q, a.q, b, a.Sq, a.Hq, h, qa, ql);
+        load_rows<D, T>(G, a.dout, b, a.Sq, a.Hq, h, qa, ql);
         if (threadIdx.x < T) {
             const int64_t at = ((int64_t)b * a.Hq + h) * a.Sq + qa + threadIdx.x;
             lse2[threadIdx.x] = threadIdx.x < ql ? a.lse[at] * LOG2E : 0.f;
@@ -348,46 +358,58 @@ __global__ void __launch_bounds__(THREADS) window_f32_dkdv_kernel(const Args a, 
         dots<D>(V, G, g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int kpos = ks + ty + 16 * i;
+            const int kpos = ks + ty + 8 * i;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = tx + 16 * j, back = qa + c + a.win.off - kpos;   // how far the key lies behind the row
                 const bool on = c < ql && (piece == 0 ? back >= 0 && back < a.win.window
                                                       : kpos < a.win.sinks && back >= a.win.window);
                 const float p = on ? exp2f(fmaf(s[i][j], sl2, -lse2[c])) : 0.f;
-                P[(ty + 16 * i) * PS + c] = p;
-                S[(ty + 16 * i) * PS + c] = on ? p * (g[i][j] - delta[c]) : 0.f;
+                P[(ty + 8 * i) * PS + c] = p;
+                S[(ty + 8 * i) * PS + c] = on ? p * (g[i][j] - delta[c]) : 0.f;
             }
         }
         __syncthreads();
         product<D>(P, G, adv);
         product<D>(S, Q, adk);
     }
+    // the cluster's shares: each block leaves its own in shared memory (dK in Q's place, dV in
+    // G's), and block `rank` adds up its part of the rows over the blocks in order
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i, kpos = ks + r;
-        if (r >= kl) continue;
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            const int at = (ty + 8 * i) * D + 4 * tx + 64 * j;
+            *reinterpret_cast<float4 *>(Q + at) = make_float4(adk[i][4 * j], adk[i][4 * j + 1], adk[i][4 * j + 2], adk[i][4 * j + 3]);
+            *reinterpret_cast<float4 *>(G + at) = make_float4(adv[i][4 * j], adv[i][4 * j + 1], adv[i][4 * j + 2], adv[i][4 * j + 3]);
+        }
+    cl.sync();
+    for (int r = rank; r < kl; r += C) {
+        const int kpos = ks + r;
         const bool sink = a.sp.pieces > 0 && kpos < a.win.sinks;
         if (!sink && piece != 0) continue;
         const int64_t at = (((int64_t)b * a.Sk + kpos) * a.Hkv + kvh) * D;
         float *slot = a.part + (((int64_t)b * a.Hkv + kvh) * window_part_rows(a.win, a.sp) + (int64_t)piece * 2 * a.win.sinks + kpos) * D;
         float *rk = sink ? slot : dk + at, *rv = sink ? slot + (int64_t)a.win.sinks * D : dv + at;
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-            const int c = 4 * tx + 64 * j;
-            *reinterpret_cast<float4 *>(rk + c) = make_float4(adk[i][4 * j] * a.scale, adk[i][4 * j + 1] * a.scale,
-                                                             adk[i][4 * j + 2] * a.scale, adk[i][4 * j + 3] * a.scale);
-            *reinterpret_cast<float4 *>(rv + c) = make_float4(adv[i][4 * j], adv[i][4 * j + 1], adv[i][4 * j + 2], adv[i][4 * j + 3]);
+        for (int c = threadIdx.x; c < 2 * D; c += THREADS) {
+            const bool v = c >= D;
+            const int el = r * D + (v ? c - D : c);
+            float sum = 0.f;
+            for (int o = 0; o < C; ++o) sum += cl.map_shared_rank(v ? G : Q, o)[el];
+            if (v) rv[c - D] = sum;
+            else rk[c] = sum * a.scale;
         }
     }
+    cl.sync();                       // the other blocks have read this one's share
 }
 
 template <int D>
-constexpr int SMEM_FWD = (3 * Rows<D>::FLOATS + T * PS) * 4;
+constexpr int SMEM_FWD = (Rows<D>::FEW + 2 * Rows<D>::FLOATS + R * PS) * 4;
 template <int D>
-constexpr int SMEM_DQ = (4 * Rows<D>::FLOATS + T * PS) * 4;
+constexpr int SMEM_DQ = (2 * Rows<D>::FEW + 2 * Rows<D>::FLOATS + R * PS) * 4;
 template <int D>
-constexpr int SMEM_DKDV = (4 * Rows<D>::FLOATS + 2 * T * PS + 2 * T) * 4;
+constexpr int SMEM_DKDV = (2 * Rows<D>::FEW + 2 * Rows<D>::FLOATS + 2 * R * PS + 2 * T) * 4;
 
 template <int D>
 int prepare()   // the kernels' shared memory, once per device
@@ -417,7 +439,7 @@ Args make_args(const FwdArgs &f)
     a.scale = f.scale;
     a.win = f.win;
     a.win.pack = 0;
-    a.sp = sink_plan<T>(a.win, a.Sq, a.Sk, a.Hq / a.Hkv);
+    a.sp = window_f32_plan(a.win, a.Sq, a.Hq / a.Hkv);
     return a;
 }
 
@@ -426,7 +448,7 @@ int forward(const Args &a, float *out, float *lse, cudaStream_t st)
 {
     const int rc = prepare<D>();
     if (rc) return rc;
-    const int64_t units = (int64_t)((a.Sq + T - 1) / T) * a.B * a.Hq;
+    const int64_t units = (int64_t)((a.Sq + R - 1) / R) * a.B * a.Hq;
     if (units > 0x7fffffffLL) return CP_EUNSUPPORTED;
     window_f32_fwd_kernel<D><<<(unsigned)units, THREADS, SMEM_FWD<D>, st>>>(a, out, lse);
     return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ECUDA;
@@ -437,17 +459,28 @@ int backward(const Args &a, float *dq, float *dk, float *dv, cudaStream_t st)
 {
     const int rc = prepare<D>();
     if (rc) return rc;
-    const int64_t units = (int64_t)((a.Sq + T - 1) / T) * a.B * a.Hq;
-    const int64_t kunits = ((int64_t)((a.Sk + T - 1) / T) + (int64_t)a.sp.tiles * a.sp.pieces) * a.B * a.Hkv;
+    const int C = window_f32_cluster(a.Hq / a.Hkv);
+    const int64_t units = (int64_t)((a.Sq + R - 1) / R) * a.B * a.Hq;
+    const int64_t kunits = ((int64_t)((a.Sk + R - 1) / R) + (int64_t)a.sp.tiles * a.sp.pieces) * a.B * a.Hkv * C;
     if (units > 0x7fffffffLL || kunits > 0x7fffffffLL) return CP_EUNSUPPORTED;
-    const int64_t rows = (int64_t)a.B * a.Sq * a.Hq, cap = (int64_t)sm_count() * 8;
-    const int64_t blocks = (rows + 7) / 8 < cap ? (rows + 7) / 8 : cap;
+    const int64_t rows = (int64_t)a.B * a.Sq * a.Hq, cap = (int64_t)sm_count() * 16;
+    const int64_t need = (rows + THREADS / 32 - 1) / (THREADS / 32), blocks = need < cap ? need : cap;
     window_f32_delta_kernel<D><<<(unsigned)blocks, THREADS, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
     window_f32_dq_kernel<D><<<(unsigned)units, THREADS, SMEM_DQ<D>, st>>>(a, dq);
     if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
-    window_f32_dkdv_kernel<D><<<(unsigned)kunits, THREADS, SMEM_DKDV<D>, st>>>(a, dk, dv);
-    if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)kunits);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_DKDV<D>;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, window_f32_dkdv_kernel<D>, a, dk, dv) != cudaSuccess) return CP_ECUDA;
     return launch_window_sinks<D>(a.part, a.win, a.sp, a.B, a.Hkv, a.Sk, dk, dv, st);
 }
 

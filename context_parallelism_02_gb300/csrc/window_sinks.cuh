@@ -11,7 +11,19 @@
 
 namespace cp {
 
-constexpr int WINDOW_F32_TILE = 64;   // tile rows of the fp32 kernels
+// Tiles of the fp32 kernels: ROWS rows stay with a block (queries, or keys in dK / dV) while
+// tiles of COLS pass by.  dK / dV gives the heads of a group to a cluster of blocks.
+constexpr int WINDOW_F32_ROWS = 32, WINDOW_F32_COLS = 64;
+CP_HD int window_f32_cluster(int grp)   // the largest divisor of the group up to 8
+{
+    int c = grp < 8 ? grp : 8;
+    while (grp % c) --c;
+    return c;
+}
+CP_HD SinkPlan window_f32_plan(const Window &w, int Sq, int grp)
+{
+    return sink_plan<WINDOW_F32_ROWS, WINDOW_F32_COLS>(w, Sq, Sq + w.off, grp / window_f32_cluster(grp));
+}
 
 // Partial gradients, fp32, [B][Hkv][1 + pieces][2 (dK, dV)][sinks][D]: slot 0 from the
 // window unit of the key's tile, the others from the pieces.

@@ -46,10 +46,10 @@ static void rows_walk(const Window &w, int Sq, int Sk, int qt)
     }
 }
 
-template <int TILE>
+template <int KEYS, int TILE>
 static void keys_walk(const Window &w, int Sq, int Sk, int grp)
 {
-    const SinkPlan sp = sink_plan<TILE>(w, Sq, Sk, grp);
+    const SinkPlan sp = sink_plan<KEYS, TILE>(w, Sq, Sk, grp);
     std::vector<int> hit((size_t)grp * Sq * Sk, 0);
     auto add = [&](WinQIter<TILE> it, int ks, int kl, bool sinks) {
         for (; it.count() > 0; it.next())
@@ -61,12 +61,12 @@ static void keys_walk(const Window &w, int Sq, int Sk, int grp)
                         ++hit[((size_t)(it.head() - 5) * Sq + row) * Sk + j];
                 }
     };
-    for (int ks = 0; ks < Sk; ks += TILE) {
-        const int kl = Sk - ks < TILE ? Sk - ks : TILE;
+    for (int ks = 0; ks < Sk; ks += KEYS) {
+        const int kl = Sk - ks < KEYS ? Sk - ks : KEYS;
         WinQIter<TILE> it;
         it.window(w, Sq, ks, kl, 5, grp);
         add(it, ks, kl, false);
-        if (ks / TILE < sp.tiles)
+        if (ks / KEYS < sp.tiles)
             for (int p = 0; p < sp.pieces; ++p) {
                 it.sinks(w, Sq, ks, 5, grp, p, sp.each);
                 add(it, ks, kl, true);
@@ -94,10 +94,10 @@ int main()
                     if (packed) w.pack = w.sinks <= 64 ? (w.sinks + 15) / 16 * 16 : 0;
                     rows_walk<256>(w, s[0], s[1], 128);
                     rows_walk<128>(w, s[0], s[1], 128);
-                    rows_walk<64>(w, s[0], s[1], 64);
+                    rows_walk<64>(w, s[0], s[1], 32);
                     if (packed) continue;
-                    keys_walk<128>(w, s[0], s[1], 1);
-                    keys_walk<64>(w, s[0], s[1], 3);
+                    keys_walk<128, 128>(w, s[0], s[1], 1);
+                    keys_walk<32, 64>(w, s[0], s[1], 3);
                 }
     // positions near the largest
     Window w{0x7ffffbff - 200, 0x7ffffbff, 4, 16};
