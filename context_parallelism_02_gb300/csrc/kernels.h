@@ -23,6 +23,7 @@ struct FwdArgs {
     uint64_t drain_ns;    // bound of the waits that drain copies and MMAs before exit
     int Sk;               // windowed attention: keys (S counts query rows)
     Window win;           // windowed attention
+    FastDiv by_heads, by_batch, by_group;   // windowed attention: Hq, B, Hq / Hkv (set by the launcher)
 };
 
 // Partial results of a split forward (fp32, normalised): n splits of every

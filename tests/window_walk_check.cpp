@@ -99,6 +99,18 @@ int main()
                     keys_walk<128, 128>(w, s[0], s[1], 1);
                     keys_walk<32, 64>(w, s[0], s[1], 3);
                 }
+    // the launches' divisions
+    const uint32_t ds[] = {1, 2, 3, 5, 7, 8, 12, 31, 32, 33, 96, 127, 1000, 4095, 65537, 16777215, 1073741825, 2147483647};
+    for (uint32_t d : ds) {
+        const FastDiv f = fast_div(d);
+        const uint32_t us[] = {0, 1, d - 1, d, d + 1, 2 * d - 1, 2147483647, 2147483646, 2147483647 / d * d, 2147483647 / d * d - 1};
+        for (uint32_t u : us)
+            if (u < 2147483648u && f.div(u) != u / d) return printf("%u / %u\n", u, d), 1;
+        for (uint32_t i = 0; i < 200000; ++i) {
+            const uint32_t u = (i * 2654435761u) >> 1;
+            if (f.div(u) != u / d) return printf("%u / %u\n", u, d), 1;
+        }
+    }
     // positions near the largest
     Window w{0x7ffffbff - 200, 0x7ffffbff, 4, 16};
     WinIter<256> it;
