@@ -196,7 +196,8 @@ enum {
     Q_DSFREE = 11 + 2 * Q_KST,   // dQ(j) complete: the dS columns may be rewritten
     Q_FIN = 12 + 2 * Q_KST,
     Q_DRAIN = 13 + 2 * Q_KST,    // one commit per issuer (2)
-    Q_NBAR = 14 + 2 * Q_KST
+    Q_QEMPTY = 14 + 2 * Q_KST,   // a unit's S MMAs complete: the Q tile may be reloaded
+    Q_NBAR = 15 + 2 * Q_KST
 };
 
 template <int D>
@@ -239,10 +240,17 @@ struct BwdArgs {
     Window win;          // windowed attention
     SinkPlan sp;
     float *part;         // the sinks' partial gradients (window_sinks.cuh)
+    int n_units;         // windowed attention: units of the launch
+    FastDiv by_tiles, by_heads, by_group;   // of its numbering: tiles, heads (query or kv), Hq / Hkv
 };
 
 // WIN: windowed attention with sinks, the walks of WinIter and WinQIter.  The dQ
-// kernel's packed first tile has boxes of its own, as the forward's.
+// kernel's packed first tile has boxes of its own, as the forward's.  Units are short
+// (about 10 tiles for a window of 1024), so a block takes several in turn: barrier phases
+// run on across them (without WIN every unit loop runs once and the running counts are
+// the unit's own), the next unit's loads and first products go out beside the current
+// one's last steps, and its set-up is paid once (16384 rows, 16 heads, window 1024, a block
+// a unit: dQ 241 us, dK / dV 368; so FIXME).
 struct PackMaps {
     CUtensorMap k_sinks, k_rest, v_sinks, v_rest;
 };
@@ -275,36 +283,57 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Geom g = make_geom(a.S, a.N, a.layout, a.causal);
-    const Unit w = decode_unit_grouped(g, a.B, a.Hq, a.upc, T, blockIdx.x);
-    const int kvh = w.h / (a.Hq / a.Hkv);
-    auto start_walk = [&](Walk &it) {
+    struct Item {
+        Unit w;
+        int kvh, n;      // kv head, key tiles
+    };
+    // the block's it-th unit; false: it has no more
+    auto unit_of = [&](int it, Item &x) -> bool {
+        if constexpr (WIN) {
+            const int64_t item = blockIdx.x + (int64_t)it * gridDim.x;
+            if (item >= a.n_units) return false;
+            const unsigned r = a.by_tiles.div((unsigned)item), t = (unsigned)item - r * (unsigned)a.upc;
+            x.w.b = (int)a.by_heads.div(r);
+            x.w.h = (int)r - x.w.b * a.Hq;
+            x.w.r = 0;
+            x.w.q0 = (int)t * T;
+            x.w.cend = a.S;
+            x.w.qmax = (x.w.q0 + T < a.S ? x.w.q0 + T : a.S) - 1;
+            x.kvh = (int)a.by_group.div((unsigned)x.w.h);
+            x.n = WinIter<T>::count(a.win, x.w.q0 + a.win.off, x.w.qmax + a.win.off);
+        } else {
+            if (it > 0) return false;
+            x.w = decode_unit_grouped(g, a.B, a.Hq, a.upc, T, blockIdx.x);
+            x.kvh = x.w.h / (a.Hq / a.Hkv);
+            x.n = KvIter<T>::count(g, x.w.r, x.w.qmax);
+        }
+        return true;
+    };
+    auto start_walk = [&](Walk &it, const Unit &w) {
         if constexpr (WIN) it.begin(a.win, w.q0 + a.win.off, w.qmax + a.win.off);
         else it.begin(g, w.r, w.qmax);
     };
-    int n;
-    if constexpr (WIN) n = WinIter<T>::count(a.win, w.q0 + a.win.off, w.qmax + a.win.off);
-    else n = KvIter<T>::count(g, w.r, w.qmax);
     // extents of the tensor maps' (rank, row) dimensions, for the debug-bounds build
     const int map_r = striped(g) ? g.N : 1, map_rows = a.S / map_r;
     // a tile of K or V into shared memory
-    auto load_tile = [&](const Walk &it, uint32_t dst, const CUtensorMap *map, const CUtensorMap *sinks,
+    auto load_tile = [&](const Item &x, const Walk &it, uint32_t dst, const CUtensorMap *map, const CUtensorMap *sinks,
                          const CUtensorMap *rest, uint32_t bar, uint64_t policy) {
         if constexpr (WIN) {
             if (it.packed()) {
                 for (int bx = 0; bx < D / 64; ++bx) {
-                    tma_load5(dst + bx * 16384, sinks, bar, bx * 64, kvh, 0, 0, w.b, policy);
-                    tma_load5(dst + bx * 16384 + it.pk * 128, rest, bar, bx * 64, kvh, 0,
-                              dbg_coord(a.err, it.start() + it.pk, a.Sk), w.b, policy);
+                    tma_load5(dst + bx * 16384, sinks, bar, bx * 64, x.kvh, 0, 0, x.w.b, policy);
+                    tma_load5(dst + bx * 16384 + it.pk * 128, rest, bar, bx * 64, x.kvh, 0,
+                              dbg_coord(a.err, it.start() + it.pk, a.Sk), x.w.b, policy);
                 }
                 return;
             }
             const int row = dbg_coord(a.err, it.start(), a.Sk);
             for (int bx = 0; bx < D / 64; ++bx)
-                tma_load5(dst + bx * 16384, map, bar, bx * 64, kvh, 0, row, w.b, policy);
+                tma_load5(dst + bx * 16384, map, bar, bx * 64, x.kvh, 0, row, x.w.b, policy);
         } else {
             const int mr = dbg_coord(a.err, it.mrank(), map_r), mw = dbg_coord(a.err, it.mrow(), map_rows);
             for (int bx = 0; bx < D / 64; ++bx)
-                tma_load5(dst + bx * 16384, map, bar, bx * 64, kvh, mr, mw, w.b, policy);
+                tma_load5(dst + bx * 16384, map, bar, bx * 64, x.kvh, mr, mw, x.w.b, policy);
         }
     };
     const CUtensorMap *pks = nullptr, *pkr = nullptr, *pvs = nullptr, *pvr = nullptr;
@@ -329,6 +358,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         mbar_init(BAR(Q_DSFREE), 1);
         mbar_init(BAR(Q_FIN), 1);
         mbar_init(BAR(Q_DRAIN), 2);
+        mbar_init(BAR(Q_QEMPTY), 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -349,15 +379,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (warp == 0 && lane == 0) {
             // ------------------------------------------------------------ K producer
             const uint64_t pol_kv = policy_evict_last();
-            Walk it;
-            start_walk(it);
             int nk = 0;
             Ring<Q_KST> kr;
-            for (int j = 0; j < n; ++j, it.next(), kr.next()) {
-                if (j >= Q_KST && !wait1(BAR(Q_KEMPTY + kr.st), kr.ph ^ 1, wc)) break;
-                mbar_arrive_expect_tx(BAR(Q_KFULL + kr.st), TB);
-                load_tile(it, sK + kr.st * TB, &tmK, pks, pkr, BAR(Q_KFULL + kr.st), pol_kv);
-                ++nk;
+            Item x;
+            bool ok = true;
+            for (int u = 0; ok && unit_of(u, x); ++u) {
+                Walk it;
+                start_walk(it, x.w);
+                for (int j = 0; j < x.n; ++j, it.next(), kr.next()) {
+                    if (nk >= Q_KST && !wait1(BAR(Q_KEMPTY + kr.st), kr.ph ^ 1, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(BAR(Q_KFULL + kr.st), TB);
+                    load_tile(x, it, sK + kr.st * TB, &tmK, pks, pkr, BAR(Q_KFULL + kr.st), pol_kv);
+                    ++nk;
+                }
             }
             {
                 // wait (bounded) for the copies still in flight before the block
@@ -371,25 +408,34 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         } else if (warp == 3 && lane == 0) {
             // ------------------------------------------------------------ dO and V producer
             const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
-            const int qmr = dbg_coord(a.err, slot_mrank(g, w.q0), map_r);
-            const int qmw = dbg_coord(a.err, slot_mrow(g, w.q0), map_rows);
-            mbar_arrive_expect_tx(BAR(Q_QTM), TB);
-            for (int bx = 0; bx < D / 64; ++bx)
-                tma_load5(sQ + bx * 16384, &tmQ, BAR(Q_QTM), bx * 64, w.h, qmr, qmw, w.b, pol_q);
-            Walk it;
-            start_walk(it);
-            int nv = 0;
-            for (int j = 0; j < n; ++j, it.next()) {
-                const int sv = j & 1;
-                if (j >= 2 && !wait1(BAR(Q_VEMPTY + sv), ((j >> 1) - 1) & 1, wc)) break;
-                mbar_arrive_expect_tx(BAR(Q_VFULL + sv), TB);
-                load_tile(it, sV + sv * TB, &tmV, pvs, pvr, BAR(Q_VFULL + sv), pol_kv);
-                ++nv;
+            int nv = 0, nq = 0;
+            Item x;
+            bool ok = true;
+            for (int u = 0; ok && unit_of(u, x); ++u) {
+                if (u > 0 && !wait1(BAR(Q_QEMPTY), (u - 1) & 1, wc)) break;
+                const int qmr = WIN ? 0 : dbg_coord(a.err, slot_mrank(g, x.w.q0), map_r);
+                const int qmw = WIN ? dbg_coord(a.err, x.w.q0, a.S) : dbg_coord(a.err, slot_mrow(g, x.w.q0), map_rows);
+                mbar_arrive_expect_tx(BAR(Q_QTM), TB);
+                for (int bx = 0; bx < D / 64; ++bx)
+                    tma_load5(sQ + bx * 16384, &tmQ, BAR(Q_QTM), bx * 64, x.w.h, qmr, qmw, x.w.b, pol_q);
+                ++nq;
+                Walk it;
+                start_walk(it, x.w);
+                for (int j = 0; j < x.n; ++j, it.next()) {
+                    const int sv = nv & 1;
+                    if (nv >= 2 && !wait1(BAR(Q_VEMPTY + sv), ((nv >> 1) - 1) & 1, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(BAR(Q_VFULL + sv), TB);
+                    load_tile(x, it, sV + sv * TB, &tmV, pvs, pvr, BAR(Q_VFULL + sv), pol_kv);
+                    ++nv;
+                }
             }
             {
                 volatile int no_abort = 0;
                 WaitCtl dc{a.err, &no_abort, a.drain_ns};
-                wait1(BAR(Q_QTM), 0, dc);
+                if (nq > 0) wait1(BAR(Q_QTM), (nq - 1) & 1, dc);
                 for (int j = nv > 2 ? nv - 2 : 0; j < nv; ++j) wait1(BAR(Q_VFULL + (j & 1)), (j >> 1) & 1, dc);
             }
         } else if (warp == 1 || warp == 2) {
@@ -407,49 +453,66 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (warp == 1) {
                 const uint64_t dQd = sdesc(sQ, 16, 1024);
                 const uint64_t dK0 = sdesc(sK, 16, 1024), dV0 = sdesc(sV, 16, 1024);
-                ok = waitw(BAR(Q_QTM), 0, wc) && waitw(BAR(Q_DOFULL), 0, wc);
                 Ring<Q_KST> kr;
-                for (int j = 0; ok && j < n; ++j, kr.next()) {
-                    const int sv = j & 1;
-                    if ((j > 0 && !waitw(BAR(Q_SFREE), (j - 1) & 1, wc)) ||
-                        !waitw(BAR(Q_KFULL + kr.st), kr.ph, wc))
-                        break;
-                    const uint64_t dK = dK0 + (uint64_t)(kr.st * (TB >> 4));
-                    if (leader) {
-                        tc_fence_after();
-                        ss_seq<0, D, 16384>(tS, dQd, dK, idSP);
-                        mma_commit(BAR(Q_SDONE));
-                        mma_commit(BAR(Q_KEMPTY + kr.st));
+                Item x;
+                int nt = 0;
+                for (int u = 0; ok && unit_of(u, x); ++u) {
+                    if (!waitw(BAR(Q_QTM), u & 1, wc) || !waitw(BAR(Q_DOFULL), u & 1, wc)) break;
+                    for (int j = 0; j < x.n; ++j, ++nt, kr.next()) {
+                        const int sv = nt & 1;
+                        if ((nt > 0 && !waitw(BAR(Q_SFREE), (nt - 1) & 1, wc)) ||
+                            !waitw(BAR(Q_KFULL + kr.st), kr.ph, wc)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint64_t dK = dK0 + (uint64_t)(kr.st * (TB >> 4));
+                        if (leader) {
+                            tc_fence_after();
+                            ss_seq<0, D, 16384>(tS, dQd, dK, idSP);
+                            mma_commit(BAR(Q_SDONE));
+                            mma_commit(BAR(Q_KEMPTY + kr.st));
+                            if (WIN && j + 1 == x.n) mma_commit(BAR(Q_QEMPTY));
+                        }
+                        __syncwarp();
+                        if ((nt > 0 && !waitw(BAR(Q_PFREE), (nt - 1) & 1, wc)) ||
+                            !waitw(BAR(Q_VFULL + sv), (nt >> 1) & 1, wc)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint64_t dV = dV0 + (uint64_t)(sv * (TB >> 4));
+                        if (leader) {
+                            tc_fence_after();
+                            ts_k_seq<0, D>(tP, tDO, dV, idSP);   // A = dO from tensor memory
+                            mma_commit(BAR(Q_PDONE));
+                            mma_commit(BAR(Q_VEMPTY + sv));
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    if ((j > 0 && !waitw(BAR(Q_PFREE), (j - 1) & 1, wc)) ||
-                        !waitw(BAR(Q_VFULL + sv), (j >> 1) & 1, wc))
-                        break;
-                    const uint64_t dV = dV0 + (uint64_t)(sv * (TB >> 4));
-                    if (leader) {
-                        tc_fence_after();
-                        ts_k_seq<0, D>(tP, tDO, dV, idSP);   // A = dO from tensor memory
-                        mma_commit(BAR(Q_PDONE));
-                        mma_commit(BAR(Q_VEMPTY + sv));
-                    }
-                    __syncwarp();
                 }
             } else {
                 const uint64_t dKmn0 = sdesc(sK, 16384, 1024);
                 Ring<Q_KST> kr;
-                for (int j = 0; ok && j < n; ++j, kr.next()) {
-                    if (!waitw(BAR(Q_DS), j & 1, wc) || !waitw(BAR(Q_KFULL + kr.st), kr.ph, wc))
-                        break;
-                    const uint64_t dK = dKmn0 + (uint64_t)(kr.st * (TB >> 4));
-                    const uint32_t acc0 = j > 0 ? 1u : 0u;
-                    if (leader) {
-                        tc_fence_after();
-                        ts_mn_seq<0, T / 16, 0>(tDQ, tDS, dK, idDQ, acc0);
-                        mma_commit(BAR(Q_KEMPTY + kr.st));
-                        mma_commit(BAR(Q_DSFREE));
-                        if (j + 1 == n) mma_commit(BAR(Q_FIN));
+                Item x;
+                int nt = 0;
+                for (int u = 0; ok && unit_of(u, x); ++u) {
+                    for (int j = 0; j < x.n; ++j, ++nt, kr.next()) {
+                        // dS(nt) written: the gradient warps have also read the previous
+                        // unit's dQ, which this unit's first product overwrites
+                        if (!waitw(BAR(Q_DS), nt & 1, wc) || !waitw(BAR(Q_KFULL + kr.st), kr.ph, wc)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint64_t dK = dKmn0 + (uint64_t)(kr.st * (TB >> 4));
+                        const uint32_t acc0 = j > 0 ? 1u : 0u;
+                        if (leader) {
+                            tc_fence_after();
+                            ts_mn_seq<0, T / 16, 0>(tDQ, tDS, dK, idDQ, acc0);
+                            mma_commit(BAR(Q_KEMPTY + kr.st));
+                            mma_commit(BAR(Q_DSFREE));
+                            if (j + 1 == x.n) mma_commit(BAR(Q_FIN));
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
             if (leader) mma_commit(BAR(Q_DRAIN));
@@ -477,30 +540,36 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const uint32_t tP = tmem + lane_off + C::TM_P + 64u * half;
         const uint32_t tDQ = tmem + lane_off + C::TM_DQ;
         const uint32_t tDS = tmem + lane_off + C::TM_DS + 32u * half;
-        const int qpos = w.q0 + row;                  // slot
-        const bool valid = qpos < w.cend;
-        const int qp = dbg_coord(a.err, valid ? slot_pos(g, qpos) : 0, a.S);   // global position
         const float sl2 = a.scale * LOG2E;
-        float lse2 = 0.f, dlt = 0.f;
-        if (valid) {
-            lse2 = lse[((int64_t)w.b * a.Hq + w.h) * a.S + qp] * LOG2E;
-            dlt = delta[((int64_t)w.b * a.Hq + w.h) * a.S + qp];
-        }
-        {
-            // this half's D/2 elements of the row's dO, as D/4 bf16 pairs, into the
-            // A operand of dP = dO V^T (rows past the unit's chunk are zero; their
-            // results are never stored)
+        // This thread's row of a unit: its statistics, and its half of the row's dO, as D/4
+        // bf16 pairs, into the A operand of dP = dO V^T (rows past the unit's chunk are zero;
+        // their results are never stored).  The dO columns are free once dP of the previous
+        // unit's last tile has been read.
+        struct Row {
+            int qpos, qp;      // slot, global position
+            bool valid;
+            float lse2, dlt;
+        };
+        auto load_row = [&](const Unit &w) -> Row {
+            Row r;
+            r.qpos = w.q0 + row;
+            r.valid = r.qpos < w.cend;
+            if constexpr (WIN) r.qp = dbg_coord(a.err, r.valid ? r.qpos : 0, a.S);
+            else r.qp = dbg_coord(a.err, r.valid ? slot_pos(g, r.qpos) : 0, a.S);
+            r.lse2 = r.dlt = 0.f;
             uint32_t dv4[D / 4];
-            if (valid) {
+            if (r.valid) {
+                r.lse2 = lse[((int64_t)w.b * a.Hq + w.h) * a.S + r.qp] * LOG2E;
+                r.dlt = delta[((int64_t)w.b * a.Hq + w.h) * a.S + r.qp];
                 const uint4 *src = reinterpret_cast<const uint4 *>(
-                    dout + (((int64_t)w.b * a.S + qp) * a.Hq + w.h) * D + (D / 2) * half);
+                    dout + (((int64_t)w.b * a.S + r.qp) * a.Hq + w.h) * D + (D / 2) * half);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    const uint4 x = src[i];
-                    dv4[4 * i] = x.x;
-                    dv4[4 * i + 1] = x.y;
-                    dv4[4 * i + 2] = x.z;
-                    dv4[4 * i + 3] = x.w;
+                    const uint4 v = src[i];
+                    dv4[4 * i] = v.x;
+                    dv4[4 * i + 1] = v.y;
+                    dv4[4 * i + 2] = v.z;
+                    dv4[4 * i + 3] = v.w;
                 }
             } else {
 #pragma unroll
@@ -515,108 +584,134 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(Q_DOFULL));
-        }
+            return r;
+        };
         bool ok = true;
-        Walk it;
-        start_walk(it);
-        for (int j = 0; j < n; ++j, it.next()) {
-            const int ks = it.start(), kl = it.len();
-            int lim = kl;                              // visible columns [0, lim) of the tile
-            uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;   // WIN: visible columns, 32 each
-            bool all = false;
-            if constexpr (WIN) {
-                const int p0 = w.q0 + a.win.off, p = qpos + a.win.off;
-                all = it.full(a.win, p0, w.qmax + a.win.off);
-                if (!all) {
-                    const int hi = (p - ks + 1 < kl ? p - ks + 1 : kl) - 64 * half;
-                    const int lo = it.window_col(a.win, p) - 64 * half, sc = it.sink_cols() - 64 * half;
-                    see0 = visible_bits(0, hi, lo, sc);
-                    see1 = visible_bits(32, hi, lo, sc);
+        int nt = 0;
+        Item xn;
+        bool have = unit_of(0, xn);
+        Row rn{};
+        if (have) rn = load_row(xn.w);
+        for (int u = 0; ok && have; ++u) {
+            const Item x = xn;
+            const Unit &w = x.w;
+            const Row rw = rn;
+            const int qpos = rw.qpos, qp = rw.qp, n = x.n;
+            const bool valid = rw.valid;
+            const float lse2 = rw.lse2, dlt = rw.dlt;
+            Walk it;
+            start_walk(it, w);
+            for (int j = 0; j < n; ++j, ++nt, it.next()) {
+                const int ks = it.start(), kl = it.len();
+                int lim = kl;                              // visible columns [0, lim) of the tile
+                uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;   // WIN: visible columns, 32 each
+                bool all = false;
+                if constexpr (WIN) {
+                    const int p0 = w.q0 + a.win.off, p = qpos + a.win.off;
+                    all = it.full(a.win, p0, w.qmax + a.win.off);
+                    if (!all) {
+                        const int hi = (p - ks + 1 < kl ? p - ks + 1 : kl) - 64 * half;
+                        const int lo = it.window_col(a.win, p) - 64 * half, sc = it.sink_cols() - 64 * half;
+                        see0 = visible_bits(0, hi, lo, sc);
+                        see1 = visible_bits(32, hi, lo, sc);
+                    }
+                } else {
+                    if (a.causal) {
+                        const int c = qpos - ks + 1 + it.shift;
+                        lim = c < lim ? c : lim;
+                    }
                 }
-            } else {
-                if (a.causal) {
-                    const int c = qpos - ks + 1 + it.shift;
-                    lim = c < lim ? c : lim;
+                lim -= 64 * half;                          // in this half's local columns
+                if (!waitw(BAR(Q_SDONE), nt & 1, wc)) {
+                    ok = false;
+                    break;
                 }
-            }
-            lim -= 64 * half;                          // in this half's local columns
-            if (!waitw(BAR(Q_SDONE), j & 1, wc)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t sr[64];
-            tmem_ld_x64(tS, sr);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(Q_SFREE));   // S(j+1) may be issued
-            // P = exp2(S sl2 - lse2); the per-element mask only where some row of
-            // the warp does not see the whole half tile
-            const bool full = WIN ? all : __all_sync(0xffffffffu, lim >= 64);
-            float p[64];
+                tc_fence_after();
+                uint32_t sr[64];
+                tmem_ld_x64(tS, sr);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(Q_SFREE));   // S(j+1) may be issued
+                // P = exp2(S sl2 - lse2); the per-element mask only where some row of
+                // the warp does not see the whole half tile
+                const bool full = WIN ? all : __all_sync(0xffffffffu, lim >= 64);
+                float p[64];
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-                ffma2(p[e], p[e + 1], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]), sl2, -lse2);
-                p[e] = ex2(p[e]);
-                p[e + 1] = ex2(p[e + 1]);
-            }
-            if (!full) {
-#pragma unroll
-                for (int e = 0; e < 64; ++e) {
-                    if constexpr (WIN) p[e] = (e < 32 ? see0 : see1) >> (e & 31) & 1u ? p[e] : 0.f;
-                    else p[e] = e < lim ? p[e] : 0.f;
+                for (int e = 0; e < 64; e += 2) {
+                    ffma2(p[e], p[e + 1], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]), sl2, -lse2);
+                    p[e] = ex2(p[e]);
+                    p[e + 1] = ex2(p[e + 1]);
                 }
-            }
-            if (!waitw(BAR(Q_PDONE), j & 1, wc)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t pr[64];
-            tmem_ld_x64(tP, pr);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(Q_PFREE));   // dP(j+1) may be issued
-            // dS = P (dP - Delta)
-            uint32_t pk[32];
+                if (!full) {
+                    if constexpr (WIN) {
+                        // runs of 32 columns that the whole warp sees are left alone
+                        if (!__all_sync(0xffffffffu, see0 == 0xffffffffu)) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                float t0, t1;
-                fadd2v(t0, t1, __uint_as_float(pr[2 * e]), __uint_as_float(pr[2 * e + 1]), -dlt, -dlt);
-                fmul2v(t0, t1, t0, t1, p[2 * e], p[2 * e + 1]);
-                pk[e] = pack_bf16(t0, t1);
-            }
-            // dS(j) may be written once dQ(j-1) has read dS(j-1)
-            if (j > 0 && !waitw(BAR(Q_DSFREE), (j - 1) & 1, wc)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            tmem_st_x32(tDS, pk);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(Q_DS));
-        }
-        if (ok && waitw(BAR(Q_FIN), 0, wc)) {
-            tc_fence_after();
-            // each half writes D/2 columns of dQ = scale * acc
-            constexpr int HD = D / 2;
-            __nv_bfloat16 *orow = dq + (((int64_t)w.b * a.S + qp) * a.Hq + w.h) * D + HD * half;
+                            for (int e = 0; e < 32; ++e) p[e] = see0 & (1u << e) ? p[e] : 0.f;
+                        }
+                        if (!__all_sync(0xffffffffu, see1 == 0xffffffffu)) {
 #pragma unroll
-            for (int c = 0; c < HD / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld_x32(tDQ + HD * half + 32u * c, o);
-                if (valid) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(orow + 32 * c);
+                            for (int e = 0; e < 32; ++e) p[32 + e] = see1 & (1u << e) ? p[32 + e] : 0.f;
+                        }
+                    } else {
 #pragma unroll
-                    for (int v4 = 0; v4 < 4; ++v4) {
-                        uint4 pkt;
-                        pkt.x = pack_bf16(__uint_as_float(o[8 * v4 + 0]) * a.scale, __uint_as_float(o[8 * v4 + 1]) * a.scale);
-                        pkt.y = pack_bf16(__uint_as_float(o[8 * v4 + 2]) * a.scale, __uint_as_float(o[8 * v4 + 3]) * a.scale);
-                        pkt.z = pack_bf16(__uint_as_float(o[8 * v4 + 4]) * a.scale, __uint_as_float(o[8 * v4 + 5]) * a.scale);
-                        pkt.w = pack_bf16(__uint_as_float(o[8 * v4 + 6]) * a.scale, __uint_as_float(o[8 * v4 + 7]) * a.scale);
-                        dst[v4] = pkt;
+                        for (int e = 0; e < 64; ++e) p[e] = e < lim ? p[e] : 0.f;
+                    }
+                }
+                if (!waitw(BAR(Q_PDONE), nt & 1, wc)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t pr[64];
+                tmem_ld_x64(tP, pr);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(Q_PFREE));   // dP(j+1) may be issued
+                // dS = P (dP - Delta)
+                uint32_t pk[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    float t0, t1;
+                    fadd2v(t0, t1, __uint_as_float(pr[2 * e]), __uint_as_float(pr[2 * e + 1]), -dlt, -dlt);
+                    fmul2v(t0, t1, t0, t1, p[2 * e], p[2 * e + 1]);
+                    pk[e] = pack_bf16(t0, t1);
+                }
+                // dS(j) may be written once dQ(j-1) has read dS(j-1)
+                if (nt > 0 && !waitw(BAR(Q_DSFREE), (nt - 1) & 1, wc)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                tmem_st_x32(tDS, pk);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(Q_DS));
+            }
+            // the next unit's rows first: its S and dP run beside this unit's epilogue
+            have = ok && unit_of(u + 1, xn);
+            if (have) rn = load_row(xn.w);
+            if (ok && waitw(BAR(Q_FIN), u & 1, wc)) {
+                tc_fence_after();
+                // each half writes D/2 columns of dQ = scale * acc
+                constexpr int HD = D / 2;
+                __nv_bfloat16 *orow = dq + (((int64_t)w.b * a.S + qp) * a.Hq + w.h) * D + HD * half;
+#pragma unroll
+                for (int c = 0; c < HD / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld_x32(tDQ + HD * half + 32u * c, o);
+                    if (valid) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(orow + 32 * c);
+#pragma unroll
+                        for (int v4 = 0; v4 < 4; ++v4) {
+                            uint4 pkt;
+                            pkt.x = pack_bf16(__uint_as_float(o[8 * v4 + 0]) * a.scale, __uint_as_float(o[8 * v4 + 1]) * a.scale);
+                            pkt.y = pack_bf16(__uint_as_float(o[8 * v4 + 2]) * a.scale, __uint_as_float(o[8 * v4 + 3]) * a.scale);
+                            pkt.z = pack_bf16(__uint_as_float(o[8 * v4 + 4]) * a.scale, __uint_as_float(o[8 * v4 + 5]) * a.scale);
+                            pkt.w = pack_bf16(__uint_as_float(o[8 * v4 + 6]) * a.scale, __uint_as_float(o[8 * v4 + 7]) * a.scale);
+                            dst[v4] = pkt;
+                        }
                     }
                 }
             }
@@ -664,7 +759,9 @@ enum {
     K_DSW = 9 + 2 * K_QST,        // 2 buffers: dS^T written (4 arrivals)
     K_DP = 11 + 2 * K_QST,        // 2 buffers: dP^T complete
     K_DPFREE = 13 + 2 * K_QST,    // 2 buffers: dK(s) complete, the dP^T columns may be rewritten
-    K_NBAR = 15 + 2 * K_QST
+    K_KVEMPTY = 15 + 2 * K_QST,   // a unit's S^T and dP^T MMAs complete (2): K and V may be reloaded
+    K_ACC = 16 + 2 * K_QST,       // a unit's dK read by its warpgroup (4 arrivals)
+    K_NBAR = 17 + 2 * K_QST
 };
 
 template <int D>
@@ -711,44 +808,51 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int grp = a.Hq / a.Hkv;
     const Geom g = make_geom(a.S, a.N, a.layout, a.causal);
     using Walk = std::conditional_t<WIN, WinQIter<T>, QIter<T>>;
-    KvUnit w;
-    int piece = 0;       // WIN: 0 a window unit, else 1 + the piece of a tile of sinks
-    if constexpr (WIN) {
-        const Geom gk = make_geom(a.Sk, 1, CP_LAYOUT_CONTIGUOUS, 1);
-        const int windows = a.tpc * a.B * a.Hkv;
-        if ((int)blockIdx.x < windows) {
-            w = decode_kv_unit<T>(gk, a.B, a.Hkv, a.tpc, blockIdx.x);
+    struct Item {
+        KvUnit w;
+        int piece;       // WIN: 0 a window unit, else 1 + the piece of a tile of sinks
+        int ns;          // half steps
+    };
+    auto start_walk = [&](Walk &it, const Item &x) {
+        if constexpr (!WIN) it.begin(g, x.w.src, x.w.ks, x.w.g * grp, grp);
+        else if (x.piece == 0) it.window(a.win, a.S, x.w.ks, x.w.kl, x.w.g * grp, grp);
+        else it.sinks(a.win, a.S, x.w.ks, x.w.g * grp, grp, x.piece - 1, a.sp.each);
+    };
+    // the block's it-th unit; false: it has no more
+    auto unit_of = [&](int it, Item &x) -> bool {
+        x.piece = 0;
+        if constexpr (WIN) {
+            const int64_t item = blockIdx.x + (int64_t)it * gridDim.x;
+            if (item >= a.n_units) return false;
+            const int windows = a.tpc * a.B * a.Hkv;
+            unsigned t, r;
+            if (item < windows) {
+                r = a.by_tiles.div((unsigned)item);
+                t = (unsigned)item - r * (unsigned)a.tpc;
+            } else {
+                const unsigned y = (unsigned)(item - windows), z = y / (unsigned)a.sp.pieces;
+                x.piece = 1 + (int)(y - z * (unsigned)a.sp.pieces);
+                r = z / (unsigned)a.sp.tiles;
+                t = z - r * (unsigned)a.sp.tiles;
+            }
+            x.w.b = (int)a.by_heads.div(r);
+            x.w.g = (int)r - x.w.b * a.Hkv;
+            x.w.src = 0;
+            x.w.ks = (int)t * T;
+            x.w.kcend = a.Sk;
+            x.w.kl = a.Sk - x.w.ks < T ? a.Sk - x.w.ks : T;
+            Walk wk;
+            start_walk(wk, x);
+            x.ns = 2 * wk.count();
         } else {
-            unsigned x = blockIdx.x - windows;
-            piece = 1 + (int)(x % (unsigned)a.sp.pieces);
-            x /= (unsigned)a.sp.pieces;
-            const unsigned t = x % (unsigned)a.sp.tiles;
-            x /= (unsigned)a.sp.tiles;
-            w.g = (int)(x % (unsigned)a.Hkv);
-            w.b = (int)(x / (unsigned)a.Hkv);
-            w.src = 0;
-            w.ks = (int)t * T;
-            w.kcend = a.Sk;
-            w.kl = a.Sk - w.ks < T ? a.Sk - w.ks : T;
+            if (it > 0) return false;
+            x.w = decode_kv_unit<T>(g, a.B, a.Hkv, a.tpc, blockIdx.x);
+            x.ns = 2 * QIter<T>::count(g, x.w.src, x.w.ks, grp);
         }
-    } else {
-        w = decode_kv_unit<T>(g, a.B, a.Hkv, a.tpc, blockIdx.x);
-    }
-    auto start_walk = [&](Walk &it) {
-        if constexpr (!WIN) it.begin(g, w.src, w.ks, w.g * grp, grp);
-        else if (piece == 0) it.window(a.win, a.S, w.ks, w.kl, w.g * grp, grp);
-        else it.sinks(a.win, a.S, w.ks, w.g * grp, grp, piece - 1, a.sp.each);
+        return true;
     };
     // extents of the tensor maps' (rank, row) dimensions, for the debug-bounds build
     const int map_r = striped(g) ? g.N : 1, map_rows = a.S / map_r;
-    int ns;   // half steps
-    if constexpr (WIN) {
-        Walk it;
-        start_walk(it);
-        ns = 2 * it.count();
-    } else {
-        ns = 2 * QIter<T>::count(g, w.src, w.ks, grp);
-    }
 
     if (threadIdx.x == 0) {
         mbar_init(BAR(K_KVFULL), 1);
@@ -766,6 +870,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         mbar_init(BAR(K_FIN), 1);
         mbar_init(BAR(K_DRAIN), 3);
+        mbar_init(BAR(K_KVEMPTY), 2);
+        mbar_init(BAR(K_ACC), 4);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -786,59 +892,69 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (warp == 0) {
             // ------------------------------------------------------------ producer (whole warp)
             const uint64_t pol_kv = policy_evict_first(), pol_q = policy_evict_last();
-            if (lane == 0) {
-                const int kmr = WIN ? 0 : dbg_coord(a.err, slot_mrank(g, w.ks), map_r);
-                const int kmw = WIN ? dbg_coord(a.err, w.ks, a.Sk) : dbg_coord(a.err, slot_mrow(g, w.ks), map_rows);
-                mbar_arrive_expect_tx(BAR(K_KVFULL), 2 * TB);
-                for (int bx = 0; bx < D / 64; ++bx) {
-                    tma_load5(sK + bx * 16384, &tmK, BAR(K_KVFULL), bx * 64, w.g, kmr, kmw, w.b, pol_kv);
-                    tma_load5(sV + bx * 16384, &tmV, BAR(K_KVFULL), bx * 64, w.g, kmr, kmw, w.b, pol_kv);
-                }
-            }
-            Walk it;
-            start_walk(it);
-            int issued = 0;
+            int issued = 0, nkv = 0;
             Ring<K_QST> qr;
-            for (int s = 0; s < ns; ++s, qr.next()) {
-                if (s >= K_QST && !waitw(BAR(K_QEMPTY + qr.st), qr.ph ^ 1, wc)) break;
-                const int hs = s & 1;
-                const int qa = it.start() + 64 * hs, ql = it.len() - 64 * hs, h = it.head();
-                // map coordinates; the second half-tile may start past the end of
-                // the map (a short last tile): the copy then reads the fill value
-                int qr_rank = 0, qr_row;
-                if constexpr (WIN) {
-                    qr_row = dbg_coord(a.err, it.start(), a.S) + 64 * hs;
-                } else {
-                    qr_rank = dbg_coord(a.err, it.mrank(), map_r);
-                    qr_row = dbg_coord(a.err, it.mrow(), map_rows) + 64 * hs;
-                }
-                // per-row statistics of the half tile, negated: -lse (log2 units), -Delta
-                float *ls = stat + qr.st * 128, *dl = ls + 64;
-                for (int e = lane; e < 64; e += 32) {
-                    float l2 = 0.f, dd = 0.f;
-                    if (e < ql) {
-                        const int64_t off =
-                            ((int64_t)w.b * a.Hq + h) * a.S + dbg_coord(a.err, slot_pos(g, qa + e), a.S);
-                        l2 = -lse[off] * LOG2E;
-                        dd = -delta[off];
-                    }
-                    ls[e] = l2;
-                    dl[e] = dd;
-                }
-                __syncwarp();
+            Item x;
+            bool ok = true;
+            for (int u = 0; ok && unit_of(u, x); ++u) {
+                if (u > 0 && !waitw(BAR(K_KVEMPTY), (u - 1) & 1, wc)) break;
                 if (lane == 0) {
-                    const uint32_t sq = sQ + qr.st * C::STAGE;
-                    mbar_arrive_expect_tx(BAR(K_QFULL + qr.st), 2 * HB);
+                    const int kmr = WIN ? 0 : dbg_coord(a.err, slot_mrank(g, x.w.ks), map_r);
+                    const int kmw =
+                        WIN ? dbg_coord(a.err, x.w.ks, a.Sk) : dbg_coord(a.err, slot_mrow(g, x.w.ks), map_rows);
+                    mbar_arrive_expect_tx(BAR(K_KVFULL), 2 * TB);
                     for (int bx = 0; bx < D / 64; ++bx) {
-                        tma_load5(sq + bx * 8192, &tmQh, BAR(K_QFULL + qr.st), bx * 64, h, qr_rank,
-                                  qr_row, w.b, pol_q);
-                        tma_load5(sq + HB + bx * 8192, &tmDOh, BAR(K_QFULL + qr.st), bx * 64, h, qr_rank,
-                                  qr_row, w.b, pol_q);
+                        tma_load5(sK + bx * 16384, &tmK, BAR(K_KVFULL), bx * 64, x.w.g, kmr, kmw, x.w.b, pol_kv);
+                        tma_load5(sV + bx * 16384, &tmV, BAR(K_KVFULL), bx * 64, x.w.g, kmr, kmw, x.w.b, pol_kv);
                     }
                 }
-                __syncwarp();
-                issued = s + 1;
-                if (hs) it.next();
+                ++nkv;
+                Walk it;
+                start_walk(it, x);
+                for (int s = 0; s < x.ns; ++s, qr.next()) {
+                    if (issued >= K_QST && !waitw(BAR(K_QEMPTY + qr.st), qr.ph ^ 1, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    const int hs = s & 1;
+                    const int qa = it.start() + 64 * hs, ql = it.len() - 64 * hs, h = it.head();
+                    // map coordinates; the second half-tile may start past the end of
+                    // the map (a short last tile): the copy then reads the fill value
+                    int qr_rank = 0, qr_row;
+                    if constexpr (WIN) {
+                        qr_row = dbg_coord(a.err, it.start(), a.S) + 64 * hs;
+                    } else {
+                        qr_rank = dbg_coord(a.err, it.mrank(), map_r);
+                        qr_row = dbg_coord(a.err, it.mrow(), map_rows) + 64 * hs;
+                    }
+                    // per-row statistics of the half tile, negated: -lse (log2 units), -Delta
+                    float *ls = stat + qr.st * 128, *dl = ls + 64;
+                    for (int e = lane; e < 64; e += 32) {
+                        float l2 = 0.f, dd = 0.f;
+                        if (e < ql) {
+                            const int64_t off =
+                                ((int64_t)x.w.b * a.Hq + h) * a.S + dbg_coord(a.err, slot_pos(g, qa + e), a.S);
+                            l2 = -lse[off] * LOG2E;
+                            dd = -delta[off];
+                        }
+                        ls[e] = l2;
+                        dl[e] = dd;
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        const uint32_t sq = sQ + qr.st * C::STAGE;
+                        mbar_arrive_expect_tx(BAR(K_QFULL + qr.st), 2 * HB);
+                        for (int bx = 0; bx < D / 64; ++bx) {
+                            tma_load5(sq + bx * 8192, &tmQh, BAR(K_QFULL + qr.st), bx * 64, h, qr_rank,
+                                      qr_row, x.w.b, pol_q);
+                            tma_load5(sq + HB + bx * 8192, &tmDOh, BAR(K_QFULL + qr.st), bx * 64, h, qr_rank,
+                                      qr_row, x.w.b, pol_q);
+                        }
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (hs) it.next();
+                }
             }
             if (lane == 0) {
                 // wait (bounded) for the copies still in flight before the block
@@ -846,7 +962,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 // was issued (after a normal run these phases are complete)
                 volatile int no_abort = 0;
                 WaitCtl dc{a.err, &no_abort, a.drain_ns};
-                wait1(BAR(K_KVFULL), 0, dc);
+                if (nkv > 0) wait1(BAR(K_KVFULL), (nkv - 1) & 1, dc);
                 for (int s = issued > K_QST ? issued - K_QST : 0; s < issued; ++s)
                     wait1(BAR(K_QFULL + s % K_QST), (s / K_QST) & 1, dc);
             }
@@ -860,7 +976,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // warp runs converged (warp-collective waits), so its operands stay
             // warp-uniform, and one elected lane issues the MMAs and commits.
             const bool leader = elect_one();
-            bool ok = waitw(BAR(K_KVFULL), 0, wc);
+            bool ok = true;
+            Item x;
+            int gs = 0;      // half steps so far (even at the end of a unit)
             if (warp >= 2) {
                 constexpr uint32_t idSP = idesc_bf16(128, 64, false);   // N = 64 queries
                 // warp 2: S^T = K Q_s^T; warp 3: dP^T = V dO_s^T
@@ -870,50 +988,76 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const int b_free = dp ? K_DPFREE : K_SFREE, b_done = dp ? K_DP : K_S;
                 const uint32_t col = dp ? 64u : 0u;
                 Ring<K_QST> rs;
-                for (int s = 0; ok && s < ns; ++s, rs.next()) {
-                    if ((s >= 2 && !waitw(BAR(b_free + (s & 1)), ((s >> 1) - 1) & 1, wc)) ||
-                        !waitw(BAR(K_QFULL + rs.st), rs.ph, wc))
-                        break;
-                    const uint32_t tb = tmem + 128u * (uint32_t)(s & 1) + col;
-                    const uint64_t so = (uint64_t)(rs.st * (C::STAGE >> 4));
-                    if (leader) {
-                        tc_fence_after();
-                        ss_seq<0, D, 8192>(tb, dA, dQ0 + so, idSP);
-                        mma_commit(BAR(b_done + (s & 1)));
+                for (int u = 0; ok && unit_of(u, x); ++u) {
+                    if (!waitw(BAR(K_KVFULL), u & 1, wc)) break;
+                    for (int s = 0; s < x.ns; ++s, ++gs, rs.next()) {
+                        if ((gs >= 2 && !waitw(BAR(b_free + (gs & 1)), ((gs >> 1) - 1) & 1, wc)) ||
+                            !waitw(BAR(K_QFULL + rs.st), rs.ph, wc)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t tb = tmem + 128u * (uint32_t)(gs & 1) + col;
+                        const uint64_t so = (uint64_t)(rs.st * (C::STAGE >> 4));
+                        if (leader) {
+                            tc_fence_after();
+                            ss_seq<0, D, 8192>(tb, dA, dQ0 + so, idSP);
+                            mma_commit(BAR(b_done + (gs & 1)));
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if constexpr (WIN) {
+                        if (leader) mma_commit(BAR(K_KVEMPTY));
+                        __syncwarp();
+                    }
                 }
             } else {
                 constexpr uint32_t idKV = idesc_bf16(128, D, true);     // dV, dK: B MN-major
                 const uint64_t dQmn0 = sdesc(sQ, 8192, 1024);          // Q_s, dO_s MN-major
                 const uint32_t tDV = tmem + C::TM_DV, tDK = tmem + C::TM_DK;
                 Ring<K_QST> rs;
-                for (int s = 0; ok && s < ns; ++s, rs.next()) {
-                    if (!waitw(BAR(K_PW + (s & 1)), (s >> 1) & 1, wc)) break;
-                    const uint32_t tb = tmem + 128u * (uint32_t)(s & 1);
-                    const uint64_t so = (uint64_t)(rs.st * (C::STAGE >> 4));
-                    const uint32_t acc0 = s > 0 ? 1u : 0u;
-                    // dV += P^T dO_s as soon as P^T is written, while the gradient
-                    // warps compute dS^T; then dK += dS^T Q_s (K = 64 queries: 4 MMAs each)
-                    if (leader) {
-                        tc_fence_after();
-                        ts_mn_seq<0, 4, 0>(tDV, tb, dQmn0 + so + (uint64_t)(HB >> 4), idKV, acc0);
-                        mma_commit(BAR(K_SFREE + (s & 1)));
+                int nf = 0;  // units with any step so far (the others have no products)
+                for (int u = 0; ok && unit_of(u, x); ++u) {
+                    for (int s = 0; s < x.ns; ++s, ++gs, rs.next()) {
+                        // P^T(gs) written: warpgroup 0, whose step s = 0 is, has also read the
+                        // previous unit's dV, which this unit's first product overwrites
+                        if (!waitw(BAR(K_PW + (gs & 1)), (gs >> 1) & 1, wc)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t tb = tmem + 128u * (uint32_t)(gs & 1);
+                        const uint64_t so = (uint64_t)(rs.st * (C::STAGE >> 4));
+                        const uint32_t acc0 = s > 0 ? 1u : 0u;
+                        // dV += P^T dO_s as soon as P^T is written, while the gradient
+                        // warps compute dS^T; then dK += dS^T Q_s (K = 64 queries: 4 MMAs each)
+                        if (leader) {
+                            tc_fence_after();
+                            ts_mn_seq<0, 4, 0>(tDV, tb, dQmn0 + so + (uint64_t)(HB >> 4), idKV, acc0);
+                            mma_commit(BAR(K_SFREE + (gs & 1)));
+                        }
+                        __syncwarp();
+                        // ... and before the first dK warpgroup 1 has read the previous unit's
+                        if (!waitw(BAR(K_DSW + (gs & 1)), (gs >> 1) & 1, wc) ||
+                            (WIN && s == 0 && nf > 0 && !waitw(BAR(K_ACC), (nf - 1) & 1, wc))) {
+                            ok = false;
+                            break;
+                        }
+                        if (leader) {
+                            tc_fence_after();
+                            ts_mn_seq<0, 4, 0>(tDK, tb + 64u, dQmn0 + so, idKV, acc0);
+                            // S^T(s) and dP^T(s) completed before the gradient warps read
+                            // them, so the stage is free once dV/dK(s) complete
+                            mma_commit(BAR(K_QEMPTY + rs.st));
+                            mma_commit(BAR(K_DPFREE + (gs & 1)));
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    if (!waitw(BAR(K_DSW + (s & 1)), (s >> 1) & 1, wc)) break;
-                    if (leader) {
-                        tc_fence_after();
-                        ts_mn_seq<0, 4, 0>(tDK, tb + 64u, dQmn0 + so, idKV, acc0);
-                        // S^T(s) and dP^T(s) completed before the gradient warps read
-                        // them, so the stage is free once dV/dK(s) complete
-                        mma_commit(BAR(K_QEMPTY + rs.st));
-                        mma_commit(BAR(K_DPFREE + (s & 1)));
+                    if (!ok) break;
+                    if (!WIN || x.ns > 0) {
+                        if (leader) mma_commit(BAR(K_FIN));
+                        __syncwarp();
+                        ++nf;
                     }
-                    __syncwarp();
                 }
-                if (leader) mma_commit(BAR(K_FIN));
-                __syncwarp();
             }
             if (leader) mma_commit(BAR(K_DRAIN));
             __syncwarp();
@@ -937,145 +1081,156 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int row = quarter * 32 + lane;        // key row of the tile
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const uint32_t tb = tmem + lane_off + 128u * (uint32_t)half;
-        const int kpos = w.ks + row;
         const float sl2 = a.scale * LOG2E;
         bool ok = true;
-        Walk it;
-        start_walk(it);
+        int gi = 0, nf = 0;  // this warpgroup's half steps so far, units with any
         Ring<K_QST> qr;
         if (half) qr.next();
-        for (int i = 0; 2 * i + half < ns; ++i, it.next(), qr.next(), qr.next()) {
-            const int qa = it.start() + 64 * half, ql = it.len() - 64 * half;
-            int sh = 0;
-            if constexpr (!WIN) sh = it.shift;
-            if (!waitw(BAR(K_S + half), i & 1, wc) || !waitw(BAR(K_QFULL + qr.st), qr.ph, wc)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t sr[64], pr[64];
-            tmem_ld_x64(tb, sr);
-            // visible query columns c: c < ql and (not causal or qa + c >= kpos)
-            int lo = a.causal ? kpos - sh - qa : 0, hi = ql;
-            if constexpr (WIN) {
-                // the query of column c stands at position qa + c + off; a window unit's
-                // keys are seen up to window - 1 behind them, a piece's sinks from there on
-                lo = kpos - a.win.off - qa;
-                if (piece == 0) hi = a.win.window - 1 < ql - 1 - lo ? lo + a.win.window : ql;
-                else lo = kpos < a.win.sinks && a.win.window <= 64 - lo ? lo + a.win.window : 64;
-            }
-            const float4 *ls4 = reinterpret_cast<const float4 *>(stat + qr.st * 128);   // -lse2
-            const float4 *dl4 = ls4 + 16;                                               // -Delta
-            // most tiles are visible to the whole warp: no per-element mask there
-            const bool full = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
-            // P^T (fp32, kept in place of S^T for dS^T) and its bf16 pairs, stored
-            // at once so that their registers are free for dS^T
-            {
-                uint32_t pp[32];
-#pragma unroll
-                for (int e4 = 0; e4 < 16; ++e4) {
-                    const float4 l = ls4[e4];
-                    const int c = 4 * e4;
-                    float p0, p1, p2, p3;
-                    ffma2v(p0, p1, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]), sl2, sl2, l.x, l.y);
-                    ffma2v(p2, p3, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]), sl2, sl2, l.z, l.w);
-                    p0 = ex2(p0);
-                    p1 = ex2(p1);
-                    p2 = ex2(p2);
-                    p3 = ex2(p3);
-                    if (!full) {
-                        p0 = (c >= lo && c < hi) ? p0 : 0.f;
-                        p1 = (c + 1 >= lo && c + 1 < hi) ? p1 : 0.f;
-                        p2 = (c + 2 >= lo && c + 2 < hi) ? p2 : 0.f;
-                        p3 = (c + 3 >= lo && c + 3 < hi) ? p3 : 0.f;
-                    }
-                    sr[c] = __float_as_uint(p0);
-                    sr[c + 1] = __float_as_uint(p1);
-                    sr[c + 2] = __float_as_uint(p2);
-                    sr[c + 3] = __float_as_uint(p3);
-                    pp[2 * e4] = pack_bf16(p0, p1);
-                    pp[2 * e4 + 1] = pack_bf16(p2, p3);
+        Item x;
+        for (int u = 0; ok && unit_of(u, x); ++u) {
+            const KvUnit &w = x.w;
+            const int ns = x.ns, piece = x.piece, kpos = w.ks + row;
+            Walk it;
+            start_walk(it, x);
+            for (int i = 0; 2 * i + half < ns; ++i, ++gi, it.next(), qr.next(), qr.next()) {
+                const int qa = it.start() + 64 * half, ql = it.len() - 64 * half;
+                int sh = 0;
+                if constexpr (!WIN) sh = it.shift;
+                if (!waitw(BAR(K_S + half), gi & 1, wc) || !waitw(BAR(K_QFULL + qr.st), qr.ph, wc)) {
+                    ok = false;
+                    break;
                 }
-                tmem_st_x32(tb, pp);
+                tc_fence_after();
+                uint32_t sr[64], pr[64];
+                tmem_ld_x64(tb, sr);
+                // visible query columns c: c < ql and (not causal or qa + c >= kpos)
+                int lo = a.causal ? kpos - sh - qa : 0, hi = ql;
+                if constexpr (WIN) {
+                    // the query of column c stands at position qa + c + off; a window unit's
+                    // keys are seen up to window - 1 behind them, a piece's sinks from there on
+                    lo = kpos - a.win.off - qa;
+                    if (piece == 0) hi = a.win.window - 1 < ql - 1 - lo ? lo + a.win.window : ql;
+                    else lo = kpos < a.win.sinks && a.win.window <= 64 - lo ? lo + a.win.window : 64;
+                }
+                const float4 *ls4 = reinterpret_cast<const float4 *>(stat + qr.st * 128);   // -lse2
+                const float4 *dl4 = ls4 + 16;                                               // -Delta
+                // most tiles are visible to the whole warp: no per-element mask there
+                const bool full = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
+                // P^T (fp32, kept in place of S^T for dS^T) and its bf16 pairs, stored
+                // at once so that their registers are free for dS^T
+                {
+                    uint32_t pp[32];
+#pragma unroll
+                    for (int e4 = 0; e4 < 16; ++e4) {
+                        const float4 l = ls4[e4];
+                        const int c = 4 * e4;
+                        float p0, p1, p2, p3;
+                        ffma2v(p0, p1, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]), sl2, sl2, l.x, l.y);
+                        ffma2v(p2, p3, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]), sl2, sl2, l.z, l.w);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        p2 = ex2(p2);
+                        p3 = ex2(p3);
+                        if (!full) {
+                            p0 = (c >= lo && c < hi) ? p0 : 0.f;
+                            p1 = (c + 1 >= lo && c + 1 < hi) ? p1 : 0.f;
+                            p2 = (c + 2 >= lo && c + 2 < hi) ? p2 : 0.f;
+                            p3 = (c + 3 >= lo && c + 3 < hi) ? p3 : 0.f;
+                        }
+                        sr[c] = __float_as_uint(p0);
+                        sr[c + 1] = __float_as_uint(p1);
+                        sr[c + 2] = __float_as_uint(p2);
+                        sr[c + 3] = __float_as_uint(p3);
+                        pp[2 * e4] = pack_bf16(p0, p1);
+                        pp[2 * e4 + 1] = pack_bf16(p2, p3);
+                    }
+                    tmem_st_x32(tb, pp);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(K_PW + half));   // dV(s) may start
+                }
+                if (!waitw(BAR(K_DP + half), gi & 1, wc)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                tmem_ld_x64(tb + 64u, pr);
+                {
+                    // dS^T = P^T (dP^T - Delta)
+                    uint32_t dd[32];
+#pragma unroll
+                    for (int e4 = 0; e4 < 16; ++e4) {
+                        const float4 d = dl4[e4];
+                        const int c = 4 * e4;
+                        float t0, t1, t2, t3;
+                        fadd2v(t0, t1, __uint_as_float(pr[c]), __uint_as_float(pr[c + 1]), d.x, d.y);
+                        fadd2v(t2, t3, __uint_as_float(pr[c + 2]), __uint_as_float(pr[c + 3]), d.z, d.w);
+                        fmul2v(t0, t1, t0, t1, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+                        fmul2v(t2, t3, t2, t3, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+                        dd[2 * e4] = pack_bf16(t0, t1);
+                        dd[2 * e4 + 1] = pack_bf16(t2, t3);
+                    }
+                    tmem_st_x32(tb + 64u, dd);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(K_PW + half));   // dV(s) may start
+                if (lane == 0) mbar_arrive(BAR(K_DSW + half));
             }
-            if (!waitw(BAR(K_DP + half), i & 1, wc)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            tmem_ld_x64(tb + 64u, pr);
-            {
-                // dS^T = P^T (dP^T - Delta)
-                uint32_t dd[32];
-#pragma unroll
-                for (int e4 = 0; e4 < 16; ++e4) {
-                    const float4 d = dl4[e4];
-                    const int c = 4 * e4;
-                    float t0, t1, t2, t3;
-                    fadd2v(t0, t1, __uint_as_float(pr[c]), __uint_as_float(pr[c + 1]), d.x, d.y);
-                    fadd2v(t2, t3, __uint_as_float(pr[c + 2]), __uint_as_float(pr[c + 3]), d.z, d.w);
-                    fmul2v(t0, t1, t0, t1, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-                    fmul2v(t2, t3, t2, t3, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
-                    dd[2 * e4] = pack_bf16(t0, t1);
-                    dd[2 * e4 + 1] = pack_bf16(t2, t3);
-                }
-                tmem_st_x32(tb + 64u, dd);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(K_DSW + half));
-        }
-        if (ok && waitw(BAR(K_FIN), 0, wc)) {
-            tc_fence_after();
-            // half 0 writes dV, half 1 writes dK (times scale)
-            bool valid = row < w.kl;
-            const float f = half ? a.scale : 1.f;
-            const uint32_t tAcc = tmem + lane_off + (half ? C::TM_DK : C::TM_DV);
-            const int krow = WIN ? dbg_coord(a.err, valid ? kpos : 0, a.Sk)
-                                 : dbg_coord(a.err, valid ? slot_pos(g, kpos) : 0, a.S);
-            __nv_bfloat16 *orow = (half ? dk : dv) + (((int64_t)w.b * (WIN ? a.Sk : a.S) + krow) * a.Hkv + w.g) * D;
-            float *prow = nullptr;   // WIN: a sink's partial gradient
-            if constexpr (WIN) {
-                const bool sink = valid && a.sp.pieces > 0 && kpos < a.win.sinks;
-                if (sink)
-                    prow = a.part + (((int64_t)w.b * a.Hkv + w.g) * window_part_rows(a.win, a.sp) +
-                                     ((int64_t)piece * 2 + (half ? 0 : 1)) * a.win.sinks + kpos) * D;
-                valid = valid && !sink && piece == 0;
-            }
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld_x32(tAcc + 32u * c, o);
+            if (ok && ((WIN && ns == 0) || waitw(BAR(K_FIN), nf & 1, wc))) {
+                tc_fence_after();
+                // half 0 writes dV, half 1 writes dK (times scale)
+                bool valid = row < w.kl;
+                const float f = half ? a.scale : 1.f;
+                const uint32_t tAcc = tmem + lane_off + (half ? C::TM_DK : C::TM_DV);
+                const int krow = WIN ? dbg_coord(a.err, valid ? kpos : 0, a.Sk)
+                                     : dbg_coord(a.err, valid ? slot_pos(g, kpos) : 0, a.S);
+                __nv_bfloat16 *orow = (half ? dk : dv) + (((int64_t)w.b * (WIN ? a.Sk : a.S) + krow) * a.Hkv + w.g) * D;
+                float *prow = nullptr;   // WIN: a sink's partial gradient
                 if constexpr (WIN) {
-                    if (ns == 0) {           // keys that no row reaches: the accumulators hold nothing
+                    const bool sink = valid && a.sp.pieces > 0 && kpos < a.win.sinks;
+                    if (sink)
+                        prow = a.part + (((int64_t)w.b * a.Hkv + w.g) * window_part_rows(a.win, a.sp) +
+                                         ((int64_t)piece * 2 + (half ? 0 : 1)) * a.win.sinks + kpos) * D;
+                    valid = valid && !sink && piece == 0;
+                }
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld_x32(tAcc + 32u * c, o);
+                    if constexpr (WIN) {
+                        if (ns == 0) {           // keys that no row reaches: the accumulators hold nothing
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = 0u;
+                        }
+                        if (prow) {
+                            float4 *dst = reinterpret_cast<float4 *>(prow + 32 * c);
+#pragma unroll
+                            for (int v4 = 0; v4 < 8; ++v4)
+                                dst[v4] = make_float4(__uint_as_float(o[4 * v4]) * f, __uint_as_float(o[4 * v4 + 1]) * f,
+                                                      __uint_as_float(o[4 * v4 + 2]) * f, __uint_as_float(o[4 * v4 + 3]) * f);
+                        }
                     }
-                    if (prow) {
-                        float4 *dst = reinterpret_cast<float4 *>(prow + 32 * c);
+                    if (valid) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(orow + 32 * c);
 #pragma unroll
-                        for (int v4 = 0; v4 < 8; ++v4)
-                            dst[v4] = make_float4(__uint_as_float(o[4 * v4]) * f, __uint_as_float(o[4 * v4 + 1]) * f,
-                                                  __uint_as_float(o[4 * v4 + 2]) * f, __uint_as_float(o[4 * v4 + 3]) * f);
+                        for (int v4 = 0; v4 < 4; ++v4) {
+                            uint4 pkt;
+                            pkt.x = pack_bf16(__uint_as_float(o[8 * v4 + 0]) * f, __uint_as_float(o[8 * v4 + 1]) * f);
+                            pkt.y = pack_bf16(__uint_as_float(o[8 * v4 + 2]) * f, __uint_as_float(o[8 * v4 + 3]) * f);
+                            pkt.z = pack_bf16(__uint_as_float(o[8 * v4 + 4]) * f, __uint_as_float(o[8 * v4 + 5]) * f);
+                            pkt.w = pack_bf16(__uint_as_float(o[8 * v4 + 6]) * f, __uint_as_float(o[8 * v4 + 7]) * f);
+                            dst[v4] = pkt;
+                        }
                     }
                 }
-                if (valid) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(orow + 32 * c);
-#pragma unroll
-                    for (int v4 = 0; v4 < 4; ++v4) {
-                        uint4 pkt;
-                        pkt.x = pack_bf16(__uint_as_float(o[8 * v4 + 0]) * f, __uint_as_float(o[8 * v4 + 1]) * f);
-                        pkt.y = pack_bf16(__uint_as_float(o[8 * v4 + 2]) * f, __uint_as_float(o[8 * v4 + 3]) * f);
-                        pkt.z = pack_bf16(__uint_as_float(o[8 * v4 + 4]) * f, __uint_as_float(o[8 * v4 + 5]) * f);
-                        pkt.w = pack_bf16(__uint_as_float(o[8 * v4 + 6]) * f, __uint_as_float(o[8 * v4 + 7]) * f);
-                        dst[v4] = pkt;
-                    }
-                }
+            }
+            if (WIN && ns > 0) {   // the accumulators may be overwritten
+                tc_fence_before();
+                __syncwarp();
+                if (half && lane == 0) mbar_arrive(BAR(K_ACC));
+                ++nf;
             }
         }
         __syncwarp();
@@ -1132,15 +1287,25 @@ int launch_window_d(const BwdPtrs &p, BwdArgs a, cudaStream_t st)
     if (qunits > 0x7fffffffLL || kunits > 0x7fffffffLL) return CP_EUNSUPPORTED;
     const int rc = launch_delta(p, a, D, st);
     if (rc) return rc;
+    const int64_t sms = sm_count();
+    const int cap = fwd_grid_limit();   // test hook: blocks with many units
+    const int64_t most = cap > 0 && cap < sms ? cap : sms;
     float *delta = static_cast<float *>(p.workspace);
     a.part = delta + bwd_workspace_bytes(a.B, a.Hq, a.S) / 4;
     __nv_bfloat16 *dk = static_cast<__nv_bfloat16 *>(p.dk), *dv = static_cast<__nv_bfloat16 *>(p.dv);
-    bwd_dq_kernel<D, true><<<(unsigned)qunits, NTHREADS, DqCfg<D>::SMEM, st>>>(
+    a.n_units = (int)qunits;
+    a.by_tiles = fast_div((uint32_t)a.upc);
+    a.by_heads = fast_div((uint32_t)a.Hq);
+    a.by_group = fast_div((uint32_t)(a.Hq / a.Hkv));
+    bwd_dq_kernel<D, true><<<(unsigned)(qunits < most ? qunits : most), NTHREADS, DqCfg<D>::SMEM, st>>>(
         mq, mk, mv, mdo64, a, p.lse, delta, static_cast<__nv_bfloat16 *>(p.dq),
         static_cast<const __nv_bfloat16 *>(p.dout), pm);
     if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
-    bwd_dkdv_kernel<D, true><<<(unsigned)kunits, NTHREADS, DkvCfg<D>::SMEM, st>>>(mq64, mk, mv, mdo64, a, p.lse, delta,
-                                                                                  dk, dv);
+    a.n_units = (int)kunits;
+    a.by_tiles = fast_div((uint32_t)a.tpc);
+    a.by_heads = fast_div((uint32_t)a.Hkv);
+    bwd_dkdv_kernel<D, true><<<(unsigned)(kunits < most ? kunits : most), NTHREADS, DkvCfg<D>::SMEM, st>>>(
+        mq64, mk, mv, mdo64, a, p.lse, delta, dk, dv);
     if (cudaGetLastError() != cudaSuccess) return CP_ECUDA;
     return launch_window_sinks<D>(a.part, a.win, a.sp, a.B, a.Hkv, a.Sk, dk, dv, st);
 }
@@ -1224,6 +1389,8 @@ BwdArgs bwd_args(const FwdArgs &f)
     a.win = f.win;
     a.sp = SinkPlan{0, 0, 1};
     a.part = nullptr;
+    a.n_units = 0;
+    a.by_tiles = a.by_heads = a.by_group = fast_div(1);
     return a;
 }
 

@@ -257,3 +257,20 @@ def test_misaligned_to_32_bytes(cuda_dev, dtype, D):
     out = torch.empty(q.numel() + e, dtype=dtype, device=cuda_dev)[e:].view(q.shape)
     api.window_attn_fwd(q, k, v, 50, 3, out=out)
     assert torch.equal(out, api.window_attn_fwd(q, k, v, 50, 3)[0])
+
+
+@pytest.mark.parametrize("shape", [(1, 1000, 1000, 6, 3, 128, 200, 4), (2, 200, 2000, 4, 2, 64, 130, 300),
+                                   (1, 300, 900, 2, 1, 128, 1, 70)])
+def test_backward_with_many_units_of_one_block(cuda_dev, shape):
+    """Few blocks with many units each, units without any row among them."""
+    q, k, v, do = make(shape, BF16, cuda_dev)
+    W, K = shape[-2:]
+    out, lse = api.window_attn_fwd(q, k, v, W, K)
+    plain = api.window_attn_bwd(q, k, v, out, lse, do, W, K)
+    api.cp_debug_set_grid_limit(2)
+    try:
+        few = api.window_attn_bwd(q, k, v, out, lse, do, W, K)
+        assert api.cp_get_error() == 0
+    finally:
+        api.cp_debug_set_grid_limit(0)
+    assert all(torch.equal(a, b) for a, b in zip(plain, few))
