@@ -385,7 +385,8 @@ struct WinQIter {
 };
 
 // How the sinks' walk is cut: tiles of KEYS sink keys, pieces per (batch, kv head, tile)
-// and tiles of QUERIES rows of a piece -- as many as a window unit has, but not below 16.
+// and tiles of QUERIES rows of a piece -- as many as a window unit has, so that none is the
+// last to end, but not below 4.
 struct SinkPlan {
     int tiles, pieces, each;
 };
@@ -399,7 +400,7 @@ CP_HD SinkPlan sink_plan(const Window &w, int Sq, int Sk, int grp)
     s.tiles = (sinks + KEYS - 1) / KEYS;
     const int64_t all = (rows + QUERIES - 1) / QUERIES * grp;
     int64_t each = ((int64_t)w.window / QUERIES + 2) * grp;
-    each = each < 16 ? 16 : each;
+    each = each < 4 ? 4 : each;
     s.each = (int)(each < all ? each : all);
     s.pieces = (int)((all + s.each - 1) / s.each);
     return s;

@@ -5,10 +5,11 @@
 // slot's mass (NaN counts as the largest).  Two kernels:
 //   select  a cluster of blocks per (sequence, kv head), each with a run of its slots in
 //           shared memory as 32-bit keys in the order of the floats: mass is read once.
-//           Four rounds of 8 bits, each a histogram summed over the cluster through
-//           distributed shared memory, find the last key that is kept and how many of its
-//           equals; prefix sums over runs then place the slots.  Bounded by latency (about
-//           nine cluster barriers).
+//           Three rounds of 11, 11 and 10 bits, each a histogram summed over the cluster
+//           through distributed shared memory, find the last key that is kept and how many
+//           of its equals; prefix sums over runs then place the slots.  Bounded by latency
+//           (five cluster barriers; with rounds of 8 bits, where a float's exponents fall on
+//           few bins, and ten barriers 8 rows of 65536 slots took 26 us).
 //   move    a warp per 16 kept tokens, kv head and K or V copies their rows of D bytes into
 //           a block of the other pages, under the largest of their scales.  Bounded by HBM.
 #include <cooperative_groups.h>
@@ -37,9 +38,9 @@ __device__ __forceinline__ uint32_t key_of(float x)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+constexpr int BINS = 2048;
 struct Shared {
-    uint32_t hist[2][256];         // alternating rounds: one is read by the cluster while the next is cleared
-    uint32_t total[256];
+    uint32_t hist[3][BINS];        // a round each: the cluster may still read one while the next fills
     uint32_t counts[2];            // of the block: keys above the last kept one, equals
     uint32_t warp[NWARP][2];
     uint32_t prefix, want;         // digits found so far; equals of them still to take
@@ -115,52 +116,49 @@ __global__ void __launch_bounds__(THREADS) kv8_select_kernel(Kv8EvictArgs a, int
         }
     }
     if (threadIdx.x == 0) sm.prefix = 0, sm.want = (uint32_t)n;
-    if (threadIdx.x < 256) sm.hist[0][threadIdx.x] = sm.hist[1][threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < 3 * BINS; i += THREADS) (&sm.hist[0][0])[i] = 0;
     __syncthreads();
-    for (int round = 0; round < 4; ++round) {
-        const int shift = 24 - 8 * round;
-        uint32_t *hist = sm.hist[round & 1];
+    // 11, 11 and 10 bits from the top
+    for (int round = 0; round < 3; ++round) {
+        const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, bits = round == 2 ? 10 : 11;
+        uint32_t *hist = sm.hist[round];
         const uint32_t prefix = sm.prefix, want = sm.want;
 #pragma unroll 4
         for (int s = s0 + threadIdx.x; s < s1; s += THREADS) {
             const uint32_t k = key(s);
-            if (round == 0 || k >> (shift + 8) == prefix) atomicAdd(&hist[k >> shift & 255u], 1u);
+            if (round == 0 || k >> (shift + bits) == prefix) atomicAdd(&hist[k >> shift & ((1u << bits) - 1)], 1u);
         }
         cl.sync();
-        if (threadIdx.x < 256) {
-            uint32_t t = 0;
+        // the digit that the want-th largest key has: a thread sums PER neighbouring bins over
+        // the cluster, from the top, and the one where the count passes `want` looks further
+        constexpr int PER = BINS / THREADS;
+        const int top = (1 << bits) - 1 - (int)threadIdx.x * PER;   // its highest bin (negative: none)
+        uint32_t v[PER] = {}, above[2] = {0, 0};
+        if (top >= 0) {
 #pragma unroll
-            for (int r = 0; r < MAX_CLUSTER; ++r)            // all loads in flight
-                if (r < C) t += cl.map_shared_rank(hist, r)[threadIdx.x];
-            sm.total[threadIdx.x] = t;
-            if (round >= 1) sm.hist[(round + 1) & 1][threadIdx.x] = 0;   // read by the cluster a round ago
+            for (int r = 0; r < MAX_CLUSTER; ++r) {                 // all loads in flight
+                if (r >= C) continue;
+                const uint4 x = *reinterpret_cast<const uint4 *>(cl.map_shared_rank(hist, r) + top - (PER - 1));
+                v[0] += x.w, v[1] += x.z, v[2] += x.y, v[3] += x.x;
+            }
+        }
+        static_assert(PER == 4, "one uint4 a thread");
+#pragma unroll
+        for (int e = 0; e < PER; ++e) above[0] += v[e];
+        const uint32_t sum = above[0];
+        scan2(sm, above);                                           // keys in higher bins
+        if (above[0] < want && above[0] + sum >= want) {            // one thread
+            uint32_t at = above[0];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                if (at < want && at + v[e] >= want) {
+                    sm.prefix = prefix << bits | (uint32_t)(top - e);
+                    sm.want = want - at;
+                }
+                at += v[e];
+            }
         }
         __syncthreads();
-        // the digit that the want-th largest key has: a warp walks the bins from the top
-        if (threadIdx.x < 32) {
-            uint32_t v[8], sum = 0;                          // lane i: bins 255 - 8 i ... 248 - 8 i
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum += v[e] = sm.total[255 - 8 * threadIdx.x - e];
-            uint32_t upto = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
-                if ((int)threadIdx.x >= o) upto += x;
-            }
-            uint32_t above = upto - sum;                     // keys in higher bins
-            if (above < want && upto >= want) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (above < want && above + v[e] >= want) {
-                        sm.prefix = prefix << 8 | (255 - 8 * threadIdx.x - e);
-                        sm.want = want - above;
-                        break;
-                    }
-                    above += v[e];
-                }
-            }
-        }
-        cl.sync();                                           // prefix is set, and nobody reads hist any more
     }
     // The last kept key is `last`; `equals` of those like it are kept, from the lowest slot on.
     const uint32_t last = sm.prefix, equals = sm.want;
