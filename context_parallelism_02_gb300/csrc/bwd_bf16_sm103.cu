@@ -109,6 +109,17 @@ __device__ __forceinline__ void ts_mn_seq(uint32_t tD, uint32_t tA, uint64_t dB,
     }
 }
 
+// 32 columns of the lane's row times f, as bf16, to 32-byte aligned memory: regrouped, so
+// that a store covers whole pieces of 64 bytes.  (Every lane its own row in 16 bytes took
+// the dK / dV epilogue of a unit 5500 cycles, as long as three of its half steps.)
+__device__ __forceinline__ void put_row_piece(__nv_bfloat16 *piece, bool ok, const uint32_t (&o)[32], float f, int lane)
+{
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+    store_warp_rows<16>(piece, ok, pk, lane);
+}
+
 // ----------------------------------------------------------------------------- Delta
 
 __global__ void __launch_bounds__(256) bwd_delta_kernel(const __nv_bfloat16 *__restrict__ out,
@@ -249,8 +260,8 @@ struct BwdArgs {
 // (about 10 tiles for a window of 1024), so a block takes several in turn: barrier phases
 // run on across them (without WIN every unit loop runs once and the running counts are
 // the unit's own), the next unit's loads and first products go out beside the current
-// one's last steps, and its set-up is paid once (16384 rows, 16 heads, window 1024, a block
-// a unit: dQ 241 us, dK / dV 368; so FIXME).
+// one's last steps, and its set-up is paid once (16384 rows, 16 heads, window 1024: dQ 241 us
+// with a block a unit, 190 so).
 struct PackMaps {
     CUtensorMap k_sinks, k_rest, v_sinks, v_rest;
 };
@@ -696,11 +707,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 tc_fence_after();
                 // each half writes D/2 columns of dQ = scale * acc
                 constexpr int HD = D / 2;
+                const bool a32 = (reinterpret_cast<uintptr_t>(dq) & 31) == 0;
                 __nv_bfloat16 *orow = dq + (((int64_t)w.b * a.S + qp) * a.Hq + w.h) * D + HD * half;
-#pragma unroll
+#pragma unroll (WIN ? 1 : HD / 32)
                 for (int c = 0; c < HD / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld_x32(tDQ + HD * half + 32u * c, o);
+                    if constexpr (WIN) {
+                        if (a32) {
+                            put_row_piece(orow + 32 * c, valid, o, a.scale, lane);
+                            continue;
+                        }
+                    }
                     if (valid) {
                         uint4 *dst = reinterpret_cast<uint4 *>(orow + 32 * c);
 #pragma unroll
@@ -896,7 +914,28 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             Ring<K_QST> qr;
             Item x;
             bool ok = true;
+            // Per-row statistics of a half tile, fetched a half step ahead (waiting for them
+            // at every step held back a unit's first loads by a memory latency each):
+            // -lse in log2 units and -Delta of rows lane and lane + 32.
+            float st_l[2], st_d[2];
+            auto fetch_stats = [&](const Walk &it, int hs) {
+                const int qa = it.start() + 64 * hs, ql = it.len() - 64 * hs;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int e = lane + 32 * i;
+                    st_l[i] = st_d[i] = 0.f;
+                    if (e < ql) {
+                        const int pos = WIN ? qa + e : slot_pos(g, qa + e);
+                        const int64_t off = ((int64_t)x.w.b * a.Hq + it.head()) * a.S + dbg_coord(a.err, pos, a.S);
+                        st_l[i] = lse[off];
+                        st_d[i] = delta[off];
+                    }
+                }
+            };
             for (int u = 0; ok && unit_of(u, x); ++u) {
+                Walk it;
+                start_walk(it, x);
+                if (x.ns > 0) fetch_stats(it, 0);
                 if (u > 0 && !waitw(BAR(K_KVEMPTY), (u - 1) & 1, wc)) break;
                 if (lane == 0) {
                     const int kmr = WIN ? 0 : dbg_coord(a.err, slot_mrank(g, x.w.ks), map_r);
@@ -909,15 +948,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     }
                 }
                 ++nkv;
-                Walk it;
-                start_walk(it, x);
                 for (int s = 0; s < x.ns; ++s, qr.next()) {
                     if (issued >= K_QST && !waitw(BAR(K_QEMPTY + qr.st), qr.ph ^ 1, wc)) {
                         ok = false;
                         break;
                     }
-                    const int hs = s & 1;
-                    const int qa = it.start() + 64 * hs, ql = it.len() - 64 * hs, h = it.head();
+                    const int hs = s & 1, h = it.head();
                     // map coordinates; the second half-tile may start past the end of
                     // the map (a short last tile): the copy then reads the fill value
                     int qr_rank = 0, qr_row;
@@ -927,18 +963,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         qr_rank = dbg_coord(a.err, it.mrank(), map_r);
                         qr_row = dbg_coord(a.err, it.mrow(), map_rows) + 64 * hs;
                     }
-                    // per-row statistics of the half tile, negated: -lse (log2 units), -Delta
                     float *ls = stat + qr.st * 128, *dl = ls + 64;
-                    for (int e = lane; e < 64; e += 32) {
-                        float l2 = 0.f, dd = 0.f;
-                        if (e < ql) {
-                            const int64_t off =
-                                ((int64_t)x.w.b * a.Hq + h) * a.S + dbg_coord(a.err, slot_pos(g, qa + e), a.S);
-                            l2 = -lse[off] * LOG2E;
-                            dd = -delta[off];
-                        }
-                        ls[e] = l2;
-                        dl[e] = dd;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        ls[lane + 32 * i] = -st_l[i] * LOG2E;
+                        dl[lane + 32 * i] = -st_d[i];
                     }
                     __syncwarp();
                     if (lane == 0) {
@@ -954,6 +983,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     __syncwarp();
                     ++issued;
                     if (hs) it.next();
+                    if (s + 1 < x.ns) fetch_stats(it, hs ^ 1);
                 }
             }
             if (lane == 0) {
@@ -1184,6 +1214,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 bool valid = row < w.kl;
                 const float f = half ? a.scale : 1.f;
                 const uint32_t tAcc = tmem + lane_off + (half ? C::TM_DK : C::TM_DV);
+                const bool a32 = (reinterpret_cast<uintptr_t>(half ? dk : dv) & 31) == 0;
                 const int krow = WIN ? dbg_coord(a.err, valid ? kpos : 0, a.Sk)
                                      : dbg_coord(a.err, valid ? slot_pos(g, kpos) : 0, a.S);
                 __nv_bfloat16 *orow = (half ? dk : dv) + (((int64_t)w.b * (WIN ? a.Sk : a.S) + krow) * a.Hkv + w.g) * D;
@@ -1195,7 +1226,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                                          ((int64_t)piece * 2 + (half ? 0 : 1)) * a.win.sinks + kpos) * D;
                     valid = valid && !sink && piece == 0;
                 }
-#pragma unroll
+#pragma unroll (WIN ? 1 : D / 32)
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld_x32(tAcc + 32u * c, o);
@@ -1210,6 +1241,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             for (int v4 = 0; v4 < 8; ++v4)
                                 dst[v4] = make_float4(__uint_as_float(o[4 * v4]) * f, __uint_as_float(o[4 * v4 + 1]) * f,
                                                       __uint_as_float(o[4 * v4 + 2]) * f, __uint_as_float(o[4 * v4 + 3]) * f);
+                        }
+                    }
+                    if constexpr (WIN) {
+                        if (a32) {
+                            put_row_piece(orow + 32 * c, valid, o, f, lane);
+                            continue;
                         }
                     }
                     if (valid) {

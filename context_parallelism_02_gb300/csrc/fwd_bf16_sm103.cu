@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         auto put_unit = [&]() {
             const float inv = p_l > 0.f ? 1.f / p_l : 0.f;
             const bool a32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
-#pragma unroll
+#pragma unroll 1
             for (int pc = 0; pc < D / 64; ++pc) {   // 32 columns at a time: P's registers are live here
                 uint32_t o[32], pk[16];
                 tmem_ld_x32(tO + 32u * pc, o);
