@@ -5,11 +5,13 @@
 // slot's mass (NaN counts as the largest).  Two kernels:
 //   select  a cluster of blocks per (sequence, kv head), each with a run of its slots in
 //           shared memory as 32-bit keys in the order of the floats: mass is read once.
-//           Three rounds of 11, 11 and 10 bits, each a histogram summed over the cluster
-//           through distributed shared memory, find the last key that is kept and how many
-//           of its equals; prefix sums over runs then place the slots.  Bounded by latency
-//           (five cluster barriers; with rounds of 8 bits, where a float's exponents fall on
-//           few bins, and ten barriers 8 rows of 65536 slots took 26 us).
+//           Four rounds of 8 bits, each a histogram summed over the cluster through
+//           distributed shared memory, find the last key that is kept and how many of its
+//           equals; counts by warps of consecutive slots then place the slots.  Bounded by
+//           latency: six cluster barriers and the passes over the keys, BATCH loads at a time
+//           (rounds of 11 bits save one, but summing 2048 bins costs 4000 cycles each; a run
+//           of slots per thread, with its bank conflicts and one load at a time, took 15000
+//           cycles for the last two passes: 8 rows of 65536 slots FIXME).
 //   move    a warp per 16 kept tokens, kv head and K or V copies their rows of D bytes into
 //           a block of the other pages, under the largest of their scales.  Bounded by HBM.
 #include <cooperative_groups.h>
@@ -38,9 +40,10 @@ __device__ __forceinline__ uint32_t key_of(float x)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int BINS = 2048;
+constexpr int BINS = 256, ROUNDS = 4;
+constexpr int BATCH = 16;          // slots of a thread whose loads are in flight together
 struct Shared {
-    uint32_t hist[3][BINS];        // a round each: the cluster may still read one while the next fills
+    uint32_t hist[ROUNDS][BINS];   // a round each: the cluster may still read one while the next fills
     uint32_t counts[2];            // of the block: keys above the last kept one, equals
     uint32_t warp[NWARP][2];
     uint32_t prefix, want;         // digits found so far; equals of them still to take
@@ -88,8 +91,11 @@ __global__ void __launch_bounds__(THREADS) kv8_select_kernel(Kv8EvictArgs a, int
         if (mass_to && i < cap_to) mass_to[i] = 0.f;
     }
     if (rank == 0 && threadIdx.x == 0 && row % (unsigned)a.pool.Hkv == 0) a.lens_to[b] = n;
-    // this block's run of slots
+    // this block's run of slots, and in it the warp's
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int run = (len + C - 1) / C, s0 = min(rank * run, len), s1 = min(s0 + run, len);
+    const int seg = ((s1 - s0 + NWARP - 1) / NWARP + 31) & ~31;
+    const int w0 = min(s0 + warp * seg, s1), w1 = min(w0 + seg, s1);
     if (len <= a.budget) {                                   // all of them (the same in the whole cluster)
         for (int s = s0 + threadIdx.x; s < s1; s += THREADS) {
             kept[s] = s;
@@ -97,98 +103,112 @@ __global__ void __launch_bounds__(THREADS) kv8_select_kernel(Kv8EvictArgs a, int
         }
         return;
     }
-    auto key_at = [&](int s) -> uint32_t {
-        if (s < a.first || s >= len - a.last) return 0xffffffffu;
-        return key_of(mass[s]);
+    auto key_from = [&](int s, float x) -> uint32_t {
+        return s < a.first || s >= len - a.last ? 0xffffffffu : key_of(x);
     };
-    auto key = [&](int s) -> uint32_t { return in_shared ? keys[s - s0] : key_at(s); };
+    // f(slot, key, whether it is there) for the warp's slots, 32 consecutive ones at a time
+    auto each_key = [&](auto f) {
+        for (int t = w0; t < w1; t += 32 * BATCH) {
+            uint32_t k[BATCH];
+            if (in_shared) {
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int s = t + 32 * i + lane;
+                    k[i] = s < w1 ? keys[s - s0] : 0u;
+                }
+            } else {
+                float x[BATCH];
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) x[i] = t + 32 * i + lane < w1 ? mass[t + 32 * i + lane] : 0.f;
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) k[i] = key_from(t + 32 * i + lane, x[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+                if (t + 32 * i < w1) f(t + 32 * i + lane, k[i], t + 32 * i + lane < w1);
+        }
+    };
     if (in_shared) {
-        constexpr int BATCH = 8;                             // loads in flight of a thread
-        for (int t = s0 + threadIdx.x; t < s1; t += BATCH * THREADS) {
+        for (int t = w0; t < w1; t += 32 * BATCH) {
             float x[BATCH];
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) x[i] = t + i * THREADS < s1 ? mass[t + i * THREADS] : 0.f;
+            for (int i = 0; i < BATCH; ++i) x[i] = t + 32 * i + lane < w1 ? mass[t + 32 * i + lane] : 0.f;
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
-                const int s = t + i * THREADS;
-                if (s < s1) keys[s - s0] = s < a.first || s >= len - a.last ? 0xffffffffu : key_of(x[i]);
+                const int s = t + 32 * i + lane;
+                if (s < w1) keys[s - s0] = key_from(s, x[i]);
             }
         }
     }
     if (threadIdx.x == 0) sm.prefix = 0, sm.want = (uint32_t)n;
-    for (int i = threadIdx.x; i < 3 * BINS; i += THREADS) (&sm.hist[0][0])[i] = 0;
+    for (int i = threadIdx.x; i < ROUNDS * BINS; i += THREADS) (&sm.hist[0][0])[i] = 0;
     __syncthreads();
-    // 11, 11 and 10 bits from the top
-    for (int round = 0; round < 3; ++round) {
-        const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, bits = round == 2 ? 10 : 11;
+    for (int round = 0; round < ROUNDS; ++round) {
+        const int shift = 24 - 8 * round;
         uint32_t *hist = sm.hist[round];
         const uint32_t prefix = sm.prefix, want = sm.want;
-#pragma unroll 4
-        for (int s = s0 + threadIdx.x; s < s1; s += THREADS) {
-            const uint32_t k = key(s);
-            if (round == 0 || k >> (shift + bits) == prefix) atomicAdd(&hist[k >> shift & ((1u << bits) - 1)], 1u);
-        }
+        each_key([&](int, uint32_t k, bool there) {
+            if (there && (round == 0 || k >> (shift + 8) == prefix)) atomicAdd(&hist[k >> shift & 255u], 1u);
+        });
         cl.sync();
-        // the digit that the want-th largest key has: a thread sums PER neighbouring bins over
-        // the cluster, from the top, and the one where the count passes `want` looks further
-        constexpr int PER = BINS / THREADS;
-        const int top = (1 << bits) - 1 - (int)threadIdx.x * PER;   // its highest bin (negative: none)
-        uint32_t v[PER] = {}, above[2] = {0, 0};
-        if (top >= 0) {
+        // the digit that the want-th largest key has: thread i sums bin 255 - i over the cluster
+        const int bin = BINS - 1 - (int)threadIdx.x;
+        uint32_t v[2] = {0, 0};
+        if (bin >= 0) {
 #pragma unroll
-            for (int r = 0; r < MAX_CLUSTER; ++r) {                 // all loads in flight
-                if (r >= C) continue;
-                const uint4 x = *reinterpret_cast<const uint4 *>(cl.map_shared_rank(hist, r) + top - (PER - 1));
-                v[0] += x.w, v[1] += x.z, v[2] += x.y, v[3] += x.x;
-            }
+            for (int r = 0; r < MAX_CLUSTER; ++r)            // all loads in flight
+                if (r < C) v[0] += cl.map_shared_rank(hist, r)[bin];
         }
-        static_assert(PER == 4, "one uint4 a thread");
-#pragma unroll
-        for (int e = 0; e < PER; ++e) above[0] += v[e];
-        const uint32_t sum = above[0];
-        scan2(sm, above);                                           // keys in higher bins
-        if (above[0] < want && above[0] + sum >= want) {            // one thread
-            uint32_t at = above[0];
-#pragma unroll
-            for (int e = 0; e < PER; ++e) {
-                if (at < want && at + v[e] >= want) {
-                    sm.prefix = prefix << bits | (uint32_t)(top - e);
-                    sm.want = want - at;
-                }
-                at += v[e];
-            }
+        const uint32_t here = v[0];
+        scan2(sm, v);                                        // v[0]: keys in higher bins
+        if (v[0] < want && v[0] + here >= want) {            // one thread
+            sm.prefix = prefix << 8 | (uint32_t)bin;
+            sm.want = want - v[0];
         }
         __syncthreads();
     }
     // The last kept key is `last`; `equals` of those like it are kept, from the lowest slot on.
     const uint32_t last = sm.prefix, equals = sm.want;
-    // a thread takes a run of neighbouring slots
-    const int per = (s1 - s0 + THREADS - 1) / THREADS;
-    const int t0 = min(s0 + (int)threadIdx.x * per, s1), t1 = min(t0 + per, s1);
-    uint32_t count[2] = {0, 0};
-    for (int s = t0; s < t1; ++s) {
-        const uint32_t k = key(s);
-        count[0] += k > last;
-        count[1] += k == last;
-    }
-    uint32_t at[2] = {count[0], count[1]};
-    scan2(sm, at);
-    if (threadIdx.x == THREADS - 1) sm.counts[0] = at[0] + count[0], sm.counts[1] = at[1] + count[1];
+    uint32_t at[2] = {0, 0};                                 // keys above it, equals: in the warp's slots
+    each_key([&](int, uint32_t k, bool there) {
+        at[0] += __popc(__ballot_sync(0xffffffffu, there && k > last));
+        at[1] += __popc(__ballot_sync(0xffffffffu, there && k == last));
+    });
+    if (lane == 0) sm.warp[warp][0] = at[0], sm.warp[warp][1] = at[1];
+    __syncthreads();
+    // ... and before them
+    at[0] = at[1] = 0;
+    for (int w = 0; w < warp; ++w) at[0] += sm.warp[w][0], at[1] += sm.warp[w][1];
+    if (threadIdx.x == THREADS - 1) sm.counts[0] = at[0] + sm.warp[warp][0], sm.counts[1] = at[1] + sm.warp[warp][1];
     cl.sync();
-    for (int r = 0; r < rank; ++r) {
-        const uint32_t *other = cl.map_shared_rank(sm.counts, r);
-        at[0] += other[0];
-        at[1] += other[1];
-    }
-    for (int s = t0; s < t1; ++s) {
-        const uint32_t k = key(s);
-        if (k > last || (k == last && at[1] < equals)) {
-            const uint32_t i = at[0] + min(at[1], equals);
-            kept[i] = s;
-            if (mass_to) mass_to[i] = mass[s];
+#pragma unroll
+    for (int r = 0; r < MAX_CLUSTER; ++r)
+        if (r < rank) {
+            const uint32_t *other = cl.map_shared_rank(sm.counts, r);
+            at[0] += other[0];
+            at[1] += other[1];
         }
-        at[0] += k > last;
-        at[1] += k == last;
+    const unsigned lower = (1u << lane) - 1u;
+    for (int t = w0; t < w1; t += 32 * BATCH) {
+        float x[BATCH];                                      // mass again, for mass_to (in L2)
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) x[i] = t + 32 * i + lane < w1 ? mass[t + 32 * i + lane] : 0.f;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int s = t + 32 * i + lane;
+            if (t + 32 * i >= w1) break;
+            const bool there = s < w1;
+            const uint32_t k = in_shared ? (there ? keys[s - s0] : 0u) : key_from(s, x[i]);
+            const unsigned gt = __ballot_sync(0xffffffffu, there && k > last), eq = __ballot_sync(0xffffffffu, there && k == last);
+            const uint32_t ties = at[1] + __popc(eq & lower);
+            if (there && (k > last || (k == last && ties < equals))) {
+                const uint32_t to = at[0] + __popc(gt & lower) + min(ties, equals);
+                kept[to] = s;
+                if (mass_to) mass_to[to] = x[i];
+            }
+            at[0] += __popc(gt);
+            at[1] += __popc(eq);
+        }
     }
     cl.sync();                                               // counts are read by other blocks
 }
@@ -268,9 +288,10 @@ int launch_kv8_evict(const Kv8EvictArgs &a, int D, cudaStream_t st)
     const __int128 units = (__int128)rows * blocks * 2;
     if (cap > 0x7fffffffLL || rows * MAX_CLUSTER > 0x7fffffffLL || units > (__int128)0x7fffffff * MOVE_WARPS)
         return CP_EUNSUPPORTED;
-    // blocks of a cluster: as many as leave each about 2048 slots
+    // blocks of a cluster: as many as leave each about 2048 slots, but no more than run at
+    // once, two to an SM (128 rows of 8192 slots: 19 us with 4 blocks each, FIXME with 2)
     int C = 1;
-    while (C < MAX_CLUSTER && cap > (int64_t)C * 2048) C *= 2;
+    while (C < MAX_CLUSTER && cap > (int64_t)C * 2048 && rows * C <= sm_count()) C *= 2;
     const int64_t run = (cap + C - 1) / C;
     const int in_shared = run <= MAX_KEYS;
     const size_t smem = in_shared ? (size_t)run * 4 : 0;
