@@ -26,6 +26,22 @@ struct Lay {
     static constexpr int N = 16 / ROWS;               // accesses
 };
 
+// The units of a launch: (batch, block, head, K or V), the last fastest, so that the warps of
+// a moment read neighbouring rows.
+struct Units {
+    FastDiv by_heads, by_blocks;
+    int n;
+    __device__ __forceinline__ void decode(int unit, int &b, int &t, int &h, int &which) const
+    {
+        which = unit & 1;
+        const unsigned x = (unsigned)unit >> 1, y = by_heads.div(x);
+        h = (int)(x - y * by_heads.d);
+        const unsigned z = by_blocks.div(y);
+        t = (int)(y - z * by_blocks.d);
+        b = (int)z;
+    }
+};
+
 // The magnitudes' bits of the elements of 16 bytes: the largest, as fp32 bits.
 template <typename T>
 __device__ __forceinline__ uint32_t top_bits(const uint4 &x)
@@ -79,20 +95,16 @@ __device__ __forceinline__ void encode(const uint4 &x, float inv, bool odd, uint
     }
 }
 
-// Heads and K / V fastest: the warps of a moment read neighbouring rows.
 template <int D, typename T>
-__global__ void __launch_bounds__(WARPS * 32) kv8_append_kernel(Kv8AppendArgs a, int blocks, int64_t units)
+__global__ void __launch_bounds__(WARPS * 32, sizeof(T) == 2 ? 4 : 2) kv8_append_kernel(Kv8AppendArgs a, Units units)
 {
     using L = Lay<D, T>;
     const int lane = threadIdx.x & 31;
     kv4_begin();
     const int64_t unit = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
-    if (unit >= units) return;
-    const int which = (int)(unit & 1);
-    int64_t rest = unit >> 1;
-    const int h = (int)(rest % a.pool.Hkv);
-    rest /= a.pool.Hkv;
-    const int t = (int)(rest % blocks), b = (int)(rest / blocks);
+    if (unit >= units.n) return;
+    int b, t, h, which;
+    units.decode((int)unit, b, t, h, which);
     const int64_t len = kv4_len(a.pool, b);
     const int n = a.n_new ? max(0, min(a.n_new[b], a.n)) : a.n;
     const int64_t slot0 = (len / KV8_BLOCK + t) * KV8_BLOCK;    // the block's first slot
@@ -146,18 +158,15 @@ __global__ void __launch_bounds__(WARPS * 32) kv8_append_kernel(Kv8AppendArgs a,
 
 // 16 rows of one head: 8 codes a lane, so that reads and writes cover whole rows.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(WARPS * 32) kv8_gather_kernel(Kv8GatherArgs a, int blocks, int64_t units)
+__global__ void __launch_bounds__(WARPS * 32) kv8_gather_kernel(Kv8GatherArgs a, Units units)
 {
     constexpr int LANES = D / 8, ROWS = 32 / LANES, N = 16 / ROWS;
     const int lane = threadIdx.x & 31;
     kv4_begin();
     const int64_t unit = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
-    if (unit >= units) return;
-    const int which = (int)(unit & 1);
-    int64_t rest = unit >> 1;
-    const int h = (int)(rest % a.pool.Hkv);
-    rest /= a.pool.Hkv;
-    const int t = (int)(rest % blocks), b = (int)(rest / blocks);
+    if (unit >= units.n) return;
+    int b, t, h, which;
+    units.decode((int)unit, b, t, h, which);
     const int64_t len = kv4_len(a.pool, b), start = a.start ? a.start[b] : 0;
     // lane r < 16: where row r comes from
     const uint8_t *src = nullptr;
@@ -207,14 +216,13 @@ __global__ void __launch_bounds__(WARPS * 32) kv8_gather_kernel(Kv8GatherArgs a,
     }
 }
 
-// Units of (b, block, head, K or V), WARPS of them a thread block.
 template <typename A>
-int launch_units(void (*kernel)(A, int, int64_t), const A &a, int64_t blocks, cudaStream_t st)
+int launch_units(void (*kernel)(A, Units), const A &a, int64_t blocks, cudaStream_t st)
 {
-    const __int128 units = (__int128)a.B * blocks * a.pool.Hkv * 2;
-    if (blocks > 0x7fffffffLL || units > (__int128)0x7fffffff * WARPS) return CP_EUNSUPPORTED;
-    const unsigned grid = (unsigned)(((int64_t)units + WARPS - 1) / WARPS);
-    return kv4_launch(kernel, grid, WARPS * 32, 0, st, a, (int)blocks, (int64_t)units) == cudaSuccess ? CP_OK : CP_ECUDA;
+    const __int128 n = (__int128)a.B * blocks * a.pool.Hkv * 2;
+    if (n > 0x7fffffff) return CP_EUNSUPPORTED;
+    const Units units{fast_div((uint32_t)a.pool.Hkv), fast_div((uint32_t)blocks), (int)n};
+    return kv4_launch(kernel, (unsigned)((n + WARPS - 1) / WARPS), WARPS * 32, 0, st, a, units) == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 
 }  // namespace

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(THREADS) kv8_select_kernel(Kv8EvictArgs a, int
 
 // 16 kept tokens of one kv head, K or V.
 template <int D>
-__global__ void __launch_bounds__(MOVE_WARPS * 32) kv8_move_kernel(Kv8EvictArgs a, int blocks, int64_t units)
+__global__ void __launch_bounds__(MOVE_WARPS * 32) kv8_move_kernel(Kv8EvictArgs a, FastDiv by_heads, FastDiv by_blocks, int units)
 {
     constexpr int LANES = D / 16, ROWS = 32 / LANES, N = 16 / ROWS;
     const int lane = threadIdx.x & 31;
@@ -223,10 +223,8 @@ __global__ void __launch_bounds__(MOVE_WARPS * 32) kv8_move_kernel(Kv8EvictArgs 
     const int64_t unit = (int64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
     if (unit >= units) return;
     const int which = (int)(unit & 1);
-    int64_t rest = unit >> 1;
-    const int h = (int)(rest % a.pool.Hkv);
-    rest /= a.pool.Hkv;
-    const int t = (int)(rest % blocks), b = (int)(rest / blocks);
+    const unsigned x0 = (unsigned)unit >> 1, y0 = by_heads.div(x0);
+    const int h = (int)(x0 - y0 * by_heads.d), b = (int)by_blocks.div(y0), t = (int)(y0 - (unsigned)b * by_blocks.d);
     const int64_t i0 = (int64_t)t * KV8_BLOCK;
     // lane r < 16: where token r of the block comes from
     int slot = -1;
@@ -286,7 +284,7 @@ int launch_kv8_evict(const Kv8EvictArgs &a, int D, cudaStream_t st)
     const int64_t rows = (int64_t)a.B * a.pool.Hkv, cap = (int64_t)a.pool.max_pages << a.pool.page_shift;
     const int64_t blocks = ((int64_t)a.budget + KV8_BLOCK - 1) / KV8_BLOCK;
     const __int128 units = (__int128)rows * blocks * 2;
-    if (cap > 0x7fffffffLL || rows * MAX_CLUSTER > 0x7fffffffLL || units > (__int128)0x7fffffff * MOVE_WARPS)
+    if (cap > 0x7fffffffLL || rows * MAX_CLUSTER > 0x7fffffffLL || units > 0x7fffffff)
         return CP_EUNSUPPORTED;
     // blocks of a cluster: as many as leave each about 2048 slots, but no more than run at
     // once, two to an SM (128 rows of 8192 slots: 19 us with 4 blocks each, FIXME with 2)
@@ -319,7 +317,7 @@ int launch_kv8_evict(const Kv8EvictArgs &a, int D, cudaStream_t st)
     if (cudaLaunchKernelEx(&cfg, kv8_select_kernel, a, in_shared) != cudaSuccess) return CP_ECUDA;
     const unsigned grid = (unsigned)(((int64_t)units + MOVE_WARPS - 1) / MOVE_WARPS);
     const cudaError_t rc = kv4_launch(D == 64 ? kv8_move_kernel<64> : kv8_move_kernel<128>, grid, MOVE_WARPS * 32, 0, st, a,
-                                      (int)blocks, (int64_t)units);
+                                      fast_div((uint32_t)a.pool.Hkv), fast_div((uint32_t)blocks), (int)units);
     return rc == cudaSuccess ? CP_OK : CP_ECUDA;
 }
 
