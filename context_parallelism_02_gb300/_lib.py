@@ -71,7 +71,7 @@ SIGNATURES = {
     "kv8_append": (_I, [_P] * 8 + [_I] * 8 + [_P]),
     "kv8_gather": (_I, [_P] * 7 + [_I] * 8 + [_P]),
     "kv8_attn": (_I, [_P] * 9 + [_I] * 8 + [_L, _L, _I, _I, _F, _P, ctypes.c_size_t, _P]),
-    "kv8_attn_workspace": (ctypes.c_size_t, [_I] * 7),
+    "kv8_attn_workspace": (ctypes.c_size_t, [_I] * 8),
     "kv8_evict": (_I, [_P] * 9 + [_I] * 10 + [_P]),
     "cp_get_error": (_I, [_P]),
     "cp_strerror": (ctypes.c_char_p, [_I]),

@@ -509,9 +509,9 @@ def kv8_gather(cache, scales, pages, lens, count: int, start=None, dtype=torch.b
     return got
 
 
-def kv8_attn_workspace(B: int, n: int, Hq: int, D: int, page: int, max_pages: int, mass: bool = False) -> int:
+def kv8_attn_workspace(B: int, n: int, Hq: int, Hkv: int, D: int, page: int, max_pages: int, mass: bool = False) -> int:
     """Bytes of scratch for :func:`kv8_attn`."""
-    return int(_lib.load().kv8_attn_workspace(B, n, Hq, D, page, max_pages, int(mass)))
+    return int(_lib.load().kv8_attn_workspace(B, n, Hq, Hkv, D, page, max_pages, int(mass)))
 
 
 def kv8_attn(q, cache, scales, pages, lens, window: int = 0, sinks: int = 0, vis=None, causal: bool = True,

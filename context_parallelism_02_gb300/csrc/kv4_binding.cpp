@@ -430,7 +430,7 @@ PyObject *attn8(PyObject *const *args, Py_ssize_t n_args)
     const at::Tensor o = out ? *out : at::empty(q.sizes(), q.options());
     const at::Tensor z = lse ? *lse : at::empty({B, Hq, n}, q.options().dtype(at::kFloat));
     const at::Tensor w = ws ? *ws
-                            : at::empty({(int64_t)a.table->attn8_workspace(b, nn, hq, p.D, p.page, p.max_pages, mass != nullptr)},
+                            : at::empty({(int64_t)a.table->attn8_workspace(b, nn, hq, p.heads, p.D, p.page, p.max_pages, mass != nullptr)},
                                         q.options().dtype(at::kByte));
     const int rc = run([&] {
         return a.table->attn8(ptr(q), ptr(cache), floats(&scales), ints(pages), ints(lens), ints(vis), ptr(o),

@@ -109,14 +109,14 @@ struct Kv8AttnArgs {
     void *out;                   // [B][n][Hq][D]
     float *lse;                  // [B][Hq][n]
     float *mass;                 // [B][Hkv][max_pages page] or null
-    float *scores;               // [B][Hkv][max_pages page][n Hq / Hkv], log2 units; with mass
+    float *scores;               // [B][Hkv][max_pages page][n Hq / Hkv, to a multiple of 4], log2 units
     int window, sinks;           // window 0: none
     int out_f32;
     float scale;
     void *ws;
     uint64_t limit_ns, drain_ns;
 };
-size_t kv8_attn_workspace_bytes(int B, int n, int Hq, int D, int64_t slots, bool mass);
+size_t kv8_attn_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int64_t slots, bool mass);
 int launch_kv8_attn(const Kv8AttnArgs &a, int D, int64_t n_pages, cudaStream_t st);
 
 struct Kv8EvictArgs {

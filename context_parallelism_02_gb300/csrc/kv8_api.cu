@@ -81,10 +81,10 @@ int kv8_gather(const void *cache, const float *scales, const int32_t *pages, con
     return launch_kv8_gather(a, D, dtype, static_cast<cudaStream_t>(stream));
 }
 
-size_t kv8_attn_workspace(int B, int n, int Hq, int D, int page, int max_pages, int mass)
+size_t kv8_attn_workspace(int B, int n, int Hq, int Hkv, int D, int page, int max_pages, int mass)
 {
-    if (B < 0 || n < 0 || Hq < 1 || page < 0 || max_pages < 0) return 0;
-    return kv8_attn_workspace_bytes(B, n, Hq, D, (int64_t)page * max_pages, mass != 0);
+    if (B < 0 || n < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv || page < 0 || max_pages < 0) return 0;
+    return kv8_attn_workspace_bytes(B, n, Hq, Hkv, D, (int64_t)page * max_pages, mass != 0);
 }
 
 int kv8_attn(const void *q, const void *cache, const float *scales, const int32_t *pages, const int32_t *lens,
@@ -101,7 +101,7 @@ int kv8_attn(const void *q, const void *cache, const float *scales, const int32_
     if (window < 0 || sinks < 0 || isnan(scale)) return CP_EINVAL;
     if (B == 0 || n == 0) return CP_OK;
     if (!out || !lse || !aligned(out, 16) || !aligned(lse, 4) || !aligned(mass, 4)) return CP_EINVAL;
-    const size_t need = kv8_attn_workspace(B, n, Hq, D, page, max_pages, mass != nullptr);
+    const size_t need = kv8_attn_workspace(B, n, Hq, Hkv, D, page, max_pages, mass != nullptr);
     if (need == 0) return CP_EUNSUPPORTED;
     if (!workspace || !aligned(workspace, 16) || ws_bytes < need) return CP_EINVAL;
     a.q = static_cast<const __nv_bfloat16 *>(q);

@@ -356,8 +356,11 @@ __device__ __forceinline__ void visible_tokens(const Rows<D, NT> &r, int slot, i
                                         : visible_bits(0, min(r.limit[t][e] - slot, KV8_BLOCK), r.low[t][e] - slot, sinks - slot) & 0xffffu;
 }
 
-// A stage: NB blocks of 16 tokens for the warp's state.  scores: where the lane's column of the
-// item's scores begins, per token `rows` apart, or null.
+// Rows of a token's scores: those of its kv head, rounded up so that they are read by fours.
+__host__ __device__ __forceinline__ int64_t score_rows(int64_t rows) { return (rows + 3) / 4 * 4; }
+
+// A stage: NB blocks of 16 tokens for the warp's state.  scores: those of the item's kv head,
+// [slot][rows], or null.
 template <int D, int NT>
 __device__ __forceinline__ void blocks_step(const uint8_t *stage, const Meta (&mt)[NB], const Rows<D, NT> &r, int sinks,
                                             float *scores, int rows, int tile_row, State<D, NT> &s)
@@ -395,9 +398,11 @@ __device__ __forceinline__ void blocks_step(const uint8_t *stage, const Meta (&m
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = tile_row + 8 * t + 2 * c + (e & 1);
-                    if (row < rows) scores[((int64_t)mt[i].slot + g + (e >> 1) * 8) * rows + row] = x[i][t][e];
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int row = tile_row + 8 * t + 2 * c;
+                    if (row < rows)
+                        *reinterpret_cast<float2 *>(scores + ((int64_t)mt[i].slot + g + hf * 8) * rows + row) =
+                            make_float2(x[i][t][2 * hf], x[i][t][2 * hf + 1]);
                 }
         }
     }
@@ -579,7 +584,8 @@ __global__ void __launch_bounds__(W * 32)
     if (a.limit_ns < SHORT_WAIT_NS) dead = !waitw(smem_u32(&sm.hold), 0, wc);
     auto take = [&](const Item &it, const Rows<D, NT> &r, State<D, NT> &s, int blocks) {   // the next blocks of the ring
         float *scores = nullptr;
-        if (a.mass) scores = a.scores + ((((int64_t)it.b * a.pool.Hkv + it.h) * a.pool.max_pages) << ps) * sh.rows;
+        const int srows = (int)score_rows(sh.rows);
+        if (a.mass) scores = a.scores + ((((int64_t)it.b * a.pool.Hkv + it.h) * a.pool.max_pages) << ps) * srows;
         for (int t = 0; t < blocks; t += NB) {
             if (!dead && !waitw(smem_u32(&sm.full[warp][get]), phase, wc)) dead = true;
             if (dead) break;
@@ -590,7 +596,7 @@ __global__ void __launch_bounds__(W * 32)
                 mt[i] = sm.meta[warp][get][i];
                 any |= mt[i].slot < r.max_limit;
             }
-            if (any) blocks_step<D, NT>(sm.ring[warp][get][0], mt, r, a.sinks, scores, sh.rows, it.tile * NT * 8, s);
+            if (any) blocks_step<D, NT>(sm.ring[warp][get][0], mt, r, a.sinks, scores, srows, it.tile * NT * 8, s);
             ++taken;
             if (++get == STAGES) get = 0, phase ^= 1;
             __syncwarp();                    // every lane has read the stage
@@ -703,8 +709,11 @@ __global__ void __launch_bounds__(W * 32)
     drain();
 }
 
-// mass += the weights, from the scores that the attention kernel left: a thread a slot, the
-// rows of its kv head in order.  Blocks of 256 slots of one (sequence, kv head).
+// mass += the weights, from the scores that the attention kernel left (in L2, as far as they
+// fit): a thread takes MASS_SLOTS slots with all their loads in flight (one slot at a time, in
+// blocks of 256, took 8 x 16384 slots and 8 kv heads 10 us, these FIXME) and adds up the rows
+// of its kv head in order.
+constexpr int MASS_SLOTS = 4, MASS_CHUNK = MASS_SLOTS * 256;
 constexpr int MASS_ROWS = 64;      // rows whose lse and range lie in shared memory at a time
 __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, int chunks)
 {
@@ -713,14 +722,22 @@ __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, 
     const int chunk = (int)(blockIdx.x % (unsigned)chunks);
     const unsigned bh = blockIdx.x / (unsigned)chunks;
     const int b = (int)(bh / (unsigned)a.pool.Hkv), h = (int)(bh % (unsigned)a.pool.Hkv);
-    kv4_begin();
+    const int srows = (int)score_rows(sh.rows);
+    kv4_wait();
+    kv4_trigger();   // as the join
     const int len = kv4_len(a.pool, b);
     const int64_t cap = (int64_t)a.pool.max_pages << a.pool.page_shift;
-    for (int64_t s0 = (int64_t)chunk * 256; s0 < len; s0 += (int64_t)chunks * 256) {
-        const int64_t slot = s0 + threadIdx.x;
-        float sum = 0.f;
-        bool any = false;
-        const float *x = a.scores + ((int64_t)bh * cap + slot) * sh.rows;
+    for (int64_t s0 = (int64_t)chunk * MASS_CHUNK; s0 < len; s0 += (int64_t)chunks * MASS_CHUNK) {
+        float *mass = a.mass + (int64_t)bh * cap + s0 + threadIdx.x;
+        const float *x = a.scores + ((int64_t)bh * cap + s0 + threadIdx.x) * srows;
+        float old[MASS_SLOTS], sum[MASS_SLOTS];
+        bool any[MASS_SLOTS];
+#pragma unroll
+        for (int i = 0; i < MASS_SLOTS; ++i) {
+            old[i] = s0 + threadIdx.x + 256 * i < len ? mass[256 * i] : 0.f;
+            sum[i] = 0.f;
+            any[i] = false;
+        }
         for (int r0 = 0; r0 < sh.rows; r0 += MASS_ROWS) {
             const int n = min(MASS_ROWS, sh.rows - r0);
             __syncthreads();
@@ -732,23 +749,28 @@ __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, 
                 lse2[threadIdx.x] = a.lse[((int64_t)b * a.rows.Hq + head) * a.rows.n + j] * LOG2E;
             }
             __syncthreads();
-            if (slot >= len) continue;
-            auto add = [&](float s, int r) {
-                if (slot < limit[r] && (slot >= low[r] || slot < a.sinks)) {
-                    sum += ex2(s - lse2[r]);
-                    any = true;
+            for (int r = 0; r < n; r += 4) {
+                float4 v[MASS_SLOTS];
+#pragma unroll
+                for (int i = 0; i < MASS_SLOTS; ++i)
+                    v[i] = s0 + threadIdx.x + 256 * i < len ? *reinterpret_cast<const float4 *>(x + (int64_t)256 * i * srows + r0 + r)
+                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < MASS_SLOTS; ++i) {
+                    const int64_t slot = s0 + threadIdx.x + 256 * i;
+                    const float w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (r + e < n && slot < limit[r + e] && (slot >= low[r + e] || slot < a.sinks)) {
+                            sum[i] += ex2(w[e] - lse2[r + e]);
+                            any[i] = true;
+                        }
                 }
-            };
-            if (sh.rows % 4 == 0) {          // n is a multiple of 4 too
-                for (int r = 0; r < n; r += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(x + r0 + r);
-                    add(v.x, r), add(v.y, r + 1), add(v.z, r + 2), add(v.w, r + 3);
-                }
-            } else {
-                for (int r = 0; r < n; ++r) add(x[r0 + r], r);
             }
         }
-        if (any) a.mass[(int64_t)bh * cap + slot] += sum;
+#pragma unroll
+        for (int i = 0; i < MASS_SLOTS; ++i)
+            if (any[i]) mass[256 * i] = old[i] + sum[i];
     }
 }
 
@@ -823,13 +845,14 @@ int launch(const Kv8AttnArgs &a, const Shape &sh, const CUtensorMap &map, cudaSt
         const unsigned n = (unsigned)joins;
         rc = cuts > 64   ? kv4_launch(kv_join_kernel<Kv8AttnArgs, D, NT, 16, 4>, n, 512, 0, st, a, sh, warps)
              : cuts > 16 ? kv4_launch(kv_join_kernel<Kv8AttnArgs, D, NT, 8, 8>, n, 256, 0, st, a, sh, warps)
-                         : kv4_launch(kv_join_kernel<Kv8AttnArgs, D, NT, 4, 4>, n, 128, 0, st, a, sh, warps);
+             : cuts > 4  ? kv4_launch(kv_join_kernel<Kv8AttnArgs, D, NT, 4, 4>, n, 128, 0, st, a, sh, warps)
+                         : kv4_launch(kv_join_rows_kernel<Kv8AttnArgs, D, NT, 4>, (n + 3) / 4, 128, 0, st, a, sh, warps, (int)n);
     }
     if (rc != cudaSuccess) return CP_ECUDA;
     if (!a.mass) return CP_OK;
     // enough blocks to fill the device a few times; longer tables are walked
     const int64_t heads = (int64_t)a.rows.B * a.pool.Hkv, cap = (int64_t)a.pool.max_pages << a.pool.page_shift;
-    int64_t chunks = (cap + 255) / 256;
+    int64_t chunks = (cap + MASS_CHUNK - 1) / MASS_CHUNK;
     const int64_t enough = ((int64_t)sm_count() * 32 + heads - 1) / heads;
     if (chunks > enough) chunks = enough;
     if (chunks < 1) return CP_OK;
@@ -840,12 +863,13 @@ int launch(const Kv8AttnArgs &a, const Shape &sh, const CUtensorMap &map, cudaSt
 }  // namespace
 
 // The warps' parts, then the scores.
-size_t kv8_attn_workspace_bytes(int B, int n, int Hq, int D, int64_t slots, bool mass)
+size_t kv8_attn_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int64_t slots, bool mass)
 {
     if (D != 64 && D != 128) return 0;
     const size_t parts = (size_t)2 * MAX_ROWS * (D + 2) * sizeof(float);
     if (!mass) return parts;
-    const unsigned __int128 b = (unsigned __int128)(unsigned)B * (unsigned)n * (unsigned)Hq * (uint64_t)slots * 4u;
+    const int64_t rows = score_rows((int64_t)n * (Hq / Hkv));
+    const unsigned __int128 b = (unsigned __int128)(unsigned)B * (unsigned)Hkv * (uint64_t)rows * (uint64_t)slots * 4u;
     if (b > ((unsigned __int128)1 << 61)) return 0;
     return parts + (((size_t)b + 255) & ~(size_t)255);
 }

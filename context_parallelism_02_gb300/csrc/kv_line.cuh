@@ -261,11 +261,13 @@ __global__ void __launch_bounds__(JW * 32) kv_join_kernel(A a, Shape sh, int war
     const unsigned item = blockIdx.x / (unsigned)sh.rows, heads = sh.per_batch / sh.tiles;
     const int rr_all = (int)(blockIdx.x - item * sh.rows);
     const int b = (int)(item / heads), x = (int)(item - b * heads);   // x: (token, kv head)
-    kv4_trigger();
     // The lengths, and nothing else, are read before the wait: the attention kernel triggers
     // after its own, so this grid starts when what wrote them is complete.  The loads are
     // coherent at the GPU's scope: this SM may hold an older line of them.  (Behind the
-    // wait they cost a call 2 us: 131072 tokens 39.6 instead of 37.8.)
+    // wait they cost a call 2 us: 131072 tokens 39.6 instead of 37.8.)  The next kernel is let
+    // start behind the wait only: where the attention kernel fills the registers of the SMs,
+    // a next call's blocks took what this kernel's were waiting for (8-bit cache, 8 x 16384
+    // tokens, D = 64, 2 query heads a kv head: 42 us with the trigger first, 28 so).
     int64_t all, before;
     count_blocks(a, b, all, before);
     all *= sh.per_batch;
@@ -278,6 +280,7 @@ __global__ void __launch_bounds__(JW * 32) kv_join_kernel(A a, Shape sh, int war
     const int64_t f = before * sh.per_batch + (int64_t)i * (nb + Line<A>::PAD);
     const int c0 = cuts.at(f), c1 = cuts.at(f + nb - 1);
     kv4_wait();
+    kv4_trigger();
     if (c0 == c1) return;
     const float *ws = static_cast<const float *>(a.ws);
     float m = -INFINITY, l = 0.f;
@@ -342,6 +345,87 @@ __global__ void __launch_bounds__(JW * 32) kv_join_kernel(A a, Shape sh, int war
     if (a.out_f32) static_cast<float *>(a.out)[at] = r;
     else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(r);
     if (threadIdx.x == 0) a.lse[((int64_t)b * a.rows.Hq + head) * a.rows.n + j] = empty ? -INFINITY : fmaf(m, LN2, logf(l));
+}
+
+// The same by a warp per row, four rows a block, where a row has few pieces: the join is then
+// bound by how many of its blocks find room beside the attention kernel's before that ends
+// (64 ragged sequences up to 8192 tokens with a window of 1024, 2048 rows: 23 us with a block
+// a row, FIXME so).
+template <typename A, int D, int NT, int DEEP>
+__global__ void __launch_bounds__(128) kv_join_rows_kernel(A a, Shape sh, int warps, int rows)
+{
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int at_row = blockIdx.x * 4 + (threadIdx.x >> 5);
+    const bool there = at_row < rows;
+    const unsigned row_all = there ? (unsigned)at_row : 0u;
+    const unsigned item = row_all / (unsigned)sh.rows, heads = sh.per_batch / sh.tiles;
+    const int rr_all = (int)(row_all - item * sh.rows);
+    const int b = (int)(item / heads), x = (int)(item - b * heads);   // x: (token, kv head)
+    // as above: the lengths, and nothing else, before the wait
+    int64_t all, before;
+    count_blocks(a, b, all, before);
+    all *= sh.per_batch;
+    const Cuts cuts(all, warps, Line<A>::LEAST);
+    const int nb = Line<A>::template blocks<true>(a, b);
+    const int tile = rr_all / (NT * 8), row = rr_all % (NT * 8);
+    const int h = x % a.pool.Hkv, j0 = x / a.pool.Hkv;
+    const int i = (j0 * sh.tiles + tile) * a.pool.Hkv + h;
+    const int64_t f = before * sh.per_batch + (int64_t)i * (nb + Line<A>::PAD);
+    const int c0 = cuts.at(f), c1 = cuts.at(f + nb - 1);
+    kv4_wait();
+    kv4_trigger();
+    if (!there || c0 == c1) return;
+    const float *ws = static_cast<const float *>(a.ws);
+    float m = -INFINITY, l = 0.f;
+    float o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int c = c0; c <= c1; c += DEEP) {
+        float pm[DEEP], pl[DEEP], v[DEEP][E], mn = m;
+#pragma unroll
+        for (int u = 0; u < DEEP; ++u) {
+            pm[u] = -INFINITY;
+            pl[u] = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+            if (c + u > c1) continue;
+            const float *part = ws + (2 * (int64_t)(c + u) + (c + u == c0 ? 1 : 0)) * Part<D, NT>::FLOATS;
+            pm[u] = part[row];
+            pl[u] = part[8 * NT + row];
+            if (E == 4) {
+                const float4 w = *reinterpret_cast<const float4 *>(part + 16 * NT + row * D + lane * 4);
+                v[u][0] = w.x, v[u][1] = w.y, v[u][E - 2] = w.z, v[u][E - 1] = w.w;
+            } else {
+                const float2 w = *reinterpret_cast<const float2 *>(part + 16 * NT + row * D + lane * 2);
+                v[u][0] = w.x, v[u][1] = w.y;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < DEEP; ++u) mn = fmaxf(mn, pm[u]);
+        const float fa = m == mn ? 1.f : ex2(m - mn);
+        l *= fa;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= fa;
+#pragma unroll
+        for (int u = 0; u < DEEP; ++u) {
+            const float fu = pm[u] == mn ? 1.f : ex2(pm[u] - mn);
+            l = fmaf(pl[u], fu, l);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(v[u][e], fu, o[e]);
+        }
+        m = mn;
+    }
+    const int j = j0 + rr_all / sh.group, head = h * sh.group + rr_all % sh.group;
+    const bool empty = l == 0.f;
+    const float inv = empty ? 0.f : 1.f / l;
+    const int64_t at = (((int64_t)b * a.rows.n + j) * a.rows.Hq + head) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        if (a.out_f32) *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at + e) = make_float2(o[e] * inv, o[e + 1] * inv);
+        else *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + at + e) = tc::pack_bf16(o[e] * inv, o[e + 1] * inv);
+    }
+    if (lane == 0) a.lse[((int64_t)b * a.rows.Hq + head) * a.rows.n + j] = empty ? -INFINITY : fmaf(m, LN2, logf(l));
 }
 
 }  // namespace

@@ -606,8 +606,9 @@ int kv8_attn(const void *q, const void *cache, const float *scales, const int32_
              void *workspace, size_t ws_bytes, void *stream);
 
 /* kv8_attn_workspace -- bytes of scratch kv8_attn needs: a constant of D, and with mass (not
- * 0) the scores, B n Hq page max_pages fp32; 0 for sizes that are not built.  Host only. */
-size_t kv8_attn_workspace(int B, int n, int Hq, int D, int page, int max_pages, int mass);
+ * 0) the scores, fp32, of n Hq / Hkv rows (rounded up to a multiple of 4) per slot and kv
+ * head; 0 for sizes that are not built.  Host only. */
+size_t kv8_attn_workspace(int B, int n, int Hq, int Hkv, int D, int page, int max_pages, int mass);
 
 /*
  * kv8_evict -- the tokens with the largest mass into other pages.  Per sequence and kv head
