@@ -42,6 +42,7 @@
 #include "kernels.h"
 #include "tc_helpers.cuh"
 #include "tmem_io.cuh"
+#include "window_fix.cuh"
 #include "window_sinks.cuh"
 
 namespace cp {
@@ -112,6 +113,15 @@ __device__ __forceinline__ void ts_mn_seq(uint32_t tD, uint32_t tA, uint64_t dB,
 // 32 columns of the lane's row times f, as bf16, to 32-byte aligned memory: regrouped, so
 // that a store covers whole pieces of 64 bytes.  (Every lane its own row in 16 bytes took
 // the dK / dV epilogue of a unit 5500 cycles, as long as three of its half steps.)
+// NaN where one of 32 columns is not finite, else 0.
+__device__ __forceinline__ float odd_columns(const uint32_t (&o)[32])
+{
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) ffma2v(a, b, __uint_as_float(o[e]), __uint_as_float(o[e + 1]), 0.f, 0.f, a, b);
+    return a + b;
+}
+
 __device__ __forceinline__ void put_row_piece(__nv_bfloat16 *piece, bool ok, const uint32_t (&o)[32], float f, int lane)
 {
     uint32_t pk[16];
@@ -219,7 +229,8 @@ struct DqCfg {
     static constexpr int OFF_V = (1 + Q_KST) * TB;      // 2 stages
     static constexpr int OFF_BAR = (3 + Q_KST) * TB;
     static constexpr int OFF_MISC = OFF_BAR + 8 * Q_NBAR;
-    static constexpr int NEED = OFF_MISC + 16;
+    static constexpr int OFF_FIX = OFF_MISC + 16;       // WIN: FixList
+    static constexpr int NEED = OFF_FIX + (int)sizeof(FixList);
     static constexpr int SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
     static_assert(SMEM <= 232448, "dQ kernel shared memory");
     static constexpr uint32_t TM_S = 0, TM_P = 128, TM_DQ = 256, TM_DS = 256 + D, TM_DO = 320 + D;
@@ -253,6 +264,7 @@ struct BwdArgs {
     float *part;         // the sinks' partial gradients (window_sinks.cuh)
     int n_units;         // windowed attention: units of the launch
     FastDiv by_tiles, by_heads, by_group;   // of its numbering: tiles, heads (query or kv), Hq / Hkv
+    FixArgs fix;         // windowed attention
 };
 
 // WIN: windowed attention with sinks, the walks of WinIter and WinQIter.  The dQ
@@ -268,11 +280,47 @@ struct PackMaps {
 struct NoMaps {
 };
 
+// WIN: the block's u-th unit; false: it has no more.
+__device__ __forceinline__ bool window_q_unit(const BwdArgs &a, int u, Unit &w)
+{
+    const int64_t item = blockIdx.x + (int64_t)u * gridDim.x;
+    if (item >= a.n_units) return false;
+    const unsigned r = a.by_tiles.div((unsigned)item), t = (unsigned)item - r * (unsigned)a.upc;
+    w.b = (int)a.by_heads.div(r);
+    w.h = (int)r - w.b * a.Hq;
+    w.r = 0;
+    w.q0 = (int)t * T;
+    w.cend = a.S;
+    w.qmax = (w.q0 + T < a.S ? w.q0 + T : a.S) - 1;
+    return true;
+}
+
+// WIN: the noted rows again (window_fix.cuh), by the gradient warps.
+template <int D>
+__device__ __noinline__ void dq_fix(const FixList &list, const BwdArgs &a, __nv_bfloat16 *dq)
+{
+    const int warp = (threadIdx.x >> 5) - 4;
+    auto task = [&](const Unit &w, int quarter) {
+        for (int r = 0; r < 32; ++r) {
+            const int i = w.q0 + 32 * quarter + r;
+            if (i < w.cend) fix::dq_row<D>(a.fix, w.b, w.h, i, dq);
+        }
+    };
+    Unit w;
+    if (list.count <= FixList::CAP) {
+        for (int e = warp; e < list.count; e += 8)
+            if (window_q_unit(a, list.entry[e] >> 3, w)) task(w, list.entry[e] & 3);
+    } else {
+        for (int u = 0; window_q_unit(a, u, w); ++u)
+            if (warp < 4) task(w, warp);
+    }
+}
+
 template <int D, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
-                  const BwdArgs a, const float *__restrict__ lse,
+                  const __grid_constant__ BwdArgs a, const float *__restrict__ lse,
                   const float *__restrict__ delta, __nv_bfloat16 *__restrict__ dq,
                   const __nv_bfloat16 *__restrict__ dout,
                   const __grid_constant__ std::conditional_t<WIN, PackMaps, NoMaps> pm)
@@ -291,6 +339,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #define BAR(i) (bar0 + 8u * (uint32_t)(i))
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem_raw + C::OFF_MISC + 4);
+    FixList *fixes = reinterpret_cast<FixList *>(smem_raw + C::OFF_FIX);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Geom g = make_geom(a.S, a.N, a.layout, a.causal);
@@ -301,15 +350,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // the block's it-th unit; false: it has no more
     auto unit_of = [&](int it, Item &x) -> bool {
         if constexpr (WIN) {
-            const int64_t item = blockIdx.x + (int64_t)it * gridDim.x;
-            if (item >= a.n_units) return false;
-            const unsigned r = a.by_tiles.div((unsigned)item), t = (unsigned)item - r * (unsigned)a.upc;
-            x.w.b = (int)a.by_heads.div(r);
-            x.w.h = (int)r - x.w.b * a.Hq;
-            x.w.r = 0;
-            x.w.q0 = (int)t * T;
-            x.w.cend = a.S;
-            x.w.qmax = (x.w.q0 + T < a.S ? x.w.q0 + T : a.S) - 1;
+            if (!window_q_unit(a, it, x.w)) return false;
             x.kvh = (int)a.by_group.div((unsigned)x.w.h);
             x.n = WinIter<T>::count(a.win, x.w.q0 + a.win.off, x.w.qmax + a.win.off);
         } else {
@@ -371,6 +412,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         mbar_init(BAR(Q_DRAIN), 2);
         mbar_init(BAR(Q_QEMPTY), 1);
         *abort_flag = 0;
+        if constexpr (WIN) fixes->count = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -708,12 +750,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 // each half writes D/2 columns of dQ = scale * acc
                 constexpr int HD = D / 2;
                 const bool a32 = (reinterpret_cast<uintptr_t>(dq) & 31) == 0;
+                float odd = 0.f;
                 __nv_bfloat16 *orow = dq + (((int64_t)w.b * a.S + qp) * a.Hq + w.h) * D + HD * half;
 #pragma unroll (WIN ? 1 : HD / 32)
                 for (int c = 0; c < HD / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld_x32(tDQ + HD * half + 32u * c, o);
                     if constexpr (WIN) {
+                        odd += odd_columns(o);
                         if (a32) {
                             put_row_piece(orow + 32 * c, valid, o, a.scale, lane);
                             continue;
@@ -732,11 +776,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         }
                     }
                 }
+                if constexpr (WIN) {
+                    if (__any_sync(0xffffffffu, valid && !(odd == 0.f)) && lane == 0) fixes->note(u, quarter);
+                }
             }
         }
         __syncwarp();
         tc_fence_before();
         asm volatile("barrier.sync 1, %0;" ::"n"(NTHREADS) : "memory");
+        if constexpr (WIN) {
+            if (fixes->count > 0) dq_fix<D>(*fixes, a, dq);
+        }
         return;
     }
 #undef BAR
@@ -793,18 +843,108 @@ struct DkvCfg {
     static constexpr int OFF_STAT = OFF_Q + K_QST * STAGE;   // K_QST x (lse2[64], delta[64]) fp32
     static constexpr int OFF_BAR = OFF_STAT + K_QST * 2 * 64 * 4;
     static constexpr int OFF_MISC = OFF_BAR + 8 * K_NBAR;
-    static constexpr int NEED = OFF_MISC + 16;
+    static constexpr int OFF_FIX = OFF_MISC + 16;            // WIN: FixList
+    static constexpr int NEED = OFF_FIX + (int)sizeof(FixList);
     static constexpr int SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
     static_assert(SMEM <= 232448, "dK/dV kernel shared memory");
     static constexpr uint32_t TM_DV = 256, TM_DK = 256 + D;
     static_assert(TM_DK + D <= 512, "dK/dV kernel tensor memory");
 };
 
+// Where key row j's gradient goes: dK's (k) or dV's row, or a sink's partial.
+template <int D>
+__device__ __forceinline__ float *partial_row(const BwdArgs &a, int b, int g, int piece, int j, bool k)
+{
+    if (a.sp.pieces == 0 || j >= a.win.sinks) return nullptr;
+    return a.part + (((int64_t)b * a.Hkv + g) * window_part_rows(a.win, a.sp) + ((int64_t)piece * 2 + (k ? 0 : 1)) * a.win.sinks + j) * D;
+}
+
+// WIN: the block's u-th unit and its piece (0: a window unit, else 1 + the piece of a tile of
+// sinks); false: it has no more.
+__device__ __forceinline__ bool window_kv_unit(const BwdArgs &a, int u, KvUnit &w, int &piece)
+{
+    const int64_t item = blockIdx.x + (int64_t)u * gridDim.x;
+    if (item >= a.n_units) return false;
+    const int windows = a.tpc * a.B * a.Hkv;
+    unsigned t, r;
+    if (item < windows) {
+        piece = 0;
+        r = a.by_tiles.div((unsigned)item);
+        t = (unsigned)item - r * (unsigned)a.tpc;
+    } else {
+        const unsigned y = (unsigned)(item - windows), z = y / (unsigned)a.sp.pieces;
+        piece = 1 + (int)(y - z * (unsigned)a.sp.pieces);
+        r = z / (unsigned)a.sp.tiles;
+        t = z - r * (unsigned)a.sp.tiles;
+    }
+    w.b = (int)a.by_heads.div(r);
+    w.g = (int)r - w.b * a.Hkv;
+    w.src = 0;
+    w.ks = (int)t * T;
+    w.kcend = a.Sk;
+    w.kl = a.Sk - w.ks < T ? a.Sk - w.ks : T;
+    return true;
+}
+
+// WIN: the noted rows again (window_fix.cuh), by the gradient warps: warps 0 to 3 of a unit
+// wrote dV, 4 to 7 dK.
+template <int D>
+__device__ __noinline__ void dkdv_fix(const FixList &list, const BwdArgs &a, __nv_bfloat16 *dk, __nv_bfloat16 *dv)
+{
+    const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31, grp = a.Hq / a.Hkv;
+    auto task = [&](const KvUnit &w, int piece, int which) {
+        const bool k = which >= 4;
+        for (int r = 0; r < 32; ++r) {
+            const int row = 32 * (which & 3) + r, j = w.ks + row;
+            if (row >= w.kl) return;
+            float *prow = partial_row<D>(a, w.b, w.g, piece, j, k);
+            if (!prow && piece != 0) continue;
+            __nv_bfloat16 *brow = (k ? dk : dv) + (((int64_t)w.b * a.Sk + j) * a.Hkv + w.g) * D;
+            fix::Piece<D> acc{};
+            if (prow) {
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) acc.x[e] = prow[2 * lane + 64 * (e >> 1) + (e & 1)];
+            } else {
+                acc = fix::load<D>(brow, lane);
+            }
+            if (fix::finite(acc)) continue;
+            acc = fix::Piece<D>{};
+            if (piece == 0) {
+                const int i0 = j - a.win.off > 0 ? j - a.win.off : 0;
+                const int64_t i1 = (int64_t)j - a.win.off + a.win.window;
+                for (int h = 0; h < grp; ++h)
+                    fix::key_rows<D>(a.fix, w.b, w.g * grp + h, j, i0, (int)(i1 < a.S ? i1 : a.S), k, acc);
+            } else {
+                WinQIter<T> it;
+                for (it.sinks(a.win, a.S, w.ks, w.g * grp, grp, piece - 1, a.sp.each); it.count() > 0; it.next()) {
+                    const int64_t from = (int64_t)j + a.win.window - a.win.off;   // the first row behind the window
+                    const int i0 = from > it.start() ? (from < a.S ? (int)from : a.S) : it.start();
+                    fix::key_rows<D>(a.fix, w.b, it.head(), j, i0, it.start() + it.len(), k, acc);
+                }
+            }
+            if (prow) {
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) prow[2 * lane + 64 * (e >> 1) + (e & 1)] = acc.x[e];
+            } else {
+                fix::store(brow, acc, 1.f, lane);
+            }
+        }
+    };
+    KvUnit w;
+    int piece = 0;
+    if (list.count <= FixList::CAP) {
+        for (int e = warp; e < list.count; e += 8)
+            if (window_kv_unit(a, list.entry[e] >> 3, w, piece)) task(w, piece, list.entry[e] & 7);
+    } else {
+        for (int u = 0; window_kv_unit(a, u, w, piece); ++u) task(w, piece, warp);
+    }
+}
+
 template <int D, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQh, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDOh,
-                    const BwdArgs a, const float *__restrict__ lse, const float *__restrict__ delta,
+                    const __grid_constant__ BwdArgs a, const float *__restrict__ lse, const float *__restrict__ delta,
                     __nv_bfloat16 *__restrict__ dk, __nv_bfloat16 *__restrict__ dv)
 {
     using C = DkvCfg<D>;
@@ -821,6 +961,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #define BAR(i) (bar0 + 8u * (uint32_t)(i))
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem_raw + C::OFF_MISC + 4);
+    FixList *fixes = reinterpret_cast<FixList *>(smem_raw + C::OFF_FIX);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grp = a.Hq / a.Hkv;
@@ -840,25 +981,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     auto unit_of = [&](int it, Item &x) -> bool {
         x.piece = 0;
         if constexpr (WIN) {
-            const int64_t item = blockIdx.x + (int64_t)it * gridDim.x;
-            if (item >= a.n_units) return false;
-            const int windows = a.tpc * a.B * a.Hkv;
-            unsigned t, r;
-            if (item < windows) {
-                r = a.by_tiles.div((unsigned)item);
-                t = (unsigned)item - r * (unsigned)a.tpc;
-            } else {
-                const unsigned y = (unsigned)(item - windows), z = y / (unsigned)a.sp.pieces;
-                x.piece = 1 + (int)(y - z * (unsigned)a.sp.pieces);
-                r = z / (unsigned)a.sp.tiles;
-                t = z - r * (unsigned)a.sp.tiles;
-            }
-            x.w.b = (int)a.by_heads.div(r);
-            x.w.g = (int)r - x.w.b * a.Hkv;
-            x.w.src = 0;
-            x.w.ks = (int)t * T;
-            x.w.kcend = a.Sk;
-            x.w.kl = a.Sk - x.w.ks < T ? a.Sk - x.w.ks : T;
+            if (!window_kv_unit(a, it, x.w, x.piece)) return false;
             Walk wk;
             start_walk(wk, x);
             x.ns = 2 * wk.count();
@@ -891,6 +1014,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         mbar_init(BAR(K_KVEMPTY), 2);
         mbar_init(BAR(K_ACC), 4);
         *abort_flag = 0;
+        if constexpr (WIN) fixes->count = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -1219,12 +1343,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                                      : dbg_coord(a.err, valid ? slot_pos(g, kpos) : 0, a.S);
                 __nv_bfloat16 *orow = (half ? dk : dv) + (((int64_t)w.b * (WIN ? a.Sk : a.S) + krow) * a.Hkv + w.g) * D;
                 float *prow = nullptr;   // WIN: a sink's partial gradient
+                float odd = 0.f;         // WIN: NaN where an element is not finite
                 if constexpr (WIN) {
-                    const bool sink = valid && a.sp.pieces > 0 && kpos < a.win.sinks;
-                    if (sink)
-                        prow = a.part + (((int64_t)w.b * a.Hkv + w.g) * window_part_rows(a.win, a.sp) +
-                                         ((int64_t)piece * 2 + (half ? 0 : 1)) * a.win.sinks + kpos) * D;
-                    valid = valid && !sink && piece == 0;
+                    if (valid) prow = partial_row<D>(a, w.b, w.g, piece, kpos, half != 0);
+                    valid = valid && !prow && piece == 0;
                 }
 #pragma unroll (WIN ? 1 : D / 32)
                 for (int c = 0; c < D / 32; ++c) {
@@ -1244,6 +1366,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         }
                     }
                     if constexpr (WIN) {
+                        odd += odd_columns(o);
                         if (a32) {
                             put_row_piece(orow + 32 * c, valid, o, f, lane);
                             continue;
@@ -1262,6 +1385,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         }
                     }
                 }
+                if constexpr (WIN) {
+                    if (__any_sync(0xffffffffu, (valid || prow) && !(odd == 0.f)) && lane == 0) fixes->note(u, half * 4 + quarter);
+                }
             }
             if (WIN && ns > 0) {   // the accumulators may be overwritten
                 tc_fence_before();
@@ -1273,6 +1399,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
         tc_fence_before();
         asm volatile("barrier.sync 1, %0;" ::"n"(NTHREADS) : "memory");
+        if constexpr (WIN) {
+            if (fixes->count > 0) dkdv_fix<D>(*fixes, a, dk, dv);
+        }
         return;
     }
 #undef BAR
@@ -1329,6 +1458,9 @@ int launch_window_d(const BwdPtrs &p, BwdArgs a, cudaStream_t st)
     const int64_t most = cap > 0 && cap < sms ? cap : sms;
     float *delta = static_cast<float *>(p.workspace);
     a.part = delta + bwd_workspace_bytes(a.B, a.Hq, a.S) / 4;
+    a.fix = FixArgs{static_cast<const __nv_bfloat16 *>(p.q), static_cast<const __nv_bfloat16 *>(p.k),
+                    static_cast<const __nv_bfloat16 *>(p.v), static_cast<const __nv_bfloat16 *>(p.out),
+                    static_cast<const __nv_bfloat16 *>(p.dout), p.lse, delta, a.S, a.Sk, a.Hq, a.Hkv, a.scale, a.win};
     __nv_bfloat16 *dk = static_cast<__nv_bfloat16 *>(p.dk), *dv = static_cast<__nv_bfloat16 *>(p.dv);
     a.n_units = (int)qunits;
     a.by_tiles = fast_div((uint32_t)a.upc);
@@ -1428,6 +1560,7 @@ BwdArgs bwd_args(const FwdArgs &f)
     a.part = nullptr;
     a.n_units = 0;
     a.by_tiles = a.by_heads = a.by_group = fast_div(1);
+    a.fix = FixArgs{};
     return a;
 }
 

@@ -59,6 +59,7 @@
 #include "kernels.h"
 #include "tc_helpers.cuh"
 #include "tmem_io.cuh"
+#include "window_fix.cuh"
 
 namespace cp {
 
@@ -107,7 +108,8 @@ struct Cfg {
     static constexpr int OFF_PM = OFF_V + 2 * VBYTES;  // row-max exchange: [2][2][128] fp32
     static constexpr int OFF_BAR = OFF_PM + 2 * 2 * 128 * 4;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-    static constexpr int SMEM_NEED = OFF_MISC + 16;
+    static constexpr int OFF_FIX = OFF_MISC + 16;      // MODE_WINDOW: FixList
+    static constexpr int SMEM_NEED = OFF_FIX + (int)sizeof(FixList);
     // at least 120 KB so that one block owns the SM and its 512 TMEM columns
     static constexpr int SMEM = SMEM_NEED > 120 * 1024 ? SMEM_NEED : 120 * 1024;
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -171,13 +173,52 @@ struct NoMaps {
 template <int MODE>
 using ModeMaps = std::conditional_t<MODE == MODE_WINDOW, PackMaps, NoMaps>;
 
+// MODE_WINDOW's items: heads fastest, then batch, rows descending; a block takes rounds of
+// gridDim.x items, alternately forwards and backwards.  False: the block has no it-th item.
+__device__ __forceinline__ bool window_unit(const FwdArgs &a, int it, Unit &w)
+{
+    const int64_t G = gridDim.x, c = blockIdx.x, item = it * G + ((it & 1) ? G - 1 - c : c);
+    if (item >= a.n_units) return false;
+    const unsigned r = a.by_heads.div((unsigned)item), t = a.by_batch.div(r);
+    w.h = (int)((unsigned)item - r * (unsigned)a.Hq);
+    w.b = (int)(r - t * (unsigned)a.B);
+    w.r = 0;
+    w.q0 = (a.upc - 1 - (int)t) * QT;
+    w.cend = a.S;
+    w.qmax = (w.q0 + QT < a.S ? w.q0 + QT : a.S) - 1;
+    return true;
+}
+
+// MODE_WINDOW: the noted rows of the block's units again (window_fix.cuh), by its softmax warps.
+template <int D>
+__device__ __noinline__ void window_fix(const FixList &list, const FwdArgs &a, __nv_bfloat16 *out, const float *lse)
+{
+    const int warp = (threadIdx.x >> 5) - 4;
+    const FixArgs f{static_cast<const __nv_bfloat16 *>(a.q), static_cast<const __nv_bfloat16 *>(a.k),
+                    static_cast<const __nv_bfloat16 *>(a.v), out, nullptr, lse, nullptr, a.S, a.Sk, a.Hq, a.Hkv, a.scale, a.win};
+    auto task = [&](const Unit &w, int quarter) {
+        for (int r = 0; r < 32; ++r) {
+            const int i = w.q0 + 32 * quarter + r;
+            if (i < w.cend) fix::out_row<D>(f, w.b, w.h, i, out);
+        }
+    };
+    Unit w;
+    if (list.count <= FixList::CAP) {
+        for (int e = warp; e < list.count; e += 8)
+            if (window_unit(a, list.entry[e] >> 3, w)) task(w, list.entry[e] & 3);
+    } else {
+        for (int u = 0; window_unit(a, u, w); ++u)
+            if (warp < 4) task(w, warp);
+    }
+}
+
 // PERSIST: the block runs several work items in turn (fewer blocks than
 // items); otherwise it runs item blockIdx.x alone and its item loops run once,
 // so every running count below folds to the per-unit index.
 template <int D, int MODE, bool PERSIST>
 __global__ void __launch_bounds__(NTHREADS, 1)
     fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const FwdArgs a, const float sl2,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdArgs a, const float sl2,
                     __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, const SplitOut so,
                     const StepOut stp, const __grid_constant__ ModeMaps<MODE> pm_maps)
 {
@@ -199,6 +240,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #define BAR(i) (bar0 + 8u * (uint32_t)(i))
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + C::OFF_MISC + 4);
+    FixList *fixes = reinterpret_cast<FixList *>(gbase + C::OFF_FIX);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Geom g = make_geom(a.S, a.N, a.layout, a.causal);
@@ -225,6 +267,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // numbering, so the blocks' totals stay close.  With one block per item
     // (gridDim.x == n_items) the block runs item blockIdx.x alone.
     auto item_of = [&](int it) -> int {
+        if constexpr (WIN)   // decode() takes the block's number of the item
+            return (int64_t)it * gridDim.x + ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x) < n_items ? it : n_items;
         if (!PERSIST) return it == 0 ? (int)blockIdx.x : n_items;
         const int64_t G = gridDim.x, c = blockIdx.x;
         const int64_t item = it * G + ((it & 1) ? G - 1 - c : c);
@@ -236,14 +280,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     };
     auto decode = [&](int item) -> Item {
         Item x;
-        if constexpr (WIN) {   // heads fastest, then batch, rows descending
-            const unsigned r = a.by_heads.div((unsigned)item), t = a.by_batch.div(r);
-            x.w.h = item - (int)r * a.Hq;
-            x.w.b = (int)r - (int)t * a.B;
-            x.w.r = 0;
-            x.w.q0 = (a.upc - 1 - (int)t) * QT;
-            x.w.cend = a.S;
-            x.w.qmax = (x.w.q0 + QT < a.S ? x.w.q0 + QT : a.S) - 1;
+        if constexpr (WIN) {   // item: the block's number of it
+            window_unit(a, item, x.w);
             x.kvh = (int)a.by_group.div((unsigned)x.w.h);
             x.sp = x.j0 = 0;
             x.n = WinIter<KT>::count(a.win, x.w.q0 + a.win.off, x.w.qmax + a.win.off);
@@ -289,6 +327,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         mbar_init(BAR(B_DRAIN), 2);
         mbar_init(BAR(B_MX), 8);
         *abort_flag = 0;
+        if constexpr (WIN) fixes->count = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -559,12 +598,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // MODE_WINDOW: a unit's output waits until the next unit's first P is computed, so that
         // the unit's last PV, and then this epilogue, run beside the next unit's first products.
         bool pend = false, p_valid = false;
-        float p_m = 0.f, p_l = 0.f;   // the unit's reference and row sum
+        int p_it = 0;                 // the unit's number in the block
+        float p_m = 0.f, p_l = 0.f;   // its reference and row sum
         __nv_bfloat16 *p_row = nullptr;
         float *p_lse = nullptr;
         auto put_unit = [&]() {
             const float inv = p_l > 0.f ? 1.f / p_l : 0.f;
             const bool a32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+            uint32_t top = 0;                       // largest magnitudes of the even and the odd columns
 #pragma unroll 1
             for (int pc = 0; pc < D / 64; ++pc) {   // 32 columns at a time: P's registers are live here
                 uint32_t o[32], pk[16];
@@ -572,6 +613,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     pk[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = __vmaxu2(top, pk[e] & 0x7fff7fffu);
                 if (a32) {
                     store_warp_rows<16>(p_row + 32 * pc, p_valid, pk, lane);
                 } else if (p_valid) {
@@ -582,6 +625,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
             }
             if (p_valid && half == 0) *p_lse = p_l > 0.f ? (p_m + lg2(p_l)) * 0.69314718055994531f : NEG_INF;
+            const bool odd = p_valid && ((top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u);
+            if (__any_sync(0xffffffffu, odd) && lane == 0) fixes->note(p_it, quarter);
             pend = false;
         };
 
@@ -812,6 +857,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 if (lane == 0) mbar_arrive(BAR(B_MX));
                 ++nx;
                 pend = true;
+                p_it = it;
                 p_m = m_run;
                 p_valid = valid;
                 const int r = dbg_coord(a.err, valid ? qpos : 0, a.S);
@@ -1016,6 +1062,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
         tc_fence_before();
         asm volatile("barrier.sync 1, %0;" ::"n"(NTHREADS) : "memory");
+        if constexpr (WIN) {
+            if (fixes->count > 0) window_fix<D>(*fixes, a, out, lse);
+        }
         return;
     }
 #undef BAR
@@ -1131,6 +1180,9 @@ int launch_window_d(const void *q, const void *k, const void *v, void *out, floa
     a.by_heads = fast_div((uint32_t)a.Hq);
     a.by_batch = fast_div((uint32_t)a.B);
     a.by_group = fast_div((uint32_t)(a.Hq / a.Hkv));
+    a.q = q;
+    a.k = k;
+    a.v = v;
     int64_t blocks = sm_count();
     const int cap = fwd_grid_limit();   // test hook
     if (cap > 0) blocks = cap;

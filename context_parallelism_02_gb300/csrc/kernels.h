@@ -24,6 +24,7 @@ struct FwdArgs {
     int Sk;               // windowed attention: keys (S counts query rows)
     Window win;           // windowed attention
     FastDiv by_heads, by_batch, by_group;   // windowed attention: Hq, B, Hq / Hkv (set by the launcher)
+    const void *q, *k, *v;                  // windowed attention (set by the launcher)
 };
 
 // Partial results of a split forward (fp32, normalised): n splits of every

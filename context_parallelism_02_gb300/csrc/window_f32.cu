@@ -48,16 +48,20 @@ struct Args {
 };
 
 // n rows of x [B][S][H][D] (head h, from row r0) into COUNT rows of shared memory, the rest 0.
+// Returns NaN if one of the thread's elements is not finite, else 0.
 template <int D, int COUNT>
-__device__ __forceinline__ void load_rows(float *dst, const float *x, int64_t b, int S, int H, int h, int r0, int n)
+__device__ __forceinline__ float load_rows(float *dst, const float *x, int64_t b, int S, int H, int h, int r0, int n)
 {
+    float odd = 0.f;
 #pragma unroll 8
     for (int i = threadIdx.x; i < COUNT * (D / 4); i += THREADS) {
         const int r = i / (D / 4), c = i % (D / 4);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < n) v = *reinterpret_cast<const float4 *>(x + ((b * S + r0 + r) * H + h) * D + c * 4);
         *reinterpret_cast<float4 *>(dst + r * Rows<D>::STRIDE + c * 4) = v;
+        odd = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, fmaf(v.w, 0.f, odd))));
     }
+    return odd;
 }
 
 // acc[i][j] = A[ty + 8 i] . B[tx + 16 j]
@@ -89,10 +93,30 @@ __device__ __forceinline__ void dots(const float *A, const float *B, float (&acc
     }
 }
 
-// acc[i][4 j + e] += sum_k P[ty + 8 i][k] B[k][4 tx + 64 j + e]
+// acc[i][4 j + e] += sum_k P[ty + 8 i][k] B[k][4 tx + 64 j + e].  `odd`: B holds values that are
+// not finite, which a weight of 0 (what the mask hides) must not carry into the sums.
 template <int D>
-__device__ __forceinline__ void product(const float *P, const float *B, float (&acc)[4][D / 16])
+__device__ __forceinline__ void product(const float *P, const float *B, bool odd, float (&acc)[4][D / 16])
 {
+    if (odd) {
+        const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 1
+        for (int k = 0; k < T; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float p = P[(ty + 8 * i) * PS + k];
+                if (p == 0.f) continue;
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) {
+                    const float4 b = *reinterpret_cast<const float4 *>(B + k * Rows<D>::STRIDE + 4 * tx + 64 * j);
+                    acc[i][4 * j + 0] = fmaf(p, b.x, acc[i][4 * j + 0]);
+                    acc[i][4 * j + 1] = fmaf(p, b.y, acc[i][4 * j + 1]);
+                    acc[i][4 * j + 2] = fmaf(p, b.z, acc[i][4 * j + 2]);
+                    acc[i][4 * j + 3] = fmaf(p, b.w, acc[i][4 * j + 3]);
+                }
+            }
+        return;
+    }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll 2
     for (int k = 0; k < T; k += 4) {
@@ -159,9 +183,9 @@ struct QUnit {
 
 // Rows of K or V for the walk's current tile.  No packed tiles here (win.pack is 0).
 template <int D>
-__device__ __forceinline__ void load_keys(float *dst, const float *x, const Args &a, const QUnit &u, const WinIter<T> &it)
+__device__ __forceinline__ float load_keys(float *dst, const float *x, const Args &a, const QUnit &u, const WinIter<T> &it)
 {
-    load_rows<D, T>(dst, x, u.b, a.Sk, a.Hkv, u.kvh, it.start(), it.len());
+    return load_rows<D, T>(dst, x, u.b, a.Sk, a.Hkv, u.kvh, it.start(), it.len());
 }
 
 template <int D>
@@ -186,8 +210,8 @@ __global__ void __launch_bounds__(THREADS) window_f32_fwd_kernel(const Args a, f
     for (it.begin(a.win, p0, p1); it.valid(); it.next()) {
         __syncthreads();
         load_keys<D>(K, a.k, a, u, it);
-        load_keys<D>(V, a.v, a, u, it);
-        __syncthreads();
+        const float odd_v = load_keys<D>(V, a.v, a, u, it);
+        const bool odd = __syncthreads_or(odd_v != odd_v);
         float x[4][4];
         dots<D>(Q, K, x);
         const bool full = it.full(a.win, p0, p1);
@@ -205,7 +229,8 @@ __global__ void __launch_bounds__(THREADS) window_f32_fwd_kernel(const Args a, f
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                x[i][j] = exp2f(x[i][j] - base);
+                // (a visible weight is never 0: product() skips those)
+                x[i][j] = x[i][j] == -INFINITY ? 0.f : fmaxf(exp2f(x[i][j] - base), 1e-45f);
                 sum += x[i][j];
                 P[(ty + 8 * i) * PS + tx + 16 * j] = x[i][j];
             }
@@ -215,7 +240,7 @@ __global__ void __launch_bounds__(THREADS) window_f32_fwd_kernel(const Args a, f
             for (int j = 0; j < D / 16; ++j) o[i][j] *= f;
         }
         __syncthreads();
-        product<D>(P, V, o);
+        product<D>(P, V, odd, o);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -272,9 +297,9 @@ __global__ void __launch_bounds__(THREADS) window_f32_dq_kernel(const Args a, fl
     WinIter<T> it;
     for (it.begin(a.win, p0, p1); it.valid(); it.next()) {
         __syncthreads();
-        load_keys<D>(K, a.k, a, u, it);
+        const float odd_k = load_keys<D>(K, a.k, a, u, it);
         load_keys<D>(V, a.v, a, u, it);
-        __syncthreads();
+        const bool odd = __syncthreads_or(odd_k != odd_k);
         float x[4][4], g[4][4];
         dots<D>(Q, K, x);
         dots<D>(G, V, g);
@@ -289,7 +314,7 @@ __global__ void __launch_bounds__(THREADS) window_f32_dq_kernel(const Args a, fl
             }
         }
         __syncthreads();
-        product<D>(P, K, acc);
+        product<D>(P, K, odd, acc);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -345,14 +370,14 @@ __global__ void __launch_bounds__(THREADS) window_f32_dkdv_kernel(const Args a, 
     for (; it.count() > 0; it.next()) {
         const int h = it.head(), qa = it.start(), ql = it.len();
         __syncthreads();
-        load_rows<D, T>(Q, a.q, b, a.Sq, a.Hq, h, qa, ql);
-        load_rows<D, T>(G, a.dout, b, a.Sq, a.Hq, h, qa, ql);
+        const float odd_q = load_rows<D, T>(Q, a.q, b, a.Sq, a.Hq, h, qa, ql) +
+                            load_rows<D, T>(G, a.dout, b, a.Sq, a.Hq, h, qa, ql);
         if (threadIdx.x < T) {
             const int64_t at = ((int64_t)b * a.Hq + h) * a.Sq + qa + threadIdx.x;
             lse2[threadIdx.x] = threadIdx.x < ql ? a.lse[at] * LOG2E : 0.f;
             delta[threadIdx.x] = threadIdx.x < ql ? a.delta[at] : 0.f;
         }
-        __syncthreads();
+        const bool odd = __syncthreads_or(odd_q != odd_q);
         float s[4][4], g[4][4];
         dots<D>(K, Q, s);
         dots<D>(V, G, g);
@@ -370,8 +395,8 @@ __global__ void __launch_bounds__(THREADS) window_f32_dkdv_kernel(const Args a, 
             }
         }
         __syncthreads();
-        product<D>(P, G, adv);
-        product<D>(S, Q, adk);
+        product<D>(P, G, odd, adv);
+        product<D>(S, Q, odd, adk);
     }
     // the cluster's shares: each block leaves its own in shared memory (dK in Q's place, dV in
     // G's), and block `rank` adds up its part of the rows over the blocks in order

@@ -371,6 +371,8 @@ int ring_attn_bwd_noalloc(const void *q, const void *k, const void *v, const voi
  *   CP_BF16 runs on the tensor cores (bf16 operands and weights, fp32 accumulation),
  *   CP_F32 on the CUDA cores in fp32 arithmetic.
  * Work goes with the visible pairs: tiles that no row of a query tile sees are not read.
+ * What a row does not see has no influence on it, also where k and v hold NaN or infinities
+ * there (rows whose tiles meet such a value are computed a second time, slowly).
  * Errors: CP_EINVAL (null pointer, misalignment, Sq > Sk, window, sinks, Hq % Hkv),
  * CP_EUNSUPPORTED (D, dtype, Sk beyond 2^31 - 1025), CP_ECUDA.
  */
@@ -382,7 +384,8 @@ int window_attn_fwd(const void *q, const void *k, const void *v, void *out, floa
  * window_attn_bwd -- gradients of L = sum(dout * out) for window_attn_fwd: the formulas of
  * ring_attn_bwd over the visible pairs, with the forward's lse.
  *   q, out, dout, dq [B][Sq][Hq][D]; k, v, dk, dv [B][Sk][Hkv][D]; lse [B][Hq][Sq].
- *   Every element of dq, dk and dv is written (0 for keys that no row sees).
+ *   Every element of dq, dk and dv is written (0 for keys that no row sees).  NaN and
+ *   infinities in rows reach the gradients of what these rows see, and no others.
  *   workspace: device, window_attn_bwd_workspace(...) bytes, 16-byte aligned, contents
  *   irrelevant; calls that may overlap on the GPU need their own.
  * No atomics: results repeat bit for bit.

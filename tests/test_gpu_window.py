@@ -274,3 +274,72 @@ def test_backward_with_many_units_of_one_block(cuda_dev, shape):
     finally:
         api.cp_debug_set_grid_limit(0)
     assert all(torch.equal(a, b) for a, b in zip(plain, few))
+
+
+BADS = [float("nan"), float("inf")]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bad", BADS)
+@pytest.mark.parametrize("shape", [(1, 200, 700, 2, 1, 64, 100, 4), (2, 300, 900, 4, 2, 128, 130, 70), (1, 129, 500, 2, 2, 128, 1, 0)])
+def test_keys_that_no_row_sees_may_hold_anything(cuda_dev, shape, dtype, bad):
+    """A chunk whose earlier rows, outside windows and sinks, are not finite."""
+    B, Sq, Sk, Hq, Hkv, D, W, K = shape
+    q, k, v, do = make(shape, dtype, cuda_dev)
+    unseen = ~ref.visible(Sq, Sk, W, K, cuda_dev).any(0)
+    assert unseen.sum() > 100
+    clean = [t.masked_fill(unseen[None, :, None, None], 0) for t in (k, v)]
+    for which in (0, 1, 2):
+        kk, vv = (t.clone() for t in clean)
+        if which != 1:
+            kk[:, unseen] = bad
+        if which != 0:
+            vv[:, unseen] = -bad
+        out, lse = api.window_attn_fwd(q, kk, vv, W, K)
+        grads = api.window_attn_bwd(q, kk, vv, out, lse, do, W, K)
+        assert api.cp_get_error() == 0
+        o, z, eo, ez = ref.forward(q, *clean, W, K, None, UNIT[dtype])
+        ref.within(out, o, eo, "out")
+        ref.within(lse, z, ez, "lse")
+        want, err = ref.backward(q, *clean, do, W, K, None, UNIT[dtype])
+        for name, x, y, e in zip(("dq", "dk", "dv"), grads, want, err):
+            ref.within(x, y, e, name)
+        assert not grads[1][:, unseen].any() and not grads[2][:, unseen].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bad", BADS)
+def test_padding_behind_the_rows_may_hold_anything(cuda_dev, dtype, bad):
+    shape = (2, 520, 520, 4, 2, 128, 90, 4)
+    q, k, v, _ = make(shape, dtype, cuda_dev)
+    o, z, eo, ez = ref.forward(q, k, v, 90, 4, None, UNIT[dtype])
+    for n in (1, 130, 300, 519):
+        qq, kk, vv = (t.clone() for t in (q, k, v))
+        for t in (qq, kk, vv):
+            t[:, n:] = bad
+        out, lse = api.window_attn_fwd(qq, kk, vv, 90, 4)
+        assert api.cp_get_error() == 0
+        ref.within(out[:, :n], o[:, :n], eo[:, :n], n)
+        ref.within(lse[..., :n], z[..., :n], ez[..., :n], n)
+        assert not torch.isfinite(out[:, n:]).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("at", [0, 150, 383, 699])
+def test_a_row_that_is_not_finite_reaches_the_gradients_of_its_keys_alone(cuda_dev, dtype, at):
+    shape = (1, 700, 700, 4, 2, 64, 60, 5)
+    q, k, v, do = make(shape, dtype, cuda_dev)
+    out, lse = api.window_attn_fwd(q, k, v, 60, 5)
+    see = ref.visible(700, 700, 60, 5, cuda_dev)[at]
+    gone = do.clone()
+    gone[:, at] = 0
+    want, err = ref.backward(q, k, v, gone, 60, 5, None, UNIT[dtype])
+    broken = do.clone()
+    broken[:, at] = float("nan")
+    dq, dk, dv = api.window_attn_bwd(q, k, v, out, lse, broken, 60, 5)
+    assert api.cp_get_error() == 0
+    rest = torch.arange(700, device=cuda_dev) != at
+    ref.within(dq[:, rest], want[0][:, rest], err[0][:, rest], "dq")
+    ref.within(dk[:, ~see], want[1][:, ~see], err[1][:, ~see], "dk")
+    ref.within(dv[:, ~see], want[2][:, ~see], err[2][:, ~see], "dv")
+    assert dq[:, at].isnan().all() and dk[:, see].isnan().all() and dv[:, see].isnan().all()
