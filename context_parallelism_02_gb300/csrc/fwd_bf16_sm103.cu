@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __nv_bfloat16 *p_row = nullptr;
         float *p_lse = nullptr;
         auto put_unit = [&]() {
-            const float inv = p_l > 0.f ? 1.f / p_l : 0.f;
+            const float inv = 1.f / p_l;            // a row sees itself; NaN where it sees a NaN
             const bool a32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
             uint32_t top = 0;                       // largest magnitudes of the even and the odd columns
 #pragma unroll 1
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         dst[v4] = make_uint4(pk[4 * v4], pk[4 * v4 + 1], pk[4 * v4 + 2], pk[4 * v4 + 3]);
                 }
             }
-            if (p_valid && half == 0) *p_lse = p_l > 0.f ? (p_m + lg2(p_l)) * 0.69314718055994531f : NEG_INF;
+            if (p_valid && half == 0) *p_lse = (p_m + lg2(p_l)) * 0.69314718055994531f;
             const bool odd = p_valid && ((top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u);
             if (__any_sync(0xffffffffu, odd) && lane == 0) fixes->note(p_it, quarter);
             pend = false;

@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(THREADS) window_f32_fwd_kernel(const Args a, f
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 // (a visible weight is never 0: product() skips those)
-                x[i][j] = x[i][j] == -INFINITY ? 0.f : fmaxf(exp2f(x[i][j] - base), 1e-45f);
+                const float w = exp2f(x[i][j] - base);
+                x[i][j] = x[i][j] == -INFINITY ? 0.f : w == 0.f ? 1e-45f : w;
                 sum += x[i][j];
                 P[(ty + 8 * i) * PS + tx + 16 * j] = x[i][j];
             }
@@ -246,13 +247,13 @@ __global__ void __launch_bounds__(THREADS) window_f32_fwd_kernel(const Args a, f
     for (int i = 0; i < 4; ++i) {
         const int r = ty + 8 * i;
         if (r >= u.rows) continue;
-        const float inv = l[i] > 0.f ? 1.f / l[i] : l[i];
+        const float inv = 1.f / l[i];           // a row sees itself; NaN where it sees a NaN
         float *row = out + (((int64_t)u.b * a.Sq + u.q0 + r) * a.Hq + u.h) * D;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j)
             *reinterpret_cast<float4 *>(row + 4 * tx + 64 * j) =
                 make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv);
-        if (tx == 0) lse[((int64_t)u.b * a.Hq + u.h) * a.Sq + u.q0 + r] = l[i] > 0.f ? fmaf(m[i], LN2, logf(l[i])) : -INFINITY;
+        if (tx == 0) lse[((int64_t)u.b * a.Hq + u.h) * a.Sq + u.q0 + r] = fmaf(m[i], LN2, logf(l[i]));
     }
 }
 

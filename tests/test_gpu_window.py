@@ -343,3 +343,37 @@ def test_a_row_that_is_not_finite_reaches_the_gradients_of_its_keys_alone(cuda_d
     ref.within(dk[:, ~see], want[1][:, ~see], err[1][:, ~see], "dk")
     ref.within(dv[:, ~see], want[2][:, ~see], err[2][:, ~see], "dv")
     assert dq[:, at].isnan().all() and dk[:, see].isnan().all() and dv[:, see].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bad", BADS)
+@pytest.mark.parametrize("which", ["q", "k", "v"])
+def test_one_row_that_is_not_finite(cuda_dev, dtype, bad, which):
+    """A row of q, k or v with NaN or infinities throughout: rows that see it are not finite (for q, k: their lse
+    as well), rows that do not are as without it, and so are the gradients of what no such row sees."""
+    S, at, W, K = 500, 260, 70, 5
+    shape = (1, S, S, 4, 2, 64, W, K)
+    q, k, v, do = make(shape, dtype, cuda_dev)
+    o, z, eo, ez = ref.forward(q, k, v, W, K, None, UNIT[dtype])
+    see = ref.visible(S, S, W, K, cuda_dev)
+    hit = see[:, at] if which != "q" else torch.arange(S, device=cuda_dev) == at    # rows
+    broken = [t.clone() for t in (q, k, v)]
+    broken["qkv".index(which)][:, at] = bad
+    out, lse = api.window_attn_fwd(*broken, W, K)
+    ref.within(out[:, ~hit], o[:, ~hit], eo[:, ~hit], "out")
+    ref.within(lse[..., ~hit], z[..., ~hit], ez[..., ~hit], "lse")
+    assert not torch.isfinite(out[:, hit]).any()
+    if which == "v":
+        ref.within(lse, z, ez, "lse")
+    else:
+        assert lse[..., hit].isnan().all()
+    far = ~see[hit].any(0)                                    # keys that no such row sees
+    gone = do.clone()
+    gone[:, hit] = 0
+    want, err = ref.backward(q, k, v, gone, W, K, None, UNIT[dtype])
+    dq, dk, dv = api.window_attn_bwd(*broken, out, lse, do, W, K)
+    assert api.cp_get_error() == 0
+    ref.within(dq[:, ~hit], want[0][:, ~hit], err[0][:, ~hit], "dq")
+    ref.within(dk[:, far], want[1][:, far], err[1][:, far], "dk")
+    ref.within(dv[:, far], want[2][:, far], err[2][:, far], "dv")
+    assert dq[:, hit].isnan().all()
