@@ -137,6 +137,11 @@ int kv8_evict(void *cache, float *scales, const int32_t *pages, const int32_t *l
     if (!pages_to || !kept || !lens_to || !aligned(pages_to, 4) || !aligned(kept, 4) || !aligned(lens_to, 4) ||
         !aligned(mass, 4) || !aligned(mass_to, 4) || (max_pages > 0 && !mass))
         return CP_EINVAL;
+    // written while other blocks of the launch still read
+    const size_t seqs = (size_t)B * 4, heads = (size_t)B * Hkv * 4;
+    if (overlap(lens, seqs, lens_to, seqs) ||
+        overlap(mass, heads * max_pages * page, mass_to, heads * max_to * page))
+        return CP_EINVAL;
     a.mass = mass;
     a.to = pages_to;
     a.kept = kept;

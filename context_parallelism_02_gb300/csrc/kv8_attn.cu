@@ -731,10 +731,13 @@ __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, 
         float *mass = a.mass + (int64_t)bh * cap + s0 + threadIdx.x;
         const float *x = a.scores + ((int64_t)bh * cap + s0 + threadIdx.x) * srows;
         float old[MASS_SLOTS], sum[MASS_SLOTS];
+        int page[MASS_SLOTS];
         bool any[MASS_SLOTS];
 #pragma unroll
         for (int i = 0; i < MASS_SLOTS; ++i) {
-            old[i] = s0 + threadIdx.x + 256 * i < len ? mass[256 * i] : 0.f;
+            const int64_t slot = s0 + threadIdx.x + 256 * i;
+            old[i] = slot < len ? mass[256 * i] : 0.f;
+            page[i] = slot < len ? a.pool.pages[(int64_t)b * a.pool.max_pages + (slot >> a.pool.page_shift)] : -1;
             sum[i] = 0.f;
             any[i] = false;
         }
@@ -770,7 +773,8 @@ __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, 
         }
 #pragma unroll
         for (int i = 0; i < MASS_SLOTS; ++i)
-            if (any[i]) mass[256 * i] = old[i] + sum[i];
+            if (any[i] && page[i] >= 0 && page[i] < a.pool.n_pages)   // slots of other pages have no scores
+                mass[256 * i] = old[i] + sum[i];
     }
 }
 

@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(MOVE_WARPS * 32) kv8_move_kernel(Kv8EvictArgs 
     float top = scale;
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (!(top > 0.f)) top = kv8_scale_of(0);
     // where it goes
     int64_t lp = i0 >> a.pool.page_shift;
     int id = lp < a.max_to ? a.to[(int64_t)b * a.max_to + lp] : -1;
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(MOVE_WARPS * 32) kv8_move_kernel(Kv8EvictArgs 
     for (int i = 0; i < N; ++i) {
         const int r = lane / LANES + i * ROWS;
         const uint8_t *p = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
-        f[i] = __shfl_sync(0xffffffffu, scale, r) / top;
+        f[i] = __shfl_sync(0xffffffffu, scale, r) / top;         // 0 for a token whose page is not there
         x[i] = p ? *reinterpret_cast<const uint4 *>(p + lane % LANES * 16) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll

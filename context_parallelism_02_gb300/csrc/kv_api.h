@@ -21,6 +21,13 @@ struct NvtxScope {
 
 inline bool aligned(const void *p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
+// Whether two buffers share a byte; null buffers do not.
+inline bool overlap(const void *p, size_t np, const void *q, size_t nq)
+{
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    return p && q && a < b + nq && b < a + np;
+}
+
 // Sizes that every call has; fills the pool except data and err.
 inline int check_pool(const void *cache, const int32_t *pages, const int32_t *lens, int B, int Hkv, int D,
                       int n_pages, int page, int max_pages, Kv4Pool &p)

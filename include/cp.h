@@ -593,7 +593,8 @@ int kv8_gather(const void *cache, const float *scales, const int32_t *pages, con
  *   fp32, natural log.  A row that sees nothing: (0, -inf).  What a row does not see has no
  *   influence on it, whatever those slots hold.
  *   mass [B][Hkv][max_pages page] fp32 or NULL: += the weights e^(s - lse) that each slot
- *   got, summed over the rows of its kv head; slots that no row sees stay as they are.
+ *   got, summed over the rows of its kv head; slots that no row sees, and those of pages
+ *   that are not there, stay as they are.
  *   fp32 sums; K, V and q enter exactly (an element of q below 2^-31 of its row's largest is
  *   rounded); the product of a weight and its block's V scale is rounded to fp16 (2^-11 of
  *   itself, or 2^-32 of the row's largest such product).  scale <= 0 selects 1/sqrt(D).  A row
@@ -625,7 +626,8 @@ size_t kv8_attn_workspace(int B, int n, int Hq, int Hkv, int D, int page, int ma
  *   mass_to [B][Hkv][max_to page] fp32 or NULL: the kept slots' mass, then 0.
  *   max_to page >= budget >= 1; keep_first + keep_last <= budget.
  * The source pages stay as they are; pages_to must not name one of them, nor a page twice.
- * Errors: as kv8_append.
+ * A kept token whose page number is out of range becomes zeros.
+ * Errors: as kv8_append, plus CP_EINVAL for lens_to or mass_to that overlap lens or mass.
  */
 int kv8_evict(void *cache, float *scales, const int32_t *pages, const int32_t *lens, const float *mass,
               const int32_t *pages_to, int32_t *kept, int32_t *lens_to, float *mass_to, int B, int Hkv, int D, int n_pages,

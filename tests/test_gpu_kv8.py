@@ -688,3 +688,37 @@ def test_no_gradient(cuda_dev):
     assert not (out.requires_grad or lse.requires_grad)
     for f in (api.kv8_append, api.kv8_gather, api.kv8_attn):
         assert "radient" in f.__doc__
+
+
+def test_a_bad_page_adds_no_mass_and_moves_as_zeros(cuda_dev):
+    """Slots of a page that is not there: their mass stays, and what is kept of them is 0."""
+    H, D, page, L = 2, 64, 16, 80
+    cache, scales, pages, _ = pool(3, 1, L, H, D, page)
+    lens = torch.tensor([L], **I32)
+    bad = pages.clone()
+    bad[0, 1] = cache.shape[0] + 5
+    q = torch.randn(1, 1, 4, D, device=cuda_dev).bfloat16()
+    mass = torch.full((1, H, pages.shape[1] * page), 2.0, device=cuda_dev)
+    ws = torch.full((api.kv8_attn_workspace(1, 1, 4, H, D, page, pages.shape[1], True),), 0x7f, dtype=torch.uint8, device=cuda_dev)
+    out, lse = api.kv8_attn(q, cache, scales, bad, lens, mass=mass, workspace=ws)
+    assert api.cp_get_error() == _lib.CP_ECACHE
+    assert torch.isfinite(out).all() and (mass[..., 16:32] == 2).all() and (mass[..., :16] > 2).all()
+    assert abs(float((mass[..., :L] - 2).sum()) - 4) < 1e-4
+    spare = [p for p in range(cache.shape[0]) if p not in pages.flatten().tolist()][:2]
+    mass.zero_()
+    mass[..., 16:32] = 1
+    kept, _, _ = api.kv8_evict(cache, scales, bad, lens, mass, torch.tensor([spare], **I32), 20)
+    assert api.cp_get_error() == _lib.CP_ECACHE
+    assert kept[0, 0].tolist() == [0, 1, 2, 3, *range(16, 32)]
+    assert not (cache[spare[0], :, :, 4:16] & 0x7f).any() and torch.isfinite(scales[spare]).all()
+
+
+def test_evict_refuses_to_write_what_it_reads(cuda_dev):
+    H, D, page, L = 2, 64, 16, 64
+    cache, scales, pages, _ = pool(4, 2, L, H, D, page)
+    lens = torch.full((2,), L, **I32)
+    mass = torch.rand(2, H, pages.shape[1] * page, device=cuda_dev)
+    for kw in (dict(lens_to=lens), dict(mass_to=mass)):
+        with pytest.raises(api.CpError) as e:
+            api.kv8_evict(cache, scales, pages, lens, mass, pages.flip(1).contiguous(), 16, **kw)
+        assert e.value.code == _lib.CP_EINVAL
