@@ -900,33 +900,33 @@ __device__ __noinline__ void dkdv_fix(const FixList &list, const BwdArgs &a, __n
             float *prow = partial_row<D>(a, w.b, w.g, piece, j, k);
             if (!prow && piece != 0) continue;
             __nv_bfloat16 *brow = (k ? dk : dv) + (((int64_t)w.b * a.Sk + j) * a.Hkv + w.g) * D;
-            fix::Piece<D> acc{};
+            fix::Piece<D> was{}, acc{};
             if (prow) {
 #pragma unroll
-                for (int e = 0; e < D / 32; ++e) acc.x[e] = prow[2 * lane + 64 * (e >> 1) + (e & 1)];
+                for (int e = 0; e < D / 32; ++e) was.x[e] = prow[2 * lane + 64 * (e >> 1) + (e & 1)];
             } else {
-                acc = fix::load<D>(brow, lane);
+                was = fix::load<D>(brow, lane);
             }
-            if (fix::finite(acc)) continue;
-            acc = fix::Piece<D>{};
+            if (fix::finite(was)) continue;
             if (piece == 0) {
                 const int i0 = j - a.win.off > 0 ? j - a.win.off : 0;
                 const int64_t i1 = (int64_t)j - a.win.off + a.win.window;
                 for (int h = 0; h < grp; ++h)
-                    fix::key_rows<D>(a.fix, w.b, w.g * grp + h, j, i0, (int)(i1 < a.S ? i1 : a.S), k, acc);
+                    if (fix::key_rows<D>(a.fix, w.b, w.g * grp + h, j, i0, (int)(i1 < a.S ? i1 : a.S), k, was, acc)) break;
             } else {
                 WinQIter<T> it;
                 for (it.sinks(a.win, a.S, w.ks, w.g * grp, grp, piece - 1, a.sp.each); it.count() > 0; it.next()) {
                     const int64_t from = (int64_t)j + a.win.window - a.win.off;   // the first row behind the window
                     const int i0 = from > it.start() ? (from < a.S ? (int)from : a.S) : it.start();
-                    fix::key_rows<D>(a.fix, w.b, it.head(), j, i0, it.start() + it.len(), k, acc);
+                    if (fix::key_rows<D>(a.fix, w.b, it.head(), j, i0, it.start() + it.len(), k, was, acc)) break;
                 }
             }
+            acc = fix::mended(was, acc, 1.f);
             if (prow) {
 #pragma unroll
                 for (int e = 0; e < D / 32; ++e) prow[2 * lane + 64 * (e >> 1) + (e & 1)] = acc.x[e];
             } else {
-                fix::store(brow, acc, 1.f, lane);
+                fix::store(brow, acc, lane);
             }
         }
     };

@@ -711,8 +711,8 @@ __global__ void __launch_bounds__(W * 32)
 
 // mass += the weights, from the scores that the attention kernel left (in L2, as far as they
 // fit): a thread takes MASS_SLOTS slots with all their loads in flight (one slot at a time, in
-// blocks of 256, took 8 x 16384 slots and 8 kv heads 10 us, these FIXME) and adds up the rows
-// of its kv head in order.
+// blocks of 256, took 8 x 16384 slots and 8 kv heads 2 us longer) and adds up the rows of its
+// kv head in order.
 constexpr int MASS_SLOTS = 4, MASS_CHUNK = MASS_SLOTS * 256;
 constexpr int MASS_ROWS = 64;      // rows whose lse and range lie in shared memory at a time
 __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, int chunks)
