@@ -110,9 +110,6 @@ __device__ __forceinline__ void ts_mn_seq(uint32_t tD, uint32_t tA, uint64_t dB,
     }
 }
 
-// 32 columns of the lane's row times f, as bf16, to 32-byte aligned memory: regrouped, so
-// that a store covers whole pieces of 64 bytes.  (Every lane its own row in 16 bytes took
-// the dK / dV epilogue of a unit 5500 cycles, as long as three of its half steps.)
 // NaN where one of 32 columns is not finite, else 0.
 __device__ __forceinline__ float odd_columns(const uint32_t (&o)[32])
 {
@@ -122,6 +119,9 @@ __device__ __forceinline__ float odd_columns(const uint32_t (&o)[32])
     return a + b;
 }
 
+// 32 columns of the lane's row times f, as bf16, to 32-byte aligned memory: regrouped, so
+// that a store covers whole pieces of 64 bytes.  (Every lane its own row in 16 bytes took
+// the dK / dV epilogue of a unit 5500 cycles, as long as three of its half steps.)
 __device__ __forceinline__ void put_row_piece(__nv_bfloat16 *piece, bool ok, const uint32_t (&o)[32], float f, int lane)
 {
     uint32_t pk[16];
