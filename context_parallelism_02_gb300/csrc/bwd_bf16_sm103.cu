@@ -130,6 +130,18 @@ __device__ __forceinline__ void put_row_piece(__nv_bfloat16 *piece, bool ok, con
     store_warp_rows<16>(piece, ok, pk, lane);
 }
 
+// 32 bytes of a row, zeros where it is not there; rows32: 32-byte aligned.
+__device__ __forceinline__ void load_chunk(const __nv_bfloat16 *p, bool there, bool rows32, uint32_t (&w)[8])
+{
+    if (there && rows32) {
+        ld_global_v8u(p, w);
+        return;
+    }
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+    if (there) x = reinterpret_cast<const uint4 *>(p)[0], y = reinterpret_cast<const uint4 *>(p)[1];
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+}
+
 // ----------------------------------------------------------------------------- Delta
 
 __global__ void __launch_bounds__(256) bwd_delta_kernel(const __nv_bfloat16 *__restrict__ out,
@@ -177,9 +189,18 @@ __global__ void __launch_bounds__(256) bwd_delta_kernel(const __nv_bfloat16 *__r
         for (int i = 1; i < ROWS; ++i) mine = lane == i ? acc[i] : mine;
         const int64_t r = r0 + lane;
         if (lane < ROWS && r < rows) {
-            const int64_t h = r % Hq;
-            const int64_t bs = r / Hq;   // b * S + s
-            const int64_t b = bs / S, s = bs % S;
+            int64_t h, b, s;
+            if (rows >> 31 == 0) {   // 64-bit divisions took 1.3 of 29.6 us
+                const unsigned bs = (unsigned)r / (unsigned)Hq, bb = bs / (unsigned)S;   // b * S + s
+                h = (unsigned)r - bs * (unsigned)Hq;
+                b = bb;
+                s = bs - bb * (unsigned)S;
+            } else {
+                const int64_t bs = r / Hq;
+                h = r % Hq;
+                b = bs / S;
+                s = bs % S;
+            }
             delta[(b * Hq + h) * S + s] = mine;
         }
     }
@@ -230,7 +251,8 @@ struct DqCfg {
     static constexpr int OFF_BAR = (3 + Q_KST) * TB;
     static constexpr int OFF_MISC = OFF_BAR + 8 * Q_NBAR;
     static constexpr int OFF_FIX = OFF_MISC + 16;       // WIN: FixList
-    static constexpr int NEED = OFF_FIX + (int)sizeof(FixList);
+    static constexpr int OFF_DELTA = OFF_FIX + ((int)sizeof(FixList) + 15) / 16 * 16;   // WIN: [2][2][T] fp32
+    static constexpr int NEED = OFF_DELTA + 4 * T * 4;
     static constexpr int SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
     static_assert(SMEM <= 232448, "dQ kernel shared memory");
     static constexpr uint32_t TM_S = 0, TM_P = 128, TM_DQ = 256, TM_DS = 256 + D, TM_DO = 320 + D;
@@ -262,6 +284,7 @@ struct BwdArgs {
     Window win;          // windowed attention
     SinkPlan sp;
     float *part;         // the sinks' partial gradients (window_sinks.cuh)
+    float *delta;        // WIN: Delta, written by the dQ kernel
     int n_units;         // windowed attention: units of the launch
     FastDiv by_tiles, by_heads, by_group;   // of its numbering: tiles, heads (query or kv), Hq / Hkv
     FixArgs fix;         // windowed attention
@@ -510,7 +533,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 Item x;
                 int nt = 0;
                 for (int u = 0; ok && unit_of(u, x); ++u) {
-                    if (!waitw(BAR(Q_QTM), u & 1, wc) || !waitw(BAR(Q_DOFULL), u & 1, wc)) break;
+                    if (!waitw(BAR(Q_QTM), u & 1, wc)) break;
                     for (int j = 0; j < x.n; ++j, ++nt, kr.next()) {
                         const int sv = nt & 1;
                         if ((nt > 0 && !waitw(BAR(Q_SFREE), (nt - 1) & 1, wc)) ||
@@ -528,7 +551,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         }
                         __syncwarp();
                         if ((nt > 0 && !waitw(BAR(Q_PFREE), (nt - 1) & 1, wc)) ||
-                            !waitw(BAR(Q_VFULL + sv), (nt >> 1) & 1, wc)) {
+                            (j == 0 && !waitw(BAR(Q_DOFULL), u & 1, wc)) || !waitw(BAR(Q_VFULL + sv), (nt >> 1) & 1, wc)) {
                             ok = false;
                             break;
                         }
@@ -603,7 +626,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             bool valid;
             float lse2, dlt;
         };
-        auto load_row = [&](const Unit &w) -> Row {
+        // WIN: Delta = rowsum(dO out) is made here, while the tensor cores finish the unit before,
+        // and written for dK / dV: 201 us for both (16384 rows, 16 heads, window 1024), where a
+        // kernel of its own took 30 and this one 190.  Rows come in chunks that cover whole
+        // sectors, from L2, where the unit before had them sent (every lane its own row, from
+        // memory: 244).  Each half leaves its share in shared memory, by the unit's parity;
+        // Q_DOFULL tells of both.
+        float *shares = reinterpret_cast<float *>(smem_raw + C::OFF_DELTA);
+        const bool rows32 = WIN && ((reinterpret_cast<uintptr_t>(dout) | reinterpret_cast<uintptr_t>(a.fix.out)) & 31) == 0;
+        auto load_row = [&](const Unit &w, int u) -> Row {
             Row r;
             r.qpos = w.q0 + row;
             r.valid = r.qpos < w.cend;
@@ -613,7 +644,35 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             uint32_t dv4[D / 4];
             if (r.valid) {
                 r.lse2 = lse[((int64_t)w.b * a.Hq + w.h) * a.S + r.qp] * LOG2E;
-                r.dlt = delta[((int64_t)w.b * a.Hq + w.h) * a.S + r.qp];
+                if constexpr (!WIN) r.dlt = delta[((int64_t)w.b * a.Hq + w.h) * a.S + r.qp];
+            }
+            if constexpr (WIN) {
+                // lane c of a group of G loads chunk c, 32 bytes, of the group's pieces in turn
+                constexpr int G = D / 32;
+                const int c = lane & (G - 1), gb = lane & ~(G - 1);
+                const int64_t at = (((int64_t)w.b * a.S + w.q0 + quarter * 32 + gb) * a.Hq + w.h) * D + (D / 2) * half + 16 * c;
+                uint32_t ld[G][8], lo[G][8];
+#pragma unroll
+                for (int m = 0; m < G; ++m) {
+                    const bool there = w.q0 + quarter * 32 + gb + m < w.cend;
+                    load_chunk(dout + at + (int64_t)m * a.Hq * D, there, rows32, ld[m]);
+                    load_chunk(a.fix.out + at + (int64_t)m * a.Hq * D, there, rows32, lo[m]);
+                }
+#pragma unroll
+                for (int m = 0; m < G; ++m) {
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        s0 = fmaf(__uint_as_float(lo[m][e] << 16), __uint_as_float(ld[m][e] << 16), s0);
+                        s1 = fmaf(__uint_as_float(lo[m][e] & 0xffff0000u), __uint_as_float(ld[m][e] & 0xffff0000u), s1);
+                    }
+                    s0 += s1;
+#pragma unroll
+                    for (int o = 1; o < G; o <<= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+                    if (c == m) r.dlt = s0;
+                }
+                chunks_to_pieces(ld, dv4, c);
+            } else if (r.valid) {
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     dout + (((int64_t)w.b * a.S + r.qp) * a.Hq + w.h) * D + (D / 2) * half);
 #pragma unroll
@@ -633,6 +692,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 tmem_st_x32(tDO, dv4);
             else
                 tmem_st_x16(tDO, dv4);
+            if constexpr (WIN) shares[((u & 1) * 2 + half) * T + row] = r.dlt;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -644,14 +704,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         Item xn;
         bool have = unit_of(0, xn);
         Row rn{};
-        if (have) rn = load_row(xn.w);
+        if (have) rn = load_row(xn.w, 0);
         for (int u = 0; ok && have; ++u) {
             const Item x = xn;
             const Unit &w = x.w;
             const Row rw = rn;
             const int qpos = rw.qpos, qp = rw.qp, n = x.n;
             const bool valid = rw.valid;
-            const float lse2 = rw.lse2, dlt = rw.dlt;
+            const float lse2 = rw.lse2;
+            float dlt = rw.dlt;
+            if constexpr (WIN) {
+                if (!waitw(BAR(Q_DOFULL), u & 1, wc)) break;
+                const float *share = shares + (u & 1) * 2 * T + row;
+                dlt = share[0] + share[T];
+                if (valid && half == 0) a.delta[((int64_t)w.b * a.Hq + w.h) * a.S + qp] = dlt;
+                Item y;
+                if (unit_of(u + 1, y) && y.w.q0 + row < a.S) {   // the next unit's rows, on their way to L2
+                    const int64_t at = (((int64_t)y.w.b * a.S + y.w.q0 + row) * a.Hq + y.w.h) * D + (D / 2) * half;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(dout + at));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.fix.out + at));
+                }
+            }
             Walk it;
             start_walk(it, w);
             for (int j = 0; j < n; ++j, ++nt, it.next()) {
@@ -744,7 +817,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             // the next unit's rows first: its S and dP run beside this unit's epilogue
             have = ok && unit_of(u + 1, xn);
-            if (have) rn = load_row(xn.w);
+            if (have) rn = load_row(xn.w, u + 1);
             if (ok && waitw(BAR(Q_FIN), u & 1, wc)) {
                 tc_fence_after();
                 // each half writes D/2 columns of dQ = scale * acc
@@ -1451,12 +1524,11 @@ int launch_window_d(const BwdPtrs &p, BwdArgs a, cudaStream_t st)
     const int64_t qunits = (int64_t)a.upc * a.B * a.Hq;
     const int64_t kunits = ((int64_t)a.tpc + (int64_t)a.sp.tiles * a.sp.pieces) * a.B * a.Hkv;
     if (qunits > 0x7fffffffLL || kunits > 0x7fffffffLL) return CP_EUNSUPPORTED;
-    const int rc = launch_delta(p, a, D, st);
-    if (rc) return rc;
     const int64_t sms = sm_count();
     const int cap = fwd_grid_limit();   // test hook: blocks with many units
     const int64_t most = cap > 0 && cap < sms ? cap : sms;
     float *delta = static_cast<float *>(p.workspace);
+    a.delta = delta;
     a.part = delta + bwd_workspace_bytes(a.B, a.Hq, a.S) / 4;
     a.fix = FixArgs{static_cast<const __nv_bfloat16 *>(p.q), static_cast<const __nv_bfloat16 *>(p.k),
                     static_cast<const __nv_bfloat16 *>(p.v), static_cast<const __nv_bfloat16 *>(p.out),
@@ -1557,7 +1629,7 @@ BwdArgs bwd_args(const FwdArgs &f)
     a.Sk = f.Sk;
     a.win = f.win;
     a.sp = SinkPlan{0, 0, 1};
-    a.part = nullptr;
+    a.part = a.delta = nullptr;
     a.n_units = 0;
     a.by_tiles = a.by_heads = a.by_group = fast_div(1);
     a.fix = FixArgs{};

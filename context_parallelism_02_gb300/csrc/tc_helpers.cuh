@@ -168,6 +168,29 @@ __device__ __forceinline__ void ld_global_v8u(const void *p, uint32_t (&v)[8])
                  : "memory");
 }
 
+// ld[m], chunk j = lane % G of the piece of the group's lane m, to each lane's own piece.
+template <int G>
+__device__ __forceinline__ void chunks_to_pieces(const uint32_t (&ld)[G][8], uint32_t (&pk)[8 * G], int j)
+{
+#pragma unroll
+    for (int e = 0; e < 8 * G; ++e) pk[e] = 0u;
+    // exchange k: this lane sends chunk j of the piece of the group's lane j ^ k, which
+    // that lane wants, and receives chunk j ^ k of its own piece
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+        const int c = j ^ k;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t v = ld[0][e];
+#pragma unroll
+            for (int mm = 1; mm < G; ++mm) v = c == mm ? ld[mm][e] : v;
+            const uint32_t r = k == 0 ? v : __shfl_xor_sync(0xffffffffu, v, k);
+#pragma unroll
+            for (int cc = 0; cc < G; ++cc) pk[8 * cc + e] = c == cc ? r : pk[8 * cc + e];
+        }
+    }
+}
+
 // The load counterpart of store_warp_rows: lane t receives the NW words of its
 // own piece, and every load instruction of the warp covers whole pieces.  Lane j
 // of a group of G = NW/8 lanes loads chunk j of each of the group's G pieces,
@@ -194,23 +217,7 @@ __device__ __forceinline__ void load_warp_rows(const void *piece, bool ok, uint3
             for (int e = 0; e < 8; ++e) ld[m][e] = 0u;
         }
     }
-#pragma unroll
-    for (int e = 0; e < NW; ++e) pk[e] = 0u;
-    // exchange k: this lane sends chunk j of the piece of lane gb + (j ^ k), which
-    // that lane wants, and receives chunk j ^ k of its own piece
-#pragma unroll
-    for (int k = 0; k < G; ++k) {
-        const int c = j ^ k;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint32_t v = ld[0][e];
-#pragma unroll
-            for (int mm = 1; mm < G; ++mm) v = c == mm ? ld[mm][e] : v;
-            const uint32_t r = k == 0 ? v : __shfl_xor_sync(0xffffffffu, v, k);
-#pragma unroll
-            for (int cc = 0; cc < G; ++cc) pk[8 * cc + e] = c == cc ? r : pk[8 * cc + e];
-        }
-    }
+    chunks_to_pieces(ld, pk, j);
 }
 
 // Eight fp32 values from / to global memory in one 32-byte access (32-byte
