@@ -717,7 +717,7 @@ constexpr int MASS_SLOTS = 4, MASS_CHUNK = MASS_SLOTS * 256;
 constexpr int MASS_ROWS = 64;      // rows whose lse and range lie in shared memory at a time
 __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, int chunks)
 {
-    __shared__ float lse2[MASS_ROWS];
+    __shared__ __align__(16) float lse2[MASS_ROWS];
     __shared__ int limit[MASS_ROWS], low[MASS_ROWS];
     const int chunk = (int)(blockIdx.x % (unsigned)chunks);
     const unsigned bh = blockIdx.x / (unsigned)chunks;
@@ -744,14 +744,32 @@ __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, 
         for (int r0 = 0; r0 < sh.rows; r0 += MASS_ROWS) {
             const int n = min(MASS_ROWS, sh.rows - r0);
             __syncthreads();
+            bool whole = true;                               // the thread's row sees all slots in hand
             if ((int)threadIdx.x < n) {
                 const int rr = r0 + threadIdx.x, j = rr / sh.group, head = h * sh.group + rr % sh.group;
                 const int lim = kv4_limit(a.rows, b, j, len);
                 limit[threadIdx.x] = lim;
                 low[threadIdx.x] = a.window > 0 ? max(lim - a.window, 0) : 0;
                 lse2[threadIdx.x] = a.lse[((int64_t)b * a.rows.Hq + head) * a.rows.n + j] * LOG2E;
+                whole = lim >= s0 + MASS_CHUNK && low[threadIdx.x] <= s0;
             }
-            __syncthreads();
+            if (__syncthreads_and(whole) && n % 4 == 0) {    // most chunks
+                for (int r = 0; r < n; r += 4) {
+                    const float4 z = *reinterpret_cast<const float4 *>(lse2 + r);
+                    float4 v[MASS_SLOTS];
+#pragma unroll
+                    for (int i = 0; i < MASS_SLOTS; ++i) v[i] = *reinterpret_cast<const float4 *>(x + (int64_t)256 * i * srows + r0 + r);
+#pragma unroll
+                    for (int i = 0; i < MASS_SLOTS; ++i) {   // row by row, as below
+                        sum[i] += ex2(v[i].x - z.x);
+                        sum[i] += ex2(v[i].y - z.y);
+                        sum[i] += ex2(v[i].z - z.z);
+                        sum[i] += ex2(v[i].w - z.w);
+                        any[i] = true;
+                    }
+                }
+                continue;
+            }
             for (int r = 0; r < n; r += 4) {
                 float4 v[MASS_SLOTS];
 #pragma unroll
