@@ -12,8 +12,10 @@
 //           (rounds of 11 bits save one, but summing 2048 bins costs 4000 cycles each; a run
 //           of slots per thread, with its bank conflicts and one load at a time, took 15000
 //           cycles for the last two passes: 8 rows of 65536 slots 28 us, these 19).
-//   move    a warp per 16 kept tokens, kv head and K or V copies their rows of D bytes into
-//           a block of the other pages, under the largest of their scales.  Bounded by HBM.
+//   move    a warp per 16 kept tokens and kv head copies their rows of D bytes, K and V, into a
+//           block of the other pages, under the largest of their scales.  Bounded by the chain
+//           kept slot, page, scale and row, then by HBM (K and V by warps of their own, twice the
+//           chains: 1 us longer).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(THREADS) kv8_select_kernel(Kv8EvictArgs a, int
     cl.sync();                                               // counts are read by other blocks
 }
 
-// 16 kept tokens of one kv head, K or V.
+// 16 kept tokens of one kv head, K and V.
 template <int D>
 __global__ void __launch_bounds__(MOVE_WARPS * 32) kv8_move_kernel(Kv8EvictArgs a, FastDiv by_heads, FastDiv by_blocks, int units)
 {
@@ -222,60 +224,68 @@ __global__ void __launch_bounds__(MOVE_WARPS * 32) kv8_move_kernel(Kv8EvictArgs 
     kv4_begin();
     const int64_t unit = (int64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
     if (unit >= units) return;
-    const int which = (int)(unit & 1);
-    const unsigned x0 = (unsigned)unit >> 1, y0 = by_heads.div(x0);
+    const unsigned x0 = (unsigned)unit, y0 = by_heads.div(x0);
     const int h = (int)(x0 - y0 * by_heads.d), b = (int)by_blocks.div(y0), t = (int)(y0 - (unsigned)b * by_blocks.d);
     const int64_t i0 = (int64_t)t * KV8_BLOCK;
+    // where it goes
+    const int64_t lp = i0 >> a.pool.page_shift;
+    const int id_to = lp < a.max_to ? a.to[(int64_t)b * a.max_to + lp] : -1;
     // lane r < 16: where token r of the block comes from
     int slot = -1;
     if (lane < KV8_BLOCK && i0 + lane < a.budget) slot = a.kept[((int64_t)b * a.pool.Hkv + h) * a.budget + i0 + lane];
-    const uint8_t *src = nullptr;
-    float scale = 0.f;
+    const int64_t v_bytes = (int64_t)D << a.pool.page_shift, v_scales = (int64_t)1 << (a.pool.page_shift - 4);
+    const uint8_t *src = nullptr;          // K's row; V's lies v_bytes behind it
+    float scale[2] = {0.f, 0.f};
     if (slot >= 0) {
         const int id = kv4_page(a.pool, b, slot >> a.pool.page_shift);
         if (id >= 0) {
             const int at = slot & ((1 << a.pool.page_shift) - 1);
-            src = kv8_row<D>(a.pool, id, h, which, at);
-            scale = *kv8_scale(a.pool, id, h, which, at);
+            src = kv8_row<D>(a.pool, id, h, 0, at);
+            const float *s = kv8_scale(a.pool, id, h, 0, at);
+            scale[0] = s[0];
+            scale[1] = s[v_scales];
         }
     }
     const unsigned there = __ballot_sync(0xffffffffu, slot >= 0);
     if (!there) return;
-    float top = scale;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (!(top > 0.f)) top = kv8_scale_of(0);
-    // where it goes
-    int64_t lp = i0 >> a.pool.page_shift;
-    int id = lp < a.max_to ? a.to[(int64_t)b * a.max_to + lp] : -1;
-    if (id < 0 || id >= a.pool.n_pages) {
-        if (lane == 0) kv4_report(a.pool.err);
-        return;
-    }
-    const int at = (int)(i0 & ((1 << a.pool.page_shift) - 1));
-    uint8_t *dst = kv8_row<D>(a.pool, id, h, which, at);
-    uint4 x[N];
-    float f[N];
+    uint4 x[2][N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int r = lane / LANES + i * ROWS;
         const uint8_t *p = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
-        f[i] = __shfl_sync(0xffffffffu, scale, r) / top;         // 0 for a token whose page is not there
-        x[i] = p ? *reinterpret_cast<const uint4 *>(p + lane % LANES * 16) : make_uint4(0, 0, 0, 0);
-    }
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int r = lane / LANES + i * ROWS;
-        if (!(there >> r & 1u)) continue;
-        if (f[i] != 1.f) {
-            x[i].x = kv8_shrink(x[i].x, f[i]);
-            x[i].y = kv8_shrink(x[i].y, f[i]);
-            x[i].z = kv8_shrink(x[i].z, f[i]);
-            x[i].w = kv8_shrink(x[i].w, f[i]);
-        }
-        *reinterpret_cast<uint4 *>(dst + r * D + lane % LANES * 16) = x[i];
+        for (int w = 0; w < 2; ++w)
+            x[w][i] = p ? *reinterpret_cast<const uint4 *>(p + w * v_bytes + lane % LANES * 16) : make_uint4(0, 0, 0, 0);
     }
-    if (lane == 0) *kv8_scale(a.pool, id, h, which, at) = top;
+    if (id_to < 0 || id_to >= a.pool.n_pages) {
+        if (lane == 0) kv4_report(a.pool.err);
+        return;
+    }
+    const int at = (int)(i0 & ((1 << a.pool.page_shift) - 1));
+    uint8_t *dst = kv8_row<D>(a.pool, id_to, h, 0, at);
+    float *scale_to = kv8_scale(a.pool, id_to, h, 0, at);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        float top = scale[w];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (!(top > 0.f)) top = kv8_scale_of(0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int r = lane / LANES + i * ROWS;
+            const float f = __shfl_sync(0xffffffffu, scale[w], r) / top;             // 0 for a token whose page is not there
+            if (!(there >> r & 1u)) continue;
+            uint4 &y = x[w][i];
+            if (f != 1.f) {
+                y.x = kv8_shrink(y.x, f);
+                y.y = kv8_shrink(y.y, f);
+                y.z = kv8_shrink(y.z, f);
+                y.w = kv8_shrink(y.w, f);
+            }
+            *reinterpret_cast<uint4 *>(dst + w * v_bytes + r * D + lane % LANES * 16) = y;
+        }
+        if (lane == 0) scale_to[w * v_scales] = top;
+    }
 }
 
 }  // namespace
@@ -284,7 +294,7 @@ int launch_kv8_evict(const Kv8EvictArgs &a, int D, cudaStream_t st)
 {
     const int64_t rows = (int64_t)a.B * a.pool.Hkv, cap = (int64_t)a.pool.max_pages << a.pool.page_shift;
     const int64_t blocks = ((int64_t)a.budget + KV8_BLOCK - 1) / KV8_BLOCK;
-    const __int128 units = (__int128)rows * blocks * 2;
+    const __int128 units = (__int128)rows * blocks;
     if (cap > 0x7fffffffLL || rows * MAX_CLUSTER > 0x7fffffffLL || units > 0x7fffffff)
         return CP_EUNSUPPORTED;
     // blocks of a cluster: as many as leave each about 2048 slots, but no more than run at
