@@ -8,7 +8,7 @@
 //           Four rounds of 8 bits, each a histogram summed over the cluster through
 //           distributed shared memory, find the last key that is kept and how many of its
 //           equals; counts by warps of consecutive slots then place the slots.  Bounded by
-//           latency: six cluster barriers and the passes over the keys, BATCH loads at a time
+//           latency: five cluster barriers and the passes over the keys, BATCH loads at a time
 //           (rounds of 11 bits save one, but summing 2048 bins costs 4000 cycles each; a run
 //           of slots per thread, with its bank conflicts and one load at a time, took 15000
 //           cycles for the last two passes: 8 rows of 65536 slots 28 us, these 19).
@@ -46,7 +46,7 @@ constexpr int BINS = 256, ROUNDS = 4;
 constexpr int BATCH = 16;          // slots of a thread whose loads are in flight together
 struct Shared {
     uint32_t hist[ROUNDS][BINS];   // a round each: the cluster may still read one while the next fills
-    uint32_t counts[2];            // of the block: keys above the last kept one, equals
+    uint32_t before[2];            // in the blocks of lower rank: keys above the last kept one, equals
     uint32_t warp[NWARP][2];
     uint32_t prefix, want;         // digits found so far; equals of them still to take
 };
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(THREADS) kv8_select_kernel(Kv8EvictArgs a, int
             }
         }
     }
-    if (threadIdx.x == 0) sm.prefix = 0, sm.want = (uint32_t)n;
+    if (threadIdx.x == 0) sm.prefix = 0, sm.want = (uint32_t)n, sm.before[0] = 0;
     for (int i = threadIdx.x; i < ROUNDS * BINS; i += THREADS) (&sm.hist[0][0])[i] = 0;
     __syncthreads();
     for (int round = 0; round < ROUNDS; ++round) {
@@ -158,17 +158,23 @@ __global__ void __launch_bounds__(THREADS) kv8_select_kernel(Kv8EvictArgs a, int
         uint32_t v[2] = {0, 0};
         if (bin >= 0) {
 #pragma unroll
-            for (int r = 0; r < MAX_CLUSTER; ++r)            // all loads in flight
-                if (r < C) v[0] += cl.map_shared_rank(hist, r)[bin];
+            for (int r = 0; r < MAX_CLUSTER; ++r) {          // all loads in flight
+                const uint32_t x = r < C ? cl.map_shared_rank(hist, r)[bin] : 0u;
+                v[0] += x;
+                v[1] += r < rank ? x : 0u;
+            }
         }
-        const uint32_t here = v[0];
-        scan2(sm, v);                                        // v[0]: keys in higher bins
+        const uint32_t here = v[0], lower = v[1];
+        scan2(sm, v);                                        // keys in higher bins
         if (v[0] < want && v[0] + here >= want) {            // one thread
             sm.prefix = prefix << 8 | (uint32_t)bin;
             sm.want = want - v[0];
+            sm.before[0] += v[1];
+            sm.before[1] = lower;
         }
         __syncthreads();
     }
+    cl.barrier_arrive();                                     // this block has read the others' histograms
     // The last kept key is `last`; `equals` of those like it are kept, from the lowest slot on.
     const uint32_t last = sm.prefix, equals = sm.want;
     uint32_t at[2] = {0, 0};                                 // keys above it, equals: in the warp's slots
@@ -179,17 +185,8 @@ __global__ void __launch_bounds__(THREADS) kv8_select_kernel(Kv8EvictArgs a, int
     if (lane == 0) sm.warp[warp][0] = at[0], sm.warp[warp][1] = at[1];
     __syncthreads();
     // ... and before them
-    at[0] = at[1] = 0;
+    at[0] = sm.before[0], at[1] = sm.before[1];
     for (int w = 0; w < warp; ++w) at[0] += sm.warp[w][0], at[1] += sm.warp[w][1];
-    if (threadIdx.x == THREADS - 1) sm.counts[0] = at[0] + sm.warp[warp][0], sm.counts[1] = at[1] + sm.warp[warp][1];
-    cl.sync();
-#pragma unroll
-    for (int r = 0; r < MAX_CLUSTER; ++r)
-        if (r < rank) {
-            const uint32_t *other = cl.map_shared_rank(sm.counts, r);
-            at[0] += other[0];
-            at[1] += other[1];
-        }
     const unsigned lower = (1u << lane) - 1u;
     for (int t = w0; t < w1; t += 32 * BATCH) {
         float x[BATCH];                                      // mass again, for mass_to (in L2)
@@ -212,7 +209,7 @@ __global__ void __launch_bounds__(THREADS) kv8_select_kernel(Kv8EvictArgs a, int
             at[1] += __popc(eq);
         }
     }
-    cl.sync();                                               // counts are read by other blocks
+    cl.barrier_wait();                                       // the others have read this one's
 }
 
 // 16 kept tokens of one kv head, K and V.
