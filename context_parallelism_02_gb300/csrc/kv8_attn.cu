@@ -796,8 +796,12 @@ __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, 
     }
 }
 
-// Short tables: a block per item where the items fit the SMs at once (see kv4_attn.cu; the same sizes).
-constexpr int ALONE_WARPS = 8, ALONE_BLOCKS = 48, ALONE_BLOCKS_MANY = 128, ALONE_BLOCKS_FULL = 64;
+// Short tables: a block per item where the items fit the SMs at once (see kv4_attn.cu; the same
+// sizes), or twice over where they are of 512 tokens at most (8 kv heads, D = 128: 64 x 256 tokens
+// 13.9 us where stretches and join take 17.5, 48 x 512 17.8 against 19.8, 64 ragged ones up to 512
+// 14.0 against 13.3; 48 x 1024 27.9 against 26.1, 64 ragged ones up to 1024 23.1 against 19.8, and
+// 128 x 256, four times over, 25.2 against 23.5).
+constexpr int ALONE_WARPS = 8, ALONE_BLOCKS = 48, ALONE_BLOCKS_MANY = 128, ALONE_BLOCKS_FULL = 64, ALONE_BLOCKS_TWICE = 32;
 
 // The pool as [plane][row][D bytes], boxes of 16 rows.
 bool make_pool_map(CUtensorMap *m, const Kv8Pool &pool, int D, int64_t n_pages)
@@ -850,11 +854,11 @@ int launch(const Kv8AttnArgs &a, const Shape &sh, const CUtensorMap &map, cudaSt
     int64_t most = min((int64_t)a.pool.max_pages << (a.pool.page_shift - 4), (int64_t)1 << 27);
     if (a.window > 0 && !a.rows.vis)   // the sinks', the window's and the drafted tokens', each cut at both ends
         most = min(most, ((int64_t)a.sinks + 15) / 16 + ((int64_t)a.window + a.rows.n + 14) / 16 + 1);
-    const int64_t items = (int64_t)a.rows.B * sh.per_batch;
+    const int64_t items = (int64_t)a.rows.B * sh.per_batch, full = fills4[dev].load(std::memory_order_relaxed);
     cudaError_t rc;
     if (items <= sm_count() && most <= (2 * items >= sm_count() ? ALONE_BLOCKS_MANY : ALONE_BLOCKS)) {
         rc = kv4_launch(kv8_attn_kernel<D, NT, ALONE_WARPS, true>, (unsigned)items, ALONE_WARPS * 32, alone, st, map, a, sh, 0);
-    } else if (items > sm_count() && items <= fills4[dev].load(std::memory_order_relaxed) && most <= ALONE_BLOCKS_FULL) {
+    } else if (items > sm_count() && ((items <= full && most <= ALONE_BLOCKS_FULL) || (items <= 2 * full && most <= ALONE_BLOCKS_TWICE))) {
         rc = kv4_launch(kv8_attn_kernel<D, NT, WARPS, true>, (unsigned)items, WARPS * 32, alone4, st, map, a, sh, 0);
     } else {
         const int64_t line = ((most > 0 ? most : 1) + PAD) * items;

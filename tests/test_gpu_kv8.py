@@ -206,6 +206,7 @@ ATTN = [  # lens, n, Hq, Hkv, D, page, window, sinks, mass, fp32 out
     ([300], 2, 4, 4, 64, 16, 290, 64, True, False),           # window and sinks meet
     ([3000, 700], 1, 4, 4, 128, 64, 5000, 4, False, False),   # a window beyond the context
     ([400] * 40, 1, 8, 4, 64, 16, 0, 0, True, False),         # more items than SMs
+    ([512, 1, 300] * 20, 1, 16, 8, 128, 16, 0, 0, True, False),   # more than run at once, of a short table
 ]
 
 
