@@ -1,8 +1,9 @@
-// kv4_binding.cpp -- Python module _kv4_binding: the calls of the paged caches (kv4_*, kv8_*)
-// and of windowed attention on torch tensors.  It checks tensors, allocates what the caller did not give and calls
-// libcp's entry points; it holds no arithmetic.  A decode step makes these calls
-// once per layer, and in Python their checks and allocations took longer than the
-// kernels (21 us of host time for an attention call of 9 us; 11 here).
+// kv4_binding.cpp -- Python module _kv4_binding: the calls of the paged caches (kv4_*,
+// kv8_*) and of windowed attention on torch tensors.  It checks tensors, allocates what
+// the caller did not give and calls libcp's entry points; it holds no arithmetic.  A
+// decode step makes these calls once per layer, and in Python their checks and
+// allocations took longer than the kernels (21 us of host time for an attention call of
+// 9 us; 11 here).
 //
 // libcp is not linked: its functions come as addresses (table()), so that the caller
 // chooses the build of the library.  Functions return their tensors, or the status
@@ -458,7 +459,7 @@ PyObject *evict8(PyObject *const *args, Py_ssize_t n_args)
     a.check("pages_to", &to, at::kInt);
     if (to.dim() != 2 || to.size(0) != B) refuse("pages_to must have shape [", B, ", max_to], not ", to.sizes());
     const int max_to = status("max_to", to.size(1));
-    if (budget < 1) return PyLong_FromLong(CP_EINVAL);
+    if (budget < 1 || budget > (int64_t)max_to * p.page) return PyLong_FromLong(CP_EINVAL);   // before kept is made
     a.check("kept", kept, at::kInt, {B, p.heads, budget});
     a.check("lens_to", lens_to, at::kInt, {B});
     const int64_t slots[3] = {B, p.heads, (int64_t)max_to * p.page};

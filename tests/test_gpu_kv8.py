@@ -719,6 +719,9 @@ def test_evict_refuses_to_write_what_it_reads(cuda_dev):
     cache, scales, pages, _ = pool(4, 2, L, H, D, page)
     lens = torch.full((2,), L, **I32)
     mass = torch.rand(2, H, pages.shape[1] * page, device=cuda_dev)
+    with pytest.raises(api.CpError) as e:                  # more than pages_to hold, and than memory would
+        api.kv8_evict(cache, scales, pages, lens, mass, pages.flip(1).contiguous(), 2 ** 31 - 1)
+    assert e.value.code == _lib.CP_EINVAL
     for kw in (dict(lens_to=lens), dict(mass_to=mass)):
         with pytest.raises(api.CpError) as e:
             api.kv8_evict(cache, scales, pages, lens, mass, pages.flip(1).contiguous(), 16, **kw)
