@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(256) bwd_delta_kernel(const __nv_bfloat16 *__r
 // has three tile groups of MMAs to land.
 
 constexpr int Q_KST = 4;
+constexpr int FEW_KEYS = 64;     // rows that see fewer get an exact Delta
 enum {
     Q_QTM = 0,                   // Q tile landed
     Q_DOFULL = 1,                // dO rows in tensor memory (8 arrivals: the gradient warps)
@@ -239,7 +240,8 @@ enum {
     Q_FIN = 12 + 2 * Q_KST,
     Q_DRAIN = 13 + 2 * Q_KST,    // one commit per issuer (2)
     Q_QEMPTY = 14 + 2 * Q_KST,   // a unit's S MMAs complete: the Q tile may be reloaded
-    Q_NBAR = 15 + 2 * Q_KST
+    Q_DELTA = 15 + 2 * Q_KST,    // WIN: shares of an exact Delta written (8 arrivals)
+    Q_NBAR = 16 + 2 * Q_KST
 };
 
 template <int D>
@@ -369,15 +371,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     struct Item {
         Unit w;
         int kvh, n;      // kv head, key tiles
+        bool twice;      // WIN: the tiles pass twice, first for Delta
+        __device__ __forceinline__ int passes() const { return WIN && twice ? 2 * n : n; }   // tiles, both times
     };
     // the block's it-th unit; false: it has no more
     auto unit_of = [&](int it, Item &x) -> bool {
         if constexpr (WIN) {
             if (!window_q_unit(a, it, x.w)) return false;
             x.kvh = (int)a.by_group.div((unsigned)x.w.h);
-            x.n = WinIter<T>::count(a.win, x.w.q0 + a.win.off, x.w.qmax + a.win.off);
+            const int p0 = x.w.q0 + a.win.off;
+            x.n = WinIter<T>::count(a.win, p0, x.w.qmax + a.win.off);
+            const int behind = p0 + 1 - a.win.window;   // keys behind the first row's window
+            x.twice = (behind < 0 ? p0 + 1 : a.win.window + (behind < a.win.sinks ? behind : a.win.sinks)) < FEW_KEYS;
         } else {
             if (it > 0) return false;
+            x.twice = false;
             x.w = decode_unit_grouped(g, a.B, a.Hq, a.upc, T, blockIdx.x);
             x.kvh = x.w.h / (a.Hq / a.Hkv);
             x.n = KvIter<T>::count(g, x.w.r, x.w.qmax);
@@ -434,6 +442,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         mbar_init(BAR(Q_FIN), 1);
         mbar_init(BAR(Q_DRAIN), 2);
         mbar_init(BAR(Q_QEMPTY), 1);
+        mbar_init(BAR(Q_DELTA), 8);
         *abort_flag = 0;
         if constexpr (WIN) fixes->count = 0;
         fence_mbar_init();
@@ -462,7 +471,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int u = 0; ok && unit_of(u, x); ++u) {
                 Walk it;
                 start_walk(it, x.w);
-                for (int j = 0; j < x.n; ++j, it.next(), kr.next()) {
+                for (int j = 0; j < x.passes(); ++j, it.next(), kr.next()) {
+                    if (WIN && x.twice && j == x.n) start_walk(it, x.w);
                     if (nk >= Q_KST && !wait1(BAR(Q_KEMPTY + kr.st), kr.ph ^ 1, wc)) {
                         ok = false;
                         break;
@@ -497,7 +507,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 ++nq;
                 Walk it;
                 start_walk(it, x.w);
-                for (int j = 0; j < x.n; ++j, it.next()) {
+                for (int j = 0; j < x.passes(); ++j, it.next()) {
+                    if (WIN && x.twice && j == x.n) start_walk(it, x.w);
                     const int sv = nv & 1;
                     if (nv >= 2 && !wait1(BAR(Q_VEMPTY + sv), ((nv >> 1) - 1) & 1, wc)) {
                         ok = false;
@@ -534,7 +545,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 int nt = 0;
                 for (int u = 0; ok && unit_of(u, x); ++u) {
                     if (!waitw(BAR(Q_QTM), u & 1, wc)) break;
-                    for (int j = 0; j < x.n; ++j, ++nt, kr.next()) {
+                    const int n = x.passes();
+                    for (int j = 0; j < n; ++j, ++nt, kr.next()) {
                         const int sv = nt & 1;
                         if ((nt > 0 && !waitw(BAR(Q_SFREE), (nt - 1) & 1, wc)) ||
                             !waitw(BAR(Q_KFULL + kr.st), kr.ph, wc)) {
@@ -547,7 +559,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             ss_seq<0, D, 16384>(tS, dQd, dK, idSP);
                             mma_commit(BAR(Q_SDONE));
                             mma_commit(BAR(Q_KEMPTY + kr.st));
-                            if (WIN && j + 1 == x.n) mma_commit(BAR(Q_QEMPTY));
+                            if (WIN && j + 1 == n) mma_commit(BAR(Q_QEMPTY));
                         }
                         __syncwarp();
                         if ((nt > 0 && !waitw(BAR(Q_PFREE), (nt - 1) & 1, wc)) ||
@@ -571,7 +583,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 Item x;
                 int nt = 0;
                 for (int u = 0; ok && unit_of(u, x); ++u) {
-                    for (int j = 0; j < x.n; ++j, ++nt, kr.next()) {
+                    const int n = x.passes(), j0 = n - x.n;   // the tiles from j0 on have a dS
+                    for (int j = 0; j < n; ++j, ++nt, kr.next()) {
                         // dS(nt) written: the gradient warps have also read the previous
                         // unit's dQ, which this unit's first product overwrites
                         if (!waitw(BAR(Q_DS), nt & 1, wc) || !waitw(BAR(Q_KFULL + kr.st), kr.ph, wc)) {
@@ -579,13 +592,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             break;
                         }
                         const uint64_t dK = dKmn0 + (uint64_t)(kr.st * (TB >> 4));
-                        const uint32_t acc0 = j > 0 ? 1u : 0u;
+                        const uint32_t acc0 = j > j0 ? 1u : 0u;
                         if (leader) {
                             tc_fence_after();
-                            ts_mn_seq<0, T / 16, 0>(tDQ, tDS, dK, idDQ, acc0);
+                            if (j >= j0) ts_mn_seq<0, T / 16, 0>(tDQ, tDS, dK, idDQ, acc0);
                             mma_commit(BAR(Q_KEMPTY + kr.st));
                             mma_commit(BAR(Q_DSFREE));
-                            if (j + 1 == x.n) mma_commit(BAR(Q_FIN));
+                            if (j + 1 == n) mma_commit(BAR(Q_FIN));
                         }
                         __syncwarp();
                     }
@@ -632,6 +645,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // sectors, from L2, where the unit before had them sent (every lane its own row, from
         // memory: 244).  Each half leaves its share in shared memory, by the unit's parity;
         // Q_DOFULL tells of both.
+        // out has been rounded to bf16, which Delta takes over: an error of 2^-9 sqrt(sum P^2) of
+        // dQ and dK, as large as their own rounding where a row sees few keys.  Units with such
+        // rows (Item::twice) pass their tiles, two at most, twice, the first time for Delta =
+        // sum_j P dP in fp32.  (Window of 2: dQ off by 0.0024 of its norm where it was 0.0038, the
+        // rounding of the result alone is 0.0017; windows below 64 take 185 us a step of 8192 rows
+        // and 16 heads where they took 162, longer ones 1 to 3 us more.)
         float *shares = reinterpret_cast<float *>(smem_raw + C::OFF_DELTA);
         const bool rows32 = WIN && ((reinterpret_cast<uintptr_t>(dout) | reinterpret_cast<uintptr_t>(a.fix.out)) & 31) == 0;
         auto load_row = [&](const Unit &w, int u) -> Row {
@@ -700,7 +719,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             return r;
         };
         bool ok = true;
-        int nt = 0;
+        int nt = 0, nd = 0;                            // tiles, units with an exact Delta so far
         Item xn;
         bool have = unit_of(0, xn);
         Row rn{};
@@ -709,15 +728,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const Item x = xn;
             const Unit &w = x.w;
             const Row rw = rn;
-            const int qpos = rw.qpos, qp = rw.qp, n = x.n;
+            const int qpos = rw.qpos, qp = rw.qp;
             const bool valid = rw.valid;
+            float sum = 0.f;                           // of P dP, the first time
             const float lse2 = rw.lse2;
             float dlt = rw.dlt;
             if constexpr (WIN) {
                 if (!waitw(BAR(Q_DOFULL), u & 1, wc)) break;
                 const float *share = shares + (u & 1) * 2 * T + row;
                 dlt = share[0] + share[T];
-                if (valid && half == 0) a.delta[((int64_t)w.b * a.Hq + w.h) * a.S + qp] = dlt;
+                if (valid && half == 0 && !x.twice) a.delta[((int64_t)w.b * a.Hq + w.h) * a.S + qp] = dlt;
                 Item y;
                 if (unit_of(u + 1, y) && y.w.q0 + row < a.S) {   // the next unit's rows, on their way to L2
                     const int64_t at = (((int64_t)y.w.b * a.S + y.w.q0 + row) * a.Hq + y.w.h) * D + (D / 2) * half;
@@ -727,7 +747,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             Walk it;
             start_walk(it, w);
-            for (int j = 0; j < n; ++j, ++nt, it.next()) {
+            // one tile; FIRST: for Delta.  False: a wait ran out.
+            auto tile = [&](auto first) -> bool {
+                constexpr bool FIRST = decltype(first)::value;
                 const int ks = it.start(), kl = it.len();
                 int lim = kl;                              // visible columns [0, lim) of the tile
                 uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;   // WIN: visible columns, 32 each
@@ -748,10 +770,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     }
                 }
                 lim -= 64 * half;                          // in this half's local columns
-                if (!waitw(BAR(Q_SDONE), nt & 1, wc)) {
-                    ok = false;
-                    break;
-                }
+                if (!waitw(BAR(Q_SDONE), nt & 1, wc)) return false;
                 tc_fence_after();
                 uint32_t sr[64];
                 tmem_ld_x64(tS, sr);
@@ -784,16 +803,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         for (int e = 0; e < 64; ++e) p[e] = e < lim ? p[e] : 0.f;
                     }
                 }
-                if (!waitw(BAR(Q_PDONE), nt & 1, wc)) {
-                    ok = false;
-                    break;
-                }
+                if (!waitw(BAR(Q_PDONE), nt & 1, wc)) return false;
                 tc_fence_after();
                 uint32_t pr[64];
                 tmem_ld_x64(tP, pr);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(Q_PFREE));   // dP(j+1) may be issued
+                if constexpr (FIRST) {
+#pragma unroll
+                    for (int e = 0; e < 64; ++e)           // (dP of what the row does not see may be NaN)
+                        sum = p[e] == 0.f ? sum : fmaf(p[e], __uint_as_float(pr[e]), sum);
+                    if (nt > 0 && !waitw(BAR(Q_DSFREE), (nt - 1) & 1, wc)) return false;
+                    if (lane == 0) mbar_arrive(BAR(Q_DS));
+                    return true;
+                }
                 // dS = P (dP - Delta)
                 uint32_t pk[32];
 #pragma unroll
@@ -804,17 +828,31 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     pk[e] = pack_bf16(t0, t1);
                 }
                 // dS(j) may be written once dQ(j-1) has read dS(j-1)
-                if (nt > 0 && !waitw(BAR(Q_DSFREE), (nt - 1) & 1, wc)) {
-                    ok = false;
-                    break;
-                }
+                if (nt > 0 && !waitw(BAR(Q_DSFREE), (nt - 1) & 1, wc)) return false;
                 tc_fence_after();
                 tmem_st_x32(tDS, pk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(Q_DS));
+                return true;
+            };
+            if constexpr (WIN) {
+                if (x.twice) {
+                    for (int j = 0; ok && j < x.n; ++j, ++nt, it.next()) ok = tile(std::true_type{});
+                    if (!ok) break;
+                    start_walk(it, w);
+                    float *share = shares + (u & 1) * 2 * T + row;
+                    share[half * T] = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(Q_DELTA));
+                    if (!waitw(BAR(Q_DELTA), nd & 1, wc)) break;
+                    ++nd;
+                    dlt = share[0] + share[T];
+                    if (valid && half == 0) a.delta[((int64_t)w.b * a.Hq + w.h) * a.S + qp] = dlt;
+                }
             }
+            for (int j = 0; ok && j < x.n; ++j, ++nt, it.next()) ok = tile(std::false_type{});
             // the next unit's rows first: its S and dP run beside this unit's epilogue
             have = ok && unit_of(u + 1, xn);
             if (have) rn = load_row(xn.w, u + 1);

@@ -377,3 +377,17 @@ def test_one_row_that_is_not_finite(cuda_dev, dtype, bad, which):
     ref.within(dk[:, far], want[1][:, far], err[1][:, far], "dk")
     ref.within(dv[:, far], want[2][:, far], err[2][:, far], "dv")
     assert dq[:, hit].isnan().all()
+
+
+@pytest.mark.parametrize("S,W,K", [(1500, 2, 0), (1500, 3, 1), (1500, 17, 0), (1500, 63, 0), (1500, 64, 0), (1500, 8, 30),
+                                   (300, 300, 0), (1200, 1200, 0)])
+def test_gradients_of_rows_that_see_few_keys(cuda_dev, S, W, K):
+    """dQ and dK are off by two roundings to bf16, of dS and of the result, each as large as the other relative to
+    the norm, and independent: sqrt(2) of one of them.  What out's rounding leaves in Delta adds at most 2^-9 sqrt(sum P^2)
+    of the rows' share, sum P^2 about e / 64 where 64 keys are seen: sqrt(2 + e / 64) = 1.43; 1.5 leaves 5 % for the
+    spread of norms over 10^5 elements."""
+    q, k, v, do = make((2, S, S, 4, 2, 64, W, K), BF16, cuda_dev)
+    out, lse = api.window_attn_fwd(q, k, v, W, K)
+    grads = api.window_attn_bwd(q, k, v, out, lse, do, W, K)
+    for x, y in zip(grads[:2], ref.backward(q, k, v, do, W, K)[0]):
+        assert (x.double() - y).norm() <= 1.5 * (y.bfloat16().double() - y).norm()
