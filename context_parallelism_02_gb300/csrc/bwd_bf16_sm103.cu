@@ -735,9 +735,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             float dlt = rw.dlt;
             if constexpr (WIN) {
                 if (!waitw(BAR(Q_DOFULL), u & 1, wc)) break;
-                const float *share = shares + (u & 1) * 2 * T + row;
-                dlt = share[0] + share[T];
-                if (valid && half == 0 && !x.twice) a.delta[((int64_t)w.b * a.Hq + w.h) * a.S + qp] = dlt;
+                if (!x.twice) {
+                    const float *share = shares + (u & 1) * 2 * T + row;
+                    dlt = share[0] + share[T];
+                    if (valid && half == 0) a.delta[((int64_t)w.b * a.Hq + w.h) * a.S + qp] = dlt;
+                }
                 Item y;
                 if (unit_of(u + 1, y) && y.w.q0 + row < a.S) {   // the next unit's rows, on their way to L2
                     const int64_t at = (((int64_t)y.w.b * a.S + y.w.q0 + row) * a.Hq + y.w.h) * D + (D / 2) * half;
