@@ -5,12 +5,14 @@
 // Tiles of 32 rows by 64 columns, 128 threads as 8 x 16, each with a 4 x 4 part of the
 // scores (rows ty + 8 i, columns tx + 16 j) and of the 32 x D products 4 rows by D / 16
 // columns (4 tx + 64 j).  Per four elements of the inner axis a thread reads 8 x 16 bytes
-// of shared memory for 64 FMAs.  Small blocks, several to an SM, cover each other's loads
-// and leave less behind the mask than 64 x 64 tiles of 256 threads (which took 318 us where
-// these take 212 for a step of 2 x 1001 rows, 6 heads on 2, D = 64, window 200).  The walks are those
-// of the bf16 kernels: WinIter for the query-stationary kernels, WinQIter and the sinks'
-// pieces for dK and dV, whose heads of a group go to the blocks of a cluster and are added
-// up in order through distributed shared memory; every output element is written once.
+// of shared memory for 64 FMAs, which go in pairs.  Small blocks, several to an SM, cover
+// each other's loads and leave less behind the mask than 64 x 64 tiles of 256 threads.
+// A step of 2 x 1001 rows, 6 heads on 2, D = 64, window 200, 5 sinks takes 137 us; 162 with
+// single FMAs and a tile for the sinks alone, 318 with the large tiles (212 with the small
+// ones at the same stage).  The walks are those of the bf16 kernels: WinIter for the
+// query-stationary kernels, WinQIter and the sinks' pieces for dK and dV, whose heads of a
+// group go to the blocks of a cluster and are added up in order through distributed shared
+// memory; every output element is written once.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -19,6 +21,7 @@
 
 #include "cp_common.cuh"
 #include "kernels.h"
+#include "tc_helpers.cuh"
 #include "window_sinks.cuh"
 
 namespace cp {
@@ -47,17 +50,18 @@ struct Args {
     SinkPlan sp;
 };
 
-// n rows of x [B][S][H][D] (head h, from row r0) into COUNT rows of shared memory, the rest 0.
-// Returns NaN if one of the thread's elements is not finite, else 0.
+// n rows of x [B][S][H][D] (head h, from row r0; the first pk of them from row 0) into COUNT rows
+// of shared memory, the rest 0.  Returns NaN if one of the thread's elements is not finite, else 0.
 template <int D, int COUNT>
-__device__ __forceinline__ float load_rows(float *dst, const float *x, int64_t b, int S, int H, int h, int r0, int n)
+__device__ __forceinline__ float load_rows(float *dst, const float *x, int64_t b, int S, int H, int h, int r0, int n,
+                                           int pk = 0)
 {
     float odd = 0.f;
 #pragma unroll 8
     for (int i = threadIdx.x; i < COUNT * (D / 4); i += THREADS) {
         const int r = i / (D / 4), c = i % (D / 4);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < n) v = *reinterpret_cast<const float4 *>(x + ((b * S + r0 + r) * H + h) * D + c * 4);
+        if (r < n) v = *reinterpret_cast<const float4 *>(x + ((b * S + (r < pk ? r : r0 + r)) * H + h) * D + c * 4);
         *reinterpret_cast<float4 *>(dst + r * Rows<D>::STRIDE + c * 4) = v;
         odd = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, fmaf(v.w, 0.f, odd))));
     }
@@ -69,10 +73,11 @@ template <int D>
 __device__ __forceinline__ void dots(const float *A, const float *B, float (&acc)[4][4])
 {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float even[4][4], odd[4][4];   // sums over the even and the odd elements: pairs of FMAs
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) even[i][j] = odd[i][j] = 0.f;
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
         float4 a[4], b[4];
@@ -85,12 +90,14 @@ __device__ __forceinline__ void dots(const float *A, const float *B, float (&acc
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
-                acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
-                acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
-                acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+                tc::ffma2v(even[i][j], odd[i][j], a[i].x, a[i].y, b[j].x, b[j].y, even[i][j], odd[i][j]);
+                tc::ffma2v(even[i][j], odd[i][j], a[i].z, a[i].w, b[j].z, b[j].w, even[i][j], odd[i][j]);
             }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = even[i][j] + odd[i][j];
 }
 
 // acc[i][4 j + e] += sum_k P[ty + 8 i][k] B[k][4 tx + 64 j + e].  `odd`: B holds values that are
@@ -131,10 +138,9 @@ __device__ __forceinline__ void product(const float *P, const float *B, bool odd
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float x = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
-                    acc[i][4 * j + 0] = fmaf(x, b.x, acc[i][4 * j + 0]);
-                    acc[i][4 * j + 1] = fmaf(x, b.y, acc[i][4 * j + 1]);
-                    acc[i][4 * j + 2] = fmaf(x, b.z, acc[i][4 * j + 2]);
-                    acc[i][4 * j + 3] = fmaf(x, b.w, acc[i][4 * j + 3]);
+                    float *o = &acc[i][4 * j];
+                    tc::ffma2v(o[0], o[1], x, x, b.x, b.y, o[0], o[1]);
+                    tc::ffma2v(o[2], o[3], x, x, b.z, b.w, o[2], o[3]);
                 }
             }
     }
@@ -181,11 +187,11 @@ struct QUnit {
     }
 };
 
-// Rows of K or V for the walk's current tile.  No packed tiles here (win.pack is 0).
+// Rows of K or V for the walk's current tile; a packed one begins with the sinks.
 template <int D>
 __device__ __forceinline__ float load_keys(float *dst, const float *x, const Args &a, const QUnit &u, const WinIter<T> &it)
 {
-    return load_rows<D, T>(dst, x, u.b, a.Sk, a.Hkv, u.kvh, it.start(), it.len());
+    return load_rows<D, T>(dst, x, u.b, a.Sk, a.Hkv, u.kvh, it.start(), it.len(), it.packed() ? it.pk : 0);
 }
 
 template <int D>
@@ -275,7 +281,7 @@ __global__ void __launch_bounds__(THREADS) window_f32_delta_kernel(const Args a)
 }
 
 template <int D>
-__global__ void __launch_bounds__(THREADS) window_f32_dq_kernel(const Args a, float *__restrict__ dq)
+__global__ void __launch_bounds__(THREADS, 3) window_f32_dq_kernel(const Args a, float *__restrict__ dq)
 {
     extern __shared__ __align__(16) float sm[];
     float *Q = sm, *G = Q + Rows<D>::FEW, *K = G + Rows<D>::FEW, *V = K + Rows<D>::FLOATS, *P = V + Rows<D>::FLOATS;
@@ -464,7 +470,9 @@ Args make_args(const FwdArgs &f)
     a.Sk = f.Sk;
     a.scale = f.scale;
     a.win = f.win;
-    a.win.pack = 0;
+    // a few sinks begin the first tile of the window and need none of their own (5 sinks, window
+    // 200: 4 tiles instead of 5)
+    a.win.pack = f.win.sinks <= T / 2 ? f.win.sinks : 0;
     a.sp = window_f32_plan(a.win, a.Sq, a.Hq / a.Hkv);
     return a;
 }

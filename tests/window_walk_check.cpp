@@ -94,6 +94,7 @@ int main()
                     if (packed) w.pack = w.sinks <= 64 ? (w.sinks + 15) / 16 * 16 : 0;
                     rows_walk<256>(w, s[0], s[1], 128);
                     rows_walk<128>(w, s[0], s[1], 128);
+                    if (packed) w.pack = w.sinks <= 32 ? w.sinks : 0;
                     rows_walk<64>(w, s[0], s[1], 32);
                     if (packed) continue;
                     keys_walk<128, 128>(w, s[0], s[1], 1);
