@@ -108,6 +108,8 @@ int kv8_attn(const void *q, const void *cache, const float *scales, const int32_
     a.out = out;
     a.lse = lse;
     a.mass = mass;
+    const size_t rows = (size_t)B * n * Hq;
+    if (overlap(q, rows * D * 2, out, rows * D * (out_dtype == CP_F32 ? 4 : 2))) return CP_EINVAL;
     // no slot lies beyond the table
     const int64_t slots = (int64_t)max_pages * page;
     a.window = (int)(window > slots ? slots + 1 : window);

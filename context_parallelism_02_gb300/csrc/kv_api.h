@@ -1,4 +1,5 @@
-// kv_api.h -- argument checks that the entry points of the paged caches share.
+// kv_api.h -- argument checks that the entry points of the paged caches (and of windowed
+// attention) share.
 #pragma once
 
 #include <stdint.h>
@@ -25,7 +26,7 @@ inline bool aligned(const void *p, unsigned n) { return ((uintptr_t)p & (n - 1))
 inline bool overlap(const void *p, size_t np, const void *q, size_t nq)
 {
     const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-    return p && q && a < b + nq && b < a + np;
+    return np && nq && p && q && a < b + nq && b < a + np;
 }
 
 // Sizes that every call has; fills the pool except data and err.

@@ -5,23 +5,22 @@
 #include <math.h>
 #include <stdint.h>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "cp.h"
 #include "kernels.h"
+#include "kv_api.h"
 
 namespace cp {
 
 namespace {
 
-struct NvtxScope {
-    explicit NvtxScope(const char *name) { nvtxRangePushA(name); }
-    ~NvtxScope() { nvtxRangePop(); }
-    NvtxScope(const NvtxScope &) = delete;
-    NvtxScope &operator=(const NvtxScope &) = delete;
-};
+bool aligned16(const void *p) { return aligned(p, 16); }
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+// Whether an output of `bytes` lies over q, out or dout (of q_bytes), k or v (of k_bytes).
+bool over_inputs(const void *x, size_t bytes, const BwdPtrs &p, size_t q_bytes, size_t k_bytes)
+{
+    return overlap(x, bytes, p.q, q_bytes) || overlap(x, bytes, p.out, q_bytes) || overlap(x, bytes, p.dout, q_bytes) ||
+           overlap(x, bytes, p.k, k_bytes) || overlap(x, bytes, p.v, k_bytes);
+}
 
 // Checks what the windowed calls share and fills the arguments; 1: nothing to do.
 int window_args(int B, int Hq, int Hkv, int64_t Sq, int64_t Sk, int D, int64_t window, int64_t sinks, int dtype,
@@ -76,6 +75,9 @@ int window_attn_fwd(const void *q, const void *k, const void *v, void *out, floa
     if (rc || Sq == 0) return CP_OK;
     if (!q || !k || !v || !out || !lse) return CP_EINVAL;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || ((uintptr_t)lse & 3u)) return CP_EINVAL;
+    const size_t row = (size_t)B * D * (dtype == CP_BF16 ? 2 : 4), nq = row * Sq * Hq, nk = row * Sk * Hkv;
+    if (over_inputs(out, nq, BwdPtrs{q, k, v, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr}, nq, nk))
+        return CP_EINVAL;
     if (!(a.err = device_error_word())) return CP_ECUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == CP_F32)
@@ -116,8 +118,12 @@ int window_attn_bwd(const void *q, const void *k, const void *v, const void *out
         ((uintptr_t)lse & 3u))
         return CP_EINVAL;
     if (ws_bytes < window_bwd_workspace_bytes(B, Hq, Hkv, a.S, D, dtype, a.win)) return CP_EINVAL;
-    if (!(a.err = device_error_word())) return CP_ECUDA;
     const BwdPtrs p{q, k, v, out, lse, dout, dq, dk, dv, workspace};
+    const size_t row = (size_t)B * D * (dtype == CP_BF16 ? 2 : 4), nq = row * Sq * Hq, nk = row * Sk * Hkv;
+    if (over_inputs(dq, nq, p, nq, nk) || over_inputs(dk, nk, p, nq, nk) || over_inputs(dv, nk, p, nq, nk) ||
+        overlap(dq, nq, dk, nk) || overlap(dq, nq, dv, nk) || overlap(dk, nk, dv, nk))
+        return CP_EINVAL;
+    if (!(a.err = device_error_word())) return CP_ECUDA;
     if (dtype == CP_F32) return launch_window_bwd_f32(p, a, st);
     return launch_window_bwd_bf16(p, a, st);
 }

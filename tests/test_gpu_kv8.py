@@ -714,6 +714,14 @@ def test_a_bad_page_adds_no_mass_and_moves_as_zeros(cuda_dev):
     assert not (cache[spare[0], :, :, 4:16] & 0x7f).any() and torch.isfinite(scales[spare]).all()
 
 
+def test_attention_refuses_to_write_over_q(cuda_dev):
+    cache, scales, pages, _ = pool(5, 1, 64, 2, 64, 16)
+    q = torch.randn(1, 1, 4, 64, device=cuda_dev).bfloat16()
+    with pytest.raises(api.CpError) as e:
+        api.kv8_attn(q, cache, scales, pages, torch.tensor([64], **I32), out=q)
+    assert e.value.code == _lib.CP_EINVAL
+
+
 def test_evict_refuses_to_write_what_it_reads(cuda_dev):
     H, D, page, L = 2, 64, 16, 64
     cache, scales, pages, _ = pool(4, 2, L, H, D, page)

@@ -232,6 +232,14 @@ def test_refusals(cuda_dev):
     for kw in (dict(out=out.float()), dict(out=out[:, :32]), dict(lse=lse.double()), dict(lse=lse[:, :1])):
         with pytest.raises(ValueError):
             api.window_attn_fwd(q, k, v, 8, **kw)
+    with pytest.raises(api.CpError):                       # outputs over inputs
+        api.window_attn_fwd(q, k, v, 8, out=q)
+    for kw in (dict(dq=q), dict(dq=do), dict(dk=v), dict(dk=k), dict(dv=k)):
+        with pytest.raises(api.CpError):
+            api.window_attn_bwd(q, k, v, out, lse, do, 8, **kw)
+    both = torch.empty_like(k)
+    with pytest.raises(api.CpError):
+        api.window_attn_bwd(q, k, v, out, lse, do, 8, dk=both, dv=both)
     for kw in (dict(dq=k), dict(dk=q), dict(dv=v.float())):
         with pytest.raises(ValueError):
             api.window_attn_bwd(q, k, v, out, lse, do, 8, **kw)
