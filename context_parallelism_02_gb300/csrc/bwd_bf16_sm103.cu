@@ -942,7 +942,8 @@ enum {
     K_DPFREE = 13 + 2 * K_QST,    // 2 buffers: dK(s) complete, the dP^T columns may be rewritten
     K_KVEMPTY = 15 + 2 * K_QST,   // a unit's S^T and dP^T MMAs complete (2): K and V may be reloaded
     K_ACC = 16 + 2 * K_QST,       // a unit's dK read by its warpgroup (4 arrivals)
-    K_NBAR = 17 + 2 * K_QST
+    K_FINV = 17 + 2 * K_QST,      // WIN: a unit's dV complete (its dK: K_FIN)
+    K_NBAR = 18 + 2 * K_QST
 };
 
 template <int D>
@@ -1123,6 +1124,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_init(BAR(K_DPFREE + i), 1);
         }
         mbar_init(BAR(K_FIN), 1);
+        mbar_init(BAR(K_FINV), 1);
         mbar_init(BAR(K_DRAIN), 3);
         mbar_init(BAR(K_KVEMPTY), 2);
         mbar_init(BAR(K_ACC), 4);
@@ -1300,6 +1302,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             tc_fence_after();
                             ts_mn_seq<0, 4, 0>(tDV, tb, dQmn0 + so + (uint64_t)(HB >> 4), idKV, acc0);
                             mma_commit(BAR(K_SFREE + (gs & 1)));
+                            // warpgroup 0 writes dV while warpgroup 1 and the tensor cores are at the last dK
+                            if (WIN && s + 1 == x.ns) mma_commit(BAR(K_FINV));
                         }
                         __syncwarp();
                         // ... and before the first dK warpgroup 1 has read the previous unit's
@@ -1445,7 +1449,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(K_DSW + half));
             }
-            if (ok && ((WIN && ns == 0) || waitw(BAR(K_FIN), nf & 1, wc))) {
+            if (ok && ((WIN && ns == 0) || waitw(BAR(WIN && half == 0 ? K_FINV : K_FIN), nf & 1, wc))) {
                 tc_fence_after();
                 // half 0 writes dV, half 1 writes dK (times scale)
                 bool valid = row < w.kl;
