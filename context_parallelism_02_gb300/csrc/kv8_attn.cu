@@ -757,8 +757,10 @@ __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, 
                 low[threadIdx.x] = a.window > 0 ? max(lim - a.window, 0) : 0;
                 lse2[threadIdx.x] = a.lse[((int64_t)b * a.rows.Hq + head) * a.rows.n + j] * LOG2E;
                 whole = lim >= s0 + MASS_CHUNK && low[threadIdx.x] <= s0;
+            } else if ((int)threadIdx.x < MASS_ROWS) {
+                lse2[threadIdx.x] = INFINITY;                // rows that only fill up a four: weight 0
             }
-            if (__syncthreads_and(whole) && n % 4 == 0) {    // most chunks
+            if (__syncthreads_and(whole)) {                  // most chunks
                 for (int r = 0; r < n; r += 4) {
                     const float4 z = *reinterpret_cast<const float4 *>(lse2 + r);
                     float4 v[MASS_SLOTS];
