@@ -76,6 +76,10 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int PAD = Line<Kv8AttnArgs>::PAD, LEAST = Line<Kv8AttnArgs>::LEAST;
+// Rows of warps' parts in the workspace (twice): of all warps that run at once.  16 rows of 64
+// elements need more than MAX_ROWS: with two blocks on most SMs and three on some a step of 5
+// tokens, 20 rows a kv head, over 64 x 1024 took 55 us, with room for three on all 45.
+__host__ __device__ constexpr int part_rows(int D) { return D == 64 ? MAX_ROWS / 2 * 3 : MAX_ROWS; }
 constexpr int NB = 2;              // blocks of a stage, taken together
 constexpr int STAGES = 2;          // of a warp's ring
 
@@ -856,7 +860,7 @@ int launch(const Kv8AttnArgs &a, const Shape &sh, const CUtensorMap &map, cudaSt
         fills4[dev].store(resident4 * sm_count(), std::memory_order_relaxed);
         fills[dev].store(fill, std::memory_order_release);
     }
-    const int64_t ctas = min(fill, MAX_ROWS / (NT * 8 * WARPS));
+    const int64_t ctas = min(fill, part_rows(D) / (NT * 8 * WARPS));
     // an upper bound of an item's blocks from the sizes alone
     int64_t most = min((int64_t)a.pool.max_pages << (a.pool.page_shift - 4), (int64_t)1 << 27);
     if (a.window > 0 && !a.rows.vis)   // the sinks', the window's and the drafted tokens', each cut at both ends
@@ -899,7 +903,7 @@ int launch(const Kv8AttnArgs &a, const Shape &sh, const CUtensorMap &map, cudaSt
 size_t kv8_attn_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int64_t slots, bool mass)
 {
     if (D != 64 && D != 128) return 0;
-    const size_t parts = (size_t)2 * MAX_ROWS * (D + 2) * sizeof(float);
+    const size_t parts = (size_t)2 * part_rows(D) * (D + 2) * sizeof(float);
     if (!mass) return parts;
     const int64_t rows = score_rows((int64_t)n * (Hq / Hkv));
     const unsigned __int128 b = (unsigned __int128)(unsigned)B * (unsigned)Hkv * (uint64_t)rows * (uint64_t)slots * 4u;
@@ -910,7 +914,7 @@ size_t kv8_attn_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int64_t sl
 int launch_kv8_attn(const Kv8AttnArgs &given, int D, int64_t n_pages, cudaStream_t st)
 {
     Kv8AttnArgs a = given;
-    if (a.mass) a.scores = static_cast<float *>(a.ws) + (size_t)2 * MAX_ROWS * (D + 2);
+    if (a.mass) a.scores = static_cast<float *>(a.ws) + (size_t)2 * part_rows(D) * (D + 2);
     Shape sh;
     sh.group = a.rows.Hq / a.pool.Hkv;
     const int64_t rows = (int64_t)a.rows.n * sh.group;
