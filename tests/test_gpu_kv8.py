@@ -703,7 +703,8 @@ def test_a_bad_page_adds_no_mass_and_moves_as_zeros(cuda_dev):
     ws = torch.full((api.kv8_attn_workspace(1, 1, 4, H, D, page, pages.shape[1], True),), 0x7f, dtype=torch.uint8, device=cuda_dev)
     out, lse = api.kv8_attn(q, cache, scales, bad, lens, mass=mass, workspace=ws)
     assert api.cp_get_error() == _lib.CP_ECACHE
-    assert torch.isfinite(out).all() and (mass[..., 16:32] == 2).all() and (mass[..., :16] > 2).all()
+    # (2 plus a weight below 2^-23 is 2: the weights of the other slots show in their sum, 160 roundings of 2^-23)
+    assert torch.isfinite(out).all() and (mass[..., 16:32] == 2).all() and (mass >= 2).all()
     assert abs(float((mass[..., :L] - 2).sum()) - 4) < 1e-4
     spare = [p for p in range(cache.shape[0]) if p not in pages.flatten().tolist()][:2]
     mass.zero_()
