@@ -347,6 +347,9 @@ __device__ __forceinline__ void block_values(const uint8_t *tile, const uint32_t
     }
 }
 
+// The scales that an append or an eviction writes lie between these.
+constexpr float MIN_SCALE = 1.f / (1ull << -KV8_E_MIN), MAX_SCALE = (float)(1ull << KV8_E_MAX);
+
 // What goes with a block in the ring.
 struct Meta {
     int slot;            // its first slot, or NO_SLOT
@@ -560,6 +563,10 @@ __global__ void __launch_bounds__(W * 32)
                     src_row = (int)(slot & ((1 << ps) - 1));
                     src_plane = (int)kv8_plane(a.pool, id, it.h, 0);
                     src = Meta{(int)slot, *kv8_scale(a.pool, id, it.h, 0, src_row), *kv8_scale(a.pool, id, it.h, 1, src_row)};
+                    // A block that no row sees (under vis) may never have been written.  Its weights
+                    // are 0, but 0 times the 2^-e of such a scale could be NaN; its K scale only
+                    // meets scores that the mask replaces.
+                    if (!(src.v >= MIN_SCALE && src.v <= MAX_SCALE)) src.v = 1.f;
                 }
             }
         }
