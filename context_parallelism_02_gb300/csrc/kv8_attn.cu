@@ -170,7 +170,9 @@ __device__ __forceinline__ void make_rows(const Kv8AttnArgs &a, const Shape &sh,
                 r.q[t][2 * i + (e >> 1)][e & 1] =
                     h2(__floats2half2_rn(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xffff0000u) * up));
         }
-        const float back = a.scale * LOG2E / up;
+        // with an infinity in the row all visible scores could be -infinity, which the end would
+        // take for a row that sees nothing: NaN (which fp16 elements that are NaN bring by themselves)
+        const float back = top < INFINITY ? a.scale * LOG2E / up : __int_as_float(0x7fffffff);
         const int lim = on ? kv4_limit(a.rows, it.b, row / sh.group, len) : 0;
         const int low = a.window > 0 && on ? max(lim - a.window, 0) : 0;
 #pragma unroll
