@@ -57,6 +57,7 @@ struct Line<Kv4AttnArgs> {
     // with 4, 64 ragged sequences up to 8192 tokens take 38 us instead of 33, with 16 34
     static constexpr int PAD = 8;
     static constexpr int LEAST = 2;   // a stage (512 tokens: 8.5 us, with 4 9.0)
+    static constexpr bool NEXT_EARLY = true;
     template <bool EARLY>
     __device__ __forceinline__ static int blocks(const Kv4AttnArgs &a, int b)
     {

@@ -65,6 +65,7 @@ template <>
 struct Line<Kv8AttnArgs> {
     static constexpr int PAD = 8;
     static constexpr int LEAST = 2;   // a stage
+    static constexpr bool NEXT_EARLY = false;
     template <bool EARLY>
     __device__ __forceinline__ static int blocks(const Kv8AttnArgs &a, int b)
     {

@@ -13,10 +13,16 @@
 
 namespace cp {
 
-// Of the arguments A: PAD, LEAST and blocks<EARLY>(a, b), at least 1 (EARLY: by a kernel
-// that has not waited yet, see kv4_len).
+// Of the arguments A: PAD, LEAST, NEXT_EARLY and blocks<EARLY>(a, b), at least 1 (EARLY: by a
+// kernel that has not waited yet, see kv4_len).
 //   PAD    what an item costs beyond its blocks, in blocks
 //   LEAST  blocks that a warp takes at least
+//   NEXT_EARLY  the join lets the next kernel start before its own wait.  That is worth 1 us
+//          of 33 to the 4-bit cache (64 ragged sequences up to 8192 tokens: 32.1 us, behind
+//          the wait 33.1; its other cases do not tell).  The 8-bit cache's attention fills
+//          the registers of the SMs: a next call's blocks take what the join's are waiting
+//          for (8 x 16384 tokens, D = 64, 2 query heads a kv head: 28 us behind the wait, 42
+//          before it).
 template <typename A>
 struct Line;
 
@@ -264,10 +270,8 @@ __global__ void __launch_bounds__(JW * 32) kv_join_kernel(A a, Shape sh, int war
     // The lengths, and nothing else, are read before the wait: the attention kernel triggers
     // after its own, so this grid starts when what wrote them is complete.  The loads are
     // coherent at the GPU's scope: this SM may hold an older line of them.  (Behind the
-    // wait they cost a call 2 us: 131072 tokens 39.6 instead of 37.8.)  The next kernel is let
-    // start behind the wait only: where the attention kernel fills the registers of the SMs,
-    // a next call's blocks took what this kernel's were waiting for (8-bit cache, 8 x 16384
-    // tokens, D = 64, 2 query heads a kv head: 42 us with the trigger first, 28 so).
+    // wait they cost a call 2 us: 131072 tokens 39.6 instead of 37.8.)
+    if (Line<A>::NEXT_EARLY) kv4_trigger();
     int64_t all, before;
     count_blocks(a, b, all, before);
     all *= sh.per_batch;
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(JW * 32) kv_join_kernel(A a, Shape sh, int war
     const int64_t f = before * sh.per_batch + (int64_t)i * (nb + Line<A>::PAD);
     const int c0 = cuts.at(f), c1 = cuts.at(f + nb - 1);
     kv4_wait();
-    kv4_trigger();
+    if (!Line<A>::NEXT_EARLY) kv4_trigger();
     if (c0 == c1) return;
     const float *ws = static_cast<const float *>(a.ws);
     float m = -INFINITY, l = 0.f;
@@ -363,6 +367,7 @@ __global__ void __launch_bounds__(128) kv_join_rows_kernel(A a, Shape sh, int wa
     const int rr_all = (int)(row_all - item * sh.rows);
     const int b = (int)(item / heads), x = (int)(item - b * heads);   // x: (token, kv head)
     // as above: the lengths, and nothing else, before the wait
+    static_assert(!Line<A>::NEXT_EARLY, "the next kernel starts behind the wait");
     int64_t all, before;
     count_blocks(a, b, all, before);
     all *= sh.per_batch;
