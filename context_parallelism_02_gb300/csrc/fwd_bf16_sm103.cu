@@ -627,7 +627,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         dst[v4] = make_uint4(pk[4 * v4], pk[4 * v4 + 1], pk[4 * v4 + 2], pk[4 * v4 + 3]);
                 }
             }
-            if (p_valid && half == 0) *p_lse = (p_m + lg2(p_l)) * 0.69314718055994531f;
+            // (a sum of 0: all its scores are -infinity, and -infinity would be the lse of an empty row)
+            if (p_valid && half == 0)
+                *p_lse = p_l == 0.f ? __int_as_float(0x7fffffff) : (p_m + lg2(p_l)) * 0.69314718055994531f;
             const bool odd = p_valid && ((top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u);
             if (__any_sync(0xffffffffu, odd) && lane == 0) fixes->note(p_it, quarter);
             pend = false;

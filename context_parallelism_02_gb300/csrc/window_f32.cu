@@ -259,7 +259,9 @@ __global__ void __launch_bounds__(THREADS) window_f32_fwd_kernel(const Args a, f
         for (int j = 0; j < D / 64; ++j)
             *reinterpret_cast<float4 *>(row + 4 * tx + 64 * j) =
                 make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv);
-        if (tx == 0) lse[((int64_t)u.b * a.Hq + u.h) * a.Sq + u.q0 + r] = fmaf(m[i], LN2, logf(l[i]));
+        // (a sum of 0: all its scores are -infinity, and -infinity would be the lse of an empty row)
+        if (tx == 0)
+            lse[((int64_t)u.b * a.Hq + u.h) * a.Sq + u.q0 + r] = l[i] == 0.f ? __int_as_float(0x7fffffff) : fmaf(m[i], LN2, logf(l[i]));
     }
 }
 

@@ -1,0 +1,36 @@
+"""Windowed attention of ranks that hold a part of the rows each, and rows whose scores are all -infinity."""
+import math
+
+import pytest
+import torch
+
+from context_parallelism_02_gb300 import api
+from oracle import window as ref
+from test_gpu_window import BF16, F32, UNIT, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D,W", [(64, 1), (128, 1), (128, 3)])
+def test_a_row_whose_scores_are_all_minus_infinity(cuda_dev, dtype, D, W):
+    """It sees keys, so it is no empty row: its lse is NaN as its output is, and a merge does not drop it."""
+    S, H = 300, 2
+    q, k, v, do = make((1, S, S, H, 1, D, W, 0), dtype, cuda_dev)
+    k[..., 7] = k[..., 7].abs() + 0.5
+    o, z, eo, ez = ref.forward(q, k, v, W, 0, None, UNIT[dtype])
+    for at in (0, 1, 130, S - 1):
+        bad = q.clone()
+        bad[0, at, 1, 7] = -math.inf
+        out, lse = api.window_attn_fwd(bad, k, v, W)
+        rest = torch.ones(S, H, dtype=torch.bool, device=cuda_dev)
+        rest[at, 1] = False
+        assert out[0, at, 1].isnan().all() and lse[0, 1, at].isnan()
+        ref.within(out[0][rest], o[0][rest], eo[0][rest], "out")
+        ref.within(lse[0].T[rest], z[0].T[rest], ez[0].T[rest], "lse")
+        rows = lambda z: z.transpose(1, 2).float().contiguous()  # noqa: E731
+        merged, zm = api.lse_merge(out.float(), rows(lse), torch.ones_like(out.float()), torch.zeros_like(rows(lse)))
+        assert merged[0, at, 1].isnan().all() and zm[0, at, 1].isnan()
+        dq, dk, dv = api.window_attn_bwd(bad, k, v, out, lse, do, W)
+        assert api.cp_get_error() == 0
+        assert dq[0, at, 1].isnan().all() and dv[0, max(0, at - W + 1):at + 1].isnan().all()
