@@ -1575,7 +1575,7 @@ int launch_window_d(const BwdPtrs &p, BwdArgs a, cudaStream_t st)
     }
     a.upc = (a.S + T - 1) / T;
     a.tpc = (a.Sk + T - 1) / T;
-    a.sp = sink_plan<T, T>(a.win, a.S, a.Sk, a.Hq / a.Hkv);
+    a.sp = sink_plan<T, T>(a.win, a.S, a.Sk, a.Hq / a.Hkv, (int64_t)a.B * a.Hkv);
     const int64_t qunits = (int64_t)a.upc * a.B * a.Hq;
     const int64_t kunits = ((int64_t)a.tpc + (int64_t)a.sp.tiles * a.sp.pieces) * a.B * a.Hkv;
     if (qunits > 0x7fffffffLL || kunits > 0x7fffffffLL) return CP_EUNSUPPORTED;
@@ -1657,7 +1657,9 @@ size_t bwd_workspace_bytes(int B, int Hq, int64_t S)
 
 size_t window_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, int dtype, const Window &w)
 {
-    const SinkPlan sp = dtype == CP_BF16 ? sink_plan<T, T>(w, Sq, Sq + w.off, Hq / Hkv) : window_f32_plan(w, Sq, Hq / Hkv);
+    const int64_t heads = (int64_t)B * Hkv;
+    const SinkPlan sp = dtype == CP_BF16 ? sink_plan<T, T>(w, Sq, Sq + w.off, Hq / Hkv, heads)
+                                         : window_f32_plan(w, Sq, Hq / Hkv, heads);
     size_t b = bwd_workspace_bytes(B, Hq, Sq);
     if (sp.pieces) b += (size_t)B * Hkv * (size_t)window_part_rows(w, sp) * D * sizeof(float);
     return (b + 255u) & ~(size_t)255u;

@@ -406,6 +406,29 @@ CP_HD SinkPlan sink_plan(const Window &w, int Sq, int Sk, int grp)
     return s;
 }
 
+// The same for `heads` (batches times kv heads) side by side.  The pieces' partial gradients lie in
+// memory, 2 x sinks rows in fp32 for each: where sinks are many, as many pieces as above would take
+// hundreds of times what K takes (65536 sinks of 131072 rows, 8 heads, window 128: 138 GB), and
+// their tiles alone keep the SMs busy.  So pieces are no more than make the partial sums of all
+// sinks as long as K, or than make ENOUGH units in all, four for each SM.  (bf16 backward, with as
+// many as above and so: 32768 rows, 32 heads on 8, window 1024, 4096 sinks 6480 -> 6380 us with 172
+// MB instead of 877; 4 x 8192 rows, 8 heads, window 256, 512 sinks 558 -> 495; 16384 rows, 8 heads
+// on one, D = 64, window 128, 8192 sinks, where 10 long pieces a tile end unevenly, 1035 -> 1150.)
+template <int KEYS, int QUERIES>
+CP_HD SinkPlan sink_plan(const Window &w, int Sq, int Sk, int grp, int64_t heads)
+{
+    constexpr int ENOUGH = 4 * 152;
+    SinkPlan s = sink_plan<KEYS, QUERIES>(w, Sq, Sk, grp);
+    if (s.pieces == 0 || heads < 1) return s;
+    const int64_t tiles = s.tiles * heads, room = Sk / (2 * (int64_t)(w.sinks < Sk ? w.sinks : Sk));
+    const int64_t fill = (ENOUGH + tiles - 1) / tiles, most = room > fill ? room : fill;
+    if (s.pieces <= most) return s;
+    const int64_t all = (int64_t)s.each * s.pieces;
+    s.each = (int)((all + most - 1) / most);
+    s.pieces = (int)((all + s.each - 1) / s.each);
+    return s;
+}
+
 // The low n bits.
 CP_HD uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 

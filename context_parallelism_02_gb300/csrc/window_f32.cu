@@ -475,7 +475,7 @@ Args make_args(const FwdArgs &f)
     // a few sinks begin the first tile of the window and need none of their own (5 sinks, window
     // 200: 4 tiles instead of 5)
     a.win.pack = f.win.sinks <= T / 2 ? f.win.sinks : 0;
-    a.sp = window_f32_plan(a.win, a.Sq, a.Hq / a.Hkv);
+    a.sp = window_f32_plan(a.win, a.Sq, a.Hq / a.Hkv, (int64_t)a.B * a.Hkv);
     return a;
 }
 

@@ -20,9 +20,9 @@ CP_HD int window_f32_cluster(int grp)   // the largest divisor of the group up t
     while (grp % c) --c;
     return c;
 }
-CP_HD SinkPlan window_f32_plan(const Window &w, int Sq, int grp)
+CP_HD SinkPlan window_f32_plan(const Window &w, int Sq, int grp, int64_t heads)
 {
-    return sink_plan<WINDOW_F32_ROWS, WINDOW_F32_COLS>(w, Sq, Sq + w.off, grp / window_f32_cluster(grp));
+    return sink_plan<WINDOW_F32_ROWS, WINDOW_F32_COLS>(w, Sq, Sq + w.off, grp / window_f32_cluster(grp), heads);
 }
 
 // Partial gradients, fp32, [B][Hkv][1 + pieces][2 (dK, dV)][sinks][D]: slot 0 from the

@@ -1,4 +1,4 @@
-"""Windowed attention of ranks that hold a part of the rows each, and rows whose scores are all -infinity."""
+"""Windowed attention of ranks that hold a part of the rows each, of many sinks, and rows whose scores are all -infinity."""
 import math
 
 import pytest
@@ -6,7 +6,7 @@ import torch
 
 from context_parallelism_02_gb300 import api
 from oracle import window as ref
-from test_gpu_window import BF16, F32, UNIT, make
+from test_gpu_window import BF16, F32, UNIT, check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,10 @@ def test_a_row_whose_scores_are_all_minus_infinity(cuda_dev, dtype, D, W):
         dq, dk, dv = api.window_attn_bwd(bad, k, v, out, lse, do, W)
         assert api.cp_get_error() == 0
         assert dq[0, at, 1].isnan().all() and dv[0, max(0, at - W + 1):at + 1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(3, 2048, 2048, 8, 8, 64, 1, 1500), (4, 1000, 1300, 16, 8, 128, 100, 900)])
+def test_so_many_sinks_that_their_pieces_are_few(cuda_dev, dtype, shape):
+    """The rows behind the window go in fewer and longer pieces than a window's units are."""
+    check(shape, dtype, *make(shape, dtype, cuda_dev))
