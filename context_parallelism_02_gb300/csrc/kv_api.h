@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include <nvtx3/nvToolsExt.h>
 
 #include "cp.h"
@@ -27,6 +29,23 @@ inline bool overlap(const void *p, size_t np, const void *q, size_t nq)
 {
     const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
     return np && nq && p && q && a < b + nq && b < a + np;
+}
+
+// Whether one of the buffers that a call writes shares a byte with one that it reads, or with
+// another that it writes.
+struct Buffer {
+    const void *p;
+    size_t bytes;
+};
+inline bool writes_over(std::initializer_list<Buffer> writes, std::initializer_list<Buffer> reads)
+{
+    for (const Buffer *w = writes.begin(); w != writes.end(); ++w) {
+        for (const Buffer *x = writes.begin(); x != w; ++x)
+            if (overlap(w->p, w->bytes, x->p, x->bytes)) return true;
+        for (const Buffer &r : reads)
+            if (overlap(w->p, w->bytes, r.p, r.bytes)) return true;
+    }
+    return false;
 }
 
 // Sizes that every call has; fills the pool except data and err.

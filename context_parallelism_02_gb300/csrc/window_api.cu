@@ -15,13 +15,6 @@ namespace {
 
 bool aligned16(const void *p) { return aligned(p, 16); }
 
-// Whether an output of `bytes` lies over q, out or dout (of q_bytes), k or v (of k_bytes).
-bool over_inputs(const void *x, size_t bytes, const BwdPtrs &p, size_t q_bytes, size_t k_bytes)
-{
-    return overlap(x, bytes, p.q, q_bytes) || overlap(x, bytes, p.out, q_bytes) || overlap(x, bytes, p.dout, q_bytes) ||
-           overlap(x, bytes, p.k, k_bytes) || overlap(x, bytes, p.v, k_bytes);
-}
-
 // Checks what the windowed calls share and fills the arguments; 1: nothing to do.
 int window_args(int B, int Hq, int Hkv, int64_t Sq, int64_t Sk, int D, int64_t window, int64_t sinks, int dtype,
                 float scale, FwdArgs &a)
@@ -64,7 +57,6 @@ using namespace cp;
 
 extern "C" {
 
-
 int window_attn_fwd(const void *q, const void *k, const void *v, void *out, float *lse, int B, int Hq, int Hkv,
                     int64_t Sq, int64_t Sk, int D, int64_t window, int64_t sinks, int dtype, float scale, void *stream)
 {
@@ -76,8 +68,7 @@ int window_attn_fwd(const void *q, const void *k, const void *v, void *out, floa
     if (!q || !k || !v || !out || !lse) return CP_EINVAL;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || ((uintptr_t)lse & 3u)) return CP_EINVAL;
     const size_t row = (size_t)B * D * (dtype == CP_BF16 ? 2 : 4), nq = row * Sq * Hq, nk = row * Sk * Hkv;
-    if (over_inputs(out, nq, BwdPtrs{q, k, v, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr}, nq, nk))
-        return CP_EINVAL;
+    if (writes_over({{out, nq}, {lse, (size_t)B * Hq * Sq * 4}}, {{q, nq}, {k, nk}, {v, nk}})) return CP_EINVAL;
     if (!(a.err = device_error_word())) return CP_ECUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == CP_F32)
@@ -107,21 +98,21 @@ int window_attn_bwd(const void *q, const void *k, const void *v, const void *out
     if (rc) return CP_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!k || !v || !dk || !dv || !aligned16(k) || !aligned16(v) || !aligned16(dk) || !aligned16(dv)) return CP_EINVAL;
+    const size_t row = (size_t)B * D * (dtype == CP_BF16 ? 2 : 4), nq = row * Sq * Hq, nk = row * Sk * Hkv;
     if (Sq == 0) {   // no row sees the keys
-        const size_t bytes = (size_t)B * (size_t)Sk * Hkv * D * (dtype == CP_BF16 ? 2 : 4);
-        return cudaMemsetAsync(dk, 0, bytes, st) == cudaSuccess && cudaMemsetAsync(dv, 0, bytes, st) == cudaSuccess
-                   ? CP_OK
-                   : CP_ECUDA;
+        if (writes_over({{dk, nk}, {dv, nk}}, {{k, nk}, {v, nk}})) return CP_EINVAL;
+        return cudaMemsetAsync(dk, 0, nk, st) == cudaSuccess && cudaMemsetAsync(dv, 0, nk, st) == cudaSuccess ? CP_OK
+                                                                                                                : CP_ECUDA;
     }
     if (!q || !out || !lse || !dout || !dq || !workspace) return CP_EINVAL;
     if (!aligned16(q) || !aligned16(out) || !aligned16(dout) || !aligned16(dq) || !aligned16(workspace) ||
         ((uintptr_t)lse & 3u))
         return CP_EINVAL;
-    if (ws_bytes < window_bwd_workspace_bytes(B, Hq, Hkv, a.S, D, dtype, a.win)) return CP_EINVAL;
+    const size_t need = window_bwd_workspace_bytes(B, Hq, Hkv, a.S, D, dtype, a.win);
+    if (ws_bytes < need) return CP_EINVAL;
     const BwdPtrs p{q, k, v, out, lse, dout, dq, dk, dv, workspace};
-    const size_t row = (size_t)B * D * (dtype == CP_BF16 ? 2 : 4), nq = row * Sq * Hq, nk = row * Sk * Hkv;
-    if (over_inputs(dq, nq, p, nq, nk) || over_inputs(dk, nk, p, nq, nk) || over_inputs(dv, nk, p, nq, nk) ||
-        overlap(dq, nq, dk, nk) || overlap(dq, nq, dv, nk) || overlap(dk, nk, dv, nk))
+    if (writes_over({{dq, nq}, {dk, nk}, {dv, nk}, {workspace, need}},
+                    {{q, nq}, {k, nk}, {v, nk}, {out, nq}, {dout, nq}, {lse, (size_t)B * Hq * Sq * 4}}))
         return CP_EINVAL;
     if (!(a.err = device_error_word())) return CP_ECUDA;
     if (dtype == CP_F32) return launch_window_bwd_f32(p, a, st);

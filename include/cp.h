@@ -373,8 +373,8 @@ int ring_attn_bwd_noalloc(const void *q, const void *k, const void *v, const voi
  * Work goes with the visible pairs: tiles that no row of a query tile sees are not read.
  * What a row does not see has no influence on it, also where k and v hold NaN or infinities
  * there (rows whose tiles meet such a value are computed a second time, slowly).
- * Errors: CP_EINVAL (null pointer, misalignment, out over an input, Sq > Sk, window, sinks,
- * Hq % Hkv), CP_EUNSUPPORTED (D, dtype, Sk beyond 2^31 - 1025), CP_ECUDA.
+ * Errors: CP_EINVAL (null pointer, misalignment, out or lse over an input or one another,
+ * Sq > Sk, window, sinks, Hq % Hkv), CP_EUNSUPPORTED (D, dtype, Sk beyond 2^31 - 1025), CP_ECUDA.
  */
 int window_attn_fwd(const void *q, const void *k, const void *v, void *out, float *lse, int B, int Hq, int Hkv,
                     int64_t Sq, int64_t Sk, int D, int64_t window, int64_t sinks, int dtype, float scale,
@@ -389,8 +389,8 @@ int window_attn_fwd(const void *q, const void *k, const void *v, void *out, floa
  *   workspace: device, window_attn_bwd_workspace(...) bytes, 16-byte aligned, contents
  *   irrelevant; calls that may overlap on the GPU need their own.
  * No atomics: results repeat bit for bit.
- * Errors: as window_attn_fwd, plus a null, misaligned or too small workspace and gradients
- * over inputs or one another.
+ * Errors: as window_attn_fwd, plus a null, misaligned or too small workspace, and gradients
+ * or the workspace over inputs or one another.
  */
 int window_attn_bwd(const void *q, const void *k, const void *v, const void *out, const float *lse, const void *dout,
                     void *dq, void *dk, void *dv, int B, int Hq, int Hkv, int64_t Sq, int64_t Sk, int D,

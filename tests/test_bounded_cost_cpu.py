@@ -17,3 +17,43 @@ def test_workspace_of_many_sinks(B, Hq, Hkv, S, W, K, dtype):
     need = _lib.load().window_attn_bwd_workspace(B, Hq, Hkv, S, S, D, W, K, dtype)
     tiles = -(-K // tile) * B * Hkv
     assert need <= 256 + B * Hq * S * 4 + max(3 * B * Hkv * S * D * 4, (4 * 152 + 2 * tiles) * tile * 2 * D * 4) + 256
+
+
+def pointers(names):
+    """Addresses a GB apart: never touched, every call below is refused first."""
+    return {n: (i + 1) << 30 for i, n in enumerate(names)}
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_windowed_attention_refuses_outputs_over_what_it_reads(dtype):
+    """By its first bytes or its last ones: q and its like have B Sq Hq D elements, k B Sk Hkv D."""
+    B, Hq, Hkv, Sq, Sk, D = 2, 4, 2, 64, 100, 64
+    size = 4 if dtype == F32 else 2
+    nq, nk, nz = B * Sq * Hq * D * size, B * Sk * Hkv * D * size, B * Hq * Sq * 4
+    L = _lib.load()
+
+    def fwd(**kw):
+        p = pointers(["q", "k", "v", "out", "lse"]) | kw
+        return L.window_attn_fwd(*p.values(), B, Hq, Hkv, Sq, Sk, D, 8, 2, dtype, -1.0, None)
+
+    need = L.window_attn_bwd_workspace(B, Hq, Hkv, Sq, Sk, D, 8, 2, dtype)
+    names = ["q", "k", "v", "out", "lse", "dout", "dq", "dk", "dv"]
+
+    def bwd(ws=1 << 40, **kw):
+        p = pointers(names) | kw
+        return L.window_attn_bwd(*p.values(), B, Hq, Hkv, Sq, Sk, D, 8, 2, dtype, -1.0, ws, need, None)
+    at = pointers(["q", "k", "v", "out", "lse"])
+    read = dict(q=nq, k=nk, v=nk)
+    for name, mine in (("out", nq), ("lse", nz)):
+        for other, n in (read | {"lse" if name == "out" else "out": nz if name == "out" else nq}).items():
+            assert fwd(**{name: at[other] + n - 16}) == _lib.CP_EINVAL, (name, other)
+            assert fwd(**{name: at[other] - mine + 16}) == _lib.CP_EINVAL, (name, other)
+    at = pointers(names)
+    read = dict(q=nq, k=nk, v=nk, out=nq, lse=nz, dout=nq)
+    wrote = dict(dq=nq, dk=nk, dv=nk)
+    for name, mine in wrote.items():
+        for other, n in (read | {w: x for w, x in wrote.items() if w != name}).items():
+            assert bwd(**{name: at[other] + n - 16}) == _lib.CP_EINVAL, (name, other)
+            assert bwd(**{name: at[other] - mine + 16}) == _lib.CP_EINVAL, (name, other)
+    for other, n in (read | wrote).items():
+        assert bwd(ws=at[other] + n - 16) == bwd(ws=at[other] - need + 16) == _lib.CP_EINVAL, other
