@@ -24,6 +24,26 @@ int check_pool8(const void *cache, const float *scales, const int32_t *pages, co
     return CP_OK;
 }
 
+// The bytes of the pool and the tables.
+struct Sizes {
+    size_t cache, scales, pages, seqs;
+    Sizes(const Kv8Pool &p, int B, int D)
+    {
+        const size_t rows = (size_t)p.n_pages * p.Hkv * 2 << p.page_shift;
+        cache = rows * D;
+        scales = rows / KV8_BLOCK * 4;
+        pages = (size_t)B * p.max_pages * 4;
+        seqs = (size_t)B * 4;
+    }
+};
+
+// From the first byte of [B][n][H][D] rows to behind the last.
+size_t extent(const int64_t (&st)[3], int B, int n, int H, int D, int elem)
+{
+    const __int128 e = (__int128)(B - 1) * st[0] + (__int128)(n - 1) * st[1] + (__int128)(H - 1) * st[2] + D;
+    return e > (__int128)1 << 56 ? (size_t)1 << 60 : (size_t)e * elem;
+}
+
 }  // namespace
 
 }  // namespace cp
@@ -50,6 +70,11 @@ int kv8_append(const void *k, const void *v, void *cache, float *scales, const i
     if ((rc = set_strides(strides, n, Hkv, D, elem, a.ks)) ||
         (rc = set_strides(strides ? strides + 3 : nullptr, n, Hkv, D, elem, a.vs)))
         return rc;
+    const Sizes z(a.pool, B, D);
+    if (writes_over({{cache, z.cache}, {scales, z.scales}},
+                    {{k, extent(a.ks, B, n, Hkv, D, elem)}, {v, extent(a.vs, B, n, Hkv, D, elem)}, {pages, z.pages},
+                     {lens, z.seqs}, {n_new, z.seqs}}))
+        return CP_EINVAL;
     a.k = k;
     a.v = v;
     a.n_new = n_new;
@@ -72,6 +97,10 @@ int kv8_gather(const void *cache, const float *scales, const int32_t *pages, con
     if (too_many(B, count, Hkv)) return CP_EUNSUPPORTED;
     if (B == 0 || count == 0) return CP_OK;
     if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4)) return CP_EINVAL;
+    const Sizes z(a.pool, B, D);
+    const size_t rows = (size_t)B * count * Hkv * D * (dtype == CP_BF16 ? 2 : 4);
+    if (writes_over({{k, rows}, {v, rows}}, {{cache, z.cache}, {scales, z.scales}, {pages, z.pages}, {lens, z.seqs}, {start, z.seqs}}))
+        return CP_EINVAL;
     a.start = start;
     a.k = k;
     a.v = v;
@@ -108,8 +137,14 @@ int kv8_attn(const void *q, const void *cache, const float *scales, const int32_
     a.out = out;
     a.lse = lse;
     a.mass = mass;
+    const Sizes z(a.pool, B, D);
     const size_t rows = (size_t)B * n * Hq;
-    if (overlap(q, rows * D * 2, out, rows * D * (out_dtype == CP_F32 ? 4 : 2))) return CP_EINVAL;
+    if (writes_over({{out, rows * D * (out_dtype == CP_F32 ? 4 : 2)},
+                     {lse, rows * 4},
+                     {mass, z.pages * page * Hkv},
+                     {workspace, need}},
+                    {{q, rows * D * 2}, {cache, z.cache}, {scales, z.scales}, {pages, z.pages}, {lens, z.seqs}, {vis, z.seqs * n}}))
+        return CP_EINVAL;
     // no slot lies beyond the table
     const int64_t slots = (int64_t)max_pages * page;
     a.window = (int)(window > slots ? slots + 1 : window);
@@ -139,10 +174,11 @@ int kv8_evict(void *cache, float *scales, const int32_t *pages, const int32_t *l
     if (!pages_to || !kept || !lens_to || !aligned(pages_to, 4) || !aligned(kept, 4) || !aligned(lens_to, 4) ||
         !aligned(mass, 4) || !aligned(mass_to, 4) || (max_pages > 0 && !mass))
         return CP_EINVAL;
-    // written while other blocks of the launch still read
-    const size_t seqs = (size_t)B * 4, heads = (size_t)B * Hkv * 4;
-    if (overlap(lens, seqs, lens_to, seqs) ||
-        overlap(mass, heads * max_pages * page, mass_to, heads * max_to * page))
+    // (written while other blocks of the launch still read)
+    const Sizes z(a.pool, B, D);
+    const size_t to = (size_t)B * max_to * 4;
+    if (writes_over({{kept, z.seqs * Hkv * budget}, {lens_to, z.seqs}, {mass_to, to * page * Hkv}},
+                    {{cache, z.cache}, {scales, z.scales}, {pages, z.pages}, {lens, z.seqs}, {mass, z.pages * page * Hkv}, {pages_to, to}}))
         return CP_EINVAL;
     a.mass = mass;
     a.to = pages_to;

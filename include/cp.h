@@ -564,8 +564,9 @@ size_t kv4_select_workspace(int B, int n, int Hkv, int max_pages);
  * nearest even; magnitudes beyond 448 2^60 count as that, infinities and NaN are held as
  * NaN and do not count for the scale.
  * Within one call no two sequences may write the same page.
- * Errors: CP_EINVAL (null pointer, misalignment, sizes), CP_EUNSUPPORTED (D, dtype, page,
- * more rows or slots than a launch counts), CP_ECUDA.
+ * Errors: CP_EINVAL (null pointer, misalignment, sizes, something written over something
+ * read or over another output), CP_EUNSUPPORTED (D, dtype, page, more rows or slots than a
+ * launch counts), CP_ECUDA.
  */
 int kv8_append(const void *k, const void *v, void *cache, float *scales, const int32_t *pages, const int32_t *lens,
                const int32_t *n_new, const int64_t *strides, int B, int n, int Hkv, int D, int n_pages, int page,
@@ -603,8 +604,7 @@ int kv8_gather(const void *cache, const float *scales, const int32_t *pages, con
  *   workspace: device, kv8_attn_workspace(...) bytes, 16-byte aligned, contents irrelevant;
  *   calls that may overlap on the GPU need their own.
  * No atomics: results repeat bit for bit.
- * Errors: as kv8_append, plus CP_EINVAL for window, sinks, out over q and a null or too small
- * workspace.
+ * Errors: as kv8_append, plus CP_EINVAL for window, sinks and a null or too small workspace.
  */
 int kv8_attn(const void *q, const void *cache, const float *scales, const int32_t *pages, const int32_t *lens,
              const int32_t *vis, void *out, float *lse, float *mass, int B, int n, int Hq, int Hkv, int D, int n_pages,
@@ -629,7 +629,7 @@ size_t kv8_attn_workspace(int B, int n, int Hq, int Hkv, int D, int page, int ma
  *   max_to page >= budget >= 1; keep_first + keep_last <= budget.
  * The source pages stay as they are; pages_to must not name one of them, nor a page twice.
  * A kept token whose page number is out of range becomes zeros.
- * Errors: as kv8_append, plus CP_EINVAL for lens_to or mass_to that overlap lens or mass.
+ * Errors: as kv8_append, plus CP_EINVAL for budget, keep_first and keep_last.
  */
 int kv8_evict(void *cache, float *scales, const int32_t *pages, const int32_t *lens, const float *mass,
               const int32_t *pages_to, int32_t *kept, int32_t *lens_to, float *mass_to, int B, int Hkv, int D, int n_pages,

@@ -57,3 +57,41 @@ def test_windowed_attention_refuses_outputs_over_what_it_reads(dtype):
             assert bwd(**{name: at[other] - mine + 16}) == _lib.CP_EINVAL, (name, other)
     for other, n in (read | wrote).items():
         assert bwd(ws=at[other] + n - 16) == bwd(ws=at[other] - need + 16) == _lib.CP_EINVAL, other
+
+
+def refused(call, wrote, read):
+    """Every output, moved over the end of each other buffer and over its beginning."""
+    at = pointers([*wrote, *read])
+    for name, mine in wrote.items():
+        for other, n in (read | {w: x for w, x in wrote.items() if w != name}).items():
+            assert call(at | {name: at[other] + n - 16}) == _lib.CP_EINVAL, (name, other)
+            assert call(at | {name: at[other] - mine + 16}) == _lib.CP_EINVAL, (name, other)
+
+
+def test_the_8_bit_cache_refuses_outputs_over_what_it_reads():
+    B, n, Hq, H, D, P, page, M, to, budget = 8, 8, 6, 2, 64, 20, 32, 5, 3, 70
+    L = _lib.load()
+    pool = dict(cache=P * H * 2 * page * D, scales=P * H * 2 * page // 16 * 4)
+    tables = dict(pages=B * M * 4, lens=B * 4)
+    mass, rows = B * H * M * page * 4, B * n * H * D * 4
+
+    def append(p):
+        return L.kv8_append(p["k"], p["v"], p["cache"], p["scales"], p["pages"], p["lens"], p["n_new"], None, B, n, H, D, P, page, M,
+                            F32, None)
+    refused(append, pool, tables | dict(k=rows, v=rows, n_new=B * 4))
+
+    def gather(p):
+        return L.kv8_gather(p["cache"], p["scales"], p["pages"], p["lens"], p["start"], p["k"], p["v"], B, n, H, D, P, page, M, F32, None)
+    refused(gather, dict(k=rows, v=rows), pool | tables | dict(start=B * 4))
+    need = L.kv8_attn_workspace(B, n, Hq, H, D, page, M, 1)
+
+    def attn(p):
+        return L.kv8_attn(p["q"], p["cache"], p["scales"], p["pages"], p["lens"], p["vis"], p["out"], p["lse"], p["mass"], B, n, Hq, H,
+                          D, P, page, M, 0, 0, 1, F32, -1.0, p["ws"], need, None)
+    heads = B * n * Hq
+    refused(attn, dict(out=heads * D * 4, lse=heads * 4, mass=mass, ws=need), pool | tables | dict(q=heads * D * 2, vis=B * n * 4))
+
+    def evict(p):
+        return L.kv8_evict(p["cache"], p["scales"], p["pages"], p["lens"], p["mass"], p["to"], p["kept"], p["lens_to"], p["mass_to"], B,
+                           H, D, P, page, M, to, budget, 2, 8, None)
+    refused(evict, dict(kept=B * H * budget * 4, lens_to=B * 4, mass_to=B * H * to * page * 4), pool | tables | dict(mass=mass, to=B * to * 4))
