@@ -67,3 +67,95 @@ def test_rows_of_q_with_an_infinity(cuda_dev, L, window, sinks):
             ref, z, _, err, ez = o.attend(q[0, 0, x].double().cpu().numpy(), kk, vv, vs.astype(np.float64), D ** -0.5)
             d = np.abs(out[0, 0, x].double().cpu().numpy() - ref) - (err + 2.0 ** -8 * (np.abs(ref) + err))
             assert d.max() <= 0 and abs(lse[0, x].item() - z) <= ez
+
+
+def attention(lens, n, Hq, H, D, page, window, sinks, want_mass, seed, f32=False):
+    """One call against the definition, with a workspace of its own that has other things around it."""
+    B = len(lens)
+    cache, scales, pages, g = pool(seed, B, max(lens), H, D, page)
+    q = torch.randn(B, n, Hq, D, generator=g, device="cuda").bfloat16()
+    mass = torch.rand(B, H, pages.shape[1] * page, generator=g, device="cuda") if want_mass else None
+    before = mass.clone() if want_mass else None
+    need = api.kv8_attn_workspace(B, n, Hq, H, D, page, pages.shape[1], want_mass)
+    ws = torch.full((need + 512,), 0x5a, dtype=torch.uint8, device="cuda")
+    out = torch.empty(q.shape, dtype=F32, device="cuda") if f32 else None
+    out, lse = api.kv8_attn(q, cache, scales, pages, torch.tensor(lens, **I32), window=window, sinks=sinks, mass=mass, out=out,
+                            workspace=ws[256:256 + need])
+    ok()
+    assert (ws[:256] == 0x5a).all() and (ws[256 + need:] == 0x5a).all()
+    limits = [[x - (n - 1) + j for j in range(n)] for x in lens]
+    check_attn(q, cache, scales, pages, lens, out, lse, limits, window, sinks, mass=(before, mass) if want_mass else None)
+
+
+# lens, n, Hq, Hkv, D, page, window, sinks, mass.  An item has more blocks than a block of warps takes by itself, so
+# warps' stretches begin and end at all of its blocks: among the sinks, at the gap behind them, in the window.
+WINDOWS = [
+    ([5000, 3000, 1030], 1, 8, 8, 128, 32, 1024, 4, False),
+    ([5000, 900, 40], 3, 8, 4, 64, 16, 800, 70, True),
+    ([4000, 4001], 2, 8, 2, 128, 64, 1000, 300, True),
+    ([2600] * 30, 1, 8, 8, 64, 16, 1100, 20, False),          # more items than SMs
+    ([6000, 6000, 17], 6, 8, 2, 64, 128, 1500, 33, True),     # 24 rows: two tiles of 16
+    ([6000], 1, 1, 1, 128, 16, 3000, 1, True),
+    ([2300 - 45 * i for i in range(50)], 1, 16, 8, 128, 16, 1100, 20, False),   # few pieces an item: joined by a warp per row
+    ([1900 - 30 * i for i in range(50)], 2, 16, 8, 64, 32, 1040, 33, True),
+]
+
+
+@pytest.mark.parametrize("case", WINDOWS)
+def test_windows_with_sinks_through_stretches_and_join(cuda_dev, case):
+    attention(*case, seed=20 + len(case[0]))
+
+
+# D = 64 with tiles of 16 rows: the workspace has room for three blocks of warps an SM
+WIDE = [
+    ([16384, 16000], 4, 16, 4, 64, 64, 0, 0, False),          # as many warps as fit at once
+    ([1040] * 24, 5, 16, 4, 64, 16, 0, 0, False),             # 20 rows, 192 items
+    ([5000, 700, 3], 3, 16, 4, 64, 16, 0, 0, True),           # 12 rows
+    ([9000], 2, 16, 2, 64, 256, 0, 0, True),
+]
+
+
+@pytest.mark.parametrize("case", WIDE)
+def test_many_rows_of_64_elements_through_stretches_and_join(cuda_dev, case):
+    attention(*case, seed=40 + len(case[0]), f32=len(case[0]) == 1)
+
+
+# more rows of a kv head than the weights' kernel takes at a time (64): lengths with stretches of slots that all rows see
+# whole, and ends, windows and short sequences where they do not
+MANY_ROWS = [
+    ([2500, 1100], 5, 17, 1, 64, 32, 0, 0, True),             # 85 rows, no multiple of four
+    ([2500, 1100], 5, 17, 1, 64, 32, 700, 5, True),
+    ([3000, 70, 1], 8, 32, 2, 128, 64, 0, 0, True),           # 128 rows
+    ([3000, 70, 1], 8, 32, 2, 128, 64, 1200, 40, True),
+    ([400], 9, 29, 1, 64, 16, 0, 0, True),                    # 261 rows, a block of warps per item
+]
+
+
+@pytest.mark.parametrize("case", MANY_ROWS)
+def test_weights_of_many_rows(cuda_dev, case):
+    attention(*case, seed=60 + len(case[0]))
+
+
+def test_widths_of_the_table_agree(cuda_dev):
+    """A table for a far longer context takes other kernels: results differ by their roundings, each within what it may be off."""
+    lens, H, Hq, D, page = [500, 64, 1, 0, 333], 2, 6, 128, 64
+    got = []
+    for width in (8, 4000):
+        cache, scales, pages, g = pool(60, 5, 500, H, D, page, width)
+        q = torch.randn(5, 1, Hq, D, generator=g, device="cuda").bfloat16()
+        out = torch.empty(q.shape, dtype=F32, device="cuda")
+        got.append((out, api.kv8_attn(q, cache, scales, pages, torch.tensor(lens, **I32), out=out)[1]))
+    ok()
+    c, s, t = cache.cpu().numpy(), scales.cpu().numpy(), pages.cpu().numpy()
+    (a, za), (b, zb) = got
+    for i, L in enumerate(lens):
+        for x in range(Hq):
+            if not L:
+                assert not a[i].any() and not b[i].any() and torch.equal(za[i], zb[i])
+                continue
+            h, at = x * H // Hq, np.arange(L)
+            kk, vv = o.read(c, s, t, i, h, at)
+            ref, z, _, err, ez = o.attend(q[i, 0, x].double().cpu().numpy(), kk, vv, s[t[i, at // page], h, 1, at % page // 16].astype(np.float64),
+                                          D ** -0.5)
+            d = (a[i, 0, x].double() - b[i, 0, x].double()).abs().cpu().numpy()
+            assert (d <= 2 * (err + 2.0 ** -24 * (np.abs(ref) + err))).all() and abs(za[i, x] - zb[i, x]).item() <= 2 * ez

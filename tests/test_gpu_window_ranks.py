@@ -41,3 +41,31 @@ def test_a_row_whose_scores_are_all_minus_infinity(cuda_dev, dtype, D, W):
 def test_so_many_sinks_that_their_pieces_are_few(cuda_dev, dtype, shape):
     """The rows behind the window go in fewer and longer pieces than a window's units are."""
     check(shape, dtype, *make(shape, dtype, cuda_dev))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("S,Hq,Hkv,D,W,K,cuts", [(1200, 4, 2, 64, 200, 5, (0, 300, 600, 900, 1200)),
+                                                 (1000, 2, 2, 128, 130, 70, (0, 64, 65, 500, 1000)),
+                                                 (700, 4, 1, 64, 1, 0, (0, 350, 700))])
+def test_ranks_behind_their_halo_make_up_the_whole_gradient(cuda_dev, dtype, S, Hq, Hkv, D, W, K, cuts):
+    """Each rank's k and v are the sinks' rows, the window - 1 rows before its shard and the shard.  Its dQ rows are the
+    whole's, and dK and dV, sent back to where the rows came from and added up, too: each rank's within what its own call may
+    be off, and so their sum within the sum of that."""
+    q, k, v, do = make((2, S, S, Hq, Hkv, D, W, K), dtype, cuda_dev)
+    whole, _ = ref.backward(q, k, v, do, W, K, None, UNIT[dtype])
+    sums = [torch.zeros_like(x) for x in whole]
+    errs = [torch.zeros_like(x) for x in whole]
+    for a, b in zip(cuts, cuts[1:]):
+        lo = max(0, a - W + 1)
+        rows = torch.cat([torch.arange(min(K, lo)), torch.arange(lo, b)]).to(cuda_dev)
+        mine = torch.arange(a, b, device=cuda_dev)
+        args = [q[:, mine].contiguous(), k[:, rows].contiguous(), v[:, rows].contiguous()]
+        out, lse = api.window_attn_fwd(*args, W, K)
+        got = api.window_attn_bwd(*args, out, lse, do[:, mine].contiguous(), W, K)
+        assert api.cp_get_error() == 0
+        _, err = ref.backward(*args, do[:, mine], W, K, None, UNIT[dtype])
+        for i, at in enumerate((mine, rows, rows)):
+            sums[i].index_add_(1, at, got[i].double())
+            errs[i].index_add_(1, at, err[i])
+    for name, x, y, e in zip(("dq", "dk", "dv"), sums, whole, errs):
+        ref.within(x, y, e, name)
