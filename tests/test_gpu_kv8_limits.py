@@ -159,3 +159,31 @@ def test_widths_of_the_table_agree(cuda_dev):
                                           D ** -0.5)
             d = (a[i, 0, x].double() - b[i, 0, x].double()).abs().cpu().numpy()
             assert (d <= 2 * (err + 2.0 ** -24 * (np.abs(ref) + err))).all() and abs(za[i, x] - zb[i, x]).item() <= 2 * ez
+
+
+def test_a_prompts_last_tokens_say_what_is_evicted(cuda_dev):
+    """Prompt, append, the weights that its last tokens give to all, eviction, a step: the queries of a prompt as rows of kv8_attn."""
+    B, S, n, H, Hq, D, page, budget = 2, 700, 24, 2, 8, 64, 32, 200
+    g = torch.Generator(device="cuda").manual_seed(70)
+    M, To = -(-S // page), -(-budget // page) + 1
+    order = torch.randperm(B * (M + To), generator=g, device="cuda").int().reshape(B, -1)
+    pages, to = order[:, :M].contiguous(), order[:, M:].contiguous()
+    cache, scales = api.kv8_cache(B * (M + To), H, page, D)
+    q, k, v = (torch.randn(B, S, h, D, generator=g, device="cuda").bfloat16() for h in (Hq, H, H))
+    api.kv8_append(k, v, cache, scales, pages, torch.zeros(B, **I32))
+    lens, mass = torch.full((B,), S, **I32), torch.zeros(B, H, M * page, device="cuda")
+    last = q[:, -n:].contiguous()
+    out, lse = api.kv8_attn(last, cache, scales, pages, lens, mass=mass)
+    ok()
+    check_attn(last, cache, scales, pages, [S] * B, out, lse, [[S - n + 1 + j for j in range(n)]] * B, 0, 0, mass=(torch.zeros_like(mass), mass))
+    assert abs(float(mass.double().sum()) - B * n * Hq) <= 1e-3 * B * n * Hq
+    kept, lens_to, mass_to = api.kv8_evict(cache, scales, pages, lens, mass, to, budget, keep_first=4, keep_last=n)
+    for b in range(B):
+        for h in range(H):
+            np.testing.assert_array_equal(kept[b, h].cpu().numpy(), o.evict(mass[b, h].cpu().numpy(), S, budget, 4, n))
+    api.kv8_append(k[:, :1], v[:, :1], cache, scales, to, lens_to)
+    lens_to += 1
+    before = mass_to.clone()
+    out, lse = api.kv8_attn(last[:, :1].contiguous(), cache, scales, to, lens_to, mass=mass_to)
+    ok()
+    check_attn(last[:, :1].contiguous(), cache, scales, to, [budget + 1] * B, out, lse, [[budget + 1]] * B, 0, 0, mass=(before, mass_to))
