@@ -524,7 +524,8 @@ def kv8_attn(q, cache, scales, pages, lens, window: int = 0, sinks: int = 0, vis
     with ``window`` the last ``window`` of them and the first ``sinks``, as
     :func:`window_attn_fwd` (pages between them may be reused).  ``mass`` fp32
     ``[B, Hkv, max_pages * page]``: each slot's attention weight, summed over the rows of its
-    kv head, is added to it, for :func:`kv8_evict`.  No gradient.
+    kv head, is added to it, for :func:`kv8_evict` (from a prompt's last tokens, then from the
+    steps').  No gradient.
     """
     if stream is not None:
         with torch.cuda.stream(stream):
@@ -565,7 +566,7 @@ def window_attn_fwd(q, k, v, window: int, sinks: int = 0, scale: float | None = 
     """Causal attention with a sliding window and first tokens that stay visible; returns
     (out, lse).
 
-    q ``[B, Sq, Hq, D]``, k/v ``[B, Sk, Hkv, D]`` (fp32 or bf16), Sq <= Sk: row i stands at
+    q ``[B, Sq, Hq, D]``, k/v ``[B, Sk, Hkv, D]`` (fp32 or bf16, contiguous), Sq <= Sk: row i stands at
     position ``p = i + Sk - Sq`` and sees key j iff ``j <= p and (j > p - window or
     j < sinks)``.  out like q, lse ``[B, Hq, Sq]`` fp32.  A chunk of a prompt, or the shard
     of a context-parallel rank, passes its own rows as q and as k and v the sinks' rows,

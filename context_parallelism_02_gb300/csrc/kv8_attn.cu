@@ -81,6 +81,7 @@ constexpr int PAD = Line<Kv8AttnArgs>::PAD, LEAST = Line<Kv8AttnArgs>::LEAST;
 // elements need more than MAX_ROWS: with two blocks on most SMs and three on some a step of 5
 // tokens, 20 rows a kv head, over 64 x 1024 took 55 us, with room for three on all 45.
 __host__ __device__ constexpr int part_rows(int D) { return D == 64 ? MAX_ROWS / 2 * 3 : MAX_ROWS; }
+static_assert(part_rows(64) / 8 < MAX_STRETCHES && part_rows(128) / 8 < MAX_STRETCHES, "a warp's part has 8 rows at least");
 constexpr int NB = 2;              // blocks of a stage, taken together
 constexpr int STAGES = 2;          // of a warp's ring
 
@@ -817,11 +818,21 @@ __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, 
     }
 }
 
-// Short tables: a block per item where the items fit the SMs at once (see kv4_attn.cu; the same
-// sizes), or twice over where they are of 512 tokens at most (8 kv heads, D = 128: 64 x 256 tokens
-// 13.9 us where stretches and join take 17.5, 48 x 512 17.8 against 19.8, 64 ragged ones up to 512
-// 14.0 against 13.3; 48 x 1024 27.9 against 26.1, 64 ragged ones up to 1024 23.1 against 19.8, and
-// 128 x 256, four times over, 25.2 against 23.5).
+// Short tables: a block per item where the items fit the SMs at once, or twice over where they are of
+// 512 tokens at most (8 kv heads, D = 128: 64 x 256 tokens 13.9 us where stretches and join take
+// 17.5, 48 x 512 17.8 against 19.8, 64 ragged ones up to 512 14.0 against 13.3; 48 x 1024 27.9
+// against 26.1, 64 ragged ones up to 1024 23.1 against 19.8, and 128 x 256, four times over, 25.2
+// against 23.5).  The limits are the 4-bit kernel's.  Measured here, block per item against stretches
+// and join (8 kv heads, 4 query heads each; D = 128 with one token, D = 64 with one, D = 64 with three,
+// which is two tiles):
+//   1 x 512     7.5 / 8.1     6.5 / 7.6     7.9 / 8.8       8 warps, up to 48 blocks
+//   1 x 1024    10.1 / 8.3    8.4 / 7.7     10.5 / 9.1      8 warps, beyond
+//   16 x 2048   16.7 / 20.9   12.7 / 15.7   16.3 / 20.5     8 warps, up to 128 blocks
+//   24 x 1024   15.3 / 18.9   12.4 / 15.3   15.4 / 20.3     4 warps, up to 64 blocks
+//   48 x 512    18.6 / 20.2   10.6 / 17.8   12.0 / 21.6     4 warps, up to 32 blocks (twice over with D = 128)
+//   64 x 1024   30.0 / 31.5   16.7 / 21.0   30.5 / 30.7     4 warps (stretches, but with D = 64 and one token)
+// and where the rule stays with stretches although a block per item is faster: 152 items of 3000 tokens
+// 22.9 / 27.7, 256 items under a window of 1000 with 4 sinks (65 blocks) 16.5 / 22.4, ragged or not.
 constexpr int ALONE_WARPS = 8, ALONE_BLOCKS = 48, ALONE_BLOCKS_MANY = 128, ALONE_BLOCKS_FULL = 64, ALONE_BLOCKS_TWICE = 32;
 
 // The pool as [plane][row][D bytes], boxes of 16 rows.

@@ -11,11 +11,12 @@
 //           latency: five cluster barriers and the passes over the keys, BATCH loads at a time
 //           (rounds of 11 bits save one, but summing 2048 bins costs 4000 cycles each; a run
 //           of slots per thread, with its bank conflicts and one load at a time, took 15000
-//           cycles for the last two passes: 8 rows of 65536 slots 28 us, these 19).
+//           cycles for the last two passes and 9 us longer).  8 rows of 65536 slots cut to 16,
+//           with next to nothing to move, 17 us; 128 rows of 8192 19.
 //   move    a warp per 16 kept tokens and kv head copies their rows of D bytes, K and V, into a
 //           block of the other pages, under the largest of their scales.  Bounded by the chain
 //           kept slot, page, scale and row, then by HBM (K and V by warps of their own, twice the
-//           chains: 1 us longer).
+//           chains: 1 us longer).  8 rows of 65536 slots to 16384: 14 us on top of the selection.
 #include <cooperative_groups.h>
 
 #include <atomic>

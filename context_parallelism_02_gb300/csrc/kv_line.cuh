@@ -95,7 +95,12 @@ struct Part {              // a piece's result in the workspace
     static constexpr int FLOATS = NT * 8 * (D + 2);   // m, l of each row, then the rows
 };
 
-constexpr int MAX_ROWS = 2560 * 8;   // rows of warps' parts that the workspace has room for (twice)
+// Rows of warps' parts that the workspace has room for (twice); kv8_attn.cu has room for more of
+// 64 elements.
+constexpr int MAX_ROWS = 2560 * 8;
+// Stretches, one a warp, are fewer than this: Cuts multiplies two numbers below theirs in 32 bits.
+constexpr int MAX_STRETCHES = 1 << 16;
+static_assert(MAX_ROWS / 8 < MAX_STRETCHES, "a warp's part has 8 rows at least");
 
 // A walk over the pieces of a warp's stretch.
 struct Walk {
@@ -162,7 +167,7 @@ struct Cuts {
     }
     __device__ __forceinline__ int64_t begin(int c) const
     {
-        return each * c + (unsigned)over * (unsigned)c / (unsigned)n;   // n is at most 2560
+        return each * c + (unsigned)over * (unsigned)c / (unsigned)n;   // over and c below MAX_STRETCHES
     }
     __device__ __forceinline__ int at(int64_t f) const
     {

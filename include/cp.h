@@ -365,14 +365,15 @@ int ring_attn_bwd_noalloc(const void *q, const void *k, const void *v, const voi
  * the window - 1 rows before its shard and its own, since only distances inside the
  * window and the number of the sinks matter (a rank whose halo reaches the sinks passes
  * all rows from 0 on).
- *   q [B][Sq][Hq][D], k, v [B][Sk][Hkv][D], out [B][Sq][Hq][D]: device, dtype CP_BF16 or
- *   CP_F32; lse [B][Hq][Sq] fp32, natural log.  D in {64, 128}; Hq % Hkv == 0.
+ *   q [B][Sq][Hq][D], k, v [B][Sk][Hkv][D], out [B][Sq][Hq][D]: device, contiguous, dtype
+ *   CP_BF16 or CP_F32; lse [B][Hq][Sq] fp32, natural log.  D in {64, 128}; Hq % Hkv == 0.
  *   window >= 1 (Sk and more: no limit), sinks >= 0; scale <= 0 selects 1/sqrt(D).
  *   CP_BF16 runs on the tensor cores (bf16 operands and weights, fp32 accumulation),
  *   CP_F32 on the CUDA cores in fp32 arithmetic.
  * Work goes with the visible pairs: tiles that no row of a query tile sees are not read.
  * What a row does not see has no influence on it, also where k and v hold NaN or infinities
- * there (rows whose tiles meet such a value are computed a second time, slowly).
+ * there (rows whose tiles meet such a value are computed a second time, slowly).  A row that does
+ * see such values, or only scores of -infinity, has NaN as its lse: -infinity is an empty row's.
  * Errors: CP_EINVAL (null pointer, misalignment, out or lse over an input or one another,
  * Sq > Sk, window, sinks, Hq % Hkv), CP_EUNSUPPORTED (D, dtype, Sk beyond 2^31 - 1025), CP_ECUDA.
  */
@@ -398,7 +399,8 @@ int window_attn_bwd(const void *q, const void *k, const void *v, const void *out
                     void *stream);
 
 /* window_attn_bwd_workspace -- bytes of scratch window_attn_bwd needs (Delta, and the
- * sinks' partial gradients); 0 for arguments that it refuses.  Host only. */
+ * sinks' partial gradients: B Sk Hkv D fp32 four times at most, or 240 MB where that is more); 0
+ * for arguments that it refuses.  Host only. */
 size_t window_attn_bwd_workspace(int B, int Hq, int Hkv, int64_t Sq, int64_t Sk, int D, int64_t window, int64_t sinks,
                                  int dtype);
 
@@ -596,11 +598,15 @@ int kv8_gather(const void *cache, const float *scales, const int32_t *pages, con
  *   influence on it, whatever those slots hold.
  *   mass [B][Hkv][max_pages page] fp32 or NULL: += the weights e^(s - lse) that each slot
  *   got, summed over the rows of its kv head; slots that no row sees, and those of pages
- *   that are not there, stay as they are.
+ *   that are not there, stay as they are.  s and lse are fp32: a weight is off by about 2^-23
+ *   (|s| + |lse|) of itself.  The rows may be a prompt's last tokens, right after it was
+ *   appended (causal: they see what they saw in the prompt); all rows of 16 read the cache once.
  *   fp32 sums; K, V and q enter exactly (an element of q below 2^-31 of its row's largest is
  *   rounded); the product of a weight and its block's V scale is rounded to fp16 (2^-11 of
- *   itself, or 2^-32 of the row's largest such product).  scale <= 0 selects 1/sqrt(D).  A row
- *   of q with a value that is not finite comes out as NaN.
+ *   itself, or 2^-32 of the row's largest such product), also where out is fp32.  scale <= 0
+ *   selects 1/sqrt(D).  A row of q with a value that is not finite comes out as NaN.  Scores
+ *   beyond fp32's range count as infinities: a row all of whose scores lie below it comes out as
+ *   one that sees nothing.
  *   workspace: device, kv8_attn_workspace(...) bytes, 16-byte aligned, contents irrelevant;
  *   calls that may overlap on the GPU need their own.
  * No atomics: results repeat bit for bit.
