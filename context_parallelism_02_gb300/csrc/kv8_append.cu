@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(WARPS * 32, sizeof(T) == 2 ? 4 : 2) kv8_append
     const int64_t len = kv4_len(a.pool, b);
     const int n = a.n_new ? max(0, min(a.n_new[b], a.n)) : a.n;
     const int64_t slot0 = (len / KV8_BLOCK + t) * KV8_BLOCK;    // the block's first slot
-    if (slot0 >= len + n) return;
+    if (n == 0 || slot0 >= len + n) return;                     // (without new tokens: its pages may be gone)
     const int lo = slot0 < len ? (int)(len - slot0) : 0;        // rows [lo, hi) of the block are new
     const int hi = (int)(len + n - slot0 < KV8_BLOCK ? len + n - slot0 : KV8_BLOCK);
     const int64_t *st = which ? a.vs : a.ks;

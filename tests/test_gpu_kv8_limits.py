@@ -187,3 +187,35 @@ def test_a_prompts_last_tokens_say_what_is_evicted(cuda_dev):
     out, lse = api.kv8_attn(last[:, :1].contiguous(), cache, scales, to, lens_to, mass=mass_to)
     ok()
     check_attn(last[:, :1].contiguous(), cache, scales, to, [budget + 1] * B, out, lse, [[budget + 1]] * B, 0, 0, mass=(before, mass_to))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_sequences_without_new_tokens_need_no_pages(cuda_dev, n):
+    """A padded batch whose idle sequences have lengths of before and no pages: nothing is written, read or reported for them."""
+    H, D, page = 2, 64, 16
+    cache, scales, pages, g = pool(14, 3, 100, H, D, page)
+    was, were = cache.clone(), scales.clone()
+    k = torch.randn(3, n, H, D, generator=g, device="cuda").bfloat16()
+    pages[1:] = -1
+    api.kv8_append(k, k, cache, scales, pages, torch.tensor([0, 37, 99], **I32), n_new=torch.tensor([n, 0, -2], **I32))
+    ok()
+    mine = torch.zeros(cache.shape[0], dtype=torch.bool, device="cuda")
+    mine[pages[0].long()] = True
+    assert torch.equal(cache[~mine], was[~mine])
+    assert torch.equal(scales[~mine].nan_to_num(-1), were[~mine].nan_to_num(-1))
+
+
+def test_evict_of_rows_that_just_fit_shared_memory(cuda_dev):
+    """A cluster of eight blocks with 195 KB of keys each."""
+    page, D, L, budget = 256, 64, 390000, 1000
+    M, To = -(-L // page), 4
+    g = torch.Generator(device="cuda").manual_seed(2)
+    cache = torch.randint(0, 127, (M + To, 1, 2, page, D), dtype=torch.uint8, generator=g, device="cuda")
+    scales = torch.ones(M + To, 1, 2, page // 16, device="cuda")
+    pages, to = torch.arange(M, **I32)[None], torch.arange(M, M + To, **I32)[None]
+    mass = torch.rand(1, 1, M * page, generator=g, device="cuda")
+    kept, _, mass_to = api.kv8_evict(cache, scales, pages, torch.tensor([L], **I32), mass, to, budget, 3, 10)
+    ok()
+    want = o.evict(mass[0, 0].cpu().numpy(), L, budget, 3, 10)
+    np.testing.assert_array_equal(kept[0, 0].cpu().numpy(), want)
+    np.testing.assert_array_equal(mass_to[0, 0, :budget].cpu().numpy(), mass[0, 0].cpu().numpy()[want])
