@@ -1683,8 +1683,8 @@ BwdArgs bwd_args(const FwdArgs &f)
     a.err = f.err;
     a.limit_ns = f.limit_ns;
     a.drain_ns = f.drain_ns;
-    a.Sk = f.Sk;
-    a.win = f.win;
+    a.Sk = 0;
+    a.win = Window{0, 0, 0, 0};
     a.sp = SinkPlan{0, 0, 1};
     a.part = a.delta = nullptr;
     a.n_units = 0;
@@ -1695,10 +1695,13 @@ BwdArgs bwd_args(const FwdArgs &f)
 
 }  // namespace
 
-int launch_window_bwd_bf16(const BwdPtrs &p, const FwdArgs &f, cudaStream_t st)
+int launch_window_bwd_bf16(const BwdPtrs &p, const WindowArgs &f, cudaStream_t st)
 {
-    if (f.D == 64) return launch_window_d<64>(p, bwd_args(f), st);
-    if (f.D == 128) return launch_window_d<128>(p, bwd_args(f), st);
+    BwdArgs a = bwd_args(f);
+    a.Sk = f.Sk;
+    a.win = f.win;
+    if (f.D == 64) return launch_window_d<64>(p, a, st);
+    if (f.D == 128) return launch_window_d<128>(p, a, st);
     return CP_EUNSUPPORTED;
 }
 

@@ -175,10 +175,14 @@ struct NoMaps {
 };
 template <int MODE>
 using ModeMaps = std::conditional_t<MODE == MODE_WINDOW, PackMaps, NoMaps>;
+// (As a plain parameter: declared __grid_constant__, the ring's instantiations took up to 2.5 %
+// longer, 8192 rows in 8 ranks with D = 64 95.6 us instead of 93.1.)
+template <int MODE>
+using ModeArgs = std::conditional_t<MODE == MODE_WINDOW, WindowArgs, FwdArgs>;
 
 // MODE_WINDOW's items: heads fastest, then batch, rows descending; a block takes rounds of
 // gridDim.x items, alternately forwards and backwards.  False: the block has no it-th item.
-__device__ __forceinline__ bool window_unit(const FwdArgs &a, int it, Unit &w)
+__device__ __forceinline__ bool window_unit(const WindowArgs &a, int it, Unit &w)
 {
     const int64_t G = gridDim.x, c = blockIdx.x, item = it * G + ((it & 1) ? G - 1 - c : c);
     if (item >= a.n_units) return false;
@@ -194,7 +198,7 @@ __device__ __forceinline__ bool window_unit(const FwdArgs &a, int it, Unit &w)
 
 // MODE_WINDOW: the noted rows of the block's units again (window_fix.cuh), by its softmax warps.
 template <int D>
-__device__ __noinline__ void window_fix(const FixList &list, const FwdArgs &a, __nv_bfloat16 *out, const float *lse)
+__device__ __noinline__ void window_fix(const FixList &list, const WindowArgs &a, __nv_bfloat16 *out, const float *lse)
 {
     const int warp = (threadIdx.x >> 5) - 4;
     const FixArgs f{static_cast<const __nv_bfloat16 *>(a.q), static_cast<const __nv_bfloat16 *>(a.k),
@@ -221,7 +225,7 @@ __device__ __noinline__ void window_fix(const FixList &list, const FwdArgs &a, _
 template <int D, int MODE, bool PERSIST>
 __global__ void __launch_bounds__(NTHREADS, 1)
     fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdArgs a, const float sl2,
+                    const __grid_constant__ CUtensorMap tmV, const ModeArgs<MODE> a, const float sl2,
                     __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, const SplitOut so,
                     const StepOut stp, const __grid_constant__ ModeMaps<MODE> pm_maps)
 {
@@ -251,7 +255,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // extents of the tensor maps' (rank, row) dimensions, for the debug-bounds build
     const int map_r = (!STEP && striped(g)) ? g.N : 1;
     const int map_rows = STEP ? C_loc : a.S / map_r;
-    const int map_keys = WIN ? a.Sk : map_rows;
     auto start_walk = [&](Walk &it, const Unit &w) {
         if constexpr (WIN) it.begin(a.win, w.q0 + a.win.off, w.qmax + a.win.off);
         else if constexpr (STEP) it.begin_steps(g, w.r, w.qmax, stp.step_k, stp.step_k + 1);
@@ -370,108 +373,141 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // Items with keys only, decoded one ahead while the current one loads;
             // the next unit's Q goes out between the current unit's last K and
             // last V (its S MMAs are done by then), so that the next unit's first
-            // S can run while the softmax warps finish this unit's epilogue.  MODE_WINDOW
-            // sends the next unit's first K along with it: units are short.
+            // S can run while the softmax warps finish this unit's epilogue.
             int it = 0;
             Item x;
             bool have = next_busy(it, x);
             bool ok = !have || load_q(x);
-            // K runs one tile ahead of V; the V loads reuse the K tile starts
-            Walk itk;
-            int kr_cur = 0, kw_cur = 0, kr_next = 0, kw_next = 0;   // map coordinates (rank, row)
-            bool primed = false;                                    // the item's first K is on its way
-            auto first_k = [&](const Item &y) {
-                start_walk(itk, y.w);
-                if constexpr (SPLIT) itk.skip(y.j0);
-            };
-            while (ok && have) {
-                int it2 = it + 1;
-                Item y = x;
-                const int kvh = dbg_coord(a.err, x.kvh, a.Hkv), qb = dbg_coord(a.err, x.w.b, a.B);
-                auto load_k = [&](int kvh, int qb) -> bool {   // the next K tile, global index nk
-                    const int st = nk & 1;
+            if constexpr (WIN) {
+                // The next unit's first K is sent along with its Q: units are short.  (A loop of its
+                // own: the ring's, with branches for this, took 0.5 % longer.)
+                Walk itk;                     // K runs one tile ahead of V
+                int kw_next = 0;              // map row of the K tile sent last, before a packed tile's sinks
+                auto load_k = [&](const Item &y) -> bool {   // the next K tile, global index nk
+                    const int st = nk & 1, kvh = dbg_coord(a.err, y.kvh, a.Hkv), qb = dbg_coord(a.err, y.w.b, a.B);
                     if (nk >= 2 && !wait1(BAR(B_KEMPTY + st), ((nk >> 1) - 1) & 1, wc)) return false;
                     mbar_arrive_expect_tx(BAR(B_KFULL + st), C::KBYTES);
-                    if constexpr (WIN) {
-                        kw_next = itk.start();
-                        if (itk.packed()) {
-                            const int row = dbg_coord(a.err, kw_next + itk.pk, map_keys);
-                            for (int bx = 0; bx < D / 64; ++bx) {
-                                const uint32_t dst = sK + st * C::KBYTES + bx * C::KBOX;
-                                tma_load5(dst, &pm_maps.k_sinks, BAR(B_KFULL + st), bx * 64, kvh, 0, 0, qb, pol_kv);
-                                tma_load5(dst + itk.pk * 128, &pm_maps.k_rest, BAR(B_KFULL + st), bx * 64, kvh, 0,
-                                          row, qb, pol_kv);
-                            }
-                            itk.next();
-                            ++nk;
-                            return true;
+                    kw_next = itk.start();
+                    if (itk.packed()) {
+                        const int row = dbg_coord(a.err, kw_next + itk.pk, a.Sk);
+                        for (int bx = 0; bx < D / 64; ++bx) {
+                            const uint32_t dst = sK + st * C::KBYTES + bx * C::KBOX;
+                            tma_load5(dst, &pm_maps.k_sinks, BAR(B_KFULL + st), bx * 64, kvh, 0, 0, qb, pol_kv);
+                            tma_load5(dst + itk.pk * 128, &pm_maps.k_rest, BAR(B_KFULL + st), bx * 64, kvh, 0, row, qb,
+                                      pol_kv);
                         }
-                        kw_next = dbg_coord(a.err, kw_next, map_keys);
                     } else {
-                        kr_next = dbg_coord(a.err, STEP ? 0 : itk.mrank(), map_r);
-                        kw_next = dbg_coord(a.err, STEP ? itk.lrow() : itk.mrow(), map_rows);
+                        kw_next = dbg_coord(a.err, kw_next, a.Sk);
+                        for (int bx = 0; bx < D / 64; ++bx)
+                            tma_load5(sK + st * C::KBYTES + bx * C::KBOX, &tmK, BAR(B_KFULL + st), bx * 64, kvh, 0, kw_next, qb,
+                                      pol_kv);
                     }
-                    for (int bx = 0; bx < D / 64; ++bx)
-                        tma_load5(sK + st * C::KBYTES + bx * C::KBOX, &tmK, BAR(B_KFULL + st), bx * 64,
-                                  kvh, kr_next, kw_next, qb, pol_kv);
                     itk.next();
                     ++nk;
                     return true;
                 };
-                if (!primed) {
-                    first_k(x);
-                    ok = load_k(kvh, qb);
+                if (have && ok) {
+                    start_walk(itk, x.w);
+                    ok = load_k(x);
                 }
-                primed = false;
-                int pk = 0;   // columns of a packed first tile that hold the sinks
-                if constexpr (WIN) pk = itk.pk;
-                const bool have2 = PERSIST && next_busy(it2, y);
-                for (int j = 0; ok && j < x.n; ++j) {
-                    kr_cur = kr_next;
-                    kw_cur = kw_next;
-                    // global index of tile j: nv / 2 (V halves are issued tile by tile)
-                    const int t = nv >> 1;
-                    if ((j + 1 < x.n && !load_k(kvh, qb)) || (j + 1 == x.n && have2 && !load_q(y))) {
-                        ok = false;
-                        break;
-                    }
-                    if constexpr (WIN) {
-                        if (j + 1 == x.n && have2) {
-                            first_k(y);
-                            primed = true;
-                            if (!load_k(dbg_coord(a.err, y.kvh, a.Hkv), dbg_coord(a.err, y.w.b, a.B))) {
+                while (ok && have) {
+                    int it2 = it + 1;
+                    Item y = x;
+                    const int kvh = dbg_coord(a.err, x.kvh, a.Hkv), qb = dbg_coord(a.err, x.w.b, a.B);
+                    const int pk = itk.pk;    // columns of a packed first tile that hold the sinks
+                    const bool have2 = next_busy(it2, y);
+                    for (int j = 0; ok && j < x.n; ++j) {
+                        const int kw_cur = kw_next;
+                        // global index of tile j: nv / 2 (V halves are issued tile by tile)
+                        const int t = nv >> 1;
+                        if (j + 1 < x.n) {
+                            ok = load_k(x);
+                        } else if (have2) {
+                            ok = load_q(y);
+                            if (ok) {
+                                start_walk(itk, y.w);
+                                ok = load_k(y);
+                            }
+                        }
+                        if (!ok) break;
+                        for (int hh = 0; hh < 2; ++hh) {
+                            if (t >= 1 && !wait1(BAR(B_VEMPTY + hh), (t - 1) & 1, wc)) {
                                 ok = false;
                                 break;
                             }
-                        }
-                    }
-                    for (int hh = 0; hh < 2; ++hh) {
-                        if (t >= 1 && !wait1(BAR(B_VEMPTY + hh), (t - 1) & 1, wc)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(BAR(B_VFULL + hh), C::VBYTES);
-                        if constexpr (WIN) {
+                            mbar_arrive_expect_tx(BAR(B_VFULL + hh), C::VBYTES);
                             if (hh == 0 && j == 0 && pk > 0) {   // the packed tile's first half
                                 for (int bx = 0; bx < D / 64; ++bx) {
                                     const uint32_t dst = sV + bx * 16384;
                                     tma_load5(dst, &pm_maps.v_sinks, BAR(B_VFULL), bx * 64, kvh, 0, 0, qb, pol_kv);
                                     tma_load5(dst + pk * 128, &pm_maps.v_rest, BAR(B_VFULL), bx * 64, kvh, 0,
-                                              dbg_coord(a.err, kw_cur + pk, map_keys), qb, pol_kv);
+                                              dbg_coord(a.err, kw_cur + pk, a.Sk), qb, pol_kv);
                                 }
-                                ++nv;
-                                continue;
+                            } else {
+                                for (int bx = 0; bx < D / 64; ++bx)
+                                    tma_load5(sV + hh * C::VBYTES + bx * 16384, &tmV, BAR(B_VFULL + hh), bx * 64, kvh, 0,
+                                              kw_cur + 128 * hh, qb, pol_kv);
                             }
+                            ++nv;
                         }
-                        for (int bx = 0; bx < D / 64; ++bx)
-                            tma_load5(sV + hh * C::VBYTES + bx * 16384, &tmV, BAR(B_VFULL + hh), bx * 64,
-                                      kvh, kr_cur, kw_cur + 128 * hh, qb, pol_kv);
-                        ++nv;
                     }
+                    x = y;
+                    it = it2;
+                    have = have2;
                 }
-                x = y;
-                it = it2;
-                have = have2;
+            } else {
+                while (ok && have) {
+                    int it2 = it + 1;
+                    Item y = x;
+                    // K runs one tile ahead of V; the V loads reuse the K tile starts
+                    KvIter<KT> itk;
+                    if (STEP)
+                        itk.begin_steps(g, x.w.r, x.w.qmax, stp.step_k, stp.step_k + 1);
+                    else
+                        itk.begin(g, x.w.r, x.w.qmax);
+                    if (SPLIT) itk.skip(x.j0);
+                    int kr_cur = 0, kw_cur = 0, kr_next = 0, kw_next = 0;   // map coordinates (rank, row)
+                    const int kvh = dbg_coord(a.err, x.kvh, a.Hkv), qb = dbg_coord(a.err, x.w.b, a.B);
+                    auto load_k = [&]() -> bool {   // the next K tile, global index nk
+                        const int st = nk & 1;
+                        if (nk >= 2 && !wait1(BAR(B_KEMPTY + st), ((nk >> 1) - 1) & 1, wc)) return false;
+                        mbar_arrive_expect_tx(BAR(B_KFULL + st), C::KBYTES);
+                        kr_next = dbg_coord(a.err, STEP ? 0 : itk.mrank(), map_r);
+                        kw_next = dbg_coord(a.err, STEP ? itk.lrow() : itk.mrow(), map_rows);
+                        for (int bx = 0; bx < D / 64; ++bx)
+                            tma_load5(sK + st * C::KBYTES + bx * C::KBOX, &tmK, BAR(B_KFULL + st), bx * 64,
+                                      kvh, kr_next, kw_next, qb, pol_kv);
+                        itk.next();
+                        ++nk;
+                        return true;
+                    };
+                    ok = load_k();
+                    const bool have2 = PERSIST && next_busy(it2, y);
+                    for (int j = 0; ok && j < x.n; ++j) {
+                        kr_cur = kr_next;
+                        kw_cur = kw_next;
+                        // global index of tile j: nv / 2 (V halves are issued tile by tile)
+                        const int t = nv >> 1;
+                        if ((j + 1 < x.n && !load_k()) || (j + 1 == x.n && have2 && !load_q(y))) {
+                            ok = false;
+                            break;
+                        }
+                        for (int hh = 0; hh < 2; ++hh) {
+                            if (t >= 1 && !wait1(BAR(B_VEMPTY + hh), (t - 1) & 1, wc)) {
+                                ok = false;
+                                break;
+                            }
+                            mbar_arrive_expect_tx(BAR(B_VFULL + hh), C::VBYTES);
+                            for (int bx = 0; bx < D / 64; ++bx)
+                                tma_load5(sV + hh * C::VBYTES + bx * 16384, &tmV, BAR(B_VFULL + hh), bx * 64,
+                                          kvh, kr_cur, kw_cur + 128 * hh, qb, pol_kv);
+                            ++nv;
+                        }
+                    }
+                    x = y;
+                    it = it2;
+                    have = have2;
+                }
             }
             {
                 // Drain: wait (bounded) for the copies still in flight -- always,
@@ -1155,7 +1191,7 @@ int launch_d(const void *q, const void *k, const void *v, void *out, float *lse,
 // window walk window + 127 keys) and are short, so one persistent block per SM
 // takes them in turn, whatever their number.
 template <int D>
-int launch_window_d(const void *q, const void *k, const void *v, void *out, float *lse, FwdArgs a, cudaStream_t st)
+int launch_window_d(const void *q, const void *k, const void *v, void *out, float *lse, WindowArgs a, cudaStream_t st)
 {
     CUtensorMap mq, mk, mv;
     PackMaps pm;
@@ -1201,7 +1237,7 @@ int launch_window_d(const void *q, const void *k, const void *v, void *out, floa
 
 }  // namespace
 
-int launch_window_fwd_bf16(const void *q, const void *k, const void *v, void *out, float *lse, FwdArgs a,
+int launch_window_fwd_bf16(const void *q, const void *k, const void *v, void *out, float *lse, WindowArgs a,
                            cudaStream_t st)
 {
     if (a.D == 64) return launch_window_d<64>(q, k, v, out, lse, a, st);

@@ -21,10 +21,15 @@ struct FwdArgs {
     unsigned *err;        // device error word
     uint64_t limit_ns;    // bound of every pipeline wait
     uint64_t drain_ns;    // bound of the waits that drain copies and MMAs before exit
-    int Sk;               // windowed attention: keys (S counts query rows)
-    Window win;           // windowed attention
-    FastDiv by_heads, by_batch, by_group;   // windowed attention: Hq, B, Hq / Hkv (set by the launcher)
-    const void *q, *k, *v;                  // windowed attention (set by the launcher)
+};
+
+// Of windowed attention.  (A type of its own: with these fields in FwdArgs, which the ring's forward
+// takes by value, its other arguments moved up and it took 2 % longer with D = 64 or striped rows.)
+struct WindowArgs : FwdArgs {
+    int Sk;               // keys (S counts query rows)
+    Window win;
+    FastDiv by_heads, by_batch, by_group;   // Hq, B, Hq / Hkv (set by the forward's launcher)
+    const void *q, *k, *v;                  // set by the forward's launcher
 };
 
 // Partial results of a split forward (fp32, normalised): n splits of every
@@ -59,9 +64,9 @@ int launch_fwd_bf16_split(const void *q, const void *k, const void *v, FwdArgs a
                           const SplitOut &so, cudaStream_t st);
 // Windowed attention (a.S query rows, a.Sk keys, a.win; N 1, contiguous, causal).
 int launch_window_fwd_bf16(const void *q, const void *k, const void *v, void *out, float *lse,
-                           FwdArgs a, cudaStream_t st);
+                           WindowArgs a, cudaStream_t st);
 int launch_window_fwd_f32(const float *q, const float *k, const float *v, float *out, float *lse,
-                          const FwdArgs &a, cudaStream_t st);
+                          const WindowArgs &a, cudaStream_t st);
 // Merge the so.n partials of the rows of ranks [a.rank_lo, a.rank_hi) into
 // out (bf16, [B][S][Hq][D]) and lse ([B][Hq][S]).
 int launch_fwd_split_combine(const FwdArgs &a, const SplitOut &so, void *out, float *lse,
@@ -91,8 +96,8 @@ int launch_bwd_bf16(const BwdPtrs &p, const FwdArgs &a, cudaStream_t st);
 int launch_bwd_f32(const BwdPtrs &p, const FwdArgs &a, cudaStream_t st);
 size_t bwd_workspace_bytes(int B, int Hq, int64_t S);
 // Windowed attention's gradients; the workspace is window_bwd_workspace_bytes() bytes.
-int launch_window_bwd_bf16(const BwdPtrs &p, const FwdArgs &a, cudaStream_t st);
-int launch_window_bwd_f32(const BwdPtrs &p, const FwdArgs &a, cudaStream_t st);
+int launch_window_bwd_bf16(const BwdPtrs &p, const WindowArgs &a, cudaStream_t st);
+int launch_window_bwd_f32(const BwdPtrs &p, const WindowArgs &a, cudaStream_t st);
 size_t window_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, int dtype, const Window &w);
 // Columns of a first tile that hold the sinks, a multiple of 16; 0: too many to share one.
 constexpr int WINDOW_MAX_PACK = 64;

@@ -17,7 +17,7 @@ bool aligned16(const void *p) { return aligned(p, 16); }
 
 // Checks what the windowed calls share and fills the arguments; 1: nothing to do.
 int window_args(int B, int Hq, int Hkv, int64_t Sq, int64_t Sk, int D, int64_t window, int64_t sinks, int dtype,
-                float scale, FwdArgs &a)
+                float scale, WindowArgs &a)
 {
     if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || Sq < 0 || Sk < Sq || window < 1 || sinks < 0 || isnan(scale))
         return CP_EINVAL;
@@ -61,7 +61,7 @@ int window_attn_fwd(const void *q, const void *k, const void *v, void *out, floa
                     int64_t Sq, int64_t Sk, int D, int64_t window, int64_t sinks, int dtype, float scale, void *stream)
 {
     NvtxScope nvtx_("window_attn_fwd");
-    FwdArgs a;
+    WindowArgs a;
     const int rc = window_args(B, Hq, Hkv, Sq, Sk, D, window, sinks, dtype, scale, a);
     if (rc < 0) return rc;
     if (rc || Sq == 0) return CP_OK;
@@ -80,7 +80,7 @@ int window_attn_fwd(const void *q, const void *k, const void *v, void *out, floa
 size_t window_attn_bwd_workspace(int B, int Hq, int Hkv, int64_t Sq, int64_t Sk, int D, int64_t window, int64_t sinks,
                                  int dtype)
 {
-    FwdArgs a;
+    WindowArgs a;
     if (window_args(B, Hq, Hkv, Sq, Sk, D, window, sinks, dtype, 1.f, a) < 0) return 0;
     const size_t b = window_bwd_workspace_bytes(B, Hq, Hkv, a.S, D, dtype, a.win);
     return b ? b : 256;
@@ -92,7 +92,7 @@ int window_attn_bwd(const void *q, const void *k, const void *v, const void *out
                     void *stream)
 {
     NvtxScope nvtx_("window_attn_bwd");
-    FwdArgs a;
+    WindowArgs a;
     const int rc = window_args(B, Hq, Hkv, Sq, Sk, D, window, sinks, dtype, scale, a);
     if (rc < 0) return rc;
     if (rc) return CP_OK;

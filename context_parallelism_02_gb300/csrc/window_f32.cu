@@ -462,7 +462,7 @@ int prepare()   // the kernels' shared memory, once per device
     return CP_OK;
 }
 
-Args make_args(const FwdArgs &f)
+Args make_args(const WindowArgs &f)
 {
     Args a{};
     a.B = f.B;
@@ -522,7 +522,7 @@ int backward(const Args &a, float *dq, float *dk, float *dv, cudaStream_t st)
 
 }  // namespace
 
-int launch_window_fwd_f32(const float *q, const float *k, const float *v, float *out, float *lse, const FwdArgs &f,
+int launch_window_fwd_f32(const float *q, const float *k, const float *v, float *out, float *lse, const WindowArgs &f,
                           cudaStream_t st)
 {
     Args a = make_args(f);
@@ -534,7 +534,7 @@ int launch_window_fwd_f32(const float *q, const float *k, const float *v, float 
     return CP_EUNSUPPORTED;
 }
 
-int launch_window_bwd_f32(const BwdPtrs &p, const FwdArgs &f, cudaStream_t st)
+int launch_window_bwd_f32(const BwdPtrs &p, const WindowArgs &f, cudaStream_t st)
 {
     Args a = make_args(f);
     a.q = static_cast<const float *>(p.q);
