@@ -770,7 +770,9 @@ __global__ void __launch_bounds__(256) kv8_mass_kernel(Kv8AttnArgs a, Shape sh, 
                 const int lim = kv4_limit(a.rows, b, j, len);
                 limit[threadIdx.x] = lim;
                 low[threadIdx.x] = a.window > 0 ? max(lim - a.window, 0) : 0;
-                lse2[threadIdx.x] = a.lse[((int64_t)b * a.rows.Hq + head) * a.rows.n + j] * LOG2E;
+                const float z = a.lse[((int64_t)b * a.rows.Hq + head) * a.rows.n + j];
+                // a row of nothing but scores of -infinity gives no weight, and not NaN
+                lse2[threadIdx.x] = z == -INFINITY ? INFINITY : z * LOG2E;
                 whole = lim >= s0 + MASS_CHUNK && low[threadIdx.x] <= s0;
             } else if ((int)threadIdx.x < MASS_ROWS) {
                 lse2[threadIdx.x] = INFINITY;                // rows that only fill up a four: weight 0

@@ -606,7 +606,7 @@ int kv8_gather(const void *cache, const float *scales, const int32_t *pages, con
  *   itself, or 2^-32 of the row's largest such product), also where out is fp32.  scale <= 0
  *   selects 1/sqrt(D).  A row of q with a value that is not finite comes out as NaN.  Scores
  *   beyond fp32's range count as infinities: a row all of whose scores lie below it comes out as
- *   one that sees nothing.
+ *   one that sees nothing, and adds nothing to mass.
  *   workspace: device, kv8_attn_workspace(...) bytes, 16-byte aligned, contents irrelevant;
  *   calls that may overlap on the GPU need their own.
  * No atomics: results repeat bit for bit.

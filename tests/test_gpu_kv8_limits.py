@@ -219,3 +219,23 @@ def test_evict_of_rows_that_just_fit_shared_memory(cuda_dev):
     want = o.evict(mass[0, 0].cpu().numpy(), L, budget, 3, 10)
     np.testing.assert_array_equal(kept[0, 0].cpu().numpy(), want)
     np.testing.assert_array_equal(mass_to[0, 0, :budget].cpu().numpy(), mass[0, 0].cpu().numpy()[want])
+
+
+@pytest.mark.parametrize("L", [1, 40, 9000])
+def test_scores_below_the_range_of_fp32(cuda_dev, L):
+    """Scores that overflow to -infinity: a row of nothing else is an empty one, (0, -inf), and adds no weight."""
+    H, Hq, D, page = 1, 4, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(15)
+    pages, P = torch.randperm(-(-L // page), generator=g, device="cuda").int()[None], -(-L // page)
+    cache, scales = api.kv8_cache(P, H, page, D)
+    k = torch.full((1, L, H, D), 1e12, device="cuda")
+    api.kv8_append(k, torch.ones_like(k), cache, scales, pages, torch.zeros(1, **I32))
+    q = torch.randn(1, 1, Hq, D, generator=g, device="cuda").mul(1e-13).bfloat16()
+    q[0, 0, 1] = -3e38
+    mass, lens = torch.zeros(1, H, P * page, device="cuda"), torch.tensor([L], **I32)
+    out, lse = api.kv8_attn(q, cache, scales, pages, lens, mass=mass)
+    ok()
+    assert not out[0, 0, 1].any() and lse[0, 1] == -math.inf
+    # all keys are alike: the other rows give each 1 / L, to the roundings of the sums, (L / 16 + 40) 2^-23, and of e^(s - lse)
+    assert (mass[0, 0, :L] * L / (Hq - 1) - 1).abs().max() <= (L / 16 + 40) * 2.0 ** -23 + 2.0 ** -18 and not mass[0, 0, L:].any()
+    assert (out[0, 0, [0, 2, 3]].float() - 1).abs().max() <= 2.0 ** -7
