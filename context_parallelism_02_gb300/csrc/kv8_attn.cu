@@ -25,7 +25,7 @@
 // 16 x 32768 tokens, 32 heads on 8, D = 128: 160.6 us, the rate of a copy; 64 ragged sequences
 // up to 8192 under a window of 1024 and 4 sinks 19.6 (47 MB: starts and the join); one of 512
 // tokens 7.0 (four dependent loads); 8 x 16384, 16 heads on 8, D = 64 27.7 for one token each,
-// 42.6 for four with the weights added up.
+// 43.2 for four with the weights added up.
 #include <atomic>
 
 #include <cuda.h>
